@@ -1,0 +1,169 @@
+// k2t_attn.cu -- the attention calls of the C ABI: checks, plan, launch.
+#include <algorithm>
+
+#include "k2t_attn.cuh"
+
+namespace k2t {
+
+int attn_forward_bf16(const AttnParams &p, int bm, cudaStream_t st);
+int attn_forward_fp16(const AttnParams &p, int bm, cudaStream_t st);
+int attn_backward_bf16(const AttnParams &p, cudaStream_t st);
+int attn_backward_fp16(const AttnParams &p, cudaStream_t st);
+
+namespace {
+
+// Sizes: the part of the checks that k2t_attn_work_bytes shares.
+int check_sizes(const k2t_attn *a)
+{
+    if (!a) return K2T_EINVAL;
+    if (a->dtype != K2T_BF16 && a->dtype != K2T_FP16) return K2T_EINVAL;
+    if (a->n_heads == 0 || a->n_kv_heads == 0 || a->n_heads % a->n_kv_heads) return K2T_EINVAL;
+    if (a->head_dim == 0 || a->head_dim % 8) return K2T_EINVAL;
+    if (a->head_dim > K2T_ATTN_MAX_HEAD_DIM || a->n_heads / a->n_kv_heads > K2T_ATTN_MAX_GROUP) return K2T_ERANGE;
+    if (a->n_kv_heads > 65535) return K2T_ERANGE;
+    if (a->n_sources > K2T_MAX_BATCH || a->n_buckets > K2T_ATTN_MAX_BUCKETS) return K2T_ERANGE;
+    if (a->n_nodes > (1ull << 32) || (uint64_t)a->n_queries * a->n_heads > (1ull << 30)) return K2T_ERANGE;
+    if (a->n_buckets && !a->n_sources) return K2T_EINVAL;
+    if (!(a->scale == a->scale)) return K2T_EINVAL;
+    for (uint32_t b = 0; b < a->n_buckets; ++b)
+        if (b == 0 ? a->edges[0] != 0 : a->edges[b] <= a->edges[b - 1]) return K2T_EINVAL;
+    return K2T_OK;
+}
+
+bool aligned(const void *p, int64_t row, int64_t head) { return !((uintptr_t)p & 15u) && !(row & 7) && !(head & 7); }
+
+// Blocks that fill the GPU: every SM holds two of the kernels' blocks.
+uint32_t fill_blocks()
+{
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        sms = 152;
+    cudaGetLastError();
+    return 2u * (uint32_t)sms;
+}
+
+struct Plan {
+    AttnParams p;
+    int bm;
+    uint64_t part_floats, ml_floats, delta_floats;
+};
+
+void make_plan(const k2t_attn *a, bool backward, Plan &pl)
+{
+    AttnParams &p = pl.p;
+    p = AttnParams{};
+    p.T = a->n_queries;
+    p.hq = a->n_heads;
+    p.hkv = a->n_kv_heads;
+    p.group = p.hq / p.hkv;
+    p.d = a->head_dim;
+    p.sources = a->n_sources;
+    p.buckets = a->n_buckets;
+    p.n = a->n_nodes;
+    p.rows = p.T * p.group;
+    p.tiles = (p.n + kAttnTile - 1) / kAttnTile;
+    p.hop_magic = p.sources ? (65536 + p.sources - 1) / p.sources : 0;
+    p.scale = a->scale;
+    p.scale_log2 = a->scale * kLog2e;
+    // rows per block: the smallest tile that holds them all, since the states are read once per row tile
+    pl.bm = backward ? 32 : p.rows <= 16 ? 16 : p.rows <= 32 ? 32 : 64;
+    p.row_tiles = std::max(1u, (p.rows + pl.bm - 1) / pl.bm);
+    const uint64_t blocks = (uint64_t)p.hkv * p.row_tiles;
+    p.splits = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(fill_blocks() / blocks, p.tiles));
+    const uint64_t rows = (uint64_t)p.T * p.hq;
+    pl.part_floats = backward || p.splits > 1 ? p.splits * rows * p.d : 0;
+    pl.ml_floats = backward ? p.splits * rows * p.buckets : p.splits > 1 ? p.splits * rows * 2 : 0;
+    pl.delta_floats = backward ? rows : 0;
+}
+
+uint64_t plan_bytes(const Plan &pl)
+{
+    return align_up(pl.part_floats * 4, 256) + align_up(pl.ml_floats * 4, 256) + align_up(pl.delta_floats * 4, 256);
+}
+
+int check_call(const k2t_attn *a, const void *work, uint64_t work_bytes, const Plan &pl)
+{
+    const bool q = a->n_queries != 0, n = a->n_nodes != 0;
+    if ((q && (!a->q || !a->out || !a->lse)) || (n && (!a->k || !a->v))) return K2T_EINVAL;
+    if (!aligned(a->q, a->q_row, a->q_head) || !aligned(a->k, a->k_row, a->k_head) ||
+        !aligned(a->v, a->v_row, a->v_head) || !aligned(a->out, a->out_row, a->out_head))
+        return K2T_EINVAL;
+    if (a->n_sources && n && !a->hops) return K2T_EINVAL;
+    if ((a->n_buckets != 0) != (a->bias != nullptr)) return K2T_EINVAL;
+    if (a->n_sources && !a->query_source && a->n_queries > a->n_sources) return K2T_ERANGE;
+    const uint64_t need = plan_bytes(pl);
+    if (need && (!work || ((uintptr_t)work & 15u))) return K2T_EINVAL;
+    if (work_bytes < need) return K2T_ENOMEM;
+    return K2T_OK;
+}
+
+void fill_pointers(const k2t_attn *a, void *work, Plan &pl)
+{
+    AttnParams &p = pl.p;
+    p.q = a->q, p.k = a->k, p.v = a->v, p.dout = a->dout;
+    if (!a->n_queries) p.q = p.dout = p.k;   // a readable address for copies of no bytes
+    p.hops = a->hops, p.qsrc = a->query_source, p.bias = a->bias;
+    p.out = a->out, p.dq = a->dq, p.dk = a->dk, p.dv = a->dv, p.dbias = a->dbias;
+    p.lse = a->lse;
+    p.q_row = a->q_row, p.q_head = a->q_head, p.k_row = a->k_row, p.k_head = a->k_head;
+    p.v_row = a->v_row, p.v_head = a->v_head, p.out_row = a->out_row, p.out_head = a->out_head;
+    p.dout_row = a->dout_row, p.dout_head = a->dout_head, p.dq_row = a->dq_row, p.dq_head = a->dq_head;
+    p.dk_row = a->dk_row, p.dk_head = a->dk_head, p.dv_row = a->dv_row, p.dv_head = a->dv_head;
+    char *w = static_cast<char *>(work);
+    p.part = reinterpret_cast<float *>(w);
+    p.part_ml = reinterpret_cast<float *>(w + align_up(pl.part_floats * 4, 256));
+    p.delta = reinterpret_cast<float *>(w + align_up(pl.part_floats * 4, 256) + align_up(pl.ml_floats * 4, 256));
+    uint32_t b = 0;
+    for (uint32_t x = 0; x < 256; ++x) {
+        while (b + 1 < a->n_buckets && a->edges[b + 1] <= x) ++b;
+        p.bucket_of[x] = (uint8_t)b;
+    }
+}
+
+}  // namespace
+}  // namespace k2t
+
+using namespace k2t;
+
+extern "C" {
+
+uint64_t k2t_attn_work_bytes(const k2t_attn *a, int32_t backward)
+{
+    if (check_sizes(a)) return 0;
+    Plan pl;
+    make_plan(a, backward != 0, pl);
+    return plan_bytes(pl);
+}
+
+int k2t_attn_forward(const k2t_attn *a, void *work, uint64_t work_bytes, void *stream)
+{
+    int rc = check_sizes(a);
+    if (rc) return rc;
+    Plan pl;
+    make_plan(a, false, pl);
+    if ((rc = check_call(a, work, work_bytes, pl))) return rc;
+    if (a->n_queries == 0) return K2T_OK;
+    fill_pointers(a, work, pl);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return a->dtype == K2T_BF16 ? attn_forward_bf16(pl.p, pl.bm, st) : attn_forward_fp16(pl.p, pl.bm, st);
+}
+
+int k2t_attn_backward(const k2t_attn *a, void *work, uint64_t work_bytes, void *stream)
+{
+    int rc = check_sizes(a);
+    if (rc) return rc;
+    Plan pl;
+    make_plan(a, true, pl);
+    if ((rc = check_call(a, work, work_bytes, pl))) return rc;
+    if (a->n_queries && (!a->dout || !a->dq)) return K2T_EINVAL;
+    if (a->n_nodes && (!a->dk || !a->dv)) return K2T_EINVAL;
+    if (a->n_buckets && !a->dbias) return K2T_EINVAL;
+    if (!aligned(a->dout, a->dout_row, a->dout_head) || !aligned(a->dq, a->dq_row, a->dq_head) ||
+        !aligned(a->dk, a->dk_row, a->dk_head) || !aligned(a->dv, a->dv_row, a->dv_head))
+        return K2T_EINVAL;
+    fill_pointers(a, work, pl);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return a->dtype == K2T_BF16 ? attn_backward_bf16(pl.p, st) : attn_backward_fp16(pl.p, st);
+}
+
+}  // extern "C"

@@ -34,7 +34,12 @@ EXPORTED = ["k2t_default_opts", "k2t_build", "k2t_workspace_bytes", "k2t_upload"
             "k2t_spmv_host", "k2t_stats_get", "k2t_level_signatures", "k2t_device_level",
             "k2t_decode", "k2t_free", "k2t_strerror", "k2t_last_cuda_error",
             "k2t_spmv_noalloc", "k2t_noalloc_scratch_limit", "k2t_msbfs",
-            "k2t_msbfs_work_bytes", "k2t_bool_product", "k2t_bool_closure", "k2t_status"]
+            "k2t_msbfs_work_bytes", "k2t_bool_product", "k2t_bool_closure", "k2t_status",
+            "k2t_attn_work_bytes", "k2t_attn_forward", "k2t_attn_backward",
+            "k2t_norm_work_bytes", "k2t_norm_forward", "k2t_norm_backward"]
+
+BF16, FP16, FP32 = 0, 1, 2
+ATTN_MAX_BUCKETS, ATTN_MAX_HOP = 64, 255
 
 
 class Opts(ctypes.Structure):
@@ -65,6 +70,29 @@ class Stats(ctypes.Structure):
                 ("leaf_k", ctypes.c_uint32), ("heavy_fp64", ctypes.c_uint32 * 2),
                 ("heavy_max_terms", ctypes.c_uint32 * 2), ("pad", ctypes.c_uint32),
                 ("heavy_partials", ctypes.c_uint64 * 2)]
+
+
+class Attn(ctypes.Structure):
+    """k2t_attn of include/k2t.h."""
+    _fields_ = [(name, ctypes.c_uint32) for name in ("dtype", "n_queries", "n_heads", "n_kv_heads", "head_dim",
+                                                     "n_sources", "n_buckets")] + \
+        [("scale", ctypes.c_float), ("n_nodes", ctypes.c_uint64), ("edges", ctypes.c_uint8 * ATTN_MAX_BUCKETS)] + \
+        [(name, ctypes.c_void_p) for name in ("q", "k", "v")] + \
+        [(name, ctypes.c_int64) for name in ("q_row", "q_head", "k_row", "k_head", "v_row", "v_head")] + \
+        [(name, ctypes.c_void_p) for name in ("hops", "query_source", "bias", "out", "lse")] + \
+        [(name, ctypes.c_int64) for name in ("out_row", "out_head")] + \
+        [("dout", ctypes.c_void_p), ("dout_row", ctypes.c_int64), ("dout_head", ctypes.c_int64)] + \
+        [(name, ctypes.c_void_p) for name in ("dq", "dk", "dv")] + \
+        [(name, ctypes.c_int64) for name in ("dq_row", "dq_head", "dk_row", "dk_head", "dv_row", "dv_head")] + \
+        [("dbias", ctypes.c_void_p)]
+
+
+class Norm(ctypes.Structure):
+    """k2t_norm of include/k2t.h."""
+    _fields_ = [("dtype", ctypes.c_uint32), ("dim", ctypes.c_uint32), ("n_rows", ctypes.c_uint64),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_uint32)] + \
+        [(name, ctypes.c_void_p) for name in ("x", "residual", "weight", "bias", "y", "z", "mean", "rstd",
+                                              "dy", "dz", "dx", "dweight", "dbias")]
 
 
 class K2TError(RuntimeError):
@@ -119,6 +147,15 @@ def load() -> ctypes.CDLL:
         lib.k2t_strerror.argtypes = [ctypes.c_int]
         lib.k2t_strerror.restype = ctypes.c_char_p
         lib.k2t_last_cuda_error.argtypes = []
+        lib.k2t_attn_work_bytes.argtypes = [ctypes.POINTER(Attn), I32]
+        lib.k2t_attn_work_bytes.restype = U64
+        lib.k2t_norm_work_bytes.argtypes = [ctypes.POINTER(Norm)]
+        lib.k2t_norm_work_bytes.restype = U64
+        lib.k2t_norm_forward.argtypes = [ctypes.POINTER(Norm), P]
+        lib.k2t_norm_forward.restype = ctypes.c_int
+        for name, struct in (("k2t_attn_forward", Attn), ("k2t_attn_backward", Attn), ("k2t_norm_backward", Norm)):
+            getattr(lib, name).argtypes = [ctypes.POINTER(struct), P, U64, P]
+            getattr(lib, name).restype = ctypes.c_int
         for name in ("k2t_build", "k2t_workspace_bytes", "k2t_upload", "k2t_spmv", "k2t_spmv_marked",
                      "k2t_spmv_host",
                      "k2t_stats_get", "k2t_level_signatures", "k2t_device_level", "k2t_decode",

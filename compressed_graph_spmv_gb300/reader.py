@@ -1,0 +1,194 @@
+"""The layers of a model that reads a graph, on device tensors: attention of
+queries to node states biased by hop distance, and layer norm of node states
+(``k2t_attn_*`` and ``k2t_norm_*`` of ``include/k2t.h``).
+
+As in ``k2t.py``, argument marshalling only.  An object holds the sizes and
+the work buffer of one layer; its calls take tensors that the caller owns,
+write the output tensors they are given and return them.  Calls of one
+object share its buffers: order them on the GPU (one stream, or events).
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+from .k2t import (ATTN_MAX_BUCKETS, ATTN_MAX_HOP, BF16, FP16, FP32, Attn, Norm, _check, _stream_ptr, load)
+
+
+def hop_edges(n_buckets: int, max_hop: int = 64) -> list:
+    """First hop of each of ``n_buckets`` buckets: one bucket a hop for the
+    first half, then growing ones; hops of ``max_hop`` or more share the last."""
+    if not 1 <= n_buckets <= ATTN_MAX_BUCKETS:
+        raise ValueError("n_buckets must be 1..%d" % ATTN_MAX_BUCKETS)
+    if not n_buckets - 1 <= max_hop <= ATTN_MAX_HOP:
+        raise ValueError("max_hop must be n_buckets - 1..%d" % ATTN_MAX_HOP)
+    half = (n_buckets + 1) // 2
+    grown = n_buckets - half
+    edges = list(range(half))
+    for i in range(1, grown + 1):
+        geometric = round(half * (max_hop / half) ** (i / grown))
+        edges.append(min(max(edges[-1] + 1, geometric), max_hop - (grown - i)))
+    return edges
+
+
+def _dtype_code(dtype, allowed):
+    import torch
+    code = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}.get(dtype)
+    if code not in allowed:
+        raise TypeError("unsupported dtype %s" % dtype)
+    return code
+
+
+def _tensor(name, t, shape, dtype, contiguous):
+    """Address of a CUDA tensor of this shape and type whose last dimension is contiguous."""
+    if t.shape != shape:
+        raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype is not dtype:
+        raise TypeError("%s: expected %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s: expected a CUDA tensor" % name)
+    if not (t.is_contiguous() if contiguous else t.stride(-1) == 1 or not t.numel()):
+        raise ValueError("%s: expected a contiguous %s" % (name, "tensor" if contiguous else "last dimension"))
+    return t.data_ptr()
+
+
+class HopAttention:
+    """Attention of ``n_queries`` queries to the states of ``n_nodes`` nodes.
+
+    ``sources`` columns of a hop table (int32 [n_nodes, sources], as
+    ``Tree.msbfs`` leaves it: -1 masks a node) and ``edges``, the first hop of
+    each bucket of the bias table [n_heads, len(edges)]; ``sources`` 0 is plain
+    attention, no ``edges`` masks without a bias.  See ``k2t_attn``.
+    """
+
+    def __init__(self, n_queries: int, n_nodes: int, n_heads: int, n_kv_heads: int, head_dim: int, dtype,
+                 sources: int = 0, edges=None, scale: float | None = None, device="cuda"):
+        import torch
+        self._torch = torch
+        self.dtype, self.device = dtype, device
+        edges = list(edges) if edges is not None else []
+        if len(edges) > ATTN_MAX_BUCKETS or any(not 0 <= e <= ATTN_MAX_HOP for e in edges):
+            raise ValueError("edges: at most %d first hops of 0..%d" % (ATTN_MAX_BUCKETS, ATTN_MAX_HOP))
+        a = self._a = Attn()
+        a.dtype = _dtype_code(dtype, (BF16, FP16))
+        a.n_queries, a.n_heads, a.n_kv_heads, a.head_dim = n_queries, n_heads, n_kv_heads, head_dim
+        a.n_sources, a.n_buckets, a.n_nodes = sources, len(edges), n_nodes
+        a.scale = 1.0 / math.sqrt(head_dim) if scale is None else scale
+        for i, e in enumerate(edges):
+            a.edges[i] = e
+        self._ref = ctypes.byref(a)
+        self._rows = torch.Size((n_queries, n_heads, head_dim))
+        self._nodes = torch.Size((n_nodes, n_kv_heads, head_dim))
+        self._lse = torch.Size((n_queries, n_heads))
+        self._hops = torch.Size((n_nodes, sources))
+        self._source = torch.Size((n_queries,))
+        self._table = torch.Size((n_heads, len(edges)))
+        self._lib = load()
+        self._work, self._bytes = [None, None], [0, 0]
+
+    def work_bytes(self, backward: bool = False) -> int:
+        """Device bytes of the work buffer of a pass (k2t_attn_work_bytes)."""
+        return int(self._lib.k2t_attn_work_bytes(self._ref, int(backward)))
+
+    def _work_of(self, backward: int):
+        if self._work[backward] is None:
+            self._bytes[backward] = self.work_bytes(bool(backward))
+            self._work[backward] = self._torch.empty(max(16, self._bytes[backward]), dtype=self._torch.uint8,
+                                                     device=self.device)
+        return self._work[backward].data_ptr(), self._bytes[backward]
+
+    def _rows_in(self, name, t, shape):
+        a = self._a
+        setattr(a, name, _tensor(name, t, shape, self.dtype, False))
+        row, head, _ = t.stride()
+        # a dimension of one value has no pitch, whatever its stride says
+        setattr(a, name + "_row", row if shape[0] > 1 else 0)
+        setattr(a, name + "_head", head if shape[1] > 1 else 0)
+
+    def _table_in(self, hops, bias, query_source):
+        a, torch = self._a, self._torch
+        if (hops is None) != (a.n_sources == 0):
+            raise ValueError("hops: given %s, sources %d" % (hops is not None, a.n_sources))
+        a.hops = None if hops is None else _tensor("hops", hops.view(self._hops), self._hops, torch.int32, True)
+        a.bias = None if bias is None else _tensor("bias", bias, self._table, self.dtype, True)
+        a.query_source = None if query_source is None else _tensor("query_source", query_source, self._source,
+                                                                   torch.int32, True)
+
+    def forward(self, q, k, v, out, lse, hops=None, bias=None, query_source=None, stream=None):
+        """out [T, n_heads, head_dim] and lse (fp32 [T, n_heads]) of q, k, v."""
+        a = self._a
+        self._rows_in("q", q, self._rows)
+        self._rows_in("k", k, self._nodes)
+        self._rows_in("v", v, self._nodes)
+        self._rows_in("out", out, self._rows)
+        a.lse = _tensor("lse", lse, self._lse, self._torch.float32, True)
+        self._table_in(hops, bias, query_source)
+        work, size = self._work_of(0)
+        _check("k2t_attn_forward", self._lib.k2t_attn_forward(self._ref, work, size, _stream_ptr(stream)))
+        return out, lse
+
+    def backward(self, dout, q, k, v, out, lse, dq, dk, dv, dbias=None, hops=None, bias=None, query_source=None,
+                 stream=None):
+        """Gradients of q, k, v and the bias table from dout, the inputs and the forward's out and lse."""
+        a = self._a
+        for name, t, shape in (("dout", dout, self._rows), ("q", q, self._rows), ("k", k, self._nodes),
+                               ("v", v, self._nodes), ("out", out, self._rows), ("dq", dq, self._rows),
+                               ("dk", dk, self._nodes), ("dv", dv, self._nodes)):
+            self._rows_in(name, t, shape)
+        a.lse = _tensor("lse", lse, self._lse, self._torch.float32, True)
+        a.dbias = None if dbias is None else _tensor("dbias", dbias, self._table, self.dtype, True)
+        self._table_in(hops, bias, query_source)
+        work, size = self._work_of(1)
+        _check("k2t_attn_backward", self._lib.k2t_attn_backward(self._ref, work, size, _stream_ptr(stream)))
+        return dq, dk, dv, dbias
+
+
+class LayerNorm:
+    """Layer norm of ``n_rows`` states of ``dim`` values, with the residual sum before it (``k2t_norm``)."""
+
+    def __init__(self, n_rows: int, dim: int, dtype, residual: bool = False, eps: float = 1e-5, device="cuda"):
+        import torch
+        self._torch = torch
+        self.dtype, self.device, self.residual = dtype, device, residual
+        a = self._a = Norm()
+        a.dtype = _dtype_code(dtype, (BF16, FP16, FP32))
+        a.dim, a.n_rows, a.eps = dim, n_rows, eps
+        self._ref = ctypes.byref(a)
+        self._rows, self._cols = torch.Size((n_rows, dim)), torch.Size((dim,))
+        self._lib = load()
+        self.mean = torch.empty(n_rows, dtype=torch.float32, device=device)
+        self.rstd = torch.empty(n_rows, dtype=torch.float32, device=device)
+        a.mean, a.rstd = self.mean.data_ptr(), self.rstd.data_ptr()
+        self._work, self._bytes = None, 0
+
+    def work_bytes(self) -> int:
+        """Device bytes of the backward pass's work buffer (k2t_norm_work_bytes)."""
+        return int(self._lib.k2t_norm_work_bytes(self._ref))
+
+    def _in(self, name, t, shape):
+        setattr(self._a, name, None if t is None else _tensor(name, t, shape, self.dtype, True))
+
+    def forward(self, x, weight, bias, y, residual=None, z=None, stream=None):
+        """y = norm(z) and, with a residual, z = x + residual; keeps mean and rstd for backward."""
+        if (residual is not None) != self.residual or (z is not None) != self.residual:
+            raise ValueError("residual and z are given exactly when the layer has a residual")
+        for name, t in (("x", x), ("residual", residual), ("y", y), ("z", z)):
+            self._in(name, t, self._rows)
+        self._in("weight", weight, self._cols)
+        self._in("bias", bias, self._cols)
+        _check("k2t_norm_forward", self._lib.k2t_norm_forward(self._ref, _stream_ptr(stream)))
+        return y if z is None else (y, z)
+
+    def backward(self, dy, z, weight, dx, dweight, dbias=None, dz=None, stream=None):
+        """dx (of x and of the residual alike), dweight and dbias from dy and the forward's z (its x without a
+        residual); dz, the gradient that reaches z from elsewhere, is added to dx."""
+        for name, t in (("dy", dy), ("z", z), ("dx", dx), ("dz", dz)):
+            self._in(name, t, self._rows)
+        for name, t in (("weight", weight), ("dweight", dweight), ("dbias", dbias)):
+            self._in(name, t, self._cols)
+        if self._work is None:
+            self._bytes = self.work_bytes()
+            self._work = self._torch.empty(max(16, self._bytes), dtype=self._torch.uint8, device=self.device)
+        _check("k2t_norm_backward", self._lib.k2t_norm_backward(self._ref, self._work.data_ptr(), self._bytes,
+                                                                _stream_ptr(stream)))
+        return dx, dweight, dbias

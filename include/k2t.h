@@ -350,6 +350,120 @@ K2T_API int k2t_msbfs(k2t_tree *t, int32_t dir, const uint32_t *sources, uint32_
 /* Bytes of the work buffer k2t_msbfs needs for this tree. */
 K2T_API uint64_t k2t_msbfs_work_bytes(const k2t_tree *t);
 
+/* ---- reading a graph with a model ------------------------------------- */
+/* The calls below take what the search and the products leave (hop tables,
+ * node states) to the layers of a model that reads the graph.  They need no
+ * tree.  All tensors are device memory of the caller; every call is
+ * asynchronous on `stream`, allocates nothing and writes only its outputs and
+ * `work`.  A work buffer may be shared by calls that are ordered on the GPU.
+ * Results do not depend on the order in which blocks run.                    */
+
+/* Element types. */
+#define K2T_BF16 0
+#define K2T_FP16 1
+#define K2T_FP32 2
+
+#define K2T_ATTN_MAX_HEAD_DIM 128
+#define K2T_ATTN_MAX_GROUP    16   /* query heads per key/value head            */
+#define K2T_ATTN_MAX_BUCKETS  64
+#define K2T_ATTN_MAX_HOP      255  /* largest first hop of a bucket              */
+
+/* Attention of n_queries queries to the states of n_nodes nodes, biased and
+ * masked by hop distance.  For query t, head h (key/value head h / G,
+ * G = n_heads / n_kv_heads) and node j:
+ *   s   = scale * q[t,h] . k[j,h/G] + bias[h, bucket(hops[j, c(t)])]
+ *   out[t,h] = sum_j softmax_j(s) v[j,h/G],   lse[t,h] = log sum_j exp(s)
+ * c(t) is the query's column of the hop table.  bucket(x) is the last b with
+ * edges[b] <= x.  Masked are: nodes with hops < 0; buckets whose entry of the
+ * table is -inf or not above the lowest finite value of its type (bf16: not
+ * above -1e38).  A query for which nothing is left has out = 0,
+ * lse = -inf and no gradient.  Sums and softmax statistics are fp32; the
+ * weights are rounded to the element type before they multiply v.
+ * The states of a node that no query of the call sees (hops < 0 for every
+ * column in use) are not used: they may hold anything, NaN included.
+ * Strides are in elements; rows must be 16-byte aligned: base pointers
+ * multiples of 16 bytes, strides and head_dim multiples of 8.              */
+typedef struct {
+    uint32_t dtype;            /* K2T_BF16 or K2T_FP16: q, k, v, out, bias and all gradients        */
+    uint32_t n_queries;        /* T, 0 or more                                                       */
+    uint32_t n_heads;          /* query heads, a multiple of n_kv_heads                             */
+    uint32_t n_kv_heads;
+    uint32_t head_dim;         /* multiple of 8, 8..128                                             */
+    uint32_t n_sources;        /* columns of hops, 1..32; 0: no table (no mask, no bias)            */
+    uint32_t n_buckets;        /* 1..64 with a bias table, else 0                                   */
+    float scale;
+    uint64_t n_nodes;          /* 0 or more, at most 2^32                                           */
+    uint8_t edges[K2T_ATTN_MAX_BUCKETS]; /* first hop of each bucket, increasing, edges[0] = 0      */
+    /* inputs */
+    const void *q, *k, *v;     /* [T, n_heads, head_dim], [n_nodes, n_kv_heads, head_dim] twice     */
+    int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+    const int32_t *hops;       /* [n_nodes, n_sources] contiguous, as k2t_msbfs writes it           */
+    const int32_t *query_source; /* [T] column of each query; outside [0, n_sources): the query has
+                                  no hop information, sees every node and gets no bias.  NULL:
+                                  query t uses column t (then n_queries <= n_sources)               */
+    const void *bias;          /* [n_heads, n_buckets] contiguous, or NULL                          */
+    /* forward outputs; backward inputs */
+    void *out;                 /* [T, n_heads, head_dim]                                            */
+    float *lse;                /* [T, n_heads] contiguous                                           */
+    int64_t out_row, out_head;
+    /* backward */
+    const void *dout;          /* gradient of out                                                   */
+    int64_t dout_row, dout_head;
+    void *dq, *dk, *dv;        /* gradients, shaped as q, k, v; overwritten                         */
+    int64_t dq_row, dq_head, dk_row, dk_head, dv_row, dv_head;
+    void *dbias;               /* [n_heads, n_buckets] contiguous; required if bias is given        */
+} k2t_attn;
+
+/* Bytes of `work` the forward (backward = 0) or backward call needs for these
+ * sizes (pointers are not read).  0 for sizes the call refuses. */
+K2T_API uint64_t k2t_attn_work_bytes(const k2t_attn *a, int32_t backward);
+
+/* out and lse.  Errors: EINVAL (null, misaligned, bad dtype or sizes, edges
+ * not increasing from 0, buckets without a table or the reverse), ERANGE
+ * (a limit above exceeded, more queries than sources without query_source),
+ * ENOMEM (work_bytes too small), ECUDA. */
+K2T_API int k2t_attn_forward(const k2t_attn *a, void *work, uint64_t work_bytes, void *stream);
+
+/* dq, dk, dv and dbias from dout, the inputs, out and lse.  Gradients of a
+ * key/value head sum over its query heads, of a bucket over queries and
+ * nodes.  Errors as k2t_attn_forward. */
+K2T_API int k2t_attn_backward(const k2t_attn *a, void *work, uint64_t work_bytes, void *stream);
+
+/* Layer norm of n_rows states of dim values, with the residual sum before it:
+ *   z = x + residual (rounded to the element type; z = x without residual)
+ *   y = weight * (z - mean) / sqrt(var + eps) + bias,  var = mean (z - mean)^2
+ * Rows are contiguous.  All tensors share dtype; statistics are fp32.        */
+#define K2T_NORM_MAX_DIM 16384
+typedef struct {
+    uint32_t dtype;            /* K2T_BF16, K2T_FP16 or K2T_FP32                                     */
+    uint32_t dim;              /* 1..16384                                                           */
+    uint64_t n_rows;           /* 0 or more, at most 2^32                                            */
+    float eps;
+    uint32_t reserved;
+    /* forward */
+    const void *x, *residual;  /* [n_rows, dim]; residual may be NULL                                */
+    const void *weight, *bias; /* [dim]; bias may be NULL (forward)                                  */
+    void *y, *z;               /* [n_rows, dim]; z required with residual, else unused               */
+    float *mean, *rstd;        /* [n_rows] each: forward outputs, backward inputs                    */
+    /* backward: gradients of x (and of residual, the same), weight and bias.  `z` is the
+     * forward's z, or its x without residual; `dz` is the gradient that reaches z from
+     * elsewhere (NULL: none) and is added to dx                                             */
+    const void *dy, *dz;
+    void *dx, *dweight, *dbias; /* dbias may be NULL                                                 */
+} k2t_norm;
+
+/* Bytes of `work` k2t_norm_backward needs; 0 for sizes it refuses. */
+K2T_API uint64_t k2t_norm_work_bytes(const k2t_norm *a);
+
+/* y, z, mean and rstd.  y may be x or residual, z may be x or residual, y and
+ * z differ.  Errors: EINVAL (null, bad dtype, eps not positive, pointers not
+ * aligned to their element), ERANGE (dim or n_rows), ECUDA. */
+K2T_API int k2t_norm_forward(const k2t_norm *a, void *stream);
+
+/* dx, dweight, dbias; dx may be dy or dz.  Errors as k2t_norm_forward, and
+ * ENOMEM (work_bytes too small). */
+K2T_API int k2t_norm_backward(const k2t_norm *a, void *work, uint64_t work_bytes, void *stream);
+
 /* Shape, per-level sizes and the device footprint broken down by part. */
 K2T_API int k2t_stats_get(const k2t_tree *t, k2t_stats *s);
 
