@@ -1,7 +1,7 @@
 // k2t_attn.cu -- the attention calls of the C ABI: checks, plan, launch.
 #include <algorithm>
 
-#include "k2t_attn.cuh"
+#include "k2t_attn_launch.cuh"
 
 namespace k2t {
 
@@ -32,14 +32,20 @@ int check_sizes(const k2t_attn *a)
 
 bool aligned(const void *p, int64_t row, int64_t head) { return !((uintptr_t)p & 15u) && !(row & 7) && !(head & 7); }
 
-// Blocks that fill the GPU: every SM holds two of the kernels' blocks.
-uint32_t fill_blocks()
+constexpr uint64_t kSms = 152;
+
+// Blocks that share the nodes of one (head, row tile): as many as make the
+// fewest rounds of the GPU's SMs times tiles a block, with two tiles' time for
+// a block's start and end.  `per_sm` blocks run on an SM at once.
+uint32_t pick_splits(uint64_t blocks, uint64_t tiles, uint64_t per_sm)
 {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        sms = 152;
-    cudaGetLastError();
-    return 2u * (uint32_t)sms;
+    const uint64_t slots = kSms * per_sm, most = std::min<uint64_t>(std::max<uint64_t>(1, tiles), slots);
+    uint64_t best = 1, cost = ~0ull;
+    for (uint64_t s = 1; s <= most; ++s) {
+        const uint64_t rounds = (blocks * s + slots - 1) / slots, c = rounds * ((tiles + s - 1) / s + 2);
+        if (c < cost) cost = c, best = s;
+    }
+    return (uint32_t)best;
 }
 
 struct Plan {
@@ -61,24 +67,29 @@ void make_plan(const k2t_attn *a, bool backward, Plan &pl)
     p.buckets = a->n_buckets;
     p.n = a->n_nodes;
     p.rows = p.T * p.group;
-    p.tiles = (p.n + kAttnTile - 1) / kAttnTile;
+    while ((1u << p.group2_log) < p.group) ++p.group2_log;
+    p.group2 = 1u << p.group2_log;
     p.hop_magic = p.sources ? (65536 + p.sources - 1) / p.sources : 0;
     p.scale = a->scale;
     p.scale_log2 = a->scale * kLog2e;
     // rows per block: the smallest tile that holds them all, since the states are read once per row tile
-    pl.bm = backward ? 32 : p.rows <= 16 ? 16 : p.rows <= 32 ? 32 : 64;
+    pl.bm = backward ? kBwdRows : p.rows <= 32 ? 32 : p.rows <= 64 ? 64 : p.rows <= 128 ? 128 : 256;
+    const int tile = backward ? kAttnTile : kTcTile;
+    p.tiles = (p.n + tile - 1) / tile;
     p.row_tiles = std::max(1u, (p.rows + pl.bm - 1) / pl.bm);
     const uint64_t blocks = (uint64_t)p.hkv * p.row_tiles;
-    p.splits = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(fill_blocks() / blocks, p.tiles));
+    p.splits = pick_splits(blocks, p.tiles, backward ? 2 : 1);
     const uint64_t rows = (uint64_t)p.T * p.hq;
     pl.part_floats = backward || p.splits > 1 ? p.splits * rows * p.d : 0;
     pl.ml_floats = backward ? p.splits * rows * p.buckets : p.splits > 1 ? p.splits * rows * 2 : 0;
     pl.delta_floats = backward ? rows : 0;
 }
 
+constexpr uint64_t kWorkHead = 256;   // the device status word
+
 uint64_t plan_bytes(const Plan &pl)
 {
-    return align_up(pl.part_floats * 4, 256) + align_up(pl.ml_floats * 4, 256) + align_up(pl.delta_floats * 4, 256);
+    return kWorkHead + align_up(pl.part_floats * 4, 256) + align_up(pl.ml_floats * 4, 256) + align_up(pl.delta_floats * 4, 256);
 }
 
 int check_call(const k2t_attn *a, const void *work, uint64_t work_bytes, const Plan &pl)
@@ -92,7 +103,7 @@ int check_call(const k2t_attn *a, const void *work, uint64_t work_bytes, const P
     if ((a->n_buckets != 0) != (a->bias != nullptr)) return K2T_EINVAL;
     if (a->n_sources && !a->query_source && a->n_queries > a->n_sources) return K2T_ERANGE;
     const uint64_t need = plan_bytes(pl);
-    if (need && (!work || ((uintptr_t)work & 15u))) return K2T_EINVAL;
+    if (!work || ((uintptr_t)work & 15u)) return K2T_EINVAL;
     if (work_bytes < need) return K2T_ENOMEM;
     return K2T_OK;
 }
@@ -109,7 +120,8 @@ void fill_pointers(const k2t_attn *a, void *work, Plan &pl)
     p.v_row = a->v_row, p.v_head = a->v_head, p.out_row = a->out_row, p.out_head = a->out_head;
     p.dout_row = a->dout_row, p.dout_head = a->dout_head, p.dq_row = a->dq_row, p.dq_head = a->dq_head;
     p.dk_row = a->dk_row, p.dk_head = a->dk_head, p.dv_row = a->dv_row, p.dv_head = a->dv_head;
-    char *w = static_cast<char *>(work);
+    p.status = static_cast<uint32_t *>(work);
+    char *w = static_cast<char *>(work) + kWorkHead;
     p.part = reinterpret_cast<float *>(w);
     p.part_ml = reinterpret_cast<float *>(w + align_up(pl.part_floats * 4, 256));
     p.delta = reinterpret_cast<float *>(w + align_up(pl.part_floats * 4, 256) + align_up(pl.ml_floats * 4, 256));

@@ -38,6 +38,7 @@ struct AttnParams {
     uint32_t T, hq, hkv, group, d, sources, buckets;
     uint64_t n;
     uint32_t rows;            // T * group
+    uint32_t group2, group2_log;  // group rounded up to a power of two
     uint32_t row_tiles;
     uint32_t splits;          // blocks that share the nodes of one head
     uint64_t tiles;           // ceil(n / kAttnTile)
@@ -53,6 +54,7 @@ struct AttnParams {
     float *part;              // partial sums: see the kernels
     float *part_ml;
     float *delta;
+    uint32_t *status;         // device status word, at the start of the work buffer
     uint8_t bucket_of[256];   // bucket of each hop count; larger hops share the last
 };
 
@@ -199,17 +201,17 @@ struct HopSmem {
     uint8_t tile[4][33 * kHopPitch];        // [buffer][column][node]
 };
 
-// Bias table in units of log2, [bucket byte][g]: -inf at 0 (masked), 0 at buckets + 1.
+// Bias table in units of log2, [bucket byte][pitch]: -inf at 0 (masked), 0 at buckets + 1.
 template <typename T>
-__device__ __forceinline__ void fill_bias(float *lut, const AttnParams &p, uint32_t hk, int tid)
+__device__ __forceinline__ void fill_bias(float *lut, const AttnParams &p, uint32_t hk, int tid, uint32_t pitch)
 {
     const T *bias = static_cast<const T *>(p.bias);
-    const uint32_t total = (p.buckets + 2) * p.group;
+    const uint32_t total = (p.buckets + 2) * pitch;
     for (uint32_t i = tid; i < total; i += blockDim.x) {
-        const uint32_t b = i / p.group, g = i - b * p.group;
+        const uint32_t b = i / pitch, g = i - b * pitch;
         float v = 0.0f;
         if (b == 0) v = -INFINITY;
-        else if (b <= p.buckets && bias) {
+        else if (b <= p.buckets && bias && g < p.group) {
             v = Elem<T>::to_float(bias[(uint64_t)(hk * p.group + g) * p.buckets + b - 1]);
             v = v <= Elem<T>::kMasked ? -INFINITY : v * kLog2e;
         }

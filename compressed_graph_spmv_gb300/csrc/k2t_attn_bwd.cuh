@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_bwd_kernel(const __grid_con
 {
     using S = BwdSmem<DP, MODE>;
     constexpr int D16 = DP / 16, R8 = kBwdRows / 8;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t hk = blockIdx.y;
     // MODE 0, 2: x = split + splits * row tile; MODE 1: x = tile of nodes
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_bwd_kernel(const __grid_con
     if (tid == 0) hs->columns = 0, hs->all = 0;
     if (p.sources)
         for (int i = tid; i < 256; i += kAttnThreads) hs->bucket_of[i] = p.bucket_of[i];
-    fill_bias<T>(lut, p, hk, tid);
+    fill_bias<T>(lut, p, hk, tid, p.group);
     for (int i = tid; i < 4 * kAttnTile; i += kAttnThreads) hs->seen[0][i] = 0;
     if (MODE != 1)
         for (uint32_t i = tid; i < (p.buckets + 2) * kAttnThreads; i += kAttnThreads) hist[i] = 0.0f;

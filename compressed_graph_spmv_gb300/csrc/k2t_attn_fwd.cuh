@@ -1,231 +1,503 @@
-// k2t_attn_fwd.cuh -- forward pass of the hop-biased attention.
+// k2t_attn_fwd.cuh -- forward pass of the hop-biased attention on tcgen05.
 //
 // One pass over the nodes with the running maximum and sum of the softmax:
-// for a tile of nodes with scores s, m' = max(m, max s), w = exp2(s - m'),
-// l = l exp2(m - m') + sum w, O = O exp2(m - m') + w V.  Few rows meet many
-// nodes, so the nodes of a head are split over `splits` blocks (tile i goes
-// to block i mod splits, which also spreads the unreached nodes that power-law
-// graphs keep side by side), and attn_join_kernel joins their (O, m, l).
+// for a tile with scores s, w = exp2(s - m), l += sum w, O += w V.  Few rows
+// meet many nodes, so the nodes of a head are split over blocks (tile i goes
+// to block i mod splits, which also spreads the unreached nodes that
+// power-law graphs keep side by side) and attn_join_kernel joins them.
+//
+// One block an SM.  Tiles of 128 nodes stream through a ring of slots (keys
+// and values alternate); scores S = Q K^T (128 rows x 128 nodes) and outputs
+// O = P V accumulate in tensor memory, the weights P go back to it over S and
+// are the A operand of the second product.  Warps:
+//   0-7   two softmax groups of 128 threads, thread = row of S (lane of
+//         tensor memory), with a running maximum, sum and O of their own
+//   8-11  hops of a tile -> bucket bytes, and which nodes are seen
+//   12-15 states of a tile's seen nodes -> slots
+//   16    one thread issues every product
+// Rows.  With more than 128 rows (TWO) the groups take two row tiles and
+// share each tile of nodes; else they take alternate tiles.  With 64 or 32
+// rows or fewer the rows are repeated 2 or 4 times down the 128 lanes, and
+// each copy takes its own part (KW = 64 or 32 nodes) of every tile: its P is
+// zero elsewhere, so its O is the sum over its part, and all 128 threads have
+// scores to work on.  The copies, the groups and the splits are joined as
+// separate softmaxes at the end.
+//
+// The maximum a group subtracts trails the true one by at most 2^8 in the
+// weights: O is rescaled (a pass over tensor memory) only when a score
+// exceeds it by more than 8 in units of log2; exact in fp32, and a weight of
+// 256 is no less precise in 16 bits than one of 1.
 #pragma once
 
+#include <type_traits>
+
 #include "k2t_attn.cuh"
+#include "k2t_tc.cuh"
 
 namespace k2t {
 
-template <int DP, int BM> struct FwdSmem {
-    static constexpr int kStages = 3;
-    static constexpr int kTileBytes = kAttnTile * DP * 2;
-    static constexpr int kStageBytes = 2 * kTileBytes;
-    static constexpr int kQ = kStages * kStageBytes;             // Q, then the hop part
-    static constexpr int kHop = kQ + BM * DP * 2;
-    static constexpr int kCol = kHop + (int)((sizeof(HopSmem) + 15) / 16 * 16);
-    static constexpr int kLut = kCol + BM * 4;
-    static size_t bytes(const AttnParams &p) { return kLut + (size_t)(p.buckets + 2) * p.group * 4; }
+constexpr int kTcTile = 128;
+constexpr int kTcThreads = 640;
+constexpr int kTcPitch = 144;       // bytes per column of a bucket tile: 16-byte loads of 8 columns meet no bank twice
+constexpr int kTcBufs = 4;          // bucket tiles
+constexpr int kTcLutAlign = 8192;   // the bias table's alignment, above its size: its address joins an index by OR
+constexpr float kTcLag = 8.0f;
+
+template <int DP, bool TWO> struct TcSmem {
+    static constexpr int kPanel = kTcTile * 128;              // 64 values of 128 rows
+    static constexpr int kSlot = kPanel * (DP / 64);
+    static constexpr int kSlots = DP == 64 ? 8 : TWO ? 4 : 5;
+    static constexpr int kQ = kSlots * kSlot;
+    static constexpr int kBuckets = kQ + kSlot * (TWO ? 2 : 1);
+    static constexpr int kCtl = kBuckets + kTcBufs * 33 * kTcPitch;
+    struct Ctl {
+        uint64_t full[kSlots], empty[kSlots], hop_full[kTcBufs], hop_empty[kTcBufs], s_full[2], p_full[2], o_full[2], drained;
+        uint32_t tmem, gave_up, columns, all;
+        uint32_t seen[kTcBufs][4];
+        uint8_t byte_of[257 + 15];        // bucket byte of hops + 1
+    };
+    static constexpr int kLut = kCtl + (int)((sizeof(Ctl) + 15) / 16 * 16);
+    static size_t bytes(const AttnParams &p) { return kLut + kTcLutAlign + (size_t)(p.buckets + 2) * p.group2 * 4; }
 };
 
-// 4 warps: BM / 16 of them side by side over the rows, the others over the
-// nodes of a tile, each with a softmax of its own, joined at the end.
-template <typename T, int DP, int BM>
-__global__ void __launch_bounds__(kAttnThreads) attn_fwd_kernel(const __grid_constant__ AttnParams p)
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
-    using S = FwdSmem<DP, BM>;
-    constexpr int WM = BM / 16, WK = 4 / WM, KEYS = kAttnTile / WK, N8 = KEYS / 8, D16 = DP / 16;
-    extern __shared__ __align__(128) uint8_t smem[];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t hk = blockIdx.y, split = blockIdx.x % p.splits, row0 = blockIdx.x / p.splits * BM;
-    HopSmem *hs = reinterpret_cast<HopSmem *>(smem + S::kHop);
-    uint32_t *col_of = reinterpret_cast<uint32_t *>(smem + S::kCol);
-    float *lut = reinterpret_cast<float *>(smem + S::kLut);
-    const uint32_t sm = smem_u32(smem);
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(*reinterpret_cast<unsigned long long *>(&d))
+        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)),
+          "l"(*reinterpret_cast<unsigned long long *>(&c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(*reinterpret_cast<unsigned long long *>(&d))
+        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float lds_f(uint32_t at)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+    return v;
+}
 
-    copy_rows<DP, BM>(sm + S::kQ, p.q, p.q_row, p.q_head, hk * p.group, row0, p, tid);
-    cp_commit();
-    if (tid == 0) hs->columns = 0, hs->all = 0;
-    if (p.sources)
-        for (int i = tid; i < 256; i += kAttnThreads) hs->bucket_of[i] = p.bucket_of[i];
-    fill_bias<T>(lut, p, hk, tid);
-    for (int i = tid; i < 4 * kAttnTile; i += kAttnThreads) hs->seen[0][i] = 0;
-    __syncthreads();
-    for (int i = tid; i < BM; i += kAttnThreads) {
-        const uint32_t c = row0 + i < p.rows ? row_column(p, row0 + i) : 0;
-        col_of[i] = c * kHopPitch;
-        if (row0 + i < p.rows && p.sources) {
-            if (c < p.sources) atomicOr(&hs->columns, 1u << c);
-            else hs->all = 1;
+// Scores of 32 nodes in units of log2, biased and masked, and their maximum
+// with `top`.  bt: shared-memory address of their bucket bytes; a byte b's
+// bias lies at lg | b << shift (floats of 2^k query heads, k = shift - 2).
+__device__ __forceinline__ float bias32(uint32_t (&s)[32], float scale, bool plain, uint32_t bt, uint32_t lg, uint32_t shift, float top)
+{
+    const float2 sc = make_float2(scale, scale);
+    if (plain) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+            const float2 x = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc, make_float2(0.0f, 0.0f));
+            s[e] = __float_as_uint(x.x);
+            s[e + 1] = __float_as_uint(x.y);
+            top = max3(top, x.x, x.y);
+        }
+        return top;
+    }
+    const uint32_t mask = 255u << shift;
+#pragma unroll
+    for (int e = 0; e < 32; e += 16) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(bt + e));
+#pragma unroll
+        for (int y = 0; y < 16; y += 2) {
+            const uint32_t v = w[y >> 2];
+            const uint32_t i0 = (y & 3) ? v >> (16 - shift) : v << shift, i1 = (y & 3) ? v >> (24 - shift) : v >> (8 - shift);
+            const float2 bias = make_float2(lds_f((i0 & mask) | lg), lds_f((i1 & mask) | lg));
+            const float2 x = fma2(make_float2(__uint_as_float(s[e + y]), __uint_as_float(s[e + y + 1])), sc, bias);
+            s[e + y] = __float_as_uint(x.x);
+            s[e + y + 1] = __float_as_uint(x.y);
+            top = max3(top, x.x, x.y);
         }
     }
-    __syncthreads();
+    return top;
+}
 
-    const uint64_t tiles = split < p.tiles ? (p.tiles - split + p.splits - 1) / p.splits : 0;
-    auto tile_at = [&](uint64_t i) { return split + i * p.splits; };
-    const char *kbase = static_cast<const char *>(p.k) + hk * p.k_head * 2;
-    const char *vbase = static_cast<const char *>(p.v) + hk * p.v_head * 2;
-    int32_t h[kHopRegs];
-    auto hops_in = [&](uint64_t i) { if (p.sources && i < tiles) hops_load(h, p, tile_at(i), tid); };
-    auto hops_out = [&](uint64_t i, int buf) {
-        if (i >= tiles) return;
-        if (p.sources) hops_store(h, hs, p, tile_at(i), buf, tid);
-        else hops_none(hs, p, tile_at(i), buf, tid);
-    };
-    auto copy = [&](uint64_t i) {
-        if (i < tiles) {
-            const uint32_t st = sm + (uint32_t)(i % S::kStages) * S::kStageBytes;
-            const uint8_t *seen = hs->seen[i & 3];
-            const int64_t node0 = (int64_t)tile_at(i) * kAttnTile;
-            copy_nodes<DP>(st, kbase, p.k_row * 2, node0, p.n, p.d / 8, seen, tid);
-            copy_nodes<DP>(st + S::kTileBytes, vbase, p.v_row * 2, node0, p.n, p.d / 8, seen, tid);
+// Weights of 32 scores, two a word in the element type, and their sum onto `sum`.
+template <typename T>
+__device__ __forceinline__ void weights32(uint32_t (&out)[16], const uint32_t (&s)[32], float m, float2 (&sum)[2])
+{
+    const float2 nm = make_float2(-m, -m);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float2 x = add2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), nm);
+        const float2 y = make_float2(ex2(x.x), ex2(x.y));
+        sum[e & 1] = add2(sum[e & 1], y);
+        out[e] = Elem<T>::pack(y.x, y.y);
+    }
+}
+
+template <typename T, int DP, int KW, bool TWO>
+__global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_constant__ AttnParams p)
+{
+    using S = TcSmem<DP, TWO>;
+    using Ctl = typename S::Ctl;
+    constexpr int kRows = KW;                      // distinct rows per 128 lanes: 128, 64 or 32
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + S::kCtl);
+    const uint32_t sm = tc::saddr(smem);
+    const uint32_t lut_at = (sm + S::kLut + kTcLutAlign - 1) & ~(uint32_t)(kTcLutAlign - 1);
+    float *lut = reinterpret_cast<float *>(smem + (lut_at - sm));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t hk = blockIdx.y, split = blockIdx.x % p.splits;
+    const uint32_t row0 = blockIdx.x / p.splits * (TWO ? 256 : kRows);
+    const uint32_t tiles = (uint32_t)(split < p.tiles ? (p.tiles - split + p.splits - 1) / p.splits : 0);
+    const uint32_t units = TWO ? tiles * 2 : tiles;      // unit u: group u & 1, tile TWO ? u / 2 : u
+    auto tile_at = [&](uint32_t i) { return split + (uint64_t)i * p.splits; };
+
+    // ---- set-up ----
+    if (warp == 16) tc::alloc(&ctl->tmem, 512);
+    if (tid == 0) {
+        for (int i = 0; i < S::kSlots; ++i) tc::bar_init(&ctl->full[i], 128), tc::bar_init(&ctl->empty[i], 1);
+        for (int i = 0; i < kTcBufs; ++i) tc::bar_init(&ctl->hop_full[i], 4), tc::bar_init(&ctl->hop_empty[i], TWO ? 8 : 4);
+        for (int i = 0; i < 2; ++i) {
+            tc::bar_init(&ctl->s_full[i], 1);
+            tc::bar_init(&ctl->p_full[i], 128);
+            tc::bar_init(&ctl->o_full[i], 1);
+        }
+        tc::bar_init(&ctl->drained, 1);
+        ctl->gave_up = ctl->columns = ctl->all = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (p.sources)
+        for (int i = tid; i < 257; i += kTcThreads) ctl->byte_of[i] = i ? p.bucket_of[i - 1] + 1 : 0;
+    fill_bias<T>(lut, p, hk, tid, p.group2);
+    {   // queries: lane l of tile w holds row row0 + w * 128 + l % kRows
+        constexpr int C = DP / 8;
+        const char *src = static_cast<const char *>(p.q);
+        for (int i = tid; i < (TWO ? 256 : 128) * C; i += kTcThreads) {
+            const uint32_t l = i / C, c = i % C, w = l >> 7, r = l & 127;
+            const uint32_t row = row0 + w * 128 + r % kRows;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row < p.rows && c < p.d / 8) {
+                const uint32_t t = row / p.group, g = row - t * p.group;
+                v = __ldg(reinterpret_cast<const uint4 *>(src + ((int64_t)t * p.q_row + (int64_t)(hk * p.group + g) * p.q_head + c * 8) * 2));
+            }
+            *reinterpret_cast<uint4 *>(smem + S::kQ + w * S::kSlot + tc::chunk(r, c, S::kPanel)) = v;
+        }
+    }
+    tc::fence_async();
+    __syncthreads();
+    if (p.sources)
+        for (int i = tid; i < (TWO ? 256 : kRows); i += kTcThreads)
+            if (row0 + i < p.rows) {
+                const uint32_t c = row_column(p, row0 + i);
+                if (c < p.sources) atomicOr(&ctl->columns, 1u << c);
+                else ctl->all = 1;
+            }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tm = ctl->tmem;                       // S of group w at w * 128, O at 256 + w * DP
+    volatile uint32_t *gave_up = &ctl->gave_up;
+
+    if (warp >= 8 && warp < 12) {
+        // ---- hops: lane = node 32 hw + lane of a tile ----
+        const int hw = warp - 8;
+        const uint32_t cols = ctl->columns, B = p.sources;
+        const bool all = ctl->all, every = cols == (B >= 32 ? ~0u : (1u << B) - 1);
+        const bool vec = (B & 3) == 0 && ((uintptr_t)p.hops & 15) == 0;
+        int32_t h[32];
+        auto hops_in = [&](uint32_t i) {
+            const uint64_t node = tile_at(i) * kTcTile + hw * 32 + lane;
+            const bool in = i < tiles && node < p.n;
+            const int32_t *at = p.hops + node * B;
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+                if (c >= (int)B) break;
+                if (vec) {
+                    int4 x = make_int4(-1, -1, -1, -1);
+                    if (in) asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(at + c));
+                    h[c] = x.x, h[c + 1] = x.y, h[c + 2] = x.z, h[c + 3] = x.w;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        h[c + e] = -1;
+                        if (in && c + e < (int)B) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(h[c + e]) : "l"(at + c + e));
+                    }
+                }
+            }
+        };
+        if (B) hops_in(0);
+        for (uint32_t i = 0; i < tiles; ++i) {
+            const uint32_t buf = i % kTcBufs;
+            if (i >= kTcBufs && !__all_sync(~0u, tc::bar_wait(&ctl->hop_empty[buf], (i / kTcBufs - 1) & 1, gave_up))) break;
+            const bool in = tile_at(i) * kTcTile + hw * 32 + lane < p.n;
+            uint8_t *bt = smem + S::kBuckets + buf * 33 * kTcPitch + hw * 32 + lane;
+            int32_t none = -1;                     // sign bit: no column in use sees this node
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+                if (c >= (int)B) break;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    bt[(c + e) * kTcPitch] = ctl->byte_of[min(h[c + e], 255) + 1];   // columns past B: bytes that nothing reads
+                    none &= every || ((cols >> (c + e)) & 1) ? h[c + e] : -1;
+                }
+            }
+            bt[B * kTcPitch] = in ? p.buckets + 1 : 0;
+            const uint32_t seen = __ballot_sync(~0u, in && (!B || all || none >= 0));
+            __syncwarp();
+            if (lane == 0) {
+                ctl->seen[buf][hw] = seen;
+                tc::bar_arrive(&ctl->hop_full[buf]);
+            }
+            if (B) hops_in(i + 1);
+        }
+    } else if (warp >= 12 && warp < 16) {
+        // ---- copies: this warp brings nodes [32 cw, 32 cw + 32) of every tile ----
+        const int cw = warp - 12;
+        constexpr int C = DP / 8, RP = 32 / C, kTurn = 8 / RP;     // chunks a row, rows a pass, passes until the swizzle repeats
+        const uint32_t c = lane % C, r0 = lane / C;
+        const uint32_t fill = (p.d / 8 + 1) & ~1u;                 // chunks the products read: whole steps of 16 values
+        uint32_t at[kTurn];
+#pragma unroll
+        for (int k = 0; k < kTurn; ++k) at[k] = sm + tc::chunk(cw * 32 + k * RP + r0, c, S::kPanel) - k * RP * 128;
+        uint32_t item = 0;
+        bool ok = true;
+        auto bring = [&](const char *src, int64_t step, uint32_t seen) {
+            const uint32_t slot = item % S::kSlots;
+            if (item >= (uint32_t)S::kSlots) ok = __all_sync(~0u, tc::bar_wait(&ctl->empty[slot], (item / S::kSlots - 1) & 1, gave_up));
+            if (!ok) return;
+            if (c < fill) {
+#pragma unroll
+                for (int k = 0; k < 32 / RP; ++k) {
+                    // a node that no query sees, or past n, or a chunk past head_dim: zeros, and nothing is read
+                    cp16(at[k % kTurn] + slot * S::kSlot + k * RP * 128, src, (seen >> (k * RP)) & 1 ? 16 : 0);
+                    src += step;
+                }
+            }
+            tc::cp_arrive(&ctl->full[slot]);      // counts this thread's copies once they have landed
+            ++item;
+        };
+        const int64_t kstep = RP * p.k_row * 2, vstep = RP * p.v_row * 2;
+        const char *k0 = static_cast<const char *>(p.k) + ((int64_t)hk * p.k_head + c * 8) * 2;
+        const char *v0 = static_cast<const char *>(p.v) + ((int64_t)hk * p.v_head + c * 8) * 2;
+        for (uint32_t i = 0; i < tiles && ok; ++i) {
+            const uint32_t buf = i % kTcBufs;
+            ok = __all_sync(~0u, tc::bar_wait(&ctl->hop_full[buf], (i / kTcBufs) & 1, gave_up));
+            if (!ok) break;
+            const uint32_t seen = c < p.d / 8 ? ctl->seen[buf][cw] >> r0 : 0;
+            const int64_t node = (int64_t)(tile_at(i) * kTcTile) + cw * 32 + r0;
+            bring(k0 + node * p.k_row * 2, kstep, seen);
+            if (ok) bring(v0 + node * p.v_row * 2, vstep, seen);
         }
         cp_commit();
-    };
-    hops_in(0); hops_out(0, 0);
-    hops_in(1); hops_out(1, 1);
-    hops_in(2);
-    __syncthreads();
-    copy(0);
-    copy(1);
-    cp_wait<2>();
-    __syncthreads();
-
-    const int wm = warp % WM, wk = warp / WM;
-    uint32_t q[D16][4];
-#pragma unroll
-    for (int i = 0; i < D16; ++i) load_a<DP>(q[i], sm + S::kQ, wm * 16, i, lane);
-    const int ra = wm * 16 + (lane >> 2), rb = ra + 8;                  // this thread's two rows
-    const uint32_t ca = col_of[ra], cb = col_of[rb];
-    const float *lut_a = lut + (row0 + ra) % p.group, *lut_b = lut + (row0 + rb) % p.group;
-    const uint32_t G = p.group;
-
-    float o[DP / 8][4];
-#pragma unroll
-    for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float ma = -INFINITY, mb = -INFINITY, la = 0.0f, lb = 0.0f;
-
-    for (uint64_t i = 0; i < tiles; ++i) {
-        hops_out(i + 2, (i + 2) & 3);
-        if (tid < kAttnTile) hs->seen[(i + 3) & 3][tid] = 0;
-        cp_wait<1>();
-        __syncthreads();
-        copy(i + 2);
-        hops_in(i + 3);
-
-        const uint32_t ks = sm + (uint32_t)(i % S::kStages) * S::kStageBytes, vs = ks + S::kTileBytes;
-        const uint8_t *bt = hs->tile[i & 3] + wk * KEYS + (lane & 3) * 2;
-        float s[N8][4];
-#pragma unroll
-        for (int j = 0; j < N8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
-#pragma unroll
-        for (int kk = 0; kk < D16; ++kk)
-#pragma unroll
-            for (int j = 0; j < N8; j += 2) {
-                uint32_t b[4];
-                load_b<DP>(b, ks, wk * KEYS + j * 8, kk, lane);
-                Elem<T>::mma(s[j], q[kk], b[0], b[1]);
-                Elem<T>::mma(s[j + 1], q[kk], b[2], b[3]);
+        cp_wait<0>();
+    } else if (warp >= 16) {
+        if (warp == 16 && lane == 0) {
+            // ---- products ----
+            const uint32_t id_s = tc::idesc(kBf16, kTcTile, false, false);
+            const uint32_t dn = (p.d + 15) & ~15u, id_o = tc::idesc(kBf16, dn, false, true);
+            const uint32_t base = sm;
+            bool ok = true;
+            auto scores = [&](uint32_t u) {
+                const uint32_t w = u & 1, i = TWO ? u >> 1 : u, item = 2 * i, slot = item % S::kSlots;
+                ok = tc::bar_wait(&ctl->full[slot], (item / S::kSlots) & 1, gave_up);
+                if (!ok) return;
+                tc::fence_async();       // the copies were made by threads, the product reads through the async proxy
+                tc::fence_after();
+                const uint32_t q = base + S::kQ + (TWO ? w * S::kSlot : 0), k = base + slot * S::kSlot;
+                for (uint32_t kk = 0; kk < dn / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * S::kPanel + (kk & 3) * 32;
+                    tc::mma_ss(tm + w * 128, tc::desc(q + off, S::kPanel), tc::desc(k + off, S::kPanel), id_s, kk > 0);
+                }
+                tc::commit(&ctl->s_full[w]);
+                if (!TWO || w == 1) tc::commit(&ctl->empty[slot]);
+            };
+            if (units > 0) scores(0);
+            if (ok && units > 1) scores(1);
+            for (uint32_t u = 0; u < units && ok; ++u) {
+                const uint32_t w = u & 1, i = TWO ? u >> 1 : u, item = 2 * i + 1, slot = item % S::kSlots;
+                ok = tc::bar_wait(&ctl->full[slot], (item / S::kSlots) & 1, gave_up) &&
+                     tc::bar_wait(&ctl->p_full[w], (u >> 1) & 1, gave_up);
+                if (!ok) break;
+                tc::fence_async();
+                tc::fence_after();
+                const uint32_t v = base + slot * S::kSlot;
+                for (uint32_t kk = 0; kk < kTcTile / 16; ++kk)
+                    tc::mma_ts(tm + 256 + w * DP, tm + w * 128 + kk * 8, tc::desc(v + kk * 2048, S::kPanel), id_o, u > 1 || kk > 0);
+                if (!TWO || w == 1) tc::commit(&ctl->empty[slot]);
+                if (u + 2 >= units) tc::commit(&ctl->o_full[w]);
+                if (u + 2 < units) scores(u + 2);
             }
-        float xa = -INFINITY, xb = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < N8; ++j) {
-            const uint32_t ba = *reinterpret_cast<const uint16_t *>(bt + ca + j * 8);
-            const uint32_t bb = *reinterpret_cast<const uint16_t *>(bt + cb + j * 8);
-            s[j][0] = fmaf(s[j][0], p.scale_log2, lut_a[(ba & 255) * G]);
-            s[j][1] = fmaf(s[j][1], p.scale_log2, lut_a[(ba >> 8) * G]);
-            s[j][2] = fmaf(s[j][2], p.scale_log2, lut_b[(bb & 255) * G]);
-            s[j][3] = fmaf(s[j][3], p.scale_log2, lut_b[(bb >> 8) * G]);
-            xa = fmaxf(xa, fmaxf(s[j][0], s[j][1]));
-            xb = fmaxf(xb, fmaxf(s[j][2], s[j][3]));
+            if (!ok) tc::drain(&ctl->drained, 0);
         }
-        xa = fmaxf(xa, __shfl_xor_sync(~0u, xa, 1));
-        xb = fmaxf(xb, __shfl_xor_sync(~0u, xb, 1));
-        xa = fmaxf(xa, __shfl_xor_sync(~0u, xa, 2));
-        xb = fmaxf(xb, __shfl_xor_sync(~0u, xb, 2));
-        // a row that has seen nothing yet keeps m = -inf; 0 stands in for it, so that no inf - inf arises
-        const float na = fmaxf(ma, xa), nb = fmaxf(mb, xb);
-        const float ua = na == -INFINITY ? 0.0f : na, ub = nb == -INFINITY ? 0.0f : nb;
-        const float fa = ex2(ma - ua), fb = ex2(mb - ub);
-        ma = na;
-        mb = nb;
-        la *= fa;
-        lb *= fb;
-#pragma unroll
-        for (int j = 0; j < DP / 8; ++j) o[j][0] *= fa, o[j][1] *= fa, o[j][2] *= fb, o[j][3] *= fb;
-#pragma unroll
-        for (int j = 0; j < N8; ++j) {
-            s[j][0] = ex2(s[j][0] - ua);
-            s[j][1] = ex2(s[j][1] - ua);
-            s[j][2] = ex2(s[j][2] - ub);
-            s[j][3] = ex2(s[j][3] - ub);
-            la += s[j][0] + s[j][1];
-            lb += s[j][2] + s[j][3];
-        }
-#pragma unroll
-        for (int j = 0; j < N8; j += 2) {
-            // weights rounded to the element type: they are at most 1, so fp16 holds them too, and their
-            // errors are independent and average out over the nodes
-            const uint32_t a[4] = {Elem<T>::pack(s[j][0], s[j][1]), Elem<T>::pack(s[j][2], s[j][3]),
-                                   Elem<T>::pack(s[j + 1][0], s[j + 1][1]), Elem<T>::pack(s[j + 1][2], s[j + 1][3])};
-#pragma unroll
-            for (int c = 0; c < D16; ++c) {
-                uint32_t b[4];
-                load_bt<DP>(b, vs, wk * KEYS + j * 8, c, lane);
-                Elem<T>::mma(o[2 * c], a, b[0], b[1]);
-                Elem<T>::mma(o[2 * c + 1], a, b[2], b[3]);
-            }
-        }
-    }
-    cp_wait<0>();
-    la += __shfl_xor_sync(~0u, la, 1);
-    lb += __shfl_xor_sync(~0u, lb, 1);
-    la += __shfl_xor_sync(~0u, la, 2);
-    lb += __shfl_xor_sync(~0u, lb, 2);
-
-    // join the WK warps that share rows, through the freed stages: [wk][row][DP + 2] floats
-    constexpr int P = DP + 4;
-    float *ex = reinterpret_cast<float *>(smem);
-    static_assert(WK * BM * P * 4 <= S::kQ, "exchange fits the stages");
-    __syncthreads();
-    {
-        float *ea = ex + (size_t)(wk * BM + ra) * P, *eb = ex + (size_t)(wk * BM + rb) * P;
-#pragma unroll
-        for (int j = 0; j < DP / 8; ++j) {
-            *reinterpret_cast<float2 *>(ea + j * 8 + (lane & 3) * 2) = make_float2(o[j][0], o[j][1]);
-            *reinterpret_cast<float2 *>(eb + j * 8 + (lane & 3) * 2) = make_float2(o[j][2], o[j][3]);
-        }
-        if ((lane & 3) == 0) ea[DP] = ma, ea[DP + 1] = la, eb[DP] = mb, eb[DP + 1] = lb;
-    }
-    __syncthreads();
-    constexpr int Q4 = DP / 4;
-    for (int i = tid; i < BM * Q4; i += kAttnThreads) {
-        const int r = i / Q4, c = (i % Q4) * 4;
-        const uint32_t row = row0 + r;
-        if (row >= p.rows || c >= (int)p.d) continue;
+        __syncwarp();
+    } else {
+        // ---- softmax: thread = lane of tensor memory ----
+        const int w = warp >> 2, l = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // lane field of this warp's tensor memory
+        const uint32_t row = row0 + (TWO ? w * 128 : 0) + l % kRows;
+        const int key0 = l / kRows * KW;                              // this copy's part of a tile
+        const uint32_t col = row < p.rows ? row_column(p, row) : 0;
+        const uint32_t G = p.group, lg = lut_at | (row < p.rows ? row % G : 0) * 4, shift = p.group2_log + 2;
+        const uint32_t s_at = tm + lanes + w * 128, o_at = tm + lanes + 256 + w * DP;
+        const uint32_t bt0 = sm + S::kBuckets + col * kTcPitch + key0;
         float m = -INFINITY;
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        bool ok = true;
+        uint32_t mine = 0;                                            // units of this group done
+        for (uint32_t u = w; u < units; u += 2, ++mine) {
+            const uint32_t i = TWO ? u >> 1 : u, buf = i % kTcBufs;
+            ok = tc::bar_wait(&ctl->hop_full[buf], (i / kTcBufs) & 1, gave_up) && tc::bar_wait(&ctl->s_full[w], mine & 1, gave_up);
+            ok = __all_sync(~0u, ok);
+            if (!ok) break;
+            tc::fence_after();
+            const bool plain = !p.sources && (tile_at(i) + 1) * kTcTile <= p.n;   // no table, no node past the end
+            const uint32_t bt = bt0 + buf * 33 * kTcPitch;
+            float top = -INFINITY;
+            uint32_t s[32];
+            if (KW == 32) {
+                tc::ld32(s, s_at + key0);
+                tc::wait_ld();
+                top = bias32(s, p.scale_log2, plain, bt, lg, shift, top);
+            } else {
+                // scores go back to tensor memory between the two passes: rolled loops of 32 nodes, since the whole
+                // row in registers makes code that the instruction caches do not hold
+#pragma unroll 1
+                for (int b = 0; b < KW; b += 32) {
+                    tc::ld32(s, s_at + key0 + b);
+                    tc::wait_ld();
+                    top = bias32(s, p.scale_log2, plain, bt + b, lg, shift, top);
+                    tc::st32(s_at + key0 + b, s);
+                }
+                tc::wait_st();
+            }
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(&ctl->hop_empty[buf]);
+            const bool grow = top > m + kTcLag || (m == -INFINITY && top > -INFINITY);
+            if (__any_sync(~0u, grow)) {
+                const float next = grow ? top : m;
+                const float f = m == -INFINITY ? 0.0f : ex2(m - next);      // m = -inf: nothing was summed yet
+                m = next;
 #pragma unroll
-        for (int w = 0; w < WK; ++w) m = fmaxf(m, ex[(size_t)(w * BM + r) * P + DP]);
-        const float u = m == -INFINITY ? 0.0f : m;
-        float l = 0.0f;
-        float4 acc = make_float4(0, 0, 0, 0);
+                for (int e = 0; e < 2; ++e) sum[e].x *= f, sum[e].y *= f;
+                if (mine > 0) {
+                    // the products issued before these scores are done, so O is at rest
+#pragma unroll 1
+                    for (int c = 0; c < DP; c += 32) {
+                        uint32_t o[32];
+                        tc::ld32(o, o_at + c);
+                        tc::wait_ld();
 #pragma unroll
-        for (int w = 0; w < WK; ++w) {
-            const float *e = ex + (size_t)(w * BM + r) * P;
-            const float f = ex2(e[DP] - u);
-            const float4 x = *reinterpret_cast<const float4 *>(e + c);
-            l += f * e[DP + 1];
-            acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tc::st32(o_at + c, o);
+                    }
+                }
+            }
+            const float u0 = m == -INFINITY ? 0.0f : m;
+            // weights in the element type, two a word, over S: nodes of the other copies' parts weigh nothing
+            if (KW == 128) {
+#pragma unroll 1
+                for (int b = 0; b < 128; b += 32) {
+                    uint32_t out[16];
+                    tc::ld32(s, s_at + b);
+                    tc::wait_ld();
+                    weights32<T>(out, s, u0, sum);
+                    tc::st16(s_at + b / 2, out);
+                }
+            } else {
+                uint32_t out[KW / 32][16];
+#pragma unroll
+                for (int b = 0; b < KW / 32; ++b) {
+                    if (KW != 32) {
+                        tc::ld32(s, s_at + key0 + b * 32);
+                        tc::wait_ld();
+                    }
+                    weights32<T>(out[b], s, u0, sum);
+                }
+                const uint32_t zero[16] = {};
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (q * 32 / KW == l / kRows) tc::st16(s_at + q * 16, out[q % (KW / 32)]);
+                    else tc::st16(s_at + q * 16, zero);
+            }
+            tc::wait_st();
+            tc::fence_before();
+            tc::bar_arrive(&ctl->p_full[w]);
         }
-        const uint32_t t = row / p.group, hd = hk * p.group + row % p.group;
-        if (p.splits > 1) {
-            const uint64_t at = ((uint64_t)split * p.T + t) * p.hq + hd;
-            *reinterpret_cast<float4 *>(p.part + at * p.d + c) = acc;
-            if (c == 0) *reinterpret_cast<float2 *>(p.part_ml + at * 2) = make_float2(m, l);
-        } else {
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            uint2 w;
-            w.x = Elem<T>::pack(acc.x * inv, acc.y * inv);
-            w.y = Elem<T>::pack(acc.z * inv, acc.w * inv);
-            *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (int64_t)t * p.out_row + (int64_t)hd * p.out_head + c) = w;
-            if (c == 0) p.lse[(uint64_t)t * p.hq + hd] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        // ---- join the copies and groups through the freed slots: [group][lane][DP + 4] ----
+        if (ok && mine > 0) {
+            ok = tc::bar_wait(&ctl->o_full[w], 0, gave_up);
+            tc::fence_after();
         }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        ok = !*gave_up;
+        constexpr int P = DP + 4;
+        static_assert(256 * P * 4 <= S::kBuckets, "the exchange fits the slots and queries");
+        float *ex = reinterpret_cast<float *>(smem);
+        if (ok) {
+            float *at = ex + (size_t)(w * 128 + l) * P;
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 32) {
+                uint32_t o[32];
+                if (mine > 0) {
+                    tc::ld32(o, o_at + c);
+                    tc::wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4 *>(at + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+            at[DP] = m;
+            at[DP + 1] = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        constexpr int kSets = TWO ? 1 : 2 * (128 / kRows), kOut = TWO ? 256 : kRows, Q4 = DP / 4;
+        if (ok)
+            for (int i = tid; i < kOut * Q4; i += 256) {
+                const int r = i / Q4, c = (i % Q4) * 4;
+                const uint32_t rw = row0 + r;
+                if (rw >= p.rows || c >= (int)p.d) continue;
+                const float *e0 = ex + (size_t)r * P;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < kSets; ++k) mx = fmaxf(mx, e0[(size_t)k * kRows * P + DP]);
+                const float ux = mx == -INFINITY ? 0.0f : mx;
+                float ls = 0.0f;
+                float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int k = 0; k < kSets; ++k) {
+                    const float *e = e0 + (size_t)k * kRows * P;
+                    const float f = ex2(e[DP] - ux);
+                    const float4 x = *reinterpret_cast<const float4 *>(e + c);
+                    ls += f * e[DP + 1];
+                    acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
+                }
+                const uint32_t t = rw / G, hd = hk * G + rw - t * G;
+                if (p.splits > 1) {
+                    const uint64_t at = ((uint64_t)split * p.T + t) * p.hq + hd;
+                    *reinterpret_cast<float4 *>(p.part + at * p.d + c) = acc;
+                    if (c == 0) *reinterpret_cast<float2 *>(p.part_ml + at * 2) = make_float2(mx, ls);
+                } else {
+                    const float inv = ls > 0.0f ? 1.0f / ls : 0.0f;
+                    uint2 o2;
+                    o2.x = Elem<T>::pack(acc.x * inv, acc.y * inv);
+                    o2.y = Elem<T>::pack(acc.z * inv, acc.w * inv);
+                    *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (int64_t)t * p.out_row + (int64_t)hd * p.out_head + c) = o2;
+                    if (c == 0) p.lse[(uint64_t)t * p.hq + hd] = ls > 0.0f ? (mx + log2f(ls)) * kLn2 : -INFINITY;
+                }
+            }
     }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 16) tc::dealloc(tm, 512);
+    if (tid == 0 && *gave_up) atomicOr(p.status, K2T_STATUS_WAIT_TIMEOUT);
 }
 
 // Joins the splits of each row: M = max m_i, out = sum O_i 2^(m_i - M) / sum l_i 2^(m_i - M).

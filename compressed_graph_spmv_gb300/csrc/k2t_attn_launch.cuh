@@ -24,15 +24,20 @@ int attn_launch(K kernel, dim3 grid, int threads, size_t smem, const AttnParams 
     return K2T_OK;
 }
 
-template <typename T, int DP, int BM> int forward_tile(const AttnParams &p, cudaStream_t st)
+// bm: rows a block takes, 32, 64, 128 or 256.
+template <typename T, int DP, int KW, bool TWO> int forward_tile(const AttnParams &p, cudaStream_t st)
 {
-    return attn_launch(attn_fwd_kernel<T, DP, BM>, dim3(p.splits * p.row_tiles, p.hkv), kAttnThreads,
-                       FwdSmem<DP, BM>::bytes(p), p, st);
+    return attn_launch(attn_fwd_kernel<T, DP, KW, TWO>, dim3(p.splits * p.row_tiles, p.hkv), kTcThreads, TcSmem<DP, TWO>::bytes(p), p, st);
 }
 
 template <typename T, int DP> int forward_dim(const AttnParams &p, int bm, cudaStream_t st)
 {
-    return bm == 16 ? forward_tile<T, DP, 16>(p, st) : bm == 32 ? forward_tile<T, DP, 32>(p, st) : forward_tile<T, DP, 64>(p, st);
+    switch (bm) {
+    case 32: return forward_tile<T, DP, 32, false>(p, st);
+    case 64: return forward_tile<T, DP, 64, false>(p, st);
+    case 128: return forward_tile<T, DP, 128, false>(p, st);
+    default: return forward_tile<T, DP, 128, true>(p, st);
+    }
 }
 
 template <typename T> int launch_forward(const AttnParams &p, int bm, cudaStream_t st)

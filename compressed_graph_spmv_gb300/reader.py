@@ -93,9 +93,18 @@ class HopAttention:
     def _work_of(self, backward: int):
         if self._work[backward] is None:
             self._bytes[backward] = self.work_bytes(bool(backward))
-            self._work[backward] = self._torch.empty(max(16, self._bytes[backward]), dtype=self._torch.uint8,
-                                                     device=self.device)
+            self._work[backward] = self._torch.empty(self._bytes[backward], dtype=self._torch.uint8, device=self.device)
+            self._work[backward][:4].zero_()
         return self._work[backward].data_ptr(), self._bytes[backward]
+
+    def status(self) -> int:
+        """The device status words of both passes, joined: waits for the device; 0, or
+        ``k2t.STATUS_WAIT_TIMEOUT`` once a bounded wait ran out in a call of this object."""
+        word = 0
+        for work in self._work:
+            if work is not None:
+                word |= int(work[:4].view(self._torch.int32).item())
+        return word
 
     def _rows_in(self, name, t, shape):
         a = self._a

@@ -355,7 +355,10 @@ K2T_API uint64_t k2t_msbfs_work_bytes(const k2t_tree *t);
  * node states) to the layers of a model that reads the graph.  They need no
  * tree.  All tensors are device memory of the caller; every call is
  * asynchronous on `stream`, allocates nothing and writes only its outputs and
- * `work`.  A work buffer may be shared by calls that are ordered on the GPU.
+ * `work`.  The first 4 bytes of an attention call's `work` are its device
+ * status word: a kernel sets K2T_STATUS_WAIT_TIMEOUT there when a bounded wait
+ * ran out (outputs are then undefined) and never clears it; a caller that
+ * wants to know zeroes the word beforehand and reads it after the stream.  A work buffer may be shared by calls that are ordered on the GPU.
  * Results do not depend on the order in which blocks run.                    */
 
 /* Element types. */

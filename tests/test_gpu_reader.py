@@ -87,6 +87,7 @@ def run(p, dtype, scale=None, backward=True, poison=True):
         for b in (0, 1):
             op._work_of(b)
             op._work[b].fill_(0xff)
+            op._work[b][:4].zero_()   # the status word is the caller's to clear
     op.forward(p["q"], p["k"], p["v"], out, lse, **table_of(p))
     got = dict(out=out, lse=lse)
     if backward:
@@ -95,6 +96,7 @@ def run(p, dtype, scale=None, backward=True, poison=True):
         op.backward(p["dout"], p["q"], p["k"], p["v"], out, lse, g["dq"], g["dk"], g["dv"], dbias=db, **table_of(p))
         got |= g | dict(dbias=db)
     torch.cuda.synchronize()
+    assert op.status() == 0
     return got
 
 
@@ -134,10 +136,11 @@ def test_attention_matches(T, n, hq, hkv, d, sources, buckets, mapped, dtype):
     check(p, dtype, run(p, dtype))
 
 
-@pytest.mark.parametrize("T,hq,hkv", [(1, 4, 4), (20, 4, 1), (32, 8, 4)])
-def test_attention_many_nodes(T, hq, hkv):
-    """Enough nodes that every block of the split takes several tiles."""
-    p = problem(T, 40000, hq, hkv, 64, T, 16, "bf16", False, seed=7)
+@pytest.mark.parametrize("T,hq,hkv,d", [(1, 4, 4, 64), (20, 4, 1, 64), (32, 8, 4, 64), (2, 2, 2, 128), (32, 4, 2, 128),
+                                        (32, 3, 1, 128), (150, 2, 1, 128), (140, 2, 1, 64), (300, 1, 1, 72)])
+def test_attention_many_nodes(T, hq, hkv, d):
+    """Enough nodes that every block of the split takes many tiles."""
+    p = problem(T, 40000 if T <= 32 else 20000, hq, hkv, d, min(T, 32), 16, "bf16", T > 32, seed=7)
     check(p, "bf16", run(p, "bf16"))
 
 
