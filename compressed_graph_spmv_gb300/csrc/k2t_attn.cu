@@ -35,11 +35,11 @@ bool aligned(const void *p, int64_t row, int64_t head) { return !((uintptr_t)p &
 constexpr uint64_t kSms = 152;
 
 // Blocks that share the nodes of one (head, row tile): as many as make the
-// fewest rounds of the GPU's SMs times tiles a block, with two tiles' time for
-// a block's start and end.  `per_sm` blocks run on an SM at once.
-uint32_t pick_splits(uint64_t blocks, uint64_t tiles, uint64_t per_sm)
+// fewest rounds of the GPU's SMs (one block each) times tiles a block, with
+// two tiles' time for a block's start and end.
+uint32_t pick_splits(uint64_t blocks, uint64_t tiles)
 {
-    const uint64_t slots = kSms * per_sm, most = std::min<uint64_t>(std::max<uint64_t>(1, tiles), slots);
+    const uint64_t slots = kSms, most = std::min<uint64_t>(std::max<uint64_t>(1, tiles), slots);
     uint64_t best = 1, cost = ~0ull;
     for (uint64_t s = 1; s <= most; ++s) {
         const uint64_t rounds = (blocks * s + slots - 1) / slots, c = rounds * ((tiles + s - 1) / s + 2);
@@ -51,7 +51,7 @@ uint32_t pick_splits(uint64_t blocks, uint64_t tiles, uint64_t per_sm)
 struct Plan {
     AttnParams p;
     int bm;
-    uint64_t part_floats, ml_floats, delta_floats;
+    uint64_t part_floats, ml_floats, info_floats;
 };
 
 void make_plan(const k2t_attn *a, bool backward, Plan &pl)
@@ -69,27 +69,36 @@ void make_plan(const k2t_attn *a, bool backward, Plan &pl)
     p.rows = p.T * p.group;
     while ((1u << p.group2_log) < p.group) ++p.group2_log;
     p.group2 = 1u << p.group2_log;
-    p.hop_magic = p.sources ? (65536 + p.sources - 1) / p.sources : 0;
     p.scale = a->scale;
     p.scale_log2 = a->scale * kLog2e;
-    // rows per block: the smallest tile that holds them all, since the states are read once per row tile
-    pl.bm = backward ? kBwdRows : p.rows <= 32 ? 32 : p.rows <= 64 ? 64 : p.rows <= 128 ? 128 : 256;
-    const int tile = backward ? kAttnTile : kTcTile;
-    p.tiles = (p.n + tile - 1) / tile;
-    p.row_tiles = std::max(1u, (p.rows + pl.bm - 1) / pl.bm);
-    const uint64_t blocks = (uint64_t)p.hkv * p.row_tiles;
-    p.splits = pick_splits(blocks, p.tiles, backward ? 2 : 1);
+    p.tiles = (p.n + kTcTile - 1) / kTcTile;
     const uint64_t rows = (uint64_t)p.T * p.hq;
-    pl.part_floats = backward || p.splits > 1 ? p.splits * rows * p.d : 0;
-    pl.ml_floats = backward ? p.splits * rows * p.buckets : p.splits > 1 ? p.splits * rows * 2 : 0;
-    pl.delta_floats = backward ? rows : 0;
+    if (backward) {
+        const uint32_t per = kBwdRows / p.group;              // whole queries of a row tile
+        p.row_tiles = std::max(1u, (p.T + per - 1) / per);
+        const uint32_t fused = bwd_fused_tiles(p.d), held = p.row_tiles <= fused ? fused : 4;
+        const uint32_t groups = (p.row_tiles + held - 1) / held;
+        p.splits = pick_splits((uint64_t)p.hkv * groups, p.tiles);
+        p.hist_parts = p.splits * groups;
+        pl.part_floats = p.splits * rows * p.d;
+        pl.ml_floats = (uint64_t)p.hist_parts * p.hq * p.buckets;
+        pl.info_floats = (uint64_t)p.hkv * p.row_tiles * (sizeof(RowInfo) / 4);
+        return;
+    }
+    // rows per block: the fewest lanes that hold them all, since the states are read once per row block
+    pl.bm = p.rows <= 32 ? 32 : p.rows <= 64 ? 64 : p.rows <= 128 ? 128 : 256;
+    p.row_tiles = std::max(1u, (p.rows + pl.bm - 1) / pl.bm);
+    p.splits = pick_splits((uint64_t)p.hkv * p.row_tiles, p.tiles);
+    pl.part_floats = p.splits > 1 ? p.splits * rows * p.d : 0;
+    pl.ml_floats = p.splits > 1 ? p.splits * rows * 2 : 0;
+    pl.info_floats = 0;
 }
 
 constexpr uint64_t kWorkHead = 256;   // the device status word
 
 uint64_t plan_bytes(const Plan &pl)
 {
-    return kWorkHead + align_up(pl.part_floats * 4, 256) + align_up(pl.ml_floats * 4, 256) + align_up(pl.delta_floats * 4, 256);
+    return kWorkHead + align_up(pl.part_floats * 4, 256) + align_up(pl.ml_floats * 4, 256) + align_up(pl.info_floats * 4, 256);
 }
 
 int check_call(const k2t_attn *a, const void *work, uint64_t work_bytes, const Plan &pl)
@@ -124,7 +133,7 @@ void fill_pointers(const k2t_attn *a, void *work, Plan &pl)
     char *w = static_cast<char *>(work) + kWorkHead;
     p.part = reinterpret_cast<float *>(w);
     p.part_ml = reinterpret_cast<float *>(w + align_up(pl.part_floats * 4, 256));
-    p.delta = reinterpret_cast<float *>(w + align_up(pl.part_floats * 4, 256) + align_up(pl.ml_floats * 4, 256));
+    p.row_info = reinterpret_cast<float *>(w + align_up(pl.part_floats * 4, 256) + align_up(pl.ml_floats * 4, 256));
     uint32_t b = 0;
     for (uint32_t x = 0; x < 256; ++x) {
         while (b + 1 < a->n_buckets && a->edges[b + 1] <= x) ++b;

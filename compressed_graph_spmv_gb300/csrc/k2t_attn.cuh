@@ -1,12 +1,12 @@
 // k2t_attn.cuh -- attention of queries to node states with a hop-bucket bias:
-// kernels on warp-level matrix instructions (m16n8k16, fp32 accumulators).
+// what its forward and backward kernels share.
 //
 // Rows of one key/value head hk are r = t * G + g (query t, head hk * G + g,
 // G query heads share hk), so the states of hk are read once for all of them.
 // Scores are kept in units of log2: s2 = (q.k) * scale * log2(e) + bias *
 // log2(e), so that a weight is one exp2.
 //
-// Hop tables.  A tile of 64 nodes brings its 64 x n_sources hops; each is
+// Hop tables.  A tile of 128 nodes brings its 128 x n_sources hops; each is
 // turned into a byte once: 0 masked, 1 + bucket, and in one more column
 // n_buckets + 1 for queries without hop information.  The bytes are stored
 // [column][node], so that the lanes of a score tile read neighbouring ones,
@@ -22,14 +22,14 @@
 #include <cstdint>
 
 #include "k2t_internal.h"
+#include "k2t_tc.cuh"
 
 namespace k2t {
 
 extern thread_local int g_last_cuda;
 
-constexpr int kAttnTile = 64;          // nodes per tile
-constexpr int kAttnThreads = 128;
-constexpr int kHopPitch = 68;          // bytes per column of a bucket tile: 17 words, odd, so that 8 columns differ in bank
+constexpr int kTcTile = 128;           // nodes per tile
+constexpr int kTcPitch = 144;          // bytes per column of a bucket tile: 16-byte loads of 8 columns meet no bank twice
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -41,8 +41,7 @@ struct AttnParams {
     uint32_t group2, group2_log;  // group rounded up to a power of two
     uint32_t row_tiles;
     uint32_t splits;          // blocks that share the nodes of one head
-    uint64_t tiles;           // ceil(n / kAttnTile)
-    uint32_t hop_magic;       // ceil(2^16 / sources): i / sources for i < 64 * 32
+    uint64_t tiles;           // ceil(n / kTcTile)
     float scale, scale_log2;
     const void *q, *k, *v, *dout;
     const int32_t *hops, *qsrc;
@@ -53,7 +52,8 @@ struct AttnParams {
     int64_t dq_row, dq_head, dk_row, dk_head, dv_row, dv_head;
     float *part;              // partial sums: see the kernels
     float *part_ml;
-    float *delta;
+    void *row_info;           // RowInfo[hkv][row_tiles * 32] (backward)
+    uint32_t hist_parts;      // partial dbias tables
     uint32_t *status;         // device status word, at the start of the work buffer
     uint8_t bucket_of[256];   // bucket of each hop count; larger hops share the last
 };
@@ -73,12 +73,6 @@ template <> struct Elem<__nv_bfloat16> {
     static __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
     static __device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
     static constexpr float kMasked = -1e38f;      // table entries not above this mask
-    static __device__ __forceinline__ void mma(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1)
-    {
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
 };
 template <> struct Elem<__half> {
     static __device__ __forceinline__ uint32_t pack(float a, float b)
@@ -90,97 +84,20 @@ template <> struct Elem<__half> {
     static __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
     static __device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
     static constexpr float kMasked = -65504.0f;
-    static __device__ __forceinline__ void mma(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1)
-    {
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
 };
 
 // ---- small PTX wrappers ---------------------------------------------------
-__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t bytes)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ void ldsm4(uint32_t r[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t r[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// Byte address of 16-byte chunk c of row r in a tile of DP 2-byte values a
-// row: the chunk index is xored with the row, so that the 8 rows of one
-// matrix load lie in 8 different bank groups (the row pitch is a multiple of
-// 128 bytes).
-template <int DP> __device__ __forceinline__ uint32_t tile_addr(uint32_t base, int r, int c)
-{
-    return base + r * (DP * 2) + ((c ^ (r & 7)) << 4);
-}
-
-// Fragment loads from such a tile.  lane-dependent row/chunk of an x4 load:
-// matrices 0..3 = (rows 0-7, k 0-7), (rows 8-15, k 0-7), (rows 0-7, k 8-15),
-// (rows 8-15, k 8-15): an A operand of 16 rows x 16 k.
-template <int DP> __device__ __forceinline__ void load_a(uint32_t a[4], uint32_t base, int row0, int k16, int lane)
-{
-    ldsm4(a, tile_addr<DP>(base, row0 + (lane & 15), k16 * 2 + (lane >> 4)));
-}
-// B operand for k = 16 along the row, n = 16 rows (two n8 blocks): b[0], b[1]
-// of the first block, b[2], b[3] of the second.
-template <int DP> __device__ __forceinline__ void load_b(uint32_t b[4], uint32_t base, int row0, int k16, int lane)
-{
-    ldsm4(b, tile_addr<DP>(base, row0 + (lane & 7) + ((lane >> 4) << 3), k16 * 2 + ((lane >> 3) & 1)));
-}
-// B operand for k = 16 rows, n = 16 values along the row (two n8 blocks).
-template <int DP> __device__ __forceinline__ void load_bt(uint32_t b[4], uint32_t base, int row0, int n16, int lane)
-{
-    ldsm4t(b, tile_addr<DP>(base, row0 + (lane & 15), n16 * 2 + (lane >> 4)));
-}
-
-// Where a block copies the states of tile nodes from: rows that no query
-// sees, rows past n and chunks past head_dim are filled with zeros.
-template <int DP>
-__device__ __forceinline__ void copy_nodes(uint32_t dst, const char *src, int64_t row_bytes, int64_t node0, uint64_t n,
-                                           uint32_t chunks, const uint8_t *seen, int tid)
-{
-    constexpr int C = DP / 8;
-    const int c = tid % C;
-#pragma unroll
-    for (int r = tid / C; r < kAttnTile; r += kAttnThreads / C) {
-        const bool on = c < (int)chunks && (uint64_t)(node0 + r) < n && seen[r];
-        cp16(tile_addr<DP>(dst, r, c), on ? src + (node0 + r) * row_bytes + c * 16 : src, on ? 16 : 0);
-    }
-}
-
-// Rows [row0, row0 + ROWS) of a [T, heads, d] tensor, as rows t * G + g.
-template <int DP, int ROWS>
-__device__ __forceinline__ void copy_rows(uint32_t dst, const void *base, int64_t s_row, int64_t s_head, uint32_t head0,
-                                          uint32_t row0, const AttnParams &p, int tid)
-{
-    constexpr int C = DP / 8;
-    const char *src = static_cast<const char *>(base);
-    for (int i = tid; i < ROWS * C; i += kAttnThreads) {
-        const int r = i / C, c = i % C;
-        const uint32_t row = row0 + r;
-        const bool on = row < p.rows && c < (int)(p.d / 8);
-        const uint32_t t = row / p.group, g = row - t * p.group;
-        cp16(tile_addr<DP>(dst, r, c), on ? src + ((int64_t)t * s_row + (int64_t)(head0 + g) * s_head + c * 8) * 2 : src,
-             on ? 16 : 0);
-    }
 }
 
 // Column of a row in the bucket tile: `sources` (the last) without hop information.
@@ -191,15 +108,6 @@ __device__ __forceinline__ uint32_t row_column(const AttnParams &p, uint32_t row
     const int32_t c = p.qsrc ? __ldg(p.qsrc + t) : (int32_t)t;
     return (uint32_t)c < p.sources ? (uint32_t)c : p.sources;
 }
-
-// The part of shared memory that turns hops into biases.
-struct HopSmem {
-    uint8_t bucket_of[256];
-    uint32_t columns;                       // bit c: some row of the block uses column c
-    uint32_t all;                           // some row sees every node
-    uint8_t seen[4][kAttnTile];
-    uint8_t tile[4][33 * kHopPitch];        // [buffer][column][node]
-};
 
 // Bias table in units of log2, [bucket byte][pitch]: -inf at 0 (masked), 0 at buckets + 1.
 template <typename T>
@@ -219,51 +127,139 @@ __device__ __forceinline__ void fill_bias(float *lut, const AttnParams &p, uint3
     }
 }
 
-// Hops of a tile: each thread holds up to 16 of the 64 x sources, flat in
-// their order in memory (neighbouring threads read neighbouring words).
-constexpr int kHopRegs = kAttnTile * 32 / kAttnThreads;
+// ---- warps that the forward and backward kernels share -------------------------
+// ctl: the kernel's control block in shared memory (barriers hop_full,
+// hop_empty, full, empty; columns in use; seen nodes).  Tile i of the block is
+// tile tile0 + i * p.splits of the nodes.
 
-__device__ __forceinline__ void hops_load(int32_t h[kHopRegs], const AttnParams &p, uint64_t tile, int tid)
+// Items 2 i (keys of tile i) and 2 i + 1 (values) go round the slots; three
+// slots are two for keys and one for values, which are read first.  use: how
+// often the slot was filled before.
+template <int SLOTS> __device__ __forceinline__ uint32_t slot_of(uint32_t item)
 {
-    const uint64_t at = tile * (uint64_t)kAttnTile * p.sources, end = p.n * (uint64_t)p.sources;
-    const uint32_t count = kAttnTile * p.sources;
+    return SLOTS == 3 ? (item & 1 ? 2 : (item >> 1) & 1) : item % SLOTS;
+}
+template <int SLOTS> __device__ __forceinline__ uint32_t slot_use(uint32_t item)
+{
+    return SLOTS == 3 ? (item & 1 ? item >> 1 : item >> 2) : item / SLOTS;
+}
+
+// Hops of nodes [32 hw, 32 hw + 32) of a tile -> bucket bytes.  Lane = (column, part): W lanes (a power of two, at
+// least n_sources) side by side read a node's columns, and 32 / W parts take W nodes each, one after another.
+template <int BUFS, typename Ctl>
+__device__ __forceinline__ void hop_warps(const AttnParams &p, Ctl *ctl, uint8_t *buckets, int hw, int lane, uint32_t tiles,
+                                          uint64_t tile0, volatile uint32_t *gave_up)
+{
+    const uint32_t cols = ctl->columns, B = p.sources;
+    const bool all = ctl->all || !B;
+    uint32_t W = 1;
+    while (W < B) W *= 2;
+    const uint32_t col = lane & (W - 1), first = lane & ~(W - 1);      // first node of this lane's part
+    const bool on = col < B, used = on && ((cols >> col) & 1);
+    constexpr int kAhead = 8;                                          // nodes a load brings
+    int32_t h[kAhead];
+    uint32_t i = 0, k0 = 0;                                            // tile and node of the loads in flight
+    const int32_t *at = p.hops;
+    uint32_t left = 0;                                                 // nodes of the lane's part from `at` on
+    auto hops_in = [&]() {
+        if (k0 == 0 && i < tiles) {
+            const uint64_t node = (tile0 + (uint64_t)i * p.splits) * kTcTile + hw * 32 + first;
+            at = p.hops + node * B + col;
+            left = on && node < p.n ? (uint32_t)min((uint64_t)W, p.n - node) : 0;
+        }
 #pragma unroll
-    for (int i = 0; i < kHopRegs; ++i) {
-        const uint32_t k = tid + i * kAttnThreads;
-        h[i] = -1;
-        if (k < count && at + k < end) h[i] = __ldg(p.hops + at + k);
+        for (int e = 0; e < kAhead; ++e) {
+            h[e] = -1;
+            if (k0 + e < left && i < tiles) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(h[e]) : "l"(at + (int64_t)e * B));
+        }
+        at += (int64_t)kAhead * B;
+        k0 += kAhead;
+        if (k0 >= W) k0 = 0, ++i;
+    };
+    if (B) hops_in();
+    for (uint32_t t = 0; t < tiles; ++t) {
+        const uint32_t buf = t % BUFS;
+        if (t >= BUFS && !__all_sync(~0u, tc::bar_wait(&ctl->hop_empty[buf], (t / BUFS - 1) & 1, gave_up))) break;
+        uint8_t *bt = buckets + buf * 33 * kTcPitch + hw * 32;
+        const uint64_t node0 = (tile0 + (uint64_t)t * p.splits) * kTcTile + hw * 32;
+        uint32_t mask = 0;                                             // nodes that this lane's column sees
+        if (B) {
+#pragma unroll 1
+            for (uint32_t k = 0; k < W; k += kAhead) {
+                uint32_t b[kAhead], sees = 0;
+#pragma unroll
+                for (int e = 0; e < kAhead; ++e) {
+                    b[e] = ctl->byte_of[min(h[e], 255) + 1];
+                    sees |= h[e] >= 0 ? 1u << e : 0u;
+                }
+                if (used) mask |= sees << (first + k);
+                hops_in();
+                if (on) {
+                    uint8_t *to = bt + col * kTcPitch + first + k;
+                    if (W >= 4) {
+                        *reinterpret_cast<uint32_t *>(to) = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
+                        if (W >= 8) *reinterpret_cast<uint32_t *>(to + 4) = b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24;
+                    } else {
+                        to[0] = b[0];
+                        if (W == 2) to[1] = b[1];
+                    }
+                }
+            }
+        }
+        const bool in = node0 + lane < p.n;
+        bt[B * kTcPitch + lane] = in ? p.buckets + 1 : 0;
+        const uint32_t inside = __ballot_sync(~0u, in), seen = (all ? ~0u : __reduce_or_sync(~0u, mask)) & inside;
+        __syncwarp();
+        if (lane == 0) {
+            ctl->seen[buf][hw] = seen;
+            tc::bar_arrive(&ctl->hop_full[buf]);
+        }
     }
 }
 
-// ... stored as bytes into buffer `buf`; the caller has zeroed seen[buf] a barrier earlier.
-__device__ __forceinline__ void hops_store(const int32_t h[kHopRegs], HopSmem *s, const AttnParams &p, uint64_t tile,
-                                           int buf, int tid)
+// States of a tile's seen nodes -> slots, keys then values; this warp brings nodes [32 cw, 32 cw + 32).
+template <int DP, int SLOTS, int BUFS, typename Ctl>
+__device__ __forceinline__ void node_warps(const AttnParams &p, Ctl *ctl, uint32_t sm, int cw, int lane, uint32_t hk,
+                                           uint32_t tiles, uint64_t tile0, volatile uint32_t *gave_up)
 {
-    const uint32_t count = kAttnTile * p.sources, columns = s->columns;
+    constexpr int kPanel = kTcTile * 128, kSlot = kPanel * (DP / 64);
+    constexpr int C = DP / 8, RP = 32 / C, kTurn = 8 / RP;     // chunks a row, rows a pass, passes until the swizzle repeats
+    const uint32_t c = lane % C, r0 = lane / C;
+    const uint32_t fill = (p.d / 8 + 1) & ~1u;                 // chunks the products read: whole steps of 16 values
+    uint32_t at[kTurn];
 #pragma unroll
-    for (int i = 0; i < kHopRegs; ++i) {
-        const uint32_t k = tid + i * kAttnThreads;
-        if (k >= count) break;
-        const uint32_t node = (k * p.hop_magic) >> 16, col = k - node * p.sources;
-        const int32_t x = h[i];
-        s->tile[buf][col * kHopPitch + node] = x < 0 ? 0 : s->bucket_of[min(x, 255)] + 1;
-        if (x >= 0 && ((columns >> col) & 1)) s->seen[buf][node] = 1;
+    for (int k = 0; k < kTurn; ++k) at[k] = sm + tc::chunk(cw * 32 + k * RP + r0, c, kPanel) - k * RP * 128;
+    uint32_t item = 0;
+    bool ok = true;
+    auto bring = [&](const char *src, int64_t step, uint32_t seen) {
+        const uint32_t slot = slot_of<SLOTS>(item), use = slot_use<SLOTS>(item);
+        if (use) ok = __all_sync(~0u, tc::bar_wait(&ctl->empty[slot], (use - 1) & 1, gave_up));
+        if (!ok) return;
+        if (c < fill) {
+#pragma unroll
+            for (int k = 0; k < 32 / RP; ++k) {
+                // a node that no query sees, or past n, or a chunk past head_dim: zeros, and nothing is read
+                cp16(at[k % kTurn] + slot * kSlot + k * RP * 128, src, (seen >> (k * RP)) & 1 ? 16 : 0);
+                src += step;
+            }
+        }
+        tc::cp_arrive(&ctl->full[slot]);      // counts this thread's copies once they have landed
+        ++item;
+    };
+    const int64_t kstep = RP * p.k_row * 2, vstep = RP * p.v_row * 2;
+    const char *k0 = static_cast<const char *>(p.k) + ((int64_t)hk * p.k_head + c * 8) * 2;
+    const char *v0 = static_cast<const char *>(p.v) + ((int64_t)hk * p.v_head + c * 8) * 2;
+    for (uint32_t i = 0; i < tiles && ok; ++i) {
+        const uint32_t buf = i % BUFS;
+        ok = __all_sync(~0u, tc::bar_wait(&ctl->hop_full[buf], (i / BUFS) & 1, gave_up));
+        if (!ok) break;
+        const uint32_t seen = c < p.d / 8 ? ctl->seen[buf][cw] >> r0 : 0;
+        const int64_t node = (int64_t)((tile0 + (uint64_t)i * p.splits) * kTcTile) + cw * 32 + r0;
+        bring(k0 + node * p.k_row * 2, kstep, seen);
+        if (ok) bring(v0 + node * p.v_row * 2, vstep, seen);
     }
-    if (tid < kAttnTile) {
-        const bool in = tile * kAttnTile + tid < p.n;
-        s->tile[buf][p.sources * kHopPitch + tid] = in ? p.buckets + 1 : 0;
-        if (in && s->all) s->seen[buf][tid] = 1;
-    }
-}
-
-// Without a hop table every node is seen; one column says which lie past n.
-__device__ __forceinline__ void hops_none(HopSmem *s, const AttnParams &p, uint64_t tile, int buf, int tid)
-{
-    if (tid < kAttnTile) {
-        const bool in = tile * kAttnTile + tid < p.n;
-        s->tile[buf][tid] = in ? p.buckets + 1 : 0;
-        s->seen[buf][tid] = in;
-    }
+    cp_commit();
+    cp_wait<0>();
 }
 
 }  // namespace k2t

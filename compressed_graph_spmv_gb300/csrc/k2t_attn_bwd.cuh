@@ -1,385 +1,626 @@
-// k2t_attn_bwd.cuh -- backward pass of the hop-biased attention.
+// k2t_attn_bwd.cuh -- backward pass of the hop-biased attention on tcgen05.
 //
 // With p = exp(s - lse), delta = dout . out and dp = dout . v:
 //   ds = p (dp - delta),  dv = sum p dout,  dk = scale sum ds q,
 //   dq = scale sum ds k,  dbias[bucket] = sum ds.
-// Scores are computed transposed, nodes x rows: a warp owns 16 nodes, its
-// weights p^T and ds^T come out of the accumulators in the layout of an A
-// operand, so dv and dk (nodes x head_dim, summed over rows) need no exchange
-// between warps.  dq sums over nodes: ds^T passes through shared memory once.
-// Where all rows of a head fit one tile (32), one pass makes everything: dk
-// and dv of a tile are final, dq stays in registers over the block's nodes
-// (MODE 0).  With more rows, one kernel loops rows for fixed nodes (MODE 1:
-// dk, dv) and one loops nodes for fixed rows (MODE 2: dq, dbias): scores are
-// computed twice, and nothing is summed by atomics, so results do not depend
-// on the order of blocks.
+// Everything is computed transposed, 128 nodes x 32 rows a unit: S^T = K Q^T
+// and dP^T = V dO^T come out of tensor memory one node a thread; P^T and dS^T
+// go back over them as A operands of dV += P^T dO and dK += dS^T Q (nodes x
+// head_dim), and dS^T goes to shared memory as B operand of
+// dQ^T += K^T dS (head_dim x rows) and for the sums by bucket.
+//
+// attn_bwd_nodes_kernel streams nodes past up to RT row tiles that stay: dQ^T
+// accumulates in tensor memory over all nodes of the block, and (DKV) dV and
+// dK of a tile are final after its row tiles: one pass makes every gradient.
+// With more rows than that, attn_bwd_rows_kernel streams rows past a tile of
+// nodes for dV and dK, and the first kernel runs without them: the scores are
+// computed twice, and nothing is summed by atomics, so that results do not
+// depend on the order of blocks.
+//
+// A row tile holds whole queries: (32 / G) queries x G heads, so that a row's
+// head is the same in every tile, and the sums by bucket need one table a row
+// of the tile.
 #pragma once
 
+#include <type_traits>
+
 #include "k2t_attn.cuh"
+#include "k2t_tc.cuh"
 
 namespace k2t {
 
-constexpr int kBwdRows = 32;   // rows per tile
+constexpr int kBwdThreads = 800;
+constexpr int kBwdRowThreads = 544;
+constexpr int kBwdRows = 32;
 
-template <int DP, int MODE> struct BwdSmem {
-    static constexpr int kTileBytes = kAttnTile * DP * 2;
-    static constexpr int kRowBytes = kBwdRows * DP * 2;
-    static constexpr int kKvStages = MODE == 1 ? 1 : 2;
-    static constexpr int kRowStages = MODE == 1 ? 2 : 1;
-    static constexpr int kRow = kKvStages * 2 * kTileBytes;                      // q, dout
-    static constexpr int kDsPitch = kBwdRows + 8;                                // values; 80 bytes, 5 x 16: no bank conflicts
-    static constexpr int kDs = kRow + kRowStages * 2 * kRowBytes;                // ds^T [node][row]
-    static constexpr int kHop = kDs + (MODE == 1 ? 0 : kAttnTile * kDsPitch * 2);
-    static constexpr int kStat = kHop + (int)((sizeof(HopSmem) + 15) / 16 * 16);  // lse (log2), delta, column, per row
-    static constexpr int kLut = kStat + 2 * 3 * kBwdRows * 4;
+// What the kernels need of a row, made once by attn_rows_kernel: lse in units
+// of log2 (+inf for a row that saw nothing or does not exist: its weights
+// become 0), delta, byte offset of its column in a bucket tile, its head's
+// offset in the bias table; a row tile's together.
+struct RowInfo {
+    float lse[kBwdRows], delta[kBwdRows];
+    uint32_t place[kBwdRows];              // column | head << 16
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ AttnParams p)
+{
+    const uint32_t at = blockIdx.x * 8 + (threadIdx.x >> 5), hk = blockIdx.y;     // row of a tile, padded: a warp each
+    if (at >= p.row_tiles * kBwdRows) return;
+    const int lane = threadIdx.x & 31;
+    const uint32_t G = p.group, per = kBwdRows / G, c = at % kBwdRows, t = at / kBwdRows * per + c / G, g = c % G;
+    float lse = INFINITY, s = 0.0f;
+    uint32_t place = 0;
+    if (c < per * G && t < p.T) {
+        const uint32_t hd = hk * G + g;
+        const T *o = static_cast<const T *>(p.out) + (int64_t)t * p.out_row + (int64_t)hd * p.out_head;
+        const T *d = static_cast<const T *>(p.dout) + (int64_t)t * p.dout_row + (int64_t)hd * p.dout_head;
+        for (uint32_t x = lane * 2; x < p.d; x += 64) {
+            const float2 a = Elem<T>::unpack(*reinterpret_cast<const uint32_t *>(o + x));
+            const float2 b = Elem<T>::unpack(*reinterpret_cast<const uint32_t *>(d + x));
+            s = fmaf(a.x, b.x, fmaf(a.y, b.y, s));
+        }
+        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
+        const float l = p.lse[(uint64_t)t * p.hq + hd];
+        if (l != -INFINITY) lse = l * kLog2e;
+        place = row_column(p, t * G) * kTcPitch | (g * 4) << 16;
+    }
+    RowInfo *to = static_cast<RowInfo *>(p.row_info) + (uint64_t)hk * p.row_tiles + at / kBwdRows;
+    if (lane == 0) to->lse[c] = lse, to->delta[c] = s, to->place[c] = place;
+}
+
+// Copies ROWS (a multiple of 32) rows of tile `tile` on of a [T, heads, d] tensor into row tiles of 32 rows:
+// panels of 64 values, 4096 bytes each, swizzled.  Rows that do not exist are zeros.
+template <int DP>
+__device__ __forceinline__ void copy_row_tile(uint32_t dst, const void *base, int64_t s_row, int64_t s_head, uint32_t head0,
+                                              uint32_t tile, const AttnParams &p, int first, int step)
+{
+    constexpr int C = DP / 8;
+    const uint32_t G = p.group, per = kBwdRows / G, fill = (p.d / 8 + 1) & ~1u;
+    for (int i = first; i < kBwdRows * C; i += step) {
+        const uint32_t r = i / C, c = i % C, q = r / G, t = tile * per + q, g = r - q * G;
+        const bool on = q < per && t < p.T && c < p.d / 8;
+        const char *src = static_cast<const char *>(base) + (on ? ((int64_t)t * s_row + (int64_t)(head0 + g) * s_head + c * 8) * 2 : 0);
+        if (c < fill) cp16(dst + tc::chunk(r, c, 4096), src, on ? 16 : 0);
+    }
+}
+
+// A unit's softmax step for one node: S^T and dP^T at `at` (32 columns each, a row of the tile a column) become P^T
+// and dS^T in the element type, two rows a column; ds: this node's row of dS^T in shared memory, from chunk `chunk` on
+// (null: not wanted); bt: the node's bytes in the bucket tile (column 0); lut: bias table, bytes.
+// Eight rows at a time in a rolled loop: the warps of an SM run half a dozen different loops, and the instruction
+// caches hold them only while each is small.
+template <typename T>
+__device__ __forceinline__ void unit32(uint32_t at, const RowInfo *info, bool plain, float scale, const uint8_t *bt,
+                                       const uint8_t *lut, uint32_t shift, uint8_t *ds, uint32_t chunk, uint32_t node)
+{
+#pragma unroll 1
+    for (int r0 = 0; r0 < kBwdRows; r0 += 8) {
+        uint32_t s[8], d[8], pw[4], dw[4];
+        tc::ld8(s, at + r0);
+        tc::ld8(d, at + 32 + r0);
+        float b[8] = {};
+        if (!plain) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+                const uint4 c4 = *reinterpret_cast<const uint4 *>(&info->place[r0 + e]);
+                const uint32_t place[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const uint32_t k = bt[place[y] & 0xffff];
+                    b[e + y] = *reinterpret_cast<const float *>(lut + (k << shift) + (place[y] >> 16));
+                }
+            }
+        }
+        tc::wait_ld();
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+            const float4 lse4 = *reinterpret_cast<const float4 *>(&info->lse[r0 + e]), dl4 = *reinterpret_cast<const float4 *>(&info->delta[r0 + e]);
+            const float lse[4] = {lse4.x, lse4.y, lse4.z, lse4.w}, delta[4] = {dl4.x, dl4.y, dl4.z, dl4.w};
+            float pv[4], dv[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                pv[y] = ex2(fmaf(__uint_as_float(s[e + y]), scale, b[e + y]) - lse[y]);
+                dv[y] = pv[y] * (__uint_as_float(d[e + y]) - delta[y]);
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                pw[e / 2 + y] = Elem<T>::pack(pv[2 * y], pv[2 * y + 1]);
+                dw[e / 2 + y] = Elem<T>::pack(dv[2 * y], dv[2 * y + 1]);
+            }
+        }
+        tc::st4(at + r0 / 2, pw);
+        tc::st4(at + 32 + r0 / 2, dw);
+        if (ds) *reinterpret_cast<uint4 *>(ds + (((chunk + r0 / 8) ^ (node & 7)) << 4)) = make_uint4(dw[0], dw[1], dw[2], dw[3]);
+    }
+}
+
+// 32 nodes (a warp's lanes) x head_dim of fp32 accumulators, rounded, through the warp's rows of a tile in shared
+// memory to global memory in 16-byte pieces.
+template <typename T, int DP>
+__device__ __forceinline__ void load_nodes(uint32_t tm_at, float f, uint32_t stage, int row)
+{
+#pragma unroll 1
+    for (int c = 0; c < DP; c += 32) {
+        uint32_t v[32];
+        tc::ld32(v, tm_at + c);
+        tc::wait_ld();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = Elem<T>::pack(__uint_as_float(v[j * 8 + 2 * e]) * f, __uint_as_float(v[j * 8 + 2 * e + 1]) * f);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(stage + tc::chunk(row, c / 8 + j, kTcTile * 128)), "r"(w[0]),
+                         "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+        }
+    }
+}
+template <typename T, int DP>
+__device__ __forceinline__ void store_nodes(uint32_t stage, void *out, int64_t s_row, uint64_t node0, int warp, const AttnParams &p)
+{
+    constexpr int C = DP / 8, RP = 32 / C;
+    const int lane = threadIdx.x & 31;
+    const uint32_t c = lane % C;
+#pragma unroll 4
+    for (int r = lane / C; r < 32; r += RP) {
+        const uint32_t row = warp * 32 + r;
+        if (node0 + row < p.n && c < p.d / 8) {
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(stage + tc::chunk(row, c, kTcTile * 128)) : "memory");
+            __stcs(reinterpret_cast<uint4 *>(static_cast<T *>(out) + (int64_t)(node0 + row) * s_row + c * 8), v);
+        }
+    }
+}
+
+// S^T = K Q^T at `at`, dP^T = V dO^T 32 columns on.
+template <int DP, int PANEL>
+__device__ __forceinline__ void score_products(bool lead, uint32_t at, uint64_t k, uint64_t q, uint64_t v, uint64_t g, uint32_t id, uint32_t dn)
+{
+#pragma unroll
+    for (uint32_t kk = 0; kk < DP / 16; ++kk)
+        if (kk * 16 < dn) tc::mma_ss(lead, at, k, (kk >> 2) * PANEL + (kk & 3) * 32, q, (kk >> 2) * 4096 + (kk & 3) * 32, id, kk > 0);
+#pragma unroll
+    for (uint32_t kk = 0; kk < DP / 16; ++kk)
+        if (kk * 16 < dn) tc::mma_ss(lead, at + 32, v, (kk >> 2) * PANEL + (kk & 3) * 32, g, (kk >> 2) * 4096 + (kk & 3) * 32, id, kk > 0);
+}
+// dV (+)= P^T dO, dK (+)= dS^T Q with P^T at `at` and dS^T 32 columns on.
+__device__ __forceinline__ void node_products(bool lead, uint32_t at, uint32_t dv, uint32_t dk, uint64_t q, uint64_t g, uint32_t id, bool add)
+{
+#pragma unroll
+    for (uint32_t kk = 0; kk < 2; ++kk) tc::mma_ts(lead, dv, at + kk * 8, g, kk * 2048, id, add || kk > 0);
+#pragma unroll
+    for (uint32_t kk = 0; kk < 2; ++kk) tc::mma_ts(lead, dk, at + 32 + kk * 8, q, kk * 2048, id, add || kk > 0);
+}
+
+template <int DP, int RT, bool DKV> struct BwdSmem {
+    static constexpr int kPanel = kTcTile * 128;
+    static constexpr int kSlot = kPanel * (DP / 64);
+    static constexpr int kSlots = DP == 64 ? 6 : DKV ? 4 : 3;
+    static constexpr int kBufs = DP == 64 ? 3 : 2;                            // bucket tiles
+    static constexpr int kRowTile = kBwdRows * DP * 2;                        // q or dout of a row tile
+    static constexpr int kRow = kSlots * kSlot;                               // [RT][q | dout]
+    static constexpr int kDs = kRow + RT * 2 * kRowTile;                      // dS^T [node][unit parity][32 rows]
+    static constexpr int kBuckets = kDs + kPanel;
+    static constexpr int kInfo = kBuckets + kBufs * 33 * kTcPitch;
+    static constexpr int kCtl = kInfo + RT * (int)sizeof(RowInfo);
+    struct Ctl {
+        uint64_t full[kSlots], empty[kSlots], hop_full[kBufs], hop_empty[kBufs], sp_full[2], ds_full[2], hist_done[2];
+        uint64_t tile_full, tile_empty, dq_full, drained;
+        uint32_t tmem, gave_up, columns, all;
+        uint32_t seen[kBufs][4];
+        uint8_t byte_of[257 + 15];
+    };
+    static constexpr int kLut = kCtl + (int)((sizeof(Ctl) + 15) / 16 * 16);
     static size_t bytes(const AttnParams &p)
     {
-        const size_t lut = (size_t)(p.buckets + 2) * p.group * 4;
-        return kLut + lut + (MODE == 1 ? 0 : (size_t)(p.buckets + 2) * kAttnThreads * 4);
+        return kLut + ((size_t)(p.buckets + 2) * p.group2 + (p.buckets ? (size_t)(p.buckets + 2) * 128 : 0)) * 4;
     }
 };
 
-// delta[t, h] = dout . out in fp32, a warp per row.
-template <typename T>
-__global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ AttnParams p)
+template <typename T, int DP, int RT, bool DKV>
+__global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __grid_constant__ AttnParams p)
 {
-    const uint64_t row = (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= (uint64_t)p.T * p.hq) return;
-    const int lane = threadIdx.x & 31;
-    const uint32_t t = (uint32_t)(row / p.hq), hd = (uint32_t)(row - (uint64_t)t * p.hq);
-    const T *o = static_cast<const T *>(p.out) + (int64_t)t * p.out_row + (int64_t)hd * p.out_head;
-    const T *g = static_cast<const T *>(p.dout) + (int64_t)t * p.dout_row + (int64_t)hd * p.dout_head;
-    float s = 0.0f;
-    for (uint32_t c = lane * 2; c < p.d; c += 64) {
-        const float2 a = Elem<T>::unpack(*reinterpret_cast<const uint32_t *>(o + c));
-        const float2 b = Elem<T>::unpack(*reinterpret_cast<const uint32_t *>(g + c));
-        s = fmaf(a.x, b.x, fmaf(a.y, b.y, s));
+    using S = BwdSmem<DP, RT, DKV>;
+    using Ctl = typename S::Ctl;
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr uint32_t kDv = 128, kDk = 128 + DP, kDq = DKV ? 128 + 2 * DP : 128;    // columns of tensor memory
+    static_assert(kDq + RT * 32 <= 512, "tensor memory");
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + S::kCtl);
+    const uint32_t sm = tc::saddr(smem);
+    float *lut = reinterpret_cast<float *>(smem + S::kLut), *hist = lut + (p.buckets + 2) * p.group2;   // [bucket byte][thread]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t hk = blockIdx.y, split = blockIdx.x % p.splits, rows_of = blockIdx.x / p.splits;
+    const uint32_t rt0 = rows_of * RT, rts = min((uint32_t)RT, p.row_tiles - rt0);      // row tiles of this block
+    const uint32_t tiles = (uint32_t)(split < p.tiles ? (p.tiles - split + p.splits - 1) / p.splits : 0);
+    const uint32_t units = tiles * rts;                                                 // unit u: tile u / rts, row tile u % rts
+    auto tile_at = [&](uint32_t i) { return split + (uint64_t)i * p.splits; };
+
+    // ---- set-up ----
+    if (warp == 24) tc::alloc(&ctl->tmem, 512);
+    if (tid == 0) {
+        for (int i = 0; i < S::kSlots; ++i) tc::bar_init(&ctl->full[i], 128), tc::bar_init(&ctl->empty[i], DKV ? 4 : 1);
+        for (int i = 0; i < S::kBufs; ++i) {
+            tc::bar_init(&ctl->hop_full[i], 4);
+            tc::bar_init(&ctl->hop_empty[i], rts * (p.buckets ? 8 : 4));
+        }
+        for (int i = 0; i < 2; ++i) tc::bar_init(&ctl->sp_full[i], 1), tc::bar_init(&ctl->ds_full[i], 128), tc::bar_init(&ctl->hist_done[i], 4);
+        tc::bar_init(&ctl->tile_full, 1);
+        tc::bar_init(&ctl->tile_empty, 128);
+        tc::bar_init(&ctl->dq_full, 1);
+        tc::bar_init(&ctl->drained, 1);
+        ctl->gave_up = ctl->columns = ctl->all = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
-    if (lane == 0) p.delta[row] = s;
+    for (uint32_t r = 0; r < rts; ++r) {
+        const uint32_t at = sm + S::kRow + r * 2 * S::kRowTile;
+        copy_row_tile<DP>(at, p.q, p.q_row, p.q_head, hk * p.group, rt0 + r, p, tid, kBwdThreads);
+        copy_row_tile<DP>(at + S::kRowTile, p.dout, p.dout_row, p.dout_head, hk * p.group, rt0 + r, p, tid, kBwdThreads);
+    }
+    cp_commit();
+    if (p.sources)
+        for (int i = tid; i < 257; i += kBwdThreads) ctl->byte_of[i] = i ? p.bucket_of[i - 1] + 1 : 0;
+    fill_bias<T>(lut, p, hk, tid, p.group2);
+    if (p.buckets)
+        for (uint32_t i = tid; i < (p.buckets + 2) * 128; i += kBwdThreads) hist[i] = 0.0f;
+    RowInfo *info = reinterpret_cast<RowInfo *>(smem + S::kInfo);
+    __syncthreads();
+    if (tid < (int)rts * kBwdRows) {
+        const RowInfo *from = static_cast<const RowInfo *>(p.row_info) + (uint64_t)hk * p.row_tiles + rt0 + tid / kBwdRows;
+        RowInfo *to = info + tid / kBwdRows;
+        const uint32_t c = tid % kBwdRows, place = from->place[c];
+        to->lse[c] = from->lse[c], to->delta[c] = from->delta[c], to->place[c] = place;
+        const uint32_t per = kBwdRows / p.group, t = (rt0 + tid / kBwdRows) * per + c / p.group;
+        if (p.sources && c < per * p.group && t < p.T) {
+            const uint32_t col = (place & 0xffff) / kTcPitch;
+            if (col < p.sources) atomicOr(&ctl->columns, 1u << col);
+            else ctl->all = 1;
+        }
+    }
+    cp_wait<0>();
+    tc::fence_async();
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tm = ctl->tmem;
+    volatile uint32_t *gave_up = &ctl->gave_up;
+
+    if (warp < 8) {
+        // ---- softmax: thread = node of a tile; group w takes the units of parity w ----
+        const int w = warp >> 2, l = tid & 127;
+        const uint32_t at = tm + ((uint32_t)(warp & 3) << 21) + w * 64, shift = p.group2_log + 2;
+        uint8_t *ds = smem + S::kDs + l * 128;
+        uint32_t i = 0, r = w;
+        while (r >= rts) r -= rts, ++i;
+        for (uint32_t u = w, k = 0; u < units; u += 2, ++k) {
+            const uint32_t buf = i % S::kBufs;
+            bool ok = tc::bar_wait(&ctl->hop_full[buf], (i / S::kBufs) & 1, gave_up) && tc::bar_wait(&ctl->sp_full[w], k & 1, gave_up);
+            if (ok && k > 0 && p.buckets) ok = tc::bar_wait(&ctl->hist_done[w], (k - 1) & 1, gave_up);
+            if (!__all_sync(~0u, ok)) break;
+            tc::fence_after();
+            const bool plain = !p.sources && (tile_at(i) + 1) * kTcTile <= p.n;
+            unit32<T>(at, info + r, plain, p.scale_log2, smem + S::kBuckets + buf * 33 * kTcPitch + l,
+                      reinterpret_cast<const uint8_t *>(lut), shift, ds, w * 4, l);
+            tc::wait_st();
+            tc::fence_async();
+            tc::fence_before();
+            tc::bar_arrive(&ctl->ds_full[w]);
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(&ctl->hop_empty[buf]);
+            r += 2;
+            while (r >= rts) r -= rts, ++i;
+        }
+    } else if (warp < 12) {
+        hop_warps<S::kBufs>(p, ctl, smem + S::kBuckets, warp - 8, lane, tiles, split, gave_up);
+    } else if (warp < 16) {
+        node_warps<DP, S::kSlots, S::kBufs>(p, ctl, sm, warp - 12, lane, hk, tiles, split, gave_up);
+    } else if (warp < 20) {
+        // ---- results: dv and dk of each tile, then dq ----
+        const int ew = warp - 16, l = ew * 32 + lane;
+        const uint32_t lanes = (uint32_t)ew << 21;
+        bool ok = true;
+        if (DKV)
+            for (uint32_t i = 0; i < tiles; ++i) {
+                ok = __all_sync(~0u, tc::bar_wait(&ctl->tile_full, i & 1, gave_up));
+                if (!ok) break;
+                tc::fence_after();
+                // the tile's own slots are free to hold its results: every product that read them is done
+                const uint32_t ks = slot_of<S::kSlots>(2 * i), vs = slot_of<S::kSlots>(2 * i + 1);
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x) load_nodes<T, DP>(tm + lanes + (x ? kDk : kDv), x ? p.scale : 1.0f, sm + (x ? ks : vs) * S::kSlot, l);
+                tc::fence_before();
+                tc::bar_arrive(&ctl->tile_empty);
+                __syncwarp();
+                const uint64_t node0 = tile_at(i) * kTcTile;
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x)
+                    store_nodes<T, DP>(sm + (x ? ks : vs) * S::kSlot, static_cast<T *>(x ? p.dk : p.dv) + (int64_t)hk * (x ? p.dk_head : p.dv_head),
+                                       x ? p.dk_row : p.dv_row, node0, ew, p);
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(&ctl->empty[ks]), tc::bar_arrive(&ctl->empty[vs]);
+            }
+        if (ok && units > 0) ok = __all_sync(~0u, tc::bar_wait(&ctl->dq_full, 0, gave_up));
+        if (ok) {
+            tc::fence_after();
+            const uint32_t G = p.group, per = kBwdRows / G;
+            for (uint32_t r = 0; r < rts; ++r) {
+                uint32_t v[32];
+                if (units > 0) {
+                    tc::ld32(v, tm + lanes + kDq + r * 32);
+                    tc::wait_ld();
+                }
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const uint32_t q = c / G, t = (rt0 + r) * per + q, hd = hk * G + c - q * G;
+                    if (l < (int)p.d && q < per && t < p.T)
+                        p.part[(((uint64_t)split * p.T + t) * p.hq + hd) * p.d + l] = units > 0 ? __uint_as_float(v[c]) : 0.0f;
+                }
+            }
+        }
+    } else if (warp < 24) {
+        // ---- sums of ds by bucket: thread = (row of the tile, quarter of the nodes), with a table of its own ----
+        if (p.buckets) {
+            const int t = tid - 640, c = t & 31, part = t >> 5;
+            float *mine = hist + t;
+            uint32_t i = 0, r = 0;
+            for (uint32_t u = 0; u < units; ++u) {
+                const uint32_t w = u & 1, buf = i % S::kBufs;
+                bool ok = tc::bar_wait(&ctl->hop_full[buf], (i / S::kBufs) & 1, gave_up) && tc::bar_wait(&ctl->ds_full[w], (u >> 1) & 1, gave_up);
+                if (!__all_sync(~0u, ok)) break;
+                const uint8_t *bt = smem + S::kBuckets + buf * 33 * kTcPitch + (info[r].place[c] & 0xffff) + part * 32;
+                const uint8_t *ds = smem + S::kDs + part * 32 * 128 + (c & 7) * 2;
+                const uint32_t chunk = w * 4 + (c >> 3);
+#pragma unroll 1
+                for (int k = 0; k < 32; k += 4) {
+                    // four nodes at once: equal buckets among them take the running value, and the last store stands
+                    const uint32_t bw = *reinterpret_cast<const uint32_t *>(bt + k);
+                    uint32_t b[4];
+                    float x[4], hv[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        b[y] = (bw >> (8 * y)) & 255;
+                        x[y] = Elem<T>::to_float(*reinterpret_cast<const T *>(ds + (k + y) * 128 + ((chunk ^ ((k + y) & 7)) << 4)));
+                        hv[y] = mine[b[y] * 128];
+                    }
+                    hv[0] += x[0];
+                    hv[1] = (b[1] == b[0] ? hv[0] : hv[1]) + x[1];
+                    hv[2] = (b[2] == b[1] ? hv[1] : b[2] == b[0] ? hv[0] : hv[2]) + x[2];
+                    hv[3] = (b[3] == b[2] ? hv[2] : b[3] == b[1] ? hv[1] : b[3] == b[0] ? hv[0] : hv[3]) + x[3];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) mine[b[y] * 128] = hv[y];
+                }
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(&ctl->hist_done[w]), tc::bar_arrive(&ctl->hop_empty[buf]);
+                if (++r == rts) r = 0, ++i;
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            // part_ml[split][row group][head][bucket]
+            const uint32_t G = p.group, per = kBwdRows / G;
+            float *out = p.part_ml + (((uint64_t)blockIdx.x * p.hkv + hk) * G) * p.buckets;
+            for (uint32_t k = t; k < G * p.buckets; k += 128) {
+                const uint32_t g = k / p.buckets, b = k - g * p.buckets;
+                float s = 0.0f;
+                for (uint32_t q = 0; q < per; ++q)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) s += hist[(b + 1) * 128 + x * 32 + q * G + g];
+                out[k] = s;
+            }
+        }
+    } else {
+        // ---- products ----
+        const bool lead = tc::elect();
+        const uint32_t dn = (p.d + 15) & ~15u;
+        const uint32_t id_s = tc::idesc(kBf16, 32, false, false), id_n = tc::idesc(kBf16, dn, false, true), id_q = tc::idesc(kBf16, 32, true, true);
+        bool ok = true;
+        uint32_t si = 0, sr = 0;        // tile and row tile of the next scores
+        auto scores = [&](uint32_t u) {
+            const uint32_t w = u & 1, ks = slot_of<S::kSlots>(2 * si), vs = slot_of<S::kSlots>(2 * si + 1);
+            if (sr == 0) {
+                ok = tc::bar_wait(&ctl->full[ks], slot_use<S::kSlots>(2 * si) & 1, gave_up) &&
+                     tc::bar_wait(&ctl->full[vs], slot_use<S::kSlots>(2 * si + 1) & 1, gave_up);
+                if (!ok) return;
+                tc::fence_async();
+            }
+            tc::fence_after();
+            const uint32_t qa = sm + S::kRow + sr * 2 * S::kRowTile;
+            const uint64_t q = tc::desc(qa, 4096), g = tc::desc(qa + S::kRowTile, 4096);
+            const uint64_t k = tc::desc(sm + ks * S::kSlot, S::kPanel), v = tc::desc(sm + vs * S::kSlot, S::kPanel);
+            score_products<DP, S::kPanel>(lead, tm + w * 64, k, q, v, g, id_s, dn);
+            tc::commit(lead, &ctl->sp_full[w]);
+            if (!DKV && sr + 1 == rts) tc::commit(lead, &ctl->empty[vs]);      // values are read by the scores alone
+            if (++sr == rts) sr = 0, ++si;
+        };
+        if (units > 0) scores(0);
+        if (ok && units > 1) scores(1);
+        uint32_t i = 0, r = 0;
+        for (uint32_t u = 0; u < units && ok; ++u) {
+            const uint32_t w = u & 1, ks = slot_of<S::kSlots>(2 * i);
+            ok = tc::bar_wait(&ctl->ds_full[w], (u >> 1) & 1, gave_up);
+            if (ok && DKV && r == 0 && i > 0) ok = tc::bar_wait(&ctl->tile_empty, (i - 1) & 1, gave_up);
+            if (!ok) break;
+            tc::fence_after();
+            const uint32_t qa = sm + S::kRow + r * 2 * S::kRowTile;
+            if (DKV) node_products(lead, tm + w * 64, tm + kDv, tm + kDk, tc::desc(qa, 4096), tc::desc(qa + S::kRowTile, 4096), id_n, r > 0);
+            const uint64_t k = tc::desc(sm + ks * S::kSlot, S::kPanel), ds = tc::desc(sm + S::kDs + w * 64, 4096);
+#pragma unroll
+            for (uint32_t kk = 0; kk < kTcTile / 16; ++kk)
+                tc::mma_ss(lead, tm + kDq + r * 32, k, kk * 2048, ds, kk * 2048, id_q, i > 0 || kk > 0);
+            if (r + 1 == rts) {
+                if (DKV) tc::commit(lead, &ctl->tile_full);
+                else tc::commit(lead, &ctl->empty[ks]);
+            }
+            if (u + 1 == units) tc::commit(lead, &ctl->dq_full);
+            if (++r == rts) r = 0, ++i;
+            if (u + 2 < units) scores(u + 2);
+        }
+        if (!ok) tc::drain(lead, &ctl->drained, 0);
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 24) tc::dealloc(tm, 512);
+    if (tid == 0 && *gave_up) atomicOr(p.status, K2T_STATUS_WAIT_TIMEOUT);
 }
 
-template <typename T, int DP, int MODE>
-__global__ void __launch_bounds__(kAttnThreads) attn_bwd_kernel(const __grid_constant__ AttnParams p)
+template <int DP> struct BwdRowSmem {
+    static constexpr int kPanel = kTcTile * 128;
+    static constexpr int kSlot = kPanel * (DP / 64);
+    static constexpr int kRowTile = kBwdRows * DP * 2;
+    static constexpr int kRing = 5;                                         // row tiles in flight
+    static constexpr int kRow = 2 * kSlot;                                  // keys, values; then [ring][q | dout]
+    static constexpr int kBuckets = kRow + kRing * 2 * kRowTile;
+    static constexpr int kInfo = kBuckets + 33 * kTcPitch;
+    static constexpr int kCtl = kInfo + kRing * (int)sizeof(RowInfo);
+    struct Ctl {
+        uint64_t full[2], empty[2], hop_full[1], hop_empty[1], row_full[kRing], row_empty[kRing], sp_full[2], ds_full[2], tile_full, drained;
+        uint32_t tmem, gave_up, columns, all;
+        uint32_t seen[1][4];
+        uint8_t byte_of[257 + 15];
+    };
+    static constexpr int kLut = kCtl + (int)((sizeof(Ctl) + 15) / 16 * 16);
+    static size_t bytes(const AttnParams &p) { return kLut + (size_t)(p.buckets + 2) * p.group2 * 4; }
+};
+
+// dv and dk of one tile of nodes: the rows stream past it.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kBwdRowThreads, 1) attn_bwd_rows_kernel(const __grid_constant__ AttnParams p)
 {
-    using S = BwdSmem<DP, MODE>;
-    constexpr int D16 = DP / 16, R8 = kBwdRows / 8;
+    using S = BwdRowSmem<DP>;
+    using Ctl = typename S::Ctl;
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr uint32_t kDv = 128, kDk = 128 + DP, kCols = DP == 64 ? 256 : 512;     // columns of tensor memory
     extern __shared__ __align__(1024) uint8_t smem[];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t hk = blockIdx.y;
-    // MODE 0, 2: x = split + splits * row tile; MODE 1: x = tile of nodes
-    const uint32_t split = MODE == 1 ? 0 : blockIdx.x % p.splits, fixed_row0 = MODE == 1 ? 0 : blockIdx.x / p.splits * kBwdRows;
-    HopSmem *hs = reinterpret_cast<HopSmem *>(smem + S::kHop);
-    float *stat = reinterpret_cast<float *>(smem + S::kStat);   // [buffer][lse | delta | column][row]
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + S::kCtl);
+    const uint32_t sm = tc::saddr(smem);
     float *lut = reinterpret_cast<float *>(smem + S::kLut);
-    float *hist = lut + (p.buckets + 2) * p.group;              // [bucket byte][thread]
-    T *ds_s = reinterpret_cast<T *>(smem + S::kDs);
-    const uint32_t sm = smem_u32(smem);
-    const uint32_t G = p.group;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t hk = blockIdx.y, units = p.row_tiles;
+    const uint64_t tile = blockIdx.x;
 
-    auto stats_in = [&](uint32_t row0, int buf) {   // per row: lse in log2 units, delta, column
-        if (tid < kBwdRows) {
-            const uint32_t row = row0 + tid;
-            float lse = INFINITY, dl = 0.0f;
-            uint32_t c = 0;
-            if (row < p.rows) {
-                const uint32_t t = row / G, hd = hk * G + row - t * G;
-                lse = p.lse[(uint64_t)t * p.hq + hd] * kLog2e;
-                if (lse == -INFINITY) lse = INFINITY;       // nothing left for this row: its weights become 0
-                dl = p.delta[(uint64_t)t * p.hq + hd];
-                c = row_column(p, row);
-            }
-            float *s = stat + buf * 3 * kBwdRows;
-            s[tid] = lse;
-            s[kBwdRows + tid] = dl;
-            reinterpret_cast<uint32_t *>(s)[2 * kBwdRows + tid] = c * kHopPitch;
-        }
-    };
-    auto rows_in = [&](uint32_t row0, int buf) {
-        const uint32_t at = sm + S::kRow + buf * 2 * S::kRowBytes;
-        copy_rows<DP, kBwdRows>(at, p.q, p.q_row, p.q_head, hk * G, row0, p, tid);
-        copy_rows<DP, kBwdRows>(at + S::kRowBytes, p.dout, p.dout_row, p.dout_head, hk * G, row0, p, tid);
-    };
-
-    if (tid == 0) hs->columns = 0, hs->all = 0;
+    if (warp == 16) tc::alloc(&ctl->tmem, kCols);
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) tc::bar_init(&ctl->full[i], 128), tc::bar_init(&ctl->empty[i], 1), tc::bar_init(&ctl->sp_full[i], 1), tc::bar_init(&ctl->ds_full[i], 128);
+        tc::bar_init(&ctl->hop_full[0], 4);
+        tc::bar_init(&ctl->hop_empty[0], 1);
+        for (int i = 0; i < S::kRing; ++i) tc::bar_init(&ctl->row_full[i], 128), tc::bar_init(&ctl->row_empty[i], 1);
+        tc::bar_init(&ctl->tile_full, 1);
+        tc::bar_init(&ctl->drained, 1);
+        ctl->gave_up = ctl->columns = ctl->all = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
     if (p.sources)
-        for (int i = tid; i < 256; i += kAttnThreads) hs->bucket_of[i] = p.bucket_of[i];
-    fill_bias<T>(lut, p, hk, tid, p.group);
-    for (int i = tid; i < 4 * kAttnTile; i += kAttnThreads) hs->seen[0][i] = 0;
-    if (MODE != 1)
-        for (uint32_t i = tid; i < (p.buckets + 2) * kAttnThreads; i += kAttnThreads) hist[i] = 0.0f;
+        for (int i = tid; i < 257; i += kBwdRowThreads) ctl->byte_of[i] = i ? p.bucket_of[i - 1] + 1 : 0;
+    fill_bias<T>(lut, p, hk, tid, p.group2);
     __syncthreads();
-    if (p.sources) {   // columns in use: of the block's rows, or of all queries
-        const uint32_t r0 = MODE == 1 ? 0 : fixed_row0, r1 = MODE == 1 ? p.rows : min(p.rows, fixed_row0 + kBwdRows);
+    if (p.sources) {
         uint32_t cols = 0;
         bool all = false;
-        for (uint32_t r = r0 + tid * (MODE == 1 ? G : 1); r < r1; r += kAttnThreads * (MODE == 1 ? G : 1)) {
-            const uint32_t c = row_column(p, r);
+        for (uint32_t t = tid; t < p.T; t += kBwdRowThreads) {
+            const uint32_t c = row_column(p, t * p.group);
             if (c < p.sources) cols |= 1u << c;
             else all = true;
         }
-        if (cols) atomicOr(&hs->columns, cols);
-        if (all) hs->all = 1;
+        if (cols) atomicOr(&ctl->columns, cols);
+        if (all) ctl->all = 1;
     }
+    tc::fence_before();
     __syncthreads();
+    tc::fence_after();
+    const uint32_t tm = ctl->tmem;
+    volatile uint32_t *gave_up = &ctl->gave_up;
 
-    const char *kbase = static_cast<const char *>(p.k) + hk * p.k_head * 2;
-    const char *vbase = static_cast<const char *>(p.v) + hk * p.v_head * 2;
-    const uint64_t tiles = MODE == 1 ? 1 : (split < p.tiles ? (p.tiles - split + p.splits - 1) / p.splits : 0);
-    auto tile_at = [&](uint64_t i) { return MODE == 1 ? (uint64_t)blockIdx.x : split + i * p.splits; };
-    int32_t h[kHopRegs];
-    auto hops_in = [&](uint64_t i) { if (p.sources && i < tiles) hops_load(h, p, tile_at(i), tid); };
-    auto hops_out = [&](uint64_t i, int buf) {
-        if (i >= tiles) return;
-        if (p.sources) hops_store(h, hs, p, tile_at(i), buf, tid);
-        else hops_none(hs, p, tile_at(i), buf, tid);
-    };
-    auto copy = [&](uint64_t i) {
-        if (i < tiles) {
-            const uint32_t st = sm + (uint32_t)(i % S::kKvStages) * 2 * S::kTileBytes;
-            const int64_t node0 = (int64_t)tile_at(i) * kAttnTile;
-            copy_nodes<DP>(st, kbase, p.k_row * 2, node0, p.n, p.d / 8, hs->seen[i & 3], tid);
-            copy_nodes<DP>(st + S::kTileBytes, vbase, p.v_row * 2, node0, p.n, p.d / 8, hs->seen[i & 3], tid);
+    if (warp < 8) {
+        const int w = warp >> 2, l = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21, shift = p.group2_log + 2;
+        const bool plain = !p.sources && (tile + 1) * kTcTile <= p.n;
+        bool ok = __all_sync(~0u, tc::bar_wait(&ctl->hop_full[0], 0, gave_up));
+        for (uint32_t u = w, k = 0; u < units && ok; u += 2, ++k) {
+            const uint32_t slot = u % S::kRing;
+            // row_full: this thread reads the row facts that came with the row tile
+            ok = tc::bar_wait(&ctl->row_full[slot], (u / S::kRing) & 1, gave_up) && tc::bar_wait(&ctl->sp_full[w], k & 1, gave_up);
+            ok = __all_sync(~0u, ok);
+            if (!ok) break;
+            tc::fence_after();
+            unit32<T>(tm + lanes + w * 64, reinterpret_cast<const RowInfo *>(smem + S::kInfo) + slot, plain, p.scale_log2,
+                      smem + S::kBuckets + l, reinterpret_cast<const uint8_t *>(lut), shift, nullptr, 0, 0);
+            tc::wait_st();
+            tc::fence_before();
+            tc::bar_arrive(&ctl->ds_full[w]);
+        }
+        // results: group 0 dv, group 1 dk, through the slots of values and keys
+        if (ok) ok = __all_sync(~0u, tc::bar_wait(&ctl->tile_full, 0, gave_up));
+        if (ok) {
+            tc::fence_after();
+            const uint32_t stage = sm + (w ? 0 : S::kSlot);
+            load_nodes<T, DP>(tm + lanes + (w ? kDk : kDv), w ? p.scale : 1.0f, stage, l);
+            __syncwarp();
+            store_nodes<T, DP>(stage, static_cast<T *>(w ? p.dk : p.dv) + (int64_t)hk * (w ? p.dk_head : p.dv_head),
+                               w ? p.dk_row : p.dv_row, tile * kTcTile, warp & 3, p);
+        }
+    } else if (warp < 12) {
+        hop_warps<1>(p, ctl, smem + S::kBuckets, warp - 8, lane, 1, tile, gave_up);
+    } else if (warp < 16) {
+        node_warps<DP, 2, 1>(p, ctl, sm, warp - 12, lane, hk, 1, tile, gave_up);
+        const int t = tid - 384;
+        bool ok = true;
+        for (uint32_t u = 0; u < units && ok; ++u) {
+            const uint32_t slot = u % S::kRing;
+            if (u >= (uint32_t)S::kRing) ok = __all_sync(~0u, tc::bar_wait(&ctl->row_empty[slot], (u / S::kRing - 1) & 1, gave_up));
+            if (!ok) break;
+            const uint32_t at = sm + S::kRow + slot * 2 * S::kRowTile;
+            copy_row_tile<DP>(at, p.q, p.q_row, p.q_head, hk * p.group, u, p, t, 128);
+            copy_row_tile<DP>(at + S::kRowTile, p.dout, p.dout_row, p.dout_head, hk * p.group, u, p, t, 128);
+            if (t < (int)sizeof(RowInfo) / 16)
+                cp16(sm + S::kInfo + slot * (int)sizeof(RowInfo) + t * 16,
+                     reinterpret_cast<const char *>(static_cast<const RowInfo *>(p.row_info) + (uint64_t)hk * p.row_tiles + u) + t * 16, 16);
+            tc::cp_arrive(&ctl->row_full[slot]);
         }
         cp_commit();
-    };
-
-    // p^T and ds^T of this warp's 16 nodes against the 32 rows in buffer rb
-    float pt[R8][4], dt[R8][4];
-    auto scores = [&](uint32_t kst, uint32_t vst, uint32_t rst, int rb, uint32_t row0, const uint8_t *bt) {
-#pragma unroll
-        for (int j = 0; j < R8; ++j)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) pt[j][x] = dt[j][x] = 0.0f;
-#pragma unroll
-        for (int kk = 0; kk < D16; ++kk) {
-            uint32_t a[4], b[4];
-            load_a<DP>(a, kst, warp * 16, kk, lane);
-#pragma unroll
-            for (int j = 0; j < R8; j += 2) {
-                load_b<DP>(b, rst, j * 8, kk, lane);
-                Elem<T>::mma(pt[j], a, b[0], b[1]);
-                Elem<T>::mma(pt[j + 1], a, b[2], b[3]);
-            }
-            load_a<DP>(a, vst, warp * 16, kk, lane);
-#pragma unroll
-            for (int j = 0; j < R8; j += 2) {
-                load_b<DP>(b, rst + S::kRowBytes, j * 8, kk, lane);
-                Elem<T>::mma(dt[j], a, b[0], b[1]);
-                Elem<T>::mma(dt[j + 1], a, b[2], b[3]);
-            }
-        }
-        const float *st = stat + rb * 3 * kBwdRows;
-        const uint32_t *cs = reinterpret_cast<const uint32_t *>(st) + 2 * kBwdRows;
-        const int na = warp * 16 + (lane >> 2), nb = na + 8;
-#pragma unroll
-        for (int j = 0; j < R8; ++j)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int r = j * 8 + (lane & 3) * 2 + x;
-                const float lse = st[r], dl = st[kBwdRows + r];
-                const uint32_t c = cs[r], g = (row0 + r) % G;
-                const float ba = lut[bt[c + na] * G + g], bb = lut[bt[c + nb] * G + g];
-                const float wa = ex2(fmaf(pt[j][x], p.scale_log2, ba) - lse);
-                const float wb = ex2(fmaf(pt[j][x + 2], p.scale_log2, bb) - lse);
-                pt[j][x] = wa;
-                pt[j][x + 2] = wb;
-                dt[j][x] = wa * (dt[j][x] - dl);
-                dt[j][x + 2] = wb * (dt[j][x + 2] - dl);
-            }
-    };
-    // acc[16 nodes x DP] += w^T (nodes x rows) times the row tile at rst (rows x DP)
-    auto node_product = [&](float (&acc)[DP / 8][4], const float (&w)[R8][4], uint32_t rst) {
-#pragma unroll
-        for (int j = 0; j < R8; j += 2) {
-            const uint32_t a[4] = {Elem<T>::pack(w[j][0], w[j][1]), Elem<T>::pack(w[j][2], w[j][3]),
-                                   Elem<T>::pack(w[j + 1][0], w[j + 1][1]), Elem<T>::pack(w[j + 1][2], w[j + 1][3])};
-#pragma unroll
-            for (int c = 0; c < D16; ++c) {
-                uint32_t b[4];
-                load_bt<DP>(b, rst, j * 8, c, lane);
-                Elem<T>::mma(acc[2 * c], a, b[0], b[1]);
-                Elem<T>::mma(acc[2 * c + 1], a, b[2], b[3]);
-            }
-        }
-    };
-    // the warp's 16 x DP accumulators to its rows of a tile in shared memory, then out in 16-byte pieces
-    auto store_nodes = [&](const float (&acc)[DP / 8][4], float f, uint32_t stage, void *out, int64_t s_row, int64_t s_head,
-                           int64_t node0) {
-        const int na = warp * 16 + (lane >> 2);
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < DP / 8; ++j) {
-            const uint32_t a = tile_addr<DP>(stage, na, j) + (lane & 3) * 4, b = tile_addr<DP>(stage, na + 8, j) + (lane & 3) * 4;
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(Elem<T>::pack(acc[j][0] * f, acc[j][1] * f)) : "memory");
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(b), "r"(Elem<T>::pack(acc[j][2] * f, acc[j][3] * f)) : "memory");
-        }
-        __syncwarp();
-        constexpr int C = DP / 8;
-        T *dst = static_cast<T *>(out) + (int64_t)hk * s_head;
-#pragma unroll
-        for (int i = lane; i < 16 * C; i += 32) {
-            const int r = warp * 16 + i / C, c = i % C;
-            if ((uint64_t)(node0 + r) < p.n && c < (int)(p.d / 8)) {
-                uint4 v;
-                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(tile_addr<DP>(stage, r, c)) : "memory");
-                __stcs(reinterpret_cast<uint4 *>(dst + (node0 + r) * s_row + c * 8), v);
-            }
-        }
-        __syncwarp();
-    };
-
-    if constexpr (MODE == 1) {
-        hops_in(0);
-        hops_out(0, 0);
-        __syncthreads();
-        copy(0);
-        const uint32_t nt = p.row_tiles;
-        if (nt) rows_in(0, 0), stats_in(0, 0);
-        cp_commit();
-        float dk[DP / 8][4], dv[DP / 8][4];
-#pragma unroll
-        for (int j = 0; j < DP / 8; ++j)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) dk[j][x] = dv[j][x] = 0.0f;
-        const uint32_t ks = sm, vs = sm + S::kTileBytes;
-        for (uint32_t i = 0; i < nt; ++i) {
-            cp_wait<0>();
-            __syncthreads();
-            if (i + 1 < nt) rows_in((i + 1) * kBwdRows, (i + 1) & 1), stats_in((i + 1) * kBwdRows, (i + 1) & 1);
-            cp_commit();
-            const uint32_t rs = sm + S::kRow + (i & 1) * 2 * S::kRowBytes;
-            scores(ks, vs, rs, i & 1, i * kBwdRows, hs->tile[0]);
-            node_product(dv, pt, rs + S::kRowBytes);
-            node_product(dk, dt, rs);
-        }
         cp_wait<0>();
-        __syncthreads();
-        const int64_t node0 = (int64_t)blockIdx.x * kAttnTile;
-        store_nodes(dv, 1.0f, vs, p.dv, p.dv_row, p.dv_head, node0);
-        store_nodes(dk, p.scale, vs, p.dk, p.dk_row, p.dk_head, node0);
     } else {
-        rows_in(fixed_row0, 0);
-        stats_in(fixed_row0, 0);
-        hops_in(0);
-        hops_out(0, 0);
-        hops_in(1);
-        __syncthreads();
-        copy(0);
-        float dq[kBwdRows / 16][DP / 32][4];     // all rows x this warp's quarter of head_dim
-#pragma unroll
-        for (int m = 0; m < kBwdRows / 16; ++m)
-#pragma unroll
-            for (int j = 0; j < DP / 32; ++j)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) dq[m][j][x] = 0.0f;
-        const uint32_t rs = sm + S::kRow;
-        const int hr = tid % kBwdRows, hp = tid / kBwdRows;    // the sum by bucket: this thread's row and quarter of the nodes
-        for (uint64_t i = 0; i < tiles; ++i) {
-            hops_out(i + 1, (i + 1) & 3);
-            if (tid < kAttnTile) hs->seen[(i + 2) & 3][tid] = 0;
-            cp_wait<0>();
-            __syncthreads();
-            copy(i + 1);
-            hops_in(i + 2);
-            const uint32_t ks = sm + (uint32_t)(i & 1) * 2 * S::kTileBytes, vs = ks + S::kTileBytes;
-            const uint8_t *bt = hs->tile[i & 3];
-            scores(ks, vs, rs, 0, fixed_row0, bt);
-            {   // ds^T to shared memory in the element type: operand of dq, and terms of dbias (summed in fp32)
-                const int na = warp * 16 + (lane >> 2);
-#pragma unroll
-                for (int j = 0; j < R8; ++j) {
-                    T *at = ds_s + na * S::kDsPitch + j * 8 + (lane & 3) * 2;
-                    *reinterpret_cast<uint32_t *>(at) = Elem<T>::pack(dt[j][0], dt[j][1]);
-                    *reinterpret_cast<uint32_t *>(at + 8 * S::kDsPitch) = Elem<T>::pack(dt[j][2], dt[j][3]);
-                }
-            }
-            if (MODE == 0) {
-                const int64_t node0 = (int64_t)tile_at(i) * kAttnTile;
-                float acc[DP / 8][4];
-#pragma unroll
-                for (int j = 0; j < DP / 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-                node_product(acc, pt, rs + S::kRowBytes);
-                store_nodes(acc, 1.0f, vs, p.dv, p.dv_row, p.dv_head, node0);
-#pragma unroll
-                for (int j = 0; j < DP / 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-                node_product(acc, dt, rs);
-                store_nodes(acc, p.scale, vs, p.dk, p.dk_row, p.dk_head, node0);
-            }
-            __syncthreads();
-            const uint32_t dss = sm + S::kDs;
-#pragma unroll
-            for (int kk = 0; kk < kAttnTile / 16; ++kk) {
-                uint32_t a[kBwdRows / 16][4];
-#pragma unroll
-                for (int m = 0; m < kBwdRows / 16; ++m) {
-                    // A (rows x nodes) from ds^T [node][row]: transposed loads; matrices (nodes 0-7, rows 0-7),
-                    // (nodes 0-7, rows 8-15), (nodes 8-15, rows 0-7), (nodes 8-15, rows 8-15)
-                    const int nd = kk * 16 + (lane & 7) + ((lane >> 4) << 3), rw = m * 16 + ((lane >> 3) & 1) * 8;
-                    ldsm4t(a[m], dss + (nd * S::kDsPitch + rw) * 2);
-                }
-#pragma unroll
-                for (int c = 0; c < DP / 64; ++c) {
-                    uint32_t b[4];
-                    load_bt<DP>(b, ks, kk * 16, warp * (DP / 64) + c, lane);
-#pragma unroll
-                    for (int m = 0; m < kBwdRows / 16; ++m) {
-                        Elem<T>::mma(dq[m][2 * c], a[m], b[0], b[1]);
-                        Elem<T>::mma(dq[m][2 * c + 1], a[m], b[2], b[3]);
-                    }
-                }
-            }
-            if (p.buckets) {
-                constexpr int N = kAttnTile / (kAttnThreads / kBwdRows);
-                const uint8_t *bc = bt + reinterpret_cast<const uint32_t *>(stat)[2 * kBwdRows + hr] + hp * N;
-                const T *d = ds_s + hp * N * S::kDsPitch + hr;
-#pragma unroll
-                for (int k = 0; k < N; k += 4) {
-                    const uint32_t b4 = *reinterpret_cast<const uint32_t *>(bc + k);
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        hist[((b4 >> (8 * y)) & 255) * kAttnThreads + tid] += Elem<T>::to_float(d[(k + y) * S::kDsPitch]);
-                }
-            }
+        const bool lead = tc::elect();
+        const uint32_t dn = (p.d + 15) & ~15u, id_s = tc::idesc(kBf16, 32, false, false), id_n = tc::idesc(kBf16, dn, false, true);
+        bool ok = tc::bar_wait(&ctl->full[0], 0, gave_up) && tc::bar_wait(&ctl->full[1], 0, gave_up);
+        auto scores = [&](uint32_t u) {
+            const uint32_t w = u & 1, slot = u % S::kRing;
+            ok = tc::bar_wait(&ctl->row_full[slot], (u / S::kRing) & 1, gave_up);
+            if (!ok) return;
+            tc::fence_async();
+            tc::fence_after();
+            const uint32_t qa = sm + S::kRow + slot * 2 * S::kRowTile;
+            score_products<DP, S::kPanel>(lead, tm + w * 64, tc::desc(sm, S::kPanel), tc::desc(qa, 4096), tc::desc(sm + S::kSlot, S::kPanel),
+                                          tc::desc(qa + S::kRowTile, 4096), id_s, dn);
+            tc::commit(lead, &ctl->sp_full[w]);
+        };
+        if (ok && units > 0) scores(0);
+        if (ok && units > 1) scores(1);
+        for (uint32_t u = 0; u < units && ok; ++u) {
+            const uint32_t w = u & 1, slot = u % S::kRing;
+            ok = tc::bar_wait(&ctl->ds_full[w], (u >> 1) & 1, gave_up);
+            if (!ok) break;
+            tc::fence_after();
+            const uint32_t qa = sm + S::kRow + slot * 2 * S::kRowTile;
+            node_products(lead, tm + w * 64, tm + kDv, tm + kDk, tc::desc(qa, 4096), tc::desc(qa + S::kRowTile, 4096), id_n, u > 0);
+            tc::commit(lead, &ctl->row_empty[slot]);
+            if (u + 1 == units) tc::commit(lead, &ctl->tile_full);
+            if (u + 2 < units) scores(u + 2);
         }
-        cp_wait<0>();
-        // partial dq of this block: part[split][t][h][d]
-        const uint32_t T_ = p.T;
-#pragma unroll
-        for (int m = 0; m < kBwdRows / 16; ++m)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const uint32_t row = fixed_row0 + m * 16 + (lane >> 2) + y * 8;
-                if (row >= p.rows) continue;
-                const uint32_t t = row / G, hd = hk * G + row - t * G;
-                float *at = p.part + (((uint64_t)split * T_ + t) * p.hq + hd) * p.d;
-#pragma unroll
-                for (int j = 0; j < DP / 32; ++j) {
-                    const uint32_t c = warp * (DP / 4) + j * 8 + (lane & 3) * 2;
-                    if (c < p.d) *reinterpret_cast<float2 *>(at + c) = make_float2(dq[m][j][2 * y], dq[m][j][2 * y + 1]);
-                }
-            }
-        __syncthreads();
-        // partial dbias: part_ml[split][t][h][bucket]
-        for (uint32_t i = tid; i < p.buckets * kBwdRows; i += kAttnThreads) {
-            const uint32_t b = i % p.buckets, r = i / p.buckets, row = fixed_row0 + r;
-            if (row >= p.rows) continue;
-            float s = 0.0f;
-#pragma unroll
-            for (int k = 0; k < kAttnThreads / kBwdRows; ++k) s += hist[(b + 1) * kAttnThreads + k * kBwdRows + r];
-            const uint32_t t = row / G, hd = hk * G + row - t * G;
-            p.part_ml[(((uint64_t)split * T_ + t) * p.hq + hd) * p.buckets + b] = s;
-        }
+        if (!ok) tc::drain(lead, &ctl->drained, 0);
     }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 16) tc::dealloc(tm, kCols);
+    if (tid == 0 && *gave_up) atomicOr(p.status, K2T_STATUS_WAIT_TIMEOUT);
 }
 
-// dq = scale * sum over splits; dbias = sum over splits and queries, in a fixed order.
-// Blocks [0, T * hq): a row of dq each; then one block per head for dbias.
+// dq = scale * sum over splits; dbias = sum over splits and row groups, in a fixed order.
+// Blocks [0, T * hq): a row of dq each; then one block per (head, bucket).
 template <typename T>
 __global__ void __launch_bounds__(256) attn_bwd_join_kernel(const __grid_constant__ AttnParams p)
 {
-    __shared__ float red[256];
     const int tid = threadIdx.x;
     const uint64_t rows = (uint64_t)p.T * p.hq;
     if (blockIdx.x < rows) {
@@ -407,22 +648,18 @@ __global__ void __launch_bounds__(256) attn_bwd_join_kernel(const __grid_constan
         }
         return;
     }
-    // block: (head, bucket)
-    const uint64_t at = blockIdx.x - rows;
-    const uint32_t hd = (uint32_t)(at / p.buckets), b = (uint32_t)(at - (uint64_t)hd * p.buckets);
+    __shared__ float red[256];
+    const uint64_t at = blockIdx.x - rows;               // head * buckets + bucket
     float s = 0.0f;
-    const uint64_t total = (uint64_t)p.splits * p.T;
-    for (uint64_t i = tid; i < total; i += 256) s += p.part_ml[(i * p.hq + hd) * p.buckets + b];
+    for (uint32_t i = tid; i < p.hist_parts; i += 256) s += p.part_ml[(uint64_t)i * p.hq * p.buckets + at];
     red[tid] = s;
     __syncthreads();
     for (int x = 128; x; x >>= 1) {
         if (tid < x) red[tid] += red[tid + x];
         __syncthreads();
     }
-    if (tid == 0) {
-        // a masked bucket has weights of 0 and so a gradient of 0
-        static_cast<T *>(p.dbias)[(uint64_t)hd * p.buckets + b] = Elem<T>::from_float(red[0]);
-    }
+    // a masked bucket has weights of 0 and so a gradient of 0
+    if (tid == 0) static_cast<T *>(p.dbias)[at] = Elem<T>::from_float(red[0]);
 }
 
 }  // namespace k2t

@@ -36,11 +36,8 @@
 
 namespace k2t {
 
-constexpr int kTcTile = 128;
 constexpr int kTcThreads = 640;
-constexpr int kTcPitch = 144;       // bytes per column of a bucket tile: 16-byte loads of 8 columns meet no bank twice
 constexpr int kTcBufs = 4;          // bucket tiles
-constexpr int kTcLutAlign = 8192;   // the bias table's alignment, above its size: its address joins an index by OR
 constexpr float kTcLag = 8.0f;
 
 template <int DP, bool TWO> struct TcSmem {
@@ -57,7 +54,7 @@ template <int DP, bool TWO> struct TcSmem {
         uint8_t byte_of[257 + 15];        // bucket byte of hops + 1
     };
     static constexpr int kLut = kCtl + (int)((sizeof(Ctl) + 15) / 16 * 16);
-    static size_t bytes(const AttnParams &p) { return kLut + kTcLutAlign + (size_t)(p.buckets + 2) * p.group2 * 4; }
+    static size_t bytes(const AttnParams &p) { return kLut + (size_t)(p.buckets + 2) * p.group2 * 4; }
 };
 
 // Two fp32 operations in one instruction.
@@ -82,17 +79,10 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-__device__ __forceinline__ float lds_f(uint32_t at)
-{
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
-    return v;
-}
-
 // Scores of 32 nodes in units of log2, biased and masked, and their maximum
-// with `top`.  bt: shared-memory address of their bucket bytes; a byte b's
-// bias lies at lg | b << shift (floats of 2^k query heads, k = shift - 2).
-__device__ __forceinline__ float bias32(uint32_t (&s)[32], float scale, bool plain, uint32_t bt, uint32_t lg, uint32_t shift, float top)
+// with `top`.  bt: their bucket bytes; a byte b's bias lies at lg + (b <<
+// shift) (floats of 2^k query heads, k = shift - 2).
+__device__ __forceinline__ float bias32(uint32_t (&s)[32], float scale, bool plain, const uint8_t *bt, const uint8_t *lg, uint32_t shift, float top)
 {
     const float2 sc = make_float2(scale, scale);
     if (plain) {
@@ -108,13 +98,13 @@ __device__ __forceinline__ float bias32(uint32_t (&s)[32], float scale, bool pla
     const uint32_t mask = 255u << shift;
 #pragma unroll
     for (int e = 0; e < 32; e += 16) {
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(bt + e));
+        const uint4 b16 = *reinterpret_cast<const uint4 *>(bt + e);
+        const uint32_t w[4] = {b16.x, b16.y, b16.z, b16.w};
 #pragma unroll
         for (int y = 0; y < 16; y += 2) {
             const uint32_t v = w[y >> 2];
             const uint32_t i0 = (y & 3) ? v >> (16 - shift) : v << shift, i1 = (y & 3) ? v >> (24 - shift) : v >> (8 - shift);
-            const float2 bias = make_float2(lds_f((i0 & mask) | lg), lds_f((i1 & mask) | lg));
+            const float2 bias = make_float2(*reinterpret_cast<const float *>(lg + (i0 & mask)), *reinterpret_cast<const float *>(lg + (i1 & mask)));
             const float2 x = fma2(make_float2(__uint_as_float(s[e + y]), __uint_as_float(s[e + y + 1])), sc, bias);
             s[e + y] = __float_as_uint(x.x);
             s[e + y + 1] = __float_as_uint(x.y);
@@ -148,8 +138,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
     extern __shared__ __align__(1024) uint8_t smem[];
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + S::kCtl);
     const uint32_t sm = tc::saddr(smem);
-    const uint32_t lut_at = (sm + S::kLut + kTcLutAlign - 1) & ~(uint32_t)(kTcLutAlign - 1);
-    float *lut = reinterpret_cast<float *>(smem + (lut_at - sm));
+    float *lut = reinterpret_cast<float *>(smem + S::kLut);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t hk = blockIdx.y, split = blockIdx.x % p.splits;
     const uint32_t row0 = blockIdx.x / p.splits * (TWO ? 256 : kRows);
@@ -204,99 +193,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
     volatile uint32_t *gave_up = &ctl->gave_up;
 
     if (warp >= 8 && warp < 12) {
-        // ---- hops: lane = node 32 hw + lane of a tile ----
-        const int hw = warp - 8;
-        const uint32_t cols = ctl->columns, B = p.sources;
-        const bool all = ctl->all, every = cols == (B >= 32 ? ~0u : (1u << B) - 1);
-        const bool vec = (B & 3) == 0 && ((uintptr_t)p.hops & 15) == 0;
-        int32_t h[32];
-        auto hops_in = [&](uint32_t i) {
-            const uint64_t node = tile_at(i) * kTcTile + hw * 32 + lane;
-            const bool in = i < tiles && node < p.n;
-            const int32_t *at = p.hops + node * B;
-#pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-                if (c >= (int)B) break;
-                if (vec) {
-                    int4 x = make_int4(-1, -1, -1, -1);
-                    if (in) asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(at + c));
-                    h[c] = x.x, h[c + 1] = x.y, h[c + 2] = x.z, h[c + 3] = x.w;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        h[c + e] = -1;
-                        if (in && c + e < (int)B) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(h[c + e]) : "l"(at + c + e));
-                    }
-                }
-            }
-        };
-        if (B) hops_in(0);
-        for (uint32_t i = 0; i < tiles; ++i) {
-            const uint32_t buf = i % kTcBufs;
-            if (i >= kTcBufs && !__all_sync(~0u, tc::bar_wait(&ctl->hop_empty[buf], (i / kTcBufs - 1) & 1, gave_up))) break;
-            const bool in = tile_at(i) * kTcTile + hw * 32 + lane < p.n;
-            uint8_t *bt = smem + S::kBuckets + buf * 33 * kTcPitch + hw * 32 + lane;
-            int32_t none = -1;                     // sign bit: no column in use sees this node
-#pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-                if (c >= (int)B) break;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    bt[(c + e) * kTcPitch] = ctl->byte_of[min(h[c + e], 255) + 1];   // columns past B: bytes that nothing reads
-                    none &= every || ((cols >> (c + e)) & 1) ? h[c + e] : -1;
-                }
-            }
-            bt[B * kTcPitch] = in ? p.buckets + 1 : 0;
-            const uint32_t seen = __ballot_sync(~0u, in && (!B || all || none >= 0));
-            __syncwarp();
-            if (lane == 0) {
-                ctl->seen[buf][hw] = seen;
-                tc::bar_arrive(&ctl->hop_full[buf]);
-            }
-            if (B) hops_in(i + 1);
-        }
+        hop_warps<kTcBufs>(p, ctl, smem + S::kBuckets, warp - 8, lane, tiles, split, gave_up);
     } else if (warp >= 12 && warp < 16) {
-        // ---- copies: this warp brings nodes [32 cw, 32 cw + 32) of every tile ----
-        const int cw = warp - 12;
-        constexpr int C = DP / 8, RP = 32 / C, kTurn = 8 / RP;     // chunks a row, rows a pass, passes until the swizzle repeats
-        const uint32_t c = lane % C, r0 = lane / C;
-        const uint32_t fill = (p.d / 8 + 1) & ~1u;                 // chunks the products read: whole steps of 16 values
-        uint32_t at[kTurn];
-#pragma unroll
-        for (int k = 0; k < kTurn; ++k) at[k] = sm + tc::chunk(cw * 32 + k * RP + r0, c, S::kPanel) - k * RP * 128;
-        uint32_t item = 0;
-        bool ok = true;
-        auto bring = [&](const char *src, int64_t step, uint32_t seen) {
-            const uint32_t slot = item % S::kSlots;
-            if (item >= (uint32_t)S::kSlots) ok = __all_sync(~0u, tc::bar_wait(&ctl->empty[slot], (item / S::kSlots - 1) & 1, gave_up));
-            if (!ok) return;
-            if (c < fill) {
-#pragma unroll
-                for (int k = 0; k < 32 / RP; ++k) {
-                    // a node that no query sees, or past n, or a chunk past head_dim: zeros, and nothing is read
-                    cp16(at[k % kTurn] + slot * S::kSlot + k * RP * 128, src, (seen >> (k * RP)) & 1 ? 16 : 0);
-                    src += step;
-                }
-            }
-            tc::cp_arrive(&ctl->full[slot]);      // counts this thread's copies once they have landed
-            ++item;
-        };
-        const int64_t kstep = RP * p.k_row * 2, vstep = RP * p.v_row * 2;
-        const char *k0 = static_cast<const char *>(p.k) + ((int64_t)hk * p.k_head + c * 8) * 2;
-        const char *v0 = static_cast<const char *>(p.v) + ((int64_t)hk * p.v_head + c * 8) * 2;
-        for (uint32_t i = 0; i < tiles && ok; ++i) {
-            const uint32_t buf = i % kTcBufs;
-            ok = __all_sync(~0u, tc::bar_wait(&ctl->hop_full[buf], (i / kTcBufs) & 1, gave_up));
-            if (!ok) break;
-            const uint32_t seen = c < p.d / 8 ? ctl->seen[buf][cw] >> r0 : 0;
-            const int64_t node = (int64_t)(tile_at(i) * kTcTile) + cw * 32 + r0;
-            bring(k0 + node * p.k_row * 2, kstep, seen);
-            if (ok) bring(v0 + node * p.v_row * 2, vstep, seen);
-        }
-        cp_commit();
-        cp_wait<0>();
+        node_warps<DP, S::kSlots, kTcBufs>(p, ctl, sm, warp - 12, lane, hk, tiles, split, gave_up);
     } else if (warp >= 16) {
-        if (warp == 16 && lane == 0) {
+        if (warp == 16) {
+            const bool lead = tc::elect();
             // ---- products ----
             const uint32_t id_s = tc::idesc(kBf16, kTcTile, false, false);
             const uint32_t dn = (p.d + 15) & ~15u, id_o = tc::idesc(kBf16, dn, false, true);
@@ -308,13 +210,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
                 if (!ok) return;
                 tc::fence_async();       // the copies were made by threads, the product reads through the async proxy
                 tc::fence_after();
-                const uint32_t q = base + S::kQ + (TWO ? w * S::kSlot : 0), k = base + slot * S::kSlot;
-                for (uint32_t kk = 0; kk < dn / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * S::kPanel + (kk & 3) * 32;
-                    tc::mma_ss(tm + w * 128, tc::desc(q + off, S::kPanel), tc::desc(k + off, S::kPanel), id_s, kk > 0);
-                }
-                tc::commit(&ctl->s_full[w]);
-                if (!TWO || w == 1) tc::commit(&ctl->empty[slot]);
+                const uint64_t q = tc::desc(base + S::kQ + (TWO ? w * S::kSlot : 0), S::kPanel), k = tc::desc(base + slot * S::kSlot, S::kPanel);
+#pragma unroll
+                for (uint32_t kk = 0; kk < DP / 16; ++kk)
+                    if (kk * 16 < dn) {
+                        const uint32_t off = (kk >> 2) * S::kPanel + (kk & 3) * 32;
+                        tc::mma_ss(lead, tm + w * 128, q, off, k, off, id_s, kk > 0);
+                    }
+                tc::commit(lead, &ctl->s_full[w]);
+                if (!TWO || w == 1) tc::commit(lead, &ctl->empty[slot]);
             };
             if (units > 0) scores(0);
             if (ok && units > 1) scores(1);
@@ -325,14 +229,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
                 if (!ok) break;
                 tc::fence_async();
                 tc::fence_after();
-                const uint32_t v = base + slot * S::kSlot;
+                const uint64_t v = tc::desc(base + slot * S::kSlot, S::kPanel);
+#pragma unroll
                 for (uint32_t kk = 0; kk < kTcTile / 16; ++kk)
-                    tc::mma_ts(tm + 256 + w * DP, tm + w * 128 + kk * 8, tc::desc(v + kk * 2048, S::kPanel), id_o, u > 1 || kk > 0);
-                if (!TWO || w == 1) tc::commit(&ctl->empty[slot]);
-                if (u + 2 >= units) tc::commit(&ctl->o_full[w]);
+                    tc::mma_ts(lead, tm + 256 + w * DP, tm + w * 128 + kk * 8, v, kk * 2048, id_o, u > 1 || kk > 0);
+                if (!TWO || w == 1) tc::commit(lead, &ctl->empty[slot]);
+                if (u + 2 >= units) tc::commit(lead, &ctl->o_full[w]);
                 if (u + 2 < units) scores(u + 2);
             }
-            if (!ok) tc::drain(&ctl->drained, 0);
+            if (!ok) tc::drain(lead, &ctl->drained, 0);
         }
         __syncwarp();
     } else {
@@ -342,9 +247,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
         const uint32_t row = row0 + (TWO ? w * 128 : 0) + l % kRows;
         const int key0 = l / kRows * KW;                              // this copy's part of a tile
         const uint32_t col = row < p.rows ? row_column(p, row) : 0;
-        const uint32_t G = p.group, lg = lut_at | (row < p.rows ? row % G : 0) * 4, shift = p.group2_log + 2;
+        const uint32_t G = p.group, shift = p.group2_log + 2;
+        const uint8_t *lg = reinterpret_cast<const uint8_t *>(lut + (row < p.rows ? row % G : 0));
         const uint32_t s_at = tm + lanes + w * 128, o_at = tm + lanes + 256 + w * DP;
-        const uint32_t bt0 = sm + S::kBuckets + col * kTcPitch + key0;
+        const uint8_t *bt0 = smem + S::kBuckets + col * kTcPitch + key0;
         float m = -INFINITY;
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         bool ok = true;
@@ -356,7 +262,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
             if (!ok) break;
             tc::fence_after();
             const bool plain = !p.sources && (tile_at(i) + 1) * kTcTile <= p.n;   // no table, no node past the end
-            const uint32_t bt = bt0 + buf * 33 * kTcPitch;
+            const uint8_t *bt = bt0 + buf * 33 * kTcPitch;
             float top = -INFINITY;
             uint32_t s[32];
             if (KW == 32) {

@@ -49,26 +49,37 @@ template <typename T> int launch_forward(const AttnParams &p, int bm, cudaStream
     return K2T_OK;
 }
 
+// Row tiles that the one-pass kernel holds: 4 of head_dim 64 or less, 2 of more (shared and tensor memory).
+inline uint32_t bwd_fused_tiles(uint32_t d) { return d <= 64 ? 4 : 2; }
+
+template <typename T, int DP, int RT, bool DKV> int backward_nodes(const AttnParams &p, cudaStream_t st)
+{
+    const uint32_t groups = (p.row_tiles + RT - 1) / RT;
+    return attn_launch(attn_bwd_nodes_kernel<T, DP, RT, DKV>, dim3(p.splits * groups, p.hkv), kBwdThreads,
+                       BwdSmem<DP, RT, DKV>::bytes(p), p, st);
+}
+
 template <typename T, int DP> int backward_dim(const AttnParams &p, cudaStream_t st)
 {
-    const dim3 by_rows(p.splits * p.row_tiles, p.hkv), by_nodes((unsigned)p.tiles, p.hkv);
-    if (p.row_tiles == 1) return attn_launch(attn_bwd_kernel<T, DP, 0>, by_rows, kAttnThreads, BwdSmem<DP, 0>::bytes(p), p, st);
-    int rc = K2T_OK;
-    if (p.tiles) rc = attn_launch(attn_bwd_kernel<T, DP, 1>, by_nodes, kAttnThreads, BwdSmem<DP, 1>::bytes(p), p, st);
-    if (!rc && p.rows) rc = attn_launch(attn_bwd_kernel<T, DP, 2>, by_rows, kAttnThreads, BwdSmem<DP, 2>::bytes(p), p, st);
-    return rc;
+    if (p.row_tiles == 1) return backward_nodes<T, DP, 1, true>(p, st);
+    if (p.row_tiles == 2) return backward_nodes<T, DP, 2, true>(p, st);
+    if constexpr (DP == 64) {
+        if (p.row_tiles <= 4) return backward_nodes<T, DP, 4, true>(p, st);
+    }
+    if (p.tiles) {
+        int rc = attn_launch(attn_bwd_rows_kernel<T, DP>, dim3((unsigned)p.tiles, p.hkv), kBwdRowThreads, BwdRowSmem<DP>::bytes(p), p, st);
+        if (rc) return rc;
+    }
+    return backward_nodes<T, DP, 4, false>(p, st);
 }
 
 template <typename T> int launch_backward(const AttnParams &p, cudaStream_t st)
 {
-    const uint64_t rows = (uint64_t)p.T * p.hq;
-    if (rows) {
-        attn_delta_kernel<T><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p);
-        K2T_ATTN_CUDA(cudaGetLastError());
-    }
+    attn_rows_kernel<T><<<dim3(p.row_tiles * (kBwdRows / 8), p.hkv), 256, 0, st>>>(p);
+    K2T_ATTN_CUDA(cudaGetLastError());
     int rc = p.d <= 64 ? backward_dim<T, 64>(p, st) : backward_dim<T, 128>(p, st);
     if (rc) return rc;
-    const uint64_t blocks = rows + (uint64_t)p.hq * p.buckets;
+    const uint64_t blocks = (uint64_t)p.T * p.hq + (uint64_t)p.hq * p.buckets;
     if (blocks) {
         attn_bwd_join_kernel<T><<<(unsigned)blocks, 256, 0, st>>>(p);
         K2T_ATTN_CUDA(cudaGetLastError());

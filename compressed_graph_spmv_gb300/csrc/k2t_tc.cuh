@@ -100,6 +100,30 @@ __device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16])
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
 }
 
+__device__ __forceinline__ void ld16(uint32_t (&r)[16], uint32_t at)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(at) : "memory");
+}
+__device__ __forceinline__ void st8(uint32_t at, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ void ld8(uint32_t (&r)[8], uint32_t at)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(at) : "memory");
+}
+__device__ __forceinline__ void st4(uint32_t at, const uint32_t (&r)[4])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
 // ---- matrix products ------------------------------------------------------------
 // Operand tiles in shared memory: panels of 64 16-bit values (128 bytes) a
 // row, 1024-byte groups of 8 rows, the 16-byte chunks of a row xored with the
@@ -123,28 +147,39 @@ __device__ __forceinline__ uint32_t idesc(bool bf16, uint32_t n, bool a_mn, bool
     return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
            ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add)
+// The products are issued by one lane of a warp whose lanes all run the issuing
+// code: descriptors and addresses then stay in uniform registers, where the
+// instruction wants them.  `off` (bytes, a multiple of 16) moves an operand's start.
+__device__ __forceinline__ bool elect()
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(id), "r"((uint32_t)add) : "memory");
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one;
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add)
+__device__ __forceinline__ void mma_ss(bool lead, uint32_t d, uint64_t a, uint32_t a_off, uint64_t b, uint32_t b_off, uint32_t id, bool add)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(id), "r"((uint32_t)add) : "memory");
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a + (a_off >> 4)), "l"(b + (b_off >> 4)), "r"(id), "r"((uint32_t)add), "r"((uint32_t)lead) : "memory");
+}
+__device__ __forceinline__ void mma_ts(bool lead, uint32_t d, uint32_t a, uint64_t b, uint32_t b_off, uint32_t id, bool add)
+{
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b + (b_off >> 4)), "r"(id), "r"((uint32_t)add), "r"((uint32_t)lead) : "memory");
 }
 // After a wait ran out: lets the products in flight end (at most 2^28 cycles) before tensor memory is freed.
-__device__ __forceinline__ void commit(uint64_t *b);
-__device__ __forceinline__ void drain(uint64_t *b, uint32_t parity)
+__device__ __forceinline__ void commit(bool lead, uint64_t *b);
+__device__ __forceinline__ void drain(bool lead, uint64_t *b, uint32_t parity)
 {
-    commit(b);
+    commit(lead, b);
     const long long start = clock64();
     while (!bar_peek(b, parity) && clock64() - start < (1ll << 28)) {}
 }
-// Arrives on the barrier when every product issued so far by this thread is done.
-__device__ __forceinline__ void commit(uint64_t *b)
+// The leading lane's arrival on the barrier, when every product that it has issued so far is done.
+__device__ __forceinline__ void commit(bool lead, uint64_t *b)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(b)) : "memory");
+    if (lead) asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(b)) : "memory");
 }
 
 template <int N> __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
