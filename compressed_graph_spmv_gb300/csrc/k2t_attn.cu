@@ -22,7 +22,7 @@ int check_sizes(const k2t_attn *a)
     if (a->head_dim > K2T_ATTN_MAX_HEAD_DIM || a->n_heads / a->n_kv_heads > K2T_ATTN_MAX_GROUP) return K2T_ERANGE;
     if (a->n_kv_heads > 65535) return K2T_ERANGE;
     if (a->n_sources > K2T_MAX_BATCH || a->n_buckets > K2T_ATTN_MAX_BUCKETS) return K2T_ERANGE;
-    if (a->n_nodes > (1ull << 32) || (uint64_t)a->n_queries * a->n_heads > (1ull << 30)) return K2T_ERANGE;
+    if (a->n_nodes > K2T_ATTN_MAX_NODES || (uint64_t)a->n_queries * a->n_heads > (1ull << 30)) return K2T_ERANGE;
     if (a->n_buckets && !a->n_sources) return K2T_EINVAL;
     if (!(a->scale == a->scale)) return K2T_EINVAL;
     for (uint32_t b = 0; b < a->n_buckets; ++b)
@@ -30,7 +30,11 @@ int check_sizes(const k2t_attn *a)
     return K2T_OK;
 }
 
-bool aligned(const void *p, int64_t row, int64_t head) { return !((uintptr_t)p & 15u) && !(row & 7) && !(head & 7); }
+// Rows of 16-byte pieces, with pitches that a tensor map holds (40 bits of bytes).
+bool aligned(const void *p, int64_t row, int64_t head)
+{
+    return !((uintptr_t)p & 15u) && !(row & 7) && !(head & 7) && row >= 0 && head >= 0 && row < (1ll << 38) && head < (1ll << 38);
+}
 
 constexpr uint64_t kSms = 152;
 
@@ -92,6 +96,35 @@ void make_plan(const k2t_attn *a, bool backward, Plan &pl)
     pl.part_floats = p.splits > 1 ? p.splits * rows * p.d : 0;
     pl.ml_floats = p.splits > 1 ? p.splits * rows * 2 : 0;
     pl.info_floats = 0;
+}
+
+// The driver's tensor map encoder, found through the runtime (nothing links to libcuda).
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encoder()
+{
+    static const EncodeTiled f = [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return reinterpret_cast<EncodeTiled>(fn);
+    }();
+    return f;
+}
+
+// A gradient [n, kv heads, head_dim] as boxes of 128 nodes x 64 values of one head.
+bool node_map(CUtensorMap *map, void *base, int64_t row, int64_t head, const AttnParams &p, uint32_t dtype)
+{
+    const cuuint64_t dims[3] = {p.d, p.hkv, p.n};
+    // a dimension of one value has no pitch
+    const cuuint64_t strides[2] = {(cuuint64_t)(p.hkv > 1 ? head : p.d) * 2, (cuuint64_t)(p.n > 1 ? row : p.d) * 2};
+    const cuuint32_t box[3] = {64, 1, kTcTile}, step[3] = {1, 1, 1};
+    return encoder() && encoder()(map, dtype == K2T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base,
+                                  dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 constexpr uint64_t kWorkHead = 256;   // the device status word
@@ -183,6 +216,9 @@ int k2t_attn_backward(const k2t_attn *a, void *work, uint64_t work_bytes, void *
         !aligned(a->dk, a->dk_row, a->dk_head) || !aligned(a->dv, a->dv_row, a->dv_head))
         return K2T_EINVAL;
     fill_pointers(a, work, pl);
+    if (a->n_nodes && (!node_map(&pl.p.dk_map, a->dk, a->dk_row, a->dk_head, pl.p, a->dtype) ||
+                       !node_map(&pl.p.dv_map, a->dv, a->dv_row, a->dv_head, pl.p, a->dtype)))
+        return K2T_ECUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return a->dtype == K2T_BF16 ? attn_backward_bf16(pl.p, st) : attn_backward_fp16(pl.p, st);
 }

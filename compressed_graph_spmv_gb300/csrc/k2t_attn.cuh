@@ -16,6 +16,7 @@
 // bytes and keeps what they hold away from the products.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -54,6 +55,7 @@ struct AttnParams {
     float *part_ml;
     void *row_info;           // RowInfo[hkv][row_tiles * 32] (backward)
     uint32_t hist_parts;      // partial dbias tables
+    CUtensorMap dk_map, dv_map;   // (head_dim, kv heads, nodes), boxes of 64 x 1 x 128 (backward)
     uint32_t *status;         // device status word, at the start of the work buffer
     uint8_t bucket_of[256];   // bucket of each hop count; larger hops share the last
 };
@@ -156,27 +158,44 @@ __device__ __forceinline__ void hop_warps(const AttnParams &p, Ctl *ctl, uint8_t
     while (W < B) W *= 2;
     const uint32_t col = lane & (W - 1), first = lane & ~(W - 1);      // first node of this lane's part
     const bool on = col < B, used = on && ((cols >> col) & 1);
-    constexpr int kAhead = 8;                                          // nodes a load brings
-    int32_t h[kAhead];
-    uint32_t i = 0, k0 = 0;                                            // tile and node of the loads in flight
-    const int32_t *at = p.hops;
-    uint32_t left = 0;                                                 // nodes of the lane's part from `at` on
-    auto hops_in = [&]() {
-        if (k0 == 0 && i < tiles) {
-            const uint64_t node = (tile0 + (uint64_t)i * p.splits) * kTcTile + hw * 32 + first;
-            at = p.hops + node * B + col;
-            left = on && node < p.n ? (uint32_t)min((uint64_t)W, p.n - node) : 0;
+    // The loads of a tile are in flight while the tile before is turned into bytes: 16 nodes of the part at a time, a
+    // set of registers each.
+    int32_t ha[16], hb[16];
+    auto hops_in = [&](int32_t (&h)[16], uint32_t t, uint32_t k) {
+        const uint64_t node = (tile0 + (uint64_t)t * p.splits) * kTcTile + hw * 32 + first + k;
+        const int32_t *at = p.hops + node * B + col;
+        const uint32_t left = t < tiles && on && node < p.n ? (uint32_t)min((uint64_t)(W - k), p.n - node) : 0;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            h[e] = -1;
+            if (e < (int)left) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(h[e]) : "l"(at));
+            at += B;
+        }
+    };
+    auto hops_out = [&](const int32_t (&h)[16], uint8_t *to) {       // bytes of up to 16 nodes; returns which are seen
+        uint32_t unseen = 0;
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            if (e >= (int)W) break;
+            uint32_t b = 0;
+#pragma unroll
+            for (int y = 3; y >= 0; --y) b = b << 8 | ctl->byte_of[min(h[e + y] + 1, 256)];
+            if (on) {
+                if (W >= 4) *reinterpret_cast<uint32_t *>(to + e) = b;
+                else {
+                    to[0] = b;
+                    if (W == 2) to[1] = b >> 8;
+                }
+            }
         }
 #pragma unroll
-        for (int e = 0; e < kAhead; ++e) {
-            h[e] = -1;
-            if (k0 + e < left && i < tiles) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(h[e]) : "l"(at + (int64_t)e * B));
-        }
-        at += (int64_t)kAhead * B;
-        k0 += kAhead;
-        if (k0 >= W) k0 = 0, ++i;
+        for (int e = 15; e >= 0; --e) unseen = __funnelshift_l(h[e], unseen, 1);      // a negative hop count's sign
+        return ~unseen & 0xffff;
     };
-    if (B) hops_in();
+    if (B) {
+        hops_in(ha, 0, 0);
+        if (W > 16) hops_in(hb, 0, 16);
+    }
     for (uint32_t t = 0; t < tiles; ++t) {
         const uint32_t buf = t % BUFS;
         if (t >= BUFS && !__all_sync(~0u, tc::bar_wait(&ctl->hop_empty[buf], (t / BUFS - 1) & 1, gave_up))) break;
@@ -184,27 +203,13 @@ __device__ __forceinline__ void hop_warps(const AttnParams &p, Ctl *ctl, uint8_t
         const uint64_t node0 = (tile0 + (uint64_t)t * p.splits) * kTcTile + hw * 32;
         uint32_t mask = 0;                                             // nodes that this lane's column sees
         if (B) {
-#pragma unroll 1
-            for (uint32_t k = 0; k < W; k += kAhead) {
-                uint32_t b[kAhead], sees = 0;
-#pragma unroll
-                for (int e = 0; e < kAhead; ++e) {
-                    b[e] = ctl->byte_of[min(h[e], 255) + 1];
-                    sees |= h[e] >= 0 ? 1u << e : 0u;
-                }
-                if (used) mask |= sees << (first + k);
-                hops_in();
-                if (on) {
-                    uint8_t *to = bt + col * kTcPitch + first + k;
-                    if (W >= 4) {
-                        *reinterpret_cast<uint32_t *>(to) = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
-                        if (W >= 8) *reinterpret_cast<uint32_t *>(to + 4) = b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24;
-                    } else {
-                        to[0] = b[0];
-                        if (W == 2) to[1] = b[1];
-                    }
-                }
+            mask = hops_out(ha, bt + col * kTcPitch + first);
+            hops_in(ha, t + 1, 0);
+            if (W > 16) {
+                mask |= hops_out(hb, bt + col * kTcPitch + first + 16) << 16;
+                hops_in(hb, t + 1, 16);
             }
+            mask = used ? mask << first : 0;
         }
         const bool in = node0 + lane < p.n;
         bt[B * kTcPitch + lane] = in ? p.buckets + 1 : 0;

@@ -135,8 +135,7 @@ __device__ __forceinline__ void unit32(uint32_t at, const RowInfo *info, bool pl
     }
 }
 
-// 32 nodes (a warp's lanes) x head_dim of fp32 accumulators, rounded, through the warp's rows of a tile in shared
-// memory to global memory in 16-byte pieces.
+// One node's (lane's) head_dim of fp32 accumulators, rounded, to row `row` of a tile in shared memory.
 template <typename T, int DP>
 __device__ __forceinline__ void load_nodes(uint32_t tm_at, float f, uint32_t stage, int row)
 {
@@ -156,24 +155,6 @@ __device__ __forceinline__ void load_nodes(uint32_t tm_at, float f, uint32_t sta
         }
     }
 }
-template <typename T, int DP>
-__device__ __forceinline__ void store_nodes(uint32_t stage, void *out, int64_t s_row, uint64_t node0, int warp, const AttnParams &p)
-{
-    constexpr int C = DP / 8, RP = 32 / C;
-    const int lane = threadIdx.x & 31;
-    const uint32_t c = lane % C;
-#pragma unroll 4
-    for (int r = lane / C; r < 32; r += RP) {
-        const uint32_t row = warp * 32 + r;
-        if (node0 + row < p.n && c < p.d / 8) {
-            uint4 v;
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                         : "r"(stage + tc::chunk(row, c, kTcTile * 128)) : "memory");
-            __stcs(reinterpret_cast<uint4 *>(static_cast<T *>(out) + (int64_t)(node0 + row) * s_row + c * 8), v);
-        }
-    }
-}
-
 // S^T = K Q^T at `at`, dP^T = V dO^T 32 columns on.
 template <int DP, int PANEL>
 __device__ __forceinline__ void score_products(bool lead, uint32_t at, uint64_t k, uint64_t q, uint64_t v, uint64_t g, uint32_t id, uint32_t dn)
@@ -207,7 +188,7 @@ template <int DP, int RT, bool DKV> struct BwdSmem {
     static constexpr int kCtl = kInfo + RT * (int)sizeof(RowInfo);
     struct Ctl {
         uint64_t full[kSlots], empty[kSlots], hop_full[kBufs], hop_empty[kBufs], sp_full[2], ds_full[2], hist_done[2];
-        uint64_t tile_full, tile_empty, dq_full, drained;
+        uint64_t tile_full, tile_empty, staged, dq_full, drained;
         uint32_t tmem, gave_up, columns, all;
         uint32_t seen[kBufs][4];
         uint8_t byte_of[257 + 15];
@@ -241,7 +222,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
     // ---- set-up ----
     if (warp == 24) tc::alloc(&ctl->tmem, 512);
     if (tid == 0) {
-        for (int i = 0; i < S::kSlots; ++i) tc::bar_init(&ctl->full[i], 128), tc::bar_init(&ctl->empty[i], DKV ? 4 : 1);
+        for (int i = 0; i < S::kSlots; ++i) tc::bar_init(&ctl->full[i], 128), tc::bar_init(&ctl->empty[i], 1);
         for (int i = 0; i < S::kBufs; ++i) {
             tc::bar_init(&ctl->hop_full[i], 4);
             tc::bar_init(&ctl->hop_empty[i], rts * (p.buckets ? 8 : 4));
@@ -249,6 +230,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
         for (int i = 0; i < 2; ++i) tc::bar_init(&ctl->sp_full[i], 1), tc::bar_init(&ctl->ds_full[i], 128), tc::bar_init(&ctl->hist_done[i], 4);
         tc::bar_init(&ctl->tile_full, 1);
         tc::bar_init(&ctl->tile_empty, 128);
+        tc::bar_init(&ctl->staged, 128);
         tc::bar_init(&ctl->dq_full, 1);
         tc::bar_init(&ctl->drained, 1);
         ctl->gave_up = ctl->columns = ctl->all = 0;
@@ -332,15 +314,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
                 for (int x = 0; x < 2; ++x) load_nodes<T, DP>(tm + lanes + (x ? kDk : kDv), x ? p.scale : 1.0f, sm + (x ? ks : vs) * S::kSlot, l);
                 tc::fence_before();
                 tc::bar_arrive(&ctl->tile_empty);
-                __syncwarp();
-                const uint64_t node0 = tile_at(i) * kTcTile;
-#pragma unroll 1
-                for (int x = 0; x < 2; ++x)
-                    store_nodes<T, DP>(sm + (x ? ks : vs) * S::kSlot, static_cast<T *>(x ? p.dk : p.dv) + (int64_t)hk * (x ? p.dk_head : p.dv_head),
-                                       x ? p.dk_row : p.dv_row, node0, ew, p);
-                __syncwarp();
-                if (lane == 0) tc::bar_arrive(&ctl->empty[ks]), tc::bar_arrive(&ctl->empty[vs]);
+                tc::fence_async();
+                tc::bar_arrive(&ctl->staged);
+                if (l == 0) {
+                    ok = tc::bar_wait(&ctl->staged, i & 1, gave_up);
+                    if (!ok) break;
+                    const int32_t node0 = (int32_t)(tile_at(i) * kTcTile);
+                    for (int c = 0; c < (int)p.d; c += 64) {
+                        tc::store_box(&p.dk_map, sm + ks * S::kSlot + c / 64 * S::kPanel, c, hk, node0);
+                        tc::store_box(&p.dv_map, sm + vs * S::kSlot + c / 64 * S::kPanel, c, hk, node0);
+                    }
+                    tc::stores_commit();
+                    tc::stores_read();
+                    tc::bar_arrive(&ctl->empty[ks]);
+                    tc::bar_arrive(&ctl->empty[vs]);
+                }
             }
+        if (l == 0) tc::stores_done();
+        ok = __all_sync(~0u, ok);
         if (ok && units > 0) ok = __all_sync(~0u, tc::bar_wait(&ctl->dq_full, 0, gave_up));
         if (ok) {
             tc::fence_after();
@@ -413,48 +404,51 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
         const bool lead = tc::elect();
         const uint32_t dn = (p.d + 15) & ~15u;
         const uint32_t id_s = tc::idesc(kBf16, 32, false, false), id_n = tc::idesc(kBf16, dn, false, true), id_q = tc::idesc(kBf16, 32, true, true);
-        bool ok = true;
-        uint32_t si = 0, sr = 0;        // tile and row tile of the next scores
-        auto scores = [&](uint32_t u) {
-            const uint32_t w = u & 1, ks = slot_of<S::kSlots>(2 * si), vs = slot_of<S::kSlots>(2 * si + 1);
-            if (sr == 0) {
-                ok = tc::bar_wait(&ctl->full[ks], slot_use<S::kSlots>(2 * si) & 1, gave_up) &&
-                     tc::bar_wait(&ctl->full[vs], slot_use<S::kSlots>(2 * si + 1) & 1, gave_up);
-                if (!ok) return;
+        // Scores run up to two units ahead of the gradients' products; whichever has its operands goes first.
+        uint32_t next = 0, si = 0, sr = 0, done = 0, i = 0, r = 0;      // (tile, row tile) of the next scores, of the next gradients
+        tc::Patience wait(gave_up);
+        while (done < units) {
+            if (next < units && next < done + 2) {
+                const uint32_t w = next & 1, ks = slot_of<S::kSlots>(2 * si), vs = slot_of<S::kSlots>(2 * si + 1);
+                if (sr > 0 || __all_sync(~0u, tc::bar_peek(&ctl->full[ks], slot_use<S::kSlots>(2 * si) & 1) &&
+                                                  tc::bar_peek(&ctl->full[vs], slot_use<S::kSlots>(2 * si + 1) & 1))) {
+                    tc::fence_async();
+                    tc::fence_after();
+                    const uint32_t qa = sm + S::kRow + sr * 2 * S::kRowTile;
+                    const uint64_t q = tc::desc(qa, 4096), g = tc::desc(qa + S::kRowTile, 4096);
+                    const uint64_t k = tc::desc(sm + ks * S::kSlot, S::kPanel), v = tc::desc(sm + vs * S::kSlot, S::kPanel);
+                    score_products<DP, S::kPanel>(lead, tm + w * 64, k, q, v, g, id_s, dn);
+                    tc::commit(lead, &ctl->sp_full[w]);
+                    if (!DKV && sr + 1 == rts) tc::commit(lead, &ctl->empty[vs]);      // values are read by the scores alone
+                    if (++sr == rts) sr = 0, ++si;
+                    ++next;
+                    wait.restart();
+                    continue;
+                }
+            }
+            const uint32_t w = done & 1;
+            if (done < next && __all_sync(~0u, tc::bar_peek(&ctl->ds_full[w], (done >> 1) & 1) &&
+                                                   (!DKV || r > 0 || i == 0 || tc::bar_peek(&ctl->tile_empty, (i - 1) & 1)))) {
                 tc::fence_async();
-            }
-            tc::fence_after();
-            const uint32_t qa = sm + S::kRow + sr * 2 * S::kRowTile;
-            const uint64_t q = tc::desc(qa, 4096), g = tc::desc(qa + S::kRowTile, 4096);
-            const uint64_t k = tc::desc(sm + ks * S::kSlot, S::kPanel), v = tc::desc(sm + vs * S::kSlot, S::kPanel);
-            score_products<DP, S::kPanel>(lead, tm + w * 64, k, q, v, g, id_s, dn);
-            tc::commit(lead, &ctl->sp_full[w]);
-            if (!DKV && sr + 1 == rts) tc::commit(lead, &ctl->empty[vs]);      // values are read by the scores alone
-            if (++sr == rts) sr = 0, ++si;
-        };
-        if (units > 0) scores(0);
-        if (ok && units > 1) scores(1);
-        uint32_t i = 0, r = 0;
-        for (uint32_t u = 0; u < units && ok; ++u) {
-            const uint32_t w = u & 1, ks = slot_of<S::kSlots>(2 * i);
-            ok = tc::bar_wait(&ctl->ds_full[w], (u >> 1) & 1, gave_up);
-            if (ok && DKV && r == 0 && i > 0) ok = tc::bar_wait(&ctl->tile_empty, (i - 1) & 1, gave_up);
-            if (!ok) break;
-            tc::fence_after();
-            const uint32_t qa = sm + S::kRow + r * 2 * S::kRowTile;
-            if (DKV) node_products(lead, tm + w * 64, tm + kDv, tm + kDk, tc::desc(qa, 4096), tc::desc(qa + S::kRowTile, 4096), id_n, r > 0);
-            const uint64_t k = tc::desc(sm + ks * S::kSlot, S::kPanel), ds = tc::desc(sm + S::kDs + w * 64, 4096);
+                tc::fence_after();
+                const uint32_t ks = slot_of<S::kSlots>(2 * i), qa = sm + S::kRow + r * 2 * S::kRowTile;
+                if (DKV) node_products(lead, tm + w * 64, tm + kDv, tm + kDk, tc::desc(qa, 4096), tc::desc(qa + S::kRowTile, 4096), id_n, r > 0);
+                const uint64_t k = tc::desc(sm + ks * S::kSlot, S::kPanel), ds = tc::desc(sm + S::kDs + w * 64, 4096);
 #pragma unroll
-            for (uint32_t kk = 0; kk < kTcTile / 16; ++kk)
-                tc::mma_ss(lead, tm + kDq + r * 32, k, kk * 2048, ds, kk * 2048, id_q, i > 0 || kk > 0);
-            if (r + 1 == rts) {
-                if (DKV) tc::commit(lead, &ctl->tile_full);
-                else tc::commit(lead, &ctl->empty[ks]);
+                for (uint32_t kk = 0; kk < kTcTile / 16; ++kk)
+                    tc::mma_ss(lead, tm + kDq + r * 32, k, kk * 2048, ds, kk * 2048, id_q, i > 0 || kk > 0);
+                if (r + 1 == rts) {
+                    if (DKV) tc::commit(lead, &ctl->tile_full);
+                    else tc::commit(lead, &ctl->empty[ks]);
+                }
+                if (++done == units) tc::commit(lead, &ctl->dq_full);
+                if (++r == rts) r = 0, ++i;
+                wait.restart();
+                continue;
             }
-            if (u + 1 == units) tc::commit(lead, &ctl->dq_full);
-            if (++r == rts) r = 0, ++i;
-            if (u + 2 < units) scores(u + 2);
+            if (!__all_sync(~0u, wait.more())) break;
         }
+        const bool ok = done == units;
         if (!ok) tc::drain(lead, &ctl->drained, 0);
     }
     __syncwarp();
@@ -551,13 +545,18 @@ __global__ void __launch_bounds__(kBwdRowThreads, 1) attn_bwd_rows_kernel(const 
         }
         // results: group 0 dv, group 1 dk, through the slots of values and keys
         if (ok) ok = __all_sync(~0u, tc::bar_wait(&ctl->tile_full, 0, gave_up));
+        const uint32_t stage = sm + (w ? 0 : S::kSlot);
         if (ok) {
             tc::fence_after();
-            const uint32_t stage = sm + (w ? 0 : S::kSlot);
             load_nodes<T, DP>(tm + lanes + (w ? kDk : kDv), w ? p.scale : 1.0f, stage, l);
-            __syncwarp();
-            store_nodes<T, DP>(stage, static_cast<T *>(w ? p.dk : p.dv) + (int64_t)hk * (w ? p.dk_head : p.dv_head),
-                               w ? p.dk_row : p.dv_row, tile * kTcTile, warp & 3, p);
+            tc::fence_async();
+        }
+        asm volatile("bar.sync %0, 128;" ::"r"(w + 1) : "memory");
+        if (l == 0 && ok) {
+            for (int c = 0; c < (int)p.d; c += 64)
+                tc::store_box(w ? &p.dk_map : &p.dv_map, stage + c / 64 * S::kPanel, c, hk, (int32_t)(tile * kTcTile));
+            tc::stores_commit();
+            tc::stores_done();
         }
     } else if (warp < 12) {
         hop_warps<1>(p, ctl, smem + S::kBuckets, warp - 8, lane, 1, tile, gave_up);

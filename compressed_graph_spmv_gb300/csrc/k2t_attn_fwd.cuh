@@ -203,40 +203,46 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
             const uint32_t id_s = tc::idesc(kBf16, kTcTile, false, false);
             const uint32_t dn = (p.d + 15) & ~15u, id_o = tc::idesc(kBf16, dn, false, true);
             const uint32_t base = sm;
-            bool ok = true;
-            auto scores = [&](uint32_t u) {
-                const uint32_t w = u & 1, i = TWO ? u >> 1 : u, item = 2 * i, slot = item % S::kSlots;
-                ok = tc::bar_wait(&ctl->full[slot], (item / S::kSlots) & 1, gave_up);
-                if (!ok) return;
-                tc::fence_async();       // the copies were made by threads, the product reads through the async proxy
-                tc::fence_after();
-                const uint64_t q = tc::desc(base + S::kQ + (TWO ? w * S::kSlot : 0), S::kPanel), k = tc::desc(base + slot * S::kSlot, S::kPanel);
+            // Scores run up to two units ahead of the outputs; whichever has its operands goes first.
+            uint32_t next = 0, done = 0;
+            tc::Patience wait(gave_up);
+            while (done < units) {
+                if (next < units && next < done + 2) {
+                    const uint32_t w = next & 1, item = 2 * (TWO ? next >> 1 : next), slot = item % S::kSlots;
+                    if (__all_sync(~0u, tc::bar_peek(&ctl->full[slot], (item / S::kSlots) & 1))) {
+                        tc::fence_async();       // the copies were made by threads, the product reads through the async proxy
+                        tc::fence_after();
+                        const uint64_t q = tc::desc(base + S::kQ + (TWO ? w * S::kSlot : 0), S::kPanel), k = tc::desc(base + slot * S::kSlot, S::kPanel);
 #pragma unroll
-                for (uint32_t kk = 0; kk < DP / 16; ++kk)
-                    if (kk * 16 < dn) {
-                        const uint32_t off = (kk >> 2) * S::kPanel + (kk & 3) * 32;
-                        tc::mma_ss(lead, tm + w * 128, q, off, k, off, id_s, kk > 0);
+                        for (uint32_t kk = 0; kk < DP / 16; ++kk)
+                            if (kk * 16 < dn) {
+                                const uint32_t off = (kk >> 2) * S::kPanel + (kk & 3) * 32;
+                                tc::mma_ss(lead, tm + w * 128, q, off, k, off, id_s, kk > 0);
+                            }
+                        tc::commit(lead, &ctl->s_full[w]);
+                        if (!TWO || w == 1) tc::commit(lead, &ctl->empty[slot]);
+                        ++next;
+                        wait.restart();
+                        continue;
                     }
-                tc::commit(lead, &ctl->s_full[w]);
-                if (!TWO || w == 1) tc::commit(lead, &ctl->empty[slot]);
-            };
-            if (units > 0) scores(0);
-            if (ok && units > 1) scores(1);
-            for (uint32_t u = 0; u < units && ok; ++u) {
-                const uint32_t w = u & 1, i = TWO ? u >> 1 : u, item = 2 * i + 1, slot = item % S::kSlots;
-                ok = tc::bar_wait(&ctl->full[slot], (item / S::kSlots) & 1, gave_up) &&
-                     tc::bar_wait(&ctl->p_full[w], (u >> 1) & 1, gave_up);
-                if (!ok) break;
-                tc::fence_async();
-                tc::fence_after();
-                const uint64_t v = tc::desc(base + slot * S::kSlot, S::kPanel);
+                }
+                const uint32_t w = done & 1, item = 2 * (TWO ? done >> 1 : done) + 1, slot = item % S::kSlots;
+                if (done < next && __all_sync(~0u, tc::bar_peek(&ctl->full[slot], (item / S::kSlots) & 1) && tc::bar_peek(&ctl->p_full[w], (done >> 1) & 1))) {
+                    tc::fence_async();
+                    tc::fence_after();
+                    const uint64_t v = tc::desc(base + slot * S::kSlot, S::kPanel);
 #pragma unroll
-                for (uint32_t kk = 0; kk < kTcTile / 16; ++kk)
-                    tc::mma_ts(lead, tm + 256 + w * DP, tm + w * 128 + kk * 8, v, kk * 2048, id_o, u > 1 || kk > 0);
-                if (!TWO || w == 1) tc::commit(lead, &ctl->empty[slot]);
-                if (u + 2 >= units) tc::commit(lead, &ctl->o_full[w]);
-                if (u + 2 < units) scores(u + 2);
+                    for (uint32_t kk = 0; kk < kTcTile / 16; ++kk)
+                        tc::mma_ts(lead, tm + 256 + w * DP, tm + w * 128 + kk * 8, v, kk * 2048, id_o, done > 1 || kk > 0);
+                    if (!TWO || w == 1) tc::commit(lead, &ctl->empty[slot]);
+                    if (done + 2 >= units) tc::commit(lead, &ctl->o_full[w]);
+                    ++done;
+                    wait.restart();
+                    continue;
+                }
+                if (!__all_sync(~0u, wait.more())) break;
             }
+            const bool ok = done == units;
             if (!ok) tc::drain(lead, &ctl->drained, 0);
         }
         __syncwarp();

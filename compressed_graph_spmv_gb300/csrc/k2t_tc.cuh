@@ -47,6 +47,22 @@ __device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, volatile 
     }
     return true;
 }
+// The same bound for a warp that polls several barriers.
+struct Patience {
+    volatile uint32_t *gave_up;
+    long long start;
+    __device__ explicit Patience(volatile uint32_t *g)
+    {
+        gave_up = g;
+        start = clock64();
+    }
+    __device__ void restart() { start = clock64(); }
+    __device__ bool more()
+    {
+        if (clock64() - start > (1ll << 31)) *gave_up = 1;
+        return !*gave_up;
+    }
+};
 // Counts on the barrier once this thread's earlier cp.async copies have landed (part of the barrier's count).
 __device__ __forceinline__ void cp_arrive(uint64_t *b)
 {
@@ -182,8 +198,15 @@ __device__ __forceinline__ void commit(bool lead, uint64_t *b)
     if (lead) asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(b)) : "memory");
 }
 
-template <int N> __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void regs_fewer() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// A box of a tensor from shared memory (128-byte swizzle): what lies past the tensor's sides is left out.
+__device__ __forceinline__ void store_box(const void *map, uint32_t from, int32_t x, int32_t y, int32_t z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map), "r"(from), "r"(x),
+                 "r"(y), "r"(z) : "memory");
+}
+__device__ __forceinline__ void stores_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }   // sources free
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 }  // namespace tc
 }  // namespace k2t

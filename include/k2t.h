@@ -370,6 +370,7 @@ K2T_API uint64_t k2t_msbfs_work_bytes(const k2t_tree *t);
 #define K2T_ATTN_MAX_GROUP    16   /* query heads per key/value head            */
 #define K2T_ATTN_MAX_BUCKETS  64
 #define K2T_ATTN_MAX_HOP      255  /* largest first hop of a bucket              */
+#define K2T_ATTN_MAX_NODES    0x7fffff00u
 
 /* Attention of n_queries queries to the states of n_nodes nodes, biased and
  * masked by hop distance.  For query t, head h (key/value head h / G,
@@ -385,7 +386,8 @@ K2T_API uint64_t k2t_msbfs_work_bytes(const k2t_tree *t);
  * The states of a node that no query of the call sees (hops < 0 for every
  * column in use) are not used: they may hold anything, NaN included.
  * Strides are in elements; rows must be 16-byte aligned: base pointers
- * multiples of 16 bytes, strides and head_dim multiples of 8.              */
+ * multiples of 16 bytes, strides and head_dim multiples of 8; strides are not
+ * negative and below 2^38.                                                  */
 typedef struct {
     uint32_t dtype;            /* K2T_BF16 or K2T_FP16: q, k, v, out, bias and all gradients        */
     uint32_t n_queries;        /* T, 0 or more                                                       */
@@ -395,7 +397,7 @@ typedef struct {
     uint32_t n_sources;        /* columns of hops, 1..32; 0: no table (no mask, no bias)            */
     uint32_t n_buckets;        /* 1..64 with a bias table, else 0                                   */
     float scale;
-    uint64_t n_nodes;          /* 0 or more, at most 2^32                                           */
+    uint64_t n_nodes;          /* 0 or more, at most K2T_ATTN_MAX_NODES                             */
     uint8_t edges[K2T_ATTN_MAX_BUCKETS]; /* first hop of each bucket, increasing, edges[0] = 0      */
     /* inputs */
     const void *q, *k, *v;     /* [T, n_heads, head_dim], [n_nodes, n_kv_heads, head_dim] twice     */

@@ -33,11 +33,11 @@ def attn(**kw):
     (dict(dtype=K.FP32), EINVAL), (dict(dtype=7), EINVAL), (dict(n_heads=0), EINVAL), (dict(n_kv_heads=0), EINVAL),
     (dict(n_heads=5), EINVAL), (dict(head_dim=0), EINVAL), (dict(head_dim=60), EINVAL), (dict(head_dim=136), ERANGE),
     (dict(n_heads=34), ERANGE), (dict(n_sources=33), ERANGE), (dict(n_buckets=65), ERANGE),
-    (dict(n_nodes=(1 << 32) + 1), ERANGE), (dict(n_queries=1 << 31), ERANGE), (dict(n_sources=0, hops=None), EINVAL),
+    (dict(n_nodes=(1 << 31)), ERANGE), (dict(n_queries=1 << 31), ERANGE), (dict(n_sources=0, hops=None), EINVAL),
     (dict(edges=(1, 2, 3)), EINVAL), (dict(edges=(0, 2, 2)), EINVAL), (dict(scale=float("nan")), EINVAL),
     (dict(q=None), EINVAL), (dict(k=None), EINVAL), (dict(v=None), EINVAL), (dict(out=None), EINVAL),
     (dict(lse=None), EINVAL), (dict(hops=None), EINVAL), (dict(bias=None), EINVAL), (dict(n_buckets=0), EINVAL),
-    (dict(q=P + 8), EINVAL), (dict(k_row=132), EINVAL), (dict(v_head=60), EINVAL), (dict(out_row=250), EINVAL),
+    (dict(q=P + 8), EINVAL), (dict(k_row=132), EINVAL), (dict(v_head=60), EINVAL), (dict(out_row=250), EINVAL), (dict(k_row=-128), EINVAL),
     (dict(n_queries=5), ERANGE),
 ])
 def test_attention_refuses(kw, status):
