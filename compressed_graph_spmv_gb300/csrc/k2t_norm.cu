@@ -64,6 +64,107 @@ template <typename T, int VEC> __device__ __forceinline__ void store(T *p, const
     }
 }
 
+// Value e of an array of pairs (e is known when compiling), and operations on pairs.
+template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> zero_pack()
+{
+    Pack<T, VEC> r;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) r.v[e] = from_f<T>(0.0f);
+    return r;
+}
+template <typename T, int VEC> __device__ __forceinline__ float2 pair_of(const Pack<T, VEC> *p, int e)
+{
+    return make_float2(to_f(p[2 * e / VEC].v[2 * e % VEC]), to_f(p[(2 * e + 1) / VEC].v[(2 * e + 1) % VEC]));
+}
+__device__ __forceinline__ float &half_of(float2 *v, int e) { return e & 1 ? v[e >> 1].y : v[e >> 1].x; }
+__device__ __forceinline__ unsigned long long bits(const float2 &v) { return *reinterpret_cast<const unsigned long long *>(&v); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(*reinterpret_cast<unsigned long long *>(&d)) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(*reinterpret_cast<unsigned long long *>(&d)) : "l"(bits(a)), "l"(bits(b)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(*reinterpret_cast<unsigned long long *>(&d)) : "l"(bits(a)), "l"(bits(b)));
+    return d;
+}
+
+// The loads of a row, either when the row's turn comes (AHEAD 0) or AHEAD rows earlier into shared memory, each thread
+// its own pieces: nothing waits on another thread, and the loads in flight (AHEAD rows of every thread) are not bounded
+// by registers.  Rows of one thread are `step` apart.
+template <typename T, int VEC, int TPR, int PER, int TENSORS, int AHEAD> struct RowStream {
+    static constexpr int kBytes = AHEAD * TENSORS * PER * 16;            // shared memory a thread
+    uint32_t base;                                                       // this thread's first piece
+    uint32_t dim;
+    uint64_t n, step, next;                                              // next row to ask for
+    const T *src[TENSORS];
+    int tid, slot_in, slot_out;
+
+    __device__ __forceinline__ RowStream(uint8_t *smem, uint64_t first, uint64_t n_, uint64_t step_, uint32_t dim_, int tid_)
+    {
+        base = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
+        dim = dim_, n = n_, step = step_, next = first, tid = tid_;
+        slot_in = slot_out = 0;
+    }
+    __device__ __forceinline__ uint32_t at(int slot, int t, int i) const { return base + ((slot * TENSORS + t) * PER + i) * (blockDim.x * 16); }
+    __device__ __forceinline__ void ask()
+    {
+        if (next < n) {
+#pragma unroll
+            for (int t = 0; t < TENSORS; ++t)
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const uint32_t c = (tid + i * TPR) * VEC;
+                    if (c < dim && src[t])
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(slot_in, t, i)), "l"(src[t] + next * dim + c) : "memory");
+                }
+            next += step;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (++slot_in == AHEAD) slot_in = 0;
+    }
+    __device__ __forceinline__ void start()
+    {
+        if constexpr (AHEAD > 0) {
+#pragma unroll
+            for (int a = 0; a < AHEAD; ++a) ask();
+        }
+    }
+    __device__ __forceinline__ void ready()
+    {
+        if constexpr (AHEAD > 0) asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD > 0 ? AHEAD - 1 : 0) : "memory");
+    }
+    __device__ __forceinline__ Pack<T, VEC> get(uint64_t row, int t, int i) const
+    {
+        const uint32_t c = (tid + i * TPR) * VEC;
+        if constexpr (AHEAD > 0) {
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at(slot_out, t, i)) : "memory");
+            Pack<T, VEC> r;
+            static_assert(sizeof(r) == 16, "whole pieces");
+            *reinterpret_cast<uint4 *>(&r) = v;
+            return r;
+        } else {
+            return load_once<T, VEC>(src[t] + row * dim + c);
+        }
+    }
+    __device__ __forceinline__ void taken()                              // the row's pieces are in registers
+    {
+        if constexpr (AHEAD > 0) {
+            if (++slot_out == AHEAD) slot_out = 0;
+            ask();
+        }
+    }
+};
+
 // Threads of a block: groups of TPR, each with a row of its own.
 template <int TPR> struct Group {
     static constexpr int kThreads = TPR < 256 ? 256 : TPR;
@@ -94,7 +195,7 @@ __device__ __forceinline__ void group_sum(float &a, float &b, float2 *buf, int g
     }
 }
 
-template <typename T, int VEC, int TPR, int PER>
+template <typename T, int VEC, int TPR, int PER, int AHEAD>
 __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __grid_constant__ NormParams p)
 {
     using P = Pack<T, VEC>;
@@ -114,19 +215,22 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
             }
         }
     }
-    for (uint64_t row = (uint64_t)blockIdx.x * Gr::kGroups + group; row < p.n; row += (uint64_t)gridDim.x * Gr::kGroups) {
+    extern __shared__ __align__(16) uint8_t ring[];
+    const uint64_t first = (uint64_t)blockIdx.x * Gr::kGroups + group, step = (uint64_t)gridDim.x * Gr::kGroups;
+    RowStream<T, VEC, TPR, PER, 2, AHEAD> in(ring, first, p.n, step, p.dim, tid);
+    in.src[0] = static_cast<const T *>(p.x);
+    in.src[1] = static_cast<const T *>(p.residual);
+    in.start();
+    for (uint64_t row = first; row < p.n; row += step) {
         const uint64_t at = row * p.dim;
         P z[PER], r[PER];
+        in.ready();
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const uint32_t c = (tid + i * TPR) * VEC;
-            if (c < p.dim) z[i] = load_once<T, VEC>(static_cast<const T *>(p.x) + at + c);
-        }
-        if (p.residual) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const uint32_t c = (tid + i * TPR) * VEC;
-                if (c < p.dim) r[i] = load_once<T, VEC>(static_cast<const T *>(p.residual) + at + c);
+            if (c < p.dim) {
+                z[i] = in.get(row, 0, i);
+                if (p.residual) r[i] = in.get(row, 1, i);
             }
         }
         float s = 0.0f, none = 0.0f;
@@ -144,6 +248,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
                 for (int e = 0; e < VEC; ++e) s += to_f(z[i].v[e]);
             }
         }
+        in.taken();
         group_sum<TPR>(s, none, buf, group, turn);
         const float mean = s * p.inv_dim;
         float q = 0.0f;
@@ -178,74 +283,80 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
 
 // dx = rstd (w dy - c1 - xh c2) + dz with c1 = mean(w dy), c2 = mean(w dy xh);
 // part[block][0 | 1][dim]: the block's sums of dy xh and dy.
-template <typename T, int VEC, int TPR, int PER>
-__global__ void __launch_bounds__(Group<TPR>::kThreads) norm_bwd_kernel(const __grid_constant__ NormParams p)
+template <typename T, int VEC, int TPR, int PER, int AHEAD>
+__global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 || PER > 1 ? 1 : 3) norm_bwd_kernel(const __grid_constant__ NormParams p)
 {
     using P = Pack<T, VEC>;
     using Gr = Group<TPR>;
     __shared__ float2 buf[2 * Gr::kGroups * Gr::kWarps];
     const int tid = threadIdx.x % TPR, group = threadIdx.x / TPR;
     int turn = 0;
-    P w[PER];
-    float dw[PER][VEC], db[PER][VEC];
+    // a thread's values go in pairs, one instruction for two; those past the row count as 0
+    constexpr int N2 = PER * VEC / 2;
+    static_assert(PER * VEC % 2 == 0, "pairs");
+    float2 w[N2], dw[N2], db[N2];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const uint32_t c = (tid + i * TPR) * VEC;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            dw[i][e] = db[i][e] = 0.0f;
-            if (c < p.dim) w[i].v[e] = static_cast<const T *>(p.weight)[c + e];
-        }
+    for (int e = 0; e < PER * VEC; ++e) {
+        const uint32_t c = (tid + e / VEC * TPR) * VEC;
+        half_of(w, e) = c < p.dim ? to_f(static_cast<const T *>(p.weight)[c + e % VEC]) : 0.0f;
+        half_of(dw, e) = half_of(db, e) = 0.0f;
     }
-    for (uint64_t row = (uint64_t)blockIdx.x * Gr::kGroups + group; row < p.n; row += (uint64_t)gridDim.x * Gr::kGroups) {
+    extern __shared__ __align__(16) uint8_t ring[];
+    const uint64_t first = (uint64_t)blockIdx.x * Gr::kGroups + group, step = (uint64_t)gridDim.x * Gr::kGroups;
+    RowStream<T, VEC, TPR, PER, 3, AHEAD> in(ring, first, p.n, step, p.dim, tid);
+    in.src[0] = static_cast<const T *>(p.z_in);
+    in.src[1] = static_cast<const T *>(p.dy);
+    in.src[2] = static_cast<const T *>(p.dz);
+    in.start();
+    for (uint64_t row = first; row < p.n; row += step) {
         const uint64_t at = row * p.dim;
-        P z[PER], g[PER], extra[PER];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const uint32_t c = (tid + i * TPR) * VEC;
-            if (c < p.dim) {
-                z[i] = load_once<T, VEC>(static_cast<const T *>(p.z_in) + at + c);
-                g[i] = load_once<T, VEC>(static_cast<const T *>(p.dy) + at + c);
-                if (p.dz) extra[i] = load_once<T, VEC>(static_cast<const T *>(p.dz) + at + c);
-            }
-        }
         const float mean = p.mean[row], rstd = p.rstd[row];
-        float c1 = 0.0f, c2 = 0.0f;
+        const float2 nm = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
+        P z[PER], g[PER], x[PER];
+        in.ready();
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const uint32_t c = (tid + i * TPR) * VEC;
-            if (c < p.dim) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float xh = (to_f(z[i].v[e]) - mean) * rstd, dy = to_f(g[i].v[e]), a = dy * to_f(w[i].v[e]);
-                    c1 += a;
-                    c2 = fmaf(a, xh, c2);
-                    dw[i][e] = fmaf(dy, xh, dw[i][e]);
-                    db[i][e] += dy;
-                }
+            if ((tid + i * TPR) * VEC < p.dim) {
+                z[i] = in.get(row, 0, i), g[i] = in.get(row, 1, i);
+                if (p.dz) x[i] = in.get(row, 2, i);
+            } else {
+                z[i] = g[i] = x[i] = zero_pack<T, VEC>();
             }
         }
+        float2 xh[N2], a[N2], s1 = make_float2(0.0f, 0.0f), s2 = s1;
+#pragma unroll
+        for (int e = 0; e < N2; ++e) {
+            const float2 dy = pair_of<T, VEC>(g, e);
+            xh[e] = mul2(add2(pair_of<T, VEC>(z, e), nm), r2);
+            a[e] = mul2(dy, w[e]);
+            s1 = add2(s1, a[e]);
+            s2 = fma2(a[e], xh[e], s2);
+            dw[e] = fma2(dy, xh[e], dw[e]);
+            db[e] = add2(db[e], dy);
+        }
+        in.taken();
+        float c1 = s1.x + s1.y, c2 = s2.x + s2.y;
         group_sum<TPR>(c1, c2, buf, group, turn);
-        c1 *= p.inv_dim;
-        c2 *= p.inv_dim;
+        const float2 n1 = make_float2(-c1 * p.inv_dim, -c1 * p.inv_dim), n2 = make_float2(-c2 * p.inv_dim, -c2 * p.inv_dim);
+#pragma unroll
+        for (int e = 0; e < N2; ++e) {
+            a[e] = fma2(xh[e], n2, add2(a[e], n1));
+            a[e] = p.dz ? fma2(a[e], r2, pair_of<T, VEC>(x, e)) : mul2(a[e], r2);
+        }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const uint32_t c = (tid + i * TPR) * VEC;
             if (c < p.dim) {
                 P o;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float xh = (to_f(z[i].v[e]) - mean) * rstd, a = to_f(g[i].v[e]) * to_f(w[i].v[e]);
-                    float dx = (a - c1 - xh * c2) * rstd;
-                    if (p.dz) dx += to_f(extra[i].v[e]);
-                    o.v[e] = from_f<T>(dx);
-                }
+                for (int e = 0; e < VEC; ++e) o.v[e] = from_f<T>(half_of(a, i * VEC + e));
                 store<T, VEC>(static_cast<T *>(p.dx) + at + c, o);
             }
         }
     }
     // the groups of a block add up one after another through shared memory
-    extern __shared__ float sums[];    // [2][dim], with more than one group
+    float *sums = reinterpret_cast<float *>(ring);    // [2][dim], with more than one group
+    if (AHEAD > 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
     float *out = p.part + (uint64_t)blockIdx.x * 2 * p.dim;
     for (int turn_of = 0; turn_of < Gr::kGroups; ++turn_of) {
         if (Gr::kGroups > 1) __syncthreads();
@@ -256,7 +367,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_bwd_kernel(const __
             if (c < p.dim) {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    float a = dw[i][e], b = db[i][e];
+                    float a = half_of(dw, i * VEC + e), b = half_of(db, i * VEC + e);
                     if (turn_of > 0) a += sums[c + e], b += sums[p.dim + c + e];
                     if (turn_of + 1 < Gr::kGroups) sums[c + e] = a, sums[p.dim + c + e] = b;
                     else out[c + e] = a, out[p.dim + c + e] = b;
@@ -266,24 +377,31 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_bwd_kernel(const __
     }
 }
 
-// dweight, dbias: 32 columns a block, 32 threads a column over the partial rows.
+// dweight, dbias: 8 columns (one 32-byte sector) a block, 128 threads a column over the partial rows, so that few loads
+// follow one another.
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__ NormParams p)
 {
-    __shared__ float red[32][33];
-    const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-    const uint32_t which = blockIdx.y, c = blockIdx.x * 32 + lane;
+    __shared__ float red[32][9];
+    const int col = threadIdx.x & 7, g = threadIdx.x >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t which = blockIdx.y, c = blockIdx.x * 8 + col;
     float s = 0.0f;
-    if (c < p.dim)
-        for (uint32_t i = g; i < p.parts; i += 32) s += p.part[((uint64_t)i * 2 + which) * p.dim + c];
-    red[g][lane] = s;
+    if (c < p.dim) {
+#pragma unroll 4
+        for (uint32_t i = g; i < p.parts; i += 128) s += p.part[((uint64_t)i * 2 + which) * p.dim + c];
+    }
+    s += __shfl_xor_sync(~0u, s, 8);
+    s += __shfl_xor_sync(~0u, s, 16);
+    if (lane < 8) red[warp][lane] = s;
     __syncthreads();
-    s = red[lane][g];
+    if (warp < 8) {
+        s = red[lane][warp];
 #pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
-    const uint32_t col = blockIdx.x * 32 + g;
-    T *out = static_cast<T *>(which ? p.dbias : p.dweight);
-    if (lane == 0 && col < p.dim && out) out[col] = from_f<T>(s);
+        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
+        const uint32_t at = blockIdx.x * 8 + warp;
+        T *out = static_cast<T *>(which ? p.dbias : p.dweight);
+        if (lane == 0 && at < p.dim && out) out[at] = from_f<T>(s);
+    }
 }
 
 #define K2T_NORM_CUDA(call)                              \
@@ -302,24 +420,60 @@ uint32_t norm_parts(uint64_t n, int groups)
     return (uint32_t)std::min<uint64_t>((n + groups - 1) / groups, kNormBlocks);
 }
 
-template <typename T, int VEC, int TPR, int PER> int run_norm(NormParams &p, bool backward, cudaStream_t st)
+// Backward blocks: as many as the GPU runs at once, and no more than `blocks`; each writes a partial row of the
+// weight's gradient, so that more of them cost more than they even out (445 us against 458 us with twice as many).
+template <typename K> uint32_t norm_resident(K kernel, uint32_t blocks, int threads, size_t smem)
 {
-    using Gr = Group<TPR>;
-    const uint32_t blocks = norm_parts(p.n, Gr::kGroups);
-    if (!backward) {
-        if (!blocks) return K2T_OK;
-        norm_fwd_kernel<T, VEC, TPR, PER><<<blocks, Gr::kThreads, 0, st>>>(p);
-        K2T_NORM_CUDA(cudaGetLastError());
-        return K2T_OK;
-    }
-    p.parts = blocks;
-    if (blocks) {
-        norm_bwd_kernel<T, VEC, TPR, PER><<<blocks, Gr::kThreads, Gr::kGroups > 1 ? 2 * p.dim * sizeof(float) : 0, st>>>(p);
-        K2T_NORM_CUDA(cudaGetLastError());
-    }
-    norm_join_kernel<T><<<dim3((p.dim + 31) / 32, p.dbias ? 2 : 1), 1024, 0, st>>>(p);
+    int per_sm = 0;
+    if (smem > 32 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1) per_sm = 1;
+    return std::min<uint32_t>(blocks, 152u * per_sm);
+}
+
+template <typename K> int norm_launch(K kernel, uint32_t blocks, int threads, size_t smem, const NormParams &p, cudaStream_t st)
+{
+    kernel<<<blocks, threads, smem, st>>>(p);
     K2T_NORM_CUDA(cudaGetLastError());
     return K2T_OK;
+}
+
+// AHEAD: rows asked for ahead where blocks stay for several (0: a row's loads wait for its turn, less to set up).
+template <typename T, int VEC, int TPR, int PER, int AHEAD> int run_norm(NormParams &p, uint32_t blocks, bool backward, cudaStream_t st)
+{
+    using Gr = Group<TPR>;
+    if (!backward) {
+        if (!blocks) return K2T_OK;
+        const auto kernel = norm_fwd_kernel<T, VEC, TPR, PER, AHEAD>;
+        const size_t ring = (size_t)Gr::kThreads * RowStream<T, VEC, TPR, PER, 2, AHEAD>::kBytes;
+        if (ring > 32 * 1024) K2T_NORM_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring));
+        // short blocks even out the SMs: 16 rounds of them 322 us, 2 rounds 357 us on 2^18 x 1024 bf16
+        if (AHEAD > 0) blocks = (uint32_t)std::min<uint64_t>((p.n + Gr::kGroups * 4 - 1) / (Gr::kGroups * 4), kNormBlocks * 4);
+        return norm_launch(kernel, blocks, Gr::kThreads, ring, p, st);
+    }
+    if (blocks) {
+        const size_t ring = (size_t)Gr::kThreads * RowStream<T, VEC, TPR, PER, 3, AHEAD>::kBytes;
+        const size_t sums = Gr::kGroups > 1 ? 2 * p.dim * sizeof(float) : 0;
+        const auto kernel = norm_bwd_kernel<T, VEC, TPR, PER, AHEAD>;
+        if (AHEAD > 0) blocks = norm_resident(kernel, blocks, Gr::kThreads, std::max(ring, sums));
+        int rc = norm_launch(kernel, blocks, Gr::kThreads, std::max(ring, sums), p, st);
+        if (rc) return rc;
+    }
+    p.parts = blocks;
+    norm_join_kernel<T><<<dim3((p.dim + 7) / 8, p.dbias ? 2 : 1), 1024, 0, st>>>(p);
+    K2T_NORM_CUDA(cudaGetLastError());
+    return K2T_OK;
+}
+
+// Blocks: every SM full of them at most (kNormBlocks).  With more than four rows a group the loads run ahead: measured
+// on 2^20 x 512 and 2^18 x 1024 bf16 against a row's own loads; below that there is little to run ahead of.
+template <typename T, int VEC, int TPR, int PER, int AHEAD> int plan_norm(NormParams &p, bool backward, cudaStream_t st)
+{
+    constexpr int G = Group<TPR>::kGroups;
+    const uint32_t blocks = norm_parts(p.n, G);
+    if constexpr (AHEAD > 0) {
+        if (p.n > (uint64_t)4 * G * kNormBlocks) return run_norm<T, VEC, TPR, PER, AHEAD>(p, norm_parts(p.n, G), backward, st);
+    }
+    return run_norm<T, VEC, TPR, PER, 0>(p, blocks, backward, st);
 }
 
 // Threads a row: as few as hold it with one load each, up to a block, then
@@ -330,18 +484,18 @@ template <typename T> int norm_dispatch(NormParams &p, bool vec, bool backward, 
     if (vec) {
         constexpr int V = 16 / sizeof(T);
         const uint32_t c = p.dim / V;
-        if (c <= 32) return run_norm<T, V, 32, 1>(p, backward, st);
-        if (c <= 64) return run_norm<T, V, 64, 1>(p, backward, st);
-        if (c <= 128) return run_norm<T, V, 128, 1>(p, backward, st);
-        if (c <= 256) return run_norm<T, V, 256, 1>(p, backward, st);
-        if (c <= 512) return run_norm<T, V, 256, 2>(p, backward, st);
-        if (c <= 1024) return run_norm<T, V, 512, 2>(p, backward, st);
-        return run_norm<T, V, 512, 8>(p, backward, st);
+        if (c <= 32) return plan_norm<T, V, 32, 1, 4>(p, backward, st);
+        if (c <= 64) return plan_norm<T, V, 64, 1, 4>(p, backward, st);
+        if (c <= 128) return plan_norm<T, V, 128, 1, 4>(p, backward, st);
+        if (c <= 256) return plan_norm<T, V, 256, 1, 4>(p, backward, st);
+        if (c <= 512) return plan_norm<T, V, 256, 2, 2>(p, backward, st);
+        if (c <= 1024) return plan_norm<T, V, 512, 2, 2>(p, backward, st);
+        return plan_norm<T, V, 512, 8, 0>(p, backward, st);
     }
-    if (p.dim <= 128) return run_norm<T, 1, 32, 4>(p, backward, st);
-    if (p.dim <= 512) return run_norm<T, 1, 128, 4>(p, backward, st);
-    if (p.dim <= 2048) return run_norm<T, 1, 256, 8>(p, backward, st);
-    return run_norm<T, 1, 512, 32>(p, backward, st);
+    if (p.dim <= 128) return plan_norm<T, 1, 32, 4, 0>(p, backward, st);
+    if (p.dim <= 512) return plan_norm<T, 1, 128, 4, 0>(p, backward, st);
+    if (p.dim <= 2048) return plan_norm<T, 1, 256, 8, 0>(p, backward, st);
+    return plan_norm<T, 1, 512, 32, 0>(p, backward, st);
 }
 
 int check_norm(const k2t_norm *a)

@@ -328,6 +328,17 @@ def norm_tolerances(dtype, x, z, xh, rstd, w, b, dy, dz, y, dx, dw, db):
                                    (4000, 1024), (33, 1000), (9, 2049), (21, 4096), (5, 8200), (3, 16384), (2, 9001)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_norm_matches(n, dim, dtype, residual):
+    check_norm(n, dim, dtype, residual)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,dim", [(40001, 64), (39999, 200), (20001, 512), (9800, 1000), (5001, 2048), (4990, 4096)])
+def test_norm_of_many_rows(n, dim, dtype):
+    """Enough rows that blocks stay for several and load ahead."""
+    check_norm(n, dim, dtype, True)
+
+
+def check_norm(n, dim, dtype, residual):
     rng = np.random.default_rng(n * 7 + dim)
     mk = lambda *s, scale=1.0, shift=0.0: torch.from_numpy(rng.standard_normal(s) * scale + shift).to(DT[dtype]).cuda()  # noqa: E731
     x, w, b, dy = mk(n, dim, shift=3.0), mk(dim, shift=1.0), mk(dim), mk(n, dim)
