@@ -40,14 +40,16 @@ constexpr uint64_t kSms = 152;
 
 // Blocks that share the nodes of one (head, row tile): as many as make the
 // fewest rounds of the GPU's SMs (one block each) times tiles a block, with
-// two tiles' time for a block's start and end.
+// two tiles' time for a block's start and end.  For a number of rounds, the
+// most blocks that it holds.
 uint32_t pick_splits(uint64_t blocks, uint64_t tiles)
 {
-    const uint64_t slots = kSms, most = std::min<uint64_t>(std::max<uint64_t>(1, tiles), slots);
+    const uint64_t most = std::min<uint64_t>(std::max<uint64_t>(1, tiles), kSms);
     uint64_t best = 1, cost = ~0ull;
-    for (uint64_t s = 1; s <= most; ++s) {
-        const uint64_t rounds = (blocks * s + slots - 1) / slots, c = rounds * ((tiles + s - 1) / s + 2);
+    for (uint64_t rounds = (blocks + kSms - 1) / kSms, last = rounds + 8; rounds <= last; ++rounds) {
+        const uint64_t s = std::min(most, rounds * kSms / blocks), c = rounds * ((tiles + s - 1) / s + 2);
         if (c < cost) cost = c, best = s;
+        if (s == most) break;
     }
     return (uint32_t)best;
 }

@@ -1,10 +1,14 @@
 // k2t_attn_launch.cuh -- launches of the attention kernels.
 #pragma once
 
+#include <atomic>
+
 #include "k2t_attn_bwd.cuh"
 #include "k2t_attn_fwd.cuh"
 
 namespace k2t {
+
+constexpr int kAttnMaxSmem = 232448;   // 227 KB
 
 #define K2T_ATTN_CUDA(call)                              \
     do {                                                 \
@@ -15,10 +19,17 @@ namespace k2t {
         }                                                \
     } while (0)
 
-template <typename K>
-int attn_launch(K kernel, dim3 grid, int threads, size_t smem, const AttnParams &p, cudaStream_t st)
+// The shared memory a kernel may have is a setting of the kernel on a device: raised once, to what any call can need.
+template <auto kernel> int attn_launch(dim3 grid, int threads, size_t smem, const AttnParams &p, cudaStream_t st)
 {
-    K2T_ATTN_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    static std::atomic<uint64_t> set{0};
+    int dev = 0;
+    K2T_ATTN_CUDA(cudaGetDevice(&dev));
+    if (dev >= 64 || !(set.load() >> dev & 1)) {
+        K2T_ATTN_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnMaxSmem));
+        if (dev < 64) set.fetch_or(1ull << dev);
+    }
+    if (smem > (size_t)kAttnMaxSmem) return K2T_ERANGE;
     kernel<<<grid, threads, smem, st>>>(p);
     K2T_ATTN_CUDA(cudaGetLastError());
     return K2T_OK;
@@ -27,7 +38,7 @@ int attn_launch(K kernel, dim3 grid, int threads, size_t smem, const AttnParams 
 // bm: rows a block takes, 32, 64, 128 or 256.
 template <typename T, int DP, int KW, bool TWO> int forward_tile(const AttnParams &p, cudaStream_t st)
 {
-    return attn_launch(attn_fwd_kernel<T, DP, KW, TWO>, dim3(p.splits * p.row_tiles, p.hkv), kTcThreads, TcSmem<DP, TWO>::bytes(p), p, st);
+    return attn_launch<attn_fwd_kernel<T, DP, KW, TWO>>(dim3(p.splits * p.row_tiles, p.hkv), kTcThreads, TcSmem<DP, TWO>::bytes(p), p, st);
 }
 
 template <typename T, int DP> int forward_dim(const AttnParams &p, int bm, cudaStream_t st)
@@ -55,7 +66,7 @@ inline uint32_t bwd_fused_tiles(uint32_t d) { return d <= 64 ? 4 : 2; }
 template <typename T, int DP, int RT, bool DKV> int backward_nodes(const AttnParams &p, cudaStream_t st)
 {
     const uint32_t groups = (p.row_tiles + RT - 1) / RT;
-    return attn_launch(attn_bwd_nodes_kernel<T, DP, RT, DKV>, dim3(p.splits * groups, p.hkv), kBwdThreads,
+    return attn_launch<attn_bwd_nodes_kernel<T, DP, RT, DKV>>(dim3(p.splits * groups, p.hkv), kBwdThreads,
                        BwdSmem<DP, RT, DKV>::bytes(p), p, st);
 }
 
@@ -67,7 +78,7 @@ template <typename T, int DP> int backward_dim(const AttnParams &p, cudaStream_t
         if (p.row_tiles <= 4) return backward_nodes<T, DP, 4, true>(p, st);
     }
     if (p.tiles) {
-        int rc = attn_launch(attn_bwd_rows_kernel<T, DP>, dim3((unsigned)p.tiles, p.hkv), kBwdRowThreads, BwdRowSmem<DP>::bytes(p), p, st);
+        int rc = attn_launch<attn_bwd_rows_kernel<T, DP>>(dim3((unsigned)p.tiles, p.hkv), kBwdRowThreads, BwdRowSmem<DP>::bytes(p), p, st);
         if (rc) return rc;
     }
     return backward_nodes<T, DP, 4, false>(p, st);

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 from .k2t import (ATTN_MAX_BUCKETS, ATTN_MAX_HOP, BF16, FP16, FP32, Attn, Norm, _check, _stream_ptr, load)
 
@@ -39,17 +40,38 @@ def _dtype_code(dtype, allowed):
     return code
 
 
-def _tensor(name, t, shape, dtype, contiguous):
-    """Address of a CUDA tensor of this shape and type whose last dimension is contiguous."""
+def _stream(torch, stream):
+    """The stream's address; the current stream's for None."""
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _stream_ptr(stream)
+
+
+def _refuse(name, t, shape, dtype, last_only):
+    """Say what is wrong with a tensor that a call does not take."""
     if t.shape != shape:
         raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if t.dtype is not dtype:
         raise TypeError("%s: expected %s, got %s" % (name, dtype, t.dtype))
     if not t.is_cuda:
         raise ValueError("%s: expected a CUDA tensor" % name)
-    if not (t.is_contiguous() if contiguous else t.stride(-1) == 1 or not t.numel()):
-        raise ValueError("%s: expected a contiguous %s" % (name, "tensor" if contiguous else "last dimension"))
+    raise ValueError("%s: expected a contiguous %s" % (name, "last dimension" if last_only else "tensor"))
+
+
+def _flat(name, t, shape, dtype):
+    """Address of a contiguous CUDA tensor of this shape and type."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        _refuse(name, t, shape, dtype, False)
     return t.data_ptr()
+
+
+def _rows(name, t, shape, dtype):
+    """(address, row pitch, head pitch) of a CUDA tensor [rows, heads, dim] whose last dimension is contiguous; a
+    dimension of one value has no pitch, whatever its stride says."""
+    row, head, last = t.stride()
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or last != 1 and t.numel():
+        _refuse(name, t, shape, dtype, True)
+    return t.data_ptr(), row if shape[0] > 1 else 0, head if shape[1] > 1 else 0
 
 
 class HopAttention:
@@ -77,6 +99,8 @@ class HopAttention:
         for i, e in enumerate(edges):
             a.edges[i] = e
         self._ref = ctypes.byref(a)
+        self._buf = memoryview(a).cast("B")
+        self._int, self._float = torch.int32, torch.float32
         self._rows = torch.Size((n_queries, n_heads, head_dim))
         self._nodes = torch.Size((n_nodes, n_kv_heads, head_dim))
         self._lse = torch.Size((n_queries, n_heads))
@@ -84,7 +108,8 @@ class HopAttention:
         self._source = torch.Size((n_queries,))
         self._table = torch.Size((n_heads, len(edges)))
         self._lib = load()
-        self._work, self._bytes = [None, None], [0, 0]
+        self._forward, self._backward = self._lib.k2t_attn_forward, self._lib.k2t_attn_backward
+        self._work, self._bytes, self._at = [None, None], [0, 0], [0, 0]
 
     def work_bytes(self, backward: bool = False) -> int:
         """Device bytes of the work buffer of a pass (k2t_attn_work_bytes)."""
@@ -95,7 +120,8 @@ class HopAttention:
             self._bytes[backward] = self.work_bytes(bool(backward))
             self._work[backward] = self._torch.empty(self._bytes[backward], dtype=self._torch.uint8, device=self.device)
             self._work[backward][:4].zero_()
-        return self._work[backward].data_ptr(), self._bytes[backward]
+            self._at[backward] = self._work[backward].data_ptr()
+        return self._at[backward], self._bytes[backward]
 
     def status(self) -> int:
         """The device status words of both passes, joined: waits for the device; 0, or
@@ -106,50 +132,50 @@ class HopAttention:
                 word |= int(work[:4].view(self._torch.int32).item())
         return word
 
-    def _rows_in(self, name, t, shape):
-        a = self._a
-        setattr(a, name, _tensor(name, t, shape, self.dtype, False))
-        row, head, _ = t.stride()
-        # a dimension of one value has no pitch, whatever its stride says
-        setattr(a, name + "_row", row if shape[0] > 1 else 0)
-        setattr(a, name + "_head", head if shape[1] > 1 else 0)
-
-    def _table_in(self, hops, bias, query_source):
-        a, torch = self._a, self._torch
+    def _inputs(self, q, k, v, out, lse, hops, bias, query_source):
+        a, dt = self._a, self.dtype
         if (hops is None) != (a.n_sources == 0):
             raise ValueError("hops: given %s, sources %d" % (hops is not None, a.n_sources))
-        a.hops = None if hops is None else _tensor("hops", hops.view(self._hops), self._hops, torch.int32, True)
-        a.bias = None if bias is None else _tensor("bias", bias, self._table, self.dtype, True)
-        a.query_source = None if query_source is None else _tensor("query_source", query_source, self._source,
-                                                                   torch.int32, True)
+        qp, qr, qh = _rows("q", q, self._rows, dt)
+        kp, kr, kh = _rows("k", k, self._nodes, dt)
+        vp, vr, vh = _rows("v", v, self._nodes, dt)
+        op, orow, oh = _rows("out", out, self._rows, dt)
+        _INPUTS.pack_into(self._buf, _AT_INPUTS, qp, kp, vp, qr, qh, kr, kh, vr, vh,
+                          0 if hops is None else _flat("hops", hops.view(self._hops), self._hops, self._int),
+                          0 if query_source is None else _flat("query_source", query_source, self._source, self._int),
+                          0 if bias is None else _flat("bias", bias, self._table, dt),
+                          op, _flat("lse", lse, self._lse, self._float), orow, oh)
 
     def forward(self, q, k, v, out, lse, hops=None, bias=None, query_source=None, stream=None):
         """out [T, n_heads, head_dim] and lse (fp32 [T, n_heads]) of q, k, v."""
-        a = self._a
-        self._rows_in("q", q, self._rows)
-        self._rows_in("k", k, self._nodes)
-        self._rows_in("v", v, self._nodes)
-        self._rows_in("out", out, self._rows)
-        a.lse = _tensor("lse", lse, self._lse, self._torch.float32, True)
-        self._table_in(hops, bias, query_source)
+        self._inputs(q, k, v, out, lse, hops, bias, query_source)
         work, size = self._work_of(0)
-        _check("k2t_attn_forward", self._lib.k2t_attn_forward(self._ref, work, size, _stream_ptr(stream)))
+        rc = self._forward(self._ref, work, size, _stream(self._torch, stream))
+        if rc:
+            _check("k2t_attn_forward", rc)
         return out, lse
 
     def backward(self, dout, q, k, v, out, lse, dq, dk, dv, dbias=None, hops=None, bias=None, query_source=None,
                  stream=None):
         """Gradients of q, k, v and the bias table from dout, the inputs and the forward's out and lse."""
-        a = self._a
-        for name, t, shape in (("dout", dout, self._rows), ("q", q, self._rows), ("k", k, self._nodes),
-                               ("v", v, self._nodes), ("out", out, self._rows), ("dq", dq, self._rows),
-                               ("dk", dk, self._nodes), ("dv", dv, self._nodes)):
-            self._rows_in(name, t, shape)
-        a.lse = _tensor("lse", lse, self._lse, self._torch.float32, True)
-        a.dbias = None if dbias is None else _tensor("dbias", dbias, self._table, self.dtype, True)
-        self._table_in(hops, bias, query_source)
+        self._inputs(q, k, v, out, lse, hops, bias, query_source)
+        dt = self.dtype
+        dqp, dqr, dqh = _rows("dq", dq, self._rows, dt)
+        dkp, dkr, dkh = _rows("dk", dk, self._nodes, dt)
+        dvp, dvr, dvh = _rows("dv", dv, self._nodes, dt)
+        _GRADIENTS.pack_into(self._buf, _AT_GRADIENTS, *_rows("dout", dout, self._rows, dt), dqp, dkp, dvp, dqr, dqh,
+                             dkr, dkh, dvr, dvh, 0 if dbias is None else _flat("dbias", dbias, self._table, dt))
         work, size = self._work_of(1)
-        _check("k2t_attn_backward", self._lib.k2t_attn_backward(self._ref, work, size, _stream_ptr(stream)))
+        rc = self._backward(self._ref, work, size, _stream(self._torch, stream))
+        if rc:
+            _check("k2t_attn_backward", rc)
         return dq, dk, dv, dbias
+
+
+# the pointers and pitches of k2t_attn, in the header's order: q .. out_head, dout .. dbias
+_INPUTS, _AT_INPUTS = struct.Struct("=3Q6q5Q2q"), Attn.q.offset
+_GRADIENTS, _AT_GRADIENTS = struct.Struct("=Q2q3Q6qQ"), Attn.dout.offset
+assert _AT_INPUTS + _INPUTS.size == _AT_GRADIENTS and _AT_GRADIENTS + _GRADIENTS.size == ctypes.sizeof(Attn)
 
 
 class LayerNorm:
@@ -163,6 +189,7 @@ class LayerNorm:
         a.dtype = _dtype_code(dtype, (BF16, FP16, FP32))
         a.dim, a.n_rows, a.eps = dim, n_rows, eps
         self._ref = ctypes.byref(a)
+        self._buf = memoryview(a).cast("B")
         self._rows, self._cols = torch.Size((n_rows, dim)), torch.Size((dim,))
         self._lib = load()
         self.mean = torch.empty(n_rows, dtype=torch.float32, device=device)
@@ -174,30 +201,38 @@ class LayerNorm:
         """Device bytes of the backward pass's work buffer (k2t_norm_work_bytes)."""
         return int(self._lib.k2t_norm_work_bytes(self._ref))
 
-    def _in(self, name, t, shape):
-        setattr(self._a, name, None if t is None else _tensor(name, t, shape, self.dtype, True))
-
     def forward(self, x, weight, bias, y, residual=None, z=None, stream=None):
         """y = norm(z) and, with a residual, z = x + residual; keeps mean and rstd for backward."""
         if (residual is not None) != self.residual or (z is not None) != self.residual:
             raise ValueError("residual and z are given exactly when the layer has a residual")
-        for name, t in (("x", x), ("residual", residual), ("y", y), ("z", z)):
-            self._in(name, t, self._rows)
-        self._in("weight", weight, self._cols)
-        self._in("bias", bias, self._cols)
-        _check("k2t_norm_forward", self._lib.k2t_norm_forward(self._ref, _stream_ptr(stream)))
+        dt, rows, cols = self.dtype, self._rows, self._cols
+        _FORWARD.pack_into(self._buf, _AT_FORWARD, _flat("x", x, rows, dt),
+                           0 if residual is None else _flat("residual", residual, rows, dt),
+                           _flat("weight", weight, cols, dt), 0 if bias is None else _flat("bias", bias, cols, dt),
+                           _flat("y", y, rows, dt), 0 if z is None else _flat("z", z, rows, dt))
+        rc = self._lib.k2t_norm_forward(self._ref, _stream(self._torch, stream))
+        if rc:
+            _check("k2t_norm_forward", rc)
         return y if z is None else (y, z)
 
     def backward(self, dy, z, weight, dx, dweight, dbias=None, dz=None, stream=None):
         """dx (of x and of the residual alike), dweight and dbias from dy and the forward's z (its x without a
         residual); dz, the gradient that reaches z from elsewhere, is added to dx."""
-        for name, t in (("dy", dy), ("z", z), ("dx", dx), ("dz", dz)):
-            self._in(name, t, self._rows)
-        for name, t in (("weight", weight), ("dweight", dweight), ("dbias", dbias)):
-            self._in(name, t, self._cols)
+        dt, rows, cols = self.dtype, self._rows, self._cols
+        a = self._a
+        a.z, a.weight = _flat("z", z, rows, dt), _flat("weight", weight, cols, dt)
+        _BACKWARD.pack_into(self._buf, _AT_BACKWARD, _flat("dy", dy, rows, dt),
+                            0 if dz is None else _flat("dz", dz, rows, dt), _flat("dx", dx, rows, dt),
+                            _flat("dweight", dweight, cols, dt), 0 if dbias is None else _flat("dbias", dbias, cols, dt))
         if self._work is None:
             self._bytes = self.work_bytes()
             self._work = self._torch.empty(max(16, self._bytes), dtype=self._torch.uint8, device=self.device)
-        _check("k2t_norm_backward", self._lib.k2t_norm_backward(self._ref, self._work.data_ptr(), self._bytes,
-                                                                _stream_ptr(stream)))
+        rc = self._lib.k2t_norm_backward(self._ref, self._work.data_ptr(), self._bytes, _stream(self._torch, stream))
+        if rc:
+            _check("k2t_norm_backward", rc)
         return dx, dweight, dbias
+
+
+_FORWARD, _AT_FORWARD = struct.Struct("=6Q"), Norm.x.offset
+_BACKWARD, _AT_BACKWARD = struct.Struct("=5Q"), Norm.dy.offset
+assert _AT_FORWARD + _FORWARD.size == Norm.mean.offset and _AT_BACKWARD + _BACKWARD.size == ctypes.sizeof(Norm)
