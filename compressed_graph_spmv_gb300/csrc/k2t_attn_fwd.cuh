@@ -10,16 +10,17 @@
 // and values alternate); scores S = Q K^T (128 rows x 128 nodes) and outputs
 // O = P V accumulate in tensor memory, the weights P go back to it over S and
 // are the A operand of the second product.  Warps:
-//   0-7   two softmax groups of 128 threads, thread = row of S (lane of
-//         tensor memory), with a running maximum, sum and O of their own
-//   8-11  hops of a tile -> bucket bytes, and which nodes are seen
-//   12-15 states of a tile's seen nodes -> slots
-//   16    one thread issues every product
+//   0-15  two softmax groups of 256 threads, with a running maximum, sum and
+//         O of their own; a row of S (lane of tensor memory) has two threads,
+//         one for each half of its nodes, which agree on the maximum
+//   16-19 hops of a tile -> bucket bytes, and which nodes are seen
+//   20-23 states of a tile's seen nodes -> slots
+//   24    issues every product
 // Rows.  With more than 128 rows (TWO) the groups take two row tiles and
 // share each tile of nodes; else they take alternate tiles.  With 64 or 32
 // rows or fewer the rows are repeated 2 or 4 times down the 128 lanes, and
 // each copy takes its own part (KW = 64 or 32 nodes) of every tile: its P is
-// zero elsewhere, so its O is the sum over its part, and all 128 threads have
+// zero elsewhere, so its O is the sum over its part, and all threads have
 // scores to work on.  The copies, the groups and the splits are joined as
 // separate softmaxes at the end.
 //
@@ -36,25 +37,27 @@
 
 namespace k2t {
 
-constexpr int kTcThreads = 640;
-constexpr int kTcBufs = 4;          // bucket tiles
+constexpr int kTcThreads = 800;
+constexpr int kTcLutAlign = 8192;   // the bias table's alignment, above its size: its address joins an index by OR
 constexpr float kTcLag = 8.0f;
 
 template <int DP, bool TWO> struct TcSmem {
     static constexpr int kPanel = kTcTile * 128;              // 64 values of 128 rows
     static constexpr int kSlot = kPanel * (DP / 64);
     static constexpr int kSlots = DP == 64 ? 8 : TWO ? 4 : 5;
+    static constexpr int kBufs = DP == 64 ? 6 : 3;            // bucket tiles
     static constexpr int kQ = kSlots * kSlot;
     static constexpr int kBuckets = kQ + kSlot * (TWO ? 2 : 1);
-    static constexpr int kCtl = kBuckets + kTcBufs * 33 * kTcPitch;
+    static constexpr int kCtl = kBuckets + kBufs * 33 * kTcPitch;
     struct Ctl {
-        uint64_t full[kSlots], empty[kSlots], hop_full[kTcBufs], hop_empty[kTcBufs], s_full[2], p_full[2], o_full[2], drained;
+        uint64_t full[kSlots], empty[kSlots], hop_full[kBufs], hop_empty[kBufs], pair[8], s_full[2], p_full[2], o_full[2], drained;
         uint32_t tmem, gave_up, columns, all;
-        uint32_t seen[kTcBufs][4];
+        uint32_t seen[kBufs][4];
+        float tops[2][2][2][128];         // [turn][group][half][lane]
         uint8_t byte_of[257 + 15];        // bucket byte of hops + 1
     };
     static constexpr int kLut = kCtl + (int)((sizeof(Ctl) + 15) / 16 * 16);
-    static size_t bytes(const AttnParams &p) { return kLut + (size_t)(p.buckets + 2) * p.group2 * 4; }
+    static size_t bytes(const AttnParams &p) { return kLut + kTcLutAlign + (size_t)(p.buckets + 2) * p.group2 * 4; }
 };
 
 // Two fp32 operations in one instruction.
@@ -73,21 +76,29 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
         : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
     return d;
 }
+// The bias table does not change once the block has set it up, so that its reads may move freely.
+__device__ __forceinline__ float table(uint32_t at)
+{
+    float v;
+    asm("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+    return v;
+}
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-// Scores of 32 nodes in units of log2, biased and masked, and their maximum
-// with `top`.  bt: their bucket bytes; a byte b's bias lies at lg + (b <<
-// shift) (floats of 2^k query heads, k = shift - 2).
-__device__ __forceinline__ float bias32(uint32_t (&s)[32], float scale, bool plain, const uint8_t *bt, const uint8_t *lg, uint32_t shift, float top)
+// Scores of N nodes in units of log2, biased and masked, and their maximum
+// with `top`.  bt: their bucket bytes; a byte b's bias lies at shared-memory
+// address lg | b << shift (floats of 2^k query heads, k = shift - 2).
+template <int N>
+__device__ __forceinline__ float bias_scores(uint32_t (&s)[N], float scale, bool plain, const uint8_t *bt, uint32_t lg, uint32_t shift, float top)
 {
     const float2 sc = make_float2(scale, scale);
     if (plain) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
+        for (int e = 0; e < N; e += 2) {
             const float2 x = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc, make_float2(0.0f, 0.0f));
             s[e] = __float_as_uint(x.x);
             s[e + 1] = __float_as_uint(x.y);
@@ -97,15 +108,15 @@ __device__ __forceinline__ float bias32(uint32_t (&s)[32], float scale, bool pla
     }
     const uint32_t mask = 255u << shift;
 #pragma unroll
-    for (int e = 0; e < 32; e += 16) {
+    for (int e = 0; e < N; e += 16) {
         const uint4 b16 = *reinterpret_cast<const uint4 *>(bt + e);
         const uint32_t w[4] = {b16.x, b16.y, b16.z, b16.w};
 #pragma unroll
         for (int y = 0; y < 16; y += 2) {
             const uint32_t v = w[y >> 2];
             const uint32_t i0 = (y & 3) ? v >> (16 - shift) : v << shift, i1 = (y & 3) ? v >> (24 - shift) : v >> (8 - shift);
-            const float2 bias = make_float2(*reinterpret_cast<const float *>(lg + (i0 & mask)), *reinterpret_cast<const float *>(lg + (i1 & mask)));
-            const float2 x = fma2(make_float2(__uint_as_float(s[e + y]), __uint_as_float(s[e + y + 1])), sc, bias);
+            const float2 x = fma2(make_float2(__uint_as_float(s[e + y]), __uint_as_float(s[e + y + 1])), sc,
+                                  make_float2(table((i0 & mask) | lg), table((i1 & mask) | lg)));
             s[e + y] = __float_as_uint(x.x);
             s[e + y + 1] = __float_as_uint(x.y);
             top = max3(top, x.x, x.y);
@@ -114,13 +125,13 @@ __device__ __forceinline__ float bias32(uint32_t (&s)[32], float scale, bool pla
     return top;
 }
 
-// Weights of 32 scores, two a word in the element type, and their sum onto `sum`.
-template <typename T>
-__device__ __forceinline__ void weights32(uint32_t (&out)[16], const uint32_t (&s)[32], float m, float2 (&sum)[2])
+// Weights of N scores, two a word in the element type, and their sum onto `sum`.
+template <typename T, int N>
+__device__ __forceinline__ void weights(uint32_t (&out)[N / 2], const uint32_t (&s)[N], float m, float2 (&sum)[2])
 {
     const float2 nm = make_float2(-m, -m);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
+    for (int e = 0; e < N / 2; ++e) {
         const float2 x = add2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), nm);
         const float2 y = make_float2(ex2(x.x), ex2(x.y));
         sum[e & 1] = add2(sum[e & 1], y);
@@ -134,11 +145,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
     using S = TcSmem<DP, TWO>;
     using Ctl = typename S::Ctl;
     constexpr int kRows = KW;                      // distinct rows per 128 lanes: 128, 64 or 32
+    constexpr int HW = KW / 2, CH = HW < 32 ? HW : 32;   // nodes of a thread's part of a tile, of them at a time
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     extern __shared__ __align__(1024) uint8_t smem[];
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + S::kCtl);
     const uint32_t sm = tc::saddr(smem);
-    float *lut = reinterpret_cast<float *>(smem + S::kLut);
+    const uint32_t lut_at = (sm + S::kLut + kTcLutAlign - 1) & ~(uint32_t)(kTcLutAlign - 1);
+    float *lut = reinterpret_cast<float *>(smem + (lut_at - sm));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t hk = blockIdx.y, split = blockIdx.x % p.splits;
     const uint32_t row0 = blockIdx.x / p.splits * (TWO ? 256 : kRows);
@@ -147,13 +160,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
     auto tile_at = [&](uint32_t i) { return split + (uint64_t)i * p.splits; };
 
     // ---- set-up ----
-    if (warp == 16) tc::alloc(&ctl->tmem, 512);
+    if (warp == 24) tc::alloc(&ctl->tmem, 512);
     if (tid == 0) {
         for (int i = 0; i < S::kSlots; ++i) tc::bar_init(&ctl->full[i], 128), tc::bar_init(&ctl->empty[i], 1);
-        for (int i = 0; i < kTcBufs; ++i) tc::bar_init(&ctl->hop_full[i], 4), tc::bar_init(&ctl->hop_empty[i], TWO ? 8 : 4);
+        for (int i = 0; i < S::kBufs; ++i) tc::bar_init(&ctl->hop_full[i], 4), tc::bar_init(&ctl->hop_empty[i], TWO ? 16 : 8);
+        for (int i = 0; i < 8; ++i) tc::bar_init(&ctl->pair[i], 2);
         for (int i = 0; i < 2; ++i) {
             tc::bar_init(&ctl->s_full[i], 1);
-            tc::bar_init(&ctl->p_full[i], 128);
+            tc::bar_init(&ctl->p_full[i], 256);
             tc::bar_init(&ctl->o_full[i], 1);
         }
         tc::bar_init(&ctl->drained, 1);
@@ -192,12 +206,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
     const uint32_t tm = ctl->tmem;                       // S of group w at w * 128, O at 256 + w * DP
     volatile uint32_t *gave_up = &ctl->gave_up;
 
-    if (warp >= 8 && warp < 12) {
-        hop_warps<kTcBufs>(p, ctl, smem + S::kBuckets, warp - 8, lane, tiles, split, gave_up);
-    } else if (warp >= 12 && warp < 16) {
-        node_warps<DP, S::kSlots, kTcBufs>(p, ctl, sm, warp - 12, lane, hk, tiles, split, gave_up);
-    } else if (warp >= 16) {
-        if (warp == 16) {
+    if (warp >= 16 && warp < 20) {
+        hop_warps<S::kBufs>(p, ctl, smem + S::kBuckets, warp - 16, lane, tiles, split, gave_up);
+    } else if (warp >= 20 && warp < 24) {
+        node_warps<DP, S::kSlots, S::kBufs>(p, ctl, sm, warp - 20, lane, hk, tiles, split, gave_up);
+    } else if (warp == 24) {
+        {
             const bool lead = tc::elect();
             // ---- products ----
             const uint32_t id_s = tc::idesc(kBf16, kTcTile, false, false);
@@ -233,7 +247,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
                     const uint64_t v = tc::desc(base + slot * S::kSlot, S::kPanel);
 #pragma unroll
                     for (uint32_t kk = 0; kk < kTcTile / 16; ++kk)
-                        tc::mma_ts(lead, tm + 256 + w * DP, tm + w * 128 + kk * 8, v, kk * 2048, id_o, done > 1 || kk > 0);
+                        tc::mma_ts(lead, tm + 256 + w * DP, tm + w * 128 + kk * 8 + (kk < 4 ? 0 : 32), v, kk * 2048, id_o, done > 1 || kk > 0);
                     if (!TWO || w == 1) tc::commit(lead, &ctl->empty[slot]);
                     if (done + 2 >= units) tc::commit(lead, &ctl->o_full[w]);
                     ++done;
@@ -247,48 +261,52 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
         }
         __syncwarp();
     } else {
-        // ---- softmax: thread = lane of tensor memory ----
-        const int w = warp >> 2, l = tid & 127;
+        // ---- softmax: thread = (lane of tensor memory, half of its copy's nodes) ----
+        const int w = warp >> 3, half = (warp >> 2) & 1, l = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // lane field of this warp's tensor memory
         const uint32_t row = row0 + (TWO ? w * 128 : 0) + l % kRows;
-        const int key0 = l / kRows * KW;                              // this copy's part of a tile
+        const int copy = l / kRows, key0 = copy * KW + half * HW;     // this thread's part of a tile
         const uint32_t col = row < p.rows ? row_column(p, row) : 0;
         const uint32_t G = p.group, shift = p.group2_log + 2;
-        const uint8_t *lg = reinterpret_cast<const uint8_t *>(lut + (row < p.rows ? row % G : 0));
+        const uint32_t lg = lut_at | (row < p.rows ? row % G : 0) * 4;
         const uint32_t s_at = tm + lanes + w * 128, o_at = tm + lanes + 256 + w * DP;
         const uint8_t *bt0 = smem + S::kBuckets + col * kTcPitch + key0;
+        float *tops = ctl->tops[0][w][0] + l;                         // [turn][group][half][lane]
+        uint64_t *pair = &ctl->pair[w * 4 + (warp & 3)];
         float m = -INFINITY;
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         bool ok = true;
         uint32_t mine = 0;                                            // units of this group done
         for (uint32_t u = w; u < units; u += 2, ++mine) {
-            const uint32_t i = TWO ? u >> 1 : u, buf = i % kTcBufs;
-            ok = tc::bar_wait(&ctl->hop_full[buf], (i / kTcBufs) & 1, gave_up) && tc::bar_wait(&ctl->s_full[w], mine & 1, gave_up);
+            const uint32_t i = TWO ? u >> 1 : u, buf = i % S::kBufs;
+            ok = tc::bar_wait(&ctl->hop_full[buf], (i / S::kBufs) & 1, gave_up) && tc::bar_wait(&ctl->s_full[w], mine & 1, gave_up);
             ok = __all_sync(~0u, ok);
             if (!ok) break;
             tc::fence_after();
             const bool plain = !p.sources && (tile_at(i) + 1) * kTcTile <= p.n;   // no table, no node past the end
             const uint8_t *bt = bt0 + buf * 33 * kTcPitch;
             float top = -INFINITY;
-            uint32_t s[32];
-            if (KW == 32) {
-                tc::ld32(s, s_at + key0);
-                tc::wait_ld();
-                top = bias32(s, p.scale_log2, plain, bt, lg, shift, top);
-            } else {
-                // scores go back to tensor memory between the two passes: rolled loops of 32 nodes, since the whole
-                // row in registers makes code that the instruction caches do not hold
+            uint32_t s[CH];
+            // With two chunks, biased scores go back to tensor memory between the passes: rolled loops, since the
+            // whole row in registers makes code that the instruction caches do not hold.
 #pragma unroll 1
-                for (int b = 0; b < KW; b += 32) {
-                    tc::ld32(s, s_at + key0 + b);
-                    tc::wait_ld();
-                    top = bias32(s, p.scale_log2, plain, bt + b, lg, shift, top);
-                    tc::st32(s_at + key0 + b, s);
-                }
-                tc::wait_st();
+            for (int b = 0; b < HW; b += CH) {
+                tc::load(s, s_at + key0 + b);
+                tc::wait_ld();
+                top = bias_scores(s, p.scale_log2, plain, bt + b, lg, shift, top);
+                if (HW > CH) tc::store(s_at + key0 + b, s);
             }
+            if (HW > CH) tc::wait_st();
+            // the two halves of a row agree on its maximum, and have both read their scores, before weights replace them
+            const int turn = (mine & 1) * 512;
+            tops[turn + half * 128] = top;
+            tc::fence_before();
             __syncwarp();
-            if (lane == 0) tc::bar_arrive(&ctl->hop_empty[buf]);
+            if (lane == 0) tc::bar_arrive(&ctl->hop_empty[buf]), tc::bar_arrive(pair);
+            ok = __all_sync(~0u, tc::bar_wait(pair, mine & 1, gave_up));
+            if (!ok) break;
+            tc::fence_after();
+            top = fmaxf(top, tops[turn + (half ^ 1) * 128]);
             const bool grow = top > m + kTcLag || (m == -INFINITY && top > -INFINITY);
             if (__any_sync(~0u, grow)) {
                 const float next = grow ? top : m;
@@ -297,44 +315,43 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
 #pragma unroll
                 for (int e = 0; e < 2; ++e) sum[e].x *= f, sum[e].y *= f;
                 if (mine > 0) {
-                    // the products issued before these scores are done, so O is at rest
+                    // the products issued before these scores are done, so O is at rest; each half takes half of it
 #pragma unroll 1
-                    for (int c = 0; c < DP; c += 32) {
-                        uint32_t o[32];
-                        tc::ld32(o, o_at + c);
+                    for (int c = half * (DP / 2); c < (half + 1) * (DP / 2); c += 16) {
+                        uint32_t o[16];
+                        tc::load(o, o_at + c);
                         tc::wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tc::st32(o_at + c, o);
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tc::store(o_at + c, o);
                     }
                 }
             }
             const float u0 = m == -INFINITY ? 0.0f : m;
-            // weights in the element type, two a word, over S: nodes of the other copies' parts weigh nothing
+            // Weights in the element type, two a word, over S: nodes [0, 64) from its column 0 on, [64, 128) from 64 on,
+            // so that a half of 64 overwrites its own scores.  Nodes of the other copies' parts weigh nothing.
             if (KW == 128) {
 #pragma unroll 1
-                for (int b = 0; b < 128; b += 32) {
-                    uint32_t out[16];
-                    tc::ld32(s, s_at + b);
+                for (int b = 0; b < HW; b += CH) {
+                    uint32_t out[CH / 2];
+                    tc::load(s, s_at + key0 + b);
                     tc::wait_ld();
-                    weights32<T>(out, s, u0, sum);
-                    tc::st16(s_at + b / 2, out);
+                    weights<T, CH>(out, s, u0, sum);
+                    tc::store(s_at + key0 + b / 2, out);
                 }
             } else {
-                uint32_t out[KW / 32][16];
+                uint32_t out[CH / 2];
+                weights<T, CH>(out, s, u0, sum);
 #pragma unroll
-                for (int b = 0; b < KW / 32; ++b) {
-                    if (KW != 32) {
-                        tc::ld32(s, s_at + key0 + b * 32);
-                        tc::wait_ld();
+                for (int j = 0; j < 128 / KW; ++j) {
+                    const uint32_t at = s_at + (j * KW < 64 ? j * KW / 2 : 64 + (j * KW - 64) / 2) + half * (HW / 2);
+                    if (j == copy) {
+                        tc::store(at, out);
+                    } else {
+                        const uint32_t zero[CH / 2] = {};
+                        tc::store(at, zero);
                     }
-                    weights32<T>(out[b], s, u0, sum);
                 }
-                const uint32_t zero[16] = {};
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (q * 32 / KW == l / kRows) tc::st16(s_at + q * 16, out[q % (KW / 32)]);
-                    else tc::st16(s_at + q * 16, zero);
             }
             tc::wait_st();
             tc::fence_before();
@@ -345,7 +362,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
             ok = tc::bar_wait(&ctl->o_full[w], 0, gave_up);
             tc::fence_after();
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("bar.sync 1, 512;" ::: "memory");
         ok = !*gave_up;
         constexpr int P = DP + 4;
         static_assert(256 * P * 4 <= S::kBuckets, "the exchange fits the slots and queries");
@@ -353,25 +370,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
         if (ok) {
             float *at = ex + (size_t)(w * 128 + l) * P;
 #pragma unroll 1
-            for (int c = 0; c < DP; c += 32) {
-                uint32_t o[32];
+            for (int c = half * (DP / 2); c < (half + 1) * (DP / 2); c += 16) {
+                uint32_t o[16];
                 if (mine > 0) {
-                    tc::ld32(o, o_at + c);
+                    tc::load(o, o_at + c);
                     tc::wait_ld();
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0;
+                    for (int e = 0; e < 16; ++e) o[e] = 0;
                 }
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4 *>(at + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4 *>(at + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
-            at[DP] = m;
-            at[DP + 1] = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            if (half == 0) at[DP] = m;
+            at[DP + 1 + half] = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("bar.sync 1, 512;" ::: "memory");
         constexpr int kSets = TWO ? 1 : 2 * (128 / kRows), kOut = TWO ? 256 : kRows, Q4 = DP / 4;
         if (ok)
-            for (int i = tid; i < kOut * Q4; i += 256) {
+            for (int i = tid; i < kOut * Q4; i += 512) {
                 const int r = i / Q4, c = (i % Q4) * 4;
                 const uint32_t rw = row0 + r;
                 if (rw >= p.rows || c >= (int)p.d) continue;
@@ -387,7 +404,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
                     const float *e = e0 + (size_t)k * kRows * P;
                     const float f = ex2(e[DP] - ux);
                     const float4 x = *reinterpret_cast<const float4 *>(e + c);
-                    ls += f * e[DP + 1];
+                    ls += f * (e[DP + 1] + e[DP + 2]);
                     acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
                 }
                 const uint32_t t = rw / G, hd = hk * G + rw - t * G;
@@ -408,7 +425,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
     __syncwarp();
     tc::fence_before();
     __syncthreads();
-    if (warp == 16) tc::dealloc(tm, 512);
+    if (warp == 24) tc::dealloc(tm, 512);
     if (tid == 0 && *gave_up) atomicOr(p.status, K2T_STATUS_WAIT_TIMEOUT);
 }
 

@@ -59,6 +59,7 @@ struct Patience {
     __device__ void restart() { start = clock64(); }
     __device__ bool more()
     {
+        __nanosleep(20);      // polling takes issue slots from the warps that share the scheduler
         if (clock64() - start > (1ll << 31)) *gave_up = 1;
         return !*gave_up;
     }
@@ -139,6 +140,12 @@ __device__ __forceinline__ void st4(uint32_t at, const uint32_t (&r)[4])
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
 }
+
+__device__ __forceinline__ void load(uint32_t (&r)[32], uint32_t at) { ld32(r, at); }
+__device__ __forceinline__ void load(uint32_t (&r)[16], uint32_t at) { ld16(r, at); }
+__device__ __forceinline__ void store(uint32_t at, const uint32_t (&r)[32]) { st32(at, r); }
+__device__ __forceinline__ void store(uint32_t at, const uint32_t (&r)[16]) { st16(at, r); }
+__device__ __forceinline__ void store(uint32_t at, const uint32_t (&r)[8]) { st8(at, r); }
 
 // ---- matrix products ------------------------------------------------------------
 // Operand tiles in shared memory: panels of 64 16-bit values (128 bytes) a
