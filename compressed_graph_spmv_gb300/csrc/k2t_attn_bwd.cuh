@@ -178,8 +178,8 @@ __device__ __forceinline__ void node_products(bool lead, uint32_t at, uint32_t d
 template <int DP, int RT, bool DKV> struct BwdSmem {
     static constexpr int kPanel = kTcTile * 128;
     static constexpr int kSlot = kPanel * (DP / 64);
-    static constexpr int kSlots = DP == 64 ? 6 : DKV ? 4 : 3;
-    static constexpr int kBufs = DP == 64 ? 3 : 2;                            // bucket tiles
+    static constexpr int kSlots = DP == 64 ? (RT == 1 ? 8 : 6) : DKV ? 4 : 3;
+    static constexpr int kBufs = DP == 64 ? 6 : 2;                            // bucket tiles
     static constexpr int kRowTile = kBwdRows * DP * 2;                        // q or dout of a row tile
     static constexpr int kRow = kSlots * kSlot;                               // [RT][q | dout]
     static constexpr int kDs = kRow + RT * 2 * kRowTile;                      // dS^T [node][unit parity][32 rows]
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
         // ---- sums of ds by bucket: thread = (row of the tile, quarter of the nodes), with a table of its own ----
         if (p.buckets) {
             const int t = tid - 640, c = t & 31, part = t >> 5;
-            float *mine = hist + t;
+            uint8_t *mine = reinterpret_cast<uint8_t *>(hist + t);
             uint32_t i = 0, r = 0;
             for (uint32_t u = 0; u < units; ++u) {
                 const uint32_t w = u & 1, buf = i % S::kBufs;
@@ -364,23 +364,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
                 const uint8_t *ds = smem + S::kDs + part * 32 * 128 + (c & 7) * 2;
                 const uint32_t chunk = w * 4 + (c >> 3);
 #pragma unroll 1
-                for (int k = 0; k < 32; k += 4) {
-                    // four nodes at once: equal buckets among them take the running value, and the last store stands
-                    const uint32_t bw = *reinterpret_cast<const uint32_t *>(bt + k);
-                    uint32_t b[4];
-                    float x[4], hv[4];
+                for (int k = 0; k < 32; k += 8) {
+                    const uint2 b8 = *reinterpret_cast<const uint2 *>(bt + k);
+                    float x[8];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        b[y] = (bw >> (8 * y)) & 255;
-                        x[y] = Elem<T>::to_float(*reinterpret_cast<const T *>(ds + (k + y) * 128 + ((chunk ^ ((k + y) & 7)) << 4)));
-                        hv[y] = mine[b[y] * 128];
+                    for (int y = 0; y < 8; ++y) x[y] = Elem<T>::to_float(*reinterpret_cast<const T *>(ds + (k + y) * 128 + ((chunk ^ y) << 4)));
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        // four nodes at once: equal buckets among them take the running value, and the last store stands
+                        const uint32_t bw = q ? b8.y : b8.x;
+                        uint32_t b[4];
+                        float hv[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            b[y] = __byte_perm(bw, 0, 0x4440 + y) << 9;       // 512 bytes a bucket
+                            hv[y] = *reinterpret_cast<const float *>(mine + b[y]);
+                        }
+                        hv[0] += x[4 * q];
+                        hv[1] = (b[1] == b[0] ? hv[0] : hv[1]) + x[4 * q + 1];
+                        hv[2] = (b[2] == b[1] ? hv[1] : b[2] == b[0] ? hv[0] : hv[2]) + x[4 * q + 2];
+                        hv[3] = (b[3] == b[2] ? hv[2] : b[3] == b[1] ? hv[1] : b[3] == b[0] ? hv[0] : hv[3]) + x[4 * q + 3];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) *reinterpret_cast<float *>(mine + b[y]) = hv[y];
                     }
-                    hv[0] += x[0];
-                    hv[1] = (b[1] == b[0] ? hv[0] : hv[1]) + x[1];
-                    hv[2] = (b[2] == b[1] ? hv[1] : b[2] == b[0] ? hv[0] : hv[2]) + x[2];
-                    hv[3] = (b[3] == b[2] ? hv[2] : b[3] == b[1] ? hv[1] : b[3] == b[0] ? hv[0] : hv[3]) + x[3];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) mine[b[y] * 128] = hv[y];
                 }
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(&ctl->hist_done[w]), tc::bar_arrive(&ctl->hop_empty[buf]);
@@ -562,18 +568,40 @@ __global__ void __launch_bounds__(kBwdRowThreads, 1) attn_bwd_rows_kernel(const 
         hop_warps<1>(p, ctl, smem + S::kBuckets, warp - 8, lane, 1, tile, gave_up);
     } else if (warp < 16) {
         node_warps<DP, 2, 1>(p, ctl, sm, warp - 12, lane, hk, 1, tile, gave_up);
+        // Row tiles: this thread's chunks are the same of every tile, so that their places are worked out once.
         const int t = tid - 384;
+        constexpr int C = DP / 8, RP = 128 / C, kPasses = kBwdRows / RP;
+        const uint32_t G = p.group, per = kBwdRows / G, c = t % C, fill = (p.d / 8 + 1) & ~1u;
+        const char *qsrc[kPasses], *gsrc[kPasses];
+        uint32_t first[kPasses];                         // query of the pass's row in tile 0; past every T for none
+#pragma unroll
+        for (int k = 0; k < kPasses; ++k) {
+            const uint32_t r = t / C + k * RP, q = r / G, g = r - q * G;
+            const bool on = q < per && c < p.d / 8;
+            first[k] = on ? q : 0x80000000u;
+            qsrc[k] = static_cast<const char *>(p.q) + (on ? ((int64_t)q * p.q_row + (int64_t)(hk * G + g) * p.q_head + c * 8) * 2 : 0);
+            gsrc[k] = static_cast<const char *>(p.dout) + (on ? ((int64_t)q * p.dout_row + (int64_t)(hk * G + g) * p.dout_head + c * 8) * 2 : 0);
+        }
+        const int64_t qstep = (int64_t)per * p.q_row * 2, gstep = (int64_t)per * p.dout_row * 2;
+        const uint32_t to = sm + S::kRow + tc::chunk(t / C, c, 4096);          // passes are whole swizzle periods apart
+        static_assert(RP % 8 == 0, "whole swizzle periods");
+        const char *info = reinterpret_cast<const char *>(static_cast<const RowInfo *>(p.row_info) + (uint64_t)hk * p.row_tiles) + t * 16;
         bool ok = true;
-        for (uint32_t u = 0; u < units && ok; ++u) {
+        for (uint32_t u = 0; u < units; ++u) {
             const uint32_t slot = u % S::kRing;
             if (u >= (uint32_t)S::kRing) ok = __all_sync(~0u, tc::bar_wait(&ctl->row_empty[slot], (u / S::kRing - 1) & 1, gave_up));
             if (!ok) break;
-            const uint32_t at = sm + S::kRow + slot * 2 * S::kRowTile;
-            copy_row_tile<DP>(at, p.q, p.q_row, p.q_head, hk * p.group, u, p, t, 128);
-            copy_row_tile<DP>(at + S::kRowTile, p.dout, p.dout_row, p.dout_head, hk * p.group, u, p, t, 128);
-            if (t < (int)sizeof(RowInfo) / 16)
-                cp16(sm + S::kInfo + slot * (int)sizeof(RowInfo) + t * 16,
-                     reinterpret_cast<const char *>(static_cast<const RowInfo *>(p.row_info) + (uint64_t)hk * p.row_tiles + u) + t * 16, 16);
+            if (c < fill) {
+#pragma unroll
+                for (int k = 0; k < kPasses; ++k) {
+                    const uint32_t n = first[k] + u * per < p.T ? 16 : 0;
+                    cp16(to + slot * 2 * S::kRowTile + k * RP * 128, n ? qsrc[k] : static_cast<const char *>(p.q), n);
+                    cp16(to + slot * 2 * S::kRowTile + S::kRowTile + k * RP * 128, n ? gsrc[k] : static_cast<const char *>(p.dout), n);
+                    qsrc[k] += qstep;
+                    gsrc[k] += gstep;
+                }
+            }
+            if (t < (int)sizeof(RowInfo) / 16) cp16(sm + S::kInfo + slot * (int)sizeof(RowInfo) + t * 16, info + (uint64_t)u * sizeof(RowInfo), 16);
             tc::cp_arrive(&ctl->row_full[slot]);
         }
         cp_commit();
