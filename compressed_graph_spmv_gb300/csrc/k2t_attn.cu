@@ -40,18 +40,20 @@ constexpr uint64_t kSms = 152;
 
 // Blocks that share the nodes of one (head, row tile): as many as make the
 // fewest rounds of the GPU's SMs (one block each) times tiles a block, with
-// two tiles' time for a block's start and end.  For a number of rounds, the
-// most blocks that it holds.
+// two tiles' time for a block's start and end and three (a short kernel) for
+// joining them.  For a number of rounds, the most blocks
+// that it holds.
 uint32_t pick_splits(uint64_t blocks, uint64_t tiles)
 {
     const uint64_t most = std::min<uint64_t>(std::max<uint64_t>(1, tiles), kSms);
     uint64_t best = 1, cost = ~0ull;
     for (uint64_t rounds = (blocks + kSms - 1) / kSms, last = rounds + 8; rounds <= last; ++rounds) {
-        const uint64_t s = std::min(most, rounds * kSms / blocks), c = rounds * ((tiles + s - 1) / s + 2);
+        const uint64_t s = std::min(most, rounds * kSms / blocks), c = rounds * ((tiles + s - 1) / s + 2) + 3;
         if (c < cost) cost = c, best = s;
         if (s == most) break;
     }
-    return (uint32_t)best;
+    const uint64_t alone = (blocks + kSms - 1) / kSms * (tiles + 2);
+    return alone <= cost ? 1 : (uint32_t)best;
 }
 
 struct Plan {
@@ -86,9 +88,9 @@ void make_plan(const k2t_attn *a, bool backward, Plan &pl)
         const uint32_t groups = (p.row_tiles + held - 1) / held;
         p.splits = pick_splits((uint64_t)p.hkv * groups, p.tiles);
         p.hist_parts = p.splits * groups;
-        pl.part_floats = p.splits * rows * p.d;
-        pl.ml_floats = (uint64_t)p.hist_parts * p.hq * p.buckets;
-        pl.info_floats = (uint64_t)p.hkv * p.row_tiles * (sizeof(RowInfo) / 4);
+        pl.part_floats = p.splits > 1 ? p.splits * rows * p.d : 0;
+        pl.ml_floats = p.hist_parts > 1 ? (uint64_t)p.hist_parts * p.hq * p.buckets : 0;
+        pl.info_floats = p.row_tiles <= fused ? 0 : (uint64_t)p.hkv * p.row_tiles * (sizeof(RowInfo) / 4);
         return;
     }
     // rows per block: the fewest lanes that hold them all, since the states are read once per row block

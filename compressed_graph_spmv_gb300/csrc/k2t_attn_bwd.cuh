@@ -249,23 +249,58 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
         for (uint32_t i = tid; i < (p.buckets + 2) * 128; i += kBwdThreads) hist[i] = 0.0f;
     RowInfo *info = reinterpret_cast<RowInfo *>(smem + S::kInfo);
     __syncthreads();
-    if (tid < (int)rts * kBwdRows) {
+    auto seen_by = [&](uint32_t place) {
+        const uint32_t col = (place & 0xffff) / kTcPitch;
+        if (col < p.sources) atomicOr(&ctl->columns, 1u << col);
+        else ctl->all = 1;
+    };
+    if (DKV) {
+        // what attn_rows_kernel does, for the rows that this block holds: eight threads a row
+        for (int at = tid >> 3; at < (int)rts * kBwdRows; at += kBwdThreads / 8) {
+            const uint32_t c = at % kBwdRows, per = kBwdRows / p.group, t = (rt0 + at / kBwdRows) * per + c / p.group, g = c % p.group;
+            const bool on = c < per * p.group && t < p.T;
+            const uint32_t hd = hk * p.group + g;
+            float s = 0.0f;
+            if (on) {
+                const T *o = static_cast<const T *>(p.out) + (int64_t)t * p.out_row + (int64_t)hd * p.out_head;
+                const T *d = static_cast<const T *>(p.dout) + (int64_t)t * p.dout_row + (int64_t)hd * p.dout_head;
+                for (uint32_t x = (tid & 7) * 8; x < p.d; x += 64) {
+                    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(o + x)), b = __ldg(reinterpret_cast<const uint4 *>(d + x));
+                    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 u = Elem<T>::unpack(aw[e]), v = Elem<T>::unpack(bw[e]);
+                        s = fmaf(u.x, v.x, fmaf(u.y, v.y, s));
+                    }
+                }
+            }
+            for (int x = 4; x; x >>= 1) s += __shfl_xor_sync(0xffu << (lane & 24), s, x);
+            if ((tid & 7) == 0) {
+                RowInfo *to = info + at / kBwdRows;
+                float lse = INFINITY;
+                uint32_t place = 0;
+                if (on) {
+                    const float l = p.lse[(uint64_t)t * p.hq + hd];
+                    if (l != -INFINITY) lse = l * kLog2e;
+                    place = row_column(p, t * p.group) * kTcPitch | (g * 4) << 16;
+                    if (p.sources) seen_by(place);
+                }
+                to->lse[c] = lse, to->delta[c] = s, to->place[c] = place;
+            }
+        }
+    } else if (tid < (int)rts * kBwdRows) {
         const RowInfo *from = static_cast<const RowInfo *>(p.row_info) + (uint64_t)hk * p.row_tiles + rt0 + tid / kBwdRows;
         RowInfo *to = info + tid / kBwdRows;
-        const uint32_t c = tid % kBwdRows, place = from->place[c];
+        const uint32_t c = tid % kBwdRows, place = from->place[c], per = kBwdRows / p.group, t = (rt0 + tid / kBwdRows) * per + c / p.group;
         to->lse[c] = from->lse[c], to->delta[c] = from->delta[c], to->place[c] = place;
-        const uint32_t per = kBwdRows / p.group, t = (rt0 + tid / kBwdRows) * per + c / p.group;
-        if (p.sources && c < per * p.group && t < p.T) {
-            const uint32_t col = (place & 0xffff) / kTcPitch;
-            if (col < p.sources) atomicOr(&ctl->columns, 1u << col);
-            else ctl->all = 1;
-        }
+        if (p.sources && c < per * p.group && t < p.T) seen_by(place);
     }
     cp_wait<0>();
     tc::fence_async();
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+    tc::grid_next();
     const uint32_t tm = ctl->tmem;
     volatile uint32_t *gave_up = &ctl->gave_up;
 
@@ -345,8 +380,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
                     const uint32_t q = c / G, t = (rt0 + r) * per + q, hd = hk * G + c - q * G;
-                    if (l < (int)p.d && q < per && t < p.T)
-                        p.part[(((uint64_t)split * p.T + t) * p.hq + hd) * p.d + l] = units > 0 ? __uint_as_float(v[c]) : 0.0f;
+                    if (l < (int)p.d && q < per && t < p.T) {
+                        const float x = units > 0 ? __uint_as_float(v[c]) : 0.0f;
+                        if (p.splits > 1) p.part[(((uint64_t)split * p.T + t) * p.hq + hd) * p.d + l] = x;
+                        else static_cast<T *>(p.dq)[(int64_t)t * p.dq_row + (int64_t)hd * p.dq_head + l] = Elem<T>::from_float(x * p.scale);
+                    }
                 }
             }
         }
@@ -402,7 +440,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
                 for (uint32_t q = 0; q < per; ++q)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) s += hist[(b + 1) * 128 + x * 32 + q * G + g];
-                out[k] = s;
+                if (p.hist_parts > 1) out[k] = s;
+                else static_cast<T *>(p.dbias)[(uint64_t)hk * G * p.buckets + k] = Elem<T>::from_float(s);
             }
         }
     } else {
@@ -649,7 +688,8 @@ template <typename T>
 __global__ void __launch_bounds__(256) attn_bwd_join_kernel(const __grid_constant__ AttnParams p)
 {
     const int tid = threadIdx.x;
-    const uint64_t rows = (uint64_t)p.T * p.hq;
+    tc::grid_wait();
+    const uint64_t rows = p.splits > 1 ? (uint64_t)p.T * p.hq : 0;        // one split: dq is written already
     if (blockIdx.x < rows) {
         const uint64_t row = blockIdx.x;
         __shared__ float4 sum[256];

@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+    tc::grid_next();
     const uint32_t tm = ctl->tmem;                       // S of group w at w * 128, O at 256 + w * DP
     volatile uint32_t *gave_up = &ctl->gave_up;
 
@@ -439,6 +440,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     const uint64_t row = blockIdx.x;             // t * hq + h
     const uint64_t stride = (uint64_t)p.T * p.hq;
     const int tid = threadIdx.x;
+    tc::grid_wait();
     float m = -INFINITY;
     for (uint32_t s = tid; s < p.splits; s += 256) m = fmaxf(m, p.part_ml[(s * stride + row) * 2]);
     for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));

@@ -35,6 +35,23 @@ template <auto kernel> int attn_launch(dim3 grid, int threads, size_t smem, cons
     return K2T_OK;
 }
 
+// A kernel that joins what the one before it on the stream left: its blocks may be set up while that one still runs, and
+// wait for its end (griddepcontrol.wait) before they read.
+template <typename K> int join_launch(K kernel, uint64_t blocks, const AttnParams &p, cudaStream_t st)
+{
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)blocks);
+    c.blockDim = dim3(256);
+    c.stream = st;
+    cudaLaunchAttribute a{};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &a;
+    c.numAttrs = 1;
+    K2T_ATTN_CUDA(cudaLaunchKernelEx(&c, kernel, p));
+    return K2T_OK;
+}
+
 // bm: rows a block takes, 32, 64, 128 or 256.
 template <typename T, int DP, int KW, bool TWO> int forward_tile(const AttnParams &p, cudaStream_t st)
 {
@@ -55,9 +72,7 @@ template <typename T> int launch_forward(const AttnParams &p, int bm, cudaStream
 {
     int rc = p.d <= 64 ? forward_dim<T, 64>(p, bm, st) : forward_dim<T, 128>(p, bm, st);
     if (rc || p.splits == 1) return rc;
-    attn_join_kernel<T><<<(unsigned)((uint64_t)p.T * p.hq), 256, 0, st>>>(p);
-    K2T_ATTN_CUDA(cudaGetLastError());
-    return K2T_OK;
+    return join_launch(attn_join_kernel<T>, (uint64_t)p.T * p.hq, p, st);
 }
 
 // Row tiles that the one-pass kernel holds: 4 of head_dim 64 or less, 2 of more (shared and tensor memory).
@@ -86,16 +101,14 @@ template <typename T, int DP> int backward_dim(const AttnParams &p, cudaStream_t
 
 template <typename T> int launch_backward(const AttnParams &p, cudaStream_t st)
 {
-    attn_rows_kernel<T><<<dim3(p.row_tiles * (kBwdRows / 8), p.hkv), 256, 0, st>>>(p);
-    K2T_ATTN_CUDA(cudaGetLastError());
-    int rc = p.d <= 64 ? backward_dim<T, 64>(p, st) : backward_dim<T, 128>(p, st);
-    if (rc) return rc;
-    const uint64_t blocks = (uint64_t)p.T * p.hq + (uint64_t)p.hq * p.buckets;
-    if (blocks) {
-        attn_bwd_join_kernel<T><<<(unsigned)blocks, 256, 0, st>>>(p);
+    if (p.row_tiles > bwd_fused_tiles(p.d)) {
+        attn_rows_kernel<T><<<dim3(p.row_tiles * (kBwdRows / 8), p.hkv), 256, 0, st>>>(p);
         K2T_ATTN_CUDA(cudaGetLastError());
     }
-    return K2T_OK;
+    int rc = p.d <= 64 ? backward_dim<T, 64>(p, st) : backward_dim<T, 128>(p, st);
+    if (rc) return rc;
+    const uint64_t rows = p.splits > 1 ? (uint64_t)p.T * p.hq : 0, cells = p.hist_parts > 1 ? (uint64_t)p.hq * p.buckets : 0;
+    return rows + cells ? join_launch(attn_bwd_join_kernel<T>, rows + cells, p, st) : K2T_OK;
 }
 
 }  // namespace k2t

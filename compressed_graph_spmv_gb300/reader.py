@@ -40,11 +40,13 @@ def _dtype_code(dtype, allowed):
     return code
 
 
-def _stream(torch, stream):
-    """The stream's address; the current stream's for None."""
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    return _stream_ptr(stream)
+def _stream_getter(torch):
+    """How a call learns the current stream's address: torch's own short way where it has one (a few hundred
+    nanoseconds less than building a stream object, of calls that take microseconds)."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None:
+        return raw
+    return lambda device: torch.cuda.current_stream(device).cuda_stream
 
 
 def _refuse(name, t, shape, dtype, last_only):
@@ -104,11 +106,12 @@ class HopAttention:
         self._rows = torch.Size((n_queries, n_heads, head_dim))
         self._nodes = torch.Size((n_nodes, n_kv_heads, head_dim))
         self._lse = torch.Size((n_queries, n_heads))
-        self._hops = torch.Size((n_nodes, sources))
+        self._hops, self._hops_flat = torch.Size((n_nodes, sources)), torch.Size((n_nodes * sources,))
         self._source = torch.Size((n_queries,))
         self._table = torch.Size((n_heads, len(edges)))
         self._lib = load()
         self._forward, self._backward = self._lib.k2t_attn_forward, self._lib.k2t_attn_backward
+        self._current = _stream_getter(torch)
         self._work, self._bytes, self._at = [None, None], [0, 0], [0, 0]
 
     def work_bytes(self, backward: bool = False) -> int:
@@ -141,7 +144,7 @@ class HopAttention:
         vp, vr, vh = _rows("v", v, self._nodes, dt)
         op, orow, oh = _rows("out", out, self._rows, dt)
         _INPUTS.pack_into(self._buf, _AT_INPUTS, qp, kp, vp, qr, qh, kr, kh, vr, vh,
-                          0 if hops is None else _flat("hops", hops.view(self._hops), self._hops, self._int),
+                          0 if hops is None else _flat("hops", hops, self._hops if hops.ndim == 2 else self._hops_flat, self._int),
                           0 if query_source is None else _flat("query_source", query_source, self._source, self._int),
                           0 if bias is None else _flat("bias", bias, self._table, dt),
                           op, _flat("lse", lse, self._lse, self._float), orow, oh)
@@ -150,7 +153,7 @@ class HopAttention:
         """out [T, n_heads, head_dim] and lse (fp32 [T, n_heads]) of q, k, v."""
         self._inputs(q, k, v, out, lse, hops, bias, query_source)
         work, size = self._work_of(0)
-        rc = self._forward(self._ref, work, size, _stream(self._torch, stream))
+        rc = self._forward(self._ref, work, size, self._current(q.get_device()) if stream is None else _stream_ptr(stream))
         if rc:
             _check("k2t_attn_forward", rc)
         return out, lse
@@ -166,7 +169,7 @@ class HopAttention:
         _GRADIENTS.pack_into(self._buf, _AT_GRADIENTS, *_rows("dout", dout, self._rows, dt), dqp, dkp, dvp, dqr, dqh,
                              dkr, dkh, dvr, dvh, 0 if dbias is None else _flat("dbias", dbias, self._table, dt))
         work, size = self._work_of(1)
-        rc = self._backward(self._ref, work, size, _stream(self._torch, stream))
+        rc = self._backward(self._ref, work, size, self._current(q.get_device()) if stream is None else _stream_ptr(stream))
         if rc:
             _check("k2t_attn_backward", rc)
         return dq, dk, dv, dbias
@@ -192,6 +195,8 @@ class LayerNorm:
         self._buf = memoryview(a).cast("B")
         self._rows, self._cols = torch.Size((n_rows, dim)), torch.Size((dim,))
         self._lib = load()
+        self._forward, self._backward = self._lib.k2t_norm_forward, self._lib.k2t_norm_backward
+        self._current = _stream_getter(torch)
         self.mean = torch.empty(n_rows, dtype=torch.float32, device=device)
         self.rstd = torch.empty(n_rows, dtype=torch.float32, device=device)
         a.mean, a.rstd = self.mean.data_ptr(), self.rstd.data_ptr()
@@ -210,7 +215,7 @@ class LayerNorm:
                            0 if residual is None else _flat("residual", residual, rows, dt),
                            _flat("weight", weight, cols, dt), 0 if bias is None else _flat("bias", bias, cols, dt),
                            _flat("y", y, rows, dt), 0 if z is None else _flat("z", z, rows, dt))
-        rc = self._lib.k2t_norm_forward(self._ref, _stream(self._torch, stream))
+        rc = self._forward(self._ref, self._current(x.get_device()) if stream is None else _stream_ptr(stream))
         if rc:
             _check("k2t_norm_forward", rc)
         return y if z is None else (y, z)
@@ -227,7 +232,8 @@ class LayerNorm:
         if self._work is None:
             self._bytes = self.work_bytes()
             self._work = self._torch.empty(max(16, self._bytes), dtype=self._torch.uint8, device=self.device)
-        rc = self._lib.k2t_norm_backward(self._ref, self._work.data_ptr(), self._bytes, _stream(self._torch, stream))
+        rc = self._backward(self._ref, self._work.data_ptr(), self._bytes,
+                            self._current(dy.get_device()) if stream is None else _stream_ptr(stream))
         if rc:
             _check("k2t_norm_backward", rc)
         return dx, dweight, dbias
