@@ -47,6 +47,7 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
 {
     const uint32_t at = blockIdx.x * 8 + (threadIdx.x >> 5), hk = blockIdx.y;     // row of a tile, padded: a warp each
     if (at >= p.row_tiles * kBwdRows) return;
+    tc::grid_wait();
     const int lane = threadIdx.x & 31;
     const uint32_t G = p.group, per = kBwdRows / G, c = at % kBwdRows, t = at / kBwdRows * per + c / G, g = c % G;
     float lse = INFINITY, s = 0.0f;
@@ -236,6 +237,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
         ctl->gave_up = ctl->columns = ctl->all = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    tc::grid_wait();
     for (uint32_t r = 0; r < rts; ++r) {
         const uint32_t at = sm + S::kRow + r * 2 * S::kRowTile;
         copy_row_tile<DP>(at, p.q, p.q_row, p.q_head, hk * p.group, rt0 + r, p, tid, kBwdThreads);
@@ -551,6 +553,7 @@ __global__ void __launch_bounds__(kBwdRowThreads, 1) attn_bwd_rows_kernel(const 
     }
     if (p.sources)
         for (int i = tid; i < 257; i += kBwdRowThreads) ctl->byte_of[i] = i ? p.bucket_of[i - 1] + 1 : 0;
+    tc::grid_wait();
     fill_bias<T>(lut, p, hk, tid, p.group2);
     __syncthreads();
     if (p.sources) {
@@ -567,6 +570,7 @@ __global__ void __launch_bounds__(kBwdRowThreads, 1) attn_bwd_rows_kernel(const 
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+    tc::grid_next();
     const uint32_t tm = ctl->tmem;
     volatile uint32_t *gave_up = &ctl->gave_up;
 

@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
     }
     if (p.sources)
         for (int i = tid; i < 257; i += kTcThreads) ctl->byte_of[i] = i ? p.bucket_of[i - 1] + 1 : 0;
+    tc::grid_wait();
     fill_bias<T>(lut, p, hk, tid, p.group2);
     {   // queries: lane l of tile w holds row row0 + w * 128 + l % kRows
         constexpr int C = DP / 8;

@@ -19,6 +19,24 @@ constexpr int kAttnMaxSmem = 232448;   // 227 KB
         }                                                \
     } while (0)
 
+// Programmatic launch: a kernel's blocks may be set up while the kernel before it on the stream (whichever that is) still
+// runs; they wait for its end (griddepcontrol.wait) before they touch global memory.
+template <typename K> int next_launch(K kernel, dim3 grid, int threads, size_t smem, const AttnParams &p, cudaStream_t st)
+{
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    cudaLaunchAttribute a{};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &a;
+    c.numAttrs = 1;
+    K2T_ATTN_CUDA(cudaLaunchKernelEx(&c, kernel, p));
+    return K2T_OK;
+}
+
 // The shared memory a kernel may have is a setting of the kernel on a device: raised once, to what any call can need.
 template <auto kernel> int attn_launch(dim3 grid, int threads, size_t smem, const AttnParams &p, cudaStream_t st)
 {
@@ -30,26 +48,7 @@ template <auto kernel> int attn_launch(dim3 grid, int threads, size_t smem, cons
         if (dev < 64) set.fetch_or(1ull << dev);
     }
     if (smem > (size_t)kAttnMaxSmem) return K2T_ERANGE;
-    kernel<<<grid, threads, smem, st>>>(p);
-    K2T_ATTN_CUDA(cudaGetLastError());
-    return K2T_OK;
-}
-
-// A kernel that joins what the one before it on the stream left: its blocks may be set up while that one still runs, and
-// wait for its end (griddepcontrol.wait) before they read.
-template <typename K> int join_launch(K kernel, uint64_t blocks, const AttnParams &p, cudaStream_t st)
-{
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)blocks);
-    c.blockDim = dim3(256);
-    c.stream = st;
-    cudaLaunchAttribute a{};
-    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    a.val.programmaticStreamSerializationAllowed = 1;
-    c.attrs = &a;
-    c.numAttrs = 1;
-    K2T_ATTN_CUDA(cudaLaunchKernelEx(&c, kernel, p));
-    return K2T_OK;
+    return next_launch(kernel, grid, threads, smem, p, st);
 }
 
 // bm: rows a block takes, 32, 64, 128 or 256.
@@ -72,7 +71,7 @@ template <typename T> int launch_forward(const AttnParams &p, int bm, cudaStream
 {
     int rc = p.d <= 64 ? forward_dim<T, 64>(p, bm, st) : forward_dim<T, 128>(p, bm, st);
     if (rc || p.splits == 1) return rc;
-    return join_launch(attn_join_kernel<T>, (uint64_t)p.T * p.hq, p, st);
+    return next_launch(attn_join_kernel<T>, dim3((unsigned)((uint64_t)p.T * p.hq)), 256, 0, p, st);
 }
 
 // Row tiles that the one-pass kernel holds: 4 of head_dim 64 or less, 2 of more (shared and tensor memory).
@@ -102,13 +101,13 @@ template <typename T, int DP> int backward_dim(const AttnParams &p, cudaStream_t
 template <typename T> int launch_backward(const AttnParams &p, cudaStream_t st)
 {
     if (p.row_tiles > bwd_fused_tiles(p.d)) {
-        attn_rows_kernel<T><<<dim3(p.row_tiles * (kBwdRows / 8), p.hkv), 256, 0, st>>>(p);
-        K2T_ATTN_CUDA(cudaGetLastError());
+        int rc = next_launch(attn_rows_kernel<T>, dim3(p.row_tiles * (kBwdRows / 8), p.hkv), 256, 0, p, st);
+        if (rc) return rc;
     }
     int rc = p.d <= 64 ? backward_dim<T, 64>(p, st) : backward_dim<T, 128>(p, st);
     if (rc) return rc;
     const uint64_t rows = p.splits > 1 ? (uint64_t)p.T * p.hq : 0, cells = p.hist_parts > 1 ? (uint64_t)p.hq * p.buckets : 0;
-    return rows + cells ? join_launch(attn_bwd_join_kernel<T>, rows + cells, p, st) : K2T_OK;
+    return rows + cells ? next_launch(attn_bwd_join_kernel<T>, dim3((unsigned)(rows + cells)), 256, 0, p, st) : K2T_OK;
 }
 
 }  // namespace k2t

@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
     __shared__ float2 buf[2 * Gr::kGroups * Gr::kWarps];
     const int tid = threadIdx.x % TPR, group = threadIdx.x / TPR;
     int turn = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     P w[PER], bi[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -294,6 +295,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 || PER > 1 ? 
     // a thread's values go in pairs, one instruction for two; those past the row count as 0
     constexpr int N2 = PER * VEC / 2;
     static_assert(PER * VEC % 2 == 0, "pairs");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float2 w[N2], dw[N2], db[N2];
 #pragma unroll
     for (int e = 0; e < PER * VEC; ++e) {
@@ -385,6 +387,7 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__
     __shared__ float red[32][9];
     const int col = threadIdx.x & 7, g = threadIdx.x >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t which = blockIdx.y, c = blockIdx.x * 8 + col;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float s = 0.0f;
     if (c < p.dim) {
 #pragma unroll 4
@@ -430,10 +433,21 @@ template <typename K> uint32_t norm_resident(K kernel, uint32_t blocks, int thre
     return std::min<uint32_t>(blocks, 152u * per_sm);
 }
 
-template <typename K> int norm_launch(K kernel, uint32_t blocks, int threads, size_t smem, const NormParams &p, cudaStream_t st)
+template <typename K> int norm_launch(K kernel, dim3 grid, int threads, size_t smem, const NormParams &p, cudaStream_t st)
 {
-    kernel<<<blocks, threads, smem, st>>>(p);
-    K2T_NORM_CUDA(cudaGetLastError());
+    // programmatic launch: blocks may be set up while the kernel before them on the stream still runs, and wait for its
+    // end before they touch global memory
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    cudaLaunchAttribute a{};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &a;
+    c.numAttrs = 1;
+    K2T_NORM_CUDA(cudaLaunchKernelEx(&c, kernel, p));
     return K2T_OK;
 }
 
@@ -448,20 +462,18 @@ template <typename T, int VEC, int TPR, int PER, int AHEAD> int run_norm(NormPar
         if (ring > 32 * 1024) K2T_NORM_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring));
         // short blocks even out the SMs: 16 rounds of them 322 us, 2 rounds 357 us on 2^18 x 1024 bf16
         if (AHEAD > 0) blocks = (uint32_t)std::min<uint64_t>((p.n + Gr::kGroups * 4 - 1) / (Gr::kGroups * 4), kNormBlocks * 4);
-        return norm_launch(kernel, blocks, Gr::kThreads, ring, p, st);
+        return norm_launch(kernel, dim3(blocks), Gr::kThreads, ring, p, st);
     }
     if (blocks) {
         const size_t ring = (size_t)Gr::kThreads * RowStream<T, VEC, TPR, PER, 3, AHEAD>::kBytes;
         const size_t sums = Gr::kGroups > 1 ? 2 * p.dim * sizeof(float) : 0;
         const auto kernel = norm_bwd_kernel<T, VEC, TPR, PER, AHEAD>;
         if (AHEAD > 0) blocks = norm_resident(kernel, blocks, Gr::kThreads, std::max(ring, sums));
-        int rc = norm_launch(kernel, blocks, Gr::kThreads, std::max(ring, sums), p, st);
+        int rc = norm_launch(kernel, dim3(blocks), Gr::kThreads, std::max(ring, sums), p, st);
         if (rc) return rc;
     }
     p.parts = blocks;
-    norm_join_kernel<T><<<dim3((p.dim + 7) / 8, p.dbias ? 2 : 1), 1024, 0, st>>>(p);
-    K2T_NORM_CUDA(cudaGetLastError());
-    return K2T_OK;
+    return norm_launch(norm_join_kernel<T>, dim3((p.dim + 7) / 8, p.dbias ? 2 : 1), 1024, 0, p, st);
 }
 
 // Blocks: every SM full of them at most (kNormBlocks).  With more than four rows a group the loads run ahead: measured
