@@ -25,10 +25,11 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC,-O3,-fvisibility=hidden",
           "-I" + os.path.join(ROOT, "include")]
 SOURCES = ["k2t_host.cpp", "k2t_device.cu", "k2t_sr_plus_times.cu", "k2t_sr_boolean.cu", "k2t_sr_min_plus.cu",
-           "k2t_static.cu", "k2t_product.cu", "k2t_attn.cu", "k2t_attn_bf16.cu", "k2t_attn_fp16.cu", "k2t_norm.cu"]
+           "k2t_static.cu", "k2t_product.cu", "k2t_attn.cu", "k2t_attn_bf16.cu", "k2t_attn_fp16.cu", "k2t_norm.cu",
+           "k2t_norm_ragged.cu"]
 PROBE_SOURCES = [os.path.join("probe", "k2t_probe.cu")]
 HEADERS = ["k2t_internal.h", "k2t_kernels.cuh", "k2t_attn.cuh", "k2t_attn_fwd.cuh", "k2t_attn_bwd.cuh",
-           "k2t_attn_launch.cuh", "k2t_tc.cuh", os.path.join("..", "..", "include", "k2t.h")]
+           "k2t_attn_launch.cuh", "k2t_norm.cuh", "k2t_tc.cuh", os.path.join("..", "..", "include", "k2t.h")]
 
 
 def _newest_input(sources) -> float:

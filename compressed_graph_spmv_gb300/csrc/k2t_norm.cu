@@ -9,36 +9,10 @@
 // keep the weight in registers, and in the backward pass sum their rows'
 // terms of dweight and dbias there; each block writes one partial row, and
 // norm_join_kernel adds those in a fixed order.
-#include <algorithm>
-
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "k2t_internal.h"
+#include "k2t_norm.cuh"
 
 namespace k2t {
-
-extern thread_local int g_last_cuda;
-
 namespace {
-
-struct NormParams {
-    uint32_t dim;
-    uint64_t n;
-    float eps, inv_dim;
-    const void *x, *residual, *weight, *bias, *z_in, *dy, *dz;
-    void *y, *z, *dx, *dweight, *dbias;
-    float *mean, *rstd, *part;
-    uint32_t parts;
-};
-
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T> __device__ __forceinline__ T from_f(float v);
-template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
-template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
 // VEC values, moved as one word where VEC fills 16 bytes.
 template <typename T, int VEC> struct alignas(VEC * sizeof(T)) Pack { T v[VEC]; };
@@ -46,22 +20,13 @@ template <typename T, int VEC> struct alignas(VEC * sizeof(T)) Pack { T v[VEC]; 
 template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> load_once(const T *p)
 {
     Pack<T, VEC> r;
-    if constexpr (VEC * sizeof(T) == 16) {
-        *reinterpret_cast<uint4 *>(&r) = __ldcs(reinterpret_cast<const uint4 *>(p));
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) r.v[i] = p[i];
-    }
+    static_assert(sizeof(r) == 16, "whole pieces");
+    *reinterpret_cast<uint4 *>(&r) = __ldcs(reinterpret_cast<const uint4 *>(p));
     return r;
 }
 template <typename T, int VEC> __device__ __forceinline__ void store(T *p, const Pack<T, VEC> &r)
 {
-    if constexpr (VEC * sizeof(T) == 16) {
-        *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(&r);
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) p[i] = r.v[i];
-    }
+    *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(&r);
 }
 
 // Value e of an array of pairs (e is known when compiling), and operations on pairs.
@@ -165,36 +130,6 @@ template <typename T, int VEC, int TPR, int PER, int TENSORS, int AHEAD> struct 
     }
 };
 
-// Threads of a block: groups of TPR, each with a row of its own.
-template <int TPR> struct Group {
-    static constexpr int kThreads = TPR < 256 ? 256 : TPR;
-    static constexpr int kGroups = kThreads / TPR;
-    static constexpr int kWarps = TPR / 32;
-};
-
-// Sums of a and b over the TPR threads of a group.  buf: two alternating
-// buffers, so that one barrier a call is enough.
-template <int TPR>
-__device__ __forceinline__ void group_sum(float &a, float &b, float2 *buf, int group, int &turn)
-{
-#pragma unroll
-    for (int x = 16; x; x >>= 1) {
-        a += __shfl_xor_sync(~0u, a, x);
-        b += __shfl_xor_sync(~0u, b, x);
-    }
-    if constexpr (TPR > 32) {
-        constexpr int W = TPR / 32;
-        float2 *at = buf + (turn * Group<TPR>::kGroups + group) * W;
-        const int tid = threadIdx.x % TPR;
-        if ((tid & 31) == 0) at[tid >> 5] = make_float2(a, b);
-        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
-        a = b = 0.0f;
-#pragma unroll
-        for (int i = 0; i < W; ++i) a += at[i].x, b += at[i].y;
-        turn ^= 1;
-    }
-}
-
 template <typename T, int VEC, int TPR, int PER, int AHEAD>
 __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __grid_constant__ NormParams p)
 {
@@ -234,7 +169,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
                 if (p.residual) r[i] = in.get(row, 1, i);
             }
         }
-        float s = 0.0f, none = 0.0f;
+        float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const uint32_t c = (tid + i * TPR) * VEC;
@@ -250,7 +185,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
             }
         }
         in.taken();
-        group_sum<TPR>(s, none, buf, group, turn);
+        s = group_sum1<TPR>(s, buf, group, turn);
         const float mean = s * p.inv_dim;
         float q = 0.0f;
 #pragma unroll
@@ -264,8 +199,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
                 }
             }
         }
-        none = 0.0f;
-        group_sum<TPR>(q, none, buf, group, turn);
+        q = group_sum1<TPR>(q, buf, group, turn);
         const float rstd = rsqrtf(q * p.inv_dim + p.eps);
         if (tid == 0) p.mean[row] = mean, p.rstd[row] = rstd;
 #pragma unroll
@@ -379,78 +313,6 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 || PER > 1 ? 
     }
 }
 
-// dweight, dbias: 8 columns (one 32-byte sector) a block, 128 threads a column over the partial rows, so that few loads
-// follow one another.
-template <typename T>
-__global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__ NormParams p)
-{
-    __shared__ float red[32][9];
-    const int col = threadIdx.x & 7, g = threadIdx.x >> 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t which = blockIdx.y, c = blockIdx.x * 8 + col;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    float s = 0.0f;
-    if (c < p.dim) {
-#pragma unroll 4
-        for (uint32_t i = g; i < p.parts; i += 128) s += p.part[((uint64_t)i * 2 + which) * p.dim + c];
-    }
-    s += __shfl_xor_sync(~0u, s, 8);
-    s += __shfl_xor_sync(~0u, s, 16);
-    if (lane < 8) red[warp][lane] = s;
-    __syncthreads();
-    if (warp < 8) {
-        s = red[lane][warp];
-#pragma unroll
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
-        const uint32_t at = blockIdx.x * 8 + warp;
-        T *out = static_cast<T *>(which ? p.dbias : p.dweight);
-        if (lane == 0 && at < p.dim && out) out[at] = from_f<T>(s);
-    }
-}
-
-#define K2T_NORM_CUDA(call)                              \
-    do {                                                 \
-        cudaError_t e_ = (call);                         \
-        if (e_ != cudaSuccess) {                         \
-            g_last_cuda = (int)e_;                       \
-            return K2T_ECUDA;                            \
-        }                                                \
-    } while (0)
-
-constexpr uint32_t kNormBlocks = 152 * 8;   // blocks of a full GPU: eight of 256 threads an SM
-
-uint32_t norm_parts(uint64_t n, int groups)
-{
-    return (uint32_t)std::min<uint64_t>((n + groups - 1) / groups, kNormBlocks);
-}
-
-// Backward blocks: as many as the GPU runs at once, and no more than `blocks`; each writes a partial row of the
-// weight's gradient, so that more of them cost more than they even out (445 us against 458 us with twice as many).
-template <typename K> uint32_t norm_resident(K kernel, uint32_t blocks, int threads, size_t smem)
-{
-    int per_sm = 0;
-    if (smem > 32 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1) per_sm = 1;
-    return std::min<uint32_t>(blocks, 152u * per_sm);
-}
-
-template <typename K> int norm_launch(K kernel, dim3 grid, int threads, size_t smem, const NormParams &p, cudaStream_t st)
-{
-    // programmatic launch: blocks may be set up while the kernel before them on the stream still runs, and wait for its
-    // end before they touch global memory
-    cudaLaunchConfig_t c{};
-    c.gridDim = grid;
-    c.blockDim = dim3(threads);
-    c.dynamicSmemBytes = smem;
-    c.stream = st;
-    cudaLaunchAttribute a{};
-    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    a.val.programmaticStreamSerializationAllowed = 1;
-    c.attrs = &a;
-    c.numAttrs = 1;
-    K2T_NORM_CUDA(cudaLaunchKernelEx(&c, kernel, p));
-    return K2T_OK;
-}
-
 // AHEAD: rows asked for ahead where blocks stay for several (0: a row's loads wait for its turn, less to set up).
 template <typename T, int VEC, int TPR, int PER, int AHEAD> int run_norm(NormParams &p, uint32_t blocks, bool backward, cudaStream_t st)
 {
@@ -462,23 +324,23 @@ template <typename T, int VEC, int TPR, int PER, int AHEAD> int run_norm(NormPar
         if (ring > 32 * 1024) K2T_NORM_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring));
         // short blocks even out the SMs: 16 rounds of them 322 us, 2 rounds 357 us on 2^18 x 1024 bf16
         if (AHEAD > 0) blocks = (uint32_t)std::min<uint64_t>((p.n + Gr::kGroups * 4 - 1) / (Gr::kGroups * 4), kNormBlocks * 4);
-        return norm_launch(kernel, dim3(blocks), Gr::kThreads, ring, p, st);
+        return norm_launch(kernel, dim3(blocks), Gr::kThreads, ring, st, p);
     }
     if (blocks) {
         const size_t ring = (size_t)Gr::kThreads * RowStream<T, VEC, TPR, PER, 3, AHEAD>::kBytes;
         const size_t sums = Gr::kGroups > 1 ? 2 * p.dim * sizeof(float) : 0;
         const auto kernel = norm_bwd_kernel<T, VEC, TPR, PER, AHEAD>;
         if (AHEAD > 0) blocks = norm_resident(kernel, blocks, Gr::kThreads, std::max(ring, sums));
-        int rc = norm_launch(kernel, dim3(blocks), Gr::kThreads, std::max(ring, sums), p, st);
+        int rc = norm_launch(kernel, dim3(blocks), Gr::kThreads, std::max(ring, sums), st, p);
         if (rc) return rc;
     }
     p.parts = blocks;
-    return norm_launch(norm_join_kernel<T>, dim3((p.dim + 7) / 8, p.dbias ? 2 : 1), 1024, 0, p, st);
+    return norm_launch(norm_join_kernel<T>, dim3((p.dim + 7) / 8, p.dbias ? 2 : 1), 1024, 0, st, p);
 }
 
 // Blocks: every SM full of them at most (kNormBlocks).  With more than four rows a group the loads run ahead: measured
 // on 2^20 x 512 and 2^18 x 1024 bf16 against a row's own loads; below that there is little to run ahead of.
-template <typename T, int VEC, int TPR, int PER, int AHEAD> int plan_norm(NormParams &p, bool backward, cudaStream_t st)
+template <typename T, int VEC, int TPR, int PER, int AHEAD> int plan_norm(NormParams &p, const bool backward, cudaStream_t st)
 {
     constexpr int G = Group<TPR>::kGroups;
     const uint32_t blocks = norm_parts(p.n, G);
@@ -488,26 +350,31 @@ template <typename T, int VEC, int TPR, int PER, int AHEAD> int plan_norm(NormPa
     return run_norm<T, VEC, TPR, PER, 0>(p, blocks, backward, st);
 }
 
-// Threads a row: as few as hold it with one load each, up to a block, then
-// more loads a thread.  Rows whose pitch is no multiple of 16 bytes (or whose
-// tensors are not 16-byte aligned) move value by value.
-template <typename T> int norm_dispatch(NormParams &p, bool vec, bool backward, cudaStream_t st)
+// Threads a row: as few as hold it, up to a block, then more loads a thread.
+// Forward with two pieces a thread (2^17 x 2048 bf16: 248 us, one piece 261),
+// backward with one, which leaves registers for more rows at once (2^18 x 1024
+// bf16: 400 us, two pieces 485).
+template <typename T> int norm_dispatch(NormParams &p, bool backward, cudaStream_t st)
 {
-    if (vec) {
-        constexpr int V = 16 / sizeof(T);
-        const uint32_t c = p.dim / V;
-        if (c <= 32) return plan_norm<T, V, 32, 1, 4>(p, backward, st);
-        if (c <= 64) return plan_norm<T, V, 64, 1, 4>(p, backward, st);
-        if (c <= 128) return plan_norm<T, V, 128, 1, 4>(p, backward, st);
-        if (c <= 256) return plan_norm<T, V, 256, 1, 4>(p, backward, st);
-        if (c <= 512) return plan_norm<T, V, 256, 2, 2>(p, backward, st);
-        if (c <= 1024) return plan_norm<T, V, 512, 2, 2>(p, backward, st);
-        return plan_norm<T, V, 512, 8, 0>(p, backward, st);
+    constexpr int V = 16 / sizeof(T);
+    const uint32_t c = p.dim / V;
+    if (backward) {
+        if (c <= 8) return plan_norm<T, V, 8, 1, 4>(p, true, st);
+        if (c <= 16) return plan_norm<T, V, 16, 1, 4>(p, true, st);
+        if (c <= 32) return plan_norm<T, V, 32, 1, 4>(p, true, st);
+        if (c <= 64) return plan_norm<T, V, 64, 1, 4>(p, true, st);
+        if (c <= 128) return plan_norm<T, V, 128, 1, 4>(p, true, st);
+        if (c <= 256) return plan_norm<T, V, 256, 1, 4>(p, true, st);
+    } else {
+        if (c <= 16) return plan_norm<T, V, 8, 2, 4>(p, false, st);
+        if (c <= 32) return plan_norm<T, V, 16, 2, 4>(p, false, st);
+        if (c <= 64) return plan_norm<T, V, 32, 2, 4>(p, false, st);
+        if (c <= 128) return plan_norm<T, V, 64, 2, 4>(p, false, st);
+        if (c <= 256) return plan_norm<T, V, 128, 2, 4>(p, false, st);
     }
-    if (p.dim <= 128) return plan_norm<T, 1, 32, 4, 0>(p, backward, st);
-    if (p.dim <= 512) return plan_norm<T, 1, 128, 4, 0>(p, backward, st);
-    if (p.dim <= 2048) return plan_norm<T, 1, 256, 8, 0>(p, backward, st);
-    return plan_norm<T, 1, 512, 32, 0>(p, backward, st);
+    if (c <= 512) return plan_norm<T, V, 256, 2, 2>(p, backward, st);
+    if (c <= 1024) return plan_norm<T, V, 512, 2, 2>(p, backward, st);
+    return plan_norm<T, V, 512, 8, 0>(p, backward, st);
 }
 
 int check_norm(const k2t_norm *a)
@@ -534,9 +401,10 @@ int dispatch(const k2t_norm *a, NormParams &p, bool backward, cudaStream_t st)
     p.weight = a->weight;
     p.mean = a->mean;
     p.rstd = a->rstd;
-    if (a->dtype == K2T_BF16) return norm_dispatch<__nv_bfloat16>(p, vec, backward, st);
-    if (a->dtype == K2T_FP16) return norm_dispatch<__half>(p, vec, backward, st);
-    return norm_dispatch<float>(p, vec, backward, st);
+    if (!vec) return norm_ragged(p, a->dtype, backward, st);
+    if (a->dtype == K2T_BF16) return norm_dispatch<__nv_bfloat16>(p, backward, st);
+    if (a->dtype == K2T_FP16) return norm_dispatch<__half>(p, backward, st);
+    return norm_dispatch<float>(p, backward, st);
 }
 
 }  // namespace

@@ -332,7 +332,8 @@ def test_norm_matches(n, dim, dtype, residual):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("n,dim", [(40001, 64), (39999, 200), (20001, 512), (9800, 1000), (5001, 2048), (4990, 4096)])
+@pytest.mark.parametrize("n,dim", [(40001, 64), (39999, 200), (20001, 512), (9800, 1000), (5001, 2048), (4990, 4096),
+                                   (40001, 63), (30011, 201), (20011, 333), (10007, 777), (6011, 1999), (3001, 4095)])
 def test_norm_of_many_rows(n, dim, dtype):
     """Enough rows that blocks stay for several and load ahead."""
     check_norm(n, dim, dtype, True)
