@@ -14,19 +14,20 @@
 namespace k2t {
 namespace {
 
-// VEC values, moved as one word where VEC fills 16 bytes.
+// VEC values, which fill 16 bytes, or a single one.
 template <typename T, int VEC> struct alignas(VEC * sizeof(T)) Pack { T v[VEC]; };
 
 template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> load_once(const T *p)
 {
     Pack<T, VEC> r;
-    static_assert(sizeof(r) == 16, "whole pieces");
-    *reinterpret_cast<uint4 *>(&r) = __ldcs(reinterpret_cast<const uint4 *>(p));
+    if constexpr (VEC == 1) r.v[0] = *p;
+    else *reinterpret_cast<uint4 *>(&r) = __ldcs(reinterpret_cast<const uint4 *>(p));
     return r;
 }
 template <typename T, int VEC> __device__ __forceinline__ void store(T *p, const Pack<T, VEC> &r)
 {
-    *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(&r);
+    if constexpr (VEC == 1) *p = r.v[0];
+    else *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(&r);
 }
 
 // Value e of an array of pairs (e is known when compiling), and operations on pairs.
@@ -354,8 +355,13 @@ template <typename T, int VEC, int TPR, int PER, int AHEAD> int plan_norm(NormPa
 // Forward with two pieces a thread (2^17 x 2048 bf16: 248 us, one piece 261),
 // backward with one, which leaves registers for more rows at once (2^18 x 1024
 // bf16: 400 us, two pieces 485).
-template <typename T> int norm_dispatch(NormParams &p, bool backward, cudaStream_t st)
+template <typename T> int norm_dispatch(NormParams &p, bool vec, bool backward, cudaStream_t st)
 {
+    if (!vec) {
+        if (p.dim <= 128) return plan_norm<T, 1, 32, 4, 0>(p, backward, st);
+        if (p.dim <= 512) return plan_norm<T, 1, 128, 4, 0>(p, backward, st);
+        return plan_norm<T, 1, 256, 8, 0>(p, backward, st);
+    }
     constexpr int V = 16 / sizeof(T);
     const uint32_t c = p.dim / V;
     if (backward) {
@@ -401,10 +407,13 @@ int dispatch(const k2t_norm *a, NormParams &p, bool backward, cudaStream_t st)
     p.weight = a->weight;
     p.mean = a->mean;
     p.rstd = a->rstd;
-    if (!vec) return norm_ragged(p, a->dtype, backward, st);
-    if (a->dtype == K2T_BF16) return norm_dispatch<__nv_bfloat16>(p, backward, st);
-    if (a->dtype == K2T_FP16) return norm_dispatch<__half>(p, backward, st);
-    return norm_dispatch<float>(p, backward, st);
+    // Rows that are not whole pieces: value by value while there are few of them, when a call is its latency (4999 x 333
+    // fp32, training: 15 us against 20), else in stretches (200000 x 333 bf16, forward: 170 us against 220; 65536 x 3999:
+    // 610 us against 2335).
+    if (!vec && (a->n_rows > 16384 || a->dim > 2048)) return norm_ragged(p, a->dtype, backward, st);
+    if (a->dtype == K2T_BF16) return norm_dispatch<__nv_bfloat16>(p, vec, backward, st);
+    if (a->dtype == K2T_FP16) return norm_dispatch<__half>(p, vec, backward, st);
+    return norm_dispatch<float>(p, vec, backward, st);
 }
 
 }  // namespace

@@ -14,8 +14,7 @@
 namespace k2t {
 namespace {
 
-constexpr uint32_t kBatchBytes = 16384;      // of one tensor, or a little more
-constexpr int kRaggedThreads = 256;
+constexpr uint32_t kBlockBytes = 73728;      // two batches of every tensor, about: three blocks an SM
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src)
 {
@@ -34,7 +33,7 @@ struct Stretch {
     }
     // whole pieces come from inside the tensor or share their 16 bytes with its first or last value: the ends are
     // copied value by value instead, so that nothing outside the tensor is read
-    template <typename T> __device__ __forceinline__ void bring(uint8_t *image, int tid) const
+    template <typename T, int kRaggedThreads> __device__ __forceinline__ void bring(uint8_t *image, int tid) const
     {
         const uint32_t s = (uint32_t)__cvta_generic_to_shared(image);
         const uint32_t lo = (skew + 15) / 16, hi = (skew + bytes) / 16;
@@ -45,7 +44,7 @@ struct Stretch {
         for (uint32_t b = tail + tid * sizeof(T); b < bytes; b += kRaggedThreads * sizeof(T))
             *reinterpret_cast<T *>(image + skew + b) = *reinterpret_cast<const T *>(at + b);
     }
-    template <typename T> __device__ __forceinline__ void leave(const uint8_t *image, int tid) const
+    template <typename T, int kRaggedThreads> __device__ __forceinline__ void leave(const uint8_t *image, int tid) const
     {
         char *to = const_cast<char *>(at);
         const uint32_t lo = (skew + 15) / 16, hi = (skew + bytes) / 16;
@@ -61,10 +60,14 @@ struct Stretch {
 
 // Rows of a batch (as many for every group, where that is not too much), and bytes of an image.
 struct Batch { uint32_t rows, image; };
-inline Batch batch_of(uint32_t dim, size_t size, uint32_t groups)
+inline Batch batch_of(uint64_t n, uint32_t dim, size_t size, uint32_t groups, uint32_t tensors)
 {
+    const uint32_t target = std::min<uint32_t>(16384, kBlockBytes / 2 / tensors);
     const uint32_t row = dim * (uint32_t)size, turn = groups * row;
-    const uint32_t rows = turn <= 24576 ? groups * std::max<uint32_t>(1, kBatchBytes / turn) : std::max<uint32_t>(1, kBatchBytes / row);
+    uint32_t rows = turn <= target * 3 / 2 ? groups * std::max<uint32_t>(1, target / turn) : std::max<uint32_t>(1, target / row);
+    // few rows: a batch for every block before a block has two
+    const uint64_t each = (n + (uint64_t)groups * kNormBlocks - 1) / ((uint64_t)groups * kNormBlocks) * groups;
+    if (each < rows) rows = (uint32_t)each;
     return {rows, (rows * row + 31 + 15) / 16 * 16};
 }
 
@@ -72,7 +75,7 @@ inline Batch batch_of(uint32_t dim, size_t size, uint32_t groups)
 __device__ __forceinline__ bool same_skew(const void *a, const void *b) { return (((uintptr_t)a ^ (uintptr_t)b) & 15) == 0; }
 
 template <typename T, int TPR, int PER>
-__global__ void __launch_bounds__(kRaggedThreads) ragged_fwd_kernel(const __grid_constant__ NormParams p, uint32_t rows, uint32_t image, int images)
+__global__ void __launch_bounds__(Group<TPR>::kThreads) ragged_fwd_kernel(const __grid_constant__ NormParams p, uint32_t rows, uint32_t image, int images)
 {
     using Gr = Group<TPR>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -98,8 +101,8 @@ __global__ void __launch_bounds__(kRaggedThreads) ragged_fwd_kernel(const __grid
         const uint64_t r = row0 + (next ? step : 0), o = off + (next ? step_bytes : 0);
         if (r < p.n) {
             const uint32_t bytes = (uint32_t)min((uint64_t)rows, p.n - r) * row_bytes;
-            Stretch(p.x, o, bytes).template bring<T>(at(slot, 0), tid);
-            if (p.residual) Stretch(p.residual, o, bytes).template bring<T>(at(slot, 1), tid);
+            Stretch(p.x, o, bytes).template bring<T, Gr::kThreads>(at(slot, 0), tid);
+            if (p.residual) Stretch(p.residual, o, bytes).template bring<T, Gr::kThreads>(at(slot, 1), tid);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -155,8 +158,8 @@ __global__ void __launch_bounds__(kRaggedThreads) ragged_fwd_kernel(const __grid
             }
         }
         __syncthreads();
-        if (y_over) stretch(p.y).template leave<T>(at(slot, 0), tid);
-        if (z_over) stretch(p.z).template leave<T>(at(slot, 1), tid);
+        if (y_over) stretch(p.y).template leave<T, Gr::kThreads>(at(slot, 0), tid);
+        if (z_over) stretch(p.z).template leave<T, Gr::kThreads>(at(slot, 1), tid);
         if (images > 1) slot ^= 1;
         else {
             __syncthreads();
@@ -166,7 +169,7 @@ __global__ void __launch_bounds__(kRaggedThreads) ragged_fwd_kernel(const __grid
 }
 
 template <typename T, int TPR, int PER>
-__global__ void __launch_bounds__(kRaggedThreads) ragged_bwd_kernel(const __grid_constant__ NormParams p, uint32_t rows, uint32_t image, int images)
+__global__ void __launch_bounds__(Group<TPR>::kThreads) ragged_bwd_kernel(const __grid_constant__ NormParams p, uint32_t rows, uint32_t image, int images)
 {
     using Gr = Group<TPR>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -192,9 +195,9 @@ __global__ void __launch_bounds__(kRaggedThreads) ragged_bwd_kernel(const __grid
         const uint64_t r = row0 + (next ? step : 0), o = off + (next ? step_bytes : 0);
         if (r < p.n) {
             const uint32_t bytes = (uint32_t)min((uint64_t)rows, p.n - r) * row_bytes;
-            Stretch(p.z_in, o, bytes).template bring<T>(at(slot, 0), tid);
-            Stretch(p.dy, o, bytes).template bring<T>(at(slot, 1), tid);
-            if (p.dz) Stretch(p.dz, o, bytes).template bring<T>(at(slot, 2), tid);
+            Stretch(p.z_in, o, bytes).template bring<T, Gr::kThreads>(at(slot, 0), tid);
+            Stretch(p.dy, o, bytes).template bring<T, Gr::kThreads>(at(slot, 1), tid);
+            if (p.dz) Stretch(p.dz, o, bytes).template bring<T, Gr::kThreads>(at(slot, 2), tid);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__(kRaggedThreads) ragged_bwd_kernel(const __grid
             }
         }
         __syncthreads();
-        if (over) stretch(p.dx).template leave<T>(at(slot, 1), tid);
+        if (over) stretch(p.dx).template leave<T, Gr::kThreads>(at(slot, 1), tid);
         if (images > 1) slot ^= 1;
         else {
             __syncthreads();
@@ -273,24 +276,25 @@ constexpr size_t kRaggedSmem = 225 * 1024;     // of the 227 KB a block may have
 
 template <typename T, int TPR, int PER> int run_ragged(NormParams &p, bool backward, cudaStream_t st)
 {
-    const Batch b = batch_of(p.dim, sizeof(T), Group<TPR>::kGroups);
     const size_t tensors = backward ? (p.dz ? 3 : 2) : p.residual ? 2 : 1;
+    const Batch b = batch_of(p.n, p.dim, sizeof(T), Group<TPR>::kGroups, (uint32_t)tensors);
     const int images = 2 * tensors * b.image <= kRaggedSmem ? 2 : 1;
     const size_t smem = std::max<size_t>(images * tensors * b.image, backward ? 2 * p.dim * sizeof(float) : 0);
     uint32_t blocks = (uint32_t)std::min<uint64_t>((p.n + b.rows - 1) / b.rows, kNormBlocks);
     auto launch = [&](auto kernel) -> int {
         // as many as run at once: blocks stay, and their copies run ahead
-        blocks = norm_resident(kernel, blocks, kRaggedThreads, smem);
+        blocks = norm_resident(kernel, blocks, Group<TPR>::kThreads, smem);
         p.parts = blocks;
         if (!blocks) return K2T_OK;
-        return norm_launch(kernel, dim3(blocks), kRaggedThreads, smem, st, p, b.rows, b.image, images);
+        return norm_launch(kernel, dim3(blocks), Group<TPR>::kThreads, smem, st, p, b.rows, b.image, images);
     };
     if (!backward) return launch(ragged_fwd_kernel<T, TPR, PER>);
     int rc = launch(ragged_bwd_kernel<T, TPR, PER>);
     return rc ? rc : norm_launch(norm_join_kernel<T>, dim3((p.dim + 7) / 8, p.dbias ? 2 : 1), 1024, 0, st, p);
 }
 
-// Threads a row: as few as hold it with eight values each, up to a block, then more values a thread.
+// Threads a row: eight values a thread, up to a block, then more.  (200000 x 333 bf16 forward: 8 values 148 us, 16 values
+// 171 us.)
 template <typename T> int ragged_dim(NormParams &p, bool backward, cudaStream_t st)
 {
     if (p.dim <= 64) return run_ragged<T, 8, 8>(p, backward, st);
