@@ -395,3 +395,14 @@ def test_norm_rows_that_hold_no_number():
     pkg.LayerNorm(10, 96, torch.float32).forward(x, w, b, y)
     fine = [i for i in range(10) if i not in (3, 7)]
     assert torch.isfinite(y[fine]).all() and torch.isnan(y[3]).all()
+
+
+def test_example_runs_them_together():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "read_graph.py")
+    spec = importlib.util.spec_from_file_location("read_graph", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    losses, dx = m.read_graph(scale=10, edges=6000, steps=20, say=lambda *_: None)
+    assert losses[-1] < 0.9 * losses[0] and torch.isfinite(dx.float()).all()
