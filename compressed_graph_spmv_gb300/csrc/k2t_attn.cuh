@@ -146,74 +146,97 @@ template <int SLOTS> __device__ __forceinline__ uint32_t slot_use(uint32_t item)
     return SLOTS == 3 ? (item & 1 ? item >> 1 : item >> 2) : item / SLOTS;
 }
 
-// Hops of nodes [32 hw, 32 hw + 32) of a tile -> bucket bytes.  Lane = (column, part): W lanes (a power of two, at
-// least n_sources) side by side read a node's columns, and 32 / W parts take W nodes each, one after another.
+// Hops of nodes [32 hw, 32 hw + 32) of a tile -> bucket bytes, and which of those nodes a column in use sees.  W lanes
+// side by side (a power of two, at least n_sources; a quarter of that where four columns come in one load) read a node's
+// columns, and the other lanes the nodes after those that the first ones take one after another.  The loads of a tile
+// are in flight while the tile before is turned into bytes.  Four columns a load halve the instructions: of few rows and
+// many columns these warps set the pace (32 queries over 2^18 nodes, head_dim 64: 2400 clocks a tile before).
 template <int BUFS, typename Ctl>
 __device__ __forceinline__ void hop_warps(const AttnParams &p, Ctl *ctl, uint8_t *buckets, int hw, int lane, uint32_t tiles,
                                           uint64_t tile0, volatile uint32_t *gave_up)
 {
     const uint32_t cols = ctl->columns, B = p.sources;
-    const bool all = ctl->all || !B;
+    const bool all = ctl->all || !B, four = B && (B & 3) == 0 && ((uintptr_t)p.hops & 15) == 0;
     uint32_t W = 1;
     while (W < B) W *= 2;
-    const uint32_t col = lane & (W - 1), first = lane & ~(W - 1);      // first node of this lane's part
-    const bool on = col < B, used = on && ((cols >> col) & 1);
-    // The loads of a tile are in flight while the tile before is turned into bytes: 16 nodes of the part at a time, a
-    // set of registers each.
-    int32_t ha[16], hb[16];
-    auto hops_in = [&](int32_t (&h)[16], uint32_t t, uint32_t k) {
-        const uint64_t node = (tile0 + (uint64_t)t * p.splits) * kTcTile + hw * 32 + first + k;
+    const uint32_t Q = four ? W / 4 : W;                                // lanes of a node, and nodes of a lane
+    const uint32_t col = (lane & (Q - 1)) * (four ? 4 : 1), first = lane & ~(Q - 1);
+    const bool on = col < B;
+    uint32_t unused[4];                                                // all ones where a column does not count
+#pragma unroll
+    for (int j = 0; j < 4; ++j) unused[j] = col + j < 32 && ((cols >> (col + j)) & 1) ? 0u : ~0u;
+    int32_t h[32];       // four columns of 8 nodes, or one column of 32; those past a lane's part stay masked
+#pragma unroll
+    for (int e = 0; e < 32; ++e) h[e] = -1;
+    auto hops_in = [&](uint32_t t) {
+        const uint64_t node = (tile0 + (uint64_t)t * p.splits) * kTcTile + hw * 32 + first;
         const int32_t *at = p.hops + node * B + col;
-        const uint32_t left = t < tiles && on && node < p.n ? (uint32_t)min((uint64_t)(W - k), p.n - node) : 0;
+        const uint32_t left = t < tiles && on && node < p.n ? (uint32_t)min((uint64_t)Q, p.n - node) : 0;
+        if (four) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            h[e] = -1;
-            if (e < (int)left) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(h[e]) : "l"(at));
-            at += B;
-        }
-    };
-    auto hops_out = [&](const int32_t (&h)[16], uint8_t *to) {       // bytes of up to 16 nodes; returns which are seen
-        uint32_t unseen = 0;
+            for (int e = 0; e < 8; ++e) {
+                int4 x = make_int4(-1, -1, -1, -1);
+                if (e < (int)left) asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(at));
+                h[4 * e] = x.x, h[4 * e + 1] = x.y, h[4 * e + 2] = x.z, h[4 * e + 3] = x.w;
+                at += B;
+            }
+        } else {
 #pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-            if (e >= (int)W) break;
-            uint32_t b = 0;
-#pragma unroll
-            for (int y = 3; y >= 0; --y) b = b << 8 | ctl->byte_of[min(h[e + y] + 1, 256)];
-            if (on) {
-                if (W >= 4) *reinterpret_cast<uint32_t *>(to + e) = b;
-                else {
-                    to[0] = b;
-                    if (W == 2) to[1] = b >> 8;
-                }
+            for (int e = 0; e < 32; ++e) {
+                if (e >= (int)Q) break;
+                h[e] = -1;
+                if (e < (int)left) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(h[e]) : "l"(at));
+                at += B;
             }
         }
-#pragma unroll
-        for (int e = 15; e >= 0; --e) unseen = __funnelshift_l(h[e], unseen, 1);      // a negative hop count's sign
-        return ~unseen & 0xffff;
     };
-    if (B) {
-        hops_in(ha, 0, 0);
-        if (W > 16) hops_in(hb, 0, 16);
-    }
+    // any int32 may stand in the table: clamped to [-1, 255] before it becomes an index
+    auto byte = [&](int32_t x) -> uint32_t { return ctl->byte_of[__viaddmax_s32(min(x, 255), 1, 0)]; };
+    auto put = [&](uint8_t *to, uint32_t nodes, uint32_t b) {           // the bytes of up to 4 nodes of a column
+        if (nodes >= 4) *reinterpret_cast<uint32_t *>(to) = b;
+        else if (nodes == 2) *reinterpret_cast<uint16_t *>(to) = (uint16_t)b;
+        else *to = (uint8_t)b;
+    };
+    if (B) hops_in(0);
     for (uint32_t t = 0; t < tiles; ++t) {
         const uint32_t buf = t % BUFS;
         if (t >= BUFS && !__all_sync(~0u, tc::bar_wait(&ctl->hop_empty[buf], (t / BUFS - 1) & 1, gave_up))) break;
-        uint8_t *bt = buckets + buf * 33 * kTcPitch + hw * 32;
+        uint8_t *bt = buckets + buf * 33 * kTcPitch + hw * 32, *to = bt + col * kTcPitch + first;
         const uint64_t node0 = (tile0 + (uint64_t)t * p.splits) * kTcTile + hw * 32;
-        uint32_t mask = 0;                                             // nodes that this lane's column sees
-        if (B) {
-            mask = hops_out(ha, bt + col * kTcPitch + first);
-            hops_in(ha, t + 1, 0);
-            if (W > 16) {
-                mask |= hops_out(hb, bt + col * kTcPitch + first + 16) << 16;
-                hops_in(hb, t + 1, 16);
+        uint32_t unseen = 0;                                           // bit e: this lane's columns do not see its node e
+        if (four) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+                if (e && Q <= 4) break;
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = (byte(h[4 * e + 12 + j]) * 256 + byte(h[4 * e + 8 + j])) * 65536 + byte(h[4 * e + 4 + j]) * 256 + byte(h[4 * e + j]);
+                if (on) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) put(to + j * kTcPitch + e, Q, w[j]);
+                }
             }
-            mask = used ? mask << first : 0;
+#pragma unroll
+            for (int e = 7; e >= 0; --e) {
+                const int32_t m = max(max(h[4 * e] | (int)unused[0], h[4 * e + 1] | (int)unused[1]), max(h[4 * e + 2] | (int)unused[2], h[4 * e + 3] | (int)unused[3]));
+                unseen = __funnelshift_l(m, unseen, 1);                // a negative hop count's sign
+            }
+        } else if (B) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+                if (e >= (int)Q) break;
+                const uint32_t w = (byte(h[e + 3]) * 256 + byte(h[e + 2])) * 65536 + byte(h[e + 1]) * 256 + byte(h[e]);
+                if (on) put(to + e, Q, w);
+            }
+#pragma unroll
+            for (int e = 31; e >= 0; --e) unseen = __funnelshift_l(e < (int)Q ? h[e] | (int)unused[0] : -1, unseen, 1);
         }
+        if (B) hops_in(t + 1);
+        const uint32_t mine = Q >= 32 ? ~0u : (1u << Q) - 1, sees = on ? (~unseen & mine) << first : 0;
         const bool in = node0 + lane < p.n;
         bt[B * kTcPitch + lane] = in ? p.buckets + 1 : 0;
-        const uint32_t inside = __ballot_sync(~0u, in), seen = (all ? ~0u : __reduce_or_sync(~0u, mask)) & inside;
+        const uint32_t inside = __ballot_sync(~0u, in), seen = (all ? ~0u : __reduce_or_sync(~0u, sees)) & inside;
         __syncwarp();
         if (lane == 0) {
             ctl->seen[buf][hw] = seen;

@@ -217,6 +217,18 @@ def test_unseen_nodes_may_hold_anything(T):
     assert (got["dk"][hidden] == 0).all() and (got["dv"][hidden] == 0).all()
 
 
+@pytest.mark.parametrize("T,sources", [(5, 5), (8, 8), (32, 32), (40, 20)])
+def test_hops_of_any_value(T, sources):
+    """Every negative number masks, every large one falls into the last bucket."""
+    p = problem(T, 700, 2, 1, 64, sources, 6, "bf16", T > 32, seed=43)
+    odd = torch.tensor([-(1 << 31), -(1 << 31) + 1, -1000, -257, -256, -2, (1 << 31) - 1, (1 << 31) - 2, 65536, 257, 256, 255, 254],
+                       dtype=torch.int32, device="cuda")
+    where = torch.rand(p["hops"].shape, device="cuda") < 0.5
+    pick = odd[torch.randint(0, odd.numel(), p["hops"].shape, device="cuda")]
+    p["hops"] = torch.where(where, pick, p["hops"]).contiguous()
+    check(p, "bf16", run(p, "bf16"))
+
+
 def test_lengths_of_zero():
     p = problem(3, 0, 4, 2, 64, 3, 4, "bf16", False, seed=1)
     got = run(p, "bf16")
