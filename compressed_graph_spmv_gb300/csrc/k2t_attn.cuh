@@ -150,7 +150,8 @@ template <int SLOTS> __device__ __forceinline__ uint32_t slot_use(uint32_t item)
 // side by side (a power of two, at least n_sources; a quarter of that where four columns come in one load) read a node's
 // columns, and the other lanes the nodes after those that the first ones take one after another.  The loads of a tile
 // are in flight while the tile before is turned into bytes.  Four columns a load halve the instructions: of few rows and
-// many columns these warps set the pace (32 queries over 2^18 nodes, head_dim 64: 2400 clocks a tile before).
+// many columns these warps set the pace (32 queries over 2^18 nodes, head_dim 64: 2400 clocks a tile before).  Other
+// numbers of columns go 16 nodes at a time in a rolled loop: code that is not fetched is what a short call waits least for.
 template <int BUFS, typename Ctl>
 __device__ __forceinline__ void hop_warps(const AttnParams &p, Ctl *ctl, uint8_t *buckets, int hw, int lane, uint32_t tiles,
                                           uint64_t tile0, volatile uint32_t *gave_up)
@@ -165,39 +166,43 @@ __device__ __forceinline__ void hop_warps(const AttnParams &p, Ctl *ctl, uint8_t
     uint32_t unused[4];                                                // all ones where a column does not count
 #pragma unroll
     for (int j = 0; j < 4; ++j) unused[j] = col + j < 32 && ((cols >> (col + j)) & 1) ? 0u : ~0u;
-    int32_t h[32];       // four columns of 8 nodes, or one column of 32; those past a lane's part stay masked
+    int32_t h[32];       // four columns of 8 nodes, or one column of 16; those past a lane's part stay masked
 #pragma unroll
     for (int e = 0; e < 32; ++e) h[e] = -1;
-    auto hops_in = [&](uint32_t t) {
-        const uint64_t node = (tile0 + (uint64_t)t * p.splits) * kTcTile + hw * 32 + first;
-        const int32_t *at = p.hops + node * B + col;
-        const uint32_t left = t < tiles && on && node < p.n ? (uint32_t)min((uint64_t)Q, p.n - node) : 0;
-        if (four) {
+    auto place = [&](uint32_t t, uint32_t k, uint32_t &left) {         // the lane's node k of tile t on, and how many follow
+        const uint64_t node = (tile0 + (uint64_t)t * p.splits) * kTcTile + hw * 32 + first + k;
+        left = t < tiles && on && node < p.n ? (uint32_t)min((uint64_t)(Q - k), p.n - node) : 0;
+        return p.hops + node * B + col;
+    };
+    auto four_in = [&](uint32_t t) {
+        uint32_t left;
+        const int32_t *at = place(t, 0, left);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                int4 x = make_int4(-1, -1, -1, -1);
-                if (e < (int)left) asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(at));
-                h[4 * e] = x.x, h[4 * e + 1] = x.y, h[4 * e + 2] = x.z, h[4 * e + 3] = x.w;
-                at += B;
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                if (e >= (int)Q) break;
-                h[e] = -1;
-                if (e < (int)left) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(h[e]) : "l"(at));
-                at += B;
-            }
+        for (int e = 0; e < 8; ++e) {
+            int4 x = make_int4(-1, -1, -1, -1);
+            if (e < (int)left) asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(at));
+            h[4 * e] = x.x, h[4 * e + 1] = x.y, h[4 * e + 2] = x.z, h[4 * e + 3] = x.w;
+            at += B;
         }
     };
-    // any int32 may stand in the table: clamped to [-1, 255] before it becomes an index
+    auto one_in = [&](uint32_t t, uint32_t k) {
+        uint32_t left;
+        const int32_t *at = place(t, k, left);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            h[e] = -1;
+            if (e < (int)left) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(h[e]) : "l"(at));
+            at += B;
+        }
+    };
     auto byte = [&](int32_t x) -> uint32_t { return ctl->byte_of[__viaddmax_s32(min(x, 255), 1, 0)]; };
     auto put = [&](uint8_t *to, uint32_t nodes, uint32_t b) {           // the bytes of up to 4 nodes of a column
         if (nodes >= 4) *reinterpret_cast<uint32_t *>(to) = b;
         else if (nodes == 2) *reinterpret_cast<uint16_t *>(to) = (uint16_t)b;
         else *to = (uint8_t)b;
     };
-    if (B) hops_in(0);
+    if (four) four_in(0);
+    else if (B) one_in(0, 0);
     for (uint32_t t = 0; t < tiles; ++t) {
         const uint32_t buf = t % BUFS;
         if (t >= BUFS && !__all_sync(~0u, tc::bar_wait(&ctl->hop_empty[buf], (t / BUFS - 1) & 1, gave_up))) break;
@@ -222,17 +227,24 @@ __device__ __forceinline__ void hop_warps(const AttnParams &p, Ctl *ctl, uint8_t
                 const int32_t m = max(max(h[4 * e] | (int)unused[0], h[4 * e + 1] | (int)unused[1]), max(h[4 * e + 2] | (int)unused[2], h[4 * e + 3] | (int)unused[3]));
                 unseen = __funnelshift_l(m, unseen, 1);                // a negative hop count's sign
             }
+            four_in(t + 1);
         } else if (B) {
+#pragma unroll 1
+            for (uint32_t k = 0; k < Q; k += 16) {
+                uint32_t part = 0;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-                if (e >= (int)Q) break;
-                const uint32_t w = (byte(h[e + 3]) * 256 + byte(h[e + 2])) * 65536 + byte(h[e + 1]) * 256 + byte(h[e]);
-                if (on) put(to + e, Q, w);
+                for (int e = 0; e < 16; e += 4) {
+                    if (e >= (int)Q) break;
+                    const uint32_t w = (byte(h[e + 3]) * 256 + byte(h[e + 2])) * 65536 + byte(h[e + 1]) * 256 + byte(h[e]);
+                    if (on) put(to + k + e, Q, w);
+                }
+#pragma unroll
+                for (int e = 15; e >= 0; --e) part = __funnelshift_l(h[e] | (int)unused[0], part, 1);
+                unseen |= part << k;
+                const bool more = k + 16 < Q;
+                one_in(more ? t : t + 1, more ? k + 16 : 0);
             }
-#pragma unroll
-            for (int e = 31; e >= 0; --e) unseen = __funnelshift_l(e < (int)Q ? h[e] | (int)unused[0] : -1, unseen, 1);
         }
-        if (B) hops_in(t + 1);
         const uint32_t mine = Q >= 32 ? ~0u : (1u << Q) - 1, sees = on ? (~unseen & mine) << first : 0;
         const bool in = node0 + lane < p.n;
         bt[B * kTcPitch + lane] = in ? p.buckets + 1 : 0;
