@@ -404,29 +404,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
                 const uint8_t *ds = smem + S::kDs + part * 32 * 128 + (c & 7) * 2;
                 const uint32_t chunk = w * 4 + (c >> 3);
 #pragma unroll 1
-                for (int k = 0; k < 32; k += 8) {
-                    const uint2 b8 = *reinterpret_cast<const uint2 *>(bt + k);
-                    float x[8];
+                for (int k = 0; k < 32; k += 4) {
+                    const uint32_t bw = *reinterpret_cast<const uint32_t *>(bt + k);
+                    float x[4];
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) x[y] = Elem<T>::to_float(*reinterpret_cast<const T *>(ds + (k + y) * 128 + ((chunk ^ y) << 4)));
+                    for (int y = 0; y < 4; ++y) x[y] = Elem<T>::to_float(*reinterpret_cast<const T *>(ds + (k + y) * 128 + ((chunk ^ ((k & 4) + y)) << 4)));
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        // four nodes at once: equal buckets among them take the running value, and the last store stands
-                        const uint32_t bw = q ? b8.y : b8.x;
-                        uint32_t b[4];
-                        float hv[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            b[y] = __byte_perm(bw, 0, 0x4440 + y) << 9;       // 512 bytes a bucket
-                            hv[y] = *reinterpret_cast<const float *>(mine + b[y]);
-                        }
-                        hv[0] += x[4 * q];
-                        hv[1] = (b[1] == b[0] ? hv[0] : hv[1]) + x[4 * q + 1];
-                        hv[2] = (b[2] == b[1] ? hv[1] : b[2] == b[0] ? hv[0] : hv[2]) + x[4 * q + 2];
-                        hv[3] = (b[3] == b[2] ? hv[2] : b[3] == b[1] ? hv[1] : b[3] == b[0] ? hv[0] : hv[3]) + x[4 * q + 3];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) *reinterpret_cast<float *>(mine + b[y]) = hv[y];
-                    }
+                    for (int y = 0; y < 4; ++y) *reinterpret_cast<float *>(mine + (__byte_perm(bw, 0, 0x4440 + y) << 9)) += x[y];      // 512 bytes a bucket
                 }
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(&ctl->hist_done[w]), tc::bar_arrive(&ctl->hop_empty[buf]);
