@@ -55,6 +55,7 @@ struct AttnParams {
     float *part_ml;
     void *row_info;           // RowInfo[hkv][row_tiles * 32] (backward)
     uint32_t hist_parts;      // partial dbias tables
+    uint32_t hist_tables;     // tables a thread sums by bucket into, 1 or 2
     CUtensorMap dk_map, dv_map;   // (head_dim, kv heads, nodes), boxes of 64 x 1 x 128 (backward)
     uint32_t *status;         // device status word, at the start of the work buffer
     uint8_t bucket_of[256];   // bucket of each hop count; larger hops share the last

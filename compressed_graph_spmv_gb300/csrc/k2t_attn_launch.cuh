@@ -77,11 +77,13 @@ template <typename T> int launch_forward(const AttnParams &p, int bm, cudaStream
 // Row tiles that the one-pass kernel holds: 4 of head_dim 64 or less, 2 of more (shared and tensor memory).
 inline uint32_t bwd_fused_tiles(uint32_t d) { return d <= 64 ? 4 : 2; }
 
-template <typename T, int DP, int RT, bool DKV> int backward_nodes(const AttnParams &p, cudaStream_t st)
+template <typename T, int DP, int RT, bool DKV> int backward_nodes(const AttnParams &from, cudaStream_t st)
 {
+    using S = BwdSmem<DP, RT, DKV>;
+    AttnParams p = from;
     const uint32_t groups = (p.row_tiles + RT - 1) / RT;
-    return attn_launch<attn_bwd_nodes_kernel<T, DP, RT, DKV>>(dim3(p.splits * groups, p.hkv), kBwdThreads,
-                       BwdSmem<DP, RT, DKV>::bytes(p), p, st);
+    p.hist_tables = S::bytes(p, 2) <= (size_t)kAttnMaxSmem ? 2 : 1;
+    return attn_launch<attn_bwd_nodes_kernel<T, DP, RT, DKV>>(dim3(p.splits * groups, p.hkv), kBwdThreads, S::bytes(p, p.hist_tables), p, st);
 }
 
 template <typename T, int DP> int backward_dim(const AttnParams &p, cudaStream_t st)
