@@ -67,7 +67,7 @@ inline Batch batch_of(uint64_t n, uint32_t dim, size_t size, uint32_t groups, ui
     uint32_t rows = turn <= target * 3 / 2 ? groups * std::max<uint32_t>(1, target / turn) : std::max<uint32_t>(1, target / row);
     // few rows: a batch for every block before a block has two
     const uint64_t each = (n + (uint64_t)groups * kNormBlocks - 1) / ((uint64_t)groups * kNormBlocks) * groups;
-    if (each < rows) rows = (uint32_t)each;
+    if (each && each < rows) rows = (uint32_t)each;
     return {rows, (rows * row + 31 + 15) / 16 * 16};
 }
 

@@ -392,9 +392,57 @@ def test_norm_unaligned_in_place_and_empty():
     none.forward(e, w, b, e)
     none.backward(e, e, w, e, dw, db)
     assert (dw == 0).all() and (db == 0).all()
+    for dim in (63, 2049, 5000, 5001):
+        none = pkg.LayerNorm(0, dim, torch.bfloat16, residual=True)
+        e, one = torch.empty(0, dim, dtype=torch.bfloat16, device="cuda"), torch.ones(dim, dtype=torch.bfloat16, device="cuda")
+        dw0, db0 = torch.full_like(one, float("nan")), torch.full_like(one, float("nan"))
+        none.forward(e, one, one, e.clone(), residual=e, z=e.clone())
+        none.backward(e, e, one, e.clone(), dw0, db0)
+        assert (dw0 == 0).all() and (db0 == 0).all()
     first = [t.clone() for t in op.backward(y, want, w, dx, dw, db)]
     again = op.backward(y, want, w, dx, dw, db)
     assert all(torch.equal(a, c) for a, c in zip(first, again))
+
+
+@pytest.mark.parametrize("offsets", [(1, 1, 1, 1), (3, 3, 3, 3), (1, 2, 0, 5)])
+@pytest.mark.parametrize("dim", [63, 1001, 2500])
+def test_norm_of_many_unaligned_rows(dim, offsets):
+    """Tensors that start anywhere: alike modulo 16 bytes, and not."""
+    n = 20001
+    rng = np.random.default_rng(dim)
+    w, b = (torch.from_numpy(rng.standard_normal(dim)).to(torch.float16).cuda() for _ in range(2))
+
+    def tensor(off, values=None):
+        flat = torch.full((n * dim + off + 8,), float("nan"), dtype=torch.float16, device="cuda")
+        t = flat[off:off + n * dim].view(n, dim)
+        if values is not None:
+            t.copy_(values)
+        return flat, t
+    values = torch.randn(n, dim, device="cuda")
+    _, x = tensor(offsets[0], values)
+    _, dy = tensor(offsets[1], values.flip(0))
+    fy, y = tensor(offsets[2])
+    fdx, dx = tensor(offsets[3])
+    op = pkg.LayerNorm(n, dim, torch.float16)
+    dw, db = torch.empty_like(w), torch.empty_like(w)
+    op.forward(x, w, b, y)
+    op.backward(dy, x, w, dx, dw, db)
+    al = {k: t.contiguous().clone() for k, t in (("x", x), ("dy", dy))}
+    y2, dx2, dw2, db2 = torch.empty_like(al["x"]), torch.empty_like(al["x"]), torch.empty_like(w), torch.empty_like(w)
+    pick = slice(0, 300)                       # few rows go another way: the same values up to rounding
+    few = pkg.LayerNorm(300, dim, torch.float16)
+    few.forward(al["x"][pick], w, b, y2[pick])
+    few.backward(al["dy"][pick], al["x"][pick], w, dx2[pick], dw2, db2)
+    assert torch.allclose(y[pick].float(), y2[pick].float(), atol=2.0 ** -8, rtol=2.0 ** -9)
+    assert torch.allclose(dx[pick].float(), dx2[pick].float(), atol=2.0 ** -8, rtol=2.0 ** -9)
+    for flat, off in ((fy, offsets[2]), (fdx, offsets[3])):   # nothing around them was written
+        assert torch.isnan(flat[:off]).all() and torch.isnan(flat[off + n * dim:]).all() and not torch.isnan(flat[off:off + n * dim]).any()
+    zz, g = f64(x), f64(dy)
+    ny, _, _, rstd, xh = ref.norm(zz, f64(w), f64(b), 1e-5)
+    ndx, ndw, ndb = ref.norm_gradients(g, xh, rstd, f64(w))
+    tol = norm_tolerances("fp16", zz, zz, xh, rstd, f64(w), f64(b), g, None, ny, ndx, ndw, ndb)
+    for name, got, want in (("y", y, ny), ("dx", dx, ndx), ("dw", dw, ndw), ("db", db, ndb)):
+        close(name, got, want, tol[name])
 
 
 def test_norm_rows_that_hold_no_number():
