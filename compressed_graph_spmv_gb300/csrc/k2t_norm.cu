@@ -66,18 +66,24 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
 // The loads of a row, either when the row's turn comes (AHEAD 0) or AHEAD rows earlier into shared memory, each thread
 // its own pieces: nothing waits on another thread, and the loads in flight (AHEAD rows of every thread) are not bounded
 // by registers.  Rows of one thread are `step` apart.
-template <typename T, int VEC, int TPR, int PER, int TENSORS, int AHEAD> struct RowStream {
+//
+// SHIFT: rows whose pitch is no multiple of 16 bytes, of tensors that start on one.  Pieces are still the 16 aligned
+// bytes: a row that starts `shift` values into one has its pieces that much to the left, the first and the last of them
+// shared with the neighbour rows.  Rows of a thread are a multiple of VEC apart, so that its shift stays, and with it
+// the columns of its registers (weights, sums of the weight's gradient).  A shared piece's other values count as 0 and
+// are not written; past the end of the tensor nothing is read.
+template <typename T, int VEC, int TPR, int PER, int TENSORS, int AHEAD, bool SHIFT> struct RowStream {
     static constexpr int kBytes = AHEAD * TENSORS * PER * 16;            // shared memory a thread
     uint32_t base;                                                       // this thread's first piece
     uint32_t dim;
     uint64_t n, step, next;                                              // next row to ask for
     const T *src[TENSORS];
-    int tid, slot_in, slot_out;
+    int tid, slot_in, slot_out, shift;
 
-    __device__ __forceinline__ RowStream(uint8_t *smem, uint64_t first, uint64_t n_, uint64_t step_, uint32_t dim_, int tid_)
+    __device__ __forceinline__ RowStream(uint8_t *smem, uint64_t first, uint64_t n_, uint64_t step_, uint32_t dim_, int tid_, int shift_)
     {
         base = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
-        dim = dim_, n = n_, step = step_, next = first, tid = tid_;
+        dim = dim_, n = n_, step = step_, next = first, tid = tid_, shift = shift_;
         slot_in = slot_out = 0;
     }
     __device__ __forceinline__ uint32_t at(int slot, int t, int i) const { return base + ((slot * TENSORS + t) * PER + i) * (blockDim.x * 16); }
@@ -88,9 +94,16 @@ template <typename T, int VEC, int TPR, int PER, int TENSORS, int AHEAD> struct 
             for (int t = 0; t < TENSORS; ++t)
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    const uint32_t c = (tid + i * TPR) * VEC;
-                    if (c < dim && src[t])
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(slot_in, t, i)), "l"(src[t] + next * dim + c) : "memory");
+                    const int c = (tid + i * TPR) * VEC - shift;
+                    if (c < (int)dim && src[t]) {
+                        const int64_t from = (int64_t)(next * dim) + c;
+                        if constexpr (SHIFT) {
+                            const uint32_t bytes = (uint32_t)min((int64_t)VEC, (int64_t)(n * dim) - from) * (uint32_t)sizeof(T);
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(slot_in, t, i)), "l"(src[t] + from), "r"(bytes) : "memory");
+                        } else {
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(slot_in, t, i)), "l"(src[t] + from) : "memory");
+                        }
+                    }
                 }
             next += step;
         }
@@ -110,7 +123,6 @@ template <typename T, int VEC, int TPR, int PER, int TENSORS, int AHEAD> struct 
     }
     __device__ __forceinline__ Pack<T, VEC> get(uint64_t row, int t, int i) const
     {
-        const uint32_t c = (tid + i * TPR) * VEC;
         if constexpr (AHEAD > 0) {
             uint4 v;
             asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at(slot_out, t, i)) : "memory");
@@ -119,7 +131,7 @@ template <typename T, int VEC, int TPR, int PER, int TENSORS, int AHEAD> struct 
             *reinterpret_cast<uint4 *>(&r) = v;
             return r;
         } else {
-            return load_once<T, VEC>(src[t] + row * dim + c);
+            return load_once<T, VEC>(src[t] + row * dim + (tid + i * TPR) * VEC);
         }
     }
     __device__ __forceinline__ void taken()                              // the row's pieces are in registers
@@ -131,7 +143,56 @@ template <typename T, int VEC, int TPR, int PER, int TENSORS, int AHEAD> struct 
     }
 };
 
-template <typename T, int VEC, int TPR, int PER, int AHEAD>
+// A thread's piece of a row: columns c .. c + VEC - 1.  Of a shifted row's first piece only the last values are its own,
+// of its last only the first ones; rows of kShiftMin pieces have none that is both.
+template <typename T, int VEC, bool SHIFT> struct Piece {
+    int c, dim;
+    __device__ __forceinline__ Piece(int first, uint32_t d) : c(first), dim((int)d) {}
+    __device__ __forceinline__ bool on() const { return c < dim; }
+    __device__ __forceinline__ bool has(int e) const { return !SHIFT || (c + e >= 0 && c + e < dim); }
+    __device__ __forceinline__ bool whole() const { return !SHIFT || (c >= 0 && c + VEC <= dim); }
+    __device__ __forceinline__ Pack<T, VEC> own(Pack<T, VEC> v) const           // others' values as 0
+    {
+        if constexpr (SHIFT) {
+            if (!whole()) {
+                int at = c;
+                asm volatile("" : "+r"(at));                                    // worked out here, not kept in registers from row to row
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (at + e < 0 || at + e >= dim) v.v[e] = from_f<T>(0.0f);
+            }
+        }
+        return v;
+    }
+    // An edge is written in stores of 8, 4 and 2 bytes, one for each bit of its length, the widest to the side of the row.
+    __device__ __forceinline__ void put(T *row, const Pack<T, VEC> &v) const
+    {
+        if constexpr (SHIFT) {
+            if (!whole()) {
+                int first = c;
+                asm volatile("" : "+r"(first));
+                const bool left = first < 0;
+                const int len = left ? VEC + first : dim - first;
+                const uint4 u = *reinterpret_cast<const uint4 *>(&v);
+                char *to = reinterpret_cast<char *>(row + c);
+                const int bytes = len * (int)sizeof(T);
+                if (bytes & 8) *reinterpret_cast<uint2 *>(to + (left ? 8 : 0)) = left ? make_uint2(u.z, u.w) : make_uint2(u.x, u.y);
+                const uint2 half = ((bytes & 8) != 0) == left ? make_uint2(u.x, u.y) : make_uint2(u.z, u.w);
+                const int at = ((bytes & 8) != 0) == left ? 0 : 8;
+                if (bytes & 4) *reinterpret_cast<uint32_t *>(to + at + (left ? 4 : 0)) = left ? half.y : half.x;
+                if constexpr (sizeof(T) == 2) {
+                    const bool second = ((bytes & 4) != 0) != left;
+                    const uint32_t word = second ? half.y : half.x;
+                    if (bytes & 2) *reinterpret_cast<uint16_t *>(to + at + (second ? 4 : 0) + (left ? 2 : 0)) = (uint16_t)(left ? word >> 16 : word);
+                }
+                return;
+            }
+        }
+        store<T, VEC>(row + c, v);
+    }
+};
+
+template <typename T, int VEC, int TPR, int PER, int AHEAD, bool SHIFT>
 __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __grid_constant__ NormParams p)
 {
     using P = Pack<T, VEC>;
@@ -140,21 +201,26 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
     const int tid = threadIdx.x % TPR, group = threadIdx.x / TPR;
     int turn = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint64_t first = (uint64_t)blockIdx.x * Gr::kGroups + group, step = (uint64_t)gridDim.x * Gr::kGroups;
+    const int shift = SHIFT ? (int)(first * p.dim % VEC) : 0;
+    using Pc = Piece<T, VEC, SHIFT>;
+    auto piece = [&](int i) { return Pc((tid + i * TPR) * VEC - shift, p.dim); };
     P w[PER], bi[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const uint32_t c = (tid + i * TPR) * VEC;
-        if (c < p.dim) {
+        const auto c = piece(i);
+        w[i] = bi[i] = zero_pack<T, VEC>();
+        if (c.on()) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                w[i].v[e] = static_cast<const T *>(p.weight)[c + e];
-                bi[i].v[e] = p.bias ? static_cast<const T *>(p.bias)[c + e] : from_f<T>(0.0f);
-            }
+            for (int e = 0; e < VEC; ++e)
+                if (c.has(e)) {
+                    w[i].v[e] = static_cast<const T *>(p.weight)[c.c + e];
+                    if (p.bias) bi[i].v[e] = static_cast<const T *>(p.bias)[c.c + e];
+                }
         }
     }
     extern __shared__ __align__(16) uint8_t ring[];
-    const uint64_t first = (uint64_t)blockIdx.x * Gr::kGroups + group, step = (uint64_t)gridDim.x * Gr::kGroups;
-    RowStream<T, VEC, TPR, PER, 2, AHEAD> in(ring, first, p.n, step, p.dim, tid);
+    RowStream<T, VEC, TPR, PER, 2, AHEAD, SHIFT> in(ring, first, p.n, step, p.dim, tid, shift);
     in.src[0] = static_cast<const T *>(p.x);
     in.src[1] = static_cast<const T *>(p.residual);
     in.start();
@@ -164,22 +230,22 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
         in.ready();
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const uint32_t c = (tid + i * TPR) * VEC;
-            if (c < p.dim) {
-                z[i] = in.get(row, 0, i);
-                if (p.residual) r[i] = in.get(row, 1, i);
+            const auto c = piece(i);
+            if (c.on()) {
+                z[i] = c.own(in.get(row, 0, i));
+                if (p.residual) r[i] = c.own(in.get(row, 1, i));
             }
         }
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const uint32_t c = (tid + i * TPR) * VEC;
-            if (c < p.dim) {
+            const auto c = piece(i);
+            if (c.on()) {
                 if (p.residual) {
                     // the sum is what the next layer reads: rounded first, then normalised as it stands
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) z[i].v[e] = from_f<T>(to_f(z[i].v[e]) + to_f(r[i].v[e]));
-                    store<T, VEC>(static_cast<T *>(p.z) + at + c, z[i]);
+                    c.put(static_cast<T *>(p.z) + at, z[i]);
                 }
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) s += to_f(z[i].v[e]);
@@ -191,12 +257,22 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
         float q = 0.0f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const uint32_t c = (tid + i * TPR) * VEC;
-            if (c < p.dim) {
+            const auto c = piece(i);
+            if (c.on()) {
+                if (c.whole()) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float d = to_f(z[i].v[e]) - mean;
-                    q = fmaf(d, d, q);
+                    for (int e = 0; e < VEC; ++e) {
+                        const float d = to_f(z[i].v[e]) - mean;
+                        q = fmaf(d, d, q);
+                    }
+                } else {
+                    int at = c.c;
+                    asm volatile("" : "+r"(at));
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float d = at + e >= 0 && at + e < c.dim ? to_f(z[i].v[e]) - mean : 0.0f;
+                        q = fmaf(d, d, q);
+                    }
                 }
             }
         }
@@ -205,13 +281,13 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
         if (tid == 0) p.mean[row] = mean, p.rstd[row] = rstd;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const uint32_t c = (tid + i * TPR) * VEC;
-            if (c < p.dim) {
+            const auto c = piece(i);
+            if (c.on()) {
                 P y;
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
                     y.v[e] = from_f<T>(fmaf((to_f(z[i].v[e]) - mean) * rstd, to_f(w[i].v[e]), to_f(bi[i].v[e])));
-                store<T, VEC>(static_cast<T *>(p.y) + at + c, y);
+                c.put(static_cast<T *>(p.y) + at, y);
             }
         }
     }
@@ -219,7 +295,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
 
 // dx = rstd (w dy - c1 - xh c2) + dz with c1 = mean(w dy), c2 = mean(w dy xh);
 // part[block][0 | 1][dim]: the block's sums of dy xh and dy.
-template <typename T, int VEC, int TPR, int PER, int AHEAD>
+template <typename T, int VEC, int TPR, int PER, int AHEAD, bool SHIFT>
 __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 || PER > 1 ? 1 : 3) norm_bwd_kernel(const __grid_constant__ NormParams p)
 {
     using P = Pack<T, VEC>;
@@ -231,16 +307,19 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 || PER > 1 ? 
     constexpr int N2 = PER * VEC / 2;
     static_assert(PER * VEC % 2 == 0, "pairs");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint64_t first = (uint64_t)blockIdx.x * Gr::kGroups + group, step = (uint64_t)gridDim.x * Gr::kGroups;
+    const int shift = SHIFT ? (int)(first * p.dim % VEC) : 0;
+    using Pc = Piece<T, VEC, SHIFT>;
+    auto piece = [&](int i) { return Pc((tid + i * TPR) * VEC - shift, p.dim); };
     float2 w[N2], dw[N2], db[N2];
 #pragma unroll
     for (int e = 0; e < PER * VEC; ++e) {
-        const uint32_t c = (tid + e / VEC * TPR) * VEC;
-        half_of(w, e) = c < p.dim ? to_f(static_cast<const T *>(p.weight)[c + e % VEC]) : 0.0f;
+        const auto c = piece(e / VEC);
+        half_of(w, e) = c.on() && c.has(e % VEC) ? to_f(static_cast<const T *>(p.weight)[c.c + e % VEC]) : 0.0f;
         half_of(dw, e) = half_of(db, e) = 0.0f;
     }
     extern __shared__ __align__(16) uint8_t ring[];
-    const uint64_t first = (uint64_t)blockIdx.x * Gr::kGroups + group, step = (uint64_t)gridDim.x * Gr::kGroups;
-    RowStream<T, VEC, TPR, PER, 3, AHEAD> in(ring, first, p.n, step, p.dim, tid);
+    RowStream<T, VEC, TPR, PER, 3, AHEAD, SHIFT> in(ring, first, p.n, step, p.dim, tid, shift);
     in.src[0] = static_cast<const T *>(p.z_in);
     in.src[1] = static_cast<const T *>(p.dy);
     in.src[2] = static_cast<const T *>(p.dz);
@@ -253,8 +332,9 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 || PER > 1 ? 
         in.ready();
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            if ((tid + i * TPR) * VEC < p.dim) {
-                z[i] = in.get(row, 0, i), g[i] = in.get(row, 1, i);
+            const auto c = piece(i);
+            if (c.on()) {
+                z[i] = c.own(in.get(row, 0, i)), g[i] = c.own(in.get(row, 1, i));
                 if (p.dz) x[i] = in.get(row, 2, i);
             } else {
                 z[i] = g[i] = x[i] = zero_pack<T, VEC>();
@@ -282,12 +362,12 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 || PER > 1 ? 
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const uint32_t c = (tid + i * TPR) * VEC;
-            if (c < p.dim) {
+            const auto c = piece(i);
+            if (c.on()) {
                 P o;
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) o.v[e] = from_f<T>(half_of(a, i * VEC + e));
-                store<T, VEC>(static_cast<T *>(p.dx) + at + c, o);
+                c.put(static_cast<T *>(p.dx) + at, o);
             }
         }
     }
@@ -300,14 +380,16 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 || PER > 1 ? 
         if (group != turn_of) continue;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const uint32_t c = (tid + i * TPR) * VEC;
-            if (c < p.dim) {
+            const auto c = piece(i);
+            if (c.on()) {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
+                    if (!c.has(e)) continue;
+                    const uint32_t k = c.c + e;
                     float a = half_of(dw, i * VEC + e), b = half_of(db, i * VEC + e);
-                    if (turn_of > 0) a += sums[c + e], b += sums[p.dim + c + e];
-                    if (turn_of + 1 < Gr::kGroups) sums[c + e] = a, sums[p.dim + c + e] = b;
-                    else out[c + e] = a, out[p.dim + c + e] = b;
+                    if (turn_of > 0) a += sums[k], b += sums[p.dim + k];
+                    if (turn_of + 1 < Gr::kGroups) sums[k] = a, sums[p.dim + k] = b;
+                    else out[k] = a, out[p.dim + k] = b;
                 }
             }
         }
@@ -315,23 +397,25 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 || PER > 1 ? 
 }
 
 // AHEAD: rows asked for ahead where blocks stay for several (0: a row's loads wait for its turn, less to set up).
-template <typename T, int VEC, int TPR, int PER, int AHEAD> int run_norm(NormParams &p, uint32_t blocks, bool backward, cudaStream_t st)
+template <typename T, int VEC, int TPR, int PER, int AHEAD, bool SHIFT> int run_norm(NormParams &p, uint32_t blocks, bool backward, cudaStream_t st)
 {
     using Gr = Group<TPR>;
     if (!backward) {
         if (!blocks) return K2T_OK;
-        const auto kernel = norm_fwd_kernel<T, VEC, TPR, PER, AHEAD>;
-        const size_t ring = (size_t)Gr::kThreads * RowStream<T, VEC, TPR, PER, 2, AHEAD>::kBytes;
+        const auto kernel = norm_fwd_kernel<T, VEC, TPR, PER, AHEAD, SHIFT>;
+        const size_t ring = (size_t)Gr::kThreads * RowStream<T, VEC, TPR, PER, 2, AHEAD, SHIFT>::kBytes;
         if (ring > 32 * 1024) K2T_NORM_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring));
         // short blocks even out the SMs: 16 rounds of them 322 us, 2 rounds 357 us on 2^18 x 1024 bf16
         if (AHEAD > 0) blocks = (uint32_t)std::min<uint64_t>((p.n + Gr::kGroups * 4 - 1) / (Gr::kGroups * 4), kNormBlocks * 4);
+        if (SHIFT) blocks = (blocks + 7) / 8 * 8;      // a thread's rows a multiple of VEC apart
         return norm_launch(kernel, dim3(blocks), Gr::kThreads, ring, st, p);
     }
     if (blocks) {
-        const size_t ring = (size_t)Gr::kThreads * RowStream<T, VEC, TPR, PER, 3, AHEAD>::kBytes;
+        const size_t ring = (size_t)Gr::kThreads * RowStream<T, VEC, TPR, PER, 3, AHEAD, SHIFT>::kBytes;
         const size_t sums = Gr::kGroups > 1 ? 2 * p.dim * sizeof(float) : 0;
-        const auto kernel = norm_bwd_kernel<T, VEC, TPR, PER, AHEAD>;
+        const auto kernel = norm_bwd_kernel<T, VEC, TPR, PER, AHEAD, SHIFT>;
         if (AHEAD > 0) blocks = norm_resident(kernel, blocks, Gr::kThreads, std::max(ring, sums));
+        if (SHIFT) blocks = blocks < 8 ? 8 : blocks / 8 * 8;
         int rc = norm_launch(kernel, dim3(blocks), Gr::kThreads, std::max(ring, sums), st, p);
         if (rc) return rc;
     }
@@ -346,22 +430,17 @@ template <typename T, int VEC, int TPR, int PER, int AHEAD> int plan_norm(NormPa
     constexpr int G = Group<TPR>::kGroups;
     const uint32_t blocks = norm_parts(p.n, G);
     if constexpr (AHEAD > 0) {
-        if (p.n > (uint64_t)4 * G * kNormBlocks) return run_norm<T, VEC, TPR, PER, AHEAD>(p, norm_parts(p.n, G), backward, st);
+        if (p.n > (uint64_t)4 * G * kNormBlocks) return run_norm<T, VEC, TPR, PER, AHEAD, false>(p, norm_parts(p.n, G), backward, st);
     }
-    return run_norm<T, VEC, TPR, PER, 0>(p, blocks, backward, st);
+    return run_norm<T, VEC, TPR, PER, 0, false>(p, blocks, backward, st);
 }
 
 // Threads a row: as few as hold it, up to a block, then more loads a thread.
 // Forward with two pieces a thread (2^17 x 2048 bf16: 248 us, one piece 261),
 // backward with one, which leaves registers for more rows at once (2^18 x 1024
 // bf16: 400 us, two pieces 485).
-template <typename T> int norm_dispatch(NormParams &p, bool vec, bool backward, cudaStream_t st)
+template <typename T> int norm_pieces(NormParams &p, bool backward, cudaStream_t st)
 {
-    if (!vec) {
-        if (p.dim <= 128) return plan_norm<T, 1, 32, 4, 0>(p, backward, st);
-        if (p.dim <= 512) return plan_norm<T, 1, 128, 4, 0>(p, backward, st);
-        return plan_norm<T, 1, 256, 8, 0>(p, backward, st);
-    }
     constexpr int V = 16 / sizeof(T);
     const uint32_t c = p.dim / V;
     if (backward) {
@@ -381,6 +460,31 @@ template <typename T> int norm_dispatch(NormParams &p, bool vec, bool backward, 
     if (c <= 512) return plan_norm<T, V, 256, 2, 2>(p, backward, st);
     if (c <= 1024) return plan_norm<T, V, 512, 2, 2>(p, backward, st);
     return plan_norm<T, V, 512, 8, 0>(p, backward, st);
+}
+
+// Shifted rows of kShiftMin to kShiftMax pieces: 100000 x 1465 fp16 271 us forward and 301 backward, value by value 303 and
+// in stretches 393; 65536 x 3999 bf16 390 and 609, in stretches 610 and 1118.  In shorter rows the two edges cost more than
+// the wide loads give (200000 x 333 fp32 175 and 207 us, in stretches 148 and 188).
+constexpr uint32_t kShiftMin = 129, kShiftMax = 1024;
+
+inline uint32_t shifted_pieces(uint32_t dim, uint32_t v) { return (dim + 2 * v - 2) / v; }   // at the largest shift
+
+template <typename T> int norm_shifted(NormParams &p, bool backward, cudaStream_t st)
+{
+    constexpr int V = 16 / sizeof(T);
+    const uint32_t c = shifted_pieces(p.dim, V), blocks = norm_parts(p.n, 1);
+    if (c <= 256) return run_norm<T, V, 256, 1, 4, true>(p, blocks, backward, st);
+    if (c <= 512) return run_norm<T, V, 256, 2, 2, true>(p, blocks, backward, st);
+    return run_norm<T, V, 512, 2, 2, true>(p, blocks, backward, st);
+}
+
+template <typename T> int norm_dispatch(NormParams &p, bool vec, bool shift, bool backward, cudaStream_t st)
+{
+    if (vec) return norm_pieces<T>(p, backward, st);
+    if (shift) return norm_shifted<T>(p, backward, st);
+    if (p.dim <= 128) return plan_norm<T, 1, 32, 4, 0>(p, backward, st);
+    if (p.dim <= 512) return plan_norm<T, 1, 128, 4, 0>(p, backward, st);
+    return plan_norm<T, 1, 256, 8, 0>(p, backward, st);
 }
 
 int check_norm(const k2t_norm *a)
@@ -407,15 +511,17 @@ int dispatch(const k2t_norm *a, NormParams &p, bool backward, cudaStream_t st)
     p.weight = a->weight;
     p.mean = a->mean;
     p.rstd = a->rstd;
-    // Rows that are not whole pieces: value by value while there are few of them, when a call is its latency (4999 x 333
-    // fp32, training: 15 us against 20), else in stretches (200000 x 333 bf16, forward: 170 us against 220; 65536 x 3999:
-    // 610 us against 2335).  Forward rows of 513 to 2048 values fill a block with single values and stay with them
-    // (100000 x 1465 fp16: 303 us against 417; backward 422 against 392).
-    const bool fill = !backward && a->dim > 512 && a->dim <= 2048;
-    if (!vec && !fill && (a->n_rows > 16384 || a->dim > 2048)) return norm_ragged(p, a->dtype, backward, st);
-    if (a->dtype == K2T_BF16) return norm_dispatch<__nv_bfloat16>(p, vec, backward, st);
-    if (a->dtype == K2T_FP16) return norm_dispatch<__half>(p, vec, backward, st);
-    return norm_dispatch<float>(p, vec, backward, st);
+    // Rows that are not whole pieces: shifted where that pays; else value by value while there are few of them, when a call
+    // is its latency (4999 x 333 fp32, training: 15 us against 20), else in stretches (200000 x 333 bf16, forward: 170 us
+    // against 220; 65536 x 3999: 610 us against 2335).  Forward rows of 513 to 2048 values fill a block with single values
+    // and stay with them (100000 x 1465 fp16: 303 us against 417; backward 422 against 392).
+    const bool few = a->n_rows <= 16384 && a->dim <= 2048, fill = !backward && a->dim > 512 && a->dim <= 2048;
+    const uint32_t c = shifted_pieces(a->dim, 16 / size);
+    const bool shift = !vec && !few && !(all & 15) && c >= kShiftMin && c <= kShiftMax;
+    if (!vec && !shift && !few && !fill) return norm_ragged(p, a->dtype, backward, st);
+    if (a->dtype == K2T_BF16) return norm_dispatch<__nv_bfloat16>(p, vec, shift, backward, st);
+    if (a->dtype == K2T_FP16) return norm_dispatch<__half>(p, vec, shift, backward, st);
+    return norm_dispatch<float>(p, vec, shift, backward, st);
 }
 
 }  // namespace
@@ -428,7 +534,7 @@ extern "C" {
 uint64_t k2t_norm_work_bytes(const k2t_norm *a)
 {
     if (check_norm(a)) return 0;
-    return align_up((uint64_t)norm_parts(a->n_rows, 1) * 2 * a->dim * sizeof(float), 256);
+    return align_up(((uint64_t)norm_parts(a->n_rows, 1) + 7) / 8 * 8 * 2 * a->dim * sizeof(float), 256);
 }
 
 int k2t_norm_forward(const k2t_norm *a, void *stream)

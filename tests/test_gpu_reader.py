@@ -445,6 +445,45 @@ def test_norm_of_many_unaligned_rows(dim, offsets):
         close(name, got, want, tol[name])
 
 
+@pytest.mark.parametrize("n,dim,dtype,residual", [(16390, 1031, "bf16", False), (16387, 1466, "fp16", True), (16391, 517, "fp32", True),
+                                                  (25, 2051, "bf16", True), (1, 2055, "fp16", False), (2500, 3999, "fp16", True),
+                                                  (70, 7001, "bf16", False), (33, 2049, "fp32", False), (3, 4086, "fp32", True)])
+def test_norm_of_shifted_rows(n, dim, dtype, residual):
+    """Rows whose pitch is no multiple of 16 bytes, long enough to be read in aligned pieces all the same."""
+    check_norm(n, dim, dtype, residual)
+
+
+def test_norm_of_shifted_rows_stays_in_them():
+    """In place, between guards, and beside a row of NaN: the neighbours' values are read with a row but not used."""
+    n, dim = 203, 2053
+    t = lambda: torch.randn(n, dim, device="cuda").to(torch.float16)  # noqa: E731
+    x, r, dy, dz = t(), t(), t(), t()
+    x[77] = float("nan")
+    dy[101, 0] = float("inf")
+    w, b = torch.randn(2, dim, device="cuda").to(torch.float16)
+    op = pkg.LayerNorm(n, dim, torch.float16, residual=True)
+    z, y, dx, dw, db = t(), t(), t(), torch.empty_like(w), torch.empty_like(w)
+    op.forward(x, w, b, y, residual=r, z=z)
+    op.backward(dy, z, w, dx, dw, db, dz=dz)
+    good = torch.ones(n, dtype=torch.bool, device="cuda")
+    good[77] = False
+    assert not torch.isnan(y[good]).any() and torch.isnan(y[77]).all()
+    good[101] = False
+    assert torch.isfinite(dx[good]).all()
+    guarded = []
+    for v in (x, dy):
+        flat = torch.full((8 + n * dim + 9,), 7.0, dtype=torch.float16, device="cuda")
+        flat[8:8 + n * dim].copy_(v.flatten())
+        guarded.append((flat, flat[8:8 + n * dim].view(n, dim)))
+    (fx, gx), (fdy, gdy) = guarded
+    op.forward(gx, w, b, gx, residual=r, z=r)              # y over x, z over the residual
+    assert torch.equal(gx.nan_to_num(), y.nan_to_num()) and torch.equal(r.nan_to_num(), z.nan_to_num())
+    op.backward(gdy, z, w, gdy, dw, db, dz=dz)             # dx over dy
+    assert torch.equal(gdy.nan_to_num(), dx.nan_to_num())
+    for flat in (fx, fdy):
+        assert (flat[:8] == 7).all() and (flat[8 + n * dim:] == 7).all()
+
+
 def test_norm_rows_that_hold_no_number():
     """A row with an infinity or NaN spoils itself and the weight's gradient, no other row."""
     x = torch.randn(10, 96, device="cuda")
