@@ -11,6 +11,8 @@
 // norm_join_kernel adds those in a fixed order.
 #include "k2t_norm.cuh"
 
+#include <type_traits>
+
 namespace k2t {
 namespace {
 
@@ -40,7 +42,24 @@ template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> zero_pack
 }
 template <typename T, int VEC> __device__ __forceinline__ float2 pair_of(const Pack<T, VEC> *p, int e)
 {
-    return make_float2(to_f(p[2 * e / VEC].v[2 * e % VEC]), to_f(p[(2 * e + 1) / VEC].v[(2 * e + 1) % VEC]));
+    if constexpr (sizeof(T) == 2 && VEC > 1) {
+        const uint32_t word = reinterpret_cast<const uint32_t *>(p[2 * e / VEC].v)[e % (VEC / 2)];
+        if constexpr (std::is_same_v<T, __half>) return __half22float2(*reinterpret_cast<const __half2 *>(&word));
+        else return make_float2(__uint_as_float(word << 16), __uint_as_float(word & 0xffff0000u));
+    } else {
+        return make_float2(to_f(p[2 * e / VEC].v[2 * e % VEC]), to_f(p[(2 * e + 1) / VEC].v[(2 * e + 1) % VEC]));
+    }
+}
+template <typename T, int VEC> __device__ __forceinline__ void set_pair(Pack<T, VEC> *p, int e, float2 v)
+{
+    if constexpr (sizeof(T) == 2 && VEC > 1) {
+        uint32_t &word = reinterpret_cast<uint32_t *>(p[2 * e / VEC].v)[e % (VEC / 2)];
+        if constexpr (std::is_same_v<T, __half>) *reinterpret_cast<__half2 *>(&word) = __float22half2_rn(v);
+        else *reinterpret_cast<__nv_bfloat162 *>(&word) = __float22bfloat162_rn(v);
+    } else {
+        p[2 * e / VEC].v[2 * e % VEC] = from_f<T>(v.x);
+        p[(2 * e + 1) / VEC].v[(2 * e + 1) % VEC] = from_f<T>(v.y);
+    }
 }
 __device__ __forceinline__ float &half_of(float2 *v, int e) { return e & 1 ? v[e >> 1].y : v[e >> 1].x; }
 __device__ __forceinline__ unsigned long long bits(const float2 &v) { return *reinterpret_cast<const unsigned long long *>(&v); }
@@ -150,7 +169,7 @@ template <typename T, int VEC, bool SHIFT> struct Piece {
     __device__ __forceinline__ Piece(int first, uint32_t d) : c(first), dim((int)d) {}
     __device__ __forceinline__ bool on() const { return c < dim; }
     __device__ __forceinline__ bool has(int e) const { return !SHIFT || (c + e >= 0 && c + e < dim); }
-    __device__ __forceinline__ bool whole() const { return !SHIFT || (c >= 0 && c + VEC <= dim); }
+    __device__ __forceinline__ bool whole() const { return SHIFT ? c >= 0 && c + VEC <= dim : c < dim; }
     __device__ __forceinline__ Pack<T, VEC> own(Pack<T, VEC> v) const           // others' values as 0
     {
         if constexpr (SHIFT) {
@@ -205,6 +224,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
     const int shift = SHIFT ? (int)(first * p.dim % VEC) : 0;
     using Pc = Piece<T, VEC, SHIFT>;
     auto piece = [&](int i) { return Pc((tid + i * TPR) * VEC - shift, p.dim); };
+    constexpr int N2 = PER * VEC / 2;
     P w[PER], bi[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -231,64 +251,52 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const auto c = piece(i);
+            z[i] = r[i] = zero_pack<T, VEC>();
             if (c.on()) {
                 z[i] = c.own(in.get(row, 0, i));
                 if (p.residual) r[i] = c.own(in.get(row, 1, i));
             }
         }
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const auto c = piece(i);
-            if (c.on()) {
-                if (p.residual) {
-                    // the sum is what the next layer reads: rounded first, then normalised as it stands
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) z[i].v[e] = from_f<T>(to_f(z[i].v[e]) + to_f(r[i].v[e]));
-                    c.put(static_cast<T *>(p.z) + at, z[i]);
-                }
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) s += to_f(z[i].v[e]);
-            }
-        }
         in.taken();
-        s = group_sum1<TPR>(s, buf, group, turn);
-        const float mean = s * p.inv_dim;
-        float q = 0.0f;
+        if (p.residual) {
+            // the sum is what the next layer reads: rounded first, then normalised as it stands
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const auto c = piece(i);
-            if (c.on()) {
-                if (c.whole()) {
+            for (int e = 0; e < N2; ++e) set_pair<T, VEC>(z, e, add2(pair_of<T, VEC>(z, e), pair_of<T, VEC>(r, e)));
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float d = to_f(z[i].v[e]) - mean;
-                        q = fmaf(d, d, q);
-                    }
-                } else {
-                    int at = c.c;
-                    asm volatile("" : "+r"(at));
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float d = at + e >= 0 && at + e < c.dim ? to_f(z[i].v[e]) - mean : 0.0f;
-                        q = fmaf(d, d, q);
-                    }
-                }
+            for (int i = 0; i < PER; ++i) {
+                const auto c = piece(i);
+                if (c.on()) c.put(static_cast<T *>(p.z) + at, z[i]);
             }
         }
-        q = group_sum1<TPR>(q, buf, group, turn);
-        const float rstd = rsqrtf(q * p.inv_dim + p.eps);
-        if (tid == 0) p.mean[row] = mean, p.rstd[row] = rstd;
+        float2 d[N2], s = make_float2(0.0f, 0.0f), q = s;
+#pragma unroll
+        for (int e = 0; e < N2; ++e) d[e] = pair_of<T, VEC>(z, e), s = add2(s, d[e]);
+        const float mean = group_sum1<TPR>(s.x + s.y, buf, group, turn) * p.inv_dim;
+        const float2 nm = make_float2(-mean, -mean);
+#pragma unroll
+        for (int e = 0; e < N2; ++e) d[e] = add2(d[e], nm);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const auto c = piece(i);
-            if (c.on()) {
-                P y;
+            if (!c.whole()) {
+                int first_c = c.c;
+                if constexpr (SHIFT) asm volatile("" : "+r"(first_c));
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
-                    y.v[e] = from_f<T>(fmaf((to_f(z[i].v[e]) - mean) * rstd, to_f(w[i].v[e]), to_f(bi[i].v[e])));
-                c.put(static_cast<T *>(p.y) + at, y);
+                    if (first_c + e < 0 || first_c + e >= c.dim) half_of(d, i * VEC + e) = 0.0f;
             }
+        }
+#pragma unroll
+        for (int e = 0; e < N2; ++e) q = fma2(d[e], d[e], q);
+        const float rstd = rsqrtf(group_sum1<TPR>(q.x + q.y, buf, group, turn) * p.inv_dim + p.eps);
+        const float2 r2 = make_float2(rstd, rstd);
+        if (tid == 0) p.mean[row] = mean, p.rstd[row] = rstd;
+#pragma unroll
+        for (int e = 0; e < N2; ++e) set_pair<T, VEC>(z, e, fma2(mul2(d[e], r2), pair_of<T, VEC>(w, e), pair_of<T, VEC>(bi, e)));
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const auto c = piece(i);
+            if (c.on()) c.put(static_cast<T *>(p.y) + at, z[i]);
         }
     }
 }
@@ -358,16 +366,13 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 || PER > 1 ? 
 #pragma unroll
         for (int e = 0; e < N2; ++e) {
             a[e] = fma2(xh[e], n2, add2(a[e], n1));
-            a[e] = p.dz ? fma2(a[e], r2, pair_of<T, VEC>(x, e)) : mul2(a[e], r2);
+            set_pair<T, VEC>(z, e, p.dz ? fma2(a[e], r2, pair_of<T, VEC>(x, e)) : mul2(a[e], r2));
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const auto c = piece(i);
             if (c.on()) {
-                P o;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) o.v[e] = from_f<T>(half_of(a, i * VEC + e));
-                c.put(static_cast<T *>(p.dx) + at, o);
+                c.put(static_cast<T *>(p.dx) + at, z[i]);
             }
         }
     }
@@ -397,10 +402,10 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 || PER > 1 ? 
 }
 
 // AHEAD: rows asked for ahead where blocks stay for several (0: a row's loads wait for its turn, less to set up).
-template <typename T, int VEC, int TPR, int PER, int AHEAD, bool SHIFT> int run_norm(NormParams &p, uint32_t blocks, bool backward, cudaStream_t st)
+template <typename T, int VEC, int TPR, int PER, int AHEAD, bool SHIFT, bool BACK> int run_norm(NormParams &p, uint32_t blocks, cudaStream_t st)
 {
     using Gr = Group<TPR>;
-    if (!backward) {
+    if constexpr (!BACK) {
         if (!blocks) return K2T_OK;
         const auto kernel = norm_fwd_kernel<T, VEC, TPR, PER, AHEAD, SHIFT>;
         const size_t ring = (size_t)Gr::kThreads * RowStream<T, VEC, TPR, PER, 2, AHEAD, SHIFT>::kBytes;
@@ -409,57 +414,58 @@ template <typename T, int VEC, int TPR, int PER, int AHEAD, bool SHIFT> int run_
         if (AHEAD > 0) blocks = (uint32_t)std::min<uint64_t>((p.n + Gr::kGroups * 4 - 1) / (Gr::kGroups * 4), kNormBlocks * 4);
         if (SHIFT) blocks = (blocks + 7) / 8 * 8;      // a thread's rows a multiple of VEC apart
         return norm_launch(kernel, dim3(blocks), Gr::kThreads, ring, st, p);
+    } else {
+        if (blocks) {
+            const size_t ring = (size_t)Gr::kThreads * RowStream<T, VEC, TPR, PER, 3, AHEAD, SHIFT>::kBytes;
+            const size_t sums = Gr::kGroups > 1 ? 2 * p.dim * sizeof(float) : 0;
+            const auto kernel = norm_bwd_kernel<T, VEC, TPR, PER, AHEAD, SHIFT>;
+            if (AHEAD > 0) blocks = norm_resident(kernel, blocks, Gr::kThreads, std::max(ring, sums));
+            if (SHIFT) blocks = blocks < 8 ? 8 : blocks / 8 * 8;
+            int rc = norm_launch(kernel, dim3(blocks), Gr::kThreads, std::max(ring, sums), st, p);
+            if (rc) return rc;
+        }
+        p.parts = blocks;
+        return norm_launch(norm_join_kernel<T>, dim3((p.dim + 7) / 8, p.dbias ? 2 : 1), 1024, 0, st, p);
     }
-    if (blocks) {
-        const size_t ring = (size_t)Gr::kThreads * RowStream<T, VEC, TPR, PER, 3, AHEAD, SHIFT>::kBytes;
-        const size_t sums = Gr::kGroups > 1 ? 2 * p.dim * sizeof(float) : 0;
-        const auto kernel = norm_bwd_kernel<T, VEC, TPR, PER, AHEAD, SHIFT>;
-        if (AHEAD > 0) blocks = norm_resident(kernel, blocks, Gr::kThreads, std::max(ring, sums));
-        if (SHIFT) blocks = blocks < 8 ? 8 : blocks / 8 * 8;
-        int rc = norm_launch(kernel, dim3(blocks), Gr::kThreads, std::max(ring, sums), st, p);
-        if (rc) return rc;
-    }
-    p.parts = blocks;
-    return norm_launch(norm_join_kernel<T>, dim3((p.dim + 7) / 8, p.dbias ? 2 : 1), 1024, 0, st, p);
 }
 
 // Blocks: every SM full of them at most (kNormBlocks).  With more than four rows a group the loads run ahead: measured
 // on 2^20 x 512 and 2^18 x 1024 bf16 against a row's own loads; below that there is little to run ahead of.
-template <typename T, int VEC, int TPR, int PER, int AHEAD> int plan_norm(NormParams &p, const bool backward, cudaStream_t st)
+template <typename T, int VEC, int TPR, int PER, int AHEAD, bool BACK> int plan_norm(NormParams &p, cudaStream_t st)
 {
     constexpr int G = Group<TPR>::kGroups;
     const uint32_t blocks = norm_parts(p.n, G);
     if constexpr (AHEAD > 0) {
-        if (p.n > (uint64_t)4 * G * kNormBlocks) return run_norm<T, VEC, TPR, PER, AHEAD, false>(p, norm_parts(p.n, G), backward, st);
+        if (p.n > (uint64_t)4 * G * kNormBlocks) return run_norm<T, VEC, TPR, PER, AHEAD, false, BACK>(p, blocks, st);
     }
-    return run_norm<T, VEC, TPR, PER, 0, false>(p, blocks, backward, st);
+    return run_norm<T, VEC, TPR, PER, 0, false, BACK>(p, blocks, st);
 }
 
 // Threads a row: as few as hold it, up to a block, then more loads a thread.
 // Forward with two pieces a thread (2^17 x 2048 bf16: 248 us, one piece 261),
 // backward with one, which leaves registers for more rows at once (2^18 x 1024
 // bf16: 400 us, two pieces 485).
-template <typename T> int norm_pieces(NormParams &p, bool backward, cudaStream_t st)
+template <typename T, bool BACK> int norm_pieces(NormParams &p, cudaStream_t st)
 {
     constexpr int V = 16 / sizeof(T);
     const uint32_t c = p.dim / V;
-    if (backward) {
-        if (c <= 8) return plan_norm<T, V, 8, 1, 4>(p, true, st);
-        if (c <= 16) return plan_norm<T, V, 16, 1, 4>(p, true, st);
-        if (c <= 32) return plan_norm<T, V, 32, 1, 4>(p, true, st);
-        if (c <= 64) return plan_norm<T, V, 64, 1, 4>(p, true, st);
-        if (c <= 128) return plan_norm<T, V, 128, 1, 4>(p, true, st);
-        if (c <= 256) return plan_norm<T, V, 256, 1, 4>(p, true, st);
+    if constexpr (BACK) {
+        if (c <= 8) return plan_norm<T, V, 8, 1, 4, BACK>(p, st);
+        if (c <= 16) return plan_norm<T, V, 16, 1, 4, BACK>(p, st);
+        if (c <= 32) return plan_norm<T, V, 32, 1, 4, BACK>(p, st);
+        if (c <= 64) return plan_norm<T, V, 64, 1, 4, BACK>(p, st);
+        if (c <= 128) return plan_norm<T, V, 128, 1, 4, BACK>(p, st);
+        if (c <= 256) return plan_norm<T, V, 256, 1, 4, BACK>(p, st);
     } else {
-        if (c <= 16) return plan_norm<T, V, 8, 2, 4>(p, false, st);
-        if (c <= 32) return plan_norm<T, V, 16, 2, 4>(p, false, st);
-        if (c <= 64) return plan_norm<T, V, 32, 2, 4>(p, false, st);
-        if (c <= 128) return plan_norm<T, V, 64, 2, 4>(p, false, st);
-        if (c <= 256) return plan_norm<T, V, 128, 2, 4>(p, false, st);
+        if (c <= 16) return plan_norm<T, V, 8, 2, 4, BACK>(p, st);
+        if (c <= 32) return plan_norm<T, V, 16, 2, 4, BACK>(p, st);
+        if (c <= 64) return plan_norm<T, V, 32, 2, 4, BACK>(p, st);
+        if (c <= 128) return plan_norm<T, V, 64, 2, 4, BACK>(p, st);
+        if (c <= 256) return plan_norm<T, V, 128, 2, 4, BACK>(p, st);
     }
-    if (c <= 512) return plan_norm<T, V, 256, 2, 2>(p, backward, st);
-    if (c <= 1024) return plan_norm<T, V, 512, 2, 2>(p, backward, st);
-    return plan_norm<T, V, 512, 8, 0>(p, backward, st);
+    if (c <= 512) return plan_norm<T, V, 256, 2, 2, BACK>(p, st);
+    if (c <= 1024) return plan_norm<T, V, 512, 2, 2, BACK>(p, st);
+    return plan_norm<T, V, 512, 8, 0, BACK>(p, st);
 }
 
 // Shifted rows of kShiftMin to kShiftMax pieces: 100000 x 1465 fp16 271 us forward and 301 backward, value by value 303 and
@@ -469,22 +475,22 @@ constexpr uint32_t kShiftMin = 129, kShiftMax = 1024;
 
 inline uint32_t shifted_pieces(uint32_t dim, uint32_t v) { return (dim + 2 * v - 2) / v; }   // at the largest shift
 
-template <typename T> int norm_shifted(NormParams &p, bool backward, cudaStream_t st)
+template <typename T, bool BACK> int norm_shifted(NormParams &p, cudaStream_t st)
 {
     constexpr int V = 16 / sizeof(T);
     const uint32_t c = shifted_pieces(p.dim, V), blocks = norm_parts(p.n, 1);
-    if (c <= 256) return run_norm<T, V, 256, 1, 4, true>(p, blocks, backward, st);
-    if (c <= 512) return run_norm<T, V, 256, 2, 2, true>(p, blocks, backward, st);
-    return run_norm<T, V, 512, 2, 2, true>(p, blocks, backward, st);
+    if (c <= 256) return run_norm<T, V, 256, 1, 4, true, BACK>(p, blocks, st);
+    if (c <= 512) return run_norm<T, V, 256, 2, 2, true, BACK>(p, blocks, st);
+    return run_norm<T, V, 512, 2, 2, true, BACK>(p, blocks, st);
 }
 
-template <typename T> int norm_dispatch(NormParams &p, bool vec, bool shift, bool backward, cudaStream_t st)
+template <typename T, bool BACK> int norm_dispatch(NormParams &p, bool vec, bool shift, cudaStream_t st)
 {
-    if (vec) return norm_pieces<T>(p, backward, st);
-    if (shift) return norm_shifted<T>(p, backward, st);
-    if (p.dim <= 128) return plan_norm<T, 1, 32, 4, 0>(p, backward, st);
-    if (p.dim <= 512) return plan_norm<T, 1, 128, 4, 0>(p, backward, st);
-    return plan_norm<T, 1, 256, 8, 0>(p, backward, st);
+    if (vec) return norm_pieces<T, BACK>(p, st);
+    if (shift) return norm_shifted<T, BACK>(p, st);
+    if (p.dim <= 128) return plan_norm<T, 1, 32, 4, 0, BACK>(p, st);
+    if (p.dim <= 512) return plan_norm<T, 1, 128, 4, 0, BACK>(p, st);
+    return plan_norm<T, 1, 256, 8, 0, BACK>(p, st);
 }
 
 int check_norm(const k2t_norm *a)
@@ -519,9 +525,13 @@ int dispatch(const k2t_norm *a, NormParams &p, bool backward, cudaStream_t st)
     const uint32_t c = shifted_pieces(a->dim, 16 / size);
     const bool shift = !vec && !few && !(all & 15) && c >= kShiftMin && c <= kShiftMax;
     if (!vec && !shift && !few && !fill) return norm_ragged(p, a->dtype, backward, st);
-    if (a->dtype == K2T_BF16) return norm_dispatch<__nv_bfloat16>(p, vec, shift, backward, st);
-    if (a->dtype == K2T_FP16) return norm_dispatch<__half>(p, vec, shift, backward, st);
-    return norm_dispatch<float>(p, vec, shift, backward, st);
+    const auto run = [&](auto zero) {
+        using T = decltype(zero);
+        return backward ? norm_dispatch<T, true>(p, vec, shift, st) : norm_dispatch<T, false>(p, vec, shift, st);
+    };
+    if (a->dtype == K2T_BF16) return run(__nv_bfloat16());
+    if (a->dtype == K2T_FP16) return run(__half());
+    return run(0.0f);
 }
 
 }  // namespace
