@@ -163,7 +163,7 @@ template <typename T, int VEC, int TPR, int PER, int TENSORS, int AHEAD, bool SH
 };
 
 // A thread's piece of a row: columns c .. c + VEC - 1.  Of a shifted row's first piece only the last values are its own,
-// of its last only the first ones; rows of kShiftMin pieces have none that is both.
+// of its last only the first ones; rows this long have none that is both.
 template <typename T, int VEC, bool SHIFT> struct Piece {
     int c, dim;
     __device__ __forceinline__ Piece(int first, uint32_t d) : c(first), dim((int)d) {}
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
 // dx = rstd (w dy - c1 - xh c2) + dz with c1 = mean(w dy), c2 = mean(w dy xh);
 // part[block][0 | 1][dim]: the block's sums of dy xh and dy.
 template <typename T, int VEC, int TPR, int PER, int AHEAD, bool SHIFT>
-__global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 || PER > 1 ? 1 : 3) norm_bwd_kernel(const __grid_constant__ NormParams p)
+__global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 ? 1 : PER > 1 ? 2 : 3) norm_bwd_kernel(const __grid_constant__ NormParams p)
 {
     using P = Pack<T, VEC>;
     using Gr = Group<TPR>;
@@ -441,44 +441,39 @@ template <typename T, int VEC, int TPR, int PER, int AHEAD, bool BACK> int plan_
     return run_norm<T, VEC, TPR, PER, 0, false, BACK>(p, blocks, st);
 }
 
-// Threads a row: as few as hold it, up to a block, then more loads a thread.
-// Forward with two pieces a thread (2^17 x 2048 bf16: 248 us, one piece 261),
-// backward with one, which leaves registers for more rows at once (2^18 x 1024
-// bf16: 400 us, two pieces 485).
+// Threads a row: as few as hold it with two pieces each, up to a block, then more loads a thread.  Two pieces spread the
+// work of a row that does not grow with it, in registers of which every thread has 128 backward (2^18 x 1024 bf16: 325 us,
+// one piece 365; 2^20 x 256: 326 and 354); rows of 8 pieces only lose threads (2^20 x 64: 131 us, one piece 108).
 template <typename T, bool BACK> int norm_pieces(NormParams &p, cudaStream_t st)
 {
     constexpr int V = 16 / sizeof(T);
     const uint32_t c = p.dim / V;
-    if constexpr (BACK) {
+    constexpr int A = BACK ? 2 : 4;                        // rows ahead
+    if constexpr (BACK)
         if (c <= 8) return plan_norm<T, V, 8, 1, 4, BACK>(p, st);
-        if (c <= 16) return plan_norm<T, V, 16, 1, 4, BACK>(p, st);
-        if (c <= 32) return plan_norm<T, V, 32, 1, 4, BACK>(p, st);
-        if (c <= 64) return plan_norm<T, V, 64, 1, 4, BACK>(p, st);
-        if (c <= 128) return plan_norm<T, V, 128, 1, 4, BACK>(p, st);
-        if (c <= 256) return plan_norm<T, V, 256, 1, 4, BACK>(p, st);
-    } else {
-        if (c <= 16) return plan_norm<T, V, 8, 2, 4, BACK>(p, st);
-        if (c <= 32) return plan_norm<T, V, 16, 2, 4, BACK>(p, st);
-        if (c <= 64) return plan_norm<T, V, 32, 2, 4, BACK>(p, st);
-        if (c <= 128) return plan_norm<T, V, 64, 2, 4, BACK>(p, st);
-        if (c <= 256) return plan_norm<T, V, 128, 2, 4, BACK>(p, st);
-    }
+    if (c <= 16) return plan_norm<T, V, 8, 2, A, BACK>(p, st);
+    if (c <= 32) return plan_norm<T, V, 16, 2, A, BACK>(p, st);
+    if (c <= 64) return plan_norm<T, V, 32, 2, A, BACK>(p, st);
+    if (c <= 128) return plan_norm<T, V, 64, 2, A, BACK>(p, st);
+    if (c <= 256) return plan_norm<T, V, 128, 2, A, BACK>(p, st);
     if (c <= 512) return plan_norm<T, V, 256, 2, 2, BACK>(p, st);
     if (c <= 1024) return plan_norm<T, V, 512, 2, 2, BACK>(p, st);
     return plan_norm<T, V, 512, 8, 0, BACK>(p, st);
 }
 
-// Shifted rows of kShiftMin to kShiftMax pieces: 100000 x 1465 fp16 271 us forward and 301 backward, value by value 303 and
-// in stretches 393; 65536 x 3999 bf16 390 and 609, in stretches 610 and 1118.  In shorter rows the two edges cost more than
-// the wide loads give (200000 x 333 fp32 175 and 207 us, in stretches 148 and 188).
-constexpr uint32_t kShiftMin = 129, kShiftMax = 1024;
-
+// Shifted rows, forward of more than 512 values and backward of 97 pieces, up to 1024 pieces: 200000 x 513 fp16 229 us
+// forward, value by value 438; 200000 x 777 bf16 321 and 318, value by value 541 and in stretches 502; 65536 x 3999 bf16
+// 338 and 432, in stretches 611 and 1117.  In shorter rows the two edges cost more than the wide loads give (200000 x 513
+// fp16 backward 315 us, in stretches 275; 200000 x 333 fp32 172 and 207, in stretches 148 and 187).  One piece a thread
+// up to 256 (100000 x 1465 fp16: 259 and 283 us, two pieces 284 and 332): an edge holds up fewer others.
+inline bool shift_pays(uint32_t dim, uint32_t pieces, bool backward) { return (backward ? pieces > 96 : dim > 512) && pieces <= 1024; }
 inline uint32_t shifted_pieces(uint32_t dim, uint32_t v) { return (dim + 2 * v - 2) / v; }   // at the largest shift
 
 template <typename T, bool BACK> int norm_shifted(NormParams &p, cudaStream_t st)
 {
     constexpr int V = 16 / sizeof(T);
     const uint32_t c = shifted_pieces(p.dim, V), blocks = norm_parts(p.n, 1);
+    if (c <= 128) return run_norm<T, V, 128, 1, 4, true, BACK>(p, norm_parts(p.n, Group<128>::kGroups), st);
     if (c <= 256) return run_norm<T, V, 256, 1, 4, true, BACK>(p, blocks, st);
     if (c <= 512) return run_norm<T, V, 256, 2, 2, true, BACK>(p, blocks, st);
     return run_norm<T, V, 512, 2, 2, true, BACK>(p, blocks, st);
@@ -519,11 +514,11 @@ int dispatch(const k2t_norm *a, NormParams &p, bool backward, cudaStream_t st)
     p.rstd = a->rstd;
     // Rows that are not whole pieces: shifted where that pays; else value by value while there are few of them, when a call
     // is its latency (4999 x 333 fp32, training: 15 us against 20), else in stretches (200000 x 333 bf16, forward: 170 us
-    // against 220; 65536 x 3999: 610 us against 2335).  Forward rows of 513 to 2048 values fill a block with single values
-    // and stay with them (100000 x 1465 fp16: 303 us against 417; backward 422 against 392).
-    const bool few = a->n_rows <= 16384 && a->dim <= 2048, fill = !backward && a->dim > 512 && a->dim <= 2048;
+    // against 220; 65536 x 3999: 610 us against 2335).  Forward rows of 1025 to 2048 values fill a block with single values
+    // and stay with them (100000 x 1465 fp16: 308 us against 417; backward 422 against 393).
+    const bool few = a->n_rows <= 16384 && a->dim <= 2048, fill = !backward && a->dim > 1024 && a->dim <= 2048;
     const uint32_t c = shifted_pieces(a->dim, 16 / size);
-    const bool shift = !vec && !few && !(all & 15) && c >= kShiftMin && c <= kShiftMax;
+    const bool shift = !vec && !few && !(all & 15) && shift_pays(a->dim, c, backward);
     if (!vec && !shift && !few && !fill) return norm_ragged(p, a->dtype, backward, st);
     const auto run = [&](auto zero) {
         using T = decltype(zero);
