@@ -89,7 +89,7 @@ void make_plan(const k2t_attn *a, bool backward, Plan &pl)
         p.splits = pick_splits((uint64_t)p.hkv * groups, p.tiles);
         p.hist_parts = p.splits * groups;
         pl.part_floats = p.splits > 1 ? p.splits * rows * p.d : 0;
-        pl.ml_floats = p.hist_parts > 1 ? (uint64_t)p.hist_parts * p.hq * p.buckets : 0;
+        pl.ml_floats = (uint64_t)p.hist_parts * p.hq * p.buckets;
         pl.info_floats = p.row_tiles <= fused ? 0 : (uint64_t)p.hkv * p.row_tiles * (sizeof(RowInfo) / 4);
         return;
     }

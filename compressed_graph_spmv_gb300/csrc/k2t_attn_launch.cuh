@@ -108,8 +108,8 @@ template <typename T> int launch_backward(const AttnParams &p, cudaStream_t st)
     }
     int rc = p.d <= 64 ? backward_dim<T, 64>(p, st) : backward_dim<T, 128>(p, st);
     if (rc) return rc;
-    const uint64_t rows = p.splits > 1 ? (uint64_t)p.T * p.hq : 0, cells = p.hist_parts > 1 ? (uint64_t)p.hq * p.buckets : 0;
-    return rows + cells ? next_launch(attn_bwd_join_kernel<T>, dim3((unsigned)(rows + cells)), 256, 0, p, st) : K2T_OK;
+    const uint64_t rows = p.splits > 1 ? (uint64_t)p.T * p.hq : 0, blocks = (rows + 3) / 4 + (p.buckets ? p.hq : 0);
+    return blocks ? next_launch(attn_bwd_join_kernel<T>, dim3((unsigned)blocks), kJoinThreads, 0, p, st) : K2T_OK;
 }
 
 }  // namespace k2t

@@ -201,6 +201,20 @@ def test_masked_buckets(dtype, T, value):
     assert (got["dbias"][:, 2] == 0).all() and (got["dbias"][1] == 0).all()
 
 
+@pytest.mark.parametrize("T,n,hq,hkv,d,sources,buckets,mapped", [
+    (3, 41, 1, 1, 128, 3, 6, False), (121, 66, 4, 4, 128, 18, 2, True), (387, 1498, 8, 8, 64, 13, 2, True),
+    (8, 3, 2, 1, 64, 8, 32, False), (40, 9000, 8, 2, 72, 5, 64, True), (1, 1, 2, 2, 64, 1, 3, False), (2, 300000, 3, 3, 40, 2, 1, False)])
+def test_bias_gradients_add_up_to_zero(T, n, hq, hkv, d, sources, buckets, mapped):
+    """A row's weights always sum to 1, so shifting all buckets of a head changes nothing."""
+    p = problem(T, n, hq, hkv, d, sources, buckets, "bf16", mapped, seed=T + n)
+    got = run(p, "bf16")
+    db = f64(got["dbias"])
+    # each value is rounded once (2^-9 of it); the sums before it have 32 bits, and no value exceeds the largest of dout . v
+    most = np.abs(f64(p["dout"])).sum(axis=2).max() * np.abs(f64(p["v"])).max()
+    assert (np.abs(db.sum(axis=1)) <= 2.0 ** -9 * np.abs(db).sum(axis=1) + 2.0 ** -20 * T * most).all()
+    check(p, "bf16", got)
+
+
 @pytest.mark.parametrize("T", [6, 100])
 def test_unseen_nodes_may_hold_anything(T):
     p = problem(T, 333, 4, 2, 128, 6, 5, "bf16", False, seed=17) if T <= 6 else problem(T, 333, 4, 2, 128, 6, 5, "bf16", True, seed=17)
