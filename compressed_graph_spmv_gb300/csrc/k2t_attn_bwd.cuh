@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tc::grid_wait();
+    tc::grid_next();                    // the joining kernel may start on SMs that this one leaves free
     for (uint32_t r = 0; r < rts; ++r) {
         const uint32_t at = sm + S::kRow + r * 2 * S::kRowTile;
         copy_row_tile<DP>(at, p.q, p.q_row, p.q_head, hk * p.group, rt0 + r, p, tid, kBwdThreads);
@@ -701,7 +702,7 @@ __device__ __forceinline__ void pair_at(const AttnParams &p, uint32_t j, uint32_
 }
 
 // dq = scale * sum over splits; dbias = sum over splits and row groups, in a fixed order.
-// Blocks [0, ceil(T * hq / 4)): four rows of dq each; then one block per head of dbias.
+// One block per head of dbias, which take longest, then one per four rows of dq (with one split, dq is written already).
 //
 // The ds of a row add up to 0, and so do a head's buckets.  What is left of them is what rounding delta (from a rounded
 // out) and ds to 16 bits has added, and where few buckets hold most of the probability that is much of their sums: each
@@ -711,15 +712,16 @@ template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) attn_bwd_join_kernel(const __grid_constant__ AttnParams p)
 {
     const int tid = threadIdx.x;
-    tc::grid_wait();
-    const uint64_t rows = p.splits > 1 ? (uint64_t)p.T * p.hq : 0, row_blocks = (rows + 3) / 4;   // one split: dq is written already
-    if (blockIdx.x < row_blocks) {
-        const uint64_t row = (uint64_t)blockIdx.x * 4 + (tid >> 8);
+    const uint32_t heads = p.buckets ? p.hq : 0;
+    if (blockIdx.x >= heads) {
+        tc::grid_wait();
+        const uint64_t rows = (uint64_t)p.T * p.hq, row = (uint64_t)(blockIdx.x - heads) * 4 + (tid >> 8);
         const uint32_t in = tid & 255;
         __shared__ float4 sum[kJoinThreads];
         const uint32_t q4 = p.d / 4, groups = 256 / q4, c = in % q4, g = in / q4;
         float4 acc = make_float4(0, 0, 0, 0);
         if (g < groups && row < rows)
+#pragma unroll 4
             for (uint32_t s = g; s < p.splits; s += groups) {
                 const float4 x = *reinterpret_cast<const float4 *>(p.part + (s * rows + row) * p.d + c * 4);
                 acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
@@ -741,8 +743,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_bwd_join_kernel(const __gri
     }
     __shared__ float weight[kPairs], sum_of[K2T_ATTN_MAX_BUCKETS], share_of[K2T_ATTN_MAX_BUCKETS];
     __shared__ uint32_t bucket_of[kPairs];
-    const uint32_t hd = (uint32_t)(blockIdx.x - row_blocks);
-    // the pairs' probabilities, eight threads a pair
+    const uint32_t hd = blockIdx.x;
+    // The pairs' probabilities, eight threads a pair.  These read only what was there before the kernel that this one waits
+    // for began, so they go on beside its last blocks.
     const uint64_t pairs = (uint64_t)p.T * p.n;
 #pragma unroll 2
     for (uint32_t j = tid >> 3; j < kPairs; j += kJoinThreads / 8) {
@@ -783,6 +786,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_bwd_join_kernel(const __gri
             weight[j] = w, bucket_of[j] = b;
         }
     }
+    tc::grid_wait();
     // W neighbour threads of a warp a bucket
     uint32_t W = 32;
     while (W * p.buckets > kJoinThreads) W >>= 1;
