@@ -28,7 +28,7 @@ SOURCES = ["k2t_host.cpp", "k2t_device.cu", "k2t_sr_plus_times.cu", "k2t_sr_bool
            "k2t_static.cu", "k2t_product.cu", "k2t_attn.cu", "k2t_attn_bf16.cu", "k2t_attn_fp16.cu", "k2t_norm.cu",
            "k2t_norm_ragged.cu"]
 PROBE_SOURCES = [os.path.join("probe", "k2t_probe.cu")]
-HEADERS = ["k2t_internal.h", "k2t_kernels.cuh", "k2t_attn.cuh", "k2t_attn_fwd.cuh", "k2t_attn_bwd.cuh",
+HEADERS = ["k2t_internal.h", "k2t_kernels.cuh", "k2t_attn.cuh", "k2t_attn_fwd.cuh", "k2t_attn_bwd.cuh", "k2t_attn_delta.cuh",
            "k2t_attn_launch.cuh", "k2t_norm.cuh", "k2t_tc.cuh", os.path.join("..", "..", "include", "k2t.h")]
 
 

@@ -59,7 +59,7 @@ uint32_t pick_splits(uint64_t blocks, uint64_t tiles)
 struct Plan {
     AttnParams p;
     int bm;
-    uint64_t part_floats, ml_floats, info_floats;
+    uint64_t part_floats, ml_floats, info_floats, delta_floats;
 };
 
 void make_plan(const k2t_attn *a, bool backward, Plan &pl)
@@ -81,7 +81,13 @@ void make_plan(const k2t_attn *a, bool backward, Plan &pl)
     p.scale_log2 = a->scale * kLog2e;
     p.tiles = (p.n + kTcTile - 1) / kTcTile;
     const uint64_t rows = (uint64_t)p.T * p.hq;
+    pl.delta_floats = 0;
     if (backward) {
+        if (p.buckets && p.T && p.n) {
+            p.delta_tiles = (p.rows + delta_rows(p) - 1) / delta_rows(p);
+            p.delta_splits = pick_splits((uint64_t)p.hkv * p.delta_tiles, p.tiles);
+            pl.delta_floats = p.delta_splits * rows * 2;
+        }
         const uint32_t per = kBwdRows / p.group;              // whole queries of a row tile
         p.row_tiles = std::max(1u, (p.T + per - 1) / per);
         const uint32_t fused = bwd_fused_tiles(p.d), held = p.row_tiles <= fused ? fused : 4;
@@ -137,7 +143,8 @@ constexpr uint64_t kWorkHead = 256;   // the device status word
 
 uint64_t plan_bytes(const Plan &pl)
 {
-    return kWorkHead + align_up(pl.part_floats * 4, 256) + align_up(pl.ml_floats * 4, 256) + align_up(pl.info_floats * 4, 256);
+    return kWorkHead + align_up(pl.part_floats * 4, 256) + align_up(pl.ml_floats * 4, 256) + align_up(pl.info_floats * 4, 256) +
+           align_up(pl.delta_floats * 4, 256);
 }
 
 int check_call(const k2t_attn *a, const void *work, uint64_t work_bytes, const Plan &pl)
@@ -172,7 +179,9 @@ void fill_pointers(const k2t_attn *a, void *work, Plan &pl)
     char *w = static_cast<char *>(work) + kWorkHead;
     p.part = reinterpret_cast<float *>(w);
     p.part_ml = reinterpret_cast<float *>(w + align_up(pl.part_floats * 4, 256));
-    p.row_info = reinterpret_cast<float *>(w + align_up(pl.part_floats * 4, 256) + align_up(pl.ml_floats * 4, 256));
+    w += align_up(pl.part_floats * 4, 256) + align_up(pl.ml_floats * 4, 256);
+    p.row_info = w;
+    p.delta_part = reinterpret_cast<float2 *>(w + align_up(pl.info_floats * 4, 256));
     uint32_t b = 0;
     for (uint32_t x = 0; x < 256; ++x) {
         while (b + 1 < a->n_buckets && a->edges[b + 1] <= x) ++b;

@@ -54,8 +54,10 @@ struct AttnParams {
     float *part;              // partial sums: see the kernels
     float *part_ml;
     void *row_info;           // RowInfo[hkv][row_tiles * 32] (backward)
+    float2 *delta_part;       // [delta_splits][T][hq]: sums of p dp and of p
+    uint32_t delta_splits, delta_tiles;   // of attn_delta_kernel; 0: delta is dout . out
     uint32_t hist_parts;      // partial dbias tables
-    uint32_t hist_tables;     // tables a thread sums by bucket into, 1 or 2
+    uint32_t hist_threads;    // threads that sum by bucket, 128 or 64
     CUtensorMap dk_map, dv_map;   // (head_dim, kv heads, nodes), boxes of 64 x 1 x 128 (backward)
     uint32_t *status;         // device status word, at the start of the work buffer
     uint8_t bucket_of[256];   // bucket of each hop count; larger hops share the last

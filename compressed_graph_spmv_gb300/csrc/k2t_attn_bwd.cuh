@@ -1,13 +1,16 @@
 // k2t_attn_bwd.cuh -- backward pass of the hop-biased attention on tcgen05.
 //
-// With p = exp(s - lse), delta = dout . out and dp = dout . v:
+// With p = exp(s - lse), dp = dout . v and delta = sum p dp = dout . out:
 //   ds = p (dp - delta),  dv = sum p dout,  dk = scale sum ds q,
 //   dq = scale sum ds k,  dbias[bucket] = sum ds.
+// delta comes from attn_delta_kernel where there is a bias table.
 // Everything is computed transposed, 128 nodes x 32 rows a unit: S^T = K Q^T
 // and dP^T = V dO^T come out of tensor memory one node a thread; P^T and dS^T
 // go back over them as A operands of dV += P^T dO and dK += dS^T Q (nodes x
 // head_dim), and dS^T goes to shared memory as B operand of
-// dQ^T += K^T dS (head_dim x rows) and for the sums by bucket.
+// dQ^T += K^T dS (head_dim x rows) and for the sums by bucket.  As an operand it
+// is rounded to the element type; the sums by bucket add what that took off,
+// itself rounded, so that they sum 16 bits or more of each term.
 //
 // attn_bwd_nodes_kernel streams nodes past up to RT row tiles that stay: dQ^T
 // accumulates in tensor memory over all nodes of the block, and (DKV) dV and
@@ -50,6 +53,36 @@ struct RowInfo {
     uint32_t place[kBwdRows];              // column | head << 16
 };
 
+// delta of query t, head hd, by L neighbour lanes (x: this one of them): the sums over nodes that attn_delta_kernel left, or
+// dout . out without them; 0 for a query that does not exist or saw nothing.
+template <typename T, int L>
+__device__ __forceinline__ float row_delta(const AttnParams &p, uint32_t t, uint32_t hd, int x, uint32_t lanes)
+{
+    float s = 0.0f, m = p.delta_splits ? 0.0f : 1.0f / L;
+    if (t < p.T) {
+        if (p.delta_splits) {
+            for (uint32_t i = x; i < p.delta_splits; i += L) {
+                const float2 v = p.delta_part[((uint64_t)i * p.T + t) * p.hq + hd];
+                s += v.x, m += v.y;
+            }
+        } else {
+            const T *o = static_cast<const T *>(p.out) + (int64_t)t * p.out_row + (int64_t)hd * p.out_head;
+            const T *d = static_cast<const T *>(p.dout) + (int64_t)t * p.dout_row + (int64_t)hd * p.dout_head;
+            for (uint32_t k = x * 8; k < p.d; k += L * 8) {
+                const uint4 a = __ldg(reinterpret_cast<const uint4 *>(o + k)), b = __ldg(reinterpret_cast<const uint4 *>(d + k));
+                const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 u = Elem<T>::unpack(aw[e]), v = Elem<T>::unpack(bw[e]);
+                    s = fmaf(u.x, v.x, fmaf(u.y, v.y, s));
+                }
+            }
+        }
+    }
+    for (int y = L / 2; y; y >>= 1) s += __shfl_xor_sync(lanes, s, y), m += __shfl_xor_sync(lanes, m, y);
+    return m == 0.0f ? 0.0f : s / m;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ AttnParams p)
 {
@@ -62,14 +95,7 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
     uint32_t place = 0;
     if (c < per * G && t < p.T) {
         const uint32_t hd = hk * G + g;
-        const T *o = static_cast<const T *>(p.out) + (int64_t)t * p.out_row + (int64_t)hd * p.out_head;
-        const T *d = static_cast<const T *>(p.dout) + (int64_t)t * p.dout_row + (int64_t)hd * p.dout_head;
-        for (uint32_t x = lane * 2; x < p.d; x += 64) {
-            const float2 a = Elem<T>::unpack(*reinterpret_cast<const uint32_t *>(o + x));
-            const float2 b = Elem<T>::unpack(*reinterpret_cast<const uint32_t *>(d + x));
-            s = fmaf(a.x, b.x, fmaf(a.y, b.y, s));
-        }
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
+        s = row_delta<T, 32>(p, t, hd, lane, ~0u);
         const float l = p.lse[(uint64_t)t * p.hq + hd];
         if (l != -INFINITY) lse = l * kLog2e;
         place = row_column(p, t * G) * kTcPitch | (g * 4) << 16;
@@ -96,16 +122,16 @@ __device__ __forceinline__ void copy_row_tile(uint32_t dst, const void *base, in
 
 // A unit's softmax step for one node: S^T and dP^T at `at` (32 columns each, a row of the tile a column) become P^T
 // and dS^T in the element type, two rows a column; ds: this node's row of dS^T in shared memory, from chunk `chunk` on
-// (null: not wanted); bt: the node's bytes in the bucket tile (column 0); lut: bias table, bytes.
+// (null: not wanted), and `rest` bytes on what the rounding took off, itself rounded (rest 0: not wanted); bt: the node's bytes in the bucket tile (column 0); lut: bias table, bytes.
 // Eight rows at a time in a rolled loop: the warps of an SM run half a dozen different loops, and the instruction
 // caches hold them only while each is small.
 template <typename T>
 __device__ __forceinline__ void unit32(uint32_t at, const RowInfo *info, bool plain, float scale, const uint8_t *bt,
-                                       const uint8_t *lut, uint32_t shift, uint8_t *ds, uint32_t chunk, uint32_t node)
+                                       const uint8_t *lut, uint32_t shift, uint8_t *ds, uint32_t rest, uint32_t chunk, uint32_t node)
 {
 #pragma unroll 1
     for (int r0 = 0; r0 < kBwdRows; r0 += 8) {
-        uint32_t s[8], d[8], pw[4], dw[4];
+        uint32_t s[8], d[8], pw[4], dw[4], rw[4];
         tc::ld8(s, at + r0);
         tc::ld8(d, at + 32 + r0);
         float b[8] = {};
@@ -136,11 +162,17 @@ __device__ __forceinline__ void unit32(uint32_t at, const RowInfo *info, bool pl
             for (int y = 0; y < 2; ++y) {
                 pw[e / 2 + y] = Elem<T>::pack(pv[2 * y], pv[2 * y + 1]);
                 dw[e / 2 + y] = Elem<T>::pack(dv[2 * y], dv[2 * y + 1]);
+                const float2 kept = Elem<T>::unpack(dw[e / 2 + y]);
+                rw[e / 2 + y] = Elem<T>::pack(dv[2 * y] - kept.x, dv[2 * y + 1] - kept.y);
             }
         }
         tc::st4(at + r0 / 2, pw);
         tc::st4(at + 32 + r0 / 2, dw);
-        if (ds) *reinterpret_cast<uint4 *>(ds + (((chunk + r0 / 8) ^ (node & 7)) << 4)) = make_uint4(dw[0], dw[1], dw[2], dw[3]);
+        if (ds) {
+            uint8_t *to = ds + (((chunk + r0 / 8) ^ (node & 7)) << 4);
+            *reinterpret_cast<uint4 *>(to) = make_uint4(dw[0], dw[1], dw[2], dw[3]);
+            if (rest) *reinterpret_cast<uint4 *>(to + rest) = make_uint4(rw[0], rw[1], rw[2], rw[3]);
+        }
     }
 }
 
@@ -192,7 +224,7 @@ template <int DP, int RT, bool DKV> struct BwdSmem {
     static constexpr int kRowTile = kBwdRows * DP * 2;                        // q or dout of a row tile
     static constexpr int kRow = kSlots * kSlot;                               // [RT][q | dout]
     static constexpr int kDs = kRow + RT * 2 * kRowTile;                      // dS^T [node][unit parity][32 rows]
-    static constexpr int kBuckets = kDs + kPanel;
+    static constexpr int kBuckets = kDs + 2 * kPanel;                         // after what rounding took off dS^T
     static constexpr int kInfo = kBuckets + kBufs * 33 * kTcPitch;
     static constexpr int kCtl = kInfo + RT * (int)sizeof(RowInfo);
     struct Ctl {
@@ -203,10 +235,10 @@ template <int DP, int RT, bool DKV> struct BwdSmem {
         uint8_t byte_of[257 + 15];
     };
     static constexpr int kLut = kCtl + (int)((sizeof(Ctl) + 15) / 16 * 16);
-    // tables: for the sums by bucket, of each of 128 threads
-    static size_t bytes(const AttnParams &p, uint32_t tables)
+    // threads: those that sum by bucket, a table each
+    static size_t bytes(const AttnParams &p, uint32_t threads)
     {
-        return kLut + ((size_t)(p.buckets + 2) * p.group2 + (p.buckets ? (size_t)(p.buckets + 2) * 128 * tables : 0)) * 4;
+        return kLut + ((size_t)(p.buckets + 2) * p.group2 + (p.buckets ? (size_t)(p.buckets + 2) * threads : 0)) * 4;
     }
 };
 
@@ -221,7 +253,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
     extern __shared__ __align__(1024) uint8_t smem[];
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + S::kCtl);
     const uint32_t sm = tc::saddr(smem);
-    float *lut = reinterpret_cast<float *>(smem + S::kLut), *hist = lut + (p.buckets + 2) * p.group2;   // [bucket byte][table][thread]
+    float *lut = reinterpret_cast<float *>(smem + S::kLut), *hist = lut + (p.buckets + 2) * p.group2;   // [bucket byte][thread]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t hk = blockIdx.y, split = blockIdx.x % p.splits, rows_of = blockIdx.x / p.splits;
     const uint32_t rt0 = rows_of * RT, rts = min((uint32_t)RT, p.row_tiles - rt0);      // row tiles of this block
@@ -235,9 +267,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
         for (int i = 0; i < S::kSlots; ++i) tc::bar_init(&ctl->full[i], 128), tc::bar_init(&ctl->empty[i], 1);
         for (int i = 0; i < S::kBufs; ++i) {
             tc::bar_init(&ctl->hop_full[i], 4);
-            tc::bar_init(&ctl->hop_empty[i], rts * (p.buckets ? 8 : 4));
+            tc::bar_init(&ctl->hop_empty[i], rts * (4 + (p.buckets ? p.hist_threads / 32 : 0)));
         }
-        for (int i = 0; i < 2; ++i) tc::bar_init(&ctl->sp_full[i], 1), tc::bar_init(&ctl->ds_full[i], 128), tc::bar_init(&ctl->hist_done[i], 4);
+        for (int i = 0; i < 2; ++i) tc::bar_init(&ctl->sp_full[i], 1), tc::bar_init(&ctl->ds_full[i], 128), tc::bar_init(&ctl->hist_done[i], p.hist_threads / 32);
         tc::bar_init(&ctl->tile_full, 1);
         tc::bar_init(&ctl->tile_empty, 128);
         tc::bar_init(&ctl->staged, 128);
@@ -247,7 +279,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tc::grid_wait();
-    tc::grid_next();                    // the joining kernel may start on SMs that this one leaves free
     for (uint32_t r = 0; r < rts; ++r) {
         const uint32_t at = sm + S::kRow + r * 2 * S::kRowTile;
         copy_row_tile<DP>(at, p.q, p.q_row, p.q_head, hk * p.group, rt0 + r, p, tid, kBwdThreads);
@@ -258,7 +289,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
         for (int i = tid; i < 257; i += kBwdThreads) ctl->byte_of[i] = i ? p.bucket_of[i - 1] + 1 : 0;
     fill_bias<T>(lut, p, hk, tid, p.group2);
     if (p.buckets)
-        for (uint32_t i = tid; i < (p.buckets + 2) * 128 * p.hist_tables; i += kBwdThreads) hist[i] = 0.0f;
+        for (uint32_t i = tid; i < (p.buckets + 2) * p.hist_threads; i += kBwdThreads) hist[i] = 0.0f;
     RowInfo *info = reinterpret_cast<RowInfo *>(smem + S::kInfo);
     __syncthreads();
     auto seen_by = [&](uint32_t place) {
@@ -272,21 +303,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
             const uint32_t c = at % kBwdRows, per = kBwdRows / p.group, t = (rt0 + at / kBwdRows) * per + c / p.group, g = c % p.group;
             const bool on = c < per * p.group && t < p.T;
             const uint32_t hd = hk * p.group + g;
-            float s = 0.0f;
-            if (on) {
-                const T *o = static_cast<const T *>(p.out) + (int64_t)t * p.out_row + (int64_t)hd * p.out_head;
-                const T *d = static_cast<const T *>(p.dout) + (int64_t)t * p.dout_row + (int64_t)hd * p.dout_head;
-                for (uint32_t x = (tid & 7) * 8; x < p.d; x += 64) {
-                    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(o + x)), b = __ldg(reinterpret_cast<const uint4 *>(d + x));
-                    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 u = Elem<T>::unpack(aw[e]), v = Elem<T>::unpack(bw[e]);
-                        s = fmaf(u.x, v.x, fmaf(u.y, v.y, s));
-                    }
-                }
-            }
-            for (int x = 4; x; x >>= 1) s += __shfl_xor_sync(0xffu << (lane & 24), s, x);
+            const float s = row_delta<T, 8>(p, on ? t : p.T, hd, tid & 7, 0xffu << (lane & 24));
             if ((tid & 7) == 0) {
                 RowInfo *to = info + at / kBwdRows;
                 float lse = INFINITY;
@@ -331,7 +348,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
             tc::fence_after();
             const bool plain = !p.sources && (tile_at(i) + 1) * kTcTile <= p.n;
             unit32<T>(at, info + r, plain, p.scale_log2, smem + S::kBuckets + buf * 33 * kTcPitch + l,
-                      reinterpret_cast<const uint8_t *>(lut), shift, ds, w * 4, l);
+                      reinterpret_cast<const uint8_t *>(lut), shift, ds, p.buckets ? S::kPanel : 0, w * 4, l);
             tc::wait_st();
             tc::fence_async();
             tc::fence_before();
@@ -401,42 +418,46 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
             }
         }
     } else if (warp < 24) {
-        // ---- sums of ds by bucket: thread = (row of the tile, quarter of the nodes), with a table of its own ----
+        // ---- sums of ds by bucket: thread = (row of the tile, quarter or half of the nodes), with a table of its own ----
         if (p.buckets) {
-            const int t = tid - 640, c = t & 31, part = t >> 5;
+            const int t = tid - 640, c = t & 31, part = t >> 5, parts = p.hist_threads / 32, span = kTcTile / parts;
+            const uint32_t pitch = p.hist_threads * 4;                          // bytes a bucket
             uint8_t *mine = reinterpret_cast<uint8_t *>(hist + t);
             uint32_t i = 0, r = 0;
-            for (uint32_t u = 0; u < units; ++u) {
+            for (uint32_t u = 0; u < units && part < parts; ++u) {
                 const uint32_t w = u & 1, buf = i % S::kBufs;
                 bool ok = tc::bar_wait(&ctl->hop_full[buf], (i / S::kBufs) & 1, gave_up) && tc::bar_wait(&ctl->ds_full[w], (u >> 1) & 1, gave_up);
                 if (!__all_sync(~0u, ok)) break;
-                const uint8_t *bt = smem + S::kBuckets + buf * 33 * kTcPitch + (info[r].place[c] & 0xffff) + part * 32;
-                const uint8_t *ds = smem + S::kDs + part * 32 * 128 + (c & 7) * 2;
+                const uint8_t *bt = smem + S::kBuckets + buf * 33 * kTcPitch + (info[r].place[c] & 0xffff) + part * span;
+                const uint8_t *ds = smem + S::kDs + part * span * 128 + (c & 7) * 2;
                 const uint32_t chunk = w * 4 + (c >> 3);
-                auto term = [&](int node) { return Elem<T>::to_float(*reinterpret_cast<const T *>(ds + node * 128 + ((chunk ^ (node & 7)) << 4))); };
-                if (p.hist_tables == 2) {
-                    // A node is a read, an add and a write of its bucket, which follow the last node's: about 80 clocks.
-                    // With two tables two nodes go on at once (257 tokens over 8191 nodes, forward and backward: 136 us
-                    // with one, 131 us with two).
+                // ds in full: its rounded value and what that took off
+                auto term = [&](int node) {
+                    const uint8_t *at = ds + node * 128 + ((chunk ^ (node & 7)) << 4);
+                    return Elem<T>::to_float(*reinterpret_cast<const T *>(at)) + Elem<T>::to_float(*reinterpret_cast<const T *>(at + S::kPanel));
+                };
+                // A node is a read, an add and a write of its bucket.  Four nodes go on at once: the reads before the first
+                // write, a node that shares the bucket of one before it continues from that one's sum, and the writes in the
+                // nodes' order, so that the last of a bucket stands.  The next four nodes' terms are read meanwhile.
+                uint32_t bw = *reinterpret_cast<const uint32_t *>(bt);
+                float x0 = term(0), x1 = term(1), x2 = term(2), x3 = term(3);
 #pragma unroll 1
-                    for (int k = 0; k < 16; k += 4) {
-                        const uint32_t b0 = *reinterpret_cast<const uint32_t *>(bt + k), b1 = *reinterpret_cast<const uint32_t *>(bt + k + 16);
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            float *a = reinterpret_cast<float *>(mine + (__byte_perm(b0, 0, 0x4440 + y) << 10));       // 512 bytes a bucket and table
-                            float *b = reinterpret_cast<float *>(mine + (__byte_perm(b1, 0, 0x4440 + y) << 10) + 512);
-                            const float x = *a + term(k + y), z = *b + term(k + 16 + y);
-                            *a = x;
-                            *b = z;
-                        }
-                    }
-                } else {
-#pragma unroll 1
-                    for (int k = 0; k < 32; k += 4) {
-                        const uint32_t bw = *reinterpret_cast<const uint32_t *>(bt + k);
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) *reinterpret_cast<float *>(mine + (__byte_perm(bw, 0, 0x4440 + y) << 9)) += term(k + y);
-                    }
+                for (int k = 0; k < span; k += 4) {
+                    float *a0 = reinterpret_cast<float *>(mine + (bw & 255) * pitch), *a1 = reinterpret_cast<float *>(mine + (bw >> 8 & 255) * pitch);
+                    float *a2 = reinterpret_cast<float *>(mine + (bw >> 16 & 255) * pitch), *a3 = reinterpret_cast<float *>(mine + (bw >> 24) * pitch);
+                    const float s0 = *a0, s1 = *a1, s2 = *a2, s3 = *a3;
+                    const int next = k + 4 < span ? k + 4 : k;
+                    bw = *reinterpret_cast<const uint32_t *>(bt + next);
+                    const float n0 = term(next), n1 = term(next + 1), n2 = term(next + 2), n3 = term(next + 3);
+                    const float v0 = s0 + x0;
+                    const float v1 = (a1 == a0 ? v0 : s1) + x1;
+                    const float v2 = (a2 == a1 ? v1 : a2 == a0 ? v0 : s2) + x2;
+                    const float v3 = (a3 == a2 ? v2 : a3 == a1 ? v1 : a3 == a0 ? v0 : s3) + x3;
+                    *a0 = v0;
+                    *a1 = v1;
+                    *a2 = v2;
+                    *a3 = v3;
+                    x0 = n0, x1 = n1, x2 = n2, x3 = n3;
                 }
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(&ctl->hist_done[w]), tc::bar_arrive(&ctl->hop_empty[buf]);
@@ -451,8 +472,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
                 float s = 0.0f;
                 for (uint32_t q = 0; q < per; ++q)
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        if (x < 4 * (int)p.hist_tables) s += hist[(b + 1) * 128 * p.hist_tables + x * 32 + q * G + g];
+                    for (int x = 0; x < 4; ++x)
+                        if (x < parts) s += hist[(b + 1) * p.hist_threads + x * 32 + q * G + g];
                 out[k] = s;
             }
         }
@@ -597,7 +618,7 @@ __global__ void __launch_bounds__(kBwdRowThreads, 1) attn_bwd_rows_kernel(const 
             if (!ok) break;
             tc::fence_after();
             unit32<T>(tm + lanes + w * 64, reinterpret_cast<const RowInfo *>(smem + S::kInfo) + slot, plain, p.scale_log2,
-                      smem + S::kBuckets + l, reinterpret_cast<const uint8_t *>(lut), shift, nullptr, 0, 0);
+                      smem + S::kBuckets + l, reinterpret_cast<const uint8_t *>(lut), shift, nullptr, 0, 0, 0);
             tc::wait_st();
             tc::fence_before();
             tc::bar_arrive(&ctl->ds_full[w]);
@@ -696,33 +717,16 @@ __global__ void __launch_bounds__(kBwdRowThreads, 1) attn_bwd_rows_kernel(const 
     if (tid == 0 && *gave_up) atomicOr(p.status, K2T_STATUS_WAIT_TIMEOUT);
 }
 
-// Pair j of kPairs (query, node) pairs of a call: every pair where there are no more, else queries in turn and nodes spread
-// by multiples of the golden ratio.
-constexpr uint32_t kJoinThreads = 1024, kPairs = 512;
-__device__ __forceinline__ void pair_at(const AttnParams &p, uint32_t j, uint32_t &t, uint64_t &node)
-{
-    const uint64_t pairs = (uint64_t)p.T * p.n;
-    if (pairs <= kPairs) t = j / (uint32_t)p.n, node = j - t * (uint32_t)p.n;
-    else {
-        t = p.T >= kPairs ? (uint32_t)((uint64_t)j * p.T / kPairs) : j % p.T;
-        node = (uint64_t)(j * 2654435769u) * p.n >> 32;
-    }
-}
-
+constexpr uint32_t kJoinThreads = 1024;
 // dq = scale * sum over splits; dbias = sum over splits and row groups, in a fixed order.
 // One block per head of dbias, which take longest, then one per four rows of dq (with one split, dq is written already).
-//
-// The ds of a row add up to 0, and so do a head's buckets.  What is left of them is what rounding delta (from a rounded
-// out) and ds to 16 bits has added, and where few buckets hold most of the probability that is much of their sums: each
-// gives back its share of it.  Of 3 queries, 41 nodes and 6 buckets, bf16: 0.85% of dbias before, 0.29% with it.  Any shares
-// whose sum is 1 give the buckets their right total, so they are estimated, from the probabilities of kPairs pairs.
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) attn_bwd_join_kernel(const __grid_constant__ AttnParams p)
 {
     const int tid = threadIdx.x;
     const uint32_t heads = p.buckets ? p.hq : 0;
+    tc::grid_wait();
     if (blockIdx.x >= heads) {
-        tc::grid_wait();
         const uint64_t rows = (uint64_t)p.T * p.hq, row = (uint64_t)(blockIdx.x - heads) * 4 + (tid >> 8);
         const uint32_t in = tid & 255;
         __shared__ float4 sum[kJoinThreads];
@@ -749,74 +753,18 @@ __global__ void __launch_bounds__(kJoinThreads) attn_bwd_join_kernel(const __gri
         }
         return;
     }
-    __shared__ float weight[kPairs], sum_of[K2T_ATTN_MAX_BUCKETS], share_of[K2T_ATTN_MAX_BUCKETS];
-    __shared__ uint32_t bucket_of[kPairs];
     const uint32_t hd = blockIdx.x;
-    // The pairs' probabilities, eight threads a pair.  These read only what was there before the kernel that this one waits
-    // for began, so they go on beside its last blocks.
-    const uint64_t pairs = (uint64_t)p.T * p.n;
-#pragma unroll 2
-    for (uint32_t j = tid >> 3; j < kPairs; j += kJoinThreads / 8) {
-        float s = 0.0f, lse = -INFINITY;
-        int32_t hop = -1;
-        if (j < pairs) {
-            uint32_t t;
-            uint64_t node;
-            pair_at(p, j, t, node);
-            const T *q = static_cast<const T *>(p.q) + (int64_t)t * p.q_row + (int64_t)hd * p.q_head;
-            const T *k = static_cast<const T *>(p.k) + (int64_t)node * p.k_row + (int64_t)(hd / p.group) * p.k_head;
-            const uint32_t col = row_column(p, t * p.group);
-            if (col < p.sources) hop = __ldg(p.hops + node * p.sources + col);   // a query without a source has no bias
-            lse = p.lse[(uint64_t)t * p.hq + hd];
-#pragma unroll
-            for (uint32_t y = 0; y < 2; ++y) {
-                const uint32_t x = (tid & 7) * 8 + y * 64;
-                if (x < p.d) {
-                    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(q + x)), b = __ldg(reinterpret_cast<const uint4 *>(k + x));
-                    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const float2 u = Elem<T>::unpack(aw[z]), v = Elem<T>::unpack(bw[z]);
-                        s = fmaf(u.x, v.x, fmaf(u.y, v.y, s));
-                    }
-                }
-            }
-        }
-        for (uint32_t y = 4; y; y >>= 1) s += __shfl_xor_sync(~0u, s, y);
-        if ((tid & 7) == 0) {
-            float w = 0.0f;
-            uint32_t b = 0;
-            if (hop >= 0 && lse != -INFINITY) {
-                b = p.bucket_of[min(hop, 255)];
-                const float bias = Elem<T>::to_float(static_cast<const T *>(p.bias)[(uint64_t)hd * p.buckets + b]);
-                if (bias > Elem<T>::kMasked) w = exp2f(fmaf(s, p.scale_log2, (bias - lse) * kLog2e));
-            }
-            weight[j] = w, bucket_of[j] = b;
-        }
-    }
-    tc::grid_wait();
     // W neighbour threads of a warp a bucket
     uint32_t W = 32;
     while (W * p.buckets > kJoinThreads) W >>= 1;
     const uint32_t b = tid / W, x = tid % W;
-    float s = 0.0f, w = 0.0f;
+    float s = 0.0f;
     if (b < p.buckets) {
 #pragma unroll 4
         for (uint32_t i = x; i < p.hist_parts; i += W) s += p.part_ml[((uint64_t)i * p.hq + hd) * p.buckets + b];
     }
-    __syncthreads();
-    if (b < p.buckets)
-        for (uint32_t i = x; i < kPairs; i += W) w += bucket_of[i] == b ? weight[i] : 0.0f;
-    for (uint32_t y = W >> 1; y; y >>= 1) s += __shfl_xor_sync(~0u, s, y), w += __shfl_xor_sync(~0u, w, y);
-    if (x == 0 && b < p.buckets) sum_of[b] = s, share_of[b] = w;
-    __syncthreads();
-    if (b < p.buckets && x == 0) {
-        float left = 0.0f, all = 0.0f;
-        for (uint32_t i = 0; i < p.buckets; ++i) left += sum_of[i], all += share_of[i];
-        // a masked bucket has weights of 0 and so a gradient of 0
-        const bool give = all > 0.0f && isfinite(all) && isfinite(left);
-        static_cast<T *>(p.dbias)[(uint64_t)hd * p.buckets + b] = Elem<T>::from_float(give ? s - left * (w / all) : s);
-    }
+    for (uint32_t y = W >> 1; y; y >>= 1) s += __shfl_xor_sync(~0u, s, y);
+    if (b < p.buckets && x == 0) static_cast<T *>(p.dbias)[(uint64_t)hd * p.buckets + b] = Elem<T>::from_float(s);
 }
 
 }  // namespace k2t

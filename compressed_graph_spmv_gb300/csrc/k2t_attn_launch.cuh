@@ -4,6 +4,7 @@
 #include <atomic>
 
 #include "k2t_attn_bwd.cuh"
+#include "k2t_attn_delta.cuh"
 #include "k2t_attn_fwd.cuh"
 
 namespace k2t {
@@ -74,6 +75,21 @@ template <typename T> int launch_forward(const AttnParams &p, int bm, cudaStream
     return next_launch(attn_join_kernel<T>, dim3((unsigned)((uint64_t)p.T * p.hq)), 256, 0, p, st);
 }
 
+// Rows a block of attn_delta_kernel takes: the fewest lanes that hold them all, as in the forward pass.
+inline uint32_t delta_rows(const AttnParams &p) { return p.rows <= 32 ? 32 : p.rows <= 64 ? 64 : 128; }
+
+template <typename T, int DP> int delta_dim(const AttnParams &from, cudaStream_t st)
+{
+    AttnParams p = from;
+    p.splits = p.delta_splits, p.row_tiles = p.delta_tiles;
+    const dim3 grid(p.splits * p.row_tiles, p.hkv);
+    switch (delta_rows(p)) {
+    case 32: return attn_launch<attn_delta_kernel<T, DP, 32>>(grid, kTcThreads, DeltaSmem<DP>::bytes(p), p, st);
+    case 64: return attn_launch<attn_delta_kernel<T, DP, 64>>(grid, kTcThreads, DeltaSmem<DP>::bytes(p), p, st);
+    default: return attn_launch<attn_delta_kernel<T, DP, 128>>(grid, kTcThreads, DeltaSmem<DP>::bytes(p), p, st);
+    }
+}
+
 // Row tiles that the one-pass kernel holds: 4 of head_dim 64 or less, 2 of more (shared and tensor memory).  One pass reads
 // states and computes scores once: 32 queries over 2^18 nodes, forward and backward, 342 us; with two kernels 1089 us.
 inline uint32_t bwd_fused_tiles(uint32_t d) { return d <= 64 ? 4 : 2; }
@@ -83,8 +99,8 @@ template <typename T, int DP, int RT, bool DKV> int backward_nodes(const AttnPar
     using S = BwdSmem<DP, RT, DKV>;
     AttnParams p = from;
     const uint32_t groups = (p.row_tiles + RT - 1) / RT;
-    p.hist_tables = S::bytes(p, 2) <= (size_t)kAttnMaxSmem ? 2 : 1;
-    return attn_launch<attn_bwd_nodes_kernel<T, DP, RT, DKV>>(dim3(p.splits * groups, p.hkv), kBwdThreads, S::bytes(p, p.hist_tables), p, st);
+    p.hist_threads = S::bytes(p, 128) <= (size_t)kAttnMaxSmem ? 128 : 64;
+    return attn_launch<attn_bwd_nodes_kernel<T, DP, RT, DKV>>(dim3(p.splits * groups, p.hkv), kBwdThreads, S::bytes(p, p.hist_threads), p, st);
 }
 
 template <typename T, int DP> int backward_dim(const AttnParams &p, cudaStream_t st)
@@ -103,6 +119,10 @@ template <typename T, int DP> int backward_dim(const AttnParams &p, cudaStream_t
 
 template <typename T> int launch_backward(const AttnParams &p, cudaStream_t st)
 {
+    if (p.delta_splits) {
+        int rc = p.d <= 64 ? delta_dim<T, 64>(p, st) : delta_dim<T, 128>(p, st);
+        if (rc) return rc;
+    }
     if (p.row_tiles > bwd_fused_tiles(p.d)) {
         int rc = next_launch(attn_rows_kernel<T>, dim3(p.row_tiles * (kBwdRows / 8), p.hkv), 256, 0, p, st);
         if (rc) return rc;

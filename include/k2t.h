@@ -429,11 +429,11 @@ K2T_API uint64_t k2t_attn_work_bytes(const k2t_attn *a, int32_t backward);
  * ENOMEM (work_bytes too small), ECUDA. */
 K2T_API int k2t_attn_forward(const k2t_attn *a, void *work, uint64_t work_bytes, void *stream);
 
-/* dq, dk, dv and dbias from dout, the inputs, out and lse.  A head's bucket
- * gradients add up to 0: what rounding leaves of their sum is given back to
- * them in proportion to an estimate of their probability.  Gradients of a
+/* dq, dk, dv and dbias from dout, the inputs, out and lse.  Gradients of a
  * key/value head sum over its query heads, of a bucket over queries and
- * nodes.  Errors as k2t_attn_forward. */
+ * nodes, in fp32.  Score gradients are p (dout . v - delta): with a bias table
+ * delta is the weighted mean of dout . v, formed from the states in fp32 (out
+ * is not read), else dout . out.  Errors as k2t_attn_forward. */
 K2T_API int k2t_attn_backward(const k2t_attn *a, void *work, uint64_t work_bytes, void *stream);
 
 /* Layer norm of n_rows states of dim values, with the residual sum before it:

@@ -1,0 +1,135 @@
+"""Gradients of the attention where it concentrates and where it spreads over
+very many nodes, against 64-bit references on the GPU.
+
+Bounds beside those of tests/reader_ref.py (u: unit roundoff of the element
+type, w: relative error of a weight, p weights, dp = dout . v).  The sums by
+bucket are sums in 32 bits of score gradients that keep 16 bits or more, and
+delta is the mean of dp under the same weights, both in 32 bits, with at most
+256 terms in a row (2^-16 of the absolute terms):
+  delta <= sum p (w |dp - delta| + e_dp) + 2^-16 sum p |dp|
+  ds    <= p (w |dp - delta| + e_dp + tol(delta)) + 2^-15 |ds|
+  dbias <= u |dbias| + sum (tol(ds) + 2^-16 |ds|)
+"""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+K = pytest.importorskip("compressed_graph_spmv_gb300.k2t")
+import compressed_graph_spmv_gb300 as pkg  # noqa: E402
+
+torch = pytest.importorskip("torch")
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+U = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    K.load()
+
+
+def call(x, dtype, edges, scale=None):
+    """Forward and backward of one problem: every output, as 64-bit tensors."""
+    T, hq, d = x["q"].shape
+    n, hkv, _ = x["k"].shape
+    op = pkg.HopAttention(T, n, hq, hkv, d, DT[dtype], sources=0 if x["hops"] is None else x["hops"].shape[1], edges=edges,
+                          scale=scale)
+    out, lse = torch.full_like(x["q"], float("nan")), torch.full((T, hq), float("nan"), device="cuda")
+    table = dict(hops=x["hops"], bias=x["bias"], query_source=x.get("source"))
+    op.forward(x["q"], x["k"], x["v"], out, lse, **table)
+    g = {"d" + y: torch.full(x[y].shape, float("nan"), dtype=DT[dtype], device="cuda") for y in ("q", "k", "v")}
+    db = None if x["bias"] is None else torch.full_like(x["bias"], float("nan"))
+    op.backward(x["dout"], x["q"], x["k"], x["v"], out, lse, g["dq"], g["dk"], g["dv"], dbias=db, **table)
+    assert op.status() == 0
+    return {a: b.double() for a, b in dict(g, out=out, lse=lse, dbias=db).items() if b is not None}
+
+
+def reference(x, dtype, edges, scale=None):
+    """The definitions in 64 bits on the GPU, one head at a time, and the sharp bounds of dbias."""
+    u = U[dtype]
+    q, k, v, dout = (x[y].double() for y in ("q", "k", "v", "dout"))
+    T, hq, d = q.shape
+    group, scale = hq // k.shape[1], d ** -0.5 if scale is None else scale
+    bucket = hidden = None
+    if x["hops"] is not None:
+        first = torch.tensor(edges, device="cuda", dtype=torch.int32)
+        column = torch.arange(T, device="cuda") if x.get("source") is None else x["source"].long()
+        seen = x["hops"][:, column.clamp(min=0)].t()
+        bucket = torch.searchsorted(first, seen.clamp(min=0).contiguous(), right=True) - 1
+        hidden = (seen < 0) & (column >= 0)[:, None]
+        bucket[column < 0] = -1
+    r = {y: torch.zeros_like(t) for y, t in (("out", q), ("dq", q), ("dk", k), ("dv", v))}
+    r["dbias"] = tol = None
+    if x["bias"] is not None:
+        r["dbias"], tol = torch.zeros_like(x["bias"], dtype=torch.float64), torch.zeros_like(x["bias"], dtype=torch.float64)
+    for h in range(hq):
+        c = h // group
+        s = scale * q[:, h] @ k[:, c].t()
+        if x["bias"] is not None:
+            s += torch.where(bucket >= 0, x["bias"][h].double()[bucket.clamp(min=0)], 0.0)
+        if hidden is not None:
+            s[hidden] = -float("inf")
+        p = torch.softmax(s, 1)
+        dp = dout[:, h] @ v[:, c].t()
+        delta = (p * dp).sum(1, keepdim=True)
+        ds = p * (dp - delta)
+        r["out"][:, h] = p @ v[:, c]
+        r["dq"][:, h] = scale * ds @ k[:, c]
+        r["dk"][:, c] += scale * ds.t() @ q[:, h]
+        r["dv"][:, c] += p.t() @ dout[:, h]
+        if tol is None:
+            continue
+        size = (scale * q[:, h].abs() @ k[:, c].abs().t()).max() + x["bias"][h].double().abs().max()
+        w = 2.5 * (d + 8) * 2.0 ** -24 * size + 2.0 ** -20
+        e_dp = d * 2.0 ** -24 * dout[:, h].abs() @ v[:, c].abs().t()
+        e_delta = (p * (w * (dp - delta).abs() + e_dp)).sum(1, keepdim=True) + 2.0 ** -16 * (p * dp.abs()).sum(1, keepdim=True)
+        e_ds = p * (w * (dp - delta).abs() + e_dp + e_delta) + (2.0 ** -15 + 2.0 ** -16) * ds.abs()
+        for b in range(len(edges)):
+            r["dbias"][h, b] = ds[bucket == b].sum()
+            tol[h, b] = u * r["dbias"][h, b].abs() + e_ds[bucket == b].sum()
+    return r, tol
+
+
+def problem(T, n, hq, hkv, d, dtype, edges, seed, sources=None, mapped=False):
+    """Each source at hop 0 of itself, the other nodes some hops away, a twentieth not reached."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(DT[dtype])  # noqa: E731
+    sources = sources or T
+    hops = torch.randint(1, edges[-1] + 2, (n, sources), generator=g, device="cuda", dtype=torch.int32)
+    hops[torch.rand(n, generator=g, device="cuda") < 0.05] = -1
+    at = torch.randperm(n, generator=g, device="cuda")[:sources]
+    hops[at, torch.arange(sources, device="cuda")] = 0
+    x = dict(q=rand(T, hq, d), k=rand(n, hkv, d), v=rand(n, hkv, d), dout=rand(T, hq, d), hops=hops, bias=rand(hq, len(edges)), at=at)
+    if mapped:
+        x["source"] = torch.randint(-1, sources, (T,), generator=g, device="cuda", dtype=torch.int32)
+    return x
+
+
+def within(name, got, want, tol):
+    bad = ~((got - want).abs() <= tol)
+    assert not bad.any(), "%s: %d of %d off, worst %.3g of its bound" % (
+        name, int(bad.sum()), bad.numel(), float(((got - want).abs() / tol)[bad].max()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("T,n,hq,hkv,d,mapped,peak", [
+    (1, 65536, 2, 2, 64, False, 17.0), (8, 65536, 4, 2, 64, False, 17.0), (3, 65536, 2, 1, 128, False, 17.0),
+    (40, 20000, 4, 2, 64, True, 16.0), (150, 20000, 3, 1, 96, True, 16.0), (8, 3001, 2, 2, 64, False, 0.0)])
+def test_bias_gradient_where_attention_concentrates(T, n, hq, hkv, d, mapped, peak, dtype):
+    """About 0.99 of a row's weight on the source's own node: every bucket within its own bound."""
+    edges = list(range(9))
+    x = problem(T, n, hq, hkv, d, dtype, edges, seed=T + n, sources=min(T, 32), mapped=mapped)
+    if peak:
+        x["bias"][:, 0] = peak
+        x["q"] *= 0.25
+    want, tol = reference(x, dtype, edges)
+    within("dbias", call(x, dtype, edges)["dbias"], want["dbias"], tol)
+
+
+def test_bias_gradient_of_queries_that_match_their_own_node():
+    x = problem(32, 20000, 2, 2, 64, "bf16", list(range(9)), seed=5)
+    x["q"] = (x["k"][x["at"]] * 1.75).contiguous()
+    want, tol = reference(x, "bf16", list(range(9)))
+    within("dbias", call(x, "bf16", list(range(9)))["dbias"], want["dbias"], tol)
