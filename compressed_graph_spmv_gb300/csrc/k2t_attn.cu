@@ -83,10 +83,11 @@ void make_plan(const k2t_attn *a, bool backward, Plan &pl)
     const uint64_t rows = (uint64_t)p.T * p.hq;
     pl.delta_floats = 0;
     if (backward) {
-        if (p.buckets && p.T && p.n) {
+        // for sums of score gradients by bucket (see k2t_attn_delta.cuh), and for the power of two that keeps fp16 ones in range
+        if ((p.buckets || a->dtype == K2T_FP16) && p.T && p.n) {
             p.delta_tiles = (p.rows + delta_rows(p) - 1) / delta_rows(p);
             p.delta_splits = pick_splits((uint64_t)p.hkv * p.delta_tiles, p.tiles);
-            pl.delta_floats = p.delta_splits * rows * 2;
+            pl.delta_floats = p.delta_splits * rows * 3 + (uint64_t)p.hkv * p.delta_splits * p.delta_tiles;
         }
         const uint32_t per = kBwdRows / p.group;              // whole queries of a row tile
         p.row_tiles = std::max(1u, (p.T + per - 1) / per);
@@ -182,6 +183,7 @@ void fill_pointers(const k2t_attn *a, void *work, Plan &pl)
     w += align_up(pl.part_floats * 4, 256) + align_up(pl.ml_floats * 4, 256);
     p.row_info = w;
     p.delta_part = reinterpret_cast<float2 *>(w + align_up(pl.info_floats * 4, 256));
+    p.dp_top = reinterpret_cast<float *>(p.delta_part + (uint64_t)p.delta_splits * p.T * p.hq);
     uint32_t b = 0;
     for (uint32_t x = 0; x < 256; ++x) {
         while (b + 1 < a->n_buckets && a->edges[b + 1] <= x) ++b;

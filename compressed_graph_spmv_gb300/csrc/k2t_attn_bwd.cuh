@@ -46,24 +46,26 @@ constexpr int kBwdRows = 32;
 
 // What the kernels need of a row, made once by attn_rows_kernel: lse in units
 // of log2 (+inf for a row that saw nothing or does not exist: its weights
-// become 0), delta, byte offset of its column in a bucket tile, its head's
+// become 0), less Elem::kUp, delta, ds_scale of its largest |dp|, byte offset of its column in a bucket tile, its head's
 // offset in the bias table; a row tile's together.
 struct RowInfo {
-    float lse[kBwdRows], delta[kBwdRows];
+    float lse[kBwdRows], delta[kBwdRows], up[kBwdRows];
     uint32_t place[kBwdRows];              // column | head << 16
 };
 
 // delta of query t, head hd, by L neighbour lanes (x: this one of them): the sums over nodes that attn_delta_kernel left, or
-// dout . out without them; 0 for a query that does not exist or saw nothing.
+// dout . out without them; 0 for a query that does not exist or saw nothing.  up: ds_scale of the row.
 template <typename T, int L>
-__device__ __forceinline__ float row_delta(const AttnParams &p, uint32_t t, uint32_t hd, int x, uint32_t lanes)
+__device__ __forceinline__ float row_delta(const AttnParams &p, uint32_t t, uint32_t hd, int x, uint32_t lanes, float &up)
 {
-    float s = 0.0f, m = p.delta_splits ? 0.0f : 1.0f / L;
+    float top = 0.0f, s = 0.0f, m = p.delta_splits ? 0.0f : 1.0f / L;
     if (t < p.T) {
         if (p.delta_splits) {
             for (uint32_t i = x; i < p.delta_splits; i += L) {
-                const float2 v = p.delta_part[((uint64_t)i * p.T + t) * p.hq + hd];
+                const uint64_t at = ((uint64_t)i * p.T + t) * p.hq + hd;
+                const float2 v = p.delta_part[at];
                 s += v.x, m += v.y;
+                if (Elem<T>::kUp) top = fmaxf(top, p.dp_top[at]);
             }
         } else {
             const T *o = static_cast<const T *>(p.out) + (int64_t)t * p.out_row + (int64_t)hd * p.out_head;
@@ -80,6 +82,9 @@ __device__ __forceinline__ float row_delta(const AttnParams &p, uint32_t t, uint
         }
     }
     for (int y = L / 2; y; y >>= 1) s += __shfl_xor_sync(lanes, s, y), m += __shfl_xor_sync(lanes, m, y);
+    if (Elem<T>::kUp)
+        for (int y = L / 2; y; y >>= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, y));
+    up = ds_scale<T>(top);
     return m == 0.0f ? 0.0f : s / m;
 }
 
@@ -91,17 +96,26 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
     tc::grid_wait();
     const int lane = threadIdx.x & 31;
     const uint32_t G = p.group, per = kBwdRows / G, c = at % kBwdRows, t = at / kBwdRows * per + c / G, g = c % G;
-    float lse = INFINITY, s = 0.0f;
+    float lse = INFINITY, s = 0.0f, up = 1.0f;
     uint32_t place = 0;
     if (c < per * G && t < p.T) {
         const uint32_t hd = hk * G + g;
-        s = row_delta<T, 32>(p, t, hd, lane, ~0u);
+        s = row_delta<T, 32>(p, t, hd, lane, ~0u, up);
         const float l = p.lse[(uint64_t)t * p.hq + hd];
-        if (l != -INFINITY) lse = l * kLog2e;
+        if (l != -INFINITY) lse = l * kLog2e - Elem<T>::kUp;
         place = row_column(p, t * G) * kTcPitch | (g * 4) << 16;
     }
     RowInfo *to = static_cast<RowInfo *>(p.row_info) + (uint64_t)hk * p.row_tiles + at / kBwdRows;
-    if (lane == 0) to->lse[c] = lse, to->delta[c] = s, to->place[c] = place;
+    if (lane == 0) to->lse[c] = lse, to->delta[c] = s, to->up[c] = up, to->place[c] = place;
+}
+
+// The head's largest |dp| into *top (bits; 0 before), by a block's threads.
+__device__ __forceinline__ void head_top(const AttnParams &p, uint32_t hk, uint32_t *top)
+{
+    const uint64_t parts = (uint64_t)p.delta_splits * p.delta_tiles, rows = (uint64_t)p.delta_splits * p.T * p.hq;
+    uint32_t most = 0;
+    for (uint64_t i = threadIdx.x; i < parts; i += blockDim.x) most = max(most, __float_as_uint(p.dp_top[rows + hk * parts + i]));
+    if (most) atomicMax(top, most);
 }
 
 // Copies ROWS (a multiple of 32) rows of tile `tile` on of a [T, heads, d] tensor into row tiles of 32 rows:
@@ -120,18 +134,19 @@ __device__ __forceinline__ void copy_row_tile(uint32_t dst, const void *base, in
     }
 }
 
+// up: ds_scale of the head.
 // A unit's softmax step for one node: S^T and dP^T at `at` (32 columns each, a row of the tile a column) become P^T
 // and dS^T in the element type, two rows a column; ds: this node's row of dS^T in shared memory, from chunk `chunk` on
 // (null: not wanted), and `rest` bytes on what the rounding took off, itself rounded (rest 0: not wanted); bt: the node's bytes in the bucket tile (column 0); lut: bias table, bytes.
 // Eight rows at a time in a rolled loop: the warps of an SM run half a dozen different loops, and the instruction
 // caches hold them only while each is small.
 template <typename T>
-__device__ __forceinline__ void unit32(uint32_t at, const RowInfo *info, bool plain, float scale, const uint8_t *bt,
+__device__ __forceinline__ void unit32(uint32_t at, const RowInfo *info, bool plain, float scale, float up, const uint8_t *bt,
                                        const uint8_t *lut, uint32_t shift, uint8_t *ds, uint32_t rest, uint32_t chunk, uint32_t node)
 {
 #pragma unroll 1
     for (int r0 = 0; r0 < kBwdRows; r0 += 8) {
-        uint32_t s[8], d[8], pw[4], dw[4], rw[4];
+        uint32_t s[8], d[8], pw[4], dw[4], rw[4], kw[4];
         tc::ld8(s, at + r0);
         tc::ld8(d, at + 32 + r0);
         float b[8] = {};
@@ -152,11 +167,13 @@ __device__ __forceinline__ void unit32(uint32_t at, const RowInfo *info, bool pl
         for (int e = 0; e < 8; e += 4) {
             const float4 lse4 = *reinterpret_cast<const float4 *>(&info->lse[r0 + e]), dl4 = *reinterpret_cast<const float4 *>(&info->delta[r0 + e]);
             const float lse[4] = {lse4.x, lse4.y, lse4.z, lse4.w}, delta[4] = {dl4.x, dl4.y, dl4.z, dl4.w};
-            float pv[4], dv[4];
+            float pv[4], dv[4], own[4];
+            if (Elem<T>::kUp && ds) *reinterpret_cast<float4 *>(own) = *reinterpret_cast<const float4 *>(&info->up[r0 + e]);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 pv[y] = ex2(fmaf(__uint_as_float(s[e + y]), scale, b[e + y]) - lse[y]);
-                dv[y] = pv[y] * (__uint_as_float(d[e + y]) - delta[y]);
+                const float x = __uint_as_float(d[e + y]) - delta[y];
+                dv[y] = pv[y] * (Elem<T>::kUp ? x * (ds ? own[y] : up) : x);
             }
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
@@ -164,10 +181,12 @@ __device__ __forceinline__ void unit32(uint32_t at, const RowInfo *info, bool pl
                 dw[e / 2 + y] = Elem<T>::pack(dv[2 * y], dv[2 * y + 1]);
                 const float2 kept = Elem<T>::unpack(dw[e / 2 + y]);
                 rw[e / 2 + y] = Elem<T>::pack(dv[2 * y] - kept.x, dv[2 * y + 1] - kept.y);
+                kw[e / 2 + y] = Elem<T>::kUp && ds ? Elem<T>::pack(dv[2 * y] * (up * inverse_power(own[2 * y])),
+                                                                   dv[2 * y + 1] * (up * inverse_power(own[2 * y + 1]))) : dw[e / 2 + y];
             }
         }
         tc::st4(at + r0 / 2, pw);
-        tc::st4(at + 32 + r0 / 2, dw);
+        tc::st4(at + 32 + r0 / 2, kw);
         if (ds) {
             uint8_t *to = ds + (((chunk + r0 / 8) ^ (node & 7)) << 4);
             *reinterpret_cast<uint4 *>(to) = make_uint4(dw[0], dw[1], dw[2], dw[3]);
@@ -230,7 +249,7 @@ template <int DP, int RT, bool DKV> struct BwdSmem {
     struct Ctl {
         uint64_t full[kSlots], empty[kSlots], hop_full[kBufs], hop_empty[kBufs], sp_full[2], ds_full[2], hist_done[2];
         uint64_t tile_full, tile_empty, staged, dq_full, drained;
-        uint32_t tmem, gave_up, columns, all;
+        uint32_t tmem, gave_up, columns, all, top;
         uint32_t seen[kBufs][4];
         uint8_t byte_of[257 + 15];
     };
@@ -275,7 +294,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
         tc::bar_init(&ctl->staged, 128);
         tc::bar_init(&ctl->dq_full, 1);
         tc::bar_init(&ctl->drained, 1);
-        ctl->gave_up = ctl->columns = ctl->all = 0;
+        ctl->gave_up = ctl->columns = ctl->all = ctl->top = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tc::grid_wait();
@@ -292,6 +311,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
         for (uint32_t i = tid; i < (p.buckets + 2) * p.hist_threads; i += kBwdThreads) hist[i] = 0.0f;
     RowInfo *info = reinterpret_cast<RowInfo *>(smem + S::kInfo);
     __syncthreads();
+    if (Elem<T>::kUp) head_top(p, hk, &ctl->top);
     auto seen_by = [&](uint32_t place) {
         const uint32_t col = (place & 0xffff) / kTcPitch;
         if (col < p.sources) atomicOr(&ctl->columns, 1u << col);
@@ -303,25 +323,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
             const uint32_t c = at % kBwdRows, per = kBwdRows / p.group, t = (rt0 + at / kBwdRows) * per + c / p.group, g = c % p.group;
             const bool on = c < per * p.group && t < p.T;
             const uint32_t hd = hk * p.group + g;
-            const float s = row_delta<T, 8>(p, on ? t : p.T, hd, tid & 7, 0xffu << (lane & 24));
+            float row_up;
+            const float s = row_delta<T, 8>(p, on ? t : p.T, hd, tid & 7, 0xffu << (lane & 24), row_up);
             if ((tid & 7) == 0) {
                 RowInfo *to = info + at / kBwdRows;
                 float lse = INFINITY;
                 uint32_t place = 0;
                 if (on) {
                     const float l = p.lse[(uint64_t)t * p.hq + hd];
-                    if (l != -INFINITY) lse = l * kLog2e;
+                    if (l != -INFINITY) lse = l * kLog2e - Elem<T>::kUp;
                     place = row_column(p, t * p.group) * kTcPitch | (g * 4) << 16;
                     if (p.sources) seen_by(place);
                 }
-                to->lse[c] = lse, to->delta[c] = s, to->place[c] = place;
+                to->lse[c] = lse, to->delta[c] = s, to->up[c] = row_up, to->place[c] = place;
             }
         }
     } else if (tid < (int)rts * kBwdRows) {
         const RowInfo *from = static_cast<const RowInfo *>(p.row_info) + (uint64_t)hk * p.row_tiles + rt0 + tid / kBwdRows;
         RowInfo *to = info + tid / kBwdRows;
         const uint32_t c = tid % kBwdRows, place = from->place[c], per = kBwdRows / p.group, t = (rt0 + tid / kBwdRows) * per + c / p.group;
-        to->lse[c] = from->lse[c], to->delta[c] = from->delta[c], to->place[c] = place;
+        to->lse[c] = from->lse[c], to->delta[c] = from->delta[c], to->up[c] = from->up[c], to->place[c] = place;
         if (p.sources && c < per * p.group && t < p.T) seen_by(place);
     }
     cp_wait<0>();
@@ -332,6 +353,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
     tc::grid_next();
     const uint32_t tm = ctl->tmem;
     volatile uint32_t *gave_up = &ctl->gave_up;
+    const float up = ds_scale<T>(__uint_as_float(ctl->top));       // and what takes the powers of two out of the results:
+    const float p_down = 1.0f / (1u << Elem<T>::kUp), ds_down = p_down / up;
+    auto row_down = [&](uint32_t r, uint32_t c) { return Elem<T>::kUp ? p_down * inverse_power(info[r].up[c]) : 1.0f; };
 
     if (warp < 8) {
         // ---- softmax: thread = node of a tile; group w takes the units of parity w ----
@@ -347,7 +371,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
             if (!__all_sync(~0u, ok)) break;
             tc::fence_after();
             const bool plain = !p.sources && (tile_at(i) + 1) * kTcTile <= p.n;
-            unit32<T>(at, info + r, plain, p.scale_log2, smem + S::kBuckets + buf * 33 * kTcPitch + l,
+            unit32<T>(at, info + r, plain, p.scale_log2, up, smem + S::kBuckets + buf * 33 * kTcPitch + l,
                       reinterpret_cast<const uint8_t *>(lut), shift, ds, p.buckets ? S::kPanel : 0, w * 4, l);
             tc::wait_st();
             tc::fence_async();
@@ -375,7 +399,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
                 // the tile's own slots are free to hold its results: every product that read them is done
                 const uint32_t ks = slot_of<S::kSlots>(2 * i), vs = slot_of<S::kSlots>(2 * i + 1);
 #pragma unroll 1
-                for (int x = 0; x < 2; ++x) load_nodes<T, DP>(tm + lanes + (x ? kDk : kDv), x ? p.scale : 1.0f, sm + (x ? ks : vs) * S::kSlot, l);
+                for (int x = 0; x < 2; ++x) load_nodes<T, DP>(tm + lanes + (x ? kDk : kDv), x ? p.scale * ds_down : p_down, sm + (x ? ks : vs) * S::kSlot, l);
                 tc::fence_before();
                 tc::bar_arrive(&ctl->tile_empty);
                 tc::fence_async();
@@ -410,7 +434,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
                 for (int c = 0; c < 32; ++c) {
                     const uint32_t q = c / G, t = (rt0 + r) * per + q, hd = hk * G + c - q * G;
                     if (l < (int)p.d && q < per && t < p.T) {
-                        const float x = units > 0 ? __uint_as_float(v[c]) : 0.0f;
+                        const float x = units > 0 ? __uint_as_float(v[c]) * row_down(r, c) : 0.0f;
                         if (p.splits > 1) p.part[(((uint64_t)split * p.T + t) * p.hq + hd) * p.d + l] = x;
                         else static_cast<T *>(p.dq)[(int64_t)t * p.dq_row + (int64_t)hd * p.dq_head + l] = Elem<T>::from_float(x * p.scale);
                     }
@@ -432,9 +456,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
                 const uint8_t *ds = smem + S::kDs + part * span * 128 + (c & 7) * 2;
                 const uint32_t chunk = w * 4 + (c >> 3);
                 // ds in full: its rounded value and what that took off
+                const float down = row_down(r, c);
                 auto term = [&](int node) {
                     const uint8_t *at = ds + node * 128 + ((chunk ^ (node & 7)) << 4);
-                    return Elem<T>::to_float(*reinterpret_cast<const T *>(at)) + Elem<T>::to_float(*reinterpret_cast<const T *>(at + S::kPanel));
+                    const float x = Elem<T>::to_float(*reinterpret_cast<const T *>(at)) + Elem<T>::to_float(*reinterpret_cast<const T *>(at + S::kPanel));
+                    return Elem<T>::kUp ? x * down : x;
                 };
                 // A node is a read, an add and a write of its bucket.  Four nodes go on at once: the reads before the first
                 // write, a node that shares the bucket of one before it continues from that one's sum, and the writes in the
@@ -547,7 +573,7 @@ template <int DP> struct BwdRowSmem {
     static constexpr int kCtl = kInfo + kRing * (int)sizeof(RowInfo);
     struct Ctl {
         uint64_t full[2], empty[2], hop_full[1], hop_empty[1], row_full[kRing], row_empty[kRing], sp_full[2], ds_full[2], tile_full, drained;
-        uint32_t tmem, gave_up, columns, all;
+        uint32_t tmem, gave_up, columns, all, top;
         uint32_t seen[1][4];
         uint8_t byte_of[257 + 15];
     };
@@ -579,7 +605,7 @@ __global__ void __launch_bounds__(kBwdRowThreads, 1) attn_bwd_rows_kernel(const 
         for (int i = 0; i < S::kRing; ++i) tc::bar_init(&ctl->row_full[i], 128), tc::bar_init(&ctl->row_empty[i], 1);
         tc::bar_init(&ctl->tile_full, 1);
         tc::bar_init(&ctl->drained, 1);
-        ctl->gave_up = ctl->columns = ctl->all = 0;
+        ctl->gave_up = ctl->columns = ctl->all = ctl->top = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (p.sources)
@@ -587,6 +613,7 @@ __global__ void __launch_bounds__(kBwdRowThreads, 1) attn_bwd_rows_kernel(const 
     tc::grid_wait();
     fill_bias<T>(lut, p, hk, tid, p.group2);
     __syncthreads();
+    if (Elem<T>::kUp) head_top(p, hk, &ctl->top);
     if (p.sources) {
         uint32_t cols = 0;
         bool all = false;
@@ -604,6 +631,8 @@ __global__ void __launch_bounds__(kBwdRowThreads, 1) attn_bwd_rows_kernel(const 
     tc::grid_next();
     const uint32_t tm = ctl->tmem;
     volatile uint32_t *gave_up = &ctl->gave_up;
+    const float up = ds_scale<T>(__uint_as_float(ctl->top));       // and what takes the powers of two out of the results:
+    const float p_down = 1.0f / (1u << Elem<T>::kUp), ds_down = p_down / up;
 
     if (warp < 8) {
         const int w = warp >> 2, l = tid & 127;
@@ -617,7 +646,7 @@ __global__ void __launch_bounds__(kBwdRowThreads, 1) attn_bwd_rows_kernel(const 
             ok = __all_sync(~0u, ok);
             if (!ok) break;
             tc::fence_after();
-            unit32<T>(tm + lanes + w * 64, reinterpret_cast<const RowInfo *>(smem + S::kInfo) + slot, plain, p.scale_log2,
+            unit32<T>(tm + lanes + w * 64, reinterpret_cast<const RowInfo *>(smem + S::kInfo) + slot, plain, p.scale_log2, up,
                       smem + S::kBuckets + l, reinterpret_cast<const uint8_t *>(lut), shift, nullptr, 0, 0, 0);
             tc::wait_st();
             tc::fence_before();
@@ -628,7 +657,7 @@ __global__ void __launch_bounds__(kBwdRowThreads, 1) attn_bwd_rows_kernel(const 
         const uint32_t stage = sm + (w ? 0 : S::kSlot);
         if (ok) {
             tc::fence_after();
-            load_nodes<T, DP>(tm + lanes + (w ? kDk : kDv), w ? p.scale : 1.0f, stage, l);
+            load_nodes<T, DP>(tm + lanes + (w ? kDk : kDv), w ? p.scale * ds_down : p_down, stage, l);
             tc::fence_async();
         }
         asm volatile("bar.sync %0, 128;" ::"r"(w + 1) : "memory");
