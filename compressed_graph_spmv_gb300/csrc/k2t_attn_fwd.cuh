@@ -27,7 +27,9 @@
 // The maximum a group subtracts trails the true one by at most 2^8 in the
 // weights: O is rescaled (a pass over tensor memory) only when a score
 // exceeds it by more than 8 in units of log2; exact in fp32, and a weight of
-// 256 is no less precise in 16 bits than one of 1.
+// 256 is no less precise in 16 bits than one of 1.  In fp16, whose least
+// number is 2^-24, weights are 2^7 times larger (at most 2^15): many nodes of
+// small weight beside one of 1 make up much of a row.
 //
 // What bounds it: memory with few rows (4 rows a head over 2^20 nodes, bf16:
 // 297 us, the copy rate), the softmax threads' issue slots with 128 rows a head
@@ -46,6 +48,7 @@ namespace k2t {
 constexpr int kTcThreads = 800;
 constexpr int kTcLutAlign = 8192;   // the bias table's alignment, above its size: its address joins an index by OR
 constexpr float kTcLag = 8.0f;
+template <typename T> constexpr float kTcUp = std::is_same<T, __half>::value ? 7.0f : 0.0f;   // weights are 2^(s - m + kTcUp)
 
 template <int DP, bool TWO> struct TcSmem {
     static constexpr int kPanel = kTcTile * 128;              // 64 values of 128 rows
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
                     }
                 }
             }
-            const float u0 = m == -INFINITY ? 0.0f : m;
+            const float u0 = m == -INFINITY ? 0.0f : m - kTcUp<T>;
             // Weights in the element type, two a word, over S: nodes [0, 64) from its column 0 on, [64, 128) from 64 on,
             // so that a half of 64 overwrites its own scores.  Nodes of the other copies' parts weigh nothing.
             if (KW == 128) {
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4 *>(at + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
-            if (half == 0) at[DP] = m;
+            if (half == 0) at[DP] = m - kTcUp<T>;
             at[DP + 1 + half] = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
         asm volatile("bar.sync 1, 512;" ::: "memory");

@@ -1,0 +1,38 @@
+"""Attention of values at the edges of their types."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+K = pytest.importorskip("compressed_graph_spmv_gb300.k2t")
+import compressed_graph_spmv_gb300 as pkg  # noqa: E402
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    K.load()
+
+
+@pytest.mark.parametrize("T,hkv", [(1, 1), (128, 152), (40, 2), (150, 76)])
+def test_half_weights_below_the_least_number(T, hkv):
+    """2^20 nodes of relative weight 1.4 2^-24 each beside one of weight 1: together a twelfth of a row.  Scores are the
+    bias alone (q is 0).  Every value is v = 1 but the one node's, 0, so that out is that share.  Weights times 2^7 are
+    rounded to steps of 2^-24, 1/179 of each: off by 2^-8.5 at most, and the result by 2^-11."""
+    n, d = 1 << 20, 32
+    low = torch.tensor(-16.3, dtype=torch.float16)
+    k = torch.zeros(1, 1, d, dtype=torch.float16, device="cuda").expand(n, hkv, d)
+    v = torch.ones(n, 1, d, dtype=torch.float16, device="cuda")
+    v[n // 2] = 0
+    hops = torch.ones(n, 1, dtype=torch.int32, device="cuda")
+    hops[n // 2] = 0
+    q, out = (torch.zeros(T, hkv, d, dtype=torch.float16, device="cuda") for _ in range(2))
+    lse = torch.zeros(T, hkv, device="cuda")
+    bias = torch.tensor([0.0, float(low)], dtype=torch.float16, device="cuda").expand(hkv, 2).contiguous()
+    op = pkg.HopAttention(T, n, hkv, hkv, d, torch.float16, sources=1, edges=[0, 1])
+    op.forward(q, k, v.expand(n, hkv, d), out, lse, hops=hops, bias=bias, query_source=torch.zeros(T, dtype=torch.int32, device="cuda"))
+    rest = (n - 1) * torch.exp(low.double())
+    want = float(rest / (1 + rest))
+    assert abs(out.double() - want).max() <= want * (2.0 ** -8.5 + 2.0 ** -11)
