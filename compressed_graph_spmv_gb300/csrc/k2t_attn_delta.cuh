@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_delta_kernel(const __grid_
         const uint8_t *bt0 = smem + S::kBuckets + col * kTcPitch + key0;
         const float lse = row < p.rows ? p.lse[(uint64_t)t * p.hq + hk * p.group + g] : -INFINITY;
         const float nl = lse == -INFINITY ? -INFINITY : -lse * kLog2e;              // weights of a row that saw nothing are 0
-        float2 dots = make_float2(0.0f, 0.0f), mass = dots;
+        LongSum all_dots, all_mass;
         float top = 0.0f;                                             // largest |dp|
         uint32_t mine = 0;                                            // units of this group done
         for (uint32_t u = w; u < units; u += 2, ++mine) {
@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_delta_kernel(const __grid_
             if (!ok) break;
             tc::fence_after();
             const bool plain = !p.sources && (split + (uint64_t)u * p.splits + 1) * kTcTile <= p.n;     // no table, no node past the end
+            float2 dots = make_float2(0.0f, 0.0f), mass = dots;
 #pragma unroll 1
             for (int b = 0; b < HW; b += 16) {
                 uint32_t s[16], d[16];
@@ -176,9 +177,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_delta_kernel(const __grid_
             tc::bar_arrive(&ctl->s_read[w]);
             __syncwarp();
             if (lane == 0) tc::bar_arrive(&ctl->hop_empty[buf]);
+            all_dots.add(dots.x + dots.y);
+            all_mass.add(mass.x + mass.y);
         }
         // ---- the copies' and groups' sums of a row, one after another ----
-        ctl->sum[w][half][l] = make_float2(dots.x + dots.y, mass.x + mass.y);
+        ctl->sum[w][half][l] = make_float2(all_dots.total(), all_mass.total());
         if (Elem<T>::kUp) {
             ctl->tops[w][half][l] = top;
             const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(top));     // of numbers that are not negative: as their bits

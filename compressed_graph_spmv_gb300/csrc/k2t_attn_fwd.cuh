@@ -148,6 +148,19 @@ __device__ __forceinline__ void weights(uint32_t (&out)[N / 2], const uint32_t (
     }
 }
 
+// A running sum over very many tiles: a tile's terms are added up first, and what the addition to the sum cuts off is kept
+// beside it.  (2^20 nodes of 1.4 2^-24 each after one of 1, one by one to one fp32 sum: 1.1e-3 off in lse.)
+struct LongSum {
+    float sum = 0.0f, rest = 0.0f;
+    __device__ __forceinline__ void add(float x)
+    {
+        const float y = x + rest, s = sum + y, back = s - sum;
+        rest = (sum - (s - back)) + (y - back);
+        sum = s;
+    }
+    __device__ __forceinline__ float total() const { return sum + rest; }
+};
+
 template <typename T, int DP, int KW, bool TWO>
 __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_constant__ AttnParams p)
 {
@@ -285,7 +298,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
         float *tops = ctl->tops[0][w][0] + l;                         // [turn][group][half][lane]
         uint64_t *pair = &ctl->pair[w * 4 + (warp & 3)];
         float m = -INFINITY;
-        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        LongSum sum;
         bool ok = true;
         uint32_t mine = 0;                                            // units of this group done
         for (uint32_t u = w; u < units; u += 2, ++mine) {
@@ -323,8 +336,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
                 const float next = grow ? top : m;
                 const float f = m == -INFINITY ? 0.0f : ex2(m - next);      // m = -inf: nothing was summed yet
                 m = next;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) sum[e].x *= f, sum[e].y *= f;
+                sum.sum *= f, sum.rest *= f;
                 if (mine > 0) {
                     // the products issued before these scores are done, so O is at rest; each half takes half of it
 #pragma unroll 1
@@ -341,18 +353,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
             const float u0 = m == -INFINITY ? 0.0f : m - kTcUp<T>;
             // Weights in the element type, two a word, over S: nodes [0, 64) from its column 0 on, [64, 128) from 64 on,
             // so that a half of 64 overwrites its own scores.  Nodes of the other copies' parts weigh nothing.
+            float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
             if (KW == 128) {
 #pragma unroll 1
                 for (int b = 0; b < HW; b += CH) {
                     uint32_t out[CH / 2];
                     tc::load(s, s_at + key0 + b);
                     tc::wait_ld();
-                    weights<T, CH>(out, s, u0, sum);
+                    weights<T, CH>(out, s, u0, part);
                     tc::store(s_at + key0 + b / 2, out);
                 }
             } else {
                 uint32_t out[CH / 2];
-                weights<T, CH>(out, s, u0, sum);
+                weights<T, CH>(out, s, u0, part);
 #pragma unroll
                 for (int j = 0; j < 128 / KW; ++j) {
                     const uint32_t at = s_at + (j * KW < 64 ? j * KW / 2 : 64 + (j * KW - 64) / 2) + half * (HW / 2);
@@ -367,6 +380,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
             tc::wait_st();
             tc::fence_before();
             tc::bar_arrive(&ctl->p_full[w]);
+            sum.add((part[0].x + part[0].y) + (part[1].x + part[1].y));
         }
         // ---- join the copies and groups through the freed slots: [group][lane][DP + 4] ----
         if (ok && mine > 0) {
@@ -394,7 +408,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
                 for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4 *>(at + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
             if (half == 0) at[DP] = m - kTcUp<T>;
-            at[DP + 1 + half] = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            at[DP + 1 + half] = sum.total();
         }
         asm volatile("bar.sync 1, 512;" ::: "memory");
         constexpr int kSets = TWO ? 1 : 2 * (128 / kRows), kOut = TWO ? 256 : kRows, Q4 = DP / 4;

@@ -36,3 +36,23 @@ def test_half_weights_below_the_least_number(T, hkv):
     rest = (n - 1) * torch.exp(low.double())
     want = float(rest / (1 + rest))
     assert abs(out.double() - want).max() <= want * (2.0 ** -8.5 + 2.0 ** -11)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T,hkv", [(128, 152), (40, 160), (150, 76), (1, 200)])
+def test_sum_of_weights_over_very_many_nodes(T, hkv, dtype):
+    """2^20 nodes of relative weight 2^-23.5 each beside one of weight 1, all of them one block's: their sum is not lost
+    beside the one.  Scores are the bias alone."""
+    n, d = 1 << 20, 32
+    low = torch.tensor(-16.3, dtype=dtype)
+    states = torch.ones(n, 1, d, dtype=dtype, device="cuda").expand(n, hkv, d)
+    hops = torch.ones(n, 1, dtype=torch.int32, device="cuda")
+    hops[0] = 0
+    q, out = (torch.zeros(T, hkv, d, dtype=dtype, device="cuda") for _ in range(2))
+    lse = torch.zeros(T, hkv, device="cuda")
+    bias = torch.tensor([0.0, float(low)], dtype=dtype, device="cuda").expand(hkv, 2).contiguous()
+    op = pkg.HopAttention(T, n, hkv, hkv, d, dtype, sources=1, edges=[0, 1])
+    table = dict(hops=hops, bias=bias, query_source=torch.zeros(T, dtype=torch.int32, device="cuda"))
+    op.forward(q, states, states, out, lse, **table)
+    rest = (n - 1) * torch.exp(low.double())
+    assert abs(lse.double() - float(torch.log1p(rest))).max() <= 1e-5
