@@ -438,12 +438,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_kernel(const __grid_co
                     *reinterpret_cast<float4 *>(p.part + at * p.d + c) = acc;
                     if (c == 0) *reinterpret_cast<float2 *>(p.part_ml + at * 2) = make_float2(mx, ls);
                 } else {
-                    const float inv = ls > 0.0f ? 1.0f / ls : 0.0f;
+                    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;     // 0: nothing was seen; a row that is no number says so
                     uint2 o2;
                     o2.x = Elem<T>::pack(acc.x * inv, acc.y * inv);
                     o2.y = Elem<T>::pack(acc.z * inv, acc.w * inv);
                     *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (int64_t)t * p.out_row + (int64_t)hd * p.out_head + c) = o2;
-                    if (c == 0) p.lse[(uint64_t)t * p.hq + hd] = ls > 0.0f ? (mx + log2f(ls)) * kLn2 : -INFINITY;
+                    if (c == 0) p.lse[(uint64_t)t * p.hq + hd] = ls == 0.0f ? -INFINITY : (mx + log2f(ls)) * kLn2;
                 }
             }
     }
@@ -496,12 +496,12 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
             l += lsum[i * q4 + c];
         }
         const uint32_t t = (uint32_t)(row / p.hq), hd = (uint32_t)(row - (uint64_t)t * p.hq);
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         uint2 w;
         w.x = Elem<T>::pack(acc.x * inv, acc.y * inv);
         w.y = Elem<T>::pack(acc.z * inv, acc.w * inv);
         *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (int64_t)t * p.out_row + (int64_t)hd * p.out_head + c * 4) = w;
-        if (c == 0) p.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (c == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
 }
 

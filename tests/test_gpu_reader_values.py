@@ -56,3 +56,22 @@ def test_sum_of_weights_over_very_many_nodes(T, hkv, dtype):
     op.forward(q, states, states, out, lse, **table)
     rest = (n - 1) * torch.exp(low.double())
     assert abs(lse.double() - float(torch.log1p(rest))).max() <= 1e-5
+
+
+@pytest.mark.parametrize("n,hkv", [(70, 2), (5000, 1)])
+@pytest.mark.parametrize("T", [3, 40, 140])
+@pytest.mark.parametrize("what", ["nan", "inf"])
+def test_rows_that_hold_no_number(T, n, hkv, what):
+    """A query that is NaN, or whose scores overflow, says so in out and lse: -inf means that nothing was seen."""
+    g = torch.Generator(device="cuda").manual_seed(T + n)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, k, v = rand(T, hkv, 64), rand(n, hkv, 64), rand(n, hkv, 64)
+    op = pkg.HopAttention(T, n, hkv, hkv, 64, torch.bfloat16)
+    out, lse = torch.zeros_like(q), torch.zeros(T, hkv, device="cuda")
+    op.forward(q, k, v, out, lse)
+    good, good_lse = out.clone(), lse.clone()
+    q[1] = float("nan") if what == "nan" else 3e38
+    op.forward(q, k, v, out, lse)
+    others = [t for t in range(T) if t != 1]
+    assert torch.equal(out[others], good[others]) and torch.equal(lse[others], good_lse[others])
+    assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
