@@ -306,6 +306,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
 
 // dx = rstd (w dy - c1 - xh c2) + dz with c1 = mean(w dy), c2 = mean(w dy xh);
 // part[block][0 | 1][dim]: the block's sums of dy xh and dy.
+// Without the forward call's mean and rstd they are formed from z, which lies in registers: one more reduction a row.
 template <typename T, int VEC, int TPR, int PER, int AHEAD, bool SHIFT>
 __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 ? 1 : PER > 1 ? 2 : 3) norm_bwd_kernel(const __grid_constant__ NormParams p)
 {
@@ -322,6 +323,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 ? 1 : PER > 1
     const int shift = SHIFT ? (int)(first * p.dim % VEC) : 0;
     using Pc = Piece<T, VEC, SHIFT>;
     auto piece = [&](int i) { return Pc((tid + i * TPR) * VEC - shift, p.dim); };
+    const bool form = !p.mean;
     float2 w[N2], dw[N2], db[N2];
 #pragma unroll
     for (int e = 0; e < PER * VEC; ++e) {
@@ -337,8 +339,8 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 ? 1 : PER > 1
     in.start();
     for (uint64_t row = first; row < p.n; row += step) {
         const uint64_t at = row * p.dim;
-        const float mean = p.mean[row], rstd = p.rstd[row];
-        const float2 nm = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
+        float mean = 0.0f, rstd = 0.0f;
+        if (!form) mean = p.mean[row], rstd = p.rstd[row];
         P z[PER], g[PER], x[PER];
         in.ready();
 #pragma unroll
@@ -351,20 +353,55 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 ? 1 : PER > 1
                 z[i] = g[i] = x[i] = zero_pack<T, VEC>();
             }
         }
-        float2 xh[N2], a[N2], s1 = make_float2(0.0f, 0.0f), s2 = s1;
+        in.taken();
+        // the sums of one row: z and a = w dy, then the squares of z - mean and a (z - mean)
+        float2 xh[N2], a[N2], s0 = make_float2(0.0f, 0.0f), s1 = s0, s2 = s0;
 #pragma unroll
         for (int e = 0; e < N2; ++e) {
             const float2 dy = pair_of<T, VEC>(g, e);
-            xh[e] = mul2(add2(pair_of<T, VEC>(z, e), nm), r2);
+            xh[e] = pair_of<T, VEC>(z, e);
             a[e] = mul2(dy, w[e]);
+            s0 = add2(s0, xh[e]);
             s1 = add2(s1, a[e]);
-            s2 = fma2(a[e], xh[e], s2);
-            dw[e] = fma2(dy, xh[e], dw[e]);
             db[e] = add2(db[e], dy);
         }
-        in.taken();
-        float c1 = s1.x + s1.y, c2 = s2.x + s2.y;
-        group_sum<TPR>(c1, c2, buf, group, turn);
+        float c0 = s0.x + s0.y, c1 = s1.x + s1.y;
+        if (form) {
+            group_sum<TPR>(c0, c1, buf, group, turn);
+            mean = c0 * p.inv_dim;
+        }
+        const float2 nm = make_float2(-mean, -mean);
+        s0 = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int e = 0; e < N2; ++e) xh[e] = add2(xh[e], nm), s2 = fma2(a[e], xh[e], s2);
+        float c2 = s2.x + s2.y;
+        if (form) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const auto c = piece(i);
+                if (!c.whole()) {
+                    int first_c = c.c;
+                    if constexpr (SHIFT) asm volatile("" : "+r"(first_c));
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        if (first_c + e < 0 || first_c + e >= c.dim) half_of(xh, i * VEC + e) = 0.0f;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < N2; ++e) s0 = fma2(xh[e], xh[e], s0);
+            c0 = s0.x + s0.y;
+            group_sum<TPR>(c0, c2, buf, group, turn);
+            rstd = rsqrtf(c0 * p.inv_dim + p.eps);
+        } else {
+            group_sum<TPR>(c1, c2, buf, group, turn);
+        }
+        c2 *= rstd;
+        const float2 r2 = make_float2(rstd, rstd);
+#pragma unroll
+        for (int e = 0; e < N2; ++e) {
+            xh[e] = mul2(xh[e], r2);
+            dw[e] = fma2(pair_of<T, VEC>(g, e), xh[e], dw[e]);
+        }
         const float2 n1 = make_float2(-c1 * p.inv_dim, -c1 * p.inv_dim), n2 = make_float2(-c2 * p.inv_dim, -c2 * p.inv_dim);
 #pragma unroll
         for (int e = 0; e < N2; ++e) {
@@ -496,7 +533,7 @@ int check_norm(const k2t_norm *a)
     if (!a) return K2T_EINVAL;
     if (a->dtype > K2T_FP32) return K2T_EINVAL;
     if (a->dim == 0 || a->dim > K2T_NORM_MAX_DIM || a->n_rows > (1ull << 32)) return K2T_ERANGE;
-    if (!(a->eps > 0.0f)) return K2T_EINVAL;
+    if (!(a->eps > 0.0f) || (a->flags & ~(uint32_t)K2T_NORM_FORM_STATS)) return K2T_EINVAL;
     return K2T_OK;
 }
 
@@ -513,8 +550,9 @@ int dispatch(const k2t_norm *a, NormParams &p, bool backward, cudaStream_t st)
     p.eps = a->eps;
     p.inv_dim = 1.0f / (float)a->dim;
     p.weight = a->weight;
-    p.mean = a->mean;
-    p.rstd = a->rstd;
+    const bool form = backward && (a->flags & K2T_NORM_FORM_STATS);
+    p.mean = form ? nullptr : a->mean;
+    p.rstd = form ? nullptr : a->rstd;
     // Rows that are not whole pieces: shifted where that pays; else value by value while there are few of them, when a call
     // is its latency (4999 x 333 fp32, training: 15 us against 20), else in stretches (200000 x 333 bf16, forward: 170 us
     // against 220; 65536 x 3999: 610 us against 2335).  Forward rows of 1025 to 2048 values fill a block with single values
@@ -560,7 +598,8 @@ int k2t_norm_backward(const k2t_norm *a, void *work, uint64_t work_bytes, void *
 {
     int rc = check_norm(a);
     if (rc) return rc;
-    if (!a->weight || !a->dweight || (a->n_rows && (!a->z || !a->dy || !a->dx || !a->mean || !a->rstd))) return K2T_EINVAL;
+    if (!a->weight || !a->dweight || (a->n_rows && (!a->z || !a->dy || !a->dx))) return K2T_EINVAL;
+    if (a->n_rows && !(a->flags & K2T_NORM_FORM_STATS) && (!a->mean || !a->rstd)) return K2T_EINVAL;
     if (a->n_rows && (!work || ((uintptr_t)work & 15u))) return K2T_EINVAL;
     if (work_bytes < k2t_norm_work_bytes(a)) return K2T_ENOMEM;
     NormParams p{};

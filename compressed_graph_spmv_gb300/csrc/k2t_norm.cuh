@@ -18,7 +18,7 @@ struct NormParams {
     float eps, inv_dim;
     const void *x, *residual, *weight, *bias, *z_in, *dy, *dz;
     void *y, *z, *dx, *dweight, *dbias;
-    float *mean, *rstd, *part;
+    float *mean, *rstd, *part;    // backward: no mean and rstd, form them
     uint32_t parts;
 };
 

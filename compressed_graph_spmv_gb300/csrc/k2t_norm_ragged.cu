@@ -205,7 +205,8 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) ragged_bwd_kernel(const 
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    const bool over = same_skew(p.dy, p.dx);
+    const bool over = same_skew(p.dy, p.dx), form = !p.mean;
+    auto in_row = [&](int i) { return c0 + i * TPR < p.dim; };
     int slot = 0;
     bring(0, false);
     for (; row0 < p.n; row0 += step, off += step_bytes) {
@@ -219,25 +220,46 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) ragged_bwd_kernel(const 
         for (uint32_t r = group; r < here; r += Gr::kGroups) {
             const uint64_t row = row0 + r;
             const size_t off = (size_t)r * p.dim;
-            const float mean = p.mean[row], rstd = p.rstd[row];
-            float xh[PER], a[PER], c1 = 0.0f, c2 = 0.0f;
+            float mean = 0.0f, rstd = 0.0f;
+            if (!form) mean = p.mean[row], rstd = p.rstd[row];
+            float xh[PER], a[PER], sum = 0.0f, c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const uint32_t c = c0 + i * TPR;
                 xh[i] = a[i] = 0.0f;
                 if (c < p.dim) {
                     const float dy = to_f(gs[off + c]);
-                    xh[i] = (to_f(zs[off + c]) - mean) * rstd;
+                    xh[i] = to_f(zs[off + c]);
                     a[i] = dy * w[i];
+                    sum += xh[i];
                     c1 += a[i];
-                    c2 = fmaf(a[i], xh[i], c2);
-                    dw[i] = fmaf(dy, xh[i], dw[i]);
                     db[i] += dy;
                 }
             }
-            group_sum<TPR>(c1, c2, buf, group, turn);
+            if (form) {
+                group_sum<TPR>(sum, c1, buf, group, turn);
+                mean = sum * p.inv_dim;
+                sum = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                xh[i] = in_row(i) ? xh[i] - mean : 0.0f;
+                sum = fmaf(xh[i], xh[i], sum);
+                c2 = fmaf(a[i], xh[i], c2);
+            }
+            if (form) {
+                group_sum<TPR>(sum, c2, buf, group, turn);
+                rstd = rsqrtf(sum * p.inv_dim + p.eps);
+            } else {
+                group_sum<TPR>(c1, c2, buf, group, turn);
+            }
             c1 *= p.inv_dim;
-            c2 *= p.inv_dim;
+            c2 *= p.inv_dim * rstd;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                xh[i] *= rstd;
+                if (in_row(i)) dw[i] = fmaf(to_f(gs[off + c0 + i * TPR]), xh[i], dw[i]);
+            }
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const uint32_t c = c0 + i * TPR;

@@ -40,6 +40,7 @@ EXPORTED = ["k2t_default_opts", "k2t_build", "k2t_workspace_bytes", "k2t_upload"
 
 BF16, FP16, FP32 = 0, 1, 2
 ATTN_MAX_BUCKETS, ATTN_MAX_HOP = 64, 255
+NORM_FORM_STATS = 1
 
 
 class Opts(ctypes.Structure):
@@ -90,7 +91,7 @@ class Attn(ctypes.Structure):
 class Norm(ctypes.Structure):
     """k2t_norm of include/k2t.h."""
     _fields_ = [("dtype", ctypes.c_uint32), ("dim", ctypes.c_uint32), ("n_rows", ctypes.c_uint64),
-                ("eps", ctypes.c_float), ("reserved", ctypes.c_uint32)] + \
+                ("eps", ctypes.c_float), ("flags", ctypes.c_uint32)] + \
         [(name, ctypes.c_void_p) for name in ("x", "residual", "weight", "bias", "y", "z", "mean", "rstd",
                                               "dy", "dz", "dx", "dweight", "dbias")]
 

@@ -13,7 +13,7 @@ import ctypes
 import math
 import struct
 
-from .k2t import (ATTN_MAX_BUCKETS, ATTN_MAX_HOP, BF16, FP16, FP32, Attn, Norm, _check, _stream_ptr, load)
+from .k2t import (ATTN_MAX_BUCKETS, ATTN_MAX_HOP, BF16, FP16, FP32, NORM_FORM_STATS, Attn, Norm, _check, _stream_ptr, load)
 
 
 def hop_edges(n_buckets: int, max_hop: int = 64) -> list:
@@ -182,7 +182,13 @@ assert _AT_INPUTS + _INPUTS.size == _AT_GRADIENTS and _AT_GRADIENTS + _GRADIENTS
 
 
 class LayerNorm:
-    """Layer norm of ``n_rows`` states of ``dim`` values, with the residual sum before it (``k2t_norm``)."""
+    """Layer norm of ``n_rows`` states of ``dim`` values, with the residual sum before it (``k2t_norm``).
+
+    A backward call takes the mean and rstd (fp32 [n_rows] each) that its
+    forward call wrote, or forms them again from the states it is given.
+    ``mean`` and ``rstd`` of the object are of its latest forward call that was
+    not given tensors for them.
+    """
 
     def __init__(self, n_rows: int, dim: int, dtype, residual: bool = False, eps: float = 1e-5, device="cuda"):
         import torch
@@ -193,40 +199,50 @@ class LayerNorm:
         a.dim, a.n_rows, a.eps = dim, n_rows, eps
         self._ref = ctypes.byref(a)
         self._buf = memoryview(a).cast("B")
-        self._rows, self._cols = torch.Size((n_rows, dim)), torch.Size((dim,))
+        self._rows, self._cols, self._one = torch.Size((n_rows, dim)), torch.Size((dim,)), torch.Size((n_rows,))
+        self._float = torch.float32
         self._lib = load()
         self._forward, self._backward = self._lib.k2t_norm_forward, self._lib.k2t_norm_backward
         self._current = _stream_getter(torch)
         self.mean = torch.empty(n_rows, dtype=torch.float32, device=device)
         self.rstd = torch.empty(n_rows, dtype=torch.float32, device=device)
-        a.mean, a.rstd = self.mean.data_ptr(), self.rstd.data_ptr()
+        self._own_stats = self.mean.data_ptr(), self.rstd.data_ptr()
         self._work, self._bytes = None, 0
 
     def work_bytes(self) -> int:
         """Device bytes of the backward pass's work buffer (k2t_norm_work_bytes)."""
         return int(self._lib.k2t_norm_work_bytes(self._ref))
 
-    def forward(self, x, weight, bias, y, residual=None, z=None, stream=None):
-        """y = norm(z) and, with a residual, z = x + residual; keeps mean and rstd for backward."""
+    def _stats(self, mean, rstd):
+        if (mean is None) != (rstd is None):
+            raise ValueError("mean and rstd are given together")
+        if mean is None:
+            return self._own_stats
+        return _flat("mean", mean, self._one, self._float), _flat("rstd", rstd, self._one, self._float)
+
+    def forward(self, x, weight, bias, y, residual=None, z=None, stream=None, mean=None, rstd=None):
+        """y = norm(z) and, with a residual, z = x + residual; writes the rows' mean and rstd."""
         if (residual is not None) != self.residual or (z is not None) != self.residual:
             raise ValueError("residual and z are given exactly when the layer has a residual")
         dt, rows, cols = self.dtype, self._rows, self._cols
         _FORWARD.pack_into(self._buf, _AT_FORWARD, _flat("x", x, rows, dt),
                            0 if residual is None else _flat("residual", residual, rows, dt),
                            _flat("weight", weight, cols, dt), 0 if bias is None else _flat("bias", bias, cols, dt),
-                           _flat("y", y, rows, dt), 0 if z is None else _flat("z", z, rows, dt))
+                           _flat("y", y, rows, dt), 0 if z is None else _flat("z", z, rows, dt), *self._stats(mean, rstd))
         rc = self._forward(self._ref, self._current(x.get_device()) if stream is None else _stream_ptr(stream))
         if rc:
             _check("k2t_norm_forward", rc)
         return y if z is None else (y, z)
 
-    def backward(self, dy, z, weight, dx, dweight, dbias=None, dz=None, stream=None):
+    def backward(self, dy, z, weight, dx, dweight, dbias=None, dz=None, stream=None, mean=None, rstd=None):
         """dx (of x and of the residual alike), dweight and dbias from dy and the forward's z (its x without a
-        residual); dz, the gradient that reaches z from elsewhere, is added to dx."""
+        residual); dz, the gradient that reaches z from elsewhere, is added to dx.  mean and rstd: what the forward call
+        of this z wrote; without them they are formed again from z."""
         dt, rows, cols = self.dtype, self._rows, self._cols
         a = self._a
-        a.z, a.weight = _flat("z", z, rows, dt), _flat("weight", weight, cols, dt)
-        _BACKWARD.pack_into(self._buf, _AT_BACKWARD, _flat("dy", dy, rows, dt),
+        a.weight = _flat("weight", weight, cols, dt)
+        a.flags = NORM_FORM_STATS if mean is None else 0
+        _BACKWARD.pack_into(self._buf, _AT_BACKWARD, _flat("z", z, rows, dt), *self._stats(mean, rstd), _flat("dy", dy, rows, dt),
                             0 if dz is None else _flat("dz", dz, rows, dt), _flat("dx", dx, rows, dt),
                             _flat("dweight", dweight, cols, dt), 0 if dbias is None else _flat("dbias", dbias, cols, dt))
         if self._work is None:
@@ -239,6 +255,7 @@ class LayerNorm:
         return dx, dweight, dbias
 
 
-_FORWARD, _AT_FORWARD = struct.Struct("=6Q"), Norm.x.offset
-_BACKWARD, _AT_BACKWARD = struct.Struct("=5Q"), Norm.dy.offset
-assert _AT_FORWARD + _FORWARD.size == Norm.mean.offset and _AT_BACKWARD + _BACKWARD.size == ctypes.sizeof(Norm)
+# those of k2t_norm: x .. rstd, z .. dbias
+_FORWARD, _AT_FORWARD = struct.Struct("=8Q"), Norm.x.offset
+_BACKWARD, _AT_BACKWARD = struct.Struct("=8Q"), Norm.z.offset
+assert _AT_FORWARD + _FORWARD.size == Norm.dy.offset and _AT_BACKWARD + _BACKWARD.size == ctypes.sizeof(Norm)

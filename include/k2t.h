@@ -441,17 +441,19 @@ K2T_API int k2t_attn_backward(const k2t_attn *a, void *work, uint64_t work_bytes
  *   y = weight * (z - mean) / sqrt(var + eps) + bias,  var = mean (z - mean)^2
  * Rows are contiguous.  All tensors share dtype; statistics are fp32.        */
 #define K2T_NORM_MAX_DIM 16384
+#define K2T_NORM_FORM_STATS 1   /* backward: form mean and rstd from z again, with eps                */
 typedef struct {
     uint32_t dtype;            /* K2T_BF16, K2T_FP16 or K2T_FP32                                     */
     uint32_t dim;              /* 1..16384                                                           */
     uint64_t n_rows;           /* 0 or more, at most 2^32                                            */
     float eps;
-    uint32_t reserved;
+    uint32_t flags;            /* 0, or K2T_NORM_FORM_STATS                                          */
     /* forward */
     const void *x, *residual;  /* [n_rows, dim]; residual may be NULL                                */
     const void *weight, *bias; /* [dim]; bias may be NULL (forward)                                  */
     void *y, *z;               /* [n_rows, dim]; z required with residual, else unused               */
-    float *mean, *rstd;        /* [n_rows] each: forward outputs, backward inputs                    */
+    float *mean, *rstd;        /* [n_rows] each: forward outputs, backward inputs (of that forward
+                                  call; not read with K2T_NORM_FORM_STATS)                          */
     /* backward: gradients of x (and of residual, the same), weight and bias.  `z` is the
      * forward's z, or its x without residual; `dz` is the gradient that reaches z from
      * elsewhere (NULL: none) and is added to dx                                             */
@@ -463,8 +465,8 @@ typedef struct {
 K2T_API uint64_t k2t_norm_work_bytes(const k2t_norm *a);
 
 /* y, z, mean and rstd.  y may be x or residual, z may be x or residual, y and
- * z differ.  Errors: EINVAL (null, bad dtype, eps not positive, pointers not
- * aligned to their element), ERANGE (dim or n_rows), ECUDA. */
+ * z differ.  Errors: EINVAL (null, bad dtype, eps not positive, unknown flags,
+ * pointers not aligned to their element), ERANGE (dim or n_rows), ECUDA. */
 K2T_API int k2t_norm_forward(const k2t_norm *a, void *stream);
 
 /* dx, dweight, dbias; dx may be dy or dz.  Errors as k2t_norm_forward, and
