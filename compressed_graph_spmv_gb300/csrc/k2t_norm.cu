@@ -447,9 +447,9 @@ template <typename T, int VEC, int TPR, int PER, int AHEAD, bool SHIFT, bool BAC
     using Gr = Group<TPR>;
     if constexpr (!BACK) {
         if (!blocks) return K2T_OK;
-        const auto kernel = norm_fwd_kernel<T, VEC, TPR, PER, AHEAD, SHIFT>;
+        constexpr auto kernel = norm_fwd_kernel<T, VEC, TPR, PER, AHEAD, SHIFT>;
         const size_t ring = (size_t)Gr::kThreads * RowStream<T, VEC, TPR, PER, 2, AHEAD, SHIFT>::kBytes;
-        if (ring > 32 * 1024) K2T_NORM_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring));
+        if (int rc = norm_shared<kernel>()) return rc;
         // short blocks even out the SMs: 16 rounds of them 322 us, 2 rounds 357 us on 2^18 x 1024 bf16
         if (AHEAD > 0) blocks = (uint32_t)std::min<uint64_t>((p.n + Gr::kGroups * 4 - 1) / (Gr::kGroups * 4), kNormBlocks * 4);
         if (SHIFT) blocks = (blocks + 7) / 8 * 8;      // a thread's rows a multiple of VEC apart
@@ -458,10 +458,12 @@ template <typename T, int VEC, int TPR, int PER, int AHEAD, bool SHIFT, bool BAC
         if (blocks) {
             const size_t ring = (size_t)Gr::kThreads * RowStream<T, VEC, TPR, PER, 3, AHEAD, SHIFT>::kBytes;
             const size_t sums = Gr::kGroups > 1 ? 2 * p.dim * sizeof(float) : 0;
-            const auto kernel = norm_bwd_kernel<T, VEC, TPR, PER, AHEAD, SHIFT>;
-            if (AHEAD > 0) blocks = norm_resident(kernel, blocks, Gr::kThreads, std::max(ring, sums));
+            constexpr auto kernel = norm_bwd_kernel<T, VEC, TPR, PER, AHEAD, SHIFT>;
+            int rc = norm_shared<kernel>();
+            if (!rc && AHEAD > 0) rc = norm_resident(kernel, blocks, Gr::kThreads, std::max(ring, sums));
+            if (rc) return rc;
             if (SHIFT) blocks = blocks < 8 ? 8 : blocks / 8 * 8;
-            int rc = norm_launch(kernel, dim3(blocks), Gr::kThreads, std::max(ring, sums), st, p);
+            rc = norm_launch(kernel, dim3(blocks), Gr::kThreads, std::max(ring, sums), st, p);
             if (rc) return rc;
         }
         p.parts = blocks;

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -126,14 +127,29 @@ inline uint32_t norm_parts(uint64_t n, int groups)
     return (uint32_t)std::min<uint64_t>((n + groups - 1) / groups, kNormBlocks);
 }
 
+// The dynamic shared memory a kernel may have is a setting of the kernel on a device, which calls of every width and every
+// host thread share: raised once, to all that its static shared memory leaves of the 227 KB.
+template <auto kernel> int norm_shared()
+{
+    static std::atomic<uint64_t> set{0};
+    int dev = 0;
+    K2T_NORM_CUDA(cudaGetDevice(&dev));
+    if (dev < 64 && set.load() >> dev & 1) return K2T_OK;
+    cudaFuncAttributes a{};
+    K2T_NORM_CUDA(cudaFuncGetAttributes(&a, kernel));
+    K2T_NORM_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448 - (int)a.sharedSizeBytes));
+    if (dev < 64) set.fetch_or(1ull << dev);
+    return K2T_OK;
+}
+
 // Backward blocks: as many as the GPU runs at once, and no more than `blocks`; each writes a partial row of the
 // weight's gradient, so that more of them cost more than they even out (445 us against 458 us with twice as many).
-template <typename K> uint32_t norm_resident(K kernel, uint32_t blocks, int threads, size_t smem)
+template <typename K> int norm_resident(K kernel, uint32_t &blocks, int threads, size_t smem)
 {
     int per_sm = 0;
-    if (smem > 32 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1) per_sm = 1;
-    return std::min<uint32_t>(blocks, 152u * per_sm);
+    K2T_NORM_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem));
+    blocks = std::min<uint32_t>(blocks, 152u * std::max(per_sm, 1));
+    return K2T_OK;
 }
 
 template <typename K, typename... A> int norm_launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args)

@@ -298,6 +298,8 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) ragged_bwd_kernel(const 
     }
 }
 
+template <auto K> struct Kernel { static constexpr auto value = K; };
+
 constexpr size_t kRaggedSmem = 225 * 1024;     // of the 227 KB a block may have, beside the few bytes of the group sums
 
 template <typename T, int TPR, int PER> int run_ragged(NormParams &p, bool backward, cudaStream_t st)
@@ -307,15 +309,17 @@ template <typename T, int TPR, int PER> int run_ragged(NormParams &p, bool backw
     const int images = 2 * tensors * b.image <= kRaggedSmem ? 2 : 1;
     const size_t smem = std::max<size_t>(images * tensors * b.image, backward ? 2 * p.dim * sizeof(float) : 0);
     uint32_t blocks = (uint32_t)std::min<uint64_t>((p.n + b.rows - 1) / b.rows, kNormBlocks);
-    auto launch = [&](auto kernel) -> int {
+    auto launch = [&](auto of) -> int {
+        constexpr auto kernel = decltype(of)::value;
+        int rc = norm_shared<kernel>();
         // as many as run at once: blocks stay, and their copies run ahead
-        blocks = norm_resident(kernel, blocks, Group<TPR>::kThreads, smem);
+        if (!rc) rc = norm_resident(kernel, blocks, Group<TPR>::kThreads, smem);
         p.parts = blocks;
-        if (!blocks) return K2T_OK;
+        if (rc || !blocks) return rc;
         return norm_launch(kernel, dim3(blocks), Group<TPR>::kThreads, smem, st, p, b.rows, b.image, images);
     };
-    if (!backward) return launch(ragged_fwd_kernel<T, TPR, PER>);
-    int rc = launch(ragged_bwd_kernel<T, TPR, PER>);
+    if (!backward) return launch(Kernel<ragged_fwd_kernel<T, TPR, PER>>());
+    int rc = launch(Kernel<ragged_bwd_kernel<T, TPR, PER>>());
     return rc ? rc : norm_launch(norm_join_kernel<T>, dim3((p.dim + 7) / 8, p.dbias ? 2 : 1), 1024, 0, st, p);
 }
 
