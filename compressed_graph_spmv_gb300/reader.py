@@ -6,12 +6,14 @@ As in ``k2t.py``, argument marshalling only.  An object holds the sizes and
 the work buffer of one layer; its calls take tensors that the caller owns,
 write the output tensors they are given and return them.  Calls of one
 object share its buffers: order them on the GPU (one stream, or events).
+Host threads may call one object; each call queues its kernels together.
 """
 from __future__ import annotations
 
 import ctypes
 import math
 import struct
+import threading
 
 from .k2t import (ATTN_MAX_BUCKETS, ATTN_MAX_HOP, BF16, FP16, FP32, NORM_FORM_STATS, Attn, Norm, _check, _stream_ptr, load)
 
@@ -113,6 +115,7 @@ class HopAttention:
         self._forward, self._backward = self._lib.k2t_attn_forward, self._lib.k2t_attn_backward
         self._current = _stream_getter(torch)
         self._work, self._bytes, self._at = [None, None], [0, 0], [0, 0]
+        self._lock = threading.Lock()      # of the struct and the buffers: ctypes lets other threads run during a call
 
     def work_bytes(self, backward: bool = False) -> int:
         """Device bytes of the work buffer of a pass (k2t_attn_work_bytes)."""
@@ -151,9 +154,10 @@ class HopAttention:
 
     def forward(self, q, k, v, out, lse, hops=None, bias=None, query_source=None, stream=None):
         """out [T, n_heads, head_dim] and lse (fp32 [T, n_heads]) of q, k, v."""
-        self._inputs(q, k, v, out, lse, hops, bias, query_source)
-        work, size = self._work_of(0)
-        rc = self._forward(self._ref, work, size, self._current(q.get_device()) if stream is None else _stream_ptr(stream))
+        with self._lock:
+            self._inputs(q, k, v, out, lse, hops, bias, query_source)
+            work, size = self._work_of(0)
+            rc = self._forward(self._ref, work, size, self._current(q.get_device()) if stream is None else _stream_ptr(stream))
         if rc:
             _check("k2t_attn_forward", rc)
         return out, lse
@@ -161,15 +165,16 @@ class HopAttention:
     def backward(self, dout, q, k, v, out, lse, dq, dk, dv, dbias=None, hops=None, bias=None, query_source=None,
                  stream=None):
         """Gradients of q, k, v and the bias table from dout, the inputs and the forward's out and lse."""
-        self._inputs(q, k, v, out, lse, hops, bias, query_source)
         dt = self.dtype
-        dqp, dqr, dqh = _rows("dq", dq, self._rows, dt)
-        dkp, dkr, dkh = _rows("dk", dk, self._nodes, dt)
-        dvp, dvr, dvh = _rows("dv", dv, self._nodes, dt)
-        _GRADIENTS.pack_into(self._buf, _AT_GRADIENTS, *_rows("dout", dout, self._rows, dt), dqp, dkp, dvp, dqr, dqh,
-                             dkr, dkh, dvr, dvh, 0 if dbias is None else _flat("dbias", dbias, self._table, dt))
-        work, size = self._work_of(1)
-        rc = self._backward(self._ref, work, size, self._current(q.get_device()) if stream is None else _stream_ptr(stream))
+        with self._lock:
+            self._inputs(q, k, v, out, lse, hops, bias, query_source)
+            dqp, dqr, dqh = _rows("dq", dq, self._rows, dt)
+            dkp, dkr, dkh = _rows("dk", dk, self._nodes, dt)
+            dvp, dvr, dvh = _rows("dv", dv, self._nodes, dt)
+            _GRADIENTS.pack_into(self._buf, _AT_GRADIENTS, *_rows("dout", dout, self._rows, dt), dqp, dkp, dvp, dqr, dqh,
+                                 dkr, dkh, dvr, dvh, 0 if dbias is None else _flat("dbias", dbias, self._table, dt))
+            work, size = self._work_of(1)
+            rc = self._backward(self._ref, work, size, self._current(q.get_device()) if stream is None else _stream_ptr(stream))
         if rc:
             _check("k2t_attn_backward", rc)
         return dq, dk, dv, dbias
@@ -208,6 +213,7 @@ class LayerNorm:
         self.rstd = torch.empty(n_rows, dtype=torch.float32, device=device)
         self._own_stats = self.mean.data_ptr(), self.rstd.data_ptr()
         self._work, self._bytes = None, 0
+        self._lock = threading.Lock()
 
     def work_bytes(self) -> int:
         """Device bytes of the backward pass's work buffer (k2t_norm_work_bytes)."""
@@ -225,11 +231,13 @@ class LayerNorm:
         if (residual is not None) != self.residual or (z is not None) != self.residual:
             raise ValueError("residual and z are given exactly when the layer has a residual")
         dt, rows, cols = self.dtype, self._rows, self._cols
-        _FORWARD.pack_into(self._buf, _AT_FORWARD, _flat("x", x, rows, dt),
-                           0 if residual is None else _flat("residual", residual, rows, dt),
-                           _flat("weight", weight, cols, dt), 0 if bias is None else _flat("bias", bias, cols, dt),
-                           _flat("y", y, rows, dt), 0 if z is None else _flat("z", z, rows, dt), *self._stats(mean, rstd))
-        rc = self._forward(self._ref, self._current(x.get_device()) if stream is None else _stream_ptr(stream))
+        with self._lock:
+            self._a.flags = 0
+            _FORWARD.pack_into(self._buf, _AT_FORWARD, _flat("x", x, rows, dt),
+                               0 if residual is None else _flat("residual", residual, rows, dt),
+                               _flat("weight", weight, cols, dt), 0 if bias is None else _flat("bias", bias, cols, dt),
+                               _flat("y", y, rows, dt), 0 if z is None else _flat("z", z, rows, dt), *self._stats(mean, rstd))
+            rc = self._forward(self._ref, self._current(x.get_device()) if stream is None else _stream_ptr(stream))
         if rc:
             _check("k2t_norm_forward", rc)
         return y if z is None else (y, z)
@@ -240,16 +248,17 @@ class LayerNorm:
         of this z wrote; without them they are formed again from z."""
         dt, rows, cols = self.dtype, self._rows, self._cols
         a = self._a
-        a.weight = _flat("weight", weight, cols, dt)
-        a.flags = NORM_FORM_STATS if mean is None else 0
-        _BACKWARD.pack_into(self._buf, _AT_BACKWARD, _flat("z", z, rows, dt), *self._stats(mean, rstd), _flat("dy", dy, rows, dt),
-                            0 if dz is None else _flat("dz", dz, rows, dt), _flat("dx", dx, rows, dt),
-                            _flat("dweight", dweight, cols, dt), 0 if dbias is None else _flat("dbias", dbias, cols, dt))
-        if self._work is None:
-            self._bytes = self.work_bytes()
-            self._work = self._torch.empty(max(16, self._bytes), dtype=self._torch.uint8, device=self.device)
-        rc = self._backward(self._ref, self._work.data_ptr(), self._bytes,
-                            self._current(dy.get_device()) if stream is None else _stream_ptr(stream))
+        with self._lock:
+            a.weight = _flat("weight", weight, cols, dt)
+            a.flags = NORM_FORM_STATS if mean is None else 0
+            _BACKWARD.pack_into(self._buf, _AT_BACKWARD, _flat("z", z, rows, dt), *self._stats(mean, rstd), _flat("dy", dy, rows, dt),
+                                0 if dz is None else _flat("dz", dz, rows, dt), _flat("dx", dx, rows, dt),
+                                _flat("dweight", dweight, cols, dt), 0 if dbias is None else _flat("dbias", dbias, cols, dt))
+            if self._work is None:
+                self._bytes = self.work_bytes()
+                self._work = self._torch.empty(max(16, self._bytes), dtype=self._torch.uint8, device=self.device)
+            rc = self._backward(self._ref, self._work.data_ptr(), self._bytes,
+                                self._current(dy.get_device()) if stream is None else _stream_ptr(stream))
         if rc:
             _check("k2t_norm_backward", rc)
         return dx, dweight, dbias

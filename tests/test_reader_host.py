@@ -1,11 +1,16 @@
 """Graph-reading calls on the host: flags, layouts of outputs, threads, devices (no GPU)."""
 import ctypes
+import threading
+import time
 
 import pytest
 
 from test_reader_refusals import ENOMEM, EINVAL, P, norm
 
 K = pytest.importorskip("compressed_graph_spmv_gb300.k2t")
+torch = pytest.importorskip("torch")
+import compressed_graph_spmv_gb300 as pkg  # noqa: E402
+from compressed_graph_spmv_gb300 import reader  # noqa: E402
 
 
 def test_norm_flags():
@@ -19,3 +24,105 @@ def test_norm_flags():
     a = norm(flags=K.NORM_FORM_STATS, mean=None, rstd=None)
     assert lib.k2t_norm_backward(ctypes.byref(a), P, 0, None) == ENOMEM
     assert lib.k2t_norm_forward(ctypes.byref(a), None) == EINVAL
+
+
+class Card:
+    """A tensor as the calls see one, on a card that is not there."""
+
+    def __init__(self, *shape, dtype=torch.bfloat16, at=P, device=0, strides=None):
+        self.shape, self.dtype, self.ndim, self.at, self.device_index = torch.Size(shape), dtype, len(shape), at, device
+        self.is_cuda, self.strides = True, strides or torch.empty(shape, device="meta").stride()
+
+    def get_device(self):
+        return self.device_index
+
+    def is_contiguous(self):
+        return True
+
+    def stride(self):
+        return self.strides
+
+    def numel(self):
+        return self.shape.numel()
+
+    def data_ptr(self):
+        return self.at
+
+
+def attention(monkeypatch, call):
+    """An attention object whose C calls are `call(struct)`, and its tensors at addresses from `at` on."""
+    op = pkg.HopAttention(2, 3, 2, 1, 64, torch.bfloat16, sources=2, edges=[0, 1])
+    fake = lambda ref, work, size, stream: call(op._a)  # noqa: E731
+    op._forward = op._backward = fake
+    monkeypatch.setattr(op, "_work_of", lambda *a: (P, 1 << 20))
+    op._current = lambda device: 0
+
+    def tensors(at, device=0):
+        shapes = dict(q=(2, 2, 64), k=(3, 1, 64), v=(3, 1, 64), out=(2, 2, 64), lse=(2, 2), hops=(3, 2), bias=(2, 2), dout=(2, 2, 64),
+                      dq=(2, 2, 64), dk=(3, 1, 64), dv=(3, 1, 64), dbias=(2, 2))
+        types = dict(lse=torch.float32, hops=torch.int32)
+        return {x: Card(*s, dtype=types.get(x, torch.bfloat16), at=at + i * 4096, device=device) for i, (x, s) in enumerate(shapes.items())}
+    return op, tensors
+
+
+def forward(op, t):
+    op.forward(t["q"], t["k"], t["v"], t["out"], t["lse"], hops=t["hops"], bias=t["bias"])
+
+
+def backward(op, t):
+    op.backward(t["dout"], t["q"], t["k"], t["v"], t["out"], t["lse"], t["dq"], t["dk"], t["dv"], dbias=t["dbias"], hops=t["hops"],
+                bias=t["bias"])
+
+
+def in_threads(jobs):
+    errors = []
+
+    def body(job):
+        try:
+            job()
+        except Exception as e:   # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=body, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+
+
+@pytest.mark.parametrize("call", [forward, backward])
+def test_threads_share_an_attention_object(monkeypatch, call):
+    """What a C call reads does not change while it runs, and no two run at once."""
+    inside, seen = [], []
+
+    def c_call(a):
+        inside.append(1)
+        before = bytes(a)
+        time.sleep(0.02)
+        seen.append((len(inside), bytes(a) == before, a.q, a.k))
+        inside.pop()
+        return 0
+    op, tensors = attention(monkeypatch, c_call)
+    sets = [tensors(P * (i + 1)) for i in range(4)]
+    in_threads([lambda t=t: call(op, t) for t in sets])
+    assert all(n == 1 and same for n, same, _, _ in seen)
+    assert sorted((q, k) for _, _, q, k in seen) == sorted((t["q"].at, t["k"].at) for t in sets)
+
+
+def test_threads_share_a_norm_object():
+    op = pkg.LayerNorm(4, 8, torch.float32, device="cpu")
+    seen = []
+
+    def c_call(*_):
+        before = bytes(op._a)
+        time.sleep(0.02)
+        seen.append((bytes(op._a) == before, op._a.x if op._a.flags == 0 else op._a.dy, op._a.weight))
+        return 0
+    op._forward = op._backward = c_call
+    op._current = lambda device: 0
+
+    def job(i):
+        x, w = Card(4, 8, dtype=torch.float32, at=P * i), Card(8, dtype=torch.float32, at=P * i + 64)
+        return (lambda: op.forward(x, w, None, x)) if i % 2 else (lambda: op.backward(x, x, w, x, w))
+    in_threads([job(i) for i in range(1, 7)])
+    assert all(same for same, _, _ in seen) and sorted((x, w) for _, x, w in seen) == [(P * i, P * i + 64) for i in range(1, 7)]
