@@ -5,7 +5,9 @@ queries to node states biased by hop distance, and layer norm of node states
 As in ``k2t.py``, argument marshalling only.  An object holds the sizes and
 the work buffer of one layer; its calls take tensors that the caller owns,
 write the output tensors they are given and return them.  Calls of one
-object share its buffers: order them on the GPU (one stream, or events).
+object share its buffers: order them on the GPU (one stream, or events).  The
+buffers are made on the stream of the call that first needs them; a stream
+that a call was given has to outlive the object.
 Host threads may call one object; each call queues its kernels together.
 """
 from __future__ import annotations
@@ -78,6 +80,38 @@ def _rows(name, t, shape, dtype):
     return t.data_ptr(), row if shape[0] > 1 else 0, head if shape[1] > 1 else 0
 
 
+class _Buffer:
+    """Device memory of an object, made by the first call that needs it on that call's stream, so that what the allocator's
+    memory was used for before has ended there, and given back only when the work of every stream it served has ended."""
+
+    def __init__(self, torch, device, current):
+        self._torch, self._device, self._current = torch, device, current
+        self.tensor, self.at, self._streams, self.last = None, 0, None, None     # last: stream of the latest call
+
+    def _stream(self, ptr, device):
+        cuda = self._torch.cuda
+        return cuda.ExternalStream(ptr, device=device) if ptr else cuda.default_stream(device)
+
+    def get(self, size, ptr, device, zeroed=0):
+        """Address of `size` bytes for a call on stream `ptr`; the first `zeroed` ones are zero when they are made."""
+        if self.tensor is None:
+            torch = self._torch
+            if ptr == self._current(device):
+                made = torch.empty(size, dtype=torch.uint8, device=self._device)
+                made[:zeroed].zero_()
+            else:
+                with torch.cuda.stream(self._stream(ptr, device)):
+                    made = torch.empty(size, dtype=torch.uint8, device=self._device)
+                    made[:zeroed].zero_()
+            self.tensor, self.at, self._streams, self.last = made, made.data_ptr(), {ptr}, ptr
+        elif ptr != self.last:
+            if ptr not in self._streams:
+                self.tensor.record_stream(self._stream(ptr, device))
+                self._streams.add(ptr)
+            self.last = ptr
+        return self.at
+
+
 class HopAttention:
     """Attention of ``n_queries`` queries to the states of ``n_nodes`` nodes.
 
@@ -114,20 +148,24 @@ class HopAttention:
         self._lib = load()
         self._forward, self._backward = self._lib.k2t_attn_forward, self._lib.k2t_attn_backward
         self._current = _stream_getter(torch)
-        self._work, self._bytes, self._at = [None, None], [0, 0], [0, 0]
+        self._buffers, self._bytes = [_Buffer(torch, device, self._current) for _ in range(2)], [0, 0]
         self._lock = threading.Lock()      # of the struct and the buffers: ctypes lets other threads run during a call
 
     def work_bytes(self, backward: bool = False) -> int:
         """Device bytes of the work buffer of a pass (k2t_attn_work_bytes)."""
         return int(self._lib.k2t_attn_work_bytes(self._ref, int(backward)))
 
-    def _work_of(self, backward: int):
-        if self._work[backward] is None:
+    @property
+    def _work(self):
+        return [b.tensor for b in self._buffers]
+
+    def _work_of(self, backward: int, stream=None, device=None):
+        if device is None:
+            device = self._torch.cuda.current_device()
+        if not self._bytes[backward]:
             self._bytes[backward] = self.work_bytes(bool(backward))
-            self._work[backward] = self._torch.empty(self._bytes[backward], dtype=self._torch.uint8, device=self.device)
-            self._work[backward][:4].zero_()
-            self._at[backward] = self._work[backward].data_ptr()
-        return self._at[backward], self._bytes[backward]
+        size = self._bytes[backward]
+        return self._buffers[backward].get(size, self._current(device) if stream is None else stream, device, zeroed=4), size
 
     def status(self) -> int:
         """The device status words of both passes, joined: waits for the device; 0, or
@@ -135,6 +173,7 @@ class HopAttention:
         word = 0
         for work in self._work:
             if work is not None:
+                self._torch.cuda.synchronize()
                 word |= int(work[:4].view(self._torch.int32).item())
         return word
 
@@ -156,8 +195,12 @@ class HopAttention:
         """out [T, n_heads, head_dim] and lse (fp32 [T, n_heads]) of q, k, v."""
         with self._lock:
             self._inputs(q, k, v, out, lse, hops, bias, query_source)
-            work, size = self._work_of(0)
-            rc = self._forward(self._ref, work, size, self._current(q.get_device()) if stream is None else _stream_ptr(stream))
+            device = q.get_device()
+            st = self._current(device) if stream is None else _stream_ptr(stream)
+            work = self._buffers[0]
+            if work.last != st:
+                self._work_of(0, st, device)
+            rc = self._forward(self._ref, work.at, self._bytes[0], st)
         if rc:
             _check("k2t_attn_forward", rc)
         return out, lse
@@ -173,8 +216,12 @@ class HopAttention:
             dvp, dvr, dvh = _rows("dv", dv, self._nodes, dt)
             _GRADIENTS.pack_into(self._buf, _AT_GRADIENTS, *_rows("dout", dout, self._rows, dt), dqp, dkp, dvp, dqr, dqh,
                                  dkr, dkh, dvr, dvh, 0 if dbias is None else _flat("dbias", dbias, self._table, dt))
-            work, size = self._work_of(1)
-            rc = self._backward(self._ref, work, size, self._current(q.get_device()) if stream is None else _stream_ptr(stream))
+            device = q.get_device()
+            st = self._current(device) if stream is None else _stream_ptr(stream)
+            work = self._buffers[1]
+            if work.last != st:
+                self._work_of(1, st, device)
+            rc = self._backward(self._ref, work.at, self._bytes[1], st)
         if rc:
             _check("k2t_attn_backward", rc)
         return dq, dk, dv, dbias
@@ -209,21 +256,34 @@ class LayerNorm:
         self._lib = load()
         self._forward, self._backward = self._lib.k2t_norm_forward, self._lib.k2t_norm_backward
         self._current = _stream_getter(torch)
-        self.mean = torch.empty(n_rows, dtype=torch.float32, device=device)
-        self.rstd = torch.empty(n_rows, dtype=torch.float32, device=device)
-        self._own_stats = self.mean.data_ptr(), self.rstd.data_ptr()
-        self._work, self._bytes = None, 0
+        self._n = n_rows
+        self._work, self._own = (_Buffer(torch, device, self._current) for _ in range(2))     # backward's; mean and rstd
+        self._bytes = None
         self._lock = threading.Lock()
 
     def work_bytes(self) -> int:
         """Device bytes of the backward pass's work buffer (k2t_norm_work_bytes)."""
         return int(self._lib.k2t_norm_work_bytes(self._ref))
 
-    def _stats(self, mean, rstd):
+    def _own_stats(self, stream, device):
+        own = self._own
+        at = own.at if own.last == stream else own.get(max(8 * self._n, 16), stream, device)
+        return at, at + 4 * self._n
+
+    def _stat(self, which):
+        with self._lock:
+            device = self._torch.cuda.current_device()
+            self._own_stats(self._current(device), device)
+            return self._own.tensor.view(self._float)[which * self._n:(which + 1) * self._n]
+
+    mean = property(lambda self: self._stat(0), doc="Means of the latest forward call that was not given a tensor for them.")
+    rstd = property(lambda self: self._stat(1), doc="Likewise 1 / sqrt(var + eps).")
+
+    def _stats(self, mean, rstd, stream=None, device=None):
         if (mean is None) != (rstd is None):
             raise ValueError("mean and rstd are given together")
-        if mean is None:
-            return self._own_stats
+        if mean is None:      # a forward call writes the object's own, a backward call needs none
+            return (0, 0) if device is None else self._own_stats(stream, device)
         return _flat("mean", mean, self._one, self._float), _flat("rstd", rstd, self._one, self._float)
 
     def forward(self, x, weight, bias, y, residual=None, z=None, stream=None, mean=None, rstd=None):
@@ -232,12 +292,14 @@ class LayerNorm:
             raise ValueError("residual and z are given exactly when the layer has a residual")
         dt, rows, cols = self.dtype, self._rows, self._cols
         with self._lock:
-            self._a.flags = 0
-            _FORWARD.pack_into(self._buf, _AT_FORWARD, _flat("x", x, rows, dt),
+            at, device = _flat("x", x, rows, dt), x.get_device()
+            st = self._current(device) if stream is None else _stream_ptr(stream)
+            _FORWARD.pack_into(self._buf, _AT_FORWARD, 0, at,
                                0 if residual is None else _flat("residual", residual, rows, dt),
                                _flat("weight", weight, cols, dt), 0 if bias is None else _flat("bias", bias, cols, dt),
-                               _flat("y", y, rows, dt), 0 if z is None else _flat("z", z, rows, dt), *self._stats(mean, rstd))
-            rc = self._forward(self._ref, self._current(x.get_device()) if stream is None else _stream_ptr(stream))
+                               _flat("y", y, rows, dt), 0 if z is None else _flat("z", z, rows, dt),
+                               *self._stats(mean, rstd, st, device))
+            rc = self._forward(self._ref, st)
         if rc:
             _check("k2t_norm_forward", rc)
         return y if z is None else (y, z)
@@ -247,24 +309,21 @@ class LayerNorm:
         residual); dz, the gradient that reaches z from elsewhere, is added to dx.  mean and rstd: what the forward call
         of this z wrote; without them they are formed again from z."""
         dt, rows, cols = self.dtype, self._rows, self._cols
-        a = self._a
         with self._lock:
-            a.weight = _flat("weight", weight, cols, dt)
-            a.flags = NORM_FORM_STATS if mean is None else 0
-            _BACKWARD.pack_into(self._buf, _AT_BACKWARD, _flat("z", z, rows, dt), *self._stats(mean, rstd), _flat("dy", dy, rows, dt),
+            _BACKWARD.pack_into(self._buf, _AT_FORWARD, NORM_FORM_STATS if mean is None else 0, 0, 0, _flat("weight", weight, cols, dt),
+                                0, 0, _flat("z", z, rows, dt), *self._stats(mean, rstd), _flat("dy", dy, rows, dt),
                                 0 if dz is None else _flat("dz", dz, rows, dt), _flat("dx", dx, rows, dt),
                                 _flat("dweight", dweight, cols, dt), 0 if dbias is None else _flat("dbias", dbias, cols, dt))
-            if self._work is None:
+            if self._bytes is None:
                 self._bytes = self.work_bytes()
-                self._work = self._torch.empty(max(16, self._bytes), dtype=self._torch.uint8, device=self.device)
-            rc = self._backward(self._ref, self._work.data_ptr(), self._bytes,
-                                self._current(dy.get_device()) if stream is None else _stream_ptr(stream))
+            device = dy.get_device()
+            st = self._current(device) if stream is None else _stream_ptr(stream)
+            rc = self._backward(self._ref, self._work.get(max(16, self._bytes), st, device), self._bytes, st)
         if rc:
             _check("k2t_norm_backward", rc)
         return dx, dweight, dbias
 
 
-# those of k2t_norm: x .. rstd, z .. dbias
-_FORWARD, _AT_FORWARD = struct.Struct("=8Q"), Norm.x.offset
-_BACKWARD, _AT_BACKWARD = struct.Struct("=8Q"), Norm.z.offset
-assert _AT_FORWARD + _FORWARD.size == Norm.dy.offset and _AT_BACKWARD + _BACKWARD.size == ctypes.sizeof(Norm)
+# flags and pointers of k2t_norm: up to rstd, and all
+_FORWARD, _BACKWARD, _AT_FORWARD = struct.Struct("=I8Q"), struct.Struct("=I13Q"), Norm.flags.offset
+assert _AT_FORWARD + _FORWARD.size == Norm.dy.offset and _AT_FORWARD + _BACKWARD.size == ctypes.sizeof(Norm)

@@ -54,3 +54,68 @@ def test_norms_of_two_widths_in_two_threads(dims):
     jobs = [job(d) for d in dims for _ in range(3)]
     torch.cuda.synchronize()
     together(jobs)
+
+
+def attention(n=5000):
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    t = dict(q=rand(9, 4, 64), k=rand(n, 2, 64), v=rand(n, 2, 64), dout=rand(9, 4, 64))
+    t.update({"d" + x: torch.empty_like(t[x]) for x in "qkv"}, out=torch.empty_like(t["q"]), lse=torch.empty(9, 4, device="cuda"))
+    op = pkg.HopAttention(9, n, 4, 2, 64, torch.bfloat16)
+    fwd = lambda stream=None: op.forward(t["q"], t["k"], t["v"], t["out"], t["lse"], stream=stream)  # noqa: E731
+    bwd = lambda stream=None: op.backward(t["dout"], t["q"], t["k"], t["v"], t["out"], t["lse"], t["dq"], t["dk"], t["dv"],  # noqa: E731
+                                          stream=stream)
+    return op, t, fwd, bwd
+
+
+def test_first_call_on_another_stream_than_the_current():
+    """The work buffers and their cleared status words belong to the stream of the call: nothing waits for the current one."""
+    op, t, fwd, bwd = attention()
+    fwd()
+    bwd()
+    want = {x: t[x].clone() for x in ("out", "lse", "dq", "dk", "dv")}
+    op, t, fwd, bwd = attention()
+    stale = [torch.full((op.work_bytes(b),), 0xff, dtype=torch.uint8, device="cuda") for b in (False, True)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    del stale
+    torch.cuda._sleep(500_000_000)                     # the current stream is busy for a quarter of a second
+    fwd(side)
+    bwd(side)
+    with torch.cuda.stream(side):
+        words = [w[:4].cpu() for w in op._work]         # ordered after the calls on their stream alone
+        got = {x: t[x].clone() for x in want}
+    assert not torch.cuda.current_stream().query(), "the current stream was to be busy all along"
+    assert all((w == 0).all() for w in words)
+    torch.cuda.synchronize()
+    assert op.status() == 0 and all(torch.equal(want[x], got[x]) for x in want)
+
+
+@pytest.mark.parametrize("first", ["current", "side"])
+def test_buffers_of_an_object_that_goes_while_its_calls_run(first):
+    """Memory that another stream still uses is not handed out again."""
+    op, t, fwd, bwd = attention()
+    norm = pkg.LayerNorm(4000, 512, torch.bfloat16)
+    x, w = torch.randn(4000, 512, device="cuda").to(torch.bfloat16), torch.ones(512, dtype=torch.bfloat16, device="cuda")
+    y, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty_like(w)
+    side = torch.cuda.Stream()
+
+    def call(stream):
+        fwd(stream)
+        bwd(stream)
+        norm.forward(x, w, None, y, stream=stream)
+        norm.backward(x, x, w, dx, dw, stream=stream)
+    if first == "current":
+        call(None)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(500_000_000)
+    call(side)
+    sizes = [op.work_bytes(False), op.work_bytes(True), norm.work_bytes(), 8 * 4000, 4 * 4000]
+    held = [(b.at, b.tensor.numel()) for b in (*op._buffers, norm._work, norm._own)]
+    del op, fwd, bwd, norm, call
+    again = [torch.empty(s, dtype=torch.uint8, device="cuda") for s in sizes for _ in range(3)]
+    assert not side.query()
+    for a in again:
+        assert all(a.data_ptr() + a.numel() <= at or at + size <= a.data_ptr() for at, size in held)
+    torch.cuda.synchronize()

@@ -54,7 +54,8 @@ def attention(monkeypatch, call):
     op = pkg.HopAttention(2, 3, 2, 1, 64, torch.bfloat16, sources=2, edges=[0, 1])
     fake = lambda ref, work, size, stream: call(op._a)  # noqa: E731
     op._forward = op._backward = fake
-    monkeypatch.setattr(op, "_work_of", lambda *a: (P, 1 << 20))
+    for b in op._buffers:
+        b.at, b.last = P, 0
     op._current = lambda device: 0
 
     def tensors(at, device=0):
@@ -119,7 +120,7 @@ def test_threads_share_a_norm_object():
         seen.append((bytes(op._a) == before, op._a.x if op._a.flags == 0 else op._a.dy, op._a.weight))
         return 0
     op._forward = op._backward = c_call
-    op._current = lambda device: 0
+    op._current = op._own._current = op._work._current = lambda device: 0
 
     def job(i):
         x, w = Card(4, 8, dtype=torch.float32, at=P * i), Card(8, dtype=torch.float32, at=P * i + 64)
