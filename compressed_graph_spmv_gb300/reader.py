@@ -53,7 +53,12 @@ def _stream_getter(torch):
     return lambda device: torch.cuda.current_stream(device).cuda_stream
 
 
-def _refuse(name, t, shape, dtype, last_only):
+def _device_getter(torch):
+    """The current device's number, torch's own short way where it has one."""
+    return getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _refuse(name, t, shape, dtype, device, last_only):
     """Say what is wrong with a tensor that a call does not take."""
     if t.shape != shape:
         raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
@@ -61,22 +66,24 @@ def _refuse(name, t, shape, dtype, last_only):
         raise TypeError("%s: expected %s, got %s" % (name, dtype, t.dtype))
     if not t.is_cuda:
         raise ValueError("%s: expected a CUDA tensor" % name)
+    if t.get_device() != device:
+        raise ValueError("%s: on device %d, the call is on device %d" % (name, t.get_device(), device))
     raise ValueError("%s: expected a contiguous %s" % (name, "last dimension" if last_only else "tensor"))
 
 
-def _flat(name, t, shape, dtype):
-    """Address of a contiguous CUDA tensor of this shape and type."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        _refuse(name, t, shape, dtype, False)
+def _flat(name, t, shape, dtype, device):
+    """Address of a contiguous tensor of this shape and type on this device."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        _refuse(name, t, shape, dtype, device, False)
     return t.data_ptr()
 
 
-def _rows(name, t, shape, dtype):
-    """(address, row pitch, head pitch) of a CUDA tensor [rows, heads, dim] whose last dimension is contiguous; a
-    dimension of one value has no pitch, whatever its stride says."""
+def _rows(name, t, shape, dtype, device):
+    """(address, row pitch, head pitch) of a tensor [rows, heads, dim] on this device whose last dimension is contiguous;
+    a dimension of one value has no pitch, whatever its stride says."""
     row, head, last = t.stride()
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or last != 1 and t.numel():
-        _refuse(name, t, shape, dtype, True)
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or last != 1 and t.numel():
+        _refuse(name, t, shape, dtype, device, True)
     return t.data_ptr(), row if shape[0] > 1 else 0, head if shape[1] > 1 else 0
 
 
@@ -112,7 +119,28 @@ class _Buffer:
         return self.at
 
 
-class HopAttention:
+class _Placed:
+    """The device of an object: of its first call's tensors, or the one it was made for."""
+    _on = None
+
+    def _device_of(self, name, t):
+        """Device of a call whose first tensor is t (-2, which no tensor is on, for a host tensor)."""
+        device = t.get_device()
+        if device != self._on:
+            if device < 0:
+                return -2
+            if self._on is None:
+                self._on = self._torch.device(self.device).index
+            if self._on is None:
+                self._on = device
+            if device != self._on:
+                raise ValueError("%s: on device %d, the object is on device %d" % (name, device, self._on))
+        if device != self._here():
+            raise ValueError("%s: on device %d, which is not the current one" % (name, device))
+        return device
+
+
+class HopAttention(_Placed):
     """Attention of ``n_queries`` queries to the states of ``n_nodes`` nodes.
 
     ``sources`` columns of a hop table (int32 [n_nodes, sources], as
@@ -147,7 +175,7 @@ class HopAttention:
         self._table = torch.Size((n_heads, len(edges)))
         self._lib = load()
         self._forward, self._backward = self._lib.k2t_attn_forward, self._lib.k2t_attn_backward
-        self._current = _stream_getter(torch)
+        self._current, self._here = _stream_getter(torch), _device_getter(torch)
         self._buffers, self._bytes = [_Buffer(torch, device, self._current) for _ in range(2)], [0, 0]
         self._lock = threading.Lock()      # of the struct and the buffers: ctypes lets other threads run during a call
 
@@ -178,24 +206,24 @@ class HopAttention:
         return word
 
     def _inputs(self, q, k, v, out, lse, hops, bias, query_source):
-        a, dt = self._a, self.dtype
+        a, dt, device = self._a, self.dtype, self._device_of("q", q)
         if (hops is None) != (a.n_sources == 0):
             raise ValueError("hops: given %s, sources %d" % (hops is not None, a.n_sources))
-        qp, qr, qh = _rows("q", q, self._rows, dt)
-        kp, kr, kh = _rows("k", k, self._nodes, dt)
-        vp, vr, vh = _rows("v", v, self._nodes, dt)
-        op, orow, oh = _rows("out", out, self._rows, dt)
+        qp, qr, qh = _rows("q", q, self._rows, dt, device)
+        kp, kr, kh = _rows("k", k, self._nodes, dt, device)
+        vp, vr, vh = _rows("v", v, self._nodes, dt, device)
+        op, orow, oh = _rows("out", out, self._rows, dt, device)
         _INPUTS.pack_into(self._buf, _AT_INPUTS, qp, kp, vp, qr, qh, kr, kh, vr, vh,
-                          0 if hops is None else _flat("hops", hops, self._hops if hops.ndim == 2 else self._hops_flat, self._int),
-                          0 if query_source is None else _flat("query_source", query_source, self._source, self._int),
-                          0 if bias is None else _flat("bias", bias, self._table, dt),
-                          op, _flat("lse", lse, self._lse, self._float), orow, oh)
+                          0 if hops is None else _flat("hops", hops, self._hops if hops.ndim == 2 else self._hops_flat, self._int, device),
+                          0 if query_source is None else _flat("query_source", query_source, self._source, self._int, device),
+                          0 if bias is None else _flat("bias", bias, self._table, dt, device),
+                          op, _flat("lse", lse, self._lse, self._float, device), orow, oh)
+        return device
 
     def forward(self, q, k, v, out, lse, hops=None, bias=None, query_source=None, stream=None):
         """out [T, n_heads, head_dim] and lse (fp32 [T, n_heads]) of q, k, v."""
         with self._lock:
-            self._inputs(q, k, v, out, lse, hops, bias, query_source)
-            device = q.get_device()
+            device = self._inputs(q, k, v, out, lse, hops, bias, query_source)
             st = self._current(device) if stream is None else _stream_ptr(stream)
             work = self._buffers[0]
             if work.last != st:
@@ -210,13 +238,12 @@ class HopAttention:
         """Gradients of q, k, v and the bias table from dout, the inputs and the forward's out and lse."""
         dt = self.dtype
         with self._lock:
-            self._inputs(q, k, v, out, lse, hops, bias, query_source)
-            dqp, dqr, dqh = _rows("dq", dq, self._rows, dt)
-            dkp, dkr, dkh = _rows("dk", dk, self._nodes, dt)
-            dvp, dvr, dvh = _rows("dv", dv, self._nodes, dt)
-            _GRADIENTS.pack_into(self._buf, _AT_GRADIENTS, *_rows("dout", dout, self._rows, dt), dqp, dkp, dvp, dqr, dqh,
-                                 dkr, dkh, dvr, dvh, 0 if dbias is None else _flat("dbias", dbias, self._table, dt))
-            device = q.get_device()
+            device = self._inputs(q, k, v, out, lse, hops, bias, query_source)
+            dqp, dqr, dqh = _rows("dq", dq, self._rows, dt, device)
+            dkp, dkr, dkh = _rows("dk", dk, self._nodes, dt, device)
+            dvp, dvr, dvh = _rows("dv", dv, self._nodes, dt, device)
+            _GRADIENTS.pack_into(self._buf, _AT_GRADIENTS, *_rows("dout", dout, self._rows, dt, device), dqp, dkp, dvp, dqr, dqh,
+                                 dkr, dkh, dvr, dvh, 0 if dbias is None else _flat("dbias", dbias, self._table, dt, device))
             st = self._current(device) if stream is None else _stream_ptr(stream)
             work = self._buffers[1]
             if work.last != st:
@@ -233,7 +260,7 @@ _GRADIENTS, _AT_GRADIENTS = struct.Struct("=Q2q3Q6qQ"), Attn.dout.offset
 assert _AT_INPUTS + _INPUTS.size == _AT_GRADIENTS and _AT_GRADIENTS + _GRADIENTS.size == ctypes.sizeof(Attn)
 
 
-class LayerNorm:
+class LayerNorm(_Placed):
     """Layer norm of ``n_rows`` states of ``dim`` values, with the residual sum before it (``k2t_norm``).
 
     A backward call takes the mean and rstd (fp32 [n_rows] each) that its
@@ -255,7 +282,7 @@ class LayerNorm:
         self._float = torch.float32
         self._lib = load()
         self._forward, self._backward = self._lib.k2t_norm_forward, self._lib.k2t_norm_backward
-        self._current = _stream_getter(torch)
+        self._current, self._here = _stream_getter(torch), _device_getter(torch)
         self._n = n_rows
         self._work, self._own = (_Buffer(torch, device, self._current) for _ in range(2))     # backward's; mean and rstd
         self._bytes = None
@@ -279,12 +306,12 @@ class LayerNorm:
     mean = property(lambda self: self._stat(0), doc="Means of the latest forward call that was not given a tensor for them.")
     rstd = property(lambda self: self._stat(1), doc="Likewise 1 / sqrt(var + eps).")
 
-    def _stats(self, mean, rstd, stream=None, device=None):
+    def _stats(self, mean, rstd, device, stream=None):
         if (mean is None) != (rstd is None):
             raise ValueError("mean and rstd are given together")
         if mean is None:      # a forward call writes the object's own, a backward call needs none
-            return (0, 0) if device is None else self._own_stats(stream, device)
-        return _flat("mean", mean, self._one, self._float), _flat("rstd", rstd, self._one, self._float)
+            return (0, 0) if stream is None else self._own_stats(stream, device)
+        return _flat("mean", mean, self._one, self._float, device), _flat("rstd", rstd, self._one, self._float, device)
 
     def forward(self, x, weight, bias, y, residual=None, z=None, stream=None, mean=None, rstd=None):
         """y = norm(z) and, with a residual, z = x + residual; writes the rows' mean and rstd."""
@@ -292,13 +319,14 @@ class LayerNorm:
             raise ValueError("residual and z are given exactly when the layer has a residual")
         dt, rows, cols = self.dtype, self._rows, self._cols
         with self._lock:
-            at, device = _flat("x", x, rows, dt), x.get_device()
+            device = self._device_of("x", x)
+            at = _flat("x", x, rows, dt, device)
             st = self._current(device) if stream is None else _stream_ptr(stream)
             _FORWARD.pack_into(self._buf, _AT_FORWARD, 0, at,
-                               0 if residual is None else _flat("residual", residual, rows, dt),
-                               _flat("weight", weight, cols, dt), 0 if bias is None else _flat("bias", bias, cols, dt),
-                               _flat("y", y, rows, dt), 0 if z is None else _flat("z", z, rows, dt),
-                               *self._stats(mean, rstd, st, device))
+                               0 if residual is None else _flat("residual", residual, rows, dt, device),
+                               _flat("weight", weight, cols, dt, device), 0 if bias is None else _flat("bias", bias, cols, dt, device),
+                               _flat("y", y, rows, dt, device), 0 if z is None else _flat("z", z, rows, dt, device),
+                               *self._stats(mean, rstd, device, st))
             rc = self._forward(self._ref, st)
         if rc:
             _check("k2t_norm_forward", rc)
@@ -310,13 +338,14 @@ class LayerNorm:
         of this z wrote; without them they are formed again from z."""
         dt, rows, cols = self.dtype, self._rows, self._cols
         with self._lock:
-            _BACKWARD.pack_into(self._buf, _AT_FORWARD, NORM_FORM_STATS if mean is None else 0, 0, 0, _flat("weight", weight, cols, dt),
-                                0, 0, _flat("z", z, rows, dt), *self._stats(mean, rstd), _flat("dy", dy, rows, dt),
-                                0 if dz is None else _flat("dz", dz, rows, dt), _flat("dx", dx, rows, dt),
-                                _flat("dweight", dweight, cols, dt), 0 if dbias is None else _flat("dbias", dbias, cols, dt))
+            device = self._device_of("dy", dy)
+            _BACKWARD.pack_into(self._buf, _AT_FORWARD, NORM_FORM_STATS if mean is None else 0, 0, 0,
+                                _flat("weight", weight, cols, dt, device), 0, 0, _flat("z", z, rows, dt, device),
+                                *self._stats(mean, rstd, device), _flat("dy", dy, rows, dt, device),
+                                0 if dz is None else _flat("dz", dz, rows, dt, device), _flat("dx", dx, rows, dt, device),
+                                _flat("dweight", dweight, cols, dt, device), 0 if dbias is None else _flat("dbias", dbias, cols, dt, device))
             if self._bytes is None:
                 self._bytes = self.work_bytes()
-            device = dy.get_device()
             st = self._current(device) if stream is None else _stream_ptr(stream)
             rc = self._backward(self._ref, self._work.get(max(16, self._bytes), st, device), self._bytes, st)
         if rc:

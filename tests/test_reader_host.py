@@ -56,7 +56,7 @@ def attention(monkeypatch, call):
     op._forward = op._backward = fake
     for b in op._buffers:
         b.at, b.last = P, 0
-    op._current = lambda device: 0
+    op._current, op._here = (lambda device: 0), (lambda: 0)
 
     def tensors(at, device=0):
         shapes = dict(q=(2, 2, 64), k=(3, 1, 64), v=(3, 1, 64), out=(2, 2, 64), lse=(2, 2), hops=(3, 2), bias=(2, 2), dout=(2, 2, 64),
@@ -111,7 +111,7 @@ def test_threads_share_an_attention_object(monkeypatch, call):
 
 
 def test_threads_share_a_norm_object():
-    op = pkg.LayerNorm(4, 8, torch.float32, device="cpu")
+    op = pkg.LayerNorm(4, 8, torch.float32, device="cpu")        # where its buffers are
     seen = []
 
     def c_call(*_):
@@ -121,9 +121,51 @@ def test_threads_share_a_norm_object():
         return 0
     op._forward = op._backward = c_call
     op._current = op._own._current = op._work._current = lambda device: 0
+    op._here = lambda: 0
 
     def job(i):
         x, w = Card(4, 8, dtype=torch.float32, at=P * i), Card(8, dtype=torch.float32, at=P * i + 64)
         return (lambda: op.forward(x, w, None, x)) if i % 2 else (lambda: op.backward(x, x, w, x, w))
     in_threads([job(i) for i in range(1, 7)])
     assert all(same for same, _, _ in seen) and sorted((x, w) for _, x, w in seen) == [(P * i, P * i + 64) for i in range(1, 7)]
+
+
+@pytest.mark.parametrize("call,names", [(forward, "q k v out lse hops bias"), (backward, "q k v out lse hops bias dout dq dk dv dbias")])
+def test_attention_refuses_tensors_of_several_devices(monkeypatch, call, names):
+    calls = []
+    op, tensors = attention(monkeypatch, lambda a: calls.append(1) or 0)
+    call(op, tensors(P))
+    for name in names.split():
+        t = tensors(P)
+        t[name].device_index = 1
+        with pytest.raises(ValueError, match="device"):
+            call(op, t)
+    with pytest.raises(ValueError, match="the object is on device 0"):
+        call(op, tensors(P, device=1))
+    op._here = lambda: 1
+    with pytest.raises(ValueError, match="current"):
+        call(op, tensors(P))
+    assert len(calls) == 1
+    op, tensors = attention(monkeypatch, lambda a: calls.append(1) or 0)
+    op.device = "cuda:1"
+    with pytest.raises(ValueError, match="the object is on device 1"):
+        call(op, tensors(P))
+
+
+def test_norm_refuses_tensors_of_several_devices():
+    op = pkg.LayerNorm(4, 8, torch.float32, residual=True)
+    op._forward = op._backward = lambda *a: 0
+    op._here = op._current = lambda *a: 0
+    for b in (op._own, op._work):
+        b.at, b.last, b._streams = P, 0, {0}
+        b.tensor = Card(1)
+    shapes = dict(x=(4, 8), residual=(4, 8), weight=(8,), bias=(8,), y=(4, 8), z=(4, 8), mean=(4,), rstd=(4,))
+    back = dict(dy=(4, 8), z=(4, 8), weight=(8,), dx=(4, 8), dweight=(8,), dbias=(8,), dz=(4, 8), mean=(4,), rstd=(4,))
+    for call, wants in ((op.forward, shapes), (op.backward, back)):
+        for odd in (None, *wants):
+            t = {x: Card(*s, dtype=torch.float32, device=int(x == odd)) for x, s in wants.items()}
+            if odd is None:
+                call(**t)
+                continue
+            with pytest.raises(ValueError, match="device"):
+                call(**t)
