@@ -36,6 +36,20 @@ bool aligned(const void *p, int64_t row, int64_t head)
     return !((uintptr_t)p & 15u) && !(row & 7) && !(head & 7) && row >= 0 && head >= 0 && row < (1ll << 38) && head < (1ll << 38);
 }
 
+// Whether two rows of an output [rows, heads, d] share values: rows i apart and heads j apart the other way, |i row - j head| < d.
+bool overlaps(int64_t row, int64_t head, uint64_t rows, uint64_t heads, uint32_t d)
+{
+    using Wide = unsigned __int128;
+    if ((rows > 1 && row < d) || (heads > 1 && head < d)) return true;
+    if (rows < 2 || heads < 2) return false;
+    if (row >= (Wide)(heads - 1) * head + d || head >= (Wide)(rows - 1) * row + d) return false;     // one inside the other
+    for (uint64_t j = 1; j < heads; ++j) {
+        const Wide at = (Wide)j * head, i = at / row, left = at - i * row;
+        if ((i < rows && left < d) || (i + 1 < rows && row - left < d)) return true;
+    }
+    return false;
+}
+
 constexpr uint64_t kSms = 152;
 
 // Blocks that share the nodes of one (head, row tile): as many as make the
@@ -148,7 +162,7 @@ uint64_t plan_bytes(const Plan &pl)
            align_up(pl.delta_floats * 4, 256);
 }
 
-int check_call(const k2t_attn *a, const void *work, uint64_t work_bytes, const Plan &pl)
+int check_call(const k2t_attn *a, const void *work, bool backward)
 {
     const bool q = a->n_queries != 0, n = a->n_nodes != 0;
     if ((q && (!a->q || !a->out || !a->lse)) || (n && (!a->k || !a->v))) return K2T_EINVAL;
@@ -158,9 +172,17 @@ int check_call(const k2t_attn *a, const void *work, uint64_t work_bytes, const P
     if (a->n_sources && n && !a->hops) return K2T_EINVAL;
     if ((a->n_buckets != 0) != (a->bias != nullptr)) return K2T_EINVAL;
     if (a->n_sources && !a->query_source && a->n_queries > a->n_sources) return K2T_ERANGE;
-    const uint64_t need = plan_bytes(pl);
     if (!work || ((uintptr_t)work & 15u)) return K2T_EINVAL;
-    if (work_bytes < need) return K2T_ENOMEM;
+    const auto shared = [&](int64_t row, int64_t head, bool nodes) {
+        return overlaps(row, head, nodes ? a->n_nodes : a->n_queries, nodes ? a->n_kv_heads : a->n_heads, a->head_dim);
+    };
+    if (!backward) return a->n_queries && shared(a->out_row, a->out_head, false) ? K2T_EINVAL : K2T_OK;
+    if ((q && (!a->dout || !a->dq)) || (n && (!a->dk || !a->dv)) || (a->n_buckets && !a->dbias)) return K2T_EINVAL;
+    if (!aligned(a->dout, a->dout_row, a->dout_head) || !aligned(a->dq, a->dq_row, a->dq_head) ||
+        !aligned(a->dk, a->dk_row, a->dk_head) || !aligned(a->dv, a->dv_row, a->dv_head))
+        return K2T_EINVAL;
+    if ((q && shared(a->dq_row, a->dq_head, false)) || (n && (shared(a->dk_row, a->dk_head, true) || shared(a->dv_row, a->dv_head, true))))
+        return K2T_EINVAL;
     return K2T_OK;
 }
 
@@ -212,7 +234,8 @@ int k2t_attn_forward(const k2t_attn *a, void *work, uint64_t work_bytes, void *s
     if (rc) return rc;
     Plan pl;
     make_plan(a, false, pl);
-    if ((rc = check_call(a, work, work_bytes, pl))) return rc;
+    if ((rc = check_call(a, work, false))) return rc;
+    if (work_bytes < plan_bytes(pl)) return K2T_ENOMEM;
     if (a->n_queries == 0) return K2T_OK;
     fill_pointers(a, work, pl);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -225,13 +248,8 @@ int k2t_attn_backward(const k2t_attn *a, void *work, uint64_t work_bytes, void *
     if (rc) return rc;
     Plan pl;
     make_plan(a, true, pl);
-    if ((rc = check_call(a, work, work_bytes, pl))) return rc;
-    if (a->n_queries && (!a->dout || !a->dq)) return K2T_EINVAL;
-    if (a->n_nodes && (!a->dk || !a->dv)) return K2T_EINVAL;
-    if (a->n_buckets && !a->dbias) return K2T_EINVAL;
-    if (!aligned(a->dout, a->dout_row, a->dout_head) || !aligned(a->dq, a->dq_row, a->dq_head) ||
-        !aligned(a->dk, a->dk_row, a->dk_head) || !aligned(a->dv, a->dv_row, a->dv_head))
-        return K2T_EINVAL;
+    if ((rc = check_call(a, work, true))) return rc;
+    if (work_bytes < plan_bytes(pl)) return K2T_ENOMEM;
     fill_pointers(a, work, pl);
     if (a->n_nodes && (!node_map(&pl.p.dk_map, a->dk, a->dk_row, a->dk_head, pl.p, a->dtype) ||
                        !node_map(&pl.p.dv_map, a->dv, a->dv_row, a->dv_head, pl.p, a->dtype)))

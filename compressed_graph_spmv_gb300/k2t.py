@@ -39,7 +39,7 @@ EXPORTED = ["k2t_default_opts", "k2t_build", "k2t_workspace_bytes", "k2t_upload"
             "k2t_norm_work_bytes", "k2t_norm_forward", "k2t_norm_backward"]
 
 BF16, FP16, FP32 = 0, 1, 2
-ATTN_MAX_BUCKETS, ATTN_MAX_HOP = 64, 255
+ATTN_MAX_BUCKETS, ATTN_MAX_HOP, ATTN_MAX_NODES = 64, 255, 0x7fffff00
 NORM_FORM_STATS = 1
 
 

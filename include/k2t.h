@@ -387,7 +387,8 @@ K2T_API uint64_t k2t_msbfs_work_bytes(const k2t_tree *t);
  * column in use) are not used: they may hold anything, NaN included.
  * Strides are in elements; rows must be 16-byte aligned: base pointers
  * multiples of 16 bytes, strides and head_dim multiples of 8; strides are not
- * negative and below 2^38.                                                  */
+ * negative and below 2^38.  Inputs may be broadcast (stride 0); rows of out,
+ * dq, dk and dv share no values, in any order of rows and heads.            */
 typedef struct {
     uint32_t dtype;            /* K2T_BF16 or K2T_FP16: q, k, v, out, bias and all gradients        */
     uint32_t n_queries;        /* T, 0 or more                                                       */
@@ -424,7 +425,8 @@ typedef struct {
 K2T_API uint64_t k2t_attn_work_bytes(const k2t_attn *a, int32_t backward);
 
 /* out and lse.  Errors: EINVAL (null, misaligned, bad dtype or sizes, edges
- * not increasing from 0, buckets without a table or the reverse), ERANGE
+ * not increasing from 0, buckets without a table or the reverse, an output
+ * whose rows overlap), ERANGE
  * (a limit above exceeded, more queries than sources without query_source),
  * ENOMEM (work_bytes too small), ECUDA. */
 K2T_API int k2t_attn_forward(const k2t_attn *a, void *work, uint64_t work_bytes, void *stream);

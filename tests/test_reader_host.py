@@ -5,7 +5,7 @@ import time
 
 import pytest
 
-from test_reader_refusals import ENOMEM, EINVAL, P, norm
+from test_reader_refusals import ENOMEM, EINVAL, P, attn, norm
 
 K = pytest.importorskip("compressed_graph_spmv_gb300.k2t")
 torch = pytest.importorskip("torch")
@@ -169,3 +169,31 @@ def test_norm_refuses_tensors_of_several_devices():
                 continue
             with pytest.raises(ValueError, match="device"):
                 call(**t)
+
+
+def test_rows_of_outputs_that_overlap():
+    """Checked for every pair of pitches against the definition; a layout that is taken fails for its work buffer, next."""
+    lib = K.load()
+    calls = dict(out=lib.k2t_attn_forward, dq=lib.k2t_attn_backward, dk=lib.k2t_attn_backward, dv=lib.k2t_attn_backward)
+    refused = taken = 0
+    for name, call in calls.items():
+        nodes = name in ("dk", "dv")
+        for rows, heads in ((4, 4), (1, 4), (3, 2), (4, 2)) if not nodes else ((5, 2), (1, 2), (3, 2)):
+            for row in (0, 8, 16, 24, 40, 48, 56, 64, 80):
+                for head in (0, 8, 16, 24, 40, 56, 64, 72, 96):
+                    kw = {name + "_row": row, name + "_head": head}
+                    a = attn(head_dim=16, n_sources=0, n_buckets=0, bias=None, edges=(), n_heads=2 if nodes else heads,
+                             n_kv_heads=heads if nodes else 1, n_queries=4 if nodes else rows, n_nodes=rows if nodes else 5, **kw)
+                    starts = sorted(i * row + j * head for i in range(rows) for j in range(heads))
+                    free = all(b - c >= 16 for c, b in zip(starts, starts[1:]))
+                    assert call(ctypes.byref(a), P, 0, None) == (ENOMEM if free else EINVAL), (name, rows, heads, row, head)
+                    taken, refused = taken + free, refused + (not free)
+    assert taken > 300 and refused > 300
+    # very long pitches and very many nodes
+    far = dict(n_nodes=K.ATTN_MAX_NODES, n_sources=0, n_buckets=0, bias=None, edges=())
+    for kw, status in ((dict(dk_row=(1 << 38) - 8, dk_head=64), ENOMEM), (dict(dk_row=64, dk_head=(1 << 38) - 8), ENOMEM),
+                       (dict(dk_row=64, dk_head=1 << 20), EINVAL), (dict(dv_row=0), EINVAL)):
+        assert lib.k2t_attn_backward(ctypes.byref(attn(**far, **kw)), P, 0, None) == status, kw
+    # inputs may be broadcast
+    for kw in (dict(k_row=0, v_head=0), dict(q_row=0, q_head=0), dict(dout_row=0)):
+        assert lib.k2t_attn_backward(ctypes.byref(attn(**kw)), P, 0, None) == ENOMEM
