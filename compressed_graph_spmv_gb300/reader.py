@@ -206,7 +206,9 @@ class HopAttention(_Placed):
         return word
 
     def _inputs(self, q, k, v, out, lse, hops, bias, query_source):
-        a, dt, device = self._a, self.dtype, self._device_of("q", q)
+        a, dt, device = self._a, self.dtype, q.get_device()
+        if device != self._on or device != self._here():
+            device = self._device_of("q", q)
         if (hops is None) != (a.n_sources == 0):
             raise ValueError("hops: given %s, sources %d" % (hops is not None, a.n_sources))
         qp, qr, qh = _rows("q", q, self._rows, dt, device)
@@ -293,9 +295,9 @@ class LayerNorm(_Placed):
         return int(self._lib.k2t_norm_work_bytes(self._ref))
 
     def _own_stats(self, stream, device):
-        own = self._own
-        at = own.at if own.last == stream else own.get(max(8 * self._n, 16), stream, device)
-        return at, at + 4 * self._n
+        at = self._own.get(max(8 * self._n, 16), stream, device)
+        self._own_at = at, at + 4 * self._n
+        return self._own_at
 
     def _stat(self, which):
         with self._lock:
@@ -306,11 +308,9 @@ class LayerNorm(_Placed):
     mean = property(lambda self: self._stat(0), doc="Means of the latest forward call that was not given a tensor for them.")
     rstd = property(lambda self: self._stat(1), doc="Likewise 1 / sqrt(var + eps).")
 
-    def _stats(self, mean, rstd, device, stream=None):
-        if (mean is None) != (rstd is None):
+    def _stats(self, mean, rstd, device):
+        if mean is None or rstd is None:
             raise ValueError("mean and rstd are given together")
-        if mean is None:      # a forward call writes the object's own, a backward call needs none
-            return (0, 0) if stream is None else self._own_stats(stream, device)
         return _flat("mean", mean, self._one, self._float, device), _flat("rstd", rstd, self._one, self._float, device)
 
     def forward(self, x, weight, bias, y, residual=None, z=None, stream=None, mean=None, rstd=None):
@@ -319,14 +319,19 @@ class LayerNorm(_Placed):
             raise ValueError("residual and z are given exactly when the layer has a residual")
         dt, rows, cols = self.dtype, self._rows, self._cols
         with self._lock:
-            device = self._device_of("x", x)
+            device = x.get_device()
+            if device != self._on or device != self._here():
+                device = self._device_of("x", x)
             at = _flat("x", x, rows, dt, device)
             st = self._current(device) if stream is None else _stream_ptr(stream)
+            if mean is not None or rstd is not None:
+                stats = self._stats(mean, rstd, device)
+            else:
+                stats = self._own_at if self._own.last == st else self._own_stats(st, device)
             _FORWARD.pack_into(self._buf, _AT_FORWARD, 0, at,
                                0 if residual is None else _flat("residual", residual, rows, dt, device),
                                _flat("weight", weight, cols, dt, device), 0 if bias is None else _flat("bias", bias, cols, dt, device),
-                               _flat("y", y, rows, dt, device), 0 if z is None else _flat("z", z, rows, dt, device),
-                               *self._stats(mean, rstd, device, st))
+                               _flat("y", y, rows, dt, device), 0 if z is None else _flat("z", z, rows, dt, device), *stats)
             rc = self._forward(self._ref, st)
         if rc:
             _check("k2t_norm_forward", rc)
@@ -338,21 +343,28 @@ class LayerNorm(_Placed):
         of this z wrote; without them they are formed again from z."""
         dt, rows, cols = self.dtype, self._rows, self._cols
         with self._lock:
-            device = self._device_of("dy", dy)
-            _BACKWARD.pack_into(self._buf, _AT_FORWARD, NORM_FORM_STATS if mean is None else 0, 0, 0,
+            device = dy.get_device()
+            if device != self._on or device != self._here():
+                device = self._device_of("dy", dy)
+            form = mean is None and rstd is None
+            _BACKWARD.pack_into(self._buf, _AT_FORWARD, NORM_FORM_STATS if form else 0, 0, 0,
                                 _flat("weight", weight, cols, dt, device), 0, 0, _flat("z", z, rows, dt, device),
-                                *self._stats(mean, rstd, device), _flat("dy", dy, rows, dt, device),
+                                *(_NONE if form else self._stats(mean, rstd, device)), _flat("dy", dy, rows, dt, device),
                                 0 if dz is None else _flat("dz", dz, rows, dt, device), _flat("dx", dx, rows, dt, device),
                                 _flat("dweight", dweight, cols, dt, device), 0 if dbias is None else _flat("dbias", dbias, cols, dt, device))
             if self._bytes is None:
                 self._bytes = self.work_bytes()
             st = self._current(device) if stream is None else _stream_ptr(stream)
-            rc = self._backward(self._ref, self._work.get(max(16, self._bytes), st, device), self._bytes, st)
+            work = self._work
+            if work.last != st:
+                work.get(max(16, self._bytes), st, device)
+            rc = self._backward(self._ref, work.at, self._bytes, st)
         if rc:
             _check("k2t_norm_backward", rc)
         return dx, dweight, dbias
 
 
+_NONE = (0, 0)
 # flags and pointers of k2t_norm: up to rstd, and all
 _FORWARD, _BACKWARD, _AT_FORWARD = struct.Struct("=I8Q"), struct.Struct("=I13Q"), Norm.flags.offset
 assert _AT_FORWARD + _FORWARD.size == Norm.dy.offset and _AT_FORWARD + _BACKWARD.size == ctypes.sizeof(Norm)

@@ -158,7 +158,7 @@ def test_norm_refuses_tensors_of_several_devices():
     op._here = op._current = lambda *a: 0
     for b in (op._own, op._work):
         b.at, b.last, b._streams = P, 0, {0}
-        b.tensor = Card(1)
+        b.tensor, op._own_at = Card(1), (P, P)
     shapes = dict(x=(4, 8), residual=(4, 8), weight=(8,), bias=(8,), y=(4, 8), z=(4, 8), mean=(4,), rstd=(4,))
     back = dict(dy=(4, 8), z=(4, 8), weight=(8,), dx=(4, 8), dweight=(8,), dbias=(8,), dz=(4, 8), mean=(4,), rstd=(4,))
     for call, wants in ((op.forward, shapes), (op.backward, back)):
