@@ -101,7 +101,7 @@ void make_plan(const k2t_attn *a, bool backward, Plan &pl)
         if ((p.buckets || a->dtype == K2T_FP16) && p.T && p.n) {
             p.delta_tiles = (p.rows + delta_rows(p) - 1) / delta_rows(p);
             p.delta_splits = pick_splits((uint64_t)p.hkv * p.delta_tiles, p.tiles);
-            pl.delta_floats = p.delta_splits * rows * 3 + (uint64_t)p.hkv * p.delta_splits * p.delta_tiles;
+            pl.delta_floats = p.delta_splits * rows * 3;
         }
         const uint32_t per = kBwdRows / p.group;              // whole queries of a row tile
         p.row_tiles = std::max(1u, (p.T + per - 1) / per);
@@ -205,7 +205,7 @@ void fill_pointers(const k2t_attn *a, void *work, Plan &pl)
     w += align_up(pl.part_floats * 4, 256) + align_up(pl.ml_floats * 4, 256);
     p.row_info = w;
     p.delta_part = reinterpret_cast<float2 *>(w + align_up(pl.info_floats * 4, 256));
-    p.dp_top = reinterpret_cast<float *>(p.delta_part + (uint64_t)p.delta_splits * p.T * p.hq);
+    p.pdp_top = reinterpret_cast<float *>(p.delta_part + (uint64_t)p.delta_splits * p.T * p.hq);
     uint32_t b = 0;
     for (uint32_t x = 0; x < 256; ++x) {
         while (b + 1 < a->n_buckets && a->edges[b + 1] <= x) ++b;

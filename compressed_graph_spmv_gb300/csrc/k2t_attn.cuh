@@ -55,7 +55,7 @@ struct AttnParams {
     float *part_ml;
     void *row_info;           // RowInfo[hkv][row_tiles * 32] (backward)
     float2 *delta_part;       // [delta_splits][T][hq]: sums of p dp and of p
-    float *dp_top;            // fp16: [delta_splits][T][hq] largest |dp| of a row, then [hkv][delta_splits * delta_tiles] of a block
+    float *pdp_top;           // fp16: [delta_splits][T][hq]: largest p |dp|
     uint32_t delta_splits, delta_tiles;   // of attn_delta_kernel; 0: delta is dout . out
     uint32_t hist_parts;      // partial dbias tables
     uint32_t hist_threads;    // threads that sum by bucket, 128 or 64
@@ -93,18 +93,19 @@ template <> struct Elem<__half> {
     static constexpr float kMasked = -65504.0f;
     // Weights of a row over n nodes are about 1/n, below fp16's least normal number from 2^14 nodes on and 0 from 2^25 on.
     // Backward, weights (at most 1) are multiplied by 2^15 before they are rounded, which leaves 29 bits of normal numbers
-    // below 1, and score gradients by 2^15 and a power of two that brings the largest dp - delta to 1 at most (ds_scale):
-    // of the row for dq and the sums by bucket, of the head for dk, which sums over rows.  The powers are taken out of the
-    // fp32 results again.
+    // below 1, and score gradients by 2^15 and a power of two that brings the largest to 1 at most (ds_scale): of the row for
+    // dq and the sums by bucket, of the head for dk, which sums over rows.  The powers are taken out of the fp32 results
+    // again.
     static constexpr int kUp = 15;
 };
 
-// Factor of dp - delta for a largest |dp| of `top`: |dp - delta| <= 2 top.  Where top is no number the factor undoes kUp.
+// Factor of score gradients of which none exceeds `top`: |ds| <= max p |dp| + |delta|.  Where top is no number the factor
+// undoes kUp; where it is 0 it is the largest factor, since the least one of the rows is the head's.
 template <typename T> __device__ __forceinline__ float ds_scale(float top)
 {
-    if (Elem<T>::kUp == 0 || top == 0.0f) return 1.0f;
+    if (Elem<T>::kUp == 0) return 1.0f;
     if (!(top <= 3.4e38f)) return __uint_as_float((127u - Elem<T>::kUp) << 23);
-    const int e = min(max((int)(__float_as_uint(top) >> 23) - 127 + 2, -100), 100);
+    const int e = min(max((int)(__float_as_uint(top) >> 23) - 127 + 1, -100), 100);
     return __uint_as_float((uint32_t)(127 - e) << 23);
 }
 // 1 / a power of two.

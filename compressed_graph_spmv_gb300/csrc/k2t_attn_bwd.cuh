@@ -46,7 +46,7 @@ constexpr int kBwdRows = 32;
 
 // What the kernels need of a row, made once by attn_rows_kernel: lse in units
 // of log2 (+inf for a row that saw nothing or does not exist: its weights
-// become 0), less Elem::kUp, delta, ds_scale of its largest |dp|, byte offset of its column in a bucket tile, its head's
+// become 0), less Elem::kUp, delta, ds_scale, byte offset of its column in a bucket tile, its head's
 // offset in the bias table; a row tile's together.
 struct RowInfo {
     float lse[kBwdRows], delta[kBwdRows], up[kBwdRows];
@@ -65,7 +65,7 @@ __device__ __forceinline__ float row_delta(const AttnParams &p, uint32_t t, uint
                 const uint64_t at = ((uint64_t)i * p.T + t) * p.hq + hd;
                 const float2 v = p.delta_part[at];
                 s += v.x, m += v.y;
-                if (Elem<T>::kUp) top = fmaxf(top, p.dp_top[at]);
+                if (Elem<T>::kUp) top = fmaxf(top, p.pdp_top[at]);
             }
         } else {
             const T *o = static_cast<const T *>(p.out) + (int64_t)t * p.out_row + (int64_t)hd * p.out_head;
@@ -84,8 +84,9 @@ __device__ __forceinline__ float row_delta(const AttnParams &p, uint32_t t, uint
     for (int y = L / 2; y; y >>= 1) s += __shfl_xor_sync(lanes, s, y), m += __shfl_xor_sync(lanes, m, y);
     if (Elem<T>::kUp)
         for (int y = L / 2; y; y >>= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, y));
-    up = ds_scale<T>(top);
-    return m == 0.0f ? 0.0f : s / m;
+    const float delta = m == 0.0f ? 0.0f : s / m;
+    up = ds_scale<T>(top + fabsf(delta));
+    return delta;
 }
 
 template <typename T>
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
     tc::grid_wait();
     const int lane = threadIdx.x & 31;
     const uint32_t G = p.group, per = kBwdRows / G, c = at % kBwdRows, t = at / kBwdRows * per + c / G, g = c % G;
-    float lse = INFINITY, s = 0.0f, up = 1.0f;
+    float lse = INFINITY, s = 0.0f, up = ds_scale<T>(0.0f);
     uint32_t place = 0;
     if (c < per * G && t < p.T) {
         const uint32_t hd = hk * G + g;
@@ -109,13 +110,12 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
     if (lane == 0) to->lse[c] = lse, to->delta[c] = s, to->up[c] = up, to->place[c] = place;
 }
 
-// The head's largest |dp| into *top (bits; 0 before), by a block's threads.
-__device__ __forceinline__ void head_top(const AttnParams &p, uint32_t hk, uint32_t *top)
+// The least ds_scale of some row tiles' rows, by a warp.
+__device__ __forceinline__ float least_up(const RowInfo *info, uint32_t row_tiles, int lane)
 {
-    const uint64_t parts = (uint64_t)p.delta_splits * p.delta_tiles, rows = (uint64_t)p.delta_splits * p.T * p.hq;
-    uint32_t most = 0;
-    for (uint64_t i = threadIdx.x; i < parts; i += blockDim.x) most = max(most, __float_as_uint(p.dp_top[rows + hk * parts + i]));
-    if (most) atomicMax(top, most);
+    float up = info[0].up[lane];
+    for (uint32_t i = 1; i < row_tiles; ++i) up = fminf(up, info[i].up[lane]);
+    return __uint_as_float(__reduce_min_sync(~0u, __float_as_uint(up)));        // of numbers that are not negative: as their bits
 }
 
 // Copies ROWS (a multiple of 32) rows of tile `tile` on of a [T, heads, d] tensor into row tiles of 32 rows:
@@ -134,7 +134,7 @@ __device__ __forceinline__ void copy_row_tile(uint32_t dst, const void *base, in
     }
 }
 
-// up: ds_scale of the head.
+// up: the least ds_scale of the head's rows.
 // A unit's softmax step for one node: S^T and dP^T at `at` (32 columns each, a row of the tile a column) become P^T
 // and dS^T in the element type, two rows a column; ds: this node's row of dS^T in shared memory, from chunk `chunk` on
 // (null: not wanted), and `rest` bytes on what the rounding took off, itself rounded (rest 0: not wanted); bt: the node's bytes in the bucket tile (column 0); lut: bias table, bytes.
@@ -249,7 +249,7 @@ template <int DP, int RT, bool DKV> struct BwdSmem {
     struct Ctl {
         uint64_t full[kSlots], empty[kSlots], hop_full[kBufs], hop_empty[kBufs], sp_full[2], ds_full[2], hist_done[2];
         uint64_t tile_full, tile_empty, staged, dq_full, drained;
-        uint32_t tmem, gave_up, columns, all, top;
+        uint32_t tmem, gave_up, columns, all;
         uint32_t seen[kBufs][4];
         uint8_t byte_of[257 + 15];
     };
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
         tc::bar_init(&ctl->staged, 128);
         tc::bar_init(&ctl->dq_full, 1);
         tc::bar_init(&ctl->drained, 1);
-        ctl->gave_up = ctl->columns = ctl->all = ctl->top = 0;
+        ctl->gave_up = ctl->columns = ctl->all = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tc::grid_wait();
@@ -311,7 +311,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
         for (uint32_t i = tid; i < (p.buckets + 2) * p.hist_threads; i += kBwdThreads) hist[i] = 0.0f;
     RowInfo *info = reinterpret_cast<RowInfo *>(smem + S::kInfo);
     __syncthreads();
-    if (Elem<T>::kUp) head_top(p, hk, &ctl->top);
     auto seen_by = [&](uint32_t place) {
         const uint32_t col = (place & 0xffff) / kTcPitch;
         if (col < p.sources) atomicOr(&ctl->columns, 1u << col);
@@ -353,7 +352,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
     tc::grid_next();
     const uint32_t tm = ctl->tmem;
     volatile uint32_t *gave_up = &ctl->gave_up;
-    const float up = ds_scale<T>(__uint_as_float(ctl->top));       // and what takes the powers of two out of the results:
+    const float up = Elem<T>::kUp ? least_up(info, rts, lane) : 1.0f;      // and what takes the powers of two out of the results:
     const float p_down = 1.0f / (1u << Elem<T>::kUp), ds_down = p_down / up;
     auto row_down = [&](uint32_t r, uint32_t c) { return Elem<T>::kUp ? p_down * inverse_power(info[r].up[c]) : 1.0f; };
 
@@ -573,7 +572,7 @@ template <int DP> struct BwdRowSmem {
     static constexpr int kCtl = kInfo + kRing * (int)sizeof(RowInfo);
     struct Ctl {
         uint64_t full[2], empty[2], hop_full[1], hop_empty[1], row_full[kRing], row_empty[kRing], sp_full[2], ds_full[2], tile_full, drained;
-        uint32_t tmem, gave_up, columns, all, top;
+        uint32_t tmem, gave_up, columns, all, up;
         uint32_t seen[1][4];
         uint8_t byte_of[257 + 15];
     };
@@ -605,7 +604,8 @@ __global__ void __launch_bounds__(kBwdRowThreads, 1) attn_bwd_rows_kernel(const 
         for (int i = 0; i < S::kRing; ++i) tc::bar_init(&ctl->row_full[i], 128), tc::bar_init(&ctl->row_empty[i], 1);
         tc::bar_init(&ctl->tile_full, 1);
         tc::bar_init(&ctl->drained, 1);
-        ctl->gave_up = ctl->columns = ctl->all = ctl->top = 0;
+        ctl->gave_up = ctl->columns = ctl->all = 0;
+        ctl->up = __float_as_uint(INFINITY);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (p.sources)
@@ -613,7 +613,14 @@ __global__ void __launch_bounds__(kBwdRowThreads, 1) attn_bwd_rows_kernel(const 
     tc::grid_wait();
     fill_bias<T>(lut, p, hk, tid, p.group2);
     __syncthreads();
-    if (Elem<T>::kUp) head_top(p, hk, &ctl->top);
+    if (Elem<T>::kUp) {
+        const RowInfo *rows = static_cast<const RowInfo *>(p.row_info) + (uint64_t)hk * p.row_tiles;
+        const uint32_t each = (p.row_tiles + kBwdRowThreads / 32 - 1) / (kBwdRowThreads / 32), from = warp * each;
+        if (from < p.row_tiles) {
+            const float up = least_up(rows + from, min(each, p.row_tiles - from), lane);
+            if (lane == 0) atomicMin(&ctl->up, __float_as_uint(up));
+        }
+    }
     if (p.sources) {
         uint32_t cols = 0;
         bool all = false;
@@ -631,7 +638,7 @@ __global__ void __launch_bounds__(kBwdRowThreads, 1) attn_bwd_rows_kernel(const 
     tc::grid_next();
     const uint32_t tm = ctl->tmem;
     volatile uint32_t *gave_up = &ctl->gave_up;
-    const float up = ds_scale<T>(__uint_as_float(ctl->top));       // and what takes the powers of two out of the results:
+    const float up = Elem<T>::kUp ? __uint_as_float(ctl->up) : 1.0f;       // and what takes the powers of two out of the results:
     const float p_down = 1.0f / (1u << Elem<T>::kUp), ds_down = p_down / up;
 
     if (warp < 8) {

@@ -7,8 +7,8 @@
 // the weight, bf16: its bucket's gradient was 20 to 48% off).  Gradients of
 // the bias table sum ds over many nodes, so that the error adds up in each
 // bucket in proportion to its weight.  Calls with a table therefore form delta
-// from the nodes, in 32 bits; so do those in fp16, which need the largest |dp|
-// as well (ds_scale); others take dout . out, which needs no pass.
+// from the nodes, in 32 bits; so do those in fp16, which need the largest
+// p |dp| as well (ds_scale); others take dout . out, which needs no pass.
 //
 // The forward pass's layout (see there), with a row's lse known: no running
 // maximum, no weights written back, and dP = dO V^T beside S = Q K^T in place
@@ -34,10 +34,10 @@ template <int DP> struct DeltaSmem {
     static constexpr int kCtl = kBuckets + kBufs * 33 * kTcPitch;
     struct Ctl {
         uint64_t full[kSlots], empty[kSlots], hop_full[kBufs], hop_empty[kBufs], s_full[2], s_read[2], drained;
-        uint32_t tmem, gave_up, columns, all, top;
+        uint32_t tmem, gave_up, columns, all;
         uint32_t seen[kBufs][4];
         float2 sum[2][2][128];            // [group][half][lane]: sum of p dp, sum of p
-        float tops[2][2][128];            // largest |dp|
+        float tops[2][2][128];            // largest p |dp|
         uint8_t byte_of[257 + 15];
     };
     static constexpr int kLut = kCtl + (int)((sizeof(Ctl) + 15) / 16 * 16);
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_delta_kernel(const __grid_
         for (int i = 0; i < S::kBufs; ++i) tc::bar_init(&ctl->hop_full[i], 4), tc::bar_init(&ctl->hop_empty[i], 8);
         for (int i = 0; i < 2; ++i) tc::bar_init(&ctl->s_full[i], 1), tc::bar_init(&ctl->s_read[i], 256);
         tc::bar_init(&ctl->drained, 1);
-        ctl->gave_up = ctl->columns = ctl->all = ctl->top = 0;
+        ctl->gave_up = ctl->columns = ctl->all = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (p.sources)
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_delta_kernel(const __grid_
         const float lse = row < p.rows ? p.lse[(uint64_t)t * p.hq + hk * p.group + g] : -INFINITY;
         const float nl = lse == -INFINITY ? -INFINITY : -lse * kLog2e;              // weights of a row that saw nothing are 0
         LongSum all_dots, all_mass;
-        float top = 0.0f;                                             // largest |dp|
+        float top = 0.0f;                                             // largest p |dp|
         uint32_t mine = 0;                                            // units of this group done
         for (uint32_t u = w; u < units; u += 2, ++mine) {
             const uint32_t buf = u % S::kBufs;
@@ -169,8 +169,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_delta_kernel(const __grid_
                     const float2 x = add2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), make_float2(nl, nl));
                     const float2 y = make_float2(ex2(x.x), ex2(x.y));
                     mass = add2(mass, y);
-                    dots = fma2(y, make_float2(__uint_as_float(d[e]), __uint_as_float(d[e + 1])), dots);
-                    if (Elem<T>::kUp) top = max3(top, fabsf(__uint_as_float(d[e])), fabsf(__uint_as_float(d[e + 1])));
+                    const float2 dp = make_float2(__uint_as_float(d[e]), __uint_as_float(d[e + 1]));
+                    dots = fma2(y, dp, dots);
+                    if (Elem<T>::kUp) top = max3(top, fabsf(y.x * dp.x), fabsf(y.y * dp.y));
                 }
             }
             tc::fence_before();
@@ -182,14 +183,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_delta_kernel(const __grid_
         }
         // ---- the copies' and groups' sums of a row, one after another ----
         ctl->sum[w][half][l] = make_float2(all_dots.total(), all_mass.total());
-        if (Elem<T>::kUp) {
-            ctl->tops[w][half][l] = top;
-            const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(top));     // of numbers that are not negative: as their bits
-            if (lane == 0) atomicMax(&ctl->top, most);
-        }
+        if (Elem<T>::kUp) ctl->tops[w][half][l] = top;
         asm volatile("bar.sync 1, 512;" ::: "memory");
-        if (Elem<T>::kUp && tid == 0)
-            p.dp_top[(uint64_t)p.splits * p.T * p.hq + (uint64_t)hk * gridDim.x + blockIdx.x] = __uint_as_float(ctl->top);
         if (tid < kRows && row0 + tid < p.rows) {                     // warps 0-3 hold lane tid of group 0 as their own row
             float a = 0.0f, m = 0.0f, most = 0.0f;
             for (int c = tid; c < 128; c += kRows)
@@ -201,7 +196,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_delta_kernel(const __grid_
                 }
             const uint64_t at = ((uint64_t)split * p.T + t) * p.hq + hk * p.group + g;
             p.delta_part[at] = make_float2(a, m);
-            if (Elem<T>::kUp) p.dp_top[at] = most;
+            if (Elem<T>::kUp) p.pdp_top[at] = most;
         }
     }
     __syncwarp();

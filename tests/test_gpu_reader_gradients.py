@@ -186,3 +186,28 @@ def test_half_gradients_of_any_size(T, d, mapped, scale):
         least = 2.0 ** -25 * got[name].numel() ** 0.5 / float(want[name].norm())
         fits = want[name].abs() < 65000
         assert torch.isfinite(got[name][fits]).all() and off(got[name][fits], want[name][fits]) <= 2.0 ** -9 + least, name
+
+
+@pytest.mark.parametrize("T,n,hq,hkv,d,mapped", [(2, 65536, 1, 1, 32, False), (8, 65536, 4, 2, 64, False), (100, 30000, 2, 2, 128, True)])
+def test_half_gradients_beside_values_that_do_not_count(T, n, hq, hkv, d, mapped):
+    """A thousand nodes with values 2^12 times as large as the others', in a bucket whose bias leaves them 2^-58 of a weight:
+    they change nothing, nor what the others' gradients keep."""
+    edges = list(range(9))
+    x = problem(T, n, hq, hkv, d, "fp16", edges, seed=T, sources=min(T, 32), mapped=mapped)
+    if mapped:
+        x["source"].clamp_(min=0)
+    far = torch.randperm(n, device="cuda")[:1000]
+    x["hops"][far] = 8
+    x["bias"][:, 8] = -40.0
+    x["hops"][x["hops"] == 9] = 7
+    near = torch.ones(n, dtype=torch.bool, device="cuda")
+    near[far] = False
+    x["hops"][near] = x["hops"][near].clamp(max=7)
+    x["v"][far] *= 2.0 ** 12
+    x["q"] /= 16
+    x["k"] *= 16
+    want, tol = reference(x, "fp16", edges)
+    got = call(x, "fp16", edges)
+    least = 2.0 ** -25 * got["dq"].numel() ** 0.5 / float(want["dq"].norm())
+    assert off(got["dq"], want["dq"]) <= 2.0 ** -10 + least, off(got["dq"], want["dq"])
+    within("dbias", got["dbias"], want["dbias"], tol + 2.0 ** -25)
