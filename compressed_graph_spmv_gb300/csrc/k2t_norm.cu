@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
         if (c.on()) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
-                if (c.has(e)) {
+                if (c.has(e) && p.y) {
                     w[i].v[e] = static_cast<const T *>(p.weight)[c.c + e];
                     if (p.bias) bi[i].v[e] = static_cast<const T *>(p.bias)[c.c + e];
                 }
@@ -294,6 +294,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
         const float rstd = rsqrtf(group_sum1<TPR>(q.x + q.y, buf, group, turn) * p.inv_dim + p.eps);
         const float2 r2 = make_float2(rstd, rstd);
         if (tid == 0) p.mean[row] = mean, p.rstd[row] = rstd;
+        if (!p.y) continue;                              // only the statistics
 #pragma unroll
         for (int e = 0; e < N2; ++e) set_pair<T, VEC>(z, e, fma2(mul2(d[e], r2), pair_of<T, VEC>(w, e), pair_of<T, VEC>(bi, e)));
 #pragma unroll
@@ -306,13 +307,16 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) norm_fwd_kernel(const __
 
 // dx = rstd (w dy - c1 - xh c2) + dz with c1 = mean(w dy), c2 = mean(w dy xh);
 // part[block][0 | 1][dim]: the block's sums of dy xh and dy.
-// Without the forward call's mean and rstd they are formed from z, which lies in registers: one more reduction a row.
-template <typename T, int VEC, int TPR, int PER, int AHEAD, bool SHIFT>
+// FORM: mean and rstd are formed from z, which lies in registers (see WarpJoin), else read.
+template <typename T, int VEC, int TPR, int PER, int AHEAD, bool SHIFT, bool FORM>
 __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 ? 1 : PER > 1 ? 2 : 3) norm_bwd_kernel(const __grid_constant__ NormParams p)
 {
     using P = Pack<T, VEC>;
     using Gr = Group<TPR>;
-    __shared__ float2 buf[2 * Gr::kGroups * Gr::kWarps];
+    // Two barriers a row in up to 128 threads, one in more or where edges are masked: measured with the other, 2^18 x 1024
+    // bf16 (64 threads) 328 us, one barrier 369; 65536 x 4096 (256 threads) 289, two 323; 200000 x 777 (shifted) 399, two 416.
+    using Join = std::conditional_t<!FORM, NoJoin<TPR>, std::conditional_t<SHIFT || (TPR > 128), WarpJoin<TPR>, GroupJoin<TPR>>>;
+    __shared__ typename Join::Shared buf;
     const int tid = threadIdx.x % TPR, group = threadIdx.x / TPR;
     int turn = 0;
     // a thread's values go in pairs, one instruction for two; those past the row count as 0
@@ -323,7 +327,6 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 ? 1 : PER > 1
     const int shift = SHIFT ? (int)(first * p.dim % VEC) : 0;
     using Pc = Piece<T, VEC, SHIFT>;
     auto piece = [&](int i) { return Pc((tid + i * TPR) * VEC - shift, p.dim); };
-    const bool form = !p.mean;
     float2 w[N2], dw[N2], db[N2];
 #pragma unroll
     for (int e = 0; e < PER * VEC; ++e) {
@@ -337,10 +340,19 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 ? 1 : PER > 1
     in.src[1] = static_cast<const T *>(p.dy);
     in.src[2] = static_cast<const T *>(p.dz);
     in.start();
+    float count = 0.0f;
+    if (FORM) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const auto c = piece(i);
+            if (c.on()) count += SHIFT ? (float)(min(c.c + VEC, c.dim) - max(c.c, 0)) : (float)VEC;
+        }
+    }
+    Join joins(&buf, group, count, p.dim);
     for (uint64_t row = first; row < p.n; row += step) {
         const uint64_t at = row * p.dim;
         float mean = 0.0f, rstd = 0.0f;
-        if (!form) mean = p.mean[row], rstd = p.rstd[row];
+        if (!FORM) mean = p.mean[row], rstd = p.rstd[row];
         P z[PER], g[PER], x[PER];
         in.ready();
 #pragma unroll
@@ -353,29 +365,27 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 ? 1 : PER > 1
                 z[i] = g[i] = x[i] = zero_pack<T, VEC>();
             }
         }
-        in.taken();
-        // the sums of one row: z and a = w dy, then the squares of z - mean and a (z - mean)
         float2 xh[N2], a[N2], s0 = make_float2(0.0f, 0.0f), s1 = s0, s2 = s0;
+        float c1, c2;
+        if constexpr (FORM) {
+            in.taken();
 #pragma unroll
-        for (int e = 0; e < N2; ++e) {
-            const float2 dy = pair_of<T, VEC>(g, e);
-            xh[e] = pair_of<T, VEC>(z, e);
-            a[e] = mul2(dy, w[e]);
-            s0 = add2(s0, xh[e]);
-            s1 = add2(s1, a[e]);
-            db[e] = add2(db[e], dy);
-        }
-        float c0 = s0.x + s0.y, c1 = s1.x + s1.y;
-        if (form) {
-            group_sum<TPR>(c0, c1, buf, group, turn);
-            mean = c0 * p.inv_dim;
-        }
-        const float2 nm = make_float2(-mean, -mean);
-        s0 = make_float2(0.0f, 0.0f);
+            for (int e = 0; e < N2; ++e) {
+                const float2 dy = pair_of<T, VEC>(g, e);
+                xh[e] = pair_of<T, VEC>(z, e);
+                a[e] = mul2(dy, w[e]);
+                s0 = add2(s0, xh[e]);
+                s1 = add2(s1, a[e]);
+                db[e] = add2(db[e], dy);
+            }
+            float c0 = s0.x + s0.y;
+            c1 = s1.x + s1.y;
+            joins.add(c0, c1);
+            const float own = c0 * joins.inv;
+            const float2 nm = make_float2(-own, -own);
+            s0 = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int e = 0; e < N2; ++e) xh[e] = add2(xh[e], nm), s2 = fma2(a[e], xh[e], s2);
-        float c2 = s2.x + s2.y;
-        if (form) {
+            for (int e = 0; e < N2; ++e) xh[e] = add2(xh[e], nm);
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const auto c = piece(i);
@@ -388,20 +398,38 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 ? 1 : PER > 1
                 }
             }
 #pragma unroll
-            for (int e = 0; e < N2; ++e) s0 = fma2(xh[e], xh[e], s0);
+            for (int e = 0; e < N2; ++e) s0 = fma2(xh[e], xh[e], s0), s2 = fma2(a[e], xh[e], s2);
             c0 = s0.x + s0.y;
-            group_sum<TPR>(c0, c2, buf, group, turn);
-            rstd = rsqrtf(c0 * p.inv_dim + p.eps);
+            c2 = s2.x + s2.y;
+            joins.add(c0, c2);
+            const RowSums sums = joins.join(RowSums{own, c0, c1, c2}, p.inv_dim);
+            mean = sums.mean;
+            rstd = rsqrtf(sums.squares * p.inv_dim + p.eps);
+            c1 = sums.a;
+            c2 = sums.az * rstd;
+            const float2 off = make_float2(own - mean, own - mean), r2 = make_float2(rstd, rstd);
+#pragma unroll
+            for (int e = 0; e < N2; ++e) {
+                xh[e] = mul2(Join::kMoves ? add2(xh[e], off) : xh[e], r2);
+                dw[e] = fma2(pair_of<T, VEC>(g, e), xh[e], dw[e]);
+            }
         } else {
+            const float2 nm = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
+#pragma unroll
+            for (int e = 0; e < N2; ++e) {
+                const float2 dy = pair_of<T, VEC>(g, e);
+                xh[e] = mul2(add2(pair_of<T, VEC>(z, e), nm), r2);
+                a[e] = mul2(dy, w[e]);
+                s1 = add2(s1, a[e]);
+                s2 = fma2(a[e], xh[e], s2);
+                dw[e] = fma2(dy, xh[e], dw[e]);
+                db[e] = add2(db[e], dy);
+            }
+            in.taken();
+            c1 = s1.x + s1.y, c2 = s2.x + s2.y;
             group_sum<TPR>(c1, c2, buf, group, turn);
         }
-        c2 *= rstd;
         const float2 r2 = make_float2(rstd, rstd);
-#pragma unroll
-        for (int e = 0; e < N2; ++e) {
-            xh[e] = mul2(xh[e], r2);
-            dw[e] = fma2(pair_of<T, VEC>(g, e), xh[e], dw[e]);
-        }
         const float2 n1 = make_float2(-c1 * p.inv_dim, -c1 * p.inv_dim), n2 = make_float2(-c2 * p.inv_dim, -c2 * p.inv_dim);
 #pragma unroll
         for (int e = 0; e < N2; ++e) {
@@ -442,7 +470,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads, TPR == 512 ? 1 : PER > 1
 }
 
 // AHEAD: rows asked for ahead where blocks stay for several (0: a row's loads wait for its turn, less to set up).
-template <typename T, int VEC, int TPR, int PER, int AHEAD, bool SHIFT, bool BACK> int run_norm(NormParams &p, uint32_t blocks, cudaStream_t st)
+template <typename T, int VEC, int TPR, int PER, int AHEAD, bool SHIFT, bool BACK, bool FORM = false> int run_norm(NormParams &p, uint32_t blocks, cudaStream_t st)
 {
     using Gr = Group<TPR>;
     if constexpr (!BACK) {
@@ -455,10 +483,13 @@ template <typename T, int VEC, int TPR, int PER, int AHEAD, bool SHIFT, bool BAC
         if (SHIFT) blocks = (blocks + 7) / 8 * 8;      // a thread's rows a multiple of VEC apart
         return norm_launch(kernel, dim3(blocks), Gr::kThreads, ring, st, p);
     } else {
+        // rows of more than 1024 pieces spill registers as it is: their statistics come from a pass of their own (dispatch)
+        if constexpr (!FORM && (VEC == 1 || PER <= 2))
+            if (!p.mean) return run_norm<T, VEC, TPR, PER, AHEAD, SHIFT, BACK, true>(p, blocks, st);
         if (blocks) {
             const size_t ring = (size_t)Gr::kThreads * RowStream<T, VEC, TPR, PER, 3, AHEAD, SHIFT>::kBytes;
             const size_t sums = Gr::kGroups > 1 ? 2 * p.dim * sizeof(float) : 0;
-            constexpr auto kernel = norm_bwd_kernel<T, VEC, TPR, PER, AHEAD, SHIFT>;
+            constexpr auto kernel = norm_bwd_kernel<T, VEC, TPR, PER, AHEAD, SHIFT, FORM>;
             int rc = norm_shared<kernel>();
             if (!rc && AHEAD > 0) rc = norm_resident(kernel, blocks, Gr::kThreads, std::max(ring, sums));
             if (rc) return rc;
@@ -539,6 +570,12 @@ int check_norm(const k2t_norm *a)
     return K2T_OK;
 }
 
+// Partial sums of the weight's gradient: whole 256 bytes of them.
+uint64_t norm_part_floats(const k2t_norm *a)
+{
+    return align_up(((uint64_t)norm_parts(a->n_rows, 1) + 7) / 8 * 8 * 2 * a->dim * sizeof(float), 256) / sizeof(float);
+}
+
 int dispatch(const k2t_norm *a, NormParams &p, bool backward, cudaStream_t st)
 {
     uintptr_t all = 0;
@@ -562,7 +599,18 @@ int dispatch(const k2t_norm *a, NormParams &p, bool backward, cudaStream_t st)
     const bool few = a->n_rows <= 16384 && a->dim <= 2048, fill = !backward && a->dim > 1024 && a->dim <= 2048;
     const uint32_t c = shifted_pieces(a->dim, 16 / size);
     const bool shift = !vec && !few && !(all & 15) && shift_pays(a->dim, c, backward);
-    if (!vec && !shift && !few && !fill) return norm_ragged(p, a->dtype, backward, st);
+    const bool ragged = !vec && !shift && !few && !fill;
+    if (form && (ragged ? a->dim > 4096 : vec && a->dim * size / 16 > 1024)) {
+        // statistics in a forward pass that writes nothing else, behind the partial sums
+        NormParams f{};
+        f.x = p.z_in;
+        k2t_norm b = *a;
+        b.mean = p.part + norm_part_floats(a);
+        b.rstd = b.mean + a->n_rows;
+        if (int rc = dispatch(&b, f, false, st)) return rc;
+        p.mean = b.mean, p.rstd = b.rstd;
+    }
+    if (ragged) return norm_ragged(p, a->dtype, backward, st);
     const auto run = [&](auto zero) {
         using T = decltype(zero);
         return backward ? norm_dispatch<T, true>(p, vec, shift, st) : norm_dispatch<T, false>(p, vec, shift, st);
@@ -582,7 +630,7 @@ extern "C" {
 uint64_t k2t_norm_work_bytes(const k2t_norm *a)
 {
     if (check_norm(a)) return 0;
-    return align_up(((uint64_t)norm_parts(a->n_rows, 1) + 7) / 8 * 8 * 2 * a->dim * sizeof(float), 256);
+    return norm_part_floats(a) * sizeof(float) + (a->flags & K2T_NORM_FORM_STATS ? align_up(a->n_rows * 2 * sizeof(float), 256) : 0);
 }
 
 int k2t_norm_forward(const k2t_norm *a, void *stream)

@@ -3,6 +3,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -68,6 +69,67 @@ __device__ __forceinline__ void group_sum(float &a, float &b, float2 *buf, int g
     }
 }
 
+// Statistics of a row of values z formed beside the sums of a = w dy, with one barrier a row: each warp (or group, if that
+// is no more) takes its own values' mean m_w first, sums squares and products around it, and the warps' sums are joined.
+// With n_w values of a warp, sum (z - m)^2 = sum_w (squares_w + n_w (m_w - m)^2) and sum a (z - m) = sum_w (az_w +
+// (m_w - m) a_w): every difference is small against what it is taken of.
+struct RowSums { float mean, squares, a, az; };
+template <int TPR> struct WarpJoin {
+    static constexpr bool kMoves = true;      // join changes the mean
+    static constexpr int W = Group<TPR>::kWarps;
+    struct Shared { float4 sums[2][Group<TPR>::kGroups][W]; float count[Group<TPR>::kGroups][W]; };
+    Shared *sh;
+    int group, turn;
+    float inv;                          // 1 / this warp's values
+    // count: values of this thread; the same of every row
+    __device__ __forceinline__ WarpJoin(Shared *shared, int group_, float count, uint32_t dim) : sh(shared), group(group_), turn(0)
+    {
+        float none = 0.0f;
+        if (TPR > 32) add(count, none);
+        else count = (float)dim;
+        inv = count > 0.0f ? 1.0f / count : 0.0f;
+        if (TPR > 32 && (threadIdx.x & 31) == 0) sh->count[group][threadIdx.x % TPR >> 5] = count;   // read behind a row's barrier
+    }
+    __device__ __forceinline__ static void add(float &a, float &b)
+    {
+        const uint32_t lanes = group_lanes<TPR>();
+#pragma unroll
+        for (int x = TPR < 32 ? TPR / 2 : 16; x; x >>= 1) {
+            a += __shfl_xor_sync(lanes, a, x);
+            b += __shfl_xor_sync(lanes, b, x);
+        }
+    }
+    __device__ __forceinline__ RowSums join(RowSums r, float inv_dim)
+    {
+        if constexpr (TPR > 32) {
+            float4 *at = sh->sums[turn][group];
+            if ((threadIdx.x & 31) == 0) at[threadIdx.x % TPR >> 5] = make_float4(r.mean, r.squares, r.a, r.az);
+            asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
+            // lane i has warp i mod W's sums
+            const int i = threadIdx.x & (W - 1);
+            const float4 v = at[i];
+            const float n = sh->count[group][i];
+            r.mean = v.x * (n * inv_dim);
+            r.a = v.z;
+#pragma unroll
+            for (int x = W / 2; x; x >>= 1) {
+                r.mean += __shfl_xor_sync(~0u, r.mean, x);
+                r.a += __shfl_xor_sync(~0u, r.a, x);
+            }
+            const float d = v.x - r.mean;
+            r.squares = fmaf(n * d, d, v.y);
+            r.az = fmaf(d, v.z, v.w);
+#pragma unroll
+            for (int x = W / 2; x; x >>= 1) {
+                r.squares += __shfl_xor_sync(~0u, r.squares, x);
+                r.az += __shfl_xor_sync(~0u, r.az, x);
+            }
+            turn ^= 1;
+        }
+        return r;
+    }
+};
+
 // One value's sum.
 template <int TPR> __device__ __forceinline__ float group_sum1(float a, float2 *buf, int group, int &turn)
 {
@@ -82,6 +144,23 @@ template <int TPR> __device__ __forceinline__ float group_sum1(float a, float2 *
         return a;
     }
 }
+
+// The same with the whole group's sums at once: two barriers a row, fewer instructions.
+template <int TPR> struct GroupJoin {
+    static constexpr bool kMoves = false;
+    using Shared = float2[2 * Group<TPR>::kGroups * Group<TPR>::kWarps];
+    float2 *buf;
+    int group, turn;
+    float inv;
+    __device__ __forceinline__ GroupJoin(Shared *shared, int group_, float, uint32_t dim) : buf(*shared), group(group_), turn(0), inv(1.0f / (float)dim) {}
+    __device__ __forceinline__ void add(float &a, float &b) { group_sum<TPR>(a, b, buf, group, turn); }
+    __device__ __forceinline__ RowSums join(RowSums r, float) { return r; }
+};
+// A kernel that reads its statistics.
+template <int TPR> struct NoJoin {
+    using Shared = float2[2 * Group<TPR>::kGroups * Group<TPR>::kWarps];
+    template <typename... A> __device__ __forceinline__ NoJoin(const A &...) {}
+};
 
 // dweight, dbias: 8 columns (one 32-byte sector) a block, 128 threads a column over the partial rows, so that few loads
 // follow one another.

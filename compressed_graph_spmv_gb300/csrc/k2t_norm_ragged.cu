@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) ragged_fwd_kernel(const 
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const uint32_t c = c0 + i * TPR;
-        w[i] = c < p.dim ? to_f(static_cast<const T *>(p.weight)[c]) : 0.0f;
+        w[i] = c < p.dim && p.y ? to_f(static_cast<const T *>(p.weight)[c]) : 0.0f;
         b[i] = c < p.dim && p.bias ? to_f(static_cast<const T *>(p.bias)[c]) : 0.0f;
     }
     const uint32_t row_bytes = p.dim * (uint32_t)sizeof(T);
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) ragged_fwd_kernel(const 
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    const bool y_over = same_skew(p.x, p.y), z_over = p.residual && same_skew(p.residual, p.z);
+    const bool y_over = p.y && same_skew(p.x, p.y), z_over = p.residual && same_skew(p.residual, p.z);
     int slot = 0;
     bring(0, false);
     for (; row0 < p.n; row0 += step, off += step_bytes) {
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) ragged_fwd_kernel(const 
                 if (c < p.dim) {
                     const T y = from_f<T>(fmaf(v[i] * rstd, w[i], b[i]));
                     if (y_over) xr[c] = y;
-                    else static_cast<T *>(p.y)[row * p.dim + c] = y;
+                    else if (p.y) static_cast<T *>(p.y)[row * p.dim + c] = y;
                 }
             }
         }
@@ -172,12 +172,14 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) ragged_fwd_kernel(const 
     }
 }
 
-template <typename T, int TPR, int PER>
+// FORM: mean and rstd are formed from z (see WarpJoin), else read.
+template <typename T, int TPR, int PER, bool FORM>
 __global__ void __launch_bounds__(Group<TPR>::kThreads) ragged_bwd_kernel(const __grid_constant__ NormParams p, uint32_t rows, uint32_t image, int images)
 {
     using Gr = Group<TPR>;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float2 buf[2 * Gr::kGroups * Gr::kWarps];
+    using Join = std::conditional_t<FORM, WarpJoin<TPR>, NoJoin<TPR>>;
+    __shared__ typename Join::Shared buf;
     const int tid = threadIdx.x, c0 = tid % TPR, group = tid / TPR;
     const uint32_t tensors = p.dz ? 3 : 2;
     int turn = 0;
@@ -205,8 +207,14 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) ragged_bwd_kernel(const 
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    const bool over = same_skew(p.dy, p.dx), form = !p.mean;
+    const bool over = same_skew(p.dy, p.dx);
     auto in_row = [&](int i) { return c0 + i * TPR < p.dim; };
+    float count = 0.0f;
+    if (FORM) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) count += in_row(i) ? 1.0f : 0.0f;
+    }
+    Join joins(&buf, group, count, p.dim);
     int slot = 0;
     bring(0, false);
     for (; row0 < p.n; row0 += step, off += step_bytes) {
@@ -220,46 +228,63 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads) ragged_bwd_kernel(const 
         for (uint32_t r = group; r < here; r += Gr::kGroups) {
             const uint64_t row = row0 + r;
             const size_t off = (size_t)r * p.dim;
-            float mean = 0.0f, rstd = 0.0f;
-            if (!form) mean = p.mean[row], rstd = p.rstd[row];
-            float xh[PER], a[PER], sum = 0.0f, c1 = 0.0f, c2 = 0.0f;
+            float xh[PER], a[PER], rstd, c1 = 0.0f, c2 = 0.0f;
+            if constexpr (FORM) {
+                float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const uint32_t c = c0 + i * TPR;
-                xh[i] = a[i] = 0.0f;
-                if (c < p.dim) {
-                    const float dy = to_f(gs[off + c]);
-                    xh[i] = to_f(zs[off + c]);
-                    a[i] = dy * w[i];
-                    sum += xh[i];
-                    c1 += a[i];
-                    db[i] += dy;
+                for (int i = 0; i < PER; ++i) {
+                    const uint32_t c = c0 + i * TPR;
+                    xh[i] = a[i] = 0.0f;
+                    if (c < p.dim) {
+                        const float dy = to_f(gs[off + c]);
+                        xh[i] = to_f(zs[off + c]);
+                        a[i] = dy * w[i];
+                        sum += xh[i];
+                        c1 += a[i];
+                        db[i] += dy;
+                    }
                 }
-            }
-            if (form) {
-                group_sum<TPR>(sum, c1, buf, group, turn);
-                mean = sum * p.inv_dim;
+                joins.add(sum, c1);
+                const float own = sum * joins.inv;
                 sum = 0.0f;
-            }
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                xh[i] = in_row(i) ? xh[i] - mean : 0.0f;
-                sum = fmaf(xh[i], xh[i], sum);
-                c2 = fmaf(a[i], xh[i], c2);
-            }
-            if (form) {
-                group_sum<TPR>(sum, c2, buf, group, turn);
-                rstd = rsqrtf(sum * p.inv_dim + p.eps);
+                for (int i = 0; i < PER; ++i) {
+                    xh[i] = in_row(i) ? xh[i] - own : 0.0f;
+                    sum = fmaf(xh[i], xh[i], sum);
+                    c2 = fmaf(a[i], xh[i], c2);
+                }
+                joins.add(sum, c2);
+                const RowSums sums = joins.join(RowSums{own, sum, c1, c2}, p.inv_dim);
+                rstd = rsqrtf(sums.squares * p.inv_dim + p.eps);
+                c1 = sums.a;
+                c2 = sums.az * rstd;
+                const float to = own - sums.mean;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    xh[i] = (xh[i] + to) * rstd;
+                    if (in_row(i)) dw[i] = fmaf(to_f(gs[off + c0 + i * TPR]), xh[i], dw[i]);
+                }
             } else {
+                const float mean = p.mean[row];
+                rstd = p.rstd[row];
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const uint32_t c = c0 + i * TPR;
+                    xh[i] = a[i] = 0.0f;
+                    if (c < p.dim) {
+                        const float dy = to_f(gs[off + c]);
+                        xh[i] = (to_f(zs[off + c]) - mean) * rstd;
+                        a[i] = dy * w[i];
+                        c1 += a[i];
+                        c2 = fmaf(a[i], xh[i], c2);
+                        dw[i] = fmaf(dy, xh[i], dw[i]);
+                        db[i] += dy;
+                    }
+                }
                 group_sum<TPR>(c1, c2, buf, group, turn);
             }
             c1 *= p.inv_dim;
-            c2 *= p.inv_dim * rstd;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                xh[i] *= rstd;
-                if (in_row(i)) dw[i] = fmaf(to_f(gs[off + c0 + i * TPR]), xh[i], dw[i]);
-            }
+            c2 *= p.inv_dim;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const uint32_t c = c0 + i * TPR;
@@ -319,7 +344,10 @@ template <typename T, int TPR, int PER> int run_ragged(NormParams &p, bool backw
         return norm_launch(kernel, dim3(blocks), Group<TPR>::kThreads, smem, st, p, b.rows, b.image, images);
     };
     if (!backward) return launch(Kernel<ragged_fwd_kernel<T, TPR, PER>>());
-    int rc = launch(Kernel<ragged_bwd_kernel<T, TPR, PER>>());
+    int rc;
+    // rows of more than 4096 values come with their statistics
+    if constexpr (PER <= 16) rc = p.mean ? launch(Kernel<ragged_bwd_kernel<T, TPR, PER, false>>()) : launch(Kernel<ragged_bwd_kernel<T, TPR, PER, true>>());
+    else rc = launch(Kernel<ragged_bwd_kernel<T, TPR, PER, false>>());
     return rc ? rc : norm_launch(norm_join_kernel<T>, dim3((p.dim + 7) / 8, p.dbias ? 2 : 1), 1024, 0, st, p);
 }
 

@@ -287,12 +287,13 @@ class LayerNorm(_Placed):
         self._current, self._here = _stream_getter(torch), _device_getter(torch)
         self._n = n_rows
         self._work, self._own = (_Buffer(torch, device, self._current) for _ in range(2))     # backward's; mean and rstd
-        self._bytes = None
+        a.flags = NORM_FORM_STATS           # the more of the two
+        self._bytes = int(self._lib.k2t_norm_work_bytes(self._ref))
         self._lock = threading.Lock()
 
     def work_bytes(self) -> int:
-        """Device bytes of the backward pass's work buffer (k2t_norm_work_bytes)."""
-        return int(self._lib.k2t_norm_work_bytes(self._ref))
+        """Device bytes of the backward pass's work buffer (k2t_norm_work_bytes), statistics formed again or not."""
+        return self._bytes
 
     def _own_stats(self, stream, device):
         at = self._own.get(max(8 * self._n, 16), stream, device)
@@ -352,8 +353,6 @@ class LayerNorm(_Placed):
                                 *(_NONE if form else self._stats(mean, rstd, device)), _flat("dy", dy, rows, dt, device),
                                 0 if dz is None else _flat("dz", dz, rows, dt, device), _flat("dx", dx, rows, dt, device),
                                 _flat("dweight", dweight, cols, dt, device), 0 if dbias is None else _flat("dbias", dbias, cols, dt, device))
-            if self._bytes is None:
-                self._bytes = self.work_bytes()
             st = self._current(device) if stream is None else _stream_ptr(stream)
             work = self._work
             if work.last != st:

@@ -463,7 +463,7 @@ typedef struct {
     void *dx, *dweight, *dbias; /* dbias may be NULL                                                 */
 } k2t_norm;
 
-/* Bytes of `work` k2t_norm_backward needs; 0 for sizes it refuses. */
+/* Bytes of `work` k2t_norm_backward needs with these flags; 0 for what it refuses. */
 K2T_API uint64_t k2t_norm_work_bytes(const k2t_norm *a);
 
 /* y, z, mean and rstd.  y may be x or residual, z may be x or residual, y and
