@@ -61,8 +61,8 @@ def _link(objs, out: str) -> None:
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     """Compile the product library libk2t.so, its bounds-checked twin
-    libk2t_checked.so (-DK2T_CHECKED: the same ABI, kernels that test their
-    indexes and report a failure in the device status word) and the
+    libk2t_checked.so (-DK2T_CHECKED: the same ABI, and a tree's kernels test
+    their indexes and report a failure in the device status word) and the
     benchmark's probe library libk2t_probe.so where a source is newer than
     the library (all translation units in parallel); return the product
     library's path."""

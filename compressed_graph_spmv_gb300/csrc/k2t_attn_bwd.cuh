@@ -24,13 +24,14 @@
 // head is the same in every tile, and the sums by bucket need one table a row
 // of the tile.
 //
-// What bounds it: 32 queries over 2^18 nodes take 342 us forward and backward,
-// where the bytes take 147 (216 with keys and values read a second time): the
-// latency of a tile's chain of scores, softmax, products, sums and stores,
-// with two units in flight.  With 257 queries over 8191 nodes the kernel that
-// streams rows takes 39 us (tensor pipe busy 24% of it) and the one that
-// streams nodes 57 (11%): there the sums by bucket, a read, add and write of
-// shared memory for each score gradient, are the longest stage.
+// What bounds it: 32 queries over 2^18 nodes take 467 us forward and backward,
+// 115 of them for delta, where the bytes take 147 (284 with keys and values
+// read a second and third time): the latency of a tile's chain of scores,
+// softmax, products, sums and stores, with two units in flight.  With 257
+// queries over 8191 nodes the kernel that streams rows takes 40 us (tensor pipe
+// busy 18% of it) and the one that streams nodes 63 (9%): there the sums by
+// bucket, reads, adds and writes of shared memory for each score gradient, are
+// the longest stage.
 #pragma once
 
 #include <type_traits>
@@ -43,6 +44,7 @@ namespace k2t {
 constexpr int kBwdThreads = 800;
 constexpr int kBwdRowThreads = 544;
 constexpr int kBwdRows = 32;
+using Rest = __nv_bfloat16;      // what rounding took off a score gradient, in either type: where fp16 keeps nothing, this is all of it
 
 // What the kernels need of a row, made once by attn_rows_kernel: lse in units
 // of log2 (+inf for a row that saw nothing or does not exist: its weights
@@ -180,7 +182,7 @@ __device__ __forceinline__ void unit32(uint32_t at, const RowInfo *info, bool pl
                 pw[e / 2 + y] = Elem<T>::pack(pv[2 * y], pv[2 * y + 1]);
                 dw[e / 2 + y] = Elem<T>::pack(dv[2 * y], dv[2 * y + 1]);
                 const float2 kept = Elem<T>::unpack(dw[e / 2 + y]);
-                rw[e / 2 + y] = Elem<T>::pack(dv[2 * y] - kept.x, dv[2 * y + 1] - kept.y);
+                rw[e / 2 + y] = Elem<Rest>::pack(dv[2 * y] - kept.x, dv[2 * y + 1] - kept.y);
                 kw[e / 2 + y] = Elem<T>::kUp && ds ? Elem<T>::pack(dv[2 * y] * (up * inverse_power(own[2 * y])),
                                                                    dv[2 * y + 1] * (up * inverse_power(own[2 * y + 1]))) : dw[e / 2 + y];
             }
@@ -458,12 +460,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_nodes_kernel(const __
                 const float down = row_down(r, c);
                 auto term = [&](int node) {
                     const uint8_t *at = ds + node * 128 + ((chunk ^ (node & 7)) << 4);
-                    const float x = Elem<T>::to_float(*reinterpret_cast<const T *>(at)) + Elem<T>::to_float(*reinterpret_cast<const T *>(at + S::kPanel));
+                    const float x = Elem<T>::to_float(*reinterpret_cast<const T *>(at)) + Elem<Rest>::to_float(*reinterpret_cast<const Rest *>(at + S::kPanel));
                     return Elem<T>::kUp ? x * down : x;
                 };
                 // A node is a read, an add and a write of its bucket.  Four nodes go on at once: the reads before the first
                 // write, a node that shares the bucket of one before it continues from that one's sum, and the writes in the
-                // nodes' order, so that the last of a bucket stands.  The next four nodes' terms are read meanwhile.
+                // nodes' order, so that the last of a bucket stands.  The next four nodes' terms are read meanwhile.  (257 queries
+                // over 8191 nodes, forward and backward, 157 us, one node after another 163; 32 over 2^18 467 and 474.)
                 uint32_t bw = *reinterpret_cast<const uint32_t *>(bt);
                 float x0 = term(0), x1 = term(1), x2 = term(2), x3 = term(3);
 #pragma unroll 1

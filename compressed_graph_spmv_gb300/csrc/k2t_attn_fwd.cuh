@@ -32,10 +32,12 @@
 // small weight beside one of 1 make up much of a row.
 //
 // What bounds it: memory with few rows (4 rows a head over 2^20 nodes, bf16:
-// 297 us, the copy rate), the softmax threads' issue slots with 128 rows a head
-// (32 queries over 2^20 nodes: 354 us where the bytes take 241; about 15
-// instructions a score with its table lookup).  The tensor pipe is busy 18 to
-// 32% of the time.
+// 300 us, the copy rate).  With 128 rows a head or more nothing is at its limit
+// (32 queries over 2^17 nodes: DRAM 46%, issue slots 59%, tensor pipe 25%
+// busy; 1024 over 16384: 8, 57 and 25%): the softmax threads wait most for
+// scores on their way out of tensor memory, and a score is about 15
+// instructions with its table lookup.  32 queries over 2^20 nodes 363 us,
+// where the bytes take 241.
 #pragma once
 
 #include <type_traits>

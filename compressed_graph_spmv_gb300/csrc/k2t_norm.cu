@@ -6,8 +6,8 @@
 // formed, the mean first and then the squares around it, so that no
 // cancellation of large sums arises.  Bound by memory: the passes are loads,
 // two reductions of a few shuffles, and stores (2^18 x 1024 bf16 with the
-// residual: 314 us forward and 325 backward, 101 and 97% of the copy rate;
-// 2^17 x 2048 without it 177 and 309, 90 and 77%, where a row's reductions
+// residual: 314 us forward and 327 backward, 101 and 97% of the copy rate;
+// 2^17 x 2048 without it 177 and 294, 90 and 81%, where a row's reductions
 // are not hidden by a third and fourth tensor).  Blocks stay for many rows,
 // keep the weight in registers, and in the backward pass sum their rows'
 // terms of dweight and dbias there; each block writes one partial row, and
@@ -593,7 +593,7 @@ int dispatch(const k2t_norm *a, NormParams &p, bool backward, cudaStream_t st)
     p.mean = form ? nullptr : a->mean;
     p.rstd = form ? nullptr : a->rstd;
     // Rows that are not whole pieces: shifted where that pays; else value by value while there are few of them, when a call
-    // is its latency (4999 x 333 fp32, training: 15 us against 20), else in stretches (200000 x 333 bf16, forward: 170 us
+    // is its latency (4999 x 333 fp32, training: 18 us against 20), else in stretches (200000 x 333 bf16, forward: 170 us
     // against 220; 65536 x 3999: 610 us against 2335).  Forward rows of 1025 to 2048 values fill a block with single values
     // and stay with them (100000 x 1465 fp16: 308 us against 417; backward 422 against 393).
     const bool few = a->n_rows <= 16384 && a->dim <= 2048, fill = !backward && a->dim > 1024 && a->dim <= 2048;

@@ -9,8 +9,8 @@
 // the columns c, c + TPR, ..., and the results written over what they came
 // from; the stretch leaves in 16-byte pieces again, its two ragged ends value
 // by value, since the pieces there belong to the neighbours too.
-// Measured: 200000 x 333 bf16 with the residual 170 us forward and 173
-// backward, 46% of the copy rate: what bounds it is the shared memory's
+// Measured: 200000 x 333 bf16 with the residual 164 us forward and 173
+// backward (208 with the statistics formed), 46% of the copy rate: what bounds it is the shared memory's
 // accesses and the address arithmetic of single values.  Long rows of tensors
 // that start on a piece go another way (see shift_pays).
 #include "k2t_norm.cuh"

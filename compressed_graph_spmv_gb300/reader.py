@@ -147,6 +147,9 @@ class HopAttention(_Placed):
     ``Tree.msbfs`` leaves it: -1 masks a node) and ``edges``, the first hop of
     each bucket of the bias table [n_heads, len(edges)]; ``sources`` 0 is plain
     attention, no ``edges`` masks without a bias.  See ``k2t_attn``.
+
+    A call returns before its kernels have run: should a bounded wait in one of
+    them run out, the outputs are undefined and only ``status`` tells.
     """
 
     def __init__(self, n_queries: int, n_nodes: int, n_heads: int, n_kv_heads: int, head_dim: int, dtype,

@@ -357,9 +357,12 @@ K2T_API uint64_t k2t_msbfs_work_bytes(const k2t_tree *t);
  * asynchronous on `stream`, allocates nothing and writes only its outputs and
  * `work`.  The first 4 bytes of an attention call's `work` are its device
  * status word: a kernel sets K2T_STATUS_WAIT_TIMEOUT there when a bounded wait
- * ran out (outputs are then undefined) and never clears it; a caller that
- * wants to know zeroes the word beforehand and reads it after the stream.  A work buffer may be shared by calls that are ordered on the GPU.
- * Results do not depend on the order in which blocks run.                    */
+ * ran out (outputs are then undefined, and the call itself has long returned
+ * K2T_OK) and never clears it; a caller that wants to know zeroes the word
+ * beforehand and reads it after the stream.  A work buffer may be shared by
+ * calls that are ordered on the GPU.  Results do not depend on the order in
+ * which blocks run.  These kernels have no bounds-tested form:
+ * libk2t_checked.so exports the same ones.                                  */
 
 /* Element types. */
 #define K2T_BF16 0
@@ -384,7 +387,10 @@ K2T_API uint64_t k2t_msbfs_work_bytes(const k2t_tree *t);
  * lse = -inf and no gradient.  Sums and softmax statistics are fp32; the
  * weights are rounded to the element type before they multiply v.
  * The states of a node that no query of the call sees (hops < 0 for every
- * column in use) are not used: they may hold anything, NaN included.
+ * column in use) are not used: they may hold anything, NaN included.  All
+ * others have to be numbers, like q and dout of every query: what is masked
+ * for one query only has a weight of 0 there, and 0 times NaN is NaN.  A
+ * query that is no number, or whose scores overflow, has out and lse NaN.
  * Strides are in elements; rows must be 16-byte aligned: base pointers
  * multiples of 16 bytes, strides and head_dim multiples of 8; strides are not
  * negative and below 2^38.  Inputs may be broadcast (stride 0); rows of out,

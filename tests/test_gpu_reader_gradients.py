@@ -211,3 +211,17 @@ def test_half_gradients_beside_values_that_do_not_count(T, n, hq, hkv, d, mapped
     least = 2.0 ** -25 * got["dq"].numel() ** 0.5 / float(want["dq"].norm())
     assert off(got["dq"], want["dq"]) <= 2.0 ** -10 + least, off(got["dq"], want["dq"])
     within("dbias", got["dbias"], want["dbias"], tol + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,low", [(1, -8.0), (1, -6.0), (8, -8.0), (20, -10.0)])
+def test_bias_gradient_of_a_bucket_of_little_weight(T, low, dtype):
+    """A bucket whose nodes have 2^-33 to 2^-39 of the weight of a row's largest each: its sum does not lose them."""
+    edges, n = list(range(9)), 65536
+    x = problem(T, n, 2, 2, 8, dtype, edges, seed=T, sources=min(T, 32))
+    x["bias"].zero_()
+    x["bias"][:, 0], x["bias"][:, 8] = 17.0, low
+    x["q"] *= 2.0 ** -4
+    x["dout"] *= 2.0 ** 13
+    want, tol = reference(x, dtype, edges)
+    within("dbias", call(x, dtype, edges)["dbias"], want["dbias"], tol + 2.0 ** -25)
