@@ -131,8 +131,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_delta_kernel(const __grid_
                         const uint32_t off = (kk >> 2) * S::kPanel + (kk & 3) * 32;
                         tc::mma_ss(lead, tm + x * 256 + w * 128, rows, off, nodes, off, id, kk > 0);
                     }
-                if (x) tc::commit(lead, &ctl->s_full[w]);
+                // the barrier that threads wait for last, so that no arrival is under way when the block ends
                 tc::commit(lead, &ctl->empty[slot]);
+                if (x) tc::commit(lead, &ctl->s_full[w]);
             }
         }
         if (!ok) tc::drain(lead, &ctl->drained, 0);
