@@ -44,6 +44,7 @@ namespace k2t {
 constexpr int kBwdThreads = 800;
 constexpr int kBwdRowThreads = 544;
 constexpr int kBwdRows = 32;
+constexpr float kWhole = 0x1p-10f;   // how far from 1 the sum of a row's weights may be: no more than this is lost in delta, less than out's rounding
 using Rest = __nv_bfloat16;      // what rounding took off a score gradient, in either type: where fp16 keeps nothing, this is all of it
 
 // What the kernels need of a row, made once by attn_rows_kernel: lse in units
@@ -55,38 +56,53 @@ struct RowInfo {
     uint32_t place[kBwdRows];              // column | head << 16
 };
 
-// delta of query t, head hd, by L neighbour lanes (x: this one of them): the sums over nodes that attn_delta_kernel left, or
-// dout . out without them; 0 for a query that does not exist or saw nothing.  up: ds_scale of the row.
+// dout . out of query t, head hd, by L neighbour lanes (x: this one of them).
+template <typename T, int L>
+__device__ __forceinline__ float dout_out(const AttnParams &p, uint32_t t, uint32_t hd, int x, uint32_t lanes)
+{
+    float s = 0.0f;
+    const T *o = static_cast<const T *>(p.out) + (int64_t)t * p.out_row + (int64_t)hd * p.out_head;
+    const T *d = static_cast<const T *>(p.dout) + (int64_t)t * p.dout_row + (int64_t)hd * p.dout_head;
+    for (uint32_t k = x * 8; k < p.d; k += L * 8) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(o + k)), b = __ldg(reinterpret_cast<const uint4 *>(d + k));
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 u = Elem<T>::unpack(aw[e]), v = Elem<T>::unpack(bw[e]);
+            s = fmaf(u.x, v.x, fmaf(u.y, v.y, s));
+        }
+    }
+    for (int y = L / 2; y; y >>= 1) s += __shfl_xor_sync(lanes, s, y);
+    return s;
+}
+
+// delta of query t, head hd, by L neighbour lanes (x: this one of them): from the sums over nodes that attn_delta_kernel left,
+// or dout . out without them; 0 for a query that does not exist or saw nothing.  up: ds_scale of the row.
+// The weights of a row sum to 1, but for the rounding of lse, unless its lse and out are of more nodes than this call's (nodes
+// taken in parts): what these nodes' sums lack is then in out.
 template <typename T, int L>
 __device__ __forceinline__ float row_delta(const AttnParams &p, uint32_t t, uint32_t hd, int x, uint32_t lanes, float &up)
 {
-    float top = 0.0f, s = 0.0f, m = p.delta_splits ? 0.0f : 1.0f / L;
+    float top = 0.0f, delta = 0.0f;
     if (t < p.T) {
         if (p.delta_splits) {
+            float s = 0.0f, m = 0.0f;
             for (uint32_t i = x; i < p.delta_splits; i += L) {
                 const uint64_t at = ((uint64_t)i * p.T + t) * p.hq + hd;
                 const float2 v = p.delta_part[at];
                 s += v.x, m += v.y;
                 if (Elem<T>::kUp) top = fmaxf(top, p.pdp_top[at]);
             }
-        } else {
-            const T *o = static_cast<const T *>(p.out) + (int64_t)t * p.out_row + (int64_t)hd * p.out_head;
-            const T *d = static_cast<const T *>(p.dout) + (int64_t)t * p.dout_row + (int64_t)hd * p.dout_head;
-            for (uint32_t k = x * 8; k < p.d; k += L * 8) {
-                const uint4 a = __ldg(reinterpret_cast<const uint4 *>(o + k)), b = __ldg(reinterpret_cast<const uint4 *>(d + k));
-                const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 u = Elem<T>::unpack(aw[e]), v = Elem<T>::unpack(bw[e]);
-                    s = fmaf(u.x, v.x, fmaf(u.y, v.y, s));
-                }
+            for (int y = L / 2; y; y >>= 1) {
+                s += __shfl_xor_sync(lanes, s, y);
+                m += __shfl_xor_sync(lanes, m, y);
+                if (Elem<T>::kUp) top = fmaxf(top, __shfl_xor_sync(lanes, top, y));
             }
+            delta = m == 0.0f ? 0.0f : fabsf(m - 1.0f) > kWhole ? dout_out<T, L>(p, t, hd, x, lanes) : s / m;
+        } else {
+            delta = dout_out<T, L>(p, t, hd, x, lanes);
         }
     }
-    for (int y = L / 2; y; y >>= 1) s += __shfl_xor_sync(lanes, s, y), m += __shfl_xor_sync(lanes, m, y);
-    if (Elem<T>::kUp)
-        for (int y = L / 2; y; y >>= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, y));
-    const float delta = m == 0.0f ? 0.0f : s / m;
     up = ds_scale<T>(top + fabsf(delta));
     return delta;
 }

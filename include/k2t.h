@@ -440,8 +440,10 @@ K2T_API int k2t_attn_forward(const k2t_attn *a, void *work, uint64_t work_bytes,
 /* dq, dk, dv and dbias from dout, the inputs, out and lse.  Gradients of a
  * key/value head sum over its query heads, of a bucket over queries and
  * nodes, in fp32.  Score gradients are p (dout . v - delta): with a bias table
- * delta is the weighted mean of dout . v, formed from the states in fp32 (out
- * is not read), else dout . out.  Errors as k2t_attn_forward. */
+ * or in fp16 delta is the weighted mean of dout . v, formed from the states in
+ * fp32, else dout . out.  out and lse may be of more nodes than the call's
+ * (nodes taken in parts, out and lse joined over them): delta is then
+ * dout . out.  Errors as k2t_attn_forward. */
 K2T_API int k2t_attn_backward(const k2t_attn *a, void *work, uint64_t work_bytes, void *stream);
 
 /* Layer norm of n_rows states of dim values, with the residual sum before it:

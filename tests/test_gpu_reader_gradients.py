@@ -225,3 +225,40 @@ def test_bias_gradient_of_a_bucket_of_little_weight(T, low, dtype):
     x["dout"] *= 2.0 ** 13
     want, tol = reference(x, dtype, edges)
     within("dbias", call(x, dtype, edges)["dbias"], want["dbias"], tol + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,hq,hkv,d,mapped,table", [(6, 4, 2, 64, False, True), (1, 2, 2, 128, False, True), (90, 4, 2, 64, True, True),
+                                                     (150, 2, 1, 96, True, True), (6, 4, 2, 64, False, False)])
+def test_nodes_in_parts(T, hq, hkv, d, mapped, table, dtype):
+    """Forward calls of parts of the nodes, their out and lse joined, and backward calls of the parts with the joined ones:
+    the gradients of all nodes at once, within a few roundings of the outputs (delta comes from a rounded out)."""
+    edges, n = list(range(9)), 3000
+    x = problem(T, n, hq, hkv, d, dtype, edges, seed=T, sources=min(T, 6), mapped=mapped)
+    if not table:
+        x["hops"] = x["bias"] = None
+    want, _ = reference(x, dtype, edges)
+    parts = [slice(0, 1000), slice(1000, 1100), slice(1100, n)]
+    outs, lses, ops = [], [], []
+    for s in parts:
+        m = s.stop - s.start
+        op = pkg.HopAttention(T, m, hq, hkv, d, DT[dtype], sources=x["hops"].shape[1] if table else 0, edges=edges if table else None)
+        out, lse = torch.empty_like(x["q"]), torch.empty(T, hq, device="cuda")
+        hops = x["hops"][s].contiguous() if table else None
+        op.forward(x["q"], x["k"][s], x["v"][s], out, lse, hops=hops, bias=x["bias"], query_source=x.get("source"))
+        outs.append(out.double()), lses.append(lse.double()), ops.append((op, hops))
+    lse = torch.logsumexp(torch.stack(lses), 0)
+    out = sum(o * torch.exp(l - lse)[..., None] for o, l in zip(outs, lses)).to(DT[dtype])
+    lse, dq, db = lse.float(), 0, 0
+    dk, dv = torch.empty_like(x["k"]), torch.empty_like(x["v"])
+    for s, (op, hops) in zip(parts, ops):
+        dqp, dbp = torch.empty_like(x["q"]), torch.empty_like(x["bias"]) if table else None
+        op.backward(x["dout"], x["q"], x["k"][s], x["v"][s], out, lse, dqp, dk[s], dv[s], dbias=dbp, hops=hops, bias=x["bias"],
+                    query_source=x.get("source"))
+        dq = dq + dqp.double()
+        db = db + dbp.double() if table else 0
+    got = dict(dq=dq, dk=dk.double(), dv=dv.double())
+    if table:
+        got["dbias"] = db
+    for name, g in got.items():
+        assert off(g, want[name]) <= 8 * U[dtype], (name, off(g, want[name]))
