@@ -94,10 +94,15 @@ def test_first_call_on_another_stream_than_the_current():
 @pytest.mark.parametrize("first", ["current", "side"])
 def test_buffers_of_an_object_that_goes_while_its_calls_run(first):
     """Memory that another stream still uses is not handed out again."""
+    for call in attention()[2:]:
+        call()                       # kernels are loaded
     op, t, fwd, bwd = attention()
-    norm = pkg.LayerNorm(4000, 512, torch.bfloat16)
+    warm, norm = (pkg.LayerNorm(4000, 512, torch.bfloat16) for _ in range(2))
     x, w = torch.randn(4000, 512, device="cuda").to(torch.bfloat16), torch.ones(512, dtype=torch.bfloat16, device="cuda")
     y, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty_like(w)
+    warm.forward(x, w, None, y)
+    warm.backward(x, x, w, dx, dw)
+    del warm
     side = torch.cuda.Stream()
 
     def call(stream):
