@@ -26,10 +26,11 @@ COMMON = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC,-O3,-fvisibilit
           "-I" + os.path.join(ROOT, "include")]
 SOURCES = ["k2t_host.cpp", "k2t_device.cu", "k2t_sr_plus_times.cu", "k2t_sr_boolean.cu", "k2t_sr_min_plus.cu",
            "k2t_static.cu", "k2t_product.cu", "k2t_attn.cu", "k2t_attn_bf16.cu", "k2t_attn_fp16.cu", "k2t_norm.cu",
-           "k2t_norm_ragged.cu"]
+           "k2t_norm_ragged.cu", "k2t_head_norm.cu", "k2t_cache.cu", "k2t_attn_cached.cu"]
 PROBE_SOURCES = [os.path.join("probe", "k2t_probe.cu")]
 HEADERS = ["k2t_internal.h", "k2t_kernels.cuh", "k2t_attn.cuh", "k2t_attn_fwd.cuh", "k2t_attn_bwd.cuh", "k2t_attn_delta.cuh",
-           "k2t_attn_launch.cuh", "k2t_norm.cuh", "k2t_tc.cuh", os.path.join("..", "..", "include", "k2t.h")]
+           "k2t_attn_launch.cuh", "k2t_attn_cached.cuh", "k2t_cache.cuh", "k2t_head_norm.cuh", "k2t_rows.h", "k2t_norm.cuh",
+           "k2t_tc.cuh", os.path.join("..", "..", "include", "k2t.h")]
 
 
 def _newest_input(sources) -> float:

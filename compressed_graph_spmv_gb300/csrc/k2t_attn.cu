@@ -1,7 +1,9 @@
 // k2t_attn.cu -- the attention calls of the C ABI: checks, plan, launch.
 #include <algorithm>
 
+#include "k2t_attn_cached.cuh"
 #include "k2t_attn_launch.cuh"
+#include "k2t_rows.h"
 
 namespace k2t {
 
@@ -9,6 +11,7 @@ int attn_forward_bf16(const AttnParams &p, int bm, cudaStream_t st);
 int attn_forward_fp16(const AttnParams &p, int bm, cudaStream_t st);
 int attn_backward_bf16(const AttnParams &p, cudaStream_t st);
 int attn_backward_fp16(const AttnParams &p, cudaStream_t st);
+int attn_cached(const CachedParams &p, uint32_t dtype, cudaStream_t st);
 
 namespace {
 
@@ -28,26 +31,6 @@ int check_sizes(const k2t_attn *a)
     for (uint32_t b = 0; b < a->n_buckets; ++b)
         if (b == 0 ? a->edges[0] != 0 : a->edges[b] <= a->edges[b - 1]) return K2T_EINVAL;
     return K2T_OK;
-}
-
-// Rows of 16-byte pieces, with pitches that a tensor map holds (40 bits of bytes).
-bool aligned(const void *p, int64_t row, int64_t head)
-{
-    return !((uintptr_t)p & 15u) && !(row & 7) && !(head & 7) && row >= 0 && head >= 0 && row < (1ll << 38) && head < (1ll << 38);
-}
-
-// Whether two rows of an output [rows, heads, d] share values: rows i apart and heads j apart the other way, |i row - j head| < d.
-bool overlaps(int64_t row, int64_t head, uint64_t rows, uint64_t heads, uint32_t d)
-{
-    using Wide = unsigned __int128;
-    if ((rows > 1 && row < d) || (heads > 1 && head < d)) return true;
-    if (rows < 2 || heads < 2) return false;
-    if (row >= (Wide)(heads - 1) * head + d || head >= (Wide)(rows - 1) * row + d) return false;     // one inside the other
-    for (uint64_t j = 1; j < heads; ++j) {
-        const Wide at = (Wide)j * head, i = at / row, left = at - i * row;
-        if ((i < rows && left < d) || (i + 1 < rows && row - left < d)) return true;
-    }
-    return false;
 }
 
 constexpr uint64_t kSms = 152;
@@ -166,24 +149,33 @@ int check_call(const k2t_attn *a, const void *work, bool backward)
 {
     const bool q = a->n_queries != 0, n = a->n_nodes != 0;
     if ((q && (!a->q || !a->out || !a->lse)) || (n && (!a->k || !a->v))) return K2T_EINVAL;
-    if (!aligned(a->q, a->q_row, a->q_head) || !aligned(a->k, a->k_row, a->k_head) ||
-        !aligned(a->v, a->v_row, a->v_head) || !aligned(a->out, a->out_row, a->out_head))
+    if (!rows_aligned(a->q, a->q_row, a->q_head) || !rows_aligned(a->k, a->k_row, a->k_head) ||
+        !rows_aligned(a->v, a->v_row, a->v_head) || !rows_aligned(a->out, a->out_row, a->out_head))
         return K2T_EINVAL;
     if (a->n_sources && n && !a->hops) return K2T_EINVAL;
     if ((a->n_buckets != 0) != (a->bias != nullptr)) return K2T_EINVAL;
     if (a->n_sources && !a->query_source && a->n_queries > a->n_sources) return K2T_ERANGE;
     if (!work || ((uintptr_t)work & 15u)) return K2T_EINVAL;
     const auto shared = [&](int64_t row, int64_t head, bool nodes) {
-        return overlaps(row, head, nodes ? a->n_nodes : a->n_queries, nodes ? a->n_kv_heads : a->n_heads, a->head_dim);
+        return rows_overlap(row, head, nodes ? a->n_nodes : a->n_queries, nodes ? a->n_kv_heads : a->n_heads, a->head_dim);
     };
     if (!backward) return a->n_queries && shared(a->out_row, a->out_head, false) ? K2T_EINVAL : K2T_OK;
     if ((q && (!a->dout || !a->dq)) || (n && (!a->dk || !a->dv)) || (a->n_buckets && !a->dbias)) return K2T_EINVAL;
-    if (!aligned(a->dout, a->dout_row, a->dout_head) || !aligned(a->dq, a->dq_row, a->dq_head) ||
-        !aligned(a->dk, a->dk_row, a->dk_head) || !aligned(a->dv, a->dv_row, a->dv_head))
+    if (!rows_aligned(a->dout, a->dout_row, a->dout_head) || !rows_aligned(a->dq, a->dq_row, a->dq_head) ||
+        !rows_aligned(a->dk, a->dk_row, a->dk_head) || !rows_aligned(a->dv, a->dv_row, a->dv_head))
         return K2T_EINVAL;
     if ((q && shared(a->dq_row, a->dq_head, false)) || (n && (shared(a->dk_row, a->dk_head, true) || shared(a->dv_row, a->dv_head, true))))
         return K2T_EINVAL;
     return K2T_OK;
+}
+
+// The cache in the place of keys and values: what check_call reads of them.
+k2t_attn over_cache(const k2t_attn *a, const k2t_cache *c)
+{
+    k2t_attn b = *a;
+    b.k = c->k, b.v = c->v;
+    b.k_row = b.k_head = b.v_row = b.v_head = 0;
+    return b;
 }
 
 void fill_pointers(const k2t_attn *a, void *work, Plan &pl)
@@ -240,6 +232,38 @@ int k2t_attn_forward(const k2t_attn *a, void *work, uint64_t work_bytes, void *s
     fill_pointers(a, work, pl);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return a->dtype == K2T_BF16 ? attn_forward_bf16(pl.p, pl.bm, st) : attn_forward_fp16(pl.p, pl.bm, st);
+}
+
+uint64_t k2t_cached_attn_work_bytes(const k2t_attn *a)
+{
+    if (check_sizes(a)) return 0;
+    Plan pl;
+    make_plan(a, false, pl);
+    // the most blocks that pick_splits gives the nodes of any part of the cache
+    const uint64_t rows = (uint64_t)a->n_queries * a->n_heads, blocks = (uint64_t)pl.p.hkv * pl.p.row_tiles;
+    const uint64_t most = std::min(std::min<uint64_t>(std::max<uint64_t>(1, pl.p.tiles), kSms), ((blocks + kSms - 1) / kSms + 8) * kSms / blocks);
+    pl.part_floats = most * rows * a->head_dim, pl.ml_floats = most * rows * 2;
+    return plan_bytes(pl);
+}
+
+int k2t_cached_attn_forward(const k2t_attn *a, const k2t_cache *c, void *work, uint64_t work_bytes, void *stream)
+{
+    int rc = check_sizes(a);
+    if (rc || (rc = check_cache(c))) return rc;
+    if (c->n_kv_heads != a->n_kv_heads || c->head_dim != a->head_dim) return K2T_EINVAL;
+    if (a->n_nodes > c->n_nodes) return K2T_ERANGE;
+    const k2t_attn b = over_cache(a, c);
+    Plan pl;
+    make_plan(&b, false, pl);
+    if ((rc = check_call(&b, work, false))) return rc;
+    if (work_bytes < plan_bytes(pl)) return K2T_ENOMEM;
+    if (a->n_queries == 0) return K2T_OK;
+    fill_pointers(&b, work, pl);
+    CachedParams p{};
+    static_cast<AttnParams &>(p) = pl.p;
+    p.pitch = cache_pitch(c->head_dim), p.scale_pitch = cache_scale_pitch(c->n_nodes), p.cached = c->n_nodes;
+    p.kc = static_cast<const uint8_t *>(c->k), p.vc = static_cast<const uint8_t *>(c->v), p.ks = c->k_scale, p.vs = c->v_scale;
+    return attn_cached(p, a->dtype, static_cast<cudaStream_t>(stream));
 }
 
 int k2t_attn_backward(const k2t_attn *a, void *work, uint64_t work_bytes, void *stream)

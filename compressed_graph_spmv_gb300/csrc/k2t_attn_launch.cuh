@@ -22,7 +22,7 @@ constexpr int kAttnMaxSmem = 232448;   // 227 KB
 
 // Programmatic launch: a kernel's blocks may be set up while the kernel before it on the stream (whichever that is) still
 // runs; they wait for its end (griddepcontrol.wait) before they touch global memory.
-template <typename K> int next_launch(K kernel, dim3 grid, int threads, size_t smem, const AttnParams &p, cudaStream_t st)
+template <typename K, typename P> int next_launch(K kernel, dim3 grid, int threads, size_t smem, const P &p, cudaStream_t st)
 {
     cudaLaunchConfig_t c{};
     c.gridDim = grid;
@@ -39,7 +39,7 @@ template <typename K> int next_launch(K kernel, dim3 grid, int threads, size_t s
 }
 
 // The shared memory a kernel may have is a setting of the kernel on a device: raised once, to what any call can need.
-template <auto kernel> int attn_launch(dim3 grid, int threads, size_t smem, const AttnParams &p, cudaStream_t st)
+template <auto kernel, typename P> int attn_launch(dim3 grid, int threads, size_t smem, const P &p, cudaStream_t st)
 {
     static std::atomic<uint64_t> set{0};
     int dev = 0;

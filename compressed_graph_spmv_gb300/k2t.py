@@ -36,11 +36,15 @@ EXPORTED = ["k2t_default_opts", "k2t_build", "k2t_workspace_bytes", "k2t_upload"
             "k2t_spmv_noalloc", "k2t_noalloc_scratch_limit", "k2t_msbfs",
             "k2t_msbfs_work_bytes", "k2t_bool_product", "k2t_bool_closure", "k2t_status",
             "k2t_attn_work_bytes", "k2t_attn_forward", "k2t_attn_backward",
-            "k2t_norm_work_bytes", "k2t_norm_forward", "k2t_norm_backward"]
+            "k2t_norm_work_bytes", "k2t_norm_forward", "k2t_norm_backward",
+            "k2t_head_rates", "k2t_head_norm_work_bytes", "k2t_head_norm_forward", "k2t_head_norm_backward",
+            "k2t_cache_write", "k2t_cache_read", "k2t_cached_attn_work_bytes", "k2t_cached_attn_forward"]
 
 BF16, FP16, FP32 = 0, 1, 2
 ATTN_MAX_BUCKETS, ATTN_MAX_HOP, ATTN_MAX_NODES = 64, 255, 0x7fffff00
 NORM_FORM_STATS = 1
+HEAD_MAX_DIM, HEAD_PAIRED = 256, 1
+CACHE_BLOCK = 32
 
 
 class Opts(ctypes.Structure):
@@ -94,6 +98,27 @@ class Norm(ctypes.Structure):
                 ("eps", ctypes.c_float), ("flags", ctypes.c_uint32)] + \
         [(name, ctypes.c_void_p) for name in ("x", "residual", "weight", "bias", "y", "z", "mean", "rstd",
                                               "dy", "dz", "dx", "dweight", "dbias")]
+
+
+class HeadNormArgs(ctypes.Structure):
+    """k2t_head_norm of include/k2t.h."""
+    _fields_ = [(name, ctypes.c_uint32) for name in ("dtype", "n_heads", "head_dim", "rotary_dim")] + \
+        [("n_rows", ctypes.c_uint64), ("eps", ctypes.c_float), ("flags", ctypes.c_uint32),
+         ("rates", ctypes.c_uint64 * (HEAD_MAX_DIM // 2))] + \
+        [(name, ctypes.c_void_p) for name in ("x", "weight", "positions", "y")] + \
+        [(name, ctypes.c_int64) for name in ("x_row", "x_head", "y_row", "y_head")] + \
+        [(name, ctypes.c_void_p) for name in ("dy", "dx", "dweight")] + \
+        [(name, ctypes.c_int64) for name in ("dy_row", "dy_head", "dx_row", "dx_head")]
+
+
+class Cache(ctypes.Structure):
+    """k2t_cache of include/k2t.h."""
+    _fields_ = [(name, ctypes.c_uint32) for name in ("dtype", "n_kv_heads", "head_dim", "reserved")] + \
+        [("n_nodes", ctypes.c_uint64)] + \
+        [(name, ctypes.c_void_p) for name in ("k", "v", "k_scale", "v_scale")] + \
+        [("first", ctypes.c_uint64), ("count", ctypes.c_uint64)] + \
+        [(name, ctypes.c_void_p) for name in ("nodes", "x_k", "x_v")] + \
+        [(name, ctypes.c_int64) for name in ("xk_row", "xk_head", "xv_row", "xv_head")]
 
 
 class K2TError(RuntimeError):
@@ -157,6 +182,15 @@ def load() -> ctypes.CDLL:
         for name, struct in (("k2t_attn_forward", Attn), ("k2t_attn_backward", Attn), ("k2t_norm_backward", Norm)):
             getattr(lib, name).argtypes = [ctypes.POINTER(struct), P, U64, P]
             getattr(lib, name).restype = ctypes.c_int
+        H, C, A = (ctypes.POINTER(t) for t in (HeadNormArgs, Cache, Attn))
+        for name, args, res in (("k2t_head_rates", [ctypes.c_double, U32, P], ctypes.c_int),
+                                ("k2t_head_norm_work_bytes", [H], U64), ("k2t_head_norm_forward", [H, P], ctypes.c_int),
+                                ("k2t_head_norm_backward", [H, P, U64, P], ctypes.c_int),
+                                ("k2t_cache_write", [C, P], ctypes.c_int), ("k2t_cache_read", [C, P], ctypes.c_int),
+                                ("k2t_cached_attn_work_bytes", [A], U64),
+                                ("k2t_cached_attn_forward", [A, C, P, U64, P], ctypes.c_int)):
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = res
         for name in ("k2t_build", "k2t_workspace_bytes", "k2t_upload", "k2t_spmv", "k2t_spmv_marked",
                      "k2t_spmv_host",
                      "k2t_stats_get", "k2t_level_signatures", "k2t_device_level", "k2t_decode",

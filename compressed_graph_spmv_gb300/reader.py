@@ -1,6 +1,7 @@
 """The layers of a model that reads a graph, on device tensors: attention of
-queries to node states biased by hop distance, and layer norm of node states
-(``k2t_attn_*`` and ``k2t_norm_*`` of ``include/k2t.h``).
+queries to node states biased by hop distance, layer norm of node states, and
+the norm and rotation of each head of queries and keys (``k2t_attn_*``,
+``k2t_norm_*`` and ``k2t_head_*`` of ``include/k2t.h``).
 
 As in ``k2t.py``, argument marshalling only.  An object holds the sizes and
 the work buffer of one layer; its calls take tensors that the caller owns,
@@ -17,7 +18,8 @@ import math
 import struct
 import threading
 
-from .k2t import (ATTN_MAX_BUCKETS, ATTN_MAX_HOP, BF16, FP16, FP32, NORM_FORM_STATS, Attn, Norm, _check, _stream_ptr, load)
+from .k2t import (ATTN_MAX_BUCKETS, ATTN_MAX_HOP, BF16, FP16, FP32, HEAD_PAIRED, NORM_FORM_STATS, Attn, HeadNormArgs, Norm, _check,
+                  _stream_ptr, load)
 
 
 def hop_edges(n_buckets: int, max_hop: int = 64) -> list:
@@ -140,17 +142,9 @@ class _Placed:
         return device
 
 
-class HopAttention(_Placed):
-    """Attention of ``n_queries`` queries to the states of ``n_nodes`` nodes.
-
-    ``sources`` columns of a hop table (int32 [n_nodes, sources], as
-    ``Tree.msbfs`` leaves it: -1 masks a node) and ``edges``, the first hop of
-    each bucket of the bias table [n_heads, len(edges)]; ``sources`` 0 is plain
-    attention, no ``edges`` masks without a bias.  See ``k2t_attn``.
-
-    A call returns before its kernels have run: should a bounded wait in one of
-    them run out, the outputs are undefined and only ``status`` tells.
-    """
+class _Attention(_Placed):
+    """Sizes and work buffers of an attention; ``PASSES`` of them."""
+    PASSES = 2
 
     def __init__(self, n_queries: int, n_nodes: int, n_heads: int, n_kv_heads: int, head_dim: int, dtype,
                  sources: int = 0, edges=None, scale: float | None = None, device="cuda"):
@@ -177,14 +171,9 @@ class HopAttention(_Placed):
         self._source = torch.Size((n_queries,))
         self._table = torch.Size((n_heads, len(edges)))
         self._lib = load()
-        self._forward, self._backward = self._lib.k2t_attn_forward, self._lib.k2t_attn_backward
         self._current, self._here = _stream_getter(torch), _device_getter(torch)
-        self._buffers, self._bytes = [_Buffer(torch, device, self._current) for _ in range(2)], [0, 0]
+        self._buffers, self._bytes = [_Buffer(torch, device, self._current) for _ in range(self.PASSES)], [0] * self.PASSES
         self._lock = threading.Lock()      # of the struct and the buffers: ctypes lets other threads run during a call
-
-    def work_bytes(self, backward: bool = False) -> int:
-        """Device bytes of the work buffer of a pass (k2t_attn_work_bytes)."""
-        return int(self._lib.k2t_attn_work_bytes(self._ref, int(backward)))
 
     @property
     def _work(self):
@@ -199,7 +188,7 @@ class HopAttention(_Placed):
         return self._buffers[backward].get(size, self._current(device) if stream is None else stream, device, zeroed=4), size
 
     def status(self) -> int:
-        """The device status words of both passes, joined: waits for the device; 0, or
+        """The device status words of the passes, joined: waits for the device; 0, or
         ``k2t.STATUS_WAIT_TIMEOUT`` once a bounded wait ran out in a call of this object."""
         word = 0
         for work in self._work:
@@ -207,6 +196,28 @@ class HopAttention(_Placed):
                 self._torch.cuda.synchronize()
                 word |= int(work[:4].view(self._torch.int32).item())
         return word
+
+
+class HopAttention(_Attention):
+    """Attention of ``n_queries`` queries to the states of ``n_nodes`` nodes.
+
+    ``sources`` columns of a hop table (int32 [n_nodes, sources], as
+    ``Tree.msbfs`` leaves it: -1 masks a node) and ``edges``, the first hop of
+    each bucket of the bias table [n_heads, len(edges)]; ``sources`` 0 is plain
+    attention, no ``edges`` masks without a bias.  See ``k2t_attn``.
+
+    A call returns before its kernels have run: should a bounded wait in one of
+    them run out, the outputs are undefined and only ``status`` tells.
+    """
+
+    def __init__(self, n_queries: int, n_nodes: int, n_heads: int, n_kv_heads: int, head_dim: int, dtype,
+                 sources: int = 0, edges=None, scale: float | None = None, device="cuda"):
+        super().__init__(n_queries, n_nodes, n_heads, n_kv_heads, head_dim, dtype, sources, edges, scale, device)
+        self._forward, self._backward = self._lib.k2t_attn_forward, self._lib.k2t_attn_backward
+
+    def work_bytes(self, backward: bool = False) -> int:
+        """Device bytes of the work buffer of a pass (k2t_attn_work_bytes)."""
+        return int(self._lib.k2t_attn_work_bytes(self._ref, int(backward)))
 
     def _inputs(self, q, k, v, out, lse, hops, bias, query_source):
         a, dt, device = self._a, self.dtype, q.get_device()
@@ -370,3 +381,82 @@ _NONE = (0, 0)
 # flags and pointers of k2t_norm: up to rstd, and all
 _FORWARD, _BACKWARD, _AT_FORWARD = struct.Struct("=I8Q"), struct.Struct("=I13Q"), Norm.flags.offset
 assert _AT_FORWARD + _FORWARD.size == Norm.dy.offset and _AT_FORWARD + _BACKWARD.size == ctypes.sizeof(Norm)
+
+
+class HeadNorm(_Placed):
+    """RMS norm of each of ``n_heads`` heads of ``head_dim`` values of ``n_rows`` queries or keys, and their rotation by
+    position in the same pass (``k2t_head_norm``).
+
+    The first ``rotary_dim`` values of a head (all of them by default; 0: norm alone) turn in pairs, value i with
+    i + rotary_dim / 2 or, ``paired``, neighbours, by position times base^(-2 m / rotary_dim).  A backward call needs
+    the forward's input and nothing else of it.
+    """
+
+    def __init__(self, n_rows: int, n_heads: int, head_dim: int, dtype, rotary_dim: int | None = None, paired: bool = False,
+                 base: float = 10000.0, eps: float = 1e-6, device="cuda"):
+        import torch
+        self._torch = torch
+        self.dtype, self.device = dtype, device
+        a = self._a = HeadNormArgs()
+        a.dtype = _dtype_code(dtype, (BF16, FP16, FP32))
+        a.n_heads, a.head_dim, a.n_rows, a.eps, a.flags = n_heads, head_dim, n_rows, eps, HEAD_PAIRED if paired else 0
+        a.rotary_dim = head_dim if rotary_dim is None else rotary_dim
+        self._lib = load()
+        if self._lib.k2t_head_rates(base, a.rotary_dim, ctypes.cast(a.rates, ctypes.c_void_p)):
+            raise ValueError("rotary_dim must be even and at most 256, base at least 1 and finite")
+        self._ref = ctypes.byref(a)
+        self._buf = memoryview(a).cast("B")
+        self._shape, self._cols, self._one = torch.Size((n_rows, n_heads, head_dim)), torch.Size((head_dim,)), torch.Size((n_rows,))
+        self._int = torch.int32
+        self._forward, self._backward = self._lib.k2t_head_norm_forward, self._lib.k2t_head_norm_backward
+        self._current, self._here = _stream_getter(torch), _device_getter(torch)
+        self._work, self._bytes = _Buffer(torch, device, self._current), self.work_bytes()
+        self._lock = threading.Lock()
+
+    def work_bytes(self) -> int:
+        """Device bytes of the backward pass's work buffer (k2t_head_norm_work_bytes)."""
+        return int(self._lib.k2t_head_norm_work_bytes(self._ref))
+
+    def _inputs(self, x, weight, positions, device):
+        at, row, head = _rows("x", x, self._shape, self.dtype, device)
+        return (at, 0 if weight is None else _flat("weight", weight, self._cols, self.dtype, device),
+                0 if positions is None else _flat("positions", positions, self._one, self._int, device)), (row, head)
+
+    def forward(self, x, weight, y, positions=None, stream=None):
+        """y [n_rows, n_heads, head_dim] of x; weight [head_dim] or None, positions int32 [n_rows] (None: a row's number)."""
+        with self._lock:
+            device = x.get_device()
+            if device != self._on or device != self._here():
+                device = self._device_of("x", x)
+            (xp, wp, pp), (xr, xh) = self._inputs(x, weight, positions, device)
+            yp, yr, yh = _rows("y", y, self._shape, self.dtype, device)
+            _HEAD.pack_into(self._buf, _AT_HEAD, xp, wp, pp, yp, xr, xh, yr, yh, 0, 0, 0, 0, 0, 0, 0)
+            rc = self._forward(self._ref, self._current(device) if stream is None else _stream_ptr(stream))
+        if rc:
+            _check("k2t_head_norm_forward", rc)
+        return y
+
+    def backward(self, dy, x, weight, dx, dweight, positions=None, stream=None):
+        """dx and dweight (both None without a weight) from dy and the forward call's x and positions."""
+        with self._lock:
+            device = dy.get_device()
+            if device != self._on or device != self._here():
+                device = self._device_of("dy", dy)
+            (xp, wp, pp), (xr, xh) = self._inputs(x, weight, positions, device)
+            gp, gr, gh = _rows("dy", dy, self._shape, self.dtype, device)
+            dp, dr, dh = _rows("dx", dx, self._shape, self.dtype, device)
+            _HEAD.pack_into(self._buf, _AT_HEAD, xp, wp, pp, 0, xr, xh, 0, 0, gp, dp,
+                            0 if dweight is None else _flat("dweight", dweight, self._cols, self.dtype, device), gr, gh, dr, dh)
+            st = self._current(device) if stream is None else _stream_ptr(stream)
+            work = self._work
+            if wp and work.last != st:
+                work.get(max(16, self._bytes), st, device)
+            rc = self._backward(self._ref, work.at, self._bytes, st)
+        if rc:
+            _check("k2t_head_norm_backward", rc)
+        return dx, dweight
+
+
+# pointers and pitches of k2t_head_norm
+_HEAD, _AT_HEAD = struct.Struct("=4Q4q3Q4q"), HeadNormArgs.x.offset
+assert _AT_HEAD + _HEAD.size == ctypes.sizeof(HeadNormArgs)

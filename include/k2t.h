@@ -483,6 +483,113 @@ K2T_API int k2t_norm_forward(const k2t_norm *a, void *stream);
  * ENOMEM (work_bytes too small). */
 K2T_API int k2t_norm_backward(const k2t_norm *a, void *work, uint64_t work_bytes, void *stream);
 
+/* RMS norm of each head of queries or keys, with the rotation by position in
+ * the same pass.  For row i, head h and values j of the head:
+ *   u = weight[j] x[i,h,j] / sqrt(mean_j x^2 + eps)
+ *   y = u, with the first rotary_dim values turned in pairs (a, b) by the
+ *       angle f = 2 pi frac(positions[i] rates[m] / 2^64) of pair m:
+ *       a' = a cos f - b sin f,  b' = b cos f + a sin f
+ * Pair m is values m and m + rotary_dim / 2, with K2T_HEAD_PAIRED 2 m and
+ * 2 m + 1.  Rates are fractions of a turn for each position: k2t_head_rates
+ * gives base^(-2 m / rotary_dim) / (2 pi), and the angle is exact to 2^-32 of a
+ * turn however far the position.  Sums, angles and products are fp32 (squares
+ * above 3.4e38 overflow), results are rounded once.
+ * Strides are in elements, as k2t_attn's (base pointers multiples of 16 bytes,
+ * strides and head_dim multiples of 8).  Inputs may be broadcast (stride 0);
+ * rows of y and dx share no values.  y may be x, and dx may be dy or x, with
+ * the same strides.                                                         */
+#define K2T_HEAD_MAX_DIM   256
+#define K2T_HEAD_MAX_HEADS 65535
+#define K2T_HEAD_PAIRED    1
+typedef struct {
+    uint32_t dtype;            /* K2T_BF16, K2T_FP16 or K2T_FP32                                     */
+    uint32_t n_heads;          /* 1..65535                                                           */
+    uint32_t head_dim;         /* multiple of 8, 8..256                                              */
+    uint32_t rotary_dim;       /* even, 0 (no rotation) .. head_dim                                  */
+    uint64_t n_rows;           /* 0 or more, at most 2^32                                            */
+    float eps;                 /* positive                                                           */
+    uint32_t flags;            /* 0, or K2T_HEAD_PAIRED                                              */
+    uint64_t rates[K2T_HEAD_MAX_DIM / 2]; /* [rotary_dim / 2], in units of 2^-64 turns               */
+    const void *x;             /* [n_rows, n_heads, head_dim]                                        */
+    const void *weight;        /* [head_dim], 16-byte aligned; NULL: ones                            */
+    const int32_t *positions;  /* [n_rows]; NULL: a row's number                                     */
+    void *y;                   /* forward                                                            */
+    int64_t x_row, x_head, y_row, y_head;
+    /* backward: gradients of y, x and weight                                                         */
+    const void *dy;
+    void *dx, *dweight;        /* dweight exactly with weight                                        */
+    int64_t dy_row, dy_head, dx_row, dx_head;
+} k2t_head_norm;
+
+/* rates[m] = base^(-2 m / rotary_dim) / (2 pi) of a turn, for the rotary_dim / 2
+ * pairs.  EINVAL: rotary_dim odd or over K2T_HEAD_MAX_DIM, base below 1 or not
+ * finite. */
+K2T_API int k2t_head_rates(double base, uint32_t rotary_dim, uint64_t *rates);
+
+/* Bytes of `work` k2t_head_norm_backward needs with a weight; 0 for what it refuses. */
+K2T_API uint64_t k2t_head_norm_work_bytes(const k2t_head_norm *a);
+
+/* y.  Errors: EINVAL (null, misaligned, bad dtype or sizes, eps not positive,
+ * unknown flags, an output whose rows overlap), ERANGE (a limit above
+ * exceeded), ECUDA. */
+K2T_API int k2t_head_norm_forward(const k2t_head_norm *a, void *stream);
+
+/* dx and dweight from dy and the forward call's x.  dweight sums over rows and
+ * heads in fp32, in an order that does not change.  Errors as the forward
+ * call's, and ENOMEM (work_bytes too small). */
+K2T_API int k2t_head_norm_backward(const k2t_head_norm *a, void *work, uint64_t work_bytes, void *stream);
+
+/* Keys and values of a graph's nodes kept in 8 bits.  A value is e4m3 times a
+ * power of two for its block (nodes 32 b .. 32 b + 31) and head, kept as a byte
+ * s, 0..127: 2^(s - 64).  The cache is four buffers of the caller, which start
+ * out zero (a cache of zeros):
+ *   k, v              [n_kv_heads][n_nodes][pitch] bytes, pitch = head_dim
+ *                     rounded up to 16
+ *   k_scale, v_scale  [n_kv_heads][S] bytes, S = ceil(n_nodes / 32) rounded up
+ *                     to 16
+ * A write gives nodes [first, first + count) new states.  A block's scale is
+ * the least that holds the largest finite magnitude written (<= 448 2^(s - 64));
+ * where other nodes of the block stay, not less than it was, and where it
+ * grows they are rounded again.  Values are rounded to the nearest e4m3 (ties
+ * to even); magnitudes over 448 2^63 become that, those under 2^-74 zero, and
+ * what is not finite NaN.
+ * A read gives back nodes [first, first + count), or nodes[i] for i < count
+ * (zeros for one outside [0, n_nodes)), rounded to the element type: bf16 holds
+ * every value, fp16 those between 2^-24 and 65504.
+ * Writes of one cache are ordered on the GPU, by the caller, among each other
+ * and with what reads it.                                                   */
+#define K2T_CACHE_BLOCK 32
+typedef struct {
+    uint32_t dtype;            /* of x_k and x_v: K2T_BF16, K2T_FP16 or K2T_FP32                     */
+    uint32_t n_kv_heads;       /* 1..65535                                                           */
+    uint32_t head_dim;         /* multiple of 8, 8..128                                              */
+    uint32_t reserved;         /* 0                                                                  */
+    uint64_t n_nodes;          /* 0 or more, at most K2T_ATTN_MAX_NODES                              */
+    void *k, *v;               /* the cache, 16-byte aligned                                         */
+    uint8_t *k_scale, *v_scale;
+    /* a write or read */
+    uint64_t first, count;     /* first is 0 with nodes                                              */
+    const int32_t *nodes;      /* [count] (read only) or NULL                                        */
+    void *x_k, *x_v;           /* [count, n_kv_heads, head_dim]: written from, read into             */
+    int64_t xk_row, xk_head, xv_row, xv_head;   /* strides as k2t_attn's                             */
+} k2t_cache;
+
+/* Errors: EINVAL (null, misaligned, bad dtype or sizes, nodes given to a write,
+ * an output whose rows overlap), ERANGE (a limit exceeded, nodes past the
+ * cache's end), ECUDA. */
+K2T_API int k2t_cache_write(const k2t_cache *c, void *stream);
+K2T_API int k2t_cache_read(const k2t_cache *c, void *stream);
+
+/* k2t_attn_forward with the first a->n_nodes nodes of a cache in the place of
+ * a->k and a->v (which are not read, nor their strides): queries, hops, bias,
+ * masks and outputs as there.  Weights are rounded to fp16 before they
+ * multiply v, whatever the element type.  `work` may be of any n_nodes up to
+ * the one that k2t_cached_attn_work_bytes was asked about.  Errors as
+ * k2t_attn_forward; EINVAL where heads or head_dim are not the cache's, ERANGE
+ * where n_nodes is more than the cache's. */
+K2T_API uint64_t k2t_cached_attn_work_bytes(const k2t_attn *a);
+K2T_API int k2t_cached_attn_forward(const k2t_attn *a, const k2t_cache *c, void *work, uint64_t work_bytes, void *stream);
+
 /* Shape, per-level sizes and the device footprint broken down by part. */
 K2T_API int k2t_stats_get(const k2t_tree *t, k2t_stats *s);
 
