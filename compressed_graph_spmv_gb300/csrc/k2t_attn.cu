@@ -11,7 +11,7 @@ int attn_forward_bf16(const AttnParams &p, int bm, cudaStream_t st);
 int attn_forward_fp16(const AttnParams &p, int bm, cudaStream_t st);
 int attn_backward_bf16(const AttnParams &p, cudaStream_t st);
 int attn_backward_fp16(const AttnParams &p, cudaStream_t st);
-int attn_cached(const CachedParams &p, uint32_t dtype, cudaStream_t st);
+int attn_cached(const CachedParams &p, uint32_t dtype, int bm, cudaStream_t st);
 
 namespace {
 
@@ -59,7 +59,8 @@ struct Plan {
     uint64_t part_floats, ml_floats, info_floats, delta_floats;
 };
 
-void make_plan(const k2t_attn *a, bool backward, Plan &pl)
+// most: rows a block of the forward pass takes at most
+void make_plan(const k2t_attn *a, bool backward, Plan &pl, int most = 256)
 {
     AttnParams &p = pl.p;
     p = AttnParams{};
@@ -100,7 +101,7 @@ void make_plan(const k2t_attn *a, bool backward, Plan &pl)
     // rows per block: the fewest lanes that hold them all, since the states are read once per row block.  Measured, bf16:
     // 4 rows a head over 2^20 nodes 297 us, in 128 lanes 339; 39 rows over 100003 nodes (fp16) 26 us, in 128 lanes 30; 1024
     // rows over 16384 nodes 123 us, with one row tile a block 8% more.
-    pl.bm = p.rows <= 32 ? 32 : p.rows <= 64 ? 64 : p.rows <= 128 ? 128 : 256;
+    pl.bm = p.rows <= 32 ? 32 : p.rows <= 64 ? 64 : p.rows <= 128 ? 128 : most;
     p.row_tiles = std::max(1u, (p.rows + pl.bm - 1) / pl.bm);
     p.splits = pick_splits((uint64_t)p.hkv * p.row_tiles, p.tiles);
     pl.part_floats = p.splits > 1 ? p.splits * rows * p.d : 0;
@@ -238,7 +239,7 @@ uint64_t k2t_cached_attn_work_bytes(const k2t_attn *a)
 {
     if (check_sizes(a)) return 0;
     Plan pl;
-    make_plan(a, false, pl);
+    make_plan(a, false, pl, 128);
     // the most blocks that pick_splits gives the nodes of any part of the cache
     const uint64_t rows = (uint64_t)a->n_queries * a->n_heads, blocks = (uint64_t)pl.p.hkv * pl.p.row_tiles;
     const uint64_t most = std::min(std::min<uint64_t>(std::max<uint64_t>(1, pl.p.tiles), kSms), ((blocks + kSms - 1) / kSms + 8) * kSms / blocks);
@@ -254,7 +255,7 @@ int k2t_cached_attn_forward(const k2t_attn *a, const k2t_cache *c, void *work, u
     if (a->n_nodes > c->n_nodes) return K2T_ERANGE;
     const k2t_attn b = over_cache(a, c);
     Plan pl;
-    make_plan(&b, false, pl);
+    make_plan(&b, false, pl, 128);
     if ((rc = check_call(&b, work, false))) return rc;
     if (work_bytes < plan_bytes(pl)) return K2T_ENOMEM;
     if (a->n_queries == 0) return K2T_OK;
@@ -263,7 +264,7 @@ int k2t_cached_attn_forward(const k2t_attn *a, const k2t_cache *c, void *work, u
     static_cast<AttnParams &>(p) = pl.p;
     p.pitch = cache_pitch(c->head_dim), p.scale_pitch = cache_scale_pitch(c->n_nodes), p.cached = c->n_nodes;
     p.kc = static_cast<const uint8_t *>(c->k), p.vc = static_cast<const uint8_t *>(c->v), p.ks = c->k_scale, p.vs = c->v_scale;
-    return attn_cached(p, a->dtype, static_cast<cudaStream_t>(stream));
+    return attn_cached(p, a->dtype, pl.bm, static_cast<cudaStream_t>(stream));
 }
 
 int k2t_attn_backward(const k2t_attn *a, void *work, uint64_t work_bytes, void *stream)

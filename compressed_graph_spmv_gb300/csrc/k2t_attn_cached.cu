@@ -4,16 +4,28 @@
 
 namespace k2t {
 
-template <typename T> static int launch_cached(const CachedParams &p, cudaStream_t st)
+// bm: rows a block takes, 32, 64 or 128.
+template <typename T, int DP> static int cached_dim(const CachedParams &p, int bm, cudaStream_t st)
 {
-    if (int rc = next_launch(attn_cached_kernel<T>, dim3((unsigned)((uint64_t)p.T * p.hq), p.splits), 128, 0, p, st)) return rc;
-    if (p.splits == 1) return K2T_OK;
+    const dim3 grid(p.splits * p.row_tiles, p.hkv);
+    const size_t smem = CachedSmem<DP>::bytes(p);
+    switch (bm) {
+    case 32: return attn_launch<attn_cached_kernel<T, DP, 32>>(grid, kCachedThreads, smem, p, st);
+    case 64: return attn_launch<attn_cached_kernel<T, DP, 64>>(grid, kCachedThreads, smem, p, st);
+    default: return attn_launch<attn_cached_kernel<T, DP, 128>>(grid, kCachedThreads, smem, p, st);
+    }
+}
+
+template <typename T> static int launch_cached(const CachedParams &p, int bm, cudaStream_t st)
+{
+    const int rc = p.d <= 64 ? cached_dim<T, 64>(p, bm, st) : cached_dim<T, 128>(p, bm, st);
+    if (rc || p.splits == 1) return rc;
     return next_launch(attn_join_kernel<T>, dim3((unsigned)((uint64_t)p.T * p.hq)), 256, 0, static_cast<const AttnParams &>(p), st);
 }
 
-int attn_cached(const CachedParams &p, uint32_t dtype, cudaStream_t st)
+int attn_cached(const CachedParams &p, uint32_t dtype, int bm, cudaStream_t st)
 {
-    return dtype == K2T_BF16 ? launch_cached<__nv_bfloat16>(p, st) : launch_cached<__half>(p, st);
+    return dtype == K2T_BF16 ? launch_cached<__nv_bfloat16>(p, bm, st) : launch_cached<__half>(p, bm, st);
 }
 
 }  // namespace k2t
