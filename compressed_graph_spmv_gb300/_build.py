@@ -29,7 +29,7 @@ SOURCES = ["k2t_host.cpp", "k2t_device.cu", "k2t_sr_plus_times.cu", "k2t_sr_bool
            "k2t_norm_ragged.cu", "k2t_head_norm.cu", "k2t_cache.cu", "k2t_attn_cached.cu"]
 PROBE_SOURCES = [os.path.join("probe", "k2t_probe.cu")]
 HEADERS = ["k2t_internal.h", "k2t_kernels.cuh", "k2t_attn.cuh", "k2t_attn_fwd.cuh", "k2t_attn_bwd.cuh", "k2t_attn_delta.cuh",
-           "k2t_attn_launch.cuh", "k2t_attn_cached.cuh", "k2t_cache.cuh", "k2t_head_norm.cuh", "k2t_rows.h", "k2t_norm.cuh",
+           "k2t_attn_launch.cuh", "k2t_attn_cached.cuh", "k2t_attn_few.cuh", "k2t_cache.cuh", "k2t_head_norm.cuh", "k2t_rows.h", "k2t_norm.cuh",
            "k2t_tc.cuh", os.path.join("..", "..", "include", "k2t.h")]
 
 

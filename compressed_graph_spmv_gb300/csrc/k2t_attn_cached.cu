@@ -1,5 +1,6 @@
 // k2t_attn_cached.cu -- launches of the attention over the 8-bit cache.
 #include "k2t_attn_cached.cuh"
+#include "k2t_attn_few.cuh"
 #include "k2t_attn_launch.cuh"
 
 namespace k2t {
@@ -16,9 +17,18 @@ template <typename T, int DP> static int cached_dim(const CachedParams &p, int b
     }
 }
 
+template <typename T> static int few_rows(const CachedParams &p, cudaStream_t st)
+{
+    const dim3 grid(p.splits, p.hkv);
+    const size_t smem = FewSmem::bytes(p);
+    if (p.rows <= 4) return attn_launch<attn_few_kernel<T, 4>>(grid, kFewThreads, smem, p, st);
+    if (p.rows <= 8) return attn_launch<attn_few_kernel<T, 8>>(grid, kFewThreads, smem, p, st);
+    return attn_launch<attn_few_kernel<T, 16>>(grid, kFewThreads, smem, p, st);
+}
+
 template <typename T> static int launch_cached(const CachedParams &p, int bm, cudaStream_t st)
 {
-    const int rc = p.d <= 64 ? cached_dim<T, 64>(p, bm, st) : cached_dim<T, 128>(p, bm, st);
+    const int rc = p.rows <= kFewRows ? few_rows<T>(p, st) : p.d <= 64 ? cached_dim<T, 64>(p, bm, st) : cached_dim<T, 128>(p, bm, st);
     if (rc || p.splits == 1) return rc;
     return next_launch(attn_join_kernel<T>, dim3((unsigned)((uint64_t)p.T * p.hq)), 256, 0, static_cast<const AttnParams &>(p), st);
 }

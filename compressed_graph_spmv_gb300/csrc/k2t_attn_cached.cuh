@@ -91,6 +91,10 @@ __device__ __forceinline__ float2 from_e5m2(uint32_t two)
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
+// Byte offset of chunk c of row r in a slot of values: odd rows of 128 bytes have their halves exchanged, so that the eight
+// lanes that read four chunks of two rows meet no bank twice.
+template <int DP> __device__ __forceinline__ uint32_t value_chunk(uint32_t r, uint32_t c) { return r * DP + (DP == 128 ? c ^ (r & 1) << 2 : c) * 16; }
+
 // States of a tile's seen nodes -> slots, keys then values; this warp brings nodes [32 cw, 32 cw + 32).
 template <int DP, typename Ctl>
 __device__ __forceinline__ void cached_node_warps(const CachedParams &p, Ctl *ctl, uint32_t sm, int cw, int lane, uint32_t hk,
@@ -98,34 +102,34 @@ __device__ __forceinline__ void cached_node_warps(const CachedParams &p, Ctl *ct
 {
     using S = CachedSmem<DP>;
     constexpr int C = DP / 16, RP = 32 / C;                    // chunks of 16 bytes a row, rows a pass
+    constexpr int kTurn = 8 / RP;                              // passes until the key slots' swizzle repeats
     const uint32_t c = lane % C, r0 = cw * 32 + lane / C, chunks = p.pitch / 16, fill = (chunks + 1) & ~1u;
-    const uint64_t head = (uint64_t)hk * p.cached * p.pitch;
+    uint32_t k_at[kTurn];
+#pragma unroll
+    for (int k = 0; k < kTurn; ++k) k_at[k] = sm + S::kK + (r0 + k * RP) * 128 + ((c ^ ((r0 + k * RP) & 7)) << 4) - k * RP * 128;
+    const uint32_t v_at = sm + S::kV + value_chunk<DP>(r0, c);   // RP is even: the same for all of a lane's rows
+    const uint64_t first = (uint64_t)hk * p.cached * p.pitch + ((uint64_t)split * kTcTile + r0) * p.pitch + c * 16;
+    const uint32_t step = RP * p.pitch;
+    const uint64_t stride = (uint64_t)p.splits * kTcTile * p.pitch;
+    const uint8_t *kc = p.kc + first, *vc = p.vc + first;
     bool ok = true;
-    for (uint32_t i = 0; i < tiles && ok; ++i) {
+    for (uint32_t i = 0; i < tiles && ok; ++i, kc += stride, vc += stride) {
         const uint32_t buf = i % S::kBufs, ks = i % S::kKeys, vs = i % S::kValues;
         ok = __all_sync(~0u, tc::bar_wait(&ctl->hop_full[buf], (i / S::kBufs) & 1, gave_up));
         if (!ok) break;
+        // a node that no query sees, or past n, or a chunk past the row: zeros, and nothing is read
         const uint32_t seen = c < chunks ? ctl->seen[buf][cw] >> (lane / C) : 0;
-        const uint64_t at = head + ((split + (uint64_t)i * p.splits) * kTcTile + r0) * p.pitch + c * 16;
         if (i >= S::kKeys) ok = __all_sync(~0u, tc::bar_wait(&ctl->k_empty[ks], (i / S::kKeys - 1) & 1, gave_up));
         if (!ok) break;
         if (c < fill) {
 #pragma unroll
-            for (int k = 0; k < 32 / RP; ++k) {
-                const uint32_t r = r0 + k * RP;
-                // a node that no query sees, or past n, or a chunk past the row: zeros, and nothing is read
-                const bool on = seen >> (k * RP) & 1;
-                cp16(sm + S::kK + ks * S::kTile + r * 128 + ((c ^ (r & 7)) << 4), p.kc + (on ? at + (uint64_t)k * RP * p.pitch : 0), on ? 16 : 0);
-            }
+            for (int k = 0; k < 32 / RP; ++k) cp16(k_at[k % kTurn] + ks * S::kTile + k * RP * 128, kc + k * step, seen >> (k * RP) & 1 ? 16 : 0);
         }
         tc::cp_arrive(&ctl->k_full[ks]);
         if (i >= S::kValues) ok = __all_sync(~0u, tc::bar_wait(&ctl->v_empty[vs], (i / S::kValues - 1) & 1, gave_up));
         if (!ok) break;
 #pragma unroll
-        for (int k = 0; k < 32 / RP; ++k) {
-            const bool on = seen >> (k * RP) & 1;
-            cp16(sm + S::kV + vs * S::kValueSlot + (r0 + k * RP) * DP + c * 16, p.vc + (on ? at + (uint64_t)k * RP * p.pitch : 0), on ? 16 : 0);
-        }
+        for (int k = 0; k < 32 / RP; ++k) cp16(v_at + vs * S::kValueSlot + k * RP * DP, vc + k * step, seen >> (k * RP) & 1 ? 16 : 0);
         tc::cp_arrive(&ctl->v_full[vs]);
     }
     cp_commit();
@@ -137,25 +141,25 @@ template <int DP, typename Ctl>
 __device__ __forceinline__ void widen_warps(Ctl *ctl, uint8_t *smem, int tid, uint32_t tiles, volatile uint32_t *gave_up)
 {
     using S = CachedSmem<DP>;
-    constexpr int C = DP / 16, R = 128 / C;
-    const uint32_t c = tid % C, r0 = tid / C;
-    const uint32_t flip = DP == 128 ? c >> 2 : 0;               // the two panels' chunks in turn: eight lanes meet no bank twice
+    const uint32_t c0 = tid % 4, r0 = tid / 4;                  // four chunks of 32 rows a pass
     for (uint32_t i = 0; i < tiles; ++i) {
         const uint32_t vs = i % S::kValues, ws = i % S::kWide;
         bool ok = tc::bar_wait(&ctl->v_full[vs], (i / S::kValues) & 1, gave_up);
         if (ok && i >= S::kWide) ok = tc::bar_wait(&ctl->w_empty[ws], (i / S::kWide - 1) & 1, gave_up);
         if (!__all_sync(~0u, ok)) break;
-        const uint8_t *from = smem + S::kV + vs * S::kValueSlot + r0 * DP + c * 16;
-        uint8_t *to = smem + S::kWideAt + ws * S::kWideSlot;
-        const uint32_t at0 = tc::chunk(r0, 2 * c + flip, S::kTile), at1 = tc::chunk(r0, 2 * c + (flip ^ 1), S::kTile);
 #pragma unroll
-        for (int k = 0; k < C; ++k) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(from + k * R * DP);
-            const uint4 lo = make_uint4(from_e4m3(u.x & 0xffffu), from_e4m3(u.x >> 16), from_e4m3(u.y & 0xffffu), from_e4m3(u.y >> 16));
-            const uint4 hi = make_uint4(from_e4m3(u.z & 0xffffu), from_e4m3(u.z >> 16), from_e4m3(u.w & 0xffffu), from_e4m3(u.w >> 16));
-            // R is a multiple of 8 rows: the swizzle repeats
-            *reinterpret_cast<uint4 *>(to + at0 + k * R * 128) = flip ? hi : lo;
-            *reinterpret_cast<uint4 *>(to + at1 + k * R * 128) = flip ? lo : hi;
+        for (int h = 0; h < DP / 64; ++h) {                     // chunks 4 h .. 4 h + 3 are one panel
+            const uint8_t *from = smem + S::kV + vs * S::kValueSlot + value_chunk<DP>(r0, c0 + 4 * h);
+            uint8_t *to = smem + S::kWideAt + ws * S::kWideSlot + h * S::kTile;
+            const uint32_t at0 = tc::chunk(r0, 2 * c0, 0), at1 = tc::chunk(r0, 2 * c0 + 1, 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {                       // 32 rows on, the swizzle is the same
+                const uint4 u = *reinterpret_cast<const uint4 *>(from + k * 32 * DP);
+                *reinterpret_cast<uint4 *>(to + at0 + k * 32 * 128) =
+                    make_uint4(from_e4m3(u.x & 0xffffu), from_e4m3(u.x >> 16), from_e4m3(u.y & 0xffffu), from_e4m3(u.y >> 16));
+                *reinterpret_cast<uint4 *>(to + at1 + k * 32 * 128) =
+                    make_uint4(from_e4m3(u.z & 0xffffu), from_e4m3(u.z >> 16), from_e4m3(u.w & 0xffffu), from_e4m3(u.w >> 16));
+            }
         }
         tc::fence_async();
         __syncwarp();
@@ -163,54 +167,63 @@ __device__ __forceinline__ void widen_warps(Ctl *ctl, uint8_t *smem, int tid, ui
     }
 }
 
-// Queries -> three e5m2 terms; lane l holds row row0 + l % KW.  Eight threads a row, 16 values each.
+// Row `row` of the queries as three e5m2 terms, tiles of 128-byte rows `next` bytes apart, its row `l` of them; this thread's
+// are values [16 c, 16 c + 16), and a warp's are those of four rows.  Returns what multiplies the row's scores.
+template <typename T>
+__device__ __forceinline__ float query_terms_of(const CachedParams &p, uint32_t row, uint32_t c, uint32_t hk, uint8_t *to, uint32_t next, uint32_t l)
+{
+    float x[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+    if (row < p.rows && c * 16 < p.d) {
+        const uint32_t t = row / p.group, g = row - t * p.group;
+        const T *src = static_cast<const T *>(p.q) + (int64_t)t * p.q_row + (int64_t)(hk * p.group + g) * p.q_head + c * 16;
+        Eight<T> a;
+        a.load(src);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = a.v[e];
+        if (c * 16 + 8 < p.d) {
+            a.load(src + 8);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[8 + e] = a.v[e];
+        }
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const uint32_t u = __float_as_uint(x[e]) & 0x7fffffffu;
+        top = max(top, u < 0x7f800000u ? u : 0);
+    }
+#pragma unroll
+    for (int o = 4; o; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+    const int e0 = min(max((int)(top >> 23) - 127 - 14, -112), 112);        // 2^14 <= largest < 2^15
+    const float down = power_of_two(-e0);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = fmaf(x[e], down, x[e] * 0.0f);      // an infinite value becomes NaN
+#pragma unroll
+    for (int term = 0; term < 3; ++term) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t a = to_e5m2(x[4 * e], x[4 * e + 1]), b = to_e5m2(x[4 * e + 2], x[4 * e + 3]);
+            w[e] = a | b << 16;
+            const float2 y = from_e5m2(a), z = from_e5m2(b);
+            x[4 * e] -= y.x, x[4 * e + 1] -= y.y, x[4 * e + 2] -= z.x, x[4 * e + 3] -= z.y;
+        }
+        *reinterpret_cast<uint4 *>(to + term * next + l * 128 + ((c ^ (l & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return p.scale_log2 * power_of_two(e0);
+}
+
+// Queries of a block; lane l holds row row0 + l % KW.  Eight threads a row.
 template <typename T, int DP, int KW, typename Ctl>
 __device__ __forceinline__ void query_terms(const CachedParams &p, Ctl *ctl, uint8_t *smem, int tid, uint32_t row0, uint32_t hk)
 {
     using S = CachedSmem<DP>;
     for (int i = tid; i < 128 * 8; i += kCachedThreads) {        // whole warps: the count is a multiple of 32
-        const uint32_t l = i / 8, c = i % 8, row = row0 + l % KW;
-        float x[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = 0.0f;
-        if (row < p.rows && c * 16 < p.d) {
-            const uint32_t t = row / p.group, g = row - t * p.group;
-            const T *src = static_cast<const T *>(p.q) + (int64_t)t * p.q_row + (int64_t)(hk * p.group + g) * p.q_head + c * 16;
-            Eight<T> a;
-            a.load(src);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = a.v[e];
-            if (c * 16 + 8 < p.d) {
-                a.load(src + 8);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[8 + e] = a.v[e];
-            }
-        }
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const uint32_t u = __float_as_uint(x[e]) & 0x7fffffffu;
-            top = max(top, u < 0x7f800000u ? u : 0);
-        }
-#pragma unroll
-        for (int o = 4; o; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
-        const int e0 = min(max((int)(top >> 23) - 127 - 14, -112), 112);        // 2^14 <= largest < 2^15
-        const float down = power_of_two(-e0);
-        if (c == 0) ctl->row_scale[l] = p.scale_log2 * power_of_two(e0);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = fmaf(x[e], down, x[e] * 0.0f);      // an infinite value becomes NaN
-#pragma unroll
-        for (int term = 0; term < 3; ++term) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t a = to_e5m2(x[4 * e], x[4 * e + 1]), b = to_e5m2(x[4 * e + 2], x[4 * e + 3]);
-                w[e] = a | b << 16;
-                const float2 y = from_e5m2(a), z = from_e5m2(b);
-                x[4 * e] -= y.x, x[4 * e + 1] -= y.y, x[4 * e + 2] -= z.x, x[4 * e + 3] -= z.y;
-            }
-            *reinterpret_cast<uint4 *>(smem + S::kQ + term * S::kTile + l * 128 + ((c ^ (l & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        const uint32_t l = i / 8;
+        const float scale = query_terms_of<T>(p, row0 + l % KW, i % 8, hk, smem + S::kQ, S::kTile, l);
+        if (i % 8 == 0) ctl->row_scale[l] = scale;
     }
 }
 
@@ -278,45 +291,40 @@ __global__ void __launch_bounds__(kCachedThreads, 1) attn_cached_kernel(const __
         const bool lead = tc::elect();
         const uint32_t id_s = idesc_e5m2_e4m3(kTcTile);
         const uint32_t dn = (p.d + 15) & ~15u, id_o = tc::idesc(false, dn, false, true);
-        // Scores run up to two tiles ahead of the outputs; whichever has its operands goes first.
-        uint32_t next = 0, done = 0;
-        tc::Patience wait(gave_up);
-        while (done < tiles) {
-            if (next < tiles && next < done + 2) {
-                const uint32_t w = next & 1, slot = next % S::kKeys;
-                if (__all_sync(~0u, tc::bar_peek(&ctl->k_full[slot], (next / S::kKeys) & 1))) {
-                    tc::fence_async();       // the copies were made by threads, the product reads through the async proxy
-                    tc::fence_after();
-                    const uint64_t k = tc::desc(sm + S::kK + slot * S::kTile, S::kTile);
+        // Scores run two tiles ahead of the outputs, in a fixed order: S of tile u + 2 takes the place of the weights of tile
+        // u, so that it follows their product anyway.
+        auto scores = [&](uint32_t u) {
+            const uint32_t slot = u % S::kKeys;
+            if (!__all_sync(~0u, tc::bar_wait(&ctl->k_full[slot], (u / S::kKeys) & 1, gave_up))) return false;
+            tc::fence_async();       // the copies were made by threads, the product reads through the async proxy
+            tc::fence_after();
+            const uint64_t k = tc::desc(sm + S::kK + slot * S::kTile, S::kTile);
 #pragma unroll
-                    for (uint32_t term = 0; term < 3; ++term) {
-                        const uint64_t q = tc::desc(sm + S::kQ + term * S::kTile, S::kTile);
+            for (uint32_t term = 0; term < 3; ++term) {
+                const uint64_t q = tc::desc(sm + S::kQ + term * S::kTile, S::kTile);
 #pragma unroll
-                        for (uint32_t kk = 0; kk < DP / 32; ++kk)
-                            if (kk * 32 < p.pitch) mma8_ss(lead, tm + w * 128, q + kk * 2, k + kk * 2, id_s, term + kk > 0);
-                    }
-                    tc::commit(lead, &ctl->s_full[w]);
-                    tc::commit(lead, &ctl->k_empty[slot]);
-                    ++next;
-                    wait.restart();
-                    continue;
-                }
+                for (uint32_t kk = 0; kk < DP / 32; ++kk)
+                    if (kk * 32 < p.pitch) mma8_ss(lead, tm + (u & 1) * 128, q + kk * 2, k + kk * 2, id_s, term + kk > 0);
             }
+            tc::commit(lead, &ctl->s_full[u & 1]);
+            tc::commit(lead, &ctl->k_empty[slot]);
+            return true;
+        };
+        bool ok = (tiles < 1 || scores(0)) && (tiles < 2 || scores(1));
+        uint32_t done = 0;
+        for (; ok && done < tiles; ++done) {
             const uint32_t w = done & 1, slot = done % S::kWide;
-            if (done < next && __all_sync(~0u, tc::bar_peek(&ctl->w_full[slot], (done / S::kWide) & 1) && tc::bar_peek(&ctl->p_full[w], (done >> 1) & 1))) {
-                tc::fence_async();
-                tc::fence_after();
-                const uint64_t v = tc::desc(sm + S::kWideAt + slot * S::kWideSlot, S::kTile);
+            ok = __all_sync(~0u, tc::bar_wait(&ctl->w_full[slot], (done / S::kWide) & 1, gave_up) && tc::bar_wait(&ctl->p_full[w], (done >> 1) & 1, gave_up));
+            if (!ok) break;
+            tc::fence_async();
+            tc::fence_after();
+            const uint64_t v = tc::desc(sm + S::kWideAt + slot * S::kWideSlot, S::kTile);
 #pragma unroll
-                for (uint32_t kk = 0; kk < kTcTile / 16; ++kk)
-                    tc::mma_ts(lead, tm + 256 + w * DP, tm + w * 128 + (kk >> 1) * 32 + (kk & 1) * 8, v, kk * 2048, id_o, done > 1 || kk > 0);
-                tc::commit(lead, &ctl->w_empty[slot]);
-                if (done + 2 >= tiles) tc::commit(lead, &ctl->o_full[w]);
-                ++done;
-                wait.restart();
-                continue;
-            }
-            if (!__all_sync(~0u, wait.more())) break;
+            for (uint32_t kk = 0; kk < kTcTile / 16; ++kk)
+                tc::mma_ts(lead, tm + 256 + w * DP, tm + w * 128 + (kk >> 1) * 32 + (kk & 1) * 8, v, kk * 2048, id_o, done > 1 || kk > 0);
+            tc::commit(lead, &ctl->w_empty[slot]);
+            if (done + 2 >= tiles) tc::commit(lead, &ctl->o_full[w]);
+            else ok = scores(done + 2);
         }
         if (done != tiles) tc::drain(lead, &ctl->drained, 0);
         __syncwarp();

@@ -217,11 +217,27 @@ def test_attention_matches(T, n, hq, hkv, d, sources, buckets, mapped, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("T,hq,hkv,d", [(1, 4, 4, 64), (20, 4, 1, 64), (2, 2, 2, 128), (32, 4, 2, 128), (150, 2, 1, 72)])
+@pytest.mark.parametrize("T,hq,hkv,d", [(1, 4, 4, 64), (20, 4, 1, 64), (4, 4, 1, 40), (7, 1, 1, 128), (30, 1, 1, 64), (2, 2, 2, 128), (32, 4, 2, 128), (150, 2, 1, 72)])
 def test_many_nodes(T, hq, hkv, d, dtype):
     p = problem(T, 6001, hq, hkv, d, min(T, 32), 9, dtype, T > 32, seed=T + d)
     cache, held = cached(p, dtype)
     check(held, dtype, ask(p, dtype, cache))
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "shuffled"])
+@pytest.mark.parametrize("T,G", [(1, 3), (2, 4), (3, 5), (20, 1), (16, 4), (130, 1)])
+def test_scores_that_rise(T, G, order):
+    """A row's largest score grows by some 2^10 in the weights from tile to tile, in others it falls: each block has many tiles."""
+    rng = np.random.default_rng(T)
+    n, hkv, d = 2900, 40, 32
+    p = problem(T, n, hkv * G, hkv, d, min(T, 32), 4, "fp16", T > 32, seed=T + G, reach=0.9)
+    rise = np.arange(n) / 128.0 * 7.0
+    rise = {"rising": rise, "falling": rise[::-1].copy(), "shuffled": rng.permutation(rise)}[order]
+    p["q"] *= 0.1
+    p["q"][:, :, 0] = torch.from_numpy(rng.choice([-1.0, 0.25, 1.0], size=(T, hkv * G))).cuda()
+    p["k"][:, :, 0] = torch.from_numpy(rise)[:, None].cuda()
+    cache, held = cached(p, "fp16")
+    check(held, "fp16", ask(p, "fp16", cache, scale=1.0), scale=1.0)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
