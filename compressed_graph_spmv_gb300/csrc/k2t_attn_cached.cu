@@ -21,14 +21,13 @@ template <typename T> static int few_rows(const CachedParams &p, cudaStream_t st
 {
     const dim3 grid(p.splits, p.hkv);
     const size_t smem = FewSmem::bytes(p);
-    if (p.rows <= 4) return attn_launch<attn_few_kernel<T, 4>>(grid, kFewThreads, smem, p, st);
-    if (p.rows <= 8) return attn_launch<attn_few_kernel<T, 8>>(grid, kFewThreads, smem, p, st);
-    return attn_launch<attn_few_kernel<T, 16>>(grid, kFewThreads, smem, p, st);
+    if (p.rows <= 4) return attn_launch<attn_few_kernel<T, 1>>(grid, FewPlan<1>::kAll, smem, p, st);
+    return attn_launch<attn_few_kernel<T, 2>>(grid, FewPlan<2>::kAll, smem, p, st);
 }
 
 template <typename T> static int launch_cached(const CachedParams &p, int bm, cudaStream_t st)
 {
-    const int rc = p.rows <= kFewRows ? few_rows<T>(p, st) : p.d <= 64 ? cached_dim<T, 64>(p, bm, st) : cached_dim<T, 128>(p, bm, st);
+    const int rc = p.rows <= 8 ? few_rows<T>(p, st) : p.d <= 64 ? cached_dim<T, 64>(p, bm, st) : cached_dim<T, 128>(p, bm, st);
     if (rc || p.splits == 1) return rc;
     return next_launch(attn_join_kernel<T>, dim3((unsigned)((uint64_t)p.T * p.hq)), 256, 0, static_cast<const AttnParams &>(p), st);
 }

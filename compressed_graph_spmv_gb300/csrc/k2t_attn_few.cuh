@@ -1,4 +1,4 @@
-// k2t_attn_few.cuh -- attention over the 8-bit cache for at most 16 rows of a
+// k2t_attn_few.cuh -- attention over the 8-bit cache for at most 8 rows of a
 // key/value head (a few queries at a time), on tcgen05 with the products
 // turned round.
 //
@@ -11,15 +11,15 @@
 //   O^T = V^T P   (head_dim x rows, nodes summed)
 // Both products read the cached bytes as they lie, keys and values alike as
 // the 8-bit A operand, and their cost goes with the few rows.  A query is
-// three e5m2 terms, as there.  A weight is four e5m2 terms, each of what the
-// ones before leave, 2^3 times larger, and each with columns of its own, so
-// that together they hold 2^-12 of a weight and what is 2^-41 of the largest;
-// the columns are put together in fp32 at the end.
+// three e5m2 terms, as there.  A weight is four such terms (three in a bf16
+// call), each of what the ones before leave, that hold it to 2^-12 (2^-9) and
+// what is 2^-32 of the largest; each has columns of its own, which are added in
+// fp32 at the end.
 //
-// A thread has a node, and its warp's 32 are one block of the cache: both its
-// scales are the warp's.  The reference m of a row's weights (a whole number
+// A thread has four rows of a node, and its warp's 32 nodes are one block of
+// the cache: both its scales are the warp's.  The reference m of a row's weights (a whole number
 // that trails the maximum of s + ev by at most 2^8) is the block's: tiles are
-// taken by two groups of threads in turn, and a group releases its tile's
+// taken by two or three groups of threads in turn, and a group releases its tile's
 // weights only when the one before has, so that whoever has to raise m does it
 // alone: it waits for the products so far, multiplies O by powers of two and
 // forms its weights again.  Whoever used the m of before does so too.
@@ -31,33 +31,45 @@
 
 namespace k2t {
 
-// Warps: 0-7 softmax (two groups), 8-11 hops -> bucket bytes, 12-15 states -> slots, 16 products.
-constexpr int kFewThreads = 544;
-constexpr int kFewRows = 16;              // rows of the score product
-constexpr int kFewTerms = 4;              // of a weight
+// Warps: softmax (three groups of four with up to 4 rows, two of eight with up to 8), four for states -> slots, two for products.
+template <int RS> struct FewPlan {
+    static constexpr int kGroups = RS == 1 ? 3 : 2, kThreads = 128 * RS;     // of a group
+    static constexpr int kSoft = kGroups * 4 * RS, kAll = (kSoft + 6) * 32;
+};
+constexpr int kFewRows = 16;              // columns of the score product, of which 8 at most are rows
+constexpr int kFewHops = 258;             // masked, hops 0 .. 255, no hop information
 
 struct FewSmem {
     static constexpr int kTile = kTcTile * 128;               // 128 rows of 128 bytes
-    static constexpr int kSlots = 9, kBufs = 4;               // keys and values alternate; bucket tiles
-    static constexpr int kP = kSlots * kTile;                 // weights of both groups
-    static constexpr int kQ = kP + 2 * kTile;                 // three terms of 16 rows of 128 bytes
-    static constexpr int kBuckets = kQ + 3 * kFewRows * 128;
-    static constexpr int kCtl = kBuckets + kBufs * 33 * kTcPitch;
-    struct Row { float scale; uint32_t at; };                 // what multiplies the row's scores; its column of bytes and head
+    static constexpr int kKeys = 4, kValues = 6;              // slots: keys are done with long before values
+    static constexpr int kV = kKeys * kTile;
+    static constexpr int kP = kV + kValues * kTile;           // weights of the groups, 128 rows of 32 bytes
+    static constexpr int kWeights = kTcTile * 32;
+    static constexpr int kQ = kP + 3 * kWeights;              // three terms of 16 rows of 128 bytes
+    static constexpr int kCtl = kQ + 3 * kFewRows * 128;
+    struct Row { float scale; int32_t col; uint32_t head, query; }; // what multiplies the row's scores; its column of hops or -1; 4 g; t
     struct Ctl {
-        uint64_t full[kSlots], empty[kSlots], hop_full[kBufs], hop_empty[kBufs];
-        uint64_t s_full[2], s_empty[2], p_full[2], p_done[2], token[2], drained;
-        uint32_t tmem, gave_up, columns, all, version, pad[3];
-        uint32_t seen[kBufs][4];
-        Row row[kFewRows];
-        float m[2][kFewRows];             // of this version and of the one before
-        float tops[4][kFewRows];
-        float sums[8][kFewRows];
-        uint8_t byte_of[257 + 15];
+        uint64_t k_full[kKeys], k_empty[kKeys], v_full[kValues], v_empty[kValues];
+        uint64_t s_full[3], s_empty[3], p_full[3], p_done[3], token[3], drained[2];
+        uint32_t tmem, gave_up, version, pad[1];
+        Row row[8];
+        float m[4][8];                    // of this version and of the three before
+        float tops[4][8];
+        float sums[16][4];
     };
     static constexpr int kLut = kCtl + (int)((sizeof(Ctl) + 15) / 16 * 16);
-    static size_t bytes(const AttnParams &p) { return kLut + kTcLutAlign + (size_t)(p.buckets + 2) * p.group2 * 4; }
+    // Tiles of hops, [query][node]: brought when the tile kKeys before has its slots, so that the tile another kValues before is
+    // done with.
+    static constexpr int kHopTiles = kKeys + kValues;
+    static __host__ __device__ uint32_t hops_at(const AttnParams &p) { return kLut + (kFewHops * p.group2 * 4 + 15) / 16 * 16; }
+    static size_t bytes(const AttnParams &p) { return hops_at(p) + (p.sources ? kHopTiles * p.T * kTcTile * 4 : 0); }
 };
+
+// Operand rows of 32 bytes (32-byte swizzle: the chunks of rows 4 to 7 of 8 are exchanged), K along the rows.
+__device__ __forceinline__ uint64_t desc32(uint32_t addr)
+{
+    return (uint64_t)((addr & 0x3ffff) >> 4) | (1ull << 16) | ((uint64_t)(256 >> 4) << 32) | (1ull << 46) | (6ull << 61);
+}
 
 // kind::f8f6f4 with fp32 accumulators, A e4m3, B e5m2, M = 128, N = n.
 __device__ __forceinline__ uint32_t idesc_e4m3_e5m2(uint32_t n, bool a_mn, bool b_mn)
@@ -65,120 +77,152 @@ __device__ __forceinline__ uint32_t idesc_e4m3_e5m2(uint32_t n, bool a_mn, bool 
     return (1u << 4) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// States of a tile's seen nodes -> slots, keys then values, both in the products' 128-byte rows.
+// States of a tile's seen nodes -> slots, keys then values, both in the products' 128-byte rows; warp cw of kKeys brings the
+// tiles cw, cw + kKeys, .. by itself (all warps a part of every tile were each held up by every tile's waits: 193 us for one
+// query over 2^20 nodes, 4 rows a head of 128).  The hops of its next tile come first: behind a full queue of loads they take
+// as long as the states.
 template <int C>
-__device__ __forceinline__ void few_node_warps(const CachedParams &p, FewSmem::Ctl *ctl, uint32_t sm, int cw, int lane, uint32_t hk,
+__device__ __forceinline__ void few_node_warps(const CachedParams &p, FewSmem::Ctl *ctl, uint8_t *smem, uint32_t sm, int cw, int lane, uint32_t hk,
                                                uint32_t tiles, uint32_t split, volatile uint32_t *gave_up)
 {
     using S = FewSmem;
     constexpr int RP = 32 / C, kTurn = 8 / RP;                 // rows a pass; passes until the swizzle repeats
-    const uint32_t c = lane % C, r0 = cw * 32 + lane / C, chunks = p.pitch / 16, fill = (chunks + 1) & ~1u;
+    const uint32_t c = lane % C, r0 = lane / C, chunks = p.pitch / 16, fill = (chunks + 1) & ~1u;
     uint32_t to[kTurn];
 #pragma unroll
     for (int k = 0; k < kTurn; ++k) to[k] = sm + (r0 + k * RP) * 128 + ((c ^ ((r0 + k * RP) & 7)) << 4) - k * RP * 128;
-    const uint64_t first = (uint64_t)hk * p.cached * p.pitch + ((uint64_t)split * kTcTile + r0) * p.pitch + c * 16;
     const uint32_t step = RP * p.pitch;
-    const uint64_t stride = (uint64_t)p.splits * kTcTile * p.pitch;
-    const uint8_t *kc = p.kc + first, *vc = p.vc + first;
-    uint32_t slot = 0, use = 0;
-    bool ok = true;
-    auto bring = [&](const uint8_t *src, uint32_t seen) {
-        if (use) ok = __all_sync(~0u, tc::bar_wait(&ctl->empty[slot], (use - 1) & 1, gave_up));
-        if (!ok) return;
+    const uint64_t head = (uint64_t)hk * p.cached * p.pitch + (uint64_t)r0 * p.pitch + c * 16;
+    bool all = !p.sources;                                     // a query that sees every node
+    for (uint32_t r = 0; r < p.rows; ++r) all |= ctl->row[r].col < 0;
+    const uint32_t T = p.sources ? p.T : 0, hop_tile = p.T * kTcTile * 4, hops_at = S::hops_at(p) + lane * 4;
+    auto bring_hops = [&](uint32_t i) {
+        if (i < tiles) {
+            const uint64_t node = (split + (uint64_t)i * p.splits) * kTcTile + lane;
+            const uint32_t at = sm + hops_at + i % S::kHopTiles * hop_tile;
+            for (uint32_t t = 0; t < T; ++t) {
+                const int32_t *src = p.hops + node * p.sources + max(ctl->row[t * p.group].col, 0);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at + (t * kTcTile + q * 32) * 4),
+                                 "l"(src + q * 32 * p.sources), "r"(node + q * 32 < p.n ? 4 : 0) : "memory");
+            }
+        }
+        cp_commit();
+    };
+    bring_hops(cw);
+    for (uint32_t i = cw, n = 0; i < tiles; i += S::kKeys, ++n) {
+        const uint64_t node = (split + (uint64_t)i * p.splits) * kTcTile;
+        const uint32_t vs = i % S::kValues, v_use = i / S::kValues;
+        // even lanes wait for the slot of the keys, odd ones for that of the values
+        const bool ok = lane & 1 ? !v_use || tc::bar_wait(&ctl->v_empty[vs], (v_use - 1) & 1, gave_up) : !n || tc::bar_wait(&ctl->k_empty[cw], (n - 1) & 1, gave_up);
+        if (!__all_sync(~0u, ok)) break;
+        if (n) cp_wait<1>();                                   // this tile's hops, which came before the last one's states
+        else cp_wait<0>();
+        __syncwarp();
+        // a node that no query sees, or past n, or a chunk past the row: zeros, and nothing is read
+        uint32_t seen[4];
+        int32_t most[4];                                       // the sign tells whether a query sees the node
+#pragma unroll
+        for (int q = 0; q < 4; ++q) most[q] = all ? 0 : -1;
+        const uint8_t *hops = smem + hops_at + i % S::kHopTiles * hop_tile;
+        for (uint32_t t = 0; t < T; ++t, hops += kTcTile * 4)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) most[q] = max(most[q], *reinterpret_cast<const int32_t *>(hops + q * 32 * 4));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            seen[q] = __ballot_sync(~0u, most[q] >= 0 && node + q * 32 + lane < p.n);
+            seen[q] = c < chunks ? seen[q] >> r0 : 0;
+        }
+        bring_hops(i + S::kKeys);
+        const uint8_t *kc = p.kc + head + node * p.pitch, *vc = p.vc + head + node * p.pitch;
         if (c < fill) {
 #pragma unroll
-            for (int k = 0; k < 32 / RP; ++k) cp16(to[k % kTurn] + slot * S::kTile + k * RP * 128, src + k * step, seen >> (k * RP) & 1 ? 16 : 0);
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int k = 0; k < 32 / RP; ++k, kc += step)
+                    cp16(to[k % kTurn] + cw * S::kTile + (q * 32 + k * RP) * 128, kc, seen[q] >> (k * RP) & 1 ? 16 : 0);
         }
-        tc::cp_arrive(&ctl->full[slot]);
-        if (++slot == S::kSlots) slot = 0, ++use;
-    };
-    for (uint32_t i = 0; i < tiles && ok; ++i, kc += stride, vc += stride) {
-        const uint32_t buf = i % S::kBufs;
-        ok = __all_sync(~0u, tc::bar_wait(&ctl->hop_full[buf], (i / S::kBufs) & 1, gave_up));
-        if (!ok) break;
-        // a node that no query sees, or past n, or a chunk past the row: zeros, and nothing is read
-        const uint32_t seen = c < chunks ? ctl->seen[buf][cw] >> (lane / C) : 0;
-        bring(kc, seen);
-        if (ok) bring(vc, seen);
+        tc::cp_arrive(&ctl->k_full[cw]);
+        if (c < fill) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int k = 0; k < 32 / RP; ++k, vc += step)
+                    cp16(to[k % kTurn] + S::kV + vs * S::kTile + (q * 32 + k * RP) * 128, vc, seen[q] >> (k * RP) & 1 ? 16 : 0);
+        }
+        tc::cp_arrive(&ctl->v_full[vs]);
+        cp_commit();
     }
-    cp_commit();
     cp_wait<0>();
 }
 
-// Whether any of a group's 128 threads says so; a barrier of theirs.
-__device__ __forceinline__ bool group_any(int w, bool yes)
+// Whether any of a group's N threads says so; a barrier of theirs.
+template <int N> __device__ __forceinline__ bool group_any(int w, bool yes)
 {
     uint32_t any;
     __syncwarp();
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.or.aligned.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(any) : "r"(w + 1), "r"((uint32_t)yes) : "memory");
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.or.aligned.pred q, %1, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any) : "r"(w + 1), "r"((uint32_t)yes), "n"(N) : "memory");
     return any;
 }
 
-template <int N> __device__ __forceinline__ void load_columns(uint32_t (&r)[N], uint32_t at)
-{
-    if constexpr (N == 16) {
-        tc::ld16(r, at);
-    } else {
-        uint32_t x[8];
-        tc::ld8(x, at);
-#pragma unroll
-        for (int i = 0; i < N; ++i) r[i] = x[i];
-    }
-}
-
-// T: queries, bias and outputs; NR: rows, 4, 8 or 16.
-template <typename T, int NR>
-__global__ void __launch_bounds__(kFewThreads, 1) attn_few_kernel(const __grid_constant__ CachedParams p)
+// T: queries, bias and outputs; up to 4 RS rows.
+template <typename T, int RS>
+__global__ void __launch_bounds__(FewPlan<RS>::kAll, 1) attn_few_kernel(const __grid_constant__ CachedParams p)
 {
     using S = FewSmem;
+    using Plan = FewPlan<RS>;
+    constexpr int kTerms = std::is_same<T, __half>::value ? 4 : 3;
+    constexpr uint32_t G = Plan::kGroups;
     extern __shared__ __align__(1024) uint8_t smem[];
     S::Ctl *ctl = reinterpret_cast<S::Ctl *>(smem + S::kCtl);
     const uint32_t sm = tc::saddr(smem);
-    const uint32_t lut_at = (sm + S::kLut + kTcLutAlign - 1) & ~(uint32_t)(kTcLutAlign - 1);
-    float *lut = reinterpret_cast<float *>(smem + (lut_at - sm));
+    float *lut = reinterpret_cast<float *>(smem + S::kLut);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t hk = blockIdx.y, split = blockIdx.x;
     const uint32_t tiles = (uint32_t)(split < p.tiles ? (p.tiles - split + p.splits - 1) / p.splits : 0);
     auto tile_at = [&](uint32_t i) { return split + (uint64_t)i * p.splits; };
-    constexpr uint32_t kO = 32, kON = kFewTerms * NR;          // columns of tensor memory: S of group w at 16 w, O behind
+    // Columns of tensor memory: S of group w at 48 w, [term][row]: a product takes as long for 16 columns as for 48 (64 clocks,
+    // its nodes' bytes), so that all terms are in one.  O behind, [row / 4][term][row % 4].
+    constexpr uint32_t kSN = 3 * kFewRows, kO = 3 * kSN, kON = 16 * RS;
 
     // ---- set-up ----
-    if (warp == 16) tc::alloc(&ctl->tmem, 128);
+    if (warp == Plan::kSoft + 4) tc::alloc(&ctl->tmem, 256);
     if (tid == 0) {
-        for (int i = 0; i < S::kSlots; ++i) tc::bar_init(&ctl->full[i], 128), tc::bar_init(&ctl->empty[i], 1);
-        for (int i = 0; i < S::kBufs; ++i) tc::bar_init(&ctl->hop_full[i], 4), tc::bar_init(&ctl->hop_empty[i], 4);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < S::kKeys; ++i) tc::bar_init(&ctl->k_full[i], 32), tc::bar_init(&ctl->k_empty[i], 1);
+        for (int i = 0; i < S::kValues; ++i) tc::bar_init(&ctl->v_full[i], 32), tc::bar_init(&ctl->v_empty[i], 1);
+        for (int i = 0; i < 3; ++i) {
             tc::bar_init(&ctl->s_full[i], 1);
-            tc::bar_init(&ctl->s_empty[i], 4);
+            tc::bar_init(&ctl->s_empty[i], 4 * RS);
             tc::bar_init(&ctl->p_full[i], 1);
             tc::bar_init(&ctl->p_done[i], 1);
             tc::bar_init(&ctl->token[i], 1);
         }
-        tc::bar_init(&ctl->drained, 1);
-        ctl->gave_up = ctl->columns = ctl->all = ctl->version = 0;
+        for (int i = 0; i < 2; ++i) tc::bar_init(&ctl->drained[i], 1);
+        ctl->gave_up = ctl->version = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (tid < kFewRows) ctl->m[0][tid] = -INFINITY;
-    if (p.sources)
-        for (int i = tid; i < 257; i += kFewThreads) ctl->byte_of[i] = i ? p.bucket_of[i - 1] + 1 : 0;
+    if (tid < 8) ctl->m[0][tid] = -INFINITY;
     tc::grid_wait();
-    fill_bias<T>(lut, p, hk, tid, p.group2);
+    for (uint32_t i = tid; i < kFewHops * p.group2; i += Plan::kAll) {     // bias in units of log2, by hops + 1 and head
+        const uint32_t b = i >> p.group2_log, g = i & (p.group2 - 1);
+        float v = b ? 0.0f : -INFINITY;
+        if (b && b < kFewHops - 1 && p.bias && g < p.group) {
+            v = Elem<T>::to_float(static_cast<const T *>(p.bias)[(uint64_t)(hk * p.group + g) * p.buckets + p.bucket_of[b - 1]]);
+            v = v <= Elem<T>::kMasked ? -INFINITY : v * kLog2e;
+        }
+        lut[i] = v;
+    }
     if (warp < 4) {                                            // queries: eight threads a row, 16 values each
         const uint32_t r = tid / 8, c = tid % 8;
         const float scale = query_terms_of<T>(p, r, c, hk, smem + S::kQ, kFewRows * 128, r);
-        if (c == 0) {
+        if (c == 0 && r < 8) {
             const uint32_t col = r < p.rows ? row_column(p, r) : 0;
-            ctl->row[r] = S::Row{scale, col * kTcPitch << 8 | (r < p.rows ? r % p.group : 0) * 4};
+            ctl->row[r] = S::Row{scale, col < p.sources ? (int32_t)col : -1, (r < p.rows ? r % p.group : 0) * 4, r < p.rows ? r / p.group : 0};
         }
     }
     tc::fence_async();
-    __syncthreads();
-    if (p.sources && tid < NR && (uint32_t)tid < p.rows) {
-        const uint32_t c = row_column(p, tid);
-        if (c < p.sources) atomicOr(&ctl->columns, 1u << c);
-        else ctl->all = 1;
-    }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -186,252 +230,237 @@ __global__ void __launch_bounds__(kFewThreads, 1) attn_few_kernel(const __grid_c
     const uint32_t tm = ctl->tmem;
     volatile uint32_t *gave_up = &ctl->gave_up;
 
-    if (warp >= 8 && warp < 12) {
-        hop_warps<S::kBufs>(p, ctl, smem + S::kBuckets, warp - 8, lane, tiles, split, gave_up);
-    } else if (warp >= 12 && warp < 16) {
-        if (p.pitch <= 64) few_node_warps<4>(p, ctl, sm, warp - 12, lane, hk, tiles, split, gave_up);
-        else few_node_warps<8>(p, ctl, sm, warp - 12, lane, hk, tiles, split, gave_up);
-    } else if (warp == 16) {
-        // ---- products: tile u belongs to group u & 1; scores two tiles ahead of the outputs ----
+    if (warp >= Plan::kSoft && warp < Plan::kSoft + 4) {
+        if (p.pitch <= 64) few_node_warps<4>(p, ctl, smem, sm, warp - Plan::kSoft, lane, hk, tiles, split, gave_up);
+        else few_node_warps<8>(p, ctl, smem, sm, warp - Plan::kSoft, lane, hk, tiles, split, gave_up);
+    } else if (warp == Plan::kSoft + 4) {
+        // ---- scores: tile u's go to group u mod G ----
         const bool lead = tc::elect();
-        const uint32_t id_s = idesc_e4m3_e5m2(kFewRows, false, false), id_o = idesc_e4m3_e5m2(kON, true, true);
-        auto scores = [&](uint32_t u) {
-            const uint32_t w = u & 1, item = 2 * u, slot = item % S::kSlots;
-            bool ok = u < 2 || tc::bar_wait(&ctl->s_empty[w], ((u >> 1) - 1) & 1, gave_up);
-            ok = ok && tc::bar_wait(&ctl->full[slot], (item / S::kSlots) & 1, gave_up);
-            if (!__all_sync(~0u, ok)) return false;
+        const uint32_t id = idesc_e4m3_e5m2(kSN, false, false);
+        uint32_t slot = 0, use = 0, u = 0, w = 0, turn = 0;
+        for (; u < tiles; ++u) {
+            // even lanes wait for the keys, odd ones for the group to have read its last scores
+            const bool odd = lane & 1;
+            const bool ok = odd ? !turn || tc::bar_wait(&ctl->s_empty[w], (turn - 1) & 1, gave_up) : tc::bar_wait(&ctl->k_full[slot], use & 1, gave_up);
+            if (!__all_sync(~0u, ok)) break;
+            __syncwarp();            // what one lane's wait has seen, for all of them
             tc::fence_async();       // the copies were made by threads, the product reads through the async proxy
             tc::fence_after();
             const uint64_t k = tc::desc(sm + slot * S::kTile, S::kTile);
+            const uint64_t q = tc::desc(sm + S::kQ, S::kTile);
 #pragma unroll
-            for (uint32_t term = 0; term < 3; ++term) {
-                const uint64_t q = tc::desc(sm + S::kQ + term * kFewRows * 128, S::kTile);
-#pragma unroll
-                for (uint32_t kk = 0; kk < 4; ++kk)
-                    if (kk * 32 < p.pitch) mma8_ss(lead, tm + w * 16, k + kk * 2, q + kk * 2, id_s, term + kk > 0);
-            }
+            for (uint32_t kk = 0; kk < 4; ++kk)
+                if (kk * 32 < p.pitch) mma8_ss(lead, tm + w * kSN, k + kk * 2, q + kk * 2, id, kk > 0);
             tc::commit(lead, &ctl->s_full[w]);
-            tc::commit(lead, &ctl->empty[slot]);
-            return true;
-        };
-        bool ok = (tiles < 1 || scores(0)) && (tiles < 2 || scores(1));
-        uint32_t done = 0;
-        while (ok && done < tiles) {
-            const uint32_t w = done & 1, item = 2 * done + 1, slot = item % S::kSlots;
-            if (done + 2 < tiles) ok = scores(done + 2);
-            ok = ok && tc::bar_wait(&ctl->full[slot], (item / S::kSlots) & 1, gave_up) && tc::bar_wait(&ctl->p_full[w], (done >> 1) & 1, gave_up);
-            if (!__all_sync(~0u, ok)) break;
-            tc::fence_async();
-            tc::fence_after();
-            const uint64_t v = tc::desc(sm + slot * S::kTile, S::kTile), q = tc::desc(sm + S::kP + w * S::kTile, S::kTile);
-#pragma unroll
-            for (uint32_t kk = 0; kk < kTcTile / 32; ++kk) mma8_ss(lead, tm + kO, v + kk * 256, q + kk * 256, id_o, done + kk > 0);
-            tc::commit(lead, &ctl->empty[slot]);
-            tc::commit(lead, &ctl->p_done[w]);
-            ++done;
+            tc::commit(lead, &ctl->k_empty[slot]);
+            if (++slot == S::kKeys) slot = 0, ++use;
+            if (++w == G) w = 0, ++turn;
         }
-        if (done != tiles) tc::drain(lead, &ctl->drained, 0);
+        if (u != tiles) tc::drain(lead, &ctl->drained[0], 0);
+        __syncwarp();
+    } else if (warp == Plan::kSoft + 5) {
+        // ---- outputs ----
+        const bool lead = tc::elect();
+        const uint32_t id = idesc_e4m3_e5m2(kON, true, true);
+        uint32_t slot = 0, use = 0, u = 0, w = 0, turn = 0;
+        for (; u < tiles; ++u) {
+            const bool ok = lane & 1 ? tc::bar_wait(&ctl->p_full[w], turn & 1, gave_up) : tc::bar_wait(&ctl->v_full[slot], use & 1, gave_up);
+            if (!__all_sync(~0u, ok)) break;
+            __syncwarp();            // what one lane's wait has seen, for all of them
+            tc::fence_async();       // the copies were made by threads, the product reads through the async proxy
+            tc::fence_after();
+            const uint64_t v = tc::desc(sm + S::kV + slot * S::kTile, S::kTile), q = desc32(sm + S::kP + w * S::kWeights);
+#pragma unroll
+            for (uint32_t kk = 0; kk < kTcTile / 32; ++kk) mma8_ss(lead, tm + kO, v + kk * 256, q + kk * 64, id, u + kk > 0);
+            tc::commit(lead, &ctl->p_done[w]);
+            tc::commit(lead, &ctl->v_empty[slot]);
+            if (++slot == S::kValues) slot = 0, ++use;
+            if (++w == G) w = 0, ++turn;
+        }
+        if (u != tiles) tc::drain(lead, &ctl->drained[1], 0);
         __syncwarp();
     } else {
-        // ---- softmax: thread = node of every other tile ----
-        const int w = warp >> 2, l = (warp & 3) * 32 + lane;
+        // ---- softmax: thread = four rows of a node of the group's tiles ----
+        const int w = warp / (4 * RS), rs = warp / 4 % RS, l = (warp & 3) * 32 + lane;
+        const bool first_thread = tid % Plan::kThreads == 0;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // lane field of this warp's tensor memory
-        const uint32_t shift = p.group2_log + 2;
+        const uint32_t shift = p.group2_log + 2, o_at = tm + lanes + kO + rs * 16;
         const uint8_t *ks = p.ks + hk * p.scale_pitch + (warp & 3), *vs = p.vs + hk * p.scale_pitch + (warp & 3);
-        float sum[NR], rest[NR];                                      // of the weights times 2^(kCachedUp - m)
+        const S::Row *rows = ctl->row + rs * 4;
+        uint8_t *const p_at = smem + S::kP + w * S::kWeights + l * 32 + ((rs ^ (l >> 2 & 1)) << 4);
+        float sum[4], rest[4], m[4], scale[4];                        // sums of the weights times 2^(kCachedUp - m)
+        uint32_t table_at[4];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) sum[r] = rest[r] = 0.0f;
+        for (int r = 0; r < 4; ++r) {
+            sum[r] = rest[r] = 0.0f, m[r] = -INFINITY, scale[r] = rows[r].scale;
+            table_at[r] = sm + S::kLut + rows[r].head;
+        }
         uint32_t version = 0, mine = 0;
         bool ok = true;
         int kb = 0, vb = 0;                                           // the next tile's scale bytes
-        auto scales = [&](uint32_t i) {
+        auto ahead = [&](uint32_t i) {
             if (i < tiles) kb = __ldg(ks + tile_at(i) * 4), vb = __ldg(vs + tile_at(i) * 4);
         };
-        // weights of the scores x against m, as terms into the group's part of P; sums onto `part`
-        auto release = [&](const float (&x)[NR], const float *m, int ev, float (&part)[NR]) {
-            uint32_t words[NR];
+        uint32_t hop_at[4];                                           // its hops, or none
 #pragma unroll
-            for (int r = 0; r < NR; r += 4) {
-                float y[4];
+        for (int r = 0; r < 4; ++r) hop_at[r] = rows[r].col < 0 ? 0 : S::hops_at(p) + (rows[r].query * kTcTile + l) * 4;
+        // weights of the scores x against m, as terms into the group's part of P; sums in `part`
+        auto release = [&](const float (&x)[4], int ev, float (&part)[4]) {
+            uint32_t words[4] = {0, 0, 0, 0};
+            float y[4];
+            const float back = power_of_two(-ev);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float ref = m[r + e];
-                    y[e] = ex2(x[r + e] - (ref == -INFINITY ? 0.0f : ref - kCachedUp));
-                    part[r + e] = y[e] * power_of_two(-ev);
-                }
-#pragma unroll
-                for (int term = 0; term < kFewTerms; ++term) {
-                    const uint32_t a = to_e5m2(y[0], y[1]), b = to_e5m2(y[2], y[3]);
-                    words[term * (NR / 4) + r / 4] = a | b << 16;
-                    const float2 c = from_e5m2(a), d = from_e5m2(b);
-                    y[0] = (y[0] - c.x) * 8.0f, y[1] = (y[1] - c.y) * 8.0f, y[2] = (y[2] - d.x) * 8.0f, y[3] = (y[3] - d.y) * 8.0f;
-                }
+            for (int r = 0; r < 4; ++r) {
+                y[r] = ex2(x[r] - (m[r] == -INFINITY ? 0.0f : m[r] - kCachedUp));
+                part[r] = y[r] * back;
             }
-            uint8_t *to = smem + S::kP + w * S::kTile + l * 128;
 #pragma unroll
-            for (int j = 0; j < NR / 4; ++j)
-                *reinterpret_cast<uint4 *>(to + ((j ^ (l & 7)) << 4)) = make_uint4(words[4 * j], words[4 * j + 1], words[4 * j + 2], words[4 * j + 3]);
+            for (int term = 0; term < kTerms; ++term) {
+                const uint32_t a = to_e5m2(y[0], y[1]), b = to_e5m2(y[2], y[3]);
+                words[term] = a | b << 16;
+                if (term + 1 == kTerms) break;
+                const float2 c = from_e5m2(a), d = from_e5m2(b);
+                y[0] -= c.x, y[1] -= c.y, y[2] -= d.x, y[3] -= d.y;
+            }
+            *reinterpret_cast<uint4 *>(p_at) = make_uint4(words[0], words[1], words[2], words[3]);
             tc::fence_async();
         };
-        // the sums from one version's m to another's
-        auto rescale = [&](const float *from, const float *to) {
+        // a version's m in the place of this thread's, whose sums follow; f: by what
+        auto adopt = [&](const float *next, float (&f)[4]) {
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                const float f = from[r] == -INFINITY ? 0.0f : ex2(from[r] - to[r]);
-                sum[r] *= f, rest[r] *= f;
+            for (int r = 0; r < 4; ++r) {
+                f[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - next[r]);
+                m[r] = next[r];
+                sum[r] *= f[r], rest[r] *= f[r];
             }
         };
-        scales(w);
-        for (uint32_t i = w; i < tiles; i += 2, ++mine) {
-            const uint32_t buf = i % S::kBufs;
+        ahead(w);
+        for (uint32_t i = w; i < tiles; i += G, ++mine) {
             const int ek = kb - kScaleBias, ev = vb - kScaleBias;
-            ok = tc::bar_wait(&ctl->hop_full[buf], (i / S::kBufs) & 1, gave_up) && tc::bar_wait(&ctl->s_full[w], mine & 1, gave_up);
+            float x[4], part[4];
+            const float pk = power_of_two(ek), fe = (float)ev;
+            ahead(i + G);
             // after a wait that ran out the warp goes on to the group's next vote, where all leave together
-            scales(i + 2);
-            tc::fence_after();
+            // even lanes wait for the scores (and the hops, which landed before the keys), odd ones for this part of P to be free
+            ok = lane & 1 ? mine == 0 || tc::bar_wait(&ctl->p_done[w], (mine - 1) & 1, gave_up) : tc::bar_wait(&ctl->s_full[w], mine & 1, gave_up);
+            ok = __all_sync(~0u, ok);
             __syncwarp();
-            uint32_t s[NR];
-            load_columns(s, tm + lanes + w * 16);
+            tc::fence_after();
+            const uint32_t hop_tile = i % S::kHopTiles * p.T * kTcTile * 4;
+            const bool in = tile_at(i) * kTcTile + l < p.n;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                uint32_t at = in ? kFewHops - 1 : 0;                  // no hop information, or masked
+                if (in && hop_at[r]) at = __viaddmax_s32(min(*reinterpret_cast<const int32_t *>(smem + hop_at[r] + hop_tile), 255), 1, 0);
+                x[r] = fe + table(table_at[r] + (at << shift));
+            }
+            uint32_t s[3][4];
+#pragma unroll
+            for (int term = 0; term < 3; ++term) tc::ld4(s[term], tm + lanes + w * kSN + term * kFewRows + rs * 4);
             tc::wait_ld();
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::bar_arrive(&ctl->s_empty[w]);
-            const bool plain = !p.sources && (tile_at(i) + 1) * kTcTile <= p.n;   // no table, no node past the end
-            const uint8_t *bt = smem + S::kBuckets + buf * 33 * kTcPitch + l;
-            const float pk = power_of_two(ek), fe = (float)ev;
-            float x[NR];
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                const S::Row row = ctl->row[r];
-                float bias = fe;
-                if (!plain) bias += table(((uint32_t)bt[row.at >> 8] << shift) | lut_at | (row.at & 255));
-                x[r] = fmaf(__uint_as_float(s[r]), row.scale * pk, bias);
-            }
-            __syncwarp();
-            if (lane == 0) tc::bar_arrive(&ctl->hop_empty[buf]);
-            const float *m = ctl->m[version & 1];
             bool grow = false;
 #pragma unroll
-            for (int r = 0; r < NR; ++r) grow |= x[r] > m[r] + kTcLag || (m[r] == -INFINITY && x[r] > -INFINITY);
-            ok = ok && (mine == 0 || tc::bar_wait(&ctl->p_done[w], (mine - 1) & 1, gave_up));        // this part of P is free
-            float part[NR];
-            release(x, m, ev, part);
+            for (int r = 0; r < 4; ++r) {
+                x[r] = fmaf(__uint_as_float(s[0][r]) + (__uint_as_float(s[1][r]) + __uint_as_float(s[2][r])), scale[r] * pk, x[r]);
+                grow |= x[r] > m[r] + kTcLag || (m[r] == -INFINITY && x[r] > -INFINITY);
+            }
+            release(x, ev, part);
             ok = ok && (i == 0 || tc::bar_wait(&ctl->token[w], (w ? mine : mine - 1) & 1, gave_up));
-            if (group_any(w, !ok || grow || *(volatile uint32_t *)&ctl->version != version)) {
-                ok = !group_any(w, !ok);
+            if (group_any<Plan::kThreads>(w, !ok || grow || *(volatile uint32_t *)&ctl->version != version)) {
+                ok = !group_any<Plan::kThreads>(w, !ok);
                 if (!ok) break;
-                const uint32_t now = *(volatile uint32_t *)&ctl->version;
-                if (now != version) rescale(m, ctl->m[now & 1]);
-                version = now, m = ctl->m[version & 1];
+                float f[4], next[4];
+                version = *(volatile uint32_t *)&ctl->version;
+                adopt(ctl->m[version & 3] + rs * 4, f);
                 // the tile's largest of each row
 #pragma unroll
-                for (int r = 0; r < NR; ++r) {
+                for (int r = 0; r < 4; ++r) {
                     float top = x[r];
 #pragma unroll
                     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-                    if (lane == 0) ctl->tops[warp & 3][r] = top;
+                    if (lane == 0) ctl->tops[warp & 3][rs * 4 + r] = top;
                 }
-                group_any(w, false);
+                group_any<Plan::kThreads>(w, false);
                 bool raise = false;
-                float f[NR], next[NR];
 #pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    const float top = fmaxf(fmaxf(ctl->tops[0][r], ctl->tops[1][r]), fmaxf(ctl->tops[2][r], ctl->tops[3][r]));
+                for (int r = 0; r < 4; ++r) {
+                    const float *t = &ctl->tops[0][rs * 4 + r], top = fmaxf(fmaxf(t[0], t[8]), fmaxf(t[16], t[24]));
                     const bool up = top > m[r] + kTcLag || (m[r] == -INFINITY && top > -INFINITY);
                     next[r] = up ? ceilf(top) : m[r];
-                    f[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - next[r]);
                     raise |= up;
                 }
-                if (raise) {                                           // the same in all of the group's threads
+                if (group_any<Plan::kThreads>(w, raise)) {
                     if (i > 0) {
-                        ok = tc::bar_wait(&ctl->p_done[w ^ 1], ((i - 1) >> 1) & 1, gave_up);     // O is at rest
+                        ok = tc::bar_wait(&ctl->p_done[(i - 1) % G], ((i - 1) / G) & 1, gave_up);     // O is at rest
                         tc::fence_after();
                     }
-                    if (group_any(w, !ok)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = !group_any<Plan::kThreads>(w, !ok);
+                    if (!ok) break;
+                    adopt(next, f);
                     if (i > 0) {
-#pragma unroll 1
-                        for (int term = 0; term < kFewTerms; ++term) {
-                            uint32_t o[NR < 8 ? 8 : NR];              // of four rows, two terms at a time
-                            const uint32_t at = tm + lanes + kO + term * NR;
-                            if (NR == 4 && (term & 1)) continue;
-                            load_columns(o, at);
-                            tc::wait_ld();
+                        uint32_t o[16];
+                        tc::ld16(o, o_at);
+                        tc::wait_ld();
 #pragma unroll
-                            for (int r = 0; r < (NR < 8 ? 8 : NR); ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * f[r % NR]);
-                            if constexpr (NR == 16) tc::store(at, o);
-                            else tc::st8(at, o);
-                        }
+                        for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f[c & 3]);
+                        tc::st16(o_at, o);
                         tc::wait_st();
                     }
-#pragma unroll
-                    for (int r = 0; r < NR; ++r) sum[r] *= f[r], rest[r] *= f[r];
                     ++version;
-                    if (l < NR) {
-                        float mine_next = next[0];
-#pragma unroll
-                        for (int r = 1; r < NR; ++r) mine_next = l == r ? next[r] : mine_next;
-                        ctl->m[version & 1][l] = mine_next;
-                    }
-                    if (l == 0) ctl->version = version;
-                    m = ctl->m[version & 1];
+                    if (l < 4) ctl->m[version & 3][rs * 4 + l] = l == 0 ? next[0] : l == 1 ? next[1] : l == 2 ? next[2] : next[3];
+                    if (first_thread) ctl->version = version;
                 }
-                group_any(w, false);
-                release(x, m, ev, part);
+                release(x, ev, part);
                 tc::fence_before();
-                group_any(w, false);
+                group_any<Plan::kThreads>(w, false);
             }
-            if (l == 0) {
+            if (first_thread) {
                 tc::bar_arrive(&ctl->p_full[w]);
-                if (i + 1 < tiles) tc::bar_arrive(&ctl->token[w ^ 1]);
+                if (i + 1 < tiles) tc::bar_arrive(&ctl->token[w + 1 == (int)G ? 0 : w + 1]);
             }
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {      // what an addition cuts off is kept: very many small terms count beside a large one
+            for (int r = 0; r < 4; ++r) {       // what an addition cuts off is kept: very many small terms count beside a large one
                 const float y = part[r] + rest[r], a = sum[r] + y, back = a - sum[r];
                 rest[r] = (sum[r] - (a - back)) + (y - back);
                 sum[r] = a;
             }
         }
-        // ---- the block's sums and O, which both groups' tiles are in ----
-        for (int k = 0; k < 2 && ok; ++k) {
-            const uint32_t of = (tiles + 1 - k) / 2;                  // tiles of group k
+        // ---- the block's sums and O, which all groups' tiles are in ----
+        for (uint32_t k = 0; k < G && ok; ++k) {
+            const uint32_t of = (tiles + G - 1 - k) / G;              // tiles of group k
             if (of) ok = tc::bar_wait(&ctl->p_done[k], (of - 1) & 1, gave_up);
         }
         tc::fence_after();
-        asm volatile("bar.sync 3, 256;" ::: "memory");
+        asm volatile("bar.sync 4, %0;" ::"n"(Plan::kSoft * 32) : "memory");
         ok = !*gave_up;
-        const float *m = ctl->m[ctl->version & 1];
-        if (ctl->version != version) rescale(ctl->m[version & 1], m);
+        float f[4];
+        adopt(ctl->m[ctl->version & 3] + rs * 4, f);
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
+        for (int r = 0; r < 4; ++r) {
             float a = sum[r] + rest[r];
 #pragma unroll
             for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(~0u, a, o);
             if (lane == 0) ctl->sums[warp][r] = a;
         }
-        asm volatile("bar.sync 3, 256;" ::: "memory");
+        asm volatile("bar.sync 4, %0;" ::"n"(Plan::kSoft * 32) : "memory");
         if (ok && w == 0) {
-            uint32_t o[kFewTerms][NR < 8 ? 8 : NR];
-#pragma unroll
-            for (int term = 0; term < kFewTerms; ++term) {
-                if (NR == 4 && (term & 1)) continue;
-                load_columns(o[term], tm + lanes + kO + term * NR);
-            }
+            uint32_t o[16];
+            tc::ld16(o, o_at);
             tc::wait_ld();
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                if ((uint32_t)r >= p.rows) break;
+            for (int r = 0; r < 4; ++r) {
+                const uint32_t row = rs * 4 + r;
+                if (row >= p.rows) break;
                 float acc = 0.0f, ls = 0.0f;
                 if (tiles) {
 #pragma unroll
-                    for (int term = kFewTerms - 1; term >= 0; --term)
-                        acc = fmaf(acc, 0.125f, __uint_as_float(NR == 4 ? o[term & ~1][(term & 1) * 4 + r] : o[term][r]));
+                    for (int term = kTerms - 1; term >= 0; --term) acc += __uint_as_float(o[term * 4 + r]);
                 }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) ls += ctl->sums[k][r];
-                const uint32_t t = r / p.group, hd = hk * p.group + r - t * p.group;
+                for (int k = rs * 4; k < Plan::kSoft; k += 4 * RS) ls += (ctl->sums[k][r] + ctl->sums[k + 1][r]) + (ctl->sums[k + 2][r] + ctl->sums[k + 3][r]);
+                const uint32_t t = row / p.group, hd = hk * p.group + row - t * p.group;
                 const float mr = m[r] - kCachedUp;
                 if (p.splits > 1) {
                     const uint64_t at = ((uint64_t)split * p.T + t) * p.hq + hd;
@@ -448,7 +477,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) attn_few_kernel(const __grid_c
     __syncwarp();
     tc::fence_before();
     __syncthreads();
-    if (warp == 16) tc::dealloc(tm, 128);
+    if (warp == Plan::kSoft + 4) tc::dealloc(tm, 256);
     if (tid == 0 && *gave_up) atomicOr(p.status, K2T_STATUS_WAIT_TIMEOUT);
 }
 

@@ -141,6 +141,11 @@ __device__ __forceinline__ void st4(uint32_t at, const uint32_t (&r)[4])
                  : "memory");
 }
 
+__device__ __forceinline__ void ld4(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+
 __device__ __forceinline__ void load(uint32_t (&r)[32], uint32_t at) { ld32(r, at); }
 __device__ __forceinline__ void load(uint32_t (&r)[16], uint32_t at) { ld16(r, at); }
 __device__ __forceinline__ void store(uint32_t at, const uint32_t (&r)[32]) { st32(at, r); }
