@@ -48,6 +48,12 @@ __device__ __forceinline__ uint32_t from_e4m3(uint32_t two)
     return r;
 }
 
+__device__ __forceinline__ float2 e4m3_pair(uint32_t two)
+{
+    const uint32_t h = from_e4m3(two);
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
 // 8 values of a row.
 template <typename T> struct Eight;
 template <> struct Eight<float> {
@@ -65,9 +71,9 @@ template <> struct Eight<float> {
 };
 template <> struct Eight<__half> {
     float v[8];
-    __device__ __forceinline__ void load(const __half *p)
+    __device__ __forceinline__ void load(const __half *p) { set(*reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void set(uint4 u)
     {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -88,9 +94,9 @@ template <> struct Eight<__half> {
 };
 template <> struct Eight<__nv_bfloat16> {
     float v[8];
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p)
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { set(*reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void set(uint4 u)
     {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
@@ -105,6 +111,27 @@ template <> struct Eight<__nv_bfloat16> {
         }
         *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
+};
+
+// The same as they lie in memory, to be held in fewer registers.
+template <typename T> struct RawEight {
+    uint4 u;
+    __device__ __forceinline__ void clear() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load(const T *p) { u = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ Eight<T> values() const
+    {
+        Eight<T> e;
+        e.set(u);
+        return e;
+    }
+};
+template <> struct RawEight<float> : Eight<float> {
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    }
+    __device__ __forceinline__ const Eight<float> &values() const { return *this; }
 };
 
 // What the kernels need of k2t_cache, by value.

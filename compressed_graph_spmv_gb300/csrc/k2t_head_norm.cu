@@ -7,52 +7,60 @@
 namespace k2t {
 namespace {
 
-constexpr uint32_t kHeadBlocks = 152 * 8;      // of a backward pass, at most: each writes a partial row of dweight
+constexpr uint32_t kHeadBlocks = 152 * 4;       // of a backward pass, at most: each writes a partial row of dweight
 
-template <typename T, int V, int S, int HC, bool PAIRED> int head_launch(HeadParams &p, bool backward, cudaStream_t st)
+template <typename T, int V, int S, int AHEAD, bool PAIRED, bool BACK> int head_launch(HeadParams &p, cudaStream_t st)
 {
-    p.chunks = (p.heads + HC - 1) / HC;
+    const uint32_t groups = kHeadThreads / 32 * (32 / p.lanes);
+    p.chunks = (p.heads + p.per - 1) / p.per;
     p.units = p.n * p.chunks;
-    const uint32_t groups = kHeadThreads / p.lanes;
+    constexpr auto kernel = [] {
+        if constexpr (BACK) return head_norm_bwd_kernel<T, V, S, AHEAD, PAIRED>;
+        else return head_norm_fwd_kernel<T, V, S, AHEAD, PAIRED>;
+    }();
+    size_t smem = HeadStream<T, V, S, (BACK ? 4 : 2) * S, AHEAD>::kBytes + sizeof(p.rate);
+    if (BACK && p.part) smem += (size_t)groups * p.d * sizeof(float);
+    if (int rc = norm_shared<kernel>()) return rc;
     const uint64_t all = (p.units + groups - 1) / groups;
-    if (!backward) {
-        const uint32_t blocks = (uint32_t)std::min<uint64_t>(all, kHeadBlocks * 4);
-        return norm_launch(head_norm_fwd_kernel<T, V, S, HC, PAIRED>, dim3(blocks), kHeadThreads, 0, st, p);
+    uint32_t blocks = (uint32_t)std::min<uint64_t>(all, BACK ? kHeadBlocks : kHeadBlocks * 8);
+    if (AHEAD) {
+        if (int rc = norm_resident(kernel, blocks, kHeadThreads, smem)) return rc;      // each starts its own queue of loads
     }
-    constexpr auto kernel = head_norm_bwd_kernel<T, V, S, HC, PAIRED>;
-    const uint32_t blocks = (uint32_t)std::min<uint64_t>(all, kHeadBlocks);
-    const size_t smem = p.part ? (size_t)groups * p.d * sizeof(float) : 0;
+    p.blocks = blocks;
     return norm_launch(kernel, dim3(blocks), kHeadThreads, smem, st, p);
 }
 
-template <typename T, int V, int S, bool PAIRED> int head_chunks(HeadParams &p, bool backward, cudaStream_t st)
-{
-    if constexpr (V == 1) {
-        return head_launch<T, V, S, 1, PAIRED>(p, backward, st);
-    } else {
-        constexpr int HC = 2;
-        if (p.heads > 1 && p.n * p.heads * p.lanes > (uint64_t)152 * 2048) return head_launch<T, V, S, HC, PAIRED>(p, backward, st);
-        return head_launch<T, V, S, 1, PAIRED>(p, backward, st);
-    }
-}
-
-template <typename T, int V, int S> int head_pairs(HeadParams &p, bool paired, bool backward, cudaStream_t st)
+// Where there are rows enough to fill the GPU a group of lanes takes all heads of a row, whose angles it forms once, and
+// its loads run ahead; else a head each: such a call is its latency.
+template <typename T, int V, int S, bool PAIRED, bool BACK> int head_rows(HeadParams &p, cudaStream_t st)
 {
     p.slots = p.d / 2 / V;
-    p.lanes = 1;
-    while (p.lanes < 32 && p.lanes < p.slots) p.lanes *= 2;
-    return paired ? head_chunks<T, V, S, true>(p, backward, st) : head_chunks<T, V, S, false>(p, backward, st);
+    p.lanes = std::min(32u, p.slots);
+    p.reach = 0;
+    for (uint32_t r = 1; r < p.lanes; r *= 2) p.reach = r;
+    const bool many = p.n * p.lanes > (uint64_t)152 * 2048;
+    p.per = many ? p.heads : 1;
+    if constexpr (S == 1) {
+        // heads ahead: 96 bytes of a thread, 50 to 100 KB of an SM's, in 3 to 8 heads.  More costs as less does: 2^20 rows of 4
+        // heads of 128, fp32, forward, 3 heads ahead 642 us, 6 ahead 696.
+        constexpr int kBytes = (BACK ? 4 : 2) * V * (int)sizeof(T), kAhead = std::min(std::max(96 / kBytes, 3), 8);
+        if (many) return head_launch<T, V, S, kAhead, PAIRED, BACK>(p, st);
+    }
+    return head_launch<T, V, S, 0, PAIRED, BACK>(p, st);
 }
 
-// Pairs a thread takes: as many as fill a 16-byte load, where both halves of what turns, and of what does not, are whole
-// vectors of them.
-template <typename T> int head_type(HeadParams &p, bool paired, bool backward, cudaStream_t st)
+// Pairs a thread takes: vectors of 16 bytes, where both halves of what turns, and of what does not, are whole vectors of them,
+// else of fewer: what a head costs besides its values (its sums over the lanes, its loads) is shared by more of them (2^20 rows
+// of 4 heads of 128, bf16, backward 602 us, in vectors of 8 bytes 805).
+template <typename T, bool PAIRED, bool BACK> int head_type(HeadParams &p, cudaStream_t st)
 {
-    constexpr int V = 16 / sizeof(T);
     const uint32_t parts = (p.rotary / 2) | ((p.d - p.rotary) / 2);
-    if (parts % V == 0) return head_pairs<T, V, 1>(p, paired, backward, st);
-    if (V == 8 && parts % 4 == 0) return head_pairs<T, 4, 1>(p, paired, backward, st);
-    return head_pairs<T, 1, 4>(p, paired, backward, st);
+    if constexpr (sizeof(T) == 2) {
+        if (parts % 8 == 0) return head_rows<T, 8, 1, PAIRED, BACK>(p, st);
+    }
+    if (parts % 4 == 0) return head_rows<T, 4, 1, PAIRED, BACK>(p, st);
+    if (parts % 2 == 0) return p.d <= 128 ? head_rows<T, 2, 1, PAIRED, BACK>(p, st) : head_rows<T, 2, 2, PAIRED, BACK>(p, st);
+    return head_rows<T, 1, 4, PAIRED, BACK>(p, st);
 }
 
 int check_head(const k2t_head_norm *a)
@@ -76,12 +84,15 @@ void fill(const k2t_head_norm *a, HeadParams &p)
     for (uint32_t i = 0; i < p.rotary / 2; ++i) p.rate[i] = a->rates[i];
 }
 
-int run(const k2t_head_norm *a, HeadParams &p, bool backward, cudaStream_t st)
+template <bool BACK> int run(const k2t_head_norm *a, HeadParams &p, cudaStream_t st)
 {
-    const bool paired = a->flags & K2T_HEAD_PAIRED;
-    if (a->dtype == K2T_BF16) return head_type<__nv_bfloat16>(p, paired, backward, st);
-    if (a->dtype == K2T_FP16) return head_type<__half>(p, paired, backward, st);
-    return head_type<float>(p, paired, backward, st);
+    const auto go = [&](auto zero) {
+        using T = decltype(zero);
+        return a->flags & K2T_HEAD_PAIRED ? head_type<T, true, BACK>(p, st) : head_type<T, false, BACK>(p, st);
+    };
+    if (a->dtype == K2T_BF16) return go(__nv_bfloat16());
+    if (a->dtype == K2T_FP16) return go(__half());
+    return go(0.0f);
 }
 
 }  // namespace
@@ -117,7 +128,7 @@ int k2t_head_norm_forward(const k2t_head_norm *a, void *stream)
     if (!a->n_rows) return K2T_OK;
     HeadParams p{};
     fill(a, p);
-    return run(a, p, false, static_cast<cudaStream_t>(stream));
+    return run<false>(a, p, static_cast<cudaStream_t>(stream));
 }
 
 int k2t_head_norm_backward(const k2t_head_norm *a, void *work, uint64_t work_bytes, void *stream)
@@ -137,9 +148,8 @@ int k2t_head_norm_backward(const k2t_head_norm *a, void *work, uint64_t work_byt
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint32_t parts = 0;
     if (a->n_rows) {
-        if (int rc = run(a, p, true, st)) return rc;
-        const uint32_t groups = kHeadThreads / p.lanes;
-        parts = (uint32_t)std::min<uint64_t>((p.units + groups - 1) / groups, kHeadBlocks);
+        if (int rc = run<true>(a, p, st)) return rc;
+        parts = p.blocks;
     }
     if (!a->weight) return K2T_OK;
     NormParams j{};
