@@ -1,7 +1,7 @@
 // k2t_attn.cu -- the attention calls of the C ABI: checks, plan, launch.
 #include <algorithm>
 
-#include "k2t_attn_cached.cuh"
+#include "k2t_attn_few.cuh"
 #include "k2t_attn_launch.cuh"
 #include "k2t_rows.h"
 
@@ -57,6 +57,7 @@ struct Plan {
     AttnParams p;
     int bm;
     uint64_t part_floats, ml_floats, info_floats, delta_floats;
+    uint64_t hop_bytes = 0;               // over a cache: bucket bytes of its nodes, at the end of the work buffer
 };
 
 // most: rows a block of the forward pass takes at most
@@ -143,7 +144,13 @@ constexpr uint64_t kWorkHead = 256;   // the device status word
 uint64_t plan_bytes(const Plan &pl)
 {
     return kWorkHead + align_up(pl.part_floats * 4, 256) + align_up(pl.ml_floats * 4, 256) + align_up(pl.info_floats * 4, 256) +
-           align_up(pl.delta_floats * 4, 256);
+           align_up(pl.delta_floats * 4, 256) + pl.hop_bytes;
+}
+
+// Rows enough for the kernel that has its hops turned into bytes beforehand.
+void add_hops(Plan &pl)
+{
+    if (pl.p.sources && pl.p.rows > kFewMost) pl.hop_bytes = pl.p.tiles * hop_tile_bytes(pl.p.sources);
 }
 
 int check_call(const k2t_attn *a, const void *work, bool backward)
@@ -240,6 +247,7 @@ uint64_t k2t_cached_attn_work_bytes(const k2t_attn *a)
     if (check_sizes(a)) return 0;
     Plan pl;
     make_plan(a, false, pl, 128);
+    add_hops(pl);
     // the most blocks that pick_splits gives the nodes of any part of the cache
     const uint64_t rows = (uint64_t)a->n_queries * a->n_heads, blocks = (uint64_t)pl.p.hkv * pl.p.row_tiles;
     const uint64_t most = std::min(std::min<uint64_t>(std::max<uint64_t>(1, pl.p.tiles), kSms), ((blocks + kSms - 1) / kSms + 8) * kSms / blocks);
@@ -256,6 +264,7 @@ int k2t_cached_attn_forward(const k2t_attn *a, const k2t_cache *c, void *work, u
     const k2t_attn b = over_cache(a, c);
     Plan pl;
     make_plan(&b, false, pl, 128);
+    add_hops(pl);
     if ((rc = check_call(&b, work, false))) return rc;
     if (work_bytes < plan_bytes(pl)) return K2T_ENOMEM;
     if (a->n_queries == 0) return K2T_OK;
@@ -264,6 +273,8 @@ int k2t_cached_attn_forward(const k2t_attn *a, const k2t_cache *c, void *work, u
     static_cast<AttnParams &>(p) = pl.p;
     p.pitch = cache_pitch(c->head_dim), p.scale_pitch = cache_scale_pitch(c->n_nodes), p.cached = c->n_nodes;
     p.kc = static_cast<const uint8_t *>(c->k), p.vc = static_cast<const uint8_t *>(c->v), p.ks = c->k_scale, p.vs = c->v_scale;
+    p.hop_tile = hop_tile_bytes(p.sources);
+    p.hop_tiles = pl.hop_bytes ? static_cast<uint8_t *>(work) + plan_bytes(pl) - pl.hop_bytes : nullptr;
     return attn_cached(p, a->dtype, pl.bm, static_cast<cudaStream_t>(stream));
 }
 

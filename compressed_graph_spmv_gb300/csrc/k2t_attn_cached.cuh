@@ -22,10 +22,11 @@
 // weights: with the running maximum m of s + ev a weight is 2^(s + ev - m), the
 // sum takes it times 2^-ev, and no value is multiplied.
 //
-// A thread has a row and goes through its part of a tile 32 nodes at a time,
-// once: m is a whole number and trails the maximum by at most 2^8 in the
-// weights; when a score exceeds that, O, the sum and the weights of the tile
-// so far are multiplied by a power of two.
+// Two threads have a row, one each half of the nodes, and go through them 32 at
+// a time, once: m is a whole number and trails the maximum by at most 2^8 in
+// the weights; when a score exceeds that, the thread multiplies its weights of
+// the tile so far by a power of two and goes on against a larger m, and at the
+// tile's end both take the larger of theirs, with O and the sums.
 #pragma once
 
 #include "k2t_attn.cuh"
@@ -38,10 +39,12 @@ struct CachedParams : AttnParams {
     uint32_t pitch;                       // bytes of a cached row
     uint64_t scale_pitch, cached;         // of a head's scales; nodes of the cache
     const uint8_t *kc, *vc, *ks, *vs;
+    uint8_t *hop_tiles;                   // bucket bytes of the nodes, tile by tile: attn_hops_kernel
+    uint32_t hop_tile;                    // bytes of a tile: [n_sources + 1][kTcPitch], then which nodes are seen, 4 words
 };
 
-// Warps: 0-7 softmax, 8-11 hops -> bucket bytes, 12-15 states -> slots, 16-19 values -> fp16, 20 products.
-constexpr int kCachedThreads = 672;
+inline uint32_t hop_tile_bytes(uint32_t sources) { return ((sources + 1) * kTcPitch + 16 + 127) / 128 * 128; }
+
 constexpr float kCachedUp = 7.0f;         // weights are at most 2^(8 + 7)
 
 template <int DP> struct CachedSmem {
@@ -49,7 +52,9 @@ template <int DP> struct CachedSmem {
     static constexpr int kKeys = DP == 64 ? 4 : 3;            // slots of keys, of values, of values in fp16
     static constexpr int kValues = DP == 64 ? 4 : 2;
     static constexpr int kWide = DP == 64 ? 3 : 2;
-    static constexpr int kBufs = DP == 64 ? 4 : 3;            // bucket tiles
+    // Warps: 0-15 softmax, then four for values -> fp16, one for keys, one for values, products, bucket bytes.
+    static constexpr int kWiden = 16, kLoad = 20, kMma = kLoad + 2, kThreads = (kMma + 2) * 32;
+    static constexpr int kBufs = 3;                           // bucket tiles
     static constexpr int kValueSlot = kTcTile * DP, kWideSlot = kTile * (DP / 64);
     static constexpr int kQ = 0;                              // three terms
     static constexpr int kK = kQ + 3 * kTile;
@@ -60,10 +65,9 @@ template <int DP> struct CachedSmem {
     struct Ctl {
         uint64_t k_full[kKeys], k_empty[kKeys], v_full[kValues], v_empty[kValues], w_full[kWide], w_empty[kWide];
         uint64_t hop_full[kBufs], hop_empty[kBufs], s_full[2], p_full[2], o_full[2], drained;
-        uint32_t tmem, gave_up, columns, all;
-        uint32_t seen[kBufs][4];
+        uint32_t tmem, gave_up, pad[2];
         float row_scale[128];             // what multiplies a row's scores
-        uint8_t byte_of[257 + 15];
+        float most[2][2][128];            // [group][half][lane]: a thread's m, where it has grown
     };
     static constexpr int kLut = kCtl + (int)((sizeof(Ctl) + 15) / 16 * 16);
     static size_t bytes(const AttnParams &p) { return kLut + kTcLutAlign + (size_t)(p.buckets + 2) * p.group2 * 4; }
@@ -91,46 +95,127 @@ __device__ __forceinline__ float2 from_e5m2(uint32_t two)
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
+// Biases of 16 nodes, whose bucket bytes lie at shared-memory address bt: see bias_scores.
+__device__ __forceinline__ void look_up(float (&bias)[16], uint32_t bt, uint32_t lg, uint32_t shift)
+{
+    const uint32_t mask = 255u << shift;
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(bt) : "memory");
+#pragma unroll
+    for (int y = 0; y < 16; y += 2) {
+        const uint32_t v = w[y >> 2];
+        const uint32_t i0 = (y & 3) ? v >> (16 - shift) : v << shift, i1 = (y & 3) ? v >> (24 - shift) : v >> (8 - shift);
+        bias[y] = table((i0 & mask) | lg), bias[y + 1] = table((i1 & mask) | lg);
+    }
+}
+// 16 scores of N, from `from` on, in units of log2 with them, and their maximum with `top`.
+template <int N> __device__ __forceinline__ float add_bias(uint32_t (&s)[N], int from, float scale, const float (&bias)[16], float top)
+{
+    const float2 sc = make_float2(scale, scale);
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+        const float2 x = fma2(make_float2(__uint_as_float(s[from + e]), __uint_as_float(s[from + e + 1])), sc, make_float2(bias[e], bias[e + 1]));
+        s[from + e] = __float_as_uint(x.x), s[from + e + 1] = __float_as_uint(x.y);
+        top = max3(top, x.x, x.y);
+    }
+    return top;
+}
+
+// Whether any thread of the two warps that share barrier `id` says so.
+__device__ __forceinline__ bool pair_any(int id, bool yes)
+{
+    uint32_t any;
+    __syncwarp();
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.or.aligned.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any) : "r"(id), "r"((uint32_t)yes) : "memory");
+    return any;
+}
+
+// Bucket bytes of the block's tiles -> shared memory.
+template <int DP, typename Ctl>
+__device__ __forceinline__ void hop_copies(const CachedParams &p, Ctl *ctl, uint32_t sm, uint32_t tiles, uint32_t split, volatile uint32_t *gave_up)
+{
+    using S = CachedSmem<DP>;
+    const bool lead = tc::elect();
+    const uint32_t size = (p.sources + 1) * kTcPitch;
+    const uint8_t *from = p.hop_tiles + (uint64_t)split * p.hop_tile;
+    uint32_t t = 0;
+    for (; t < tiles; ++t, from += (uint64_t)p.splits * p.hop_tile) {
+        const uint32_t buf = t % S::kBufs;
+        if (t >= S::kBufs && !__all_sync(~0u, tc::bar_wait(&ctl->hop_empty[buf], (t / S::kBufs - 1) & 1, gave_up))) break;
+        if (lead) {
+            const uint32_t bar = tc::saddr(&ctl->hop_full[buf]);
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(size) : "memory");
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(sm + S::kBuckets + buf * 33 * kTcPitch),
+                         "l"(from), "r"(size), "r"(bar) : "memory");
+        }
+        __syncwarp();
+    }
+    if (t < tiles)         // copies in flight end before the block does
+        for (uint32_t u = t < S::kBufs ? 0 : t - S::kBufs; u < t; ++u) {
+            const long long start = clock64();
+            while (!tc::bar_peek(&ctl->hop_full[u % S::kBufs], (u / S::kBufs) & 1) && clock64() - start < (1ll << 28)) {}
+        }
+}
+
 // Byte offset of chunk c of row r in a slot of values: odd rows of 128 bytes have their halves exchanged, so that the eight
 // lanes that read four chunks of two rows meet no bank twice.
 template <int DP> __device__ __forceinline__ uint32_t value_chunk(uint32_t r, uint32_t c) { return r * DP + (DP == 128 ? c ^ (r & 1) << 2 : c) * 16; }
 
-// States of a tile's seen nodes -> slots, keys then values; this warp brings nodes [32 cw, 32 cw + 32).
-template <int DP, typename Ctl>
-__device__ __forceinline__ void cached_node_warps(const CachedParams &p, Ctl *ctl, uint32_t sm, int cw, int lane, uint32_t hk,
-                                                  uint32_t tiles, uint32_t split, volatile uint32_t *gave_up)
+// Keys (VALUES: values) of every tile's seen nodes -> slots, by one warp: all warps a part of every tile are each held up by
+// every tile's waits, and with a warp for some of the tiles one could wait for a slot's phase but one, which a barrier does
+// not tell from the last.
+template <int DP, int SLOTS, bool VALUES, typename Ctl>
+__device__ __forceinline__ void cached_node_warp(const CachedParams &p, Ctl *ctl, uint32_t sm, int lane, uint32_t hk,
+                                                 uint32_t tiles, uint32_t split, volatile uint32_t *gave_up)
 {
     using S = CachedSmem<DP>;
-    constexpr int C = DP / 16, RP = 32 / C;                    // chunks of 16 bytes a row, rows a pass
-    constexpr int kTurn = 8 / RP;                              // passes until the key slots' swizzle repeats
-    const uint32_t c = lane % C, r0 = cw * 32 + lane / C, chunks = p.pitch / 16, fill = (chunks + 1) & ~1u;
-    uint32_t k_at[kTurn];
+    constexpr int C = DP / 16, RP = 32 / C, kTurn = VALUES ? 1 : 8 / RP;   // chunks of 16 bytes a row, rows a pass, passes until the swizzle repeats
+    constexpr int kRow = VALUES ? DP : 128;
+    const uint32_t c = lane % C, r0 = lane / C, chunks = p.pitch / 16, fill = VALUES ? C : (chunks + 1) & ~1u;
+    uint64_t *full = VALUES ? ctl->v_full : ctl->k_full, *empty = VALUES ? ctl->v_empty : ctl->k_empty;
+    constexpr uint32_t kSlot = VALUES ? S::kValueSlot : S::kTile;
+    uint32_t to[kTurn];
 #pragma unroll
-    for (int k = 0; k < kTurn; ++k) k_at[k] = sm + S::kK + (r0 + k * RP) * 128 + ((c ^ ((r0 + k * RP) & 7)) << 4) - k * RP * 128;
-    const uint32_t v_at = sm + S::kV + value_chunk<DP>(r0, c);   // RP is even: the same for all of a lane's rows
-    const uint64_t first = (uint64_t)hk * p.cached * p.pitch + ((uint64_t)split * kTcTile + r0) * p.pitch + c * 16;
+    for (int k = 0; k < kTurn; ++k) {
+        const uint32_t r = r0 + k * RP;         // RP is even: a lane's rows of values all have their chunk at the same place
+        to[k] = VALUES ? sm + S::kV + value_chunk<DP>(r, c) : sm + S::kK + r * 128 + ((c ^ (r & 7)) << 4) - k * RP * 128;
+    }
+    const uint8_t *head = (VALUES ? p.vc : p.kc) + (uint64_t)hk * p.cached * p.pitch + (uint64_t)r0 * p.pitch + c * 16;
     const uint32_t step = RP * p.pitch;
-    const uint64_t stride = (uint64_t)p.splits * kTcTile * p.pitch;
-    const uint8_t *kc = p.kc + first, *vc = p.vc + first;
-    bool ok = true;
-    for (uint32_t i = 0; i < tiles && ok; ++i, kc += stride, vc += stride) {
-        const uint32_t buf = i % S::kBufs, ks = i % S::kKeys, vs = i % S::kValues;
-        ok = __all_sync(~0u, tc::bar_wait(&ctl->hop_full[buf], (i / S::kBufs) & 1, gave_up));
-        if (!ok) break;
-        // a node that no query sees, or past n, or a chunk past the row: zeros, and nothing is read
-        const uint32_t seen = c < chunks ? ctl->seen[buf][cw] >> (lane / C) : 0;
-        if (i >= S::kKeys) ok = __all_sync(~0u, tc::bar_wait(&ctl->k_empty[ks], (i / S::kKeys - 1) & 1, gave_up));
-        if (!ok) break;
-        if (c < fill) {
+    auto tile_at = [&](uint32_t i) { return split + (uint64_t)i * p.splits; };
+    auto seen_of = [&](uint32_t i) {
+        uint4 w = make_uint4(~0u, ~0u, ~0u, ~0u);
+        if (i >= tiles) return w;
+        if (p.sources) return __ldg(reinterpret_cast<const uint4 *>(p.hop_tiles + tile_at(i) * p.hop_tile + (p.sources + 1) * kTcPitch));
+        const uint64_t left = p.n - tile_at(i) * kTcTile;
+        if (left < kTcTile) {
+            uint32_t m[4];
 #pragma unroll
-            for (int k = 0; k < 32 / RP; ++k) cp16(k_at[k % kTurn] + ks * S::kTile + k * RP * 128, kc + k * step, seen >> (k * RP) & 1 ? 16 : 0);
+            for (uint32_t q = 0; q < 4; ++q) m[q] = left >= q * 32 + 32 ? ~0u : left > q * 32 ? (1u << (left - q * 32)) - 1 : 0;
+            w = make_uint4(m[0], m[1], m[2], m[3]);
         }
-        tc::cp_arrive(&ctl->k_full[ks]);
-        if (i >= S::kValues) ok = __all_sync(~0u, tc::bar_wait(&ctl->v_empty[vs], (i / S::kValues - 1) & 1, gave_up));
-        if (!ok) break;
+        return w;
+    };
+    uint4 next = seen_of(0), after = seen_of(1);
+    uint32_t slot = 0, use = 0;
+    for (uint32_t i = 0; i < tiles; ++i) {
+        // a node that no query sees, or past n, or a chunk past the row: zeros, and nothing is read
+        uint32_t seen[4] = {next.x >> r0, next.y >> r0, next.z >> r0, next.w >> r0};
+        if (c >= chunks) seen[0] = seen[1] = seen[2] = seen[3] = 0;
+        next = after, after = seen_of(i + 2);
+        const uint8_t *src = head + tile_at(i) * kTcTile * p.pitch;
+        if (!__all_sync(~0u, !use || tc::bar_wait(&empty[slot], (use - 1) & 1, gave_up))) break;
+        if (c < fill) {
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t bits = q == 0 ? seen[0] : q == 1 ? seen[1] : q == 2 ? seen[2] : seen[3], at = slot * kSlot + q * 32 * kRow;
 #pragma unroll
-        for (int k = 0; k < 32 / RP; ++k) cp16(v_at + vs * S::kValueSlot + k * RP * DP, vc + k * step, seen >> (k * RP) & 1 ? 16 : 0);
-        tc::cp_arrive(&ctl->v_full[vs]);
+                for (int k = 0; k < 32 / RP; ++k, src += step) cp16(to[k % kTurn] + at + k * RP * kRow, src, bits >> (k * RP) & 1 ? 16 : 0);
+            }
+        }
+        tc::cp_arrive(&full[slot]);
+        if (++slot == SLOTS) slot = 0, ++use;
     }
     cp_commit();
     cp_wait<0>();
@@ -220,7 +305,7 @@ template <typename T, int DP, int KW, typename Ctl>
 __device__ __forceinline__ void query_terms(const CachedParams &p, Ctl *ctl, uint8_t *smem, int tid, uint32_t row0, uint32_t hk)
 {
     using S = CachedSmem<DP>;
-    for (int i = tid; i < 128 * 8; i += kCachedThreads) {        // whole warps: the count is a multiple of 32
+    for (int i = tid; i < 128 * 8; i += S::kThreads) {        // whole warps: the count is a multiple of 32
         const uint32_t l = i / 8;
         const float scale = query_terms_of<T>(p, row0 + l % KW, i % 8, hk, smem + S::kQ, S::kTile, l);
         if (i % 8 == 0) ctl->row_scale[l] = scale;
@@ -228,7 +313,7 @@ __device__ __forceinline__ void query_terms(const CachedParams &p, Ctl *ctl, uin
 }
 
 template <typename T, int DP, int KW>
-__global__ void __launch_bounds__(kCachedThreads, 1) attn_cached_kernel(const __grid_constant__ CachedParams p)
+__global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kernel(const __grid_constant__ CachedParams p)
 {
     using S = CachedSmem<DP>;
     using Ctl = typename S::Ctl;
@@ -244,35 +329,25 @@ __global__ void __launch_bounds__(kCachedThreads, 1) attn_cached_kernel(const __
     auto tile_at = [&](uint32_t i) { return split + (uint64_t)i * p.splits; };
 
     // ---- set-up ----
-    if (warp == 20) tc::alloc(&ctl->tmem, 512);
+    if (warp == S::kMma) tc::alloc(&ctl->tmem, 512);
     if (tid == 0) {
-        for (int i = 0; i < S::kKeys; ++i) tc::bar_init(&ctl->k_full[i], 128), tc::bar_init(&ctl->k_empty[i], 1);
-        for (int i = 0; i < S::kValues; ++i) tc::bar_init(&ctl->v_full[i], 128), tc::bar_init(&ctl->v_empty[i], 4);
+        for (int i = 0; i < S::kKeys; ++i) tc::bar_init(&ctl->k_full[i], 32), tc::bar_init(&ctl->k_empty[i], 1);
+        for (int i = 0; i < S::kValues; ++i) tc::bar_init(&ctl->v_full[i], 32), tc::bar_init(&ctl->v_empty[i], 4);
         for (int i = 0; i < S::kWide; ++i) tc::bar_init(&ctl->w_full[i], 4), tc::bar_init(&ctl->w_empty[i], 1);
-        for (int i = 0; i < S::kBufs; ++i) tc::bar_init(&ctl->hop_full[i], 4), tc::bar_init(&ctl->hop_empty[i], 4);
+        for (int i = 0; i < S::kBufs; ++i) tc::bar_init(&ctl->hop_full[i], 1), tc::bar_init(&ctl->hop_empty[i], 8);
         for (int i = 0; i < 2; ++i) {
             tc::bar_init(&ctl->s_full[i], 1);
-            tc::bar_init(&ctl->p_full[i], 128);
+            tc::bar_init(&ctl->p_full[i], 8);
             tc::bar_init(&ctl->o_full[i], 1);
         }
         tc::bar_init(&ctl->drained, 1);
-        ctl->gave_up = ctl->columns = ctl->all = 0;
+        ctl->gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (p.sources)
-        for (int i = tid; i < 257; i += kCachedThreads) ctl->byte_of[i] = i ? p.bucket_of[i - 1] + 1 : 0;
     tc::grid_wait();
     fill_bias<T>(lut, p, hk, tid, p.group2);
     query_terms<T, DP, KW>(p, ctl, smem, tid, row0, hk);
     tc::fence_async();
-    __syncthreads();
-    if (p.sources)
-        for (int i = tid; i < KW; i += kCachedThreads)
-            if (row0 + i < p.rows) {
-                const uint32_t c = row_column(p, row0 + i);
-                if (c < p.sources) atomicOr(&ctl->columns, 1u << c);
-                else ctl->all = 1;
-            }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -280,13 +355,22 @@ __global__ void __launch_bounds__(kCachedThreads, 1) attn_cached_kernel(const __
     const uint32_t tm = ctl->tmem;                       // S of group w at w * 128, O at 256 + w * DP
     volatile uint32_t *gave_up = &ctl->gave_up;
 
-    if (warp >= 8 && warp < 12) {
-        hop_warps<S::kBufs>(p, ctl, smem + S::kBuckets, warp - 8, lane, tiles, split, gave_up);
-    } else if (warp >= 12 && warp < 16) {
-        cached_node_warps<DP>(p, ctl, sm, warp - 12, lane, hk, tiles, split, gave_up);
-    } else if (warp >= 16 && warp < 20) {
-        widen_warps<DP>(ctl, smem, tid - 16 * 32, tiles, gave_up);
-    } else if (warp == 20) {
+    if (warp >= S::kWiden && warp < S::kLoad) {
+        widen_warps<DP>(ctl, smem, tid - S::kWiden * 32, tiles, gave_up);
+    } else if (warp == S::kLoad) {
+        cached_node_warp<DP, S::kKeys, false>(p, ctl, sm, lane, hk, tiles, split, gave_up);
+    } else if (warp == S::kLoad + 1) {
+        cached_node_warp<DP, S::kValues, true>(p, ctl, sm, lane, hk, tiles, split, gave_up);
+    } else if (warp == S::kMma + 1) {
+        if (p.sources) hop_copies<DP>(p, ctl, sm, tiles, split, gave_up);
+        else if (tiles && tile_at(tiles - 1) == p.tiles - 1 && p.n % kTcTile) {
+            // without a table: the bytes of the last tile, which has nodes past the end
+            uint8_t *bt = smem + S::kBuckets + (tiles - 1) % S::kBufs * 33 * kTcPitch;
+            for (uint32_t j = lane; j < kTcTile; j += 32) bt[j] = j < p.n % kTcTile;
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(&ctl->hop_full[(tiles - 1) % S::kBufs]);
+        }
+    } else if (warp == S::kMma) {
         // ---- products: tile u belongs to group u & 1 ----
         const bool lead = tc::elect();
         const uint32_t id_s = idesc_e5m2_e4m3(kTcTile);
@@ -321,7 +405,7 @@ __global__ void __launch_bounds__(kCachedThreads, 1) attn_cached_kernel(const __
             const uint64_t v = tc::desc(sm + S::kWideAt + slot * S::kWideSlot, S::kTile);
 #pragma unroll
             for (uint32_t kk = 0; kk < kTcTile / 16; ++kk)
-                tc::mma_ts(lead, tm + 256 + w * DP, tm + w * 128 + (kk >> 1) * 32 + (kk & 1) * 8, v, kk * 2048, id_o, done > 1 || kk > 0);
+                tc::mma_ts(lead, tm + 256 + w * DP, tm + w * 128 + (kk >> 1) * 32 + (kk & 1) * (KW == 32 ? 16 : 8), v, kk * 2048, id_o, done > 1 || kk > 0);
             tc::commit(lead, &ctl->w_empty[slot]);
             if (done + 2 >= tiles) tc::commit(lead, &ctl->o_full[w]);
             else ok = scores(done + 2);
@@ -329,100 +413,160 @@ __global__ void __launch_bounds__(kCachedThreads, 1) attn_cached_kernel(const __
         if (done != tiles) tc::drain(lead, &ctl->drained, 0);
         __syncwarp();
     } else {
-        // ---- softmax: a thread has a lane of tensor memory, and of every other tile its copy's nodes ----
-        const int w = warp >> 2, l = (warp & 3) * 32 + lane;
+        // ---- softmax: a thread has a lane of tensor memory, and of every other tile half of its copy's nodes ----
+        // Biases are looked up while the scores are on their way, the first ones before they are there, where the registers
+        // hold them: 32 queries over 2^20 nodes, 8 heads of 64, 358 us, afterwards 385; with 4 key/value heads of 128 and 128
+        // rows the registers spill, and 395 us become 407.
+        constexpr bool kEarly = DP == 64 || KW < 128;
+        constexpr int HW = KW / 2, CH = HW < 32 ? HW : 32;            // nodes of a thread's part of a tile, of them at a time
+        const int w = warp >> 3, half = warp >> 2 & 1, l = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // lane field of this warp's tensor memory
         const uint32_t row = row0 + l % KW;
-        const int copy = l / KW, key0 = copy * KW;                    // this thread's part of a tile
-        const uint32_t col = row < p.rows ? row_column(p, row) : 0;
+        const int copy = l / KW, key0 = copy * KW + half * HW;        // this thread's part of a tile
+        const uint32_t col = p.sources && row < p.rows ? row_column(p, row) : 0;
         const uint32_t G = p.group, shift = p.group2_log + 2;
         const uint32_t lg = lut_at | (row < p.rows ? row % G : 0) * 4;
-        const uint32_t s_at = tm + lanes + w * 128, o_at = tm + lanes + 256 + w * DP;
-        const uint8_t *bt0 = smem + S::kBuckets + col * kTcPitch + key0;
+        const uint32_t s_at = tm + lanes + w * 128 + key0;            // the scores of its nodes
+        auto o_at = [&] { return ctl->tmem + ((uint32_t)(threadIdx.x >> 5 & 3) << 21) + 256 + w * DP + (threadIdx.x >> 7 & 1) * (DP / 2); };
+        const uint32_t bt0 = sm + S::kBuckets + col * kTcPitch + key0;
+        const uint8_t *ks = p.ks + hk * p.scale_pitch + key0 / 32 + split * 4;
+        // the tile with nodes past the end, without a table
+        const uint32_t tail = !p.sources && tiles && tile_at(tiles - 1) == p.tiles - 1 && p.n % kTcTile ? tiles - 1 : ~0u;
+        const int pair = w * 4 + (warp & 3) + 2;                      // barrier of the two warps that share rows
         const float row_scale = ctl->row_scale[l];
-        const uint8_t *ks = p.ks + hk * p.scale_pitch, *vs = p.vs + hk * p.scale_pitch;
-        float m = -INFINITY;
+        float m = -INFINITY;                                          // both halves' alike
         LongSum sum;
         bool ok = true;
         uint32_t mine = 0;                                            // tiles of this group done
         uint32_t kb = 0, vb = 0;                                      // the next tile's scale bytes
         auto scales = [&](uint32_t i) {
             if (i < tiles) {
-                kb = __ldg(reinterpret_cast<const uint32_t *>(ks + tile_at(i) * 4));
-                vb = __ldg(reinterpret_cast<const uint32_t *>(vs + tile_at(i) * 4));
+                const uint8_t *at = ks + (uint64_t)i * p.splits * 4, *av = at + (p.vs - p.ks);
+                if constexpr (HW == 64) {
+                    kb = __ldg(reinterpret_cast<const uint16_t *>(at)), vb = __ldg(reinterpret_cast<const uint16_t *>(av));
+                } else {
+                    kb = __ldg(at), vb = __ldg(av);
+                }
+            }
+        };
+        // this tile's weights so far, [0, to) of the thread's nodes, times f
+        auto scale_weights = [&](float f, int to) {
+            const __half2 hf = __float2half2_rn(f);
+            tc::wait_st();
+#pragma unroll 1
+            for (int c = 0; c < to; c += 16) {
+                uint32_t x[8];
+                const uint32_t at = s_at + (HW == 16 ? 0 : c / 32 * 32 + (c % 32) / 2);
+                tc::ld8(x, at);
+                tc::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[e]), hf);
+                    x[e] = *reinterpret_cast<const uint32_t *>(&y);
+                }
+                tc::st8(at, x);
             }
         };
         scales(w);
         for (uint32_t i = w; i < tiles; i += 2, ++mine) {
             const uint32_t buf = i % S::kBufs;
-            const uint32_t kb0 = kb >> (copy * KW / 4), vb0 = vb >> (copy * KW / 4);
-            ok = tc::bar_wait(&ctl->hop_full[buf], (i / S::kBufs) & 1, gave_up) && tc::bar_wait(&ctl->s_full[w], mine & 1, gave_up);
+            // a table, or nodes past the end
+            const bool bytes = p.sources || i == tail;
+            uint32_t kb0 = kb, vb0 = vb;
+            const uint32_t bt = bt0 + buf * 33 * kTcPitch;
+            float bias[16];
+            if constexpr (kEarly) {
+                ok = !bytes || tc::bar_wait(&ctl->hop_full[buf], p.sources ? (i / S::kBufs) & 1 : 0, gave_up);
+                if (bytes) {
+                    look_up(bias, bt, lg, shift);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) bias[e] = 0.0f;
+                }
+                ok = tc::bar_wait(&ctl->s_full[w], mine & 1, gave_up) && ok;
+            } else {
+                // even lanes wait for the scores, odd ones for the bucket bytes
+                ok = lane & 1 ? !bytes || tc::bar_wait(&ctl->hop_full[buf], p.sources ? (i / S::kBufs) & 1 : 0, gave_up) : tc::bar_wait(&ctl->s_full[w], mine & 1, gave_up);
+            }
             ok = __all_sync(~0u, ok);
-            if (!ok) break;
+            __syncwarp();
             scales(i + 2);
             tc::fence_after();
-            const bool plain = !p.sources && (tile_at(i) + 1) * kTcTile <= p.n;   // no table, no node past the end
-            const uint8_t *bt = bt0 + buf * 33 * kTcPitch;
-            float tile_sum = 0.0f;
+            float tile_sum = 0.0f, mt = m;                            // of this tile's weights, and what they are against
 #pragma unroll 1
-            for (int b = 0; b < KW; b += 32) {
-                uint32_t s[32];
-                tc::load(s, s_at + key0 + b);
-                const float sc = row_scale * power_of_two((int)(kb0 >> (b / 4) & 255) - kScaleBias);
-                const int ev = (int)(vb0 >> (b / 4) & 255) - kScaleBias;
+            for (int b = 0; b < HW; b += CH) {
+                uint32_t s[CH];
+                tc::load(s, s_at + b);
+                if constexpr (kEarly) {
+                    if (b && bytes) look_up(bias, bt + b, lg, shift);
+                }
+                const float sc = row_scale * power_of_two((int)(kb0 & 255) - kScaleBias);
+                const int ev = (int)(vb0 & 255) - kScaleBias;
                 tc::wait_ld();
-                const float top = bias_scores(s, sc, plain, bt + b, lg, shift, -INFINITY) + ev;
-                const bool grow = top > m + kTcLag || (m == -INFINITY && top > -INFINITY);
+                float top;
+                if constexpr (kEarly) {
+                    top = add_bias(s, 0, sc, bias, -INFINITY);
+                    if constexpr (CH == 32) {
+                        if (bytes) look_up(bias, bt + b + 16, lg, shift);
+                        top = add_bias(s, 16, sc, bias, top);
+                    }
+                } else {
+                    top = bias_scores(s, sc, !bytes, smem + (bt - sm) + b, lg, shift, -INFINITY);
+                }
+                top += ev;
+                const bool grow = top > mt + kTcLag || (mt == -INFINITY && top > -INFINITY);
                 if (__any_sync(~0u, grow)) {
-                    const float next = grow ? ceilf(top) : m;
-                    const float f = m == -INFINITY ? 0.0f : ex2(m - next);      // m = -inf: nothing was summed yet
-                    m = next;
-                    sum.sum *= f, sum.rest *= f, tile_sum *= f;
-                    const __half2 hf = __float2half2_rn(f);
-#pragma unroll 1
-                    for (int c = 0; c < b; c += 32) {                           // this tile's weights so far
-                        uint32_t x[16];
-                        tc::load(x, s_at + key0 + c);
-                        tc::wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[e]), hf);
-                            x[e] = *reinterpret_cast<const uint32_t *>(&y);
-                        }
-                        tc::store(s_at + key0 + c, x);
-                    }
-                    if (mine > 0) {
-                        // the products issued before these scores are done, so O is at rest
-#pragma unroll 1
-                        for (int c = 0; c < DP; c += 16) {
-                            uint32_t o[16];
-                            tc::load(o, o_at + c);
-                            tc::wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tc::store(o_at + c, o);
-                        }
-                    }
-                    tc::wait_st();
+                    const float next = grow ? ceilf(top) : mt;
+                    const float f = mt == -INFINITY ? 0.0f : ex2(mt - next);    // mt = -inf: nothing was summed yet
+                    mt = next;
+                    tile_sum *= f;
+                    scale_weights(f, b);
                 }
                 // weights over the scores they come from, two a word
                 float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                uint32_t out[16];
-                weights<__half, 32>(out, s, m == -INFINITY ? 0.0f : m - kCachedUp - ev, part);
-                tc::store(s_at + key0 + b, out);
+                uint32_t out[CH / 2];
+                weights<__half, CH>(out, s, mt == -INFINITY ? 0.0f : mt - kCachedUp - ev, part);
+                tc::store(s_at + b, out);
+                kb0 >>= 8, vb0 >>= 8;
                 tile_sum = fmaf((part[0].x + part[0].y) + (part[1].x + part[1].y), power_of_two(-ev), tile_sum);
             }
-            if (KW < 128) {                                           // nodes of the other copies weigh nothing
-                const uint32_t zero[16] = {};
+            // After a wait that ran out the warp goes on to the vote, where both leave.
+            if (pair_any(pair, !ok || mt != m)) {
+                ctl->most[w][half][l] = mt;
+                ok = !pair_any(pair, !ok);
+                if (!ok) break;
+                const float next = fmaxf(mt, ctl->most[w][half ^ 1][l]);
+                const float f = m == -INFINITY ? 0.0f : ex2(m - next), ft = mt == -INFINITY ? 0.0f : ex2(mt - next);
+                pair_any(pair, false);                                // the next tile may write there again
+                m = next;
+                sum.sum *= f, sum.rest *= f, tile_sum *= ft;
+                scale_weights(ft, HW);
+                if (mine > 0) {
+                    // the products issued before these scores are done, so O is at rest; each half takes half of it
+#pragma unroll 1
+                    for (int c = 0; c < DP / 2; c += 8) {
+                        uint32_t o[8];
+                        tc::ld8(o, o_at() + c);
+                        tc::wait_ld();
 #pragma unroll
-                for (int c = 0; c < 128; c += 32)
-                    if (c / KW != copy) tc::store(s_at + c, zero);
+                        for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tc::st8(o_at() + c, o);
+                    }
+                }
+            }
+            if (KW < 128) {                                           // nodes of the other copies' parts weigh nothing
+                const uint32_t zero[HW / 2] = {};
+#pragma unroll
+                for (int j = 0; j < 128 / KW; ++j)
+                    if (j != copy) tc::store(s_at + (j - copy) * KW, zero);
             }
             tc::wait_st();
             tc::fence_before();
-            tc::bar_arrive(&ctl->p_full[w]);
             __syncwarp();
-            if (lane == 0) tc::bar_arrive(&ctl->hop_empty[buf]);
+            if (lane == 0) {
+                tc::bar_arrive(&ctl->p_full[w]);
+                if (p.sources) tc::bar_arrive(&ctl->hop_empty[buf]);
+            }
             sum.add(tile_sum);
         }
         // ---- join the copies and groups through the freed slots: [group][lane][DP + 4] ----
@@ -430,7 +574,7 @@ __global__ void __launch_bounds__(kCachedThreads, 1) attn_cached_kernel(const __
             ok = tc::bar_wait(&ctl->o_full[w], 0, gave_up);
             tc::fence_after();
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("bar.sync 1, 512;" ::: "memory");
         ok = !*gave_up;
         constexpr int P = DP + 4;
         static_assert(256 * P * 4 <= S::kBuckets, "the exchange fits the slots and queries");
@@ -438,25 +582,25 @@ __global__ void __launch_bounds__(kCachedThreads, 1) attn_cached_kernel(const __
         if (ok) {
             float *at = ex + (size_t)(w * 128 + l) * P;
 #pragma unroll 1
-            for (int c = 0; c < DP; c += 16) {
+            for (int c = 0; c < DP / 2; c += 16) {
                 uint32_t o[16];
                 if (mine > 0) {
-                    tc::load(o, o_at + c);
+                    tc::load(o, o_at() + c);
                     tc::wait_ld();
                 } else {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) o[e] = 0;
                 }
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4 *>(at + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4 *>(at + half * (DP / 2) + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
-            at[DP] = m - kCachedUp;
-            at[DP + 1] = sum.total();
+            if (half == 0) at[DP] = m - kCachedUp;
+            at[DP + 1 + half] = sum.total();
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("bar.sync 1, 512;" ::: "memory");
         constexpr int kSets = 2 * (128 / KW), Q4 = DP / 4;
         if (ok)
-            for (int i = tid; i < KW * Q4; i += 256) {
+            for (int i = tid; i < KW * Q4; i += 512) {
                 const int r = i / Q4, c = (i % Q4) * 4;
                 const uint32_t rw = row0 + r;
                 if (rw >= p.rows || c >= (int)p.d) continue;
@@ -472,7 +616,7 @@ __global__ void __launch_bounds__(kCachedThreads, 1) attn_cached_kernel(const __
                     const float *e = e0 + (size_t)k * KW * P;
                     const float f = ex2(e[DP] - ux);
                     const float4 x = *reinterpret_cast<const float4 *>(e + c);
-                    ls += f * e[DP + 1];
+                    ls += f * (e[DP + 1] + e[DP + 2]);
                     acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
                 }
                 const uint32_t t = rw / G, hd = hk * G + rw - t * G;
@@ -493,7 +637,7 @@ __global__ void __launch_bounds__(kCachedThreads, 1) attn_cached_kernel(const __
     __syncwarp();
     tc::fence_before();
     __syncthreads();
-    if (warp == 20) tc::dealloc(tm, 512);
+    if (warp == S::kMma) tc::dealloc(tm, 512);
     if (tid == 0 && *gave_up) atomicOr(p.status, K2T_STATUS_WAIT_TIMEOUT);
 }
 

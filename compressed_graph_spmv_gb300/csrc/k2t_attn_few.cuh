@@ -37,6 +37,7 @@ template <int RS> struct FewPlan {
     static constexpr int kSoft = kGroups * 4 * RS, kAll = (kSoft + 6) * 32;
 };
 constexpr int kFewRows = 16;              // columns of the score product, of which 8 at most are rows
+constexpr uint32_t kFewMost = 8;
 constexpr int kFewHops = 258;             // masked, hops 0 .. 255, no hop information
 
 struct FewSmem {

@@ -240,6 +240,19 @@ def test_scores_that_rise(T, G, order):
     check(held, "fp16", ask(p, "fp16", cache, scale=1.0), scale=1.0)
 
 
+@pytest.mark.parametrize("T,G,d,sources", [(1, 4, 16, 1), (2, 3, 72, 2), (5, 4, 16, 5), (16, 1, 16, 16), (33, 2, 16, 7), (5, 4, 72, 0), (70, 1, 72, 31)])
+def test_many_tiles_a_block(T, G, d, sources):
+    """Some 80 tiles for each block, so that every slot and buffer goes round many times, and calls of it at once."""
+    hkv = 76 if T < 30 else 19
+    n = 20000 if T < 30 else 60000 // G
+    p = problem(T, n, hkv * G, hkv, d, sources, 6 if sources else 0, "bf16", sources not in (0, T), seed=T + d)
+    cache, held = cached(p, "bf16")
+    out = ask(p, "bf16", cache)
+    check(held, "bf16", out)
+    again = ask(p, "bf16", cache)
+    assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("T", [1, 20, 40, 140])
 def test_blocks_of_very_different_size(T, dtype):
