@@ -106,8 +106,8 @@ int k2t_head_rates(double base, uint32_t rotary_dim, uint64_t *rates)
 {
     if (!rates || rotary_dim % 2 || rotary_dim > K2T_HEAD_MAX_DIM || !(base >= 1.0) || std::isinf(base)) return K2T_EINVAL;
     for (uint32_t i = 0; i < rotary_dim / 2; ++i) {
-        const double turns = std::pow(base, -2.0 * i / rotary_dim) * 0.15915494309189535;      // at most 1 / (2 pi)
-        rates[i] = (uint64_t)(turns * 0x1p64);
+        const long double turns = powl((long double)base, -2.0L * i / rotary_dim) * 0.159154943091895335768883763372514362L;
+        rates[i] = (uint64_t)llroundl(turns * 0x1p63L) * 2;      // turns is at most 1 / (2 pi)
     }
     return K2T_OK;
 }

@@ -1,6 +1,7 @@
 """The 8-bit node cache, attention over it and the head norm on the host: what
 the calls refuse, and the references they are tested against (no GPU)."""
 import ctypes
+from decimal import Decimal, localcontext
 
 import numpy as np
 import pytest
@@ -234,3 +235,21 @@ def test_reference_head_gradients_against_differences(paired):
     f = lambda: float((ref.head_norm(x, w, angle, 6, paired, 1e-3)[0] * dy).sum())  # noqa: E731
     dx, dw, _, _ = ref.head_norm_gradients(dy, x, w, angle, 6, paired, 1e-3)
     assert np.allclose(dx, _numeric(f, x), atol=1e-7, rtol=0) and np.allclose(dw, _numeric(f, w), atol=1e-7, rtol=0)
+
+
+@pytest.mark.parametrize("base", [1e4, 5e5, 1e6])
+@pytest.mark.parametrize("rotary", [2, 64, 96, 256])
+def test_rates_hold_at_far_positions(base, rotary):
+    """A rate is right to its last bits, so that a far position turns by what it should.
+
+    A rate is rounded to a step of 2 units of 2^-64 turns: at most 1.  The power and the product
+    before it are held in 64 bits: 4.4 steps of 2^-64 relative to at most 0.16 * 2^64, 0.7 units.
+    """
+    lib = K.load()
+    rates = (ctypes.c_uint64 * 128)()
+    assert lib.k2t_head_rates(base, rotary, rates) == 0
+    with localcontext() as c:
+        c.prec = 60
+        for m in range(rotary // 2):
+            exact = Decimal(base) ** (Decimal(-2 * m) / rotary) * 2 ** 64 / (2 * Decimal("3.14159265358979323846264338327950288419716939937510582"))
+            assert abs(rates[m] - exact) <= 2
