@@ -27,6 +27,21 @@
 // the weights; when a score exceeds that, the thread multiplies its weights of
 // the tile so far by a power of two and goes on against a larger m, and at the
 // tile's end both take the larger of theirs, with O and the sums.
+//
+// Hops are turned into bucket bytes by a kernel before, once for all heads and
+// rows (39 us of the 399 below; turned by each block for itself, 425).
+//
+// Roles of the 24 warps: 16 softmax, four V -> fp16, one brings keys, one values,
+// one issues the products, in a fixed order, one copies bucket bytes.  Each slot
+// of a ring is filled by one warp in order.
+//
+// Measured, 2^20 nodes, 4 key/value heads of 128, 32 queries of 16 heads, bf16:
+// 399 us, with the hop table and the cache read once 130 us at the copy rate.
+// What bounds it: the latency of a tile's steps (scores, weights, values, one
+// after another in two groups) and no single unit; of about 3500 clocks a tile
+// shared memory is busy 2300, the tensor cores 1280, the exponential unit 1024.
+// One query term instead of three saves 5 %, so the terms stay.  1024 tokens over
+// 16384 nodes: 142 us.
 #pragma once
 
 #include "k2t_attn.cuh"

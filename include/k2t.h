@@ -582,9 +582,12 @@ K2T_API int k2t_cache_read(const k2t_cache *c, void *stream);
 
 /* k2t_attn_forward with the first a->n_nodes nodes of a cache in the place of
  * a->k and a->v (which are not read, nor their strides): queries, hops, bias,
- * masks and outputs as there.  Weights are rounded to fp16 before they
- * multiply v, whatever the element type.  `work` may be of any n_nodes up to
- * the one that k2t_cached_attn_work_bytes was asked about.  Errors as
+ * masks and outputs as there.  Before they multiply v, weights are rounded:
+ * with at most 8 rows (n_queries n_heads / n_kv_heads) to 2^-9 relative in bf16
+ * and 2^-12 in fp16, with more to fp16 whatever the element type.  `work` holds,
+ * besides what parts of the nodes leave, the hops in a byte for each node and
+ * source; it may be of any n_nodes up to the one that k2t_cached_attn_work_bytes
+ * was asked about.  Errors as
  * k2t_attn_forward; EINVAL where heads or head_dim are not the cache's, ERANGE
  * where n_nodes is more than the cache's. */
 K2T_API uint64_t k2t_cached_attn_work_bytes(const k2t_attn *a);
