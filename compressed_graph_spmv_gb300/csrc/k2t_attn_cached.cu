@@ -8,10 +8,12 @@
 namespace k2t {
 
 // Hops -> bucket bytes and seen nodes of every tile, once for all heads and row tiles of the call (the main kernel's blocks
-// each turned their tiles' hops into bytes themselves before: 32 queries over 2^20 nodes, 4 key/value heads, 425 us).  Reads
-// the table once, at memory speed.
-constexpr int kHopThreads = 256;
-static __global__ void __launch_bounds__(kHopThreads) attn_hops_kernel(const __grid_constant__ CachedParams p)
+// each turned their tiles' hops into bytes themselves before: 32 queries over 2^20 nodes, 4 key/value heads, 425 us, now
+// 388, of which this kernel 30).  Bound by memory: 32 columns of 2^20 hops at 4.4 TB/s.  As many blocks as fit at once: with
+// more than fit and 48 registers a thread it took 43 us, columns that are no multiple of 4 by a value a thread 13 us of 100003
+// nodes and 13 columns (a node a pair of threads: 7).
+constexpr int kHopThreads = 256, kHopBlocks = 6;      // of an SM
+static __global__ void __launch_bounds__(kHopThreads, kHopBlocks) attn_hops_kernel(const __grid_constant__ CachedParams p)
 {
     __shared__ __align__(16) uint8_t bytes[33 * kTcPitch];
     __shared__ __align__(16) uint32_t seen[4];
@@ -42,43 +44,48 @@ static __global__ void __launch_bounds__(kHopThreads) attn_hops_kernel(const __g
             // four columns of four nodes a thread: a word of bytes for each column
             const uint32_t Q = B / 4, q = tid % Q, m = tid / Q;
             for (uint32_t j = m; j < kTcTile / 4; j += kHopThreads / Q) {
-                    int4 h[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        h[k] = make_int4(-1, -1, -1, -1);
-                        if (j * 4 + k < in) h[k] = __ldg(reinterpret_cast<const int4 *>(hops) + (j * 4 + k) * Q + q);
-                    }
-                    const uint32_t mine = used >> (q * 4);
-                    uint32_t sees = 0;
-                    uint32_t *to = reinterpret_cast<uint32_t *>(bytes + q * 4 * kTcPitch + j * 4);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if ((h[k].x >= 0 && mine & 1) || (h[k].y >= 0 && mine & 2) || (h[k].z >= 0 && mine & 4) || (h[k].w >= 0 && mine & 8)) sees |= 1u << k;
-                    to[0] = byte(h[0].x) | byte(h[1].x) << 8 | byte(h[2].x) << 16 | byte(h[3].x) << 24;
-                    to[kTcPitch / 4] = byte(h[0].y) | byte(h[1].y) << 8 | byte(h[2].y) << 16 | byte(h[3].y) << 24;
-                    to[kTcPitch / 2] = byte(h[0].z) | byte(h[1].z) << 8 | byte(h[2].z) << 16 | byte(h[3].z) << 24;
-                    to[kTcPitch / 4 * 3] = byte(h[0].w) | byte(h[1].w) << 8 | byte(h[2].w) << 16 | byte(h[3].w) << 24;
-                    if (Q == 8) {                          // a warp's nodes are in one word
-                        sees = __reduce_or_sync(~0u, sees << ((j & 7) * 4));
-                        if ((tid & 31) == 0) atomicOr(&seen[j >> 3], sees);
-                    } else if (sees) {
-                        atomicOr(&seen[j >> 3], sees << ((j & 7) * 4));
-                    }
-                }
-        } else {
-            const uint32_t total = in * B;
-            for (uint32_t first = tid; first < kTcTile * B; first += kHopThreads * 4) {
-                int32_t h[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) h[k] = first + k * kHopThreads < total ? __ldg(hops + first + k * kHopThreads) : -1;
+                int4 h[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint32_t at = first + k * kHopThreads, node = at / B, c = at - node * B;
-                    if (at >= kTcTile * B) break;
-                    bytes[c * kTcPitch + node] = (uint8_t)byte(h[k]);
-                    if (h[k] >= 0 && used >> c & 1) atomicOr(&seen[node >> 5], 1u << (node & 31));
+                    h[k] = make_int4(-1, -1, -1, -1);
+                    if (j * 4 + k < in) h[k] = __ldg(reinterpret_cast<const int4 *>(hops) + (j * 4 + k) * Q + q);
+                }
+                const uint32_t mine = used >> (q * 4);
+                uint32_t sees = 0;
+                uint32_t *to = reinterpret_cast<uint32_t *>(bytes + q * 4 * kTcPitch + j * 4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if ((h[k].x >= 0 && mine & 1) || (h[k].y >= 0 && mine & 2) || (h[k].z >= 0 && mine & 4) || (h[k].w >= 0 && mine & 8)) sees |= 1u << k;
+                to[0] = byte(h[0].x) | byte(h[1].x) << 8 | byte(h[2].x) << 16 | byte(h[3].x) << 24;
+                to[kTcPitch / 4] = byte(h[0].y) | byte(h[1].y) << 8 | byte(h[2].y) << 16 | byte(h[3].y) << 24;
+                to[kTcPitch / 2] = byte(h[0].z) | byte(h[1].z) << 8 | byte(h[2].z) << 16 | byte(h[3].z) << 24;
+                to[kTcPitch / 4 * 3] = byte(h[0].w) | byte(h[1].w) << 8 | byte(h[2].w) << 16 | byte(h[3].w) << 24;
+                if (Q == 8) {                          // a warp's nodes are in one word
+                    sees = __reduce_or_sync(~0u, sees << ((j & 7) * 4));
+                    if ((tid & 31) == 0) atomicOr(&seen[j >> 3], sees);
+                } else if (sees) {
+                    atomicOr(&seen[j >> 3], sees << ((j & 7) * 4));
                 }
             }
+        } else {
+            static_assert(kHopThreads == 2 * kTcTile);
+            // every second column of a node a thread; neighbouring loads share their lines
+            const uint32_t node = tid % kTcTile, half = tid / kTcTile;
+            bool sees = false;
+            for (uint32_t c0 = half; c0 < B; c0 += 16) {
+                int32_t h[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) h[k] = c0 + 2 * k < B && node < in ? __ldg(hops + node * B + c0 + 2 * k) : -1;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t c = c0 + 2 * k;
+                    if (c >= B) break;
+                    bytes[c * kTcPitch + node] = (uint8_t)byte(h[k]);
+                    sees |= h[k] >= 0 && used >> c & 1;
+                }
+            }
+            const uint32_t some = __ballot_sync(~0u, sees);
+            if ((tid & 31) == 0) atomicOr(&seen[node >> 5], some);
         }
         if (tid < kTcTile) bytes[B * kTcPitch + tid] = tid < in ? (uint8_t)(p.buckets + 1) : 0;
         __syncthreads();
@@ -92,7 +99,6 @@ static __global__ void __launch_bounds__(kHopThreads) attn_hops_kernel(const __g
         __syncthreads();
     }
 }
-
 
 // bm: rows a block takes, 32, 64 or 128.
 template <typename T, int DP> static int cached_dim(const CachedParams &p, int bm, cudaStream_t st)
@@ -117,7 +123,7 @@ template <typename T> static int few_rows(const CachedParams &p, cudaStream_t st
 template <typename T> static int launch_cached(const CachedParams &p, int bm, cudaStream_t st)
 {
     if (p.hop_tiles && p.tiles) {
-        const unsigned blocks = (unsigned)std::min<uint64_t>(p.tiles, 152 * 8);
+        const unsigned blocks = (unsigned)std::min<uint64_t>(p.tiles, 152 * kHopBlocks);
         if (int rc = next_launch(attn_hops_kernel, dim3(blocks), kHopThreads, 0, p, st)) return rc;
     }
     const int rc = p.rows <= kFewMost ? few_rows<T>(p, st) : p.d <= 64 ? cached_dim<T, 64>(p, bm, st) : cached_dim<T, 128>(p, bm, st);

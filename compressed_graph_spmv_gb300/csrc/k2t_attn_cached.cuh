@@ -29,14 +29,14 @@
 // tile's end both take the larger of theirs, with O and the sums.
 //
 // Hops are turned into bucket bytes by a kernel before, once for all heads and
-// rows (39 us of the 399 below; turned by each block for itself, 425).
+// rows (30 us of the 388 below; turned by each block for itself, 425).
 //
 // Roles of the 24 warps: 16 softmax, four V -> fp16, one brings keys, one values,
 // one issues the products, in a fixed order, one copies bucket bytes.  Each slot
 // of a ring is filled by one warp in order.
 //
 // Measured, 2^20 nodes, 4 key/value heads of 128, 32 queries of 16 heads, bf16:
-// 399 us, with the hop table and the cache read once 130 us at the copy rate.
+// 388 us, with the hop table and the cache read once 130 us at the copy rate.
 // What bounds it: the latency of a tile's steps (scores, weights, values, one
 // after another in two groups) and no single unit; of about 3500 clocks a tile
 // shared memory is busy 2300, the tensor cores 1280, the exponential unit 1024.

@@ -27,7 +27,7 @@
 // What bounds it: memory with up to 4 rows a head (2^20 nodes, 4 key/value heads
 // of 128, bf16: one query of 16 heads 158 us, where its bytes take 159 at the copy
 // rate; the general kernel 290), with 5 to 8 rows the softmax threads (240 us; the
-// general kernel, to which 9 rows and more go, 281 with 64 rows).
+// general kernel, to which 9 rows and more go, 272 with 64 rows).
 #pragma once
 
 #include "k2t_attn_cached.cuh"
