@@ -29,7 +29,7 @@
 // tile's end both take the larger of theirs, with O and the sums.
 //
 // Hops are turned into bucket bytes by a kernel before, once for all heads and
-// rows (30 us of the 388 below; turned by each block for itself, 425).
+// rows (30 us of the 388 below; 425 in a form where each block turned its own and a row had one thread).
 //
 // Roles of the 24 warps: 16 softmax, four V -> fp16, one brings keys, one values,
 // one issues the products, in a fixed order, one copies bucket bytes.  Each slot
@@ -38,7 +38,7 @@
 // Measured, 2^20 nodes, 4 key/value heads of 128, 32 queries of 16 heads, bf16:
 // 388 us, with the hop table and the cache read once 130 us at the copy rate.
 // What bounds it: the latency of a tile's steps (scores, weights, values, one
-// after another in two groups) and no single unit; of about 3500 clocks a tile
+// after another in two groups) and no one unit; of about 3500 clocks a tile
 // shared memory is busy 2300, the tensor cores 1280, the exponential unit 1024.
 // One query term instead of three saves 5 %, so the terms stay.  1024 tokens over
 // 16384 nodes: 142 us.
@@ -82,7 +82,7 @@ template <int DP> struct CachedSmem {
         uint64_t hop_full[kBufs], hop_empty[kBufs], s_full[2], p_full[2], o_full[2], drained;
         uint32_t tmem, gave_up, pad[2];
         float row_scale[128];             // what multiplies a row's scores
-        float most[2][2][128];            // [group][half][lane]: a thread's m, where it has grown
+        float most[2][2][128];            // [group][half][lane]: a thread's m, where it has grown; at the end what rounding added to its sum
     };
     static constexpr int kLut = kCtl + (int)((sizeof(Ctl) + 15) / 16 * 16);
     static size_t bytes(const AttnParams &p) { return kLut + kTcLutAlign + (size_t)(p.buckets + 2) * p.group2 * 4; }
@@ -134,6 +134,23 @@ template <int N> __device__ __forceinline__ float add_bias(uint32_t (&s)[N], int
         top = max3(top, x.x, x.y);
     }
     return top;
+}
+
+// As weights() in fp16, with the sum of the weights as rounded in `kept`.  A weight is rounded to 11 bits here (y 2^13 + y takes
+// the others' place and leaves), so that below fp16's normal range, where it has fewer, the sum does not follow.
+template <int N>
+__device__ __forceinline__ void weights_kept(uint32_t (&out)[N / 2], const uint32_t (&s)[N], float m, float2 (&sum)[2], float2 (&kept)[2])
+{
+    const float2 nm = make_float2(-m, -m), up = make_float2(8193.0f, 8193.0f), zero = make_float2(0.0f, 0.0f), minus = make_float2(-1.0f, -1.0f);
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+        const float2 x = add2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), nm);
+        const float2 y = make_float2(ex2(x.x), ex2(x.y));
+        const float2 c = fma2(y, up, zero), r = fma2(fma2(y, minus, c), minus, c);
+        sum[e & 1] = add2(sum[e & 1], y);
+        kept[e & 1] = add2(kept[e & 1], r);
+        out[e] = Elem<__half>::pack(r.x, r.y);
+    }
 }
 
 // Whether any thread of the two warps that share barrier `id` says so.
@@ -451,6 +468,11 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
         const float row_scale = ctl->row_scale[l];
         float m = -INFINITY;                                          // both halves' alike
         LongSum sum;
+        // fp16: what rounding added to the weights.  O over the sum of the weights as they were multiplied: a row of one node is
+        // that node's value, and of a few what all weights were off by cancels.  (In bf16 such a value's 4 bits survive it.)
+        // It costs 32 queries over 2^20 nodes, 128 rows a head of 128, 47 us: 435, in bf16 388.
+        constexpr bool kKeep = std::is_same<T, __half>::value;
+        float off = 0.0f;
         bool ok = true;
         uint32_t mine = 0;                                            // tiles of this group done
         uint32_t kb = 0, vb = 0;                                      // the next tile's scale bytes
@@ -507,7 +529,7 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
             __syncwarp();
             scales(i + 2);
             tc::fence_after();
-            float tile_sum = 0.0f, mt = m;                            // of this tile's weights, and what they are against
+            float tile_sum = 0.0f, tile_off = 0.0f, mt = m;                            // of this tile's weights, and what they are against
 #pragma unroll 1
             for (int b = 0; b < HW; b += CH) {
                 uint32_t s[CH];
@@ -534,13 +556,21 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
                     const float next = grow ? ceilf(top) : mt;
                     const float f = mt == -INFINITY ? 0.0f : ex2(mt - next);    // mt = -inf: nothing was summed yet
                     mt = next;
-                    tile_sum *= f;
+                    tile_sum *= f, tile_off *= f;
                     scale_weights(f, b);
                 }
                 // weights over the scores they come from, two a word
                 float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                 uint32_t out[CH / 2];
-                weights<__half, CH>(out, s, mt == -INFINITY ? 0.0f : mt - kCachedUp - ev, part);
+                const float against = mt == -INFINITY ? 0.0f : mt - kCachedUp - ev;
+                if constexpr (kKeep) {
+                    float2 kept[2] = {part[0], part[1]};
+                    weights_kept<CH>(out, s, against, part, kept);
+                    tile_off = fmaf((kept[0].x - part[0].x + (kept[0].y - part[0].y)) + (kept[1].x - part[1].x + (kept[1].y - part[1].y)),
+                                    power_of_two(-ev), tile_off);
+                } else {
+                    weights<__half, CH>(out, s, against, part);
+                }
                 tc::store(s_at + b, out);
                 kb0 >>= 8, vb0 >>= 8;
                 tile_sum = fmaf((part[0].x + part[0].y) + (part[1].x + part[1].y), power_of_two(-ev), tile_sum);
@@ -554,7 +584,7 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
                 const float f = m == -INFINITY ? 0.0f : ex2(m - next), ft = mt == -INFINITY ? 0.0f : ex2(mt - next);
                 pair_any(pair, false);                                // the next tile may write there again
                 m = next;
-                sum.sum *= f, sum.rest *= f, tile_sum *= ft;
+                sum.sum *= f, sum.rest *= f, off *= f, tile_sum *= ft, tile_off *= ft;
                 scale_weights(ft, HW);
                 if (mine > 0) {
                     // the products issued before these scores are done, so O is at rest; each half takes half of it
@@ -583,6 +613,7 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
                 if (p.sources) tc::bar_arrive(&ctl->hop_empty[buf]);
             }
             sum.add(tile_sum);
+            off += tile_off;
         }
         // ---- join the copies and groups through the freed slots: [group][lane][DP + 4] ----
         if (ok && mine > 0) {
@@ -611,6 +642,7 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
             }
             if (half == 0) at[DP] = m - kCachedUp;
             at[DP + 1 + half] = sum.total();
+            if constexpr (kKeep) ctl->most[w][half][l] = off;
         }
         asm volatile("bar.sync 1, 512;" ::: "memory");
         constexpr int kSets = 2 * (128 / KW), Q4 = DP / 4;
@@ -624,7 +656,7 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
 #pragma unroll
                 for (int k = 0; k < kSets; ++k) mx = fmaxf(mx, e0[(size_t)k * KW * P + DP]);
                 const float ux = mx == -INFINITY ? 0.0f : mx;
-                float ls = 0.0f;
+                float ls = 0.0f, added = 0.0f;
                 float4 acc = make_float4(0, 0, 0, 0);
 #pragma unroll
                 for (int k = 0; k < kSets; ++k) {
@@ -632,15 +664,23 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
                     const float f = ex2(e[DP] - ux);
                     const float4 x = *reinterpret_cast<const float4 *>(e + c);
                     ls += f * (e[DP + 1] + e[DP + 2]);
+                    if constexpr (kKeep) {
+                        const int at = k * KW + r;
+                        added += f * (ctl->most[at >> 7][0][at & 127] + ctl->most[at >> 7][1][at & 127]);
+                    }
                     acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
                 }
                 const uint32_t t = rw / G, hd = hk * G + rw - t * G;
                 if (p.splits > 1) {
                     const uint64_t at = ((uint64_t)split * p.T + t) * p.hq + hd;
+                    if (kKeep && ls != 0.0f) {             // the parts are joined over the sums of the weights that were not rounded
+                        const float f = ls / (ls + added);
+                        acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+                    }
                     *reinterpret_cast<float4 *>(p.part + at * p.d + c) = acc;
                     if (c == 0) *reinterpret_cast<float2 *>(p.part_ml + at * 2) = make_float2(mx, ls);
                 } else {
-                    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;     // 0: nothing was seen; a row that is no number says so
+                    const float inv = ls == 0.0f ? 0.0f : 1.0f / (ls + added);     // 0: nothing was seen; a row that is no number says so
                     uint2 o2;
                     o2.x = Elem<T>::pack(acc.x * inv, acc.y * inv);
                     o2.y = Elem<T>::pack(acc.z * inv, acc.w * inv);

@@ -320,6 +320,25 @@ def test_queries_without_nodes_and_nodes_without_queries():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,G,n", [(1, 2, 1), (3, 1, 1), (9, 1, 1), (40, 2, 1), (130, 1, 1), (1, 2, 40), (20, 2, 40), (20, 2, 2000), (2, 4, 2000)])
+def test_one_node_alone_is_its_value(T, G, n, dtype):
+    """A row that sees one node is that node's value to the last bit: 4 bits of it, of which rounding leaves all.
+
+    The weight is off by 2^-9 (bf16) or 2^-12 (fp16) with few rows; that is less than half a step of a value of at most 1.875
+    (2^-8 of 1.875, 2^-11 of 1.875).  With more rows it is off by 2^-11, and in fp16 the same again divides it.
+    """
+    rng = np.random.default_rng(T + n)
+    p = problem(T, n, 3 * G, 3, 72, 1, 0, dtype, True, seed=T + n)
+    p["source"][:] = 0
+    p["hops"][:] = -1
+    at = int(rng.integers(0, n))
+    p["hops"][at] = 2
+    cache, held = cached(p, dtype)
+    out, _ = ask(p, dtype, cache)
+    np.testing.assert_array_equal(f64(out), np.repeat(held["v"][at][None], T, 0).repeat(G, 1))
+
+
 @pytest.mark.parametrize("value,at", [(float("nan"), "q"), (float("nan"), "v"), (float("nan"), "k")])
 def test_what_is_no_number_shows(value, at):
     p = problem(2, 200, 2, 1, 64, 0, 0, "bf16", False, seed=4)
