@@ -76,13 +76,14 @@ def test_query_layouts(T, G):
 
 @pytest.mark.parametrize("T,G", [(2, 2), (1, 8), (33, 2)])
 def test_graphs_streams_and_threads(T, G):
-    """One object: two graphs replayed in turn with calls between them, then host threads with a stream each."""
+    """Two graphs of one object replayed in turn with calls between them; its calls on streams ordered one after another; then
+    host threads with a stream and an object each (an object's calls share its work buffer) that ask one cache."""
     n = 30000
     a, b = (problem(T, n, 2 * G, 2, 64, min(T, 32), 6, "bf16", T > 32, seed=s) for s in (1, 2))
     cache, _ = cached(a, "bf16")
     op = pkg.CachedAttention(T, n, 2 * G, 2, 64, torch.bfloat16, sources=a["hops"].shape[1], edges=a["edges"])
 
-    def call(p, out, lse):
+    def call(p, out, lse, op=op):
         op.forward(p["q"], cache, out, lse, hops=p["hops"], bias=p["bias"], query_source=p["source"])
 
     def fresh():
@@ -105,15 +106,28 @@ def test_graphs_streams_and_threads(T, G):
     for g, w in zip(got + [between], want + [want[0]]):
         assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
 
-    results, errors = {}, []
+    streams, shared = [torch.cuda.Stream() for _ in range(3)], [fresh() for _ in range(6)]
+    before = torch.cuda.current_stream()
+    for i, to in enumerate(shared):
+        streams[i % 3].wait_stream(before)
+        before = streams[i % 3]
+        with torch.cuda.stream(before):
+            call((a, b)[i % 2], *to)
+    torch.cuda.synchronize()
+    for i, to in enumerate(shared):
+        assert torch.equal(to[0], want[i % 2][0]) and torch.equal(to[1], want[i % 2][1])
+
+    results, errors, ops = {}, [], []
 
     def work(i):
         try:
+            own = pkg.CachedAttention(T, n, 2 * G, 2, 64, torch.bfloat16, sources=a["hops"].shape[1], edges=a["edges"])
+            ops.append(own)
             stream = torch.cuda.Stream()
             with torch.cuda.stream(stream):
                 to = fresh()
                 for _ in range(20):
-                    call((a, b)[i % 2], *to)
+                    call((a, b)[i % 2], *to, op=own)
             stream.synchronize()
             results[i] = to
         except Exception as e:      # noqa: BLE001 - shown below
@@ -127,7 +141,7 @@ def test_graphs_streams_and_threads(T, G):
     assert not errors
     for i, to in results.items():
         assert torch.equal(to[0], want[i % 2][0]) and torch.equal(to[1], want[i % 2][1])
-    assert op.status() == 0
+    assert op.status() == 0 and len(ops) == 4 and all(o.status() == 0 for o in ops)
 
 
 @pytest.mark.parametrize("T", [1, 40])
