@@ -69,7 +69,10 @@ template <int DP> struct CachedSmem {
     static constexpr int kWide = DP == 64 ? 3 : 2;
     // Warps: 0-15 softmax, then four for values -> fp16, one for keys, one for values, products, bucket bytes.
     static constexpr int kWiden = 16, kLoad = 20, kMma = kLoad + 2, kThreads = (kMma + 2) * 32;
-    static constexpr int kBufs = 3;                           // bucket tiles
+    // Bucket tiles.  An even number, so that a buffer's tiles are all of one group, which has waited for each of them: a wait
+    // for a buffer that the other group's tile was in would pass while that one's copy is still under way.
+    static constexpr int kBufs = 4;
+    static_assert(kBufs % 2 == 0);
     static constexpr int kValueSlot = kTcTile * DP, kWideSlot = kTile * (DP / 64);
     static constexpr int kQ = 0;                              // three terms
     static constexpr int kK = kQ + 3 * kTile;
@@ -85,6 +88,7 @@ template <int DP> struct CachedSmem {
         float most[2][2][128];            // [group][half][lane]: a thread's m, where it has grown; at the end what rounding added to its sum
     };
     static constexpr int kLut = kCtl + (int)((sizeof(Ctl) + 15) / 16 * 16);
+    static_assert(kLut + kTcLutAlign + (K2T_ATTN_MAX_BUCKETS + 2) * K2T_ATTN_MAX_GROUP * 4 <= 232448, "every call's fits an SM");
     static size_t bytes(const AttnParams &p) { return kLut + kTcLutAlign + (size_t)(p.buckets + 2) * p.group2 * 4; }
 };
 
