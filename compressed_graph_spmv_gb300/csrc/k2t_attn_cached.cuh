@@ -511,13 +511,14 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
         scales(w);
         for (uint32_t i = w; i < tiles; i += 2, ++mine) {
             const uint32_t buf = i % S::kBufs;
-            // a table, or nodes past the end
-            const bool bytes = p.sources || i == tail;
+            // a table, or nodes past the end; after a wait that ran out the bytes are none: they may index past the table
+            bool bytes = p.sources || i == tail;
             uint32_t kb0 = kb, vb0 = vb;
             const uint32_t bt = bt0 + buf * 33 * kTcPitch;
             float bias[16];
             if constexpr (kEarly) {
                 ok = !bytes || tc::bar_wait(&ctl->hop_full[buf], p.sources ? (i / S::kBufs) & 1 : 0, gave_up);
+                bytes = bytes && ok;
                 if (bytes) {
                     look_up(bias, bt, lg, shift);
                 } else {
@@ -530,6 +531,7 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
                 ok = lane & 1 ? !bytes || tc::bar_wait(&ctl->hop_full[buf], p.sources ? (i / S::kBufs) & 1 : 0, gave_up) : tc::bar_wait(&ctl->s_full[w], mine & 1, gave_up);
             }
             ok = __all_sync(~0u, ok);
+            bytes = bytes && ok;
             __syncwarp();
             scales(i + 2);
             tc::fence_after();

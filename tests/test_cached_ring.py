@@ -73,3 +73,19 @@ def test_a_buffer_of_one_group_is_not(buffers):
 
 def test_the_kernels_ring_is_not_read_too_early():
     assert read_too_early(buffers_of("k2t_attn_cached.cuh")) is None
+
+
+def test_bytes_are_not_looked_up_after_a_wait_that_ran_out():
+    """What lies in a buffer whose wait ran out may be any byte, and byte 255 of 16 heads is 16320 bytes into a table of at most
+    4224 that ends less than that before the block's shared memory does.  Between such a wait and the lookups the
+    bytes are dropped, and every lookup asks whether there are any."""
+    with open(os.path.join(CSRC, "k2t_attn_cached.cuh")) as f:
+        loop = f.read().split("for (uint32_t i = w; i < tiles; i += 2, ++mine)")[1].split("sum.add(tile_sum)")[0]
+    early, rest = loop.split("ok = __all_sync(~0u, ok);")
+    first = early.split("hop_full[buf]")[1]
+    assert first.index("bytes = bytes && ok;") < first.index("look_up(")
+    assert rest.index("bytes = bytes && ok;") < min(rest.index(x) for x in ("look_up(", "bias_scores("))
+    for part in (early, rest):
+        for at in re.finditer(r"look_up\(", part):
+            assert re.search(r"if \([^\n]*bytes\)[^;]*$", part[:at.start()])
+    assert "bias_scores(s, sc, !bytes," in rest
