@@ -20,7 +20,10 @@
 // A block of 32 nodes has a power of two for keys, 2^ek, which multiplies its
 // scores, and one for values, 2^ev, which is added to the exponent of its
 // weights: with the running maximum m of s + ev a weight is 2^(s + ev - m), the
-// sum takes it times 2^-ev, and no value is multiplied.
+// sum takes it times 2^-ev, and no value is multiplied.  Where scores are so
+// large that fp32 does not hold s + ev (a soft mask of -1e9 on all that a row
+// sees), s and m are against an origin, a whole number near the row's scores:
+// (s - origin) is exact and small, and ev is added to that.
 //
 // Two threads have a row, one each half of the nodes, and go through them 32 at
 // a time, once: m is a whole number and trails the maximum by at most 2^8 in
@@ -62,6 +65,22 @@ inline uint32_t hop_tile_bytes(uint32_t sources) { return ((sources + 1) * kTcPi
 
 constexpr float kCachedUp = 7.0f;         // weights are at most 2^(8 + 7)
 
+// A row's origin: 0, and where what a larger m comes from is kCachedFar or more away from it, another whole number.  m, a
+// whole number below 2^23, and m - ev are then exact.  The halves of a row take the higher of theirs: fp32 holds the
+// difference wherever a weight against the other is not 0.
+constexpr float kCachedFar = 0x1p22f;
+__device__ __forceinline__ float origin_near(float top) { return fabsf(top) >= kCachedFar && fabsf(top) < INFINITY ? rintf(top) : 0.0f; }
+// What the sums of a row are against, without its origin: a whole number near the logarithm of the sum of the weights, so
+// that rounding it costs neither that sum its range nor another part of the row its share.  Returns what the sums are to be
+// multiplied by for it.
+__device__ __forceinline__ float without_origin(float &against, float origin, float sum)
+{
+    if (origin == 0.0f || sum == 0.0f) return 1.0f;
+    const float all = rintf(origin + (against + log2f(sum))), f = ex2(origin - all + against);
+    against = all;
+    return f;
+}
+
 template <int DP> struct CachedSmem {
     static constexpr int kTile = kTcTile * 128;               // 128 rows of 128 bytes
     static constexpr int kKeys = DP == 64 ? 4 : 3;            // slots of keys, of values, of values in fp16
@@ -83,9 +102,9 @@ template <int DP> struct CachedSmem {
     struct Ctl {
         uint64_t k_full[kKeys], k_empty[kKeys], v_full[kValues], v_empty[kValues], w_full[kWide], w_empty[kWide];
         uint64_t hop_full[kBufs], hop_empty[kBufs], s_full[2], p_full[2], o_full[2], drained;
-        uint32_t tmem, gave_up, pad[2];
+        uint32_t tmem, gave_up, far, pad;      // far: a row has, or had, an origin that is not 0
         float row_scale[128];             // what multiplies a row's scores
-        float most[2][2][128];            // [group][half][lane]: a thread's m, where it has grown; at the end what rounding added to its sum
+        float most[2][2][128];            // [group][half][lane]: a thread's origin; at votes its m, at the end what rounding added to its sum
     };
     static constexpr int kLut = kCtl + (int)((sizeof(Ctl) + 15) / 16 * 16);
     static_assert(kLut + kTcLutAlign + (K2T_ATTN_MAX_BUCKETS + 2) * K2T_ATTN_MAX_GROUP * 4 <= 232448, "every call's fits an SM");
@@ -377,7 +396,7 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
             tc::bar_init(&ctl->o_full[i], 1);
         }
         tc::bar_init(&ctl->drained, 1);
-        ctl->gave_up = 0;
+        ctl->gave_up = ctl->far = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tc::grid_wait();
@@ -470,7 +489,11 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
         const uint32_t tail = !p.sources && tiles && tile_at(tiles - 1) == p.tiles - 1 && p.n % kTcTile ? tiles - 1 : ~0u;
         const int pair = w * 4 + (warp & 3) + 2;                      // barrier of the two warps that share rows
         const float row_scale = ctl->row_scale[l];
-        float m = -INFINITY;                                          // both halves' alike
+        float m = -INFINITY;                                          // both halves' alike, as is the origin
+        // Origins are 0 but for very large scores: they are kept in shared memory.
+        auto place = [&](int of) -> float & { return (&ctl->most[0][0][0])[threadIdx.x ^ of]; };    // of 128: the other half's
+        bool shifted = false;                                         // one of the warp's is another
+        place(0) = 0.0f;
         LongSum sum;
         // fp16: what rounding added to the weights.  O over the sum of the weights as they were multiplied: a row of one node is
         // that node's value, and of a few what all weights were off by cancels.  (In bf16 such a value's 4 bits survive it.)
@@ -556,10 +579,27 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
                 } else {
                     top = bias_scores(s, sc, !bytes, smem + (bt - sm) + b, lg, shift, -INFINITY);
                 }
-                top += ev;
-                const bool grow = top > mt + kTcLag || (mt == -INFINITY && top > -INFINITY);
-                if (__any_sync(~0u, grow)) {
-                    const float next = grow ? ceilf(top) : mt;
+                float near = top + ev;
+                if (__any_sync(~0u, near > mt + kTcLag || shifted)) {
+                    if (shifted) near = top - place(0) + ev;
+                    const bool grow = near > mt + kTcLag;             // mt = -inf: of a node that is seen
+                    if (__any_sync(~0u, grow && fabsf(near) >= kCachedFar)) {
+                        float to = place(0);
+                        if (grow && fabsf(near) >= kCachedFar) {
+                            const float by = to - origin_near(top);
+                            to = origin_near(top);
+                            m += by, mt += by, near = top - to + ev;
+                            place(0) = to;
+                            ctl->far = 1;
+                        }
+                        shifted = __any_sync(~0u, to != 0.0f);
+                    }
+                    if (shifted) {
+                        const float from = place(0);
+#pragma unroll
+                        for (int e = 0; e < CH; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - from);
+                    }
+                    const float next = grow ? ceilf(near) : mt;
                     const float f = mt == -INFINITY ? 0.0f : ex2(mt - next);    // mt = -inf: nothing was summed yet
                     mt = next;
                     tile_sum *= f, tile_off *= f;
@@ -582,13 +622,26 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
                 tile_sum = fmaf((part[0].x + part[0].y) + (part[1].x + part[1].y), power_of_two(-ev), tile_sum);
             }
             // After a wait that ran out the warp goes on to the vote, where both leave.
-            if (pair_any(pair, !ok || mt != m)) {
-                ctl->most[w][half][l] = mt;
+            if (pair_any(pair, !ok || mt != m)) {                     // an origin moves only where m grows
+                float from = place(0);
+                place(0) = mt;
                 ok = !pair_any(pair, !ok);
                 if (!ok) break;
-                const float next = fmaxf(mt, ctl->most[w][half ^ 1][l]);
+                float other = place(128);
+                if (__builtin_expect(pair_any(pair, from != 0.0f), 0)) {       // the higher origin of the halves that saw something
+                    place(0) = from;
+                    pair_any(pair, false);
+                    const float theirs = place(128);
+                    pair_any(pair, false);
+                    float to = fmaxf(mt == -INFINITY ? -INFINITY : from, other == -INFINITY ? -INFINITY : theirs);
+                    if (to == -INFINITY) to = 0.0f;
+                    m += from - to, mt += from - to, other += theirs - to;
+                    from = to;
+                }
+                place(0) = from;
+                shifted = __any_sync(~0u, from != 0.0f);
+                const float next = fmaxf(mt, other);
                 const float f = m == -INFINITY ? 0.0f : ex2(m - next), ft = mt == -INFINITY ? 0.0f : ex2(mt - next);
-                pair_any(pair, false);                                // the next tile may write there again
                 m = next;
                 sum.sum *= f, sum.rest *= f, off *= f, tile_sum *= ft, tile_off *= ft;
                 scale_weights(ft, HW);
@@ -646,7 +699,7 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4 *>(at + half * (DP / 2) + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
-            if (half == 0) at[DP] = m - kCachedUp;
+            if (half == 0) at[DP] = m - kCachedUp, at[DP + 3] = place(0);
             at[DP + 1 + half] = sum.total();
             if constexpr (kKeep) ctl->most[w][half][l] = off;
         }
@@ -658,16 +711,26 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
                 const uint32_t rw = row0 + r;
                 if (rw >= p.rows || c >= (int)p.d) continue;
                 const float *e0 = ex + (size_t)r * P;
-                float mx = -INFINITY;
+                float mx = -INFINITY, origin = 0.0f, of[kSets];
 #pragma unroll
-                for (int k = 0; k < kSets; ++k) mx = fmaxf(mx, e0[(size_t)k * KW * P + DP]);
+                for (int k = 0; k < kSets; ++k) of[k] = e0[(size_t)k * KW * P + DP], mx = fmaxf(mx, of[k]);
+                if (__builtin_expect(ctl->far && mx > -INFINITY, 0)) {
+                    // against the highest origin of those that saw something
+                    origin = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < kSets; ++k)
+                        if (of[k] > -INFINITY) origin = fmaxf(origin, e0[(size_t)k * KW * P + DP + 3]);
+                    mx = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < kSets; ++k) of[k] += e0[(size_t)k * KW * P + DP + 3] - origin, mx = fmaxf(mx, of[k]);
+                }
                 const float ux = mx == -INFINITY ? 0.0f : mx;
                 float ls = 0.0f, added = 0.0f;
                 float4 acc = make_float4(0, 0, 0, 0);
 #pragma unroll
                 for (int k = 0; k < kSets; ++k) {
                     const float *e = e0 + (size_t)k * KW * P;
-                    const float f = ex2(e[DP] - ux);
+                    const float f = ex2(of[k] - ux);
                     const float4 x = *reinterpret_cast<const float4 *>(e + c);
                     ls += f * (e[DP + 1] + e[DP + 2]);
                     if constexpr (kKeep) {
@@ -675,6 +738,10 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
                         added += f * (ctl->most[at >> 7][0][at & 127] + ctl->most[at >> 7][1][at & 127]);
                     }
                     acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
+                }
+                if (origin != 0.0f) {
+                    const float f = without_origin(mx, origin, ls);
+                    acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f, ls *= f, added *= f;
                 }
                 const uint32_t t = rw / G, hd = hk * G + rw - t * G;
                 if (p.splits > 1) {

@@ -57,7 +57,7 @@ struct FewSmem {
         uint64_t s_full[3], s_empty[3], p_full[3], p_done[3], token[3], drained[2];
         uint32_t tmem, gave_up, version, pad[1];
         Row row[8];
-        float m[4][8];                    // of this version and of the three before
+        float m[4][8], origin[4][8];      // of this version and of the three before
         float tops[4][8];
         float sums[16][4];
     };
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(FewPlan<RS>::kAll, 1) attn_few_kernel(const __
         ctl->gave_up = ctl->version = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (tid < 8) ctl->m[0][tid] = -INFINITY;
+    if (tid < 8) ctl->m[0][tid] = -INFINITY, ctl->origin[0][tid] = 0.0f;
     tc::grid_wait();
     for (uint32_t i = tid; i < kFewHops * p.group2; i += Plan::kAll) {     // bias in units of log2, by hops + 1 and head
         const uint32_t b = i >> p.group2_log, g = i & (p.group2 - 1);
@@ -308,14 +308,15 @@ __global__ void __launch_bounds__(FewPlan<RS>::kAll, 1) attn_few_kernel(const __
         uint32_t hop_at[4];                                           // its hops, or none
 #pragma unroll
         for (int r = 0; r < 4; ++r) hop_at[r] = rows[r].col < 0 ? 0 : S::hops_at(p) + (rows[r].query * kTcTile + l) * 4;
-        // weights of the scores x against m, as terms into the group's part of P; sums in `part`
+        bool shifted = false;                                         // a row's origin is not 0: the path of a raise, with every tile
+        // weights of the scores x, which are against the origins, against m, as terms into the group's part of P; sums in `part`
         auto release = [&](const float (&x)[4], int ev, float (&part)[4]) {
             uint32_t words[4] = {0, 0, 0, 0};
             float y[4];
-            const float back = power_of_two(-ev);
+            const float back = power_of_two(-ev), up = (float)ev + kCachedUp;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                y[r] = ex2(x[r] - (m[r] == -INFINITY ? 0.0f : m[r] - kCachedUp));
+                y[r] = ex2(x[r] - (m[r] == -INFINITY ? 0.0f : m[r] - up));
                 part[r] = y[r] * back;
             }
 #pragma unroll
@@ -329,13 +330,29 @@ __global__ void __launch_bounds__(FewPlan<RS>::kAll, 1) attn_few_kernel(const __
             *reinterpret_cast<uint4 *>(p_at) = make_uint4(words[0], words[1], words[2], words[3]);
             tc::fence_async();
         };
-        // a version's m in the place of this thread's, whose sums follow; f: by what
-        auto adopt = [&](const float *next, float (&f)[4]) {
+        // a version's m and origins (to) in the place of this thread's, whose sums follow; f: by what
+        auto adopt = [&](const float *next, const float *from, const float *to, float (&f)[4]) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                f[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - next[r]);
+                f[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] + (from[r] - to[r]) - next[r]);
                 m[r] = next[r];
                 sum[r] *= f[r], rest[r] *= f[r];
+            }
+        };
+        // the group's largest of each row, after a vote of the group
+        auto largest = [&](const float (&y)[4], float (&top)[4]) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float a = y[r];
+#pragma unroll
+                for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
+                if (lane == 0) ctl->tops[warp & 3][rs * 4 + r] = a;
+            }
+            group_any<Plan::kThreads>(w, false);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float *t = &ctl->tops[0][rs * 4 + r];
+                top[r] = fmaxf(fmaxf(t[0], t[8]), fmaxf(t[16], t[24]));
             }
         };
         ahead(w);
@@ -356,7 +373,7 @@ __global__ void __launch_bounds__(FewPlan<RS>::kAll, 1) attn_few_kernel(const __
             for (int r = 0; r < 4; ++r) {
                 uint32_t at = in ? kFewHops - 1 : 0;                  // no hop information, or masked
                 if (in && hop_at[r]) at = __viaddmax_s32(min(*reinterpret_cast<const int32_t *>(smem + hop_at[r] + hop_tile), 255), 1, 0);
-                x[r] = fe + table(table_at[r] + (at << shift));
+                x[r] = table(table_at[r] + (at << shift));
             }
             uint32_t s[3][4];
 #pragma unroll
@@ -365,36 +382,34 @@ __global__ void __launch_bounds__(FewPlan<RS>::kAll, 1) attn_few_kernel(const __
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::bar_arrive(&ctl->s_empty[w]);
-            bool grow = false;
+            bool grow = shifted;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 x[r] = fmaf(__uint_as_float(s[0][r]) + (__uint_as_float(s[1][r]) + __uint_as_float(s[2][r])), scale[r] * pk, x[r]);
-                grow |= x[r] > m[r] + kTcLag || (m[r] == -INFINITY && x[r] > -INFINITY);
             }
+            const float low = fe - kTcLag;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) grow |= x[r] > m[r] - low;        // m = -inf: of a score that is seen
             release(x, ev, part);
             ok = ok && (i == 0 || tc::bar_wait(&ctl->token[w], (w ? mine : mine - 1) & 1, gave_up));
             if (group_any<Plan::kThreads>(w, !ok || grow || *(volatile uint32_t *)&ctl->version != version)) {
                 ok = !group_any<Plan::kThreads>(w, !ok);
                 if (!ok) break;
-                float f[4], next[4];
+                float f[4], next[4], to[4], top[4], near[4];
+                const float *from = ctl->origin[version & 3] + rs * 4;
                 version = *(volatile uint32_t *)&ctl->version;
-                adopt(ctl->m[version & 3] + rs * 4, f);
-                // the tile's largest of each row
+#pragma unroll
+                for (int r = 0; r < 4; ++r) to[r] = ctl->origin[version & 3][rs * 4 + r];
+                adopt(ctl->m[version & 3] + rs * 4, from, to, f);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) near[r] = x[r] - to[r] + fe;
+                largest(near, top);
+                bool raise = false, far = false;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    float top = x[r];
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-                    if (lane == 0) ctl->tops[warp & 3][rs * 4 + r] = top;
-                }
-                group_any<Plan::kThreads>(w, false);
-                bool raise = false;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float *t = &ctl->tops[0][rs * 4 + r], top = fmaxf(fmaxf(t[0], t[8]), fmaxf(t[16], t[24]));
-                    const bool up = top > m[r] + kTcLag || (m[r] == -INFINITY && top > -INFINITY);
-                    next[r] = up ? ceilf(top) : m[r];
-                    raise |= up;
+                    const bool up = top[r] > m[r] + kTcLag || (m[r] == -INFINITY && top[r] > -INFINITY);
+                    next[r] = up ? ceilf(top[r]) : m[r];
+                    raise |= up, far |= up && fabsf(top[r]) >= kCachedFar;
                 }
                 if (group_any<Plan::kThreads>(w, raise)) {
                     if (i > 0) {
@@ -403,7 +418,21 @@ __global__ void __launch_bounds__(FewPlan<RS>::kAll, 1) attn_few_kernel(const __
                     }
                     ok = !group_any<Plan::kThreads>(w, !ok);
                     if (!ok) break;
-                    adopt(next, f);
+                    if (group_any<Plan::kThreads>(w, far)) {          // other origins, near the largest scores
+                        bool moved[4];
+                        largest(x, top);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            moved[r] = next[r] != m[r] && fabsf(next[r]) >= kCachedFar;
+                            if (moved[r]) to[r] = origin_near(top[r]);
+                            near[r] = x[r] - to[r] + fe;
+                        }
+                        group_any<Plan::kThreads>(w, false);
+                        largest(near, top);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) next[r] = moved[r] ? ceilf(top[r]) : next[r];
+                    }
+                    adopt(next, ctl->origin[version & 3] + rs * 4, to, f);
                     if (i > 0) {
                         uint32_t o[16];
                         tc::ld16(o, o_at);
@@ -414,9 +443,15 @@ __global__ void __launch_bounds__(FewPlan<RS>::kAll, 1) attn_few_kernel(const __
                         tc::wait_st();
                     }
                     ++version;
-                    if (l < 4) ctl->m[version & 3][rs * 4 + l] = l == 0 ? next[0] : l == 1 ? next[1] : l == 2 ? next[2] : next[3];
+                    if (l < 4) {
+                        ctl->m[version & 3][rs * 4 + l] = l == 0 ? next[0] : l == 1 ? next[1] : l == 2 ? next[2] : next[3];
+                        ctl->origin[version & 3][rs * 4 + l] = l == 0 ? to[0] : l == 1 ? to[1] : l == 2 ? to[2] : to[3];
+                    }
                     if (first_thread) ctl->version = version;
                 }
+                shifted = false;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[r] = x[r] - to[r], shifted |= to[r] != 0.0f;
                 release(x, ev, part);
                 tc::fence_before();
                 group_any<Plan::kThreads>(w, false);
@@ -441,7 +476,8 @@ __global__ void __launch_bounds__(FewPlan<RS>::kAll, 1) attn_few_kernel(const __
         asm volatile("bar.sync 4, %0;" ::"n"(Plan::kSoft * 32) : "memory");
         ok = !*gave_up;
         float f[4];
-        adopt(ctl->m[ctl->version & 3] + rs * 4, f);
+        const float *origin = ctl->origin[ctl->version & 3] + rs * 4;
+        adopt(ctl->m[ctl->version & 3] + rs * 4, ctl->origin[version & 3] + rs * 4, origin, f);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             float a = sum[r] + rest[r];
@@ -465,7 +501,9 @@ __global__ void __launch_bounds__(FewPlan<RS>::kAll, 1) attn_few_kernel(const __
                 }
                 for (int k = rs * 4; k < Plan::kSoft; k += 4 * RS) ls += (ctl->sums[k][r] + ctl->sums[k + 1][r]) + (ctl->sums[k + 2][r] + ctl->sums[k + 3][r]);
                 const uint32_t t = row / p.group, hd = hk * p.group + row - t * p.group;
-                const float mr = m[r] - kCachedUp;
+                float mr = m[r] - kCachedUp;
+                const float whole = without_origin(mr, origin[r], ls);
+                acc *= whole, ls *= whole;
                 if (p.splits > 1) {
                     const uint64_t at = ((uint64_t)split * p.T + t) * p.hq + hd;
                     if (l < (int)p.d) p.part[at * p.d + l] = acc;
