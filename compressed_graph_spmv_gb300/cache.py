@@ -20,7 +20,9 @@ class NodeCache(_Placed):
 
     ``k`` and ``v`` (float8_e4m3fn [n_kv_heads, n_nodes, head_dim rounded up to 16]) and ``k_scale`` and ``v_scale``
     (uint8 s [n_kv_heads, blocks rounded up to 16], for 2^(s - 64)) are made, all zero, on the stream that is current
-    when the object is made; a stream that uses them before that is done has to wait for it.
+    when the object is made; a stream that uses them before that is done has to wait for it.  Between calls another tensor of
+    the same type and layout may be assigned in the place of one (a cache that was saved); graphs captured before go on with
+    the old one, which they do not keep.
     """
 
     def __init__(self, n_nodes: int, n_kv_heads: int, head_dim: int, dtype, device="cuda"):
@@ -36,23 +38,43 @@ class NodeCache(_Placed):
         self._current, self._here = _stream_getter(torch), _device_getter(torch)
         pitch, blocks = (head_dim + 15) // 16 * 16, -(-n_nodes // CACHE_BLOCK)
         rows, scales = (n_kv_heads, n_nodes, pitch), (n_kv_heads, (blocks + 15) // 16 * 16)
-        self.k, self.v = (torch.zeros(rows, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2))
-        self.k_scale, self.v_scale = (torch.zeros(scales, dtype=torch.uint8, device=device) for _ in range(2))
-        self._streams = {self._current(self.k.get_device())} if self.k.is_cuda else set()
+        k, v = (torch.zeros(rows, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2))
+        k_scale, v_scale = (torch.zeros(scales, dtype=torch.uint8, device=device) for _ in range(2))
+        self._tensors = dict(k=k, v=v, k_scale=k_scale, v_scale=v_scale)
+        self._streams = {self._current(k.get_device())} if k.is_cuda else set()
         self._a, self._held = Cache(), Cache()         # of a write or read; of an attention, which does not change
         for a in (self._a, self._held):
             a.dtype, a.n_kv_heads, a.head_dim, a.n_nodes = _dtype_code(dtype, (BF16, FP16, FP32)), n_kv_heads, head_dim, n_nodes
-            a.k, a.v, a.k_scale, a.v_scale = (t.data_ptr() for t in (self.k, self.v, self.k_scale, self.v_scale))
+            a.k, a.v, a.k_scale, a.v_scale = (t.data_ptr() for t in (k, v, k_scale, v_scale))
         self._ref, self._held_ref = ctypes.byref(self._a), ctypes.byref(self._held)
         self._int = torch.int32
         self._lock = threading.Lock()
+
+    def _assign(self, name, t):
+        """Another tensor in the place of one: the calls take its address from here on."""
+        with self._lock:
+            old = self._tensors[name]
+            if t.shape != old.shape or not t.is_contiguous():
+                raise ValueError("%s: expected a contiguous tensor of shape %s, got %s" % (name, tuple(old.shape), tuple(t.shape)))
+            if isinstance(t, self._torch.Tensor):
+                if t.dtype is not old.dtype:
+                    raise TypeError("%s: expected %s, got %s" % (name, old.dtype, t.dtype))
+                if t.device != old.device or t.data_ptr() % 16:
+                    raise ValueError("%s: expected a tensor on %s that begins on 16 bytes" % (name, old.device))
+            self._tensors[name] = t
+            for a in (self._a, self._held):
+                setattr(a, name, t.data_ptr())
+            self._streams = set()          # no stream is known to have used it
+
+    k, v, k_scale, v_scale = (property(lambda self, name=name: self._tensors[name], lambda self, t, name=name: self._assign(name, t))
+                              for name in ("k", "v", "k_scale", "v_scale"))
 
     def _used_on(self, ptr, device):
         """The tensors are not given back before the work of every stream that used them has ended."""
         if ptr not in self._streams:
             cuda = self._torch.cuda
             stream = cuda.ExternalStream(ptr, device=device) if ptr else cuda.default_stream(device)
-            for t in (self.k, self.v, self.k_scale, self.v_scale):
+            for t in self._tensors.values():
                 t.record_stream(stream)
             self._streams.add(ptr)
 
@@ -64,8 +86,9 @@ class NodeCache(_Placed):
             device = k.get_device()
             if device != self._on or device != self._here():
                 device = self._device_of("k", k)
-            if self.k.get_device() != device:
-                raise ValueError("k: on device %d, the cache is on device %d" % (device, self.k.get_device()))
+            own = self._tensors["k"].get_device()
+            if own != device:
+                raise ValueError("k: on device %d, the cache is on device %d" % (device, own))
             a.x_k, a.xk_row, a.xk_head = _rows("k", k, shape, self.dtype, device)
             a.x_v, a.xv_row, a.xv_head = _rows("v", v, shape, self.dtype, device)
             a.nodes = 0 if nodes is None else _flat("nodes", nodes, shape[:1], self._int, device)
