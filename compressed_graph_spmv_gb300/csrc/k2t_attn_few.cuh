@@ -12,9 +12,10 @@
 // Both products read the cached bytes as they lie, keys and values alike as
 // the 8-bit A operand, and their cost goes with the few rows.  A query is
 // three e5m2 terms, as there.  A weight is four such terms (three in a bf16
-// call), each of what the ones before leave, that hold it to 2^-12 (2^-9) and
-// what is 2^-32 of the largest; each has columns of its own, which are added in
-// fp32 at the end.
+// call), each of 8 times what the one before leaves, which is where the next
+// bits of a large weight are and keeps those of a small one above the least
+// e5m2: they hold it to 2^-12 (2^-9), and to 2^-32 (2^-29) of the largest where
+// that is more.  Each has columns of its own, which are added in fp32 at the end.
 //
 // A thread has four rows of a node, and its warp's 32 nodes are one block of
 // the cache: both its scales are the warp's.  The reference m of a row's weights (a whole number
@@ -41,6 +42,7 @@ template <int RS> struct FewPlan {
 };
 constexpr int kFewRows = 16;              // columns of the score product, of which 8 at most are rows
 constexpr uint32_t kFewMost = 8;
+constexpr float kTermUp = 8.0f;           // a weight's term is of what the one before left, times this
 constexpr int kFewHops = 258;             // masked, hops 0 .. 255, no hop information
 
 struct FewSmem {
@@ -319,13 +321,14 @@ __global__ void __launch_bounds__(FewPlan<RS>::kAll, 1) attn_few_kernel(const __
                 y[r] = ex2(x[r] - (m[r] == -INFINITY ? 0.0f : m[r] - up));
                 part[r] = y[r] * back;
             }
+            const float2 minus = make_float2(-1.0f, -1.0f), more = make_float2(kTermUp, kTermUp), zero = make_float2(0.0f, 0.0f);
+            float2 u = make_float2(y[0], y[1]), v = make_float2(y[2], y[3]);
 #pragma unroll
             for (int term = 0; term < kTerms; ++term) {
-                const uint32_t a = to_e5m2(y[0], y[1]), b = to_e5m2(y[2], y[3]);
+                const uint32_t a = to_e5m2(u.x, u.y), b = to_e5m2(v.x, v.y);
                 words[term] = a | b << 16;
                 if (term + 1 == kTerms) break;
-                const float2 c = from_e5m2(a), d = from_e5m2(b);
-                y[0] -= c.x, y[1] -= c.y, y[2] -= d.x, y[3] -= d.y;
+                u = fma2(fma2(from_e5m2(a), minus, u), more, zero), v = fma2(fma2(from_e5m2(b), minus, v), more, zero);
             }
             *reinterpret_cast<uint4 *>(p_at) = make_uint4(words[0], words[1], words[2], words[3]);
             tc::fence_async();
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(FewPlan<RS>::kAll, 1) attn_few_kernel(const __
                 float acc = 0.0f, ls = 0.0f;
                 if (tiles) {
 #pragma unroll
-                    for (int term = kTerms - 1; term >= 0; --term) acc += __uint_as_float(o[term * 4 + r]);
+                    for (int term = kTerms - 1; term >= 0; --term) acc = fmaf(acc, 1.0f / kTermUp, __uint_as_float(o[term * 4 + r]));
                 }
                 for (int k = rs * 4; k < Plan::kSoft; k += 4 * RS) ls += (ctl->sums[k][r] + ctl->sums[k + 1][r]) + (ctl->sums[k + 2][r] + ctl->sums[k + 3][r]);
                 const uint32_t t = row / p.group, hd = hk * p.group + row - t * p.group;

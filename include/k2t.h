@@ -582,9 +582,13 @@ K2T_API int k2t_cache_read(const k2t_cache *c, void *stream);
 
 /* k2t_attn_forward with the first a->n_nodes nodes of a cache in the place of
  * a->k and a->v (which are not read, nor their strides): queries, hops, bias,
- * masks and outputs as there.  Before they multiply v, weights are rounded:
- * with at most 8 rows (n_queries n_heads / n_kv_heads) to 2^-9 relative in bf16
- * and 2^-12 in fp16, with more to fp16 whatever the element type.  `work` holds,
+ * masks and outputs as there.  Before they multiply v, weights, times the power
+ * of two of their block's values, are rounded: with at most 8 rows (n_queries
+ * n_heads / n_kv_heads) to 2^-9 of them in bf16 and 2^-12 in fp16, or, where
+ * that is more, to 2^-29 (2^-32) of the row's largest; with more rows, whatever
+ * the element type, to 2^-11 or 2^-31 of the row's largest.  (A block with a
+ * very large value takes bits from weights of the others, unless its nodes
+ * are not seen or weigh little.)  `work` holds,
  * besides what parts of the nodes leave, the hops in a byte for each node and
  * source; it may be of any n_nodes up to the one that k2t_cached_attn_work_bytes
  * was asked about.  Errors as
