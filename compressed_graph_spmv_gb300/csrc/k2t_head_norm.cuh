@@ -12,7 +12,8 @@
 //
 // An angle is position x rate in turns, and rates are 64-bit fractions of a
 // turn: the product modulo 2^64 is the fraction of a turn exactly, however far
-// the position (an fp32 product of position 2^20 and rate 1 is 0.06 off).
+// the position (an fp32 product of position 2^20 and rate 1 is 0.06 off); fp32
+// then holds it to 2^-26.
 // In 16 bits sine and cosine are the special function unit's (2^-20 off in one
 // turn, where results round to 2^-9 or 2^-12), in fp32 the library's.
 //

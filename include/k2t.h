@@ -491,7 +491,7 @@ K2T_API int k2t_norm_backward(const k2t_norm *a, void *work, uint64_t work_bytes
  *       a' = a cos f - b sin f,  b' = b cos f + a sin f
  * Pair m is values m and m + rotary_dim / 2, with K2T_HEAD_PAIRED 2 m and
  * 2 m + 1.  Rates are fractions of a turn for each position: k2t_head_rates
- * gives base^(-2 m / rotary_dim) / (2 pi), and the angle is exact to 2^-32 of a
+ * gives base^(-2 m / rotary_dim) / (2 pi), and the angle is right to 2^-26 of a
  * turn however far the position.  Sums, angles and products are fp32 (squares
  * above 3.4e38 overflow), results are rounded once.
  * Strides are in elements, as k2t_attn's (base pointers multiples of 16 bytes,
