@@ -437,7 +437,7 @@ class HeadNorm(_Placed):
         return y
 
     def backward(self, dy, x, weight, dx, dweight, positions=None, stream=None):
-        """dx and dweight (both None without a weight) from dy and the forward call's x and positions."""
+        """dx and dweight from dy and the forward call's x and positions; weight and dweight are given together or are both None."""
         with self._lock:
             device = dy.get_device()
             if device != self._on or device != self._here():
