@@ -8,8 +8,8 @@
 namespace k2t {
 
 // Hops -> bucket bytes and seen nodes of every tile, once for all heads and row tiles of the call (the main kernel's blocks
-// each turned their tiles' hops into bytes themselves before: 32 queries over 2^20 nodes, 4 key/value heads, 425 us, now
-// 388, of which this kernel 30).  Bound by memory: 32 columns of 2^20 hops at 4.4 TB/s.  As many blocks as fit at once: with
+// each turned their tiles' hops into bytes themselves before: 32 queries over 2^20 nodes, 4 key/value heads, 425 us, then
+// 388, of which this kernel 30; 400 since rows may have origins).  Bound by memory: 32 columns of 2^20 hops at 4.4 TB/s.  As many blocks as fit at once: with
 // more than fit and 48 registers a thread it took 43 us, columns that are no multiple of 4 by a value a thread 13 us of 100003
 // nodes and 13 columns (a node a pair of threads: 7).
 constexpr int kHopThreads = 256, kHopBlocks = 6;      // of an SM

@@ -10,7 +10,7 @@
 //
 // S is a product of 8-bit operands: the cached bytes are the operand as they
 // lie.  A query goes in as three e5m2 terms, each what the ones before leave
-// of it; bf16 and fp16 values are three such terms exactly, down to 2^-32 of
+// of it; bf16 and fp16 values are three such terms exactly, down to 2^-31 of
 // the row's largest (the row is scaled by a power of two that brings that to
 // 2^14), so that nothing of the query is rounded.
 //
@@ -32,19 +32,19 @@
 // tile's end both take the larger of theirs, with O and the sums.
 //
 // Hops are turned into bucket bytes by a kernel before, once for all heads and
-// rows (30 us of the 388 below; 425 in a form where each block turned its own and a row had one thread).
+// rows (30 us of the 400 below; a form where each block turned its own and a row had one thread took 37 us more).
 //
 // Roles of the 24 warps: 16 softmax, four V -> fp16, one brings keys, one values,
 // one issues the products, in a fixed order, one copies bucket bytes.  Each slot
 // of a ring is filled by one warp in order.
 //
 // Measured, 2^20 nodes, 4 key/value heads of 128, 32 queries of 16 heads, bf16:
-// 388 us, with the hop table and the cache read once 130 us at the copy rate.
+// 400 us, with the hop table and the cache read once 130 us at the copy rate.
 // What bounds it: the latency of a tile's steps (scores, weights, values, one
 // after another in two groups) and no one unit; of about 3500 clocks a tile
 // shared memory is busy 2300, the tensor cores 1280, the exponential unit 1024.
 // One query term instead of three saves 5 %, so the terms stay.  1024 tokens over
-// 16384 nodes: 142 us.
+// 16384 nodes: 146 us.  Origins cost 2 % of each (393 and 142 us without).
 #pragma once
 
 #include "k2t_attn.cuh"
@@ -469,9 +469,9 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
         __syncwarp();
     } else {
         // ---- softmax: a thread has a lane of tensor memory, and of every other tile half of its copy's nodes ----
-        // Biases are looked up while the scores are on their way, the first ones before they are there, where the registers
-        // hold them: 32 queries over 2^20 nodes, 8 heads of 64, 358 us, afterwards 385; with 4 key/value heads of 128 and 128
-        // rows the registers spill, and 395 us become 407.
+        // Biases are looked up while the scores are on their way, the first ones before they are there: 32 queries over 2^20
+        // nodes, 8 heads of 64, 356 us, all afterwards 392 (fp16 376 and 413; with 64 rows a head of 128 277 and 287).  With
+        // 128 rows a head of 128 afterwards: 400 us, early 420.
         constexpr bool kEarly = DP == 64 || KW < 128;
         constexpr int HW = KW / 2, CH = HW < 32 ? HW : 32;            // nodes of a thread's part of a tile, of them at a time
         const int w = warp >> 3, half = warp >> 2 & 1, l = (warp & 3) * 32 + lane;
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(CachedSmem<DP>::kThreads, 1) attn_cached_kerne
         LongSum sum;
         // fp16: what rounding added to the weights.  O over the sum of the weights as they were multiplied: a row of one node is
         // that node's value, and of a few what all weights were off by cancels.  (In bf16 such a value's 4 bits survive it.)
-        // It costs 32 queries over 2^20 nodes, 128 rows a head of 128, 47 us: 435, in bf16 388.
+        // It costs 32 queries over 2^20 nodes, 128 rows a head of 128, 46 us: 446, in bf16 400.
         constexpr bool kKeep = std::is_same<T, __half>::value;
         float off = 0.0f;
         bool ok = true;

@@ -25,10 +25,14 @@
 // alone: it waits for the products so far, multiplies O by powers of two and
 // forms its weights again.  Whoever used the m of before does so too.
 //
-// What bounds it: memory with up to 4 rows a head (2^20 nodes, 4 key/value heads
-// of 128, bf16: one query of 16 heads 158 us, where its bytes take 159 at the copy
-// rate; the general kernel 290), with 5 to 8 rows the softmax threads (240 us; the
-// general kernel, to which 9 rows and more go, 272 with 64 rows).
+// Very large scores (see origins in k2t_attn_cached.cuh): a row with an origin
+// sends its group the way of a raise with every tile.
+//
+// What bounds it: memory with up to 4 rows a head of 128 (2^20 nodes, 4 key/value
+// heads, bf16: one query of 16 heads 161 us, where its bytes take 159 at the copy
+// rate; two, which are 8 rows, 179); with heads of 64, whose tiles are half the
+// bytes, and with 5 to 8 rows of them the softmax threads (8 heads, one query
+// 223 us, five 312, eight 326).
 #pragma once
 
 #include "k2t_attn_cached.cuh"
@@ -41,6 +45,9 @@ template <int RS> struct FewPlan {
     static constexpr int kSoft = kGroups * 4 * RS, kAll = (kSoft + 6) * 32;
 };
 constexpr int kFewRows = 16;              // columns of the score product, of which 8 at most are rows
+// More rows go to the general kernel.  Both over 2^20 nodes, bf16: 8 rows a head of 128 179 us (2 queries, 4 heads) and 193 (8
+// queries), general 231 and 234; of 64 (8 heads) 5 rows 312 us and 8 rows 326, general 335; of 32 326 and 331.  With short
+// calls of 5 to 8 rows the general one is ahead: 8 queries, 8 heads of 64, 16384 nodes, 20.6 us, general 18.7.
 constexpr uint32_t kFewMost = 8;
 constexpr float kTermUp = 8.0f;           // a weight's term is of what the one before left, times this
 constexpr int kFewHops = 258;             // masked, hops 0 .. 255, no hop information
