@@ -117,3 +117,29 @@ def test_as_over_16_bits(T, G):
     for got in (o, out):          # every score is the bias: 64 values of a few units each times 1/8 are below half of 128
         close("out", got, np.broadcast_to(mean, got.shape), np.broadcast_to(u * np.abs(mean) + (u + 2.0 ** -18) * size, got.shape))
     assert torch.equal(lse, l)
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "shuffled"])
+@pytest.mark.parametrize("T,G", SHAPES)
+def test_levels_that_change(T, G, order):
+    """Runs of nodes at one of ten levels after another, so that a row's origin moves many times in a block of many tiles; runs end
+    inside tiles, and a column sees some of them alone."""
+    rng = np.random.default_rng(T * 3 + G)
+    n, hkv, sources = 5000, 152 if T < 9 else 40, 4
+    p = problem(T, G, n, 8, "bf16", T, hkv, sources)
+    table = np.array([-3e9, -2e9, -1.01e9, -1e9, -6e6, 0.0, 4.0, 9e6, 3e8, 2e9])
+    for c in range(sources):
+        level = np.sort(rng.permutation(10)[:10 - c])
+        level = {"rising": level, "falling": level[::-1], "shuffled": rng.permutation(level)}[order]
+        ends = np.sort(rng.choice(np.arange(1, n), size=len(level) - 1, replace=False))
+        column = np.repeat(level, np.diff(np.concatenate([[0], ends, [n]])))
+        p["hops"][:, c] = torch.from_numpy(column.astype(np.int32)).cuda()
+    p["edges"] = list(range(10))
+    p["bias"] = torch.from_numpy(table).cuda().bfloat16().expand(hkv * G, 10).contiguous()
+    levels = f64(p["bias"])[0][p["hops"].cpu().numpy()]
+    top = levels.max(axis=0)
+    for c in range(sources):          # 0 and 4 together are no test of levels alone
+        if top[c] == 4.0:
+            p["hops"][:, c][p["hops"][:, c] == 5] = -1
+    levels = np.where(p["hops"].cpu().numpy() < 0, -np.inf, f64(p["bias"])[0][np.maximum(p["hops"].cpu().numpy(), 0)])
+    check(p, "bf16", 1.0, levels)
